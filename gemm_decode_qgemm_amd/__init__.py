@@ -9,14 +9,23 @@ this package only binds it.
 from .binding import (  # noqa: F401
     FLAG_NONFINITE,
     FLAG_OVERFLOW,
+    FLAG_PAGE,
+    FLAG_POSITION,
+    KV8_BLOCK,
+    KV8_PAGE,
     QG_BF16,
     QG_F32,
     SCRATCH_BYTES,
     QGemmError,
+    attn_kv8,
+    attn_kv8_workspace_bytes,
     default_split_k,
     int4_dq_packed_bytes,
     int4_packed_bytes,
     intn_packed_bytes,
+    kv8_append,
+    kv8_empty,
+    kv8_read,
     qgemm_w4a8,
     qgemm_w4a8_dq,
     qgemm_w4a8_g32,
@@ -26,6 +35,7 @@ from .binding import (  # noqa: F401
     qgemm_w4a16_noalloc,
     qgemm_w8a16,
     qgemm_wn_a16,
+    qk_norm_rope,
     quantize_int4_g32,
     quantize_int4_g32_dq,
     quantize_int8_rowwise,

@@ -25,6 +25,10 @@ MAX_M = 64
 SCRATCH_BYTES = 16 * 1024 * 1024      # QG_SCRATCH_BYTES of include/qgemm.h
 FLAG_NONFINITE = 1
 FLAG_OVERFLOW = 2
+FLAG_POSITION = 4
+FLAG_PAGE = 8
+KV8_PAGE = 64                         # tokens of a cache page
+KV8_BLOCK = 16                        # tokens that share a scale
 
 
 class QGemmError(RuntimeError):
@@ -63,6 +67,13 @@ def _load() -> ctypes.CDLL:
         "qgemm_w4a8_g32": (I32, [P, I64, I64, P, I64, I64, P, I32, I32, P, I64, P]),
         "qgemm_w4a8_dq": (I32, [P, I64, I64, P, I64, I64, P, I32, I32, P, I64, P]),
         "qgemm_w4a8_g32_dq": (I32, [P, I64, I64, P, I64, I64, P, I32, I32, P, I64, P]),
+        "qg_qk_norm_rope": (I32, [P, I64, I64, P, I64, I64, I64, I32, I32, I32, P, P, P, I64, I32, I32, P,
+                                  ctypes.c_float, P, P, P, P]),
+        "qg_kv8_append": (I32, [P, I64, I64, P, I64, I64, I64, P, P, I64, I32, I32, P, I64, P, P, I64, I64, P, P]),
+        "qg_kv8_read": (I32, [P, P, I64, I32, I32, P, I64, P, I64, I64, P, P, I32, P]),
+        "qg_attn_kv8_workspace_bytes": (I64, [I64, I64, I32, I32, I32, I64, I64, I32, I32]),
+        "qg_attn_kv8": (I32, [P, I64, I64, I64, I32, P, P, I64, I32, I32, P, I64, P, P, I64, I64, I64, I32,
+                              ctypes.c_float, P, I32, I32, P, I64, P, P]),
     }
     for name, (res, args) in sigs.items():
         fn = getattr(lib, name)
@@ -359,3 +370,195 @@ def qgemm_w4a8_g32_dq(x: torch.Tensor, packed: torch.Tensor, n: int, *, split_k:
     """qgemm_w4a8_g32 (one activation scale per group of 32) on a scale-code packed weight (m <= 64)."""
     return _w4a8_call(lib.qgemm_w4a8_g32_dq, "qgemm_w4a8_g32_dq", x, packed, n, split_k, out_dtype, out,
                       workspace)
+
+
+# ---- operators of a decoder layer around the linears -------------------------
+
+def _heads(t: torch.Tensor, name: str) -> tuple:
+    """[rows, heads, d] bf16 with contiguous channels, any row and head stride."""
+    if not t.is_cuda:
+        raise ValueError(f"{name} must be on a CUDA (HIP) device")
+    if t.dtype != torch.bfloat16 or t.dim() != 3:
+        raise ValueError(f"{name} must be bfloat16 [rows, heads, d], got {t.dtype} of rank {t.dim()}")
+    if t.shape[2] != 1 and t.stride(2) != 1:
+        raise ValueError(f"{name}: the channels of a head must be contiguous")
+    return t.shape
+
+
+def _same_device(device: torch.device, **tensors) -> None:
+    for name, t in tensors.items():
+        if t is not None and t.device != device:
+            raise ValueError(f"{name} must be on {device}, got {t.device}")
+
+
+def _flags(status: torch.Tensor | None) -> int | None:
+    if status is None:
+        return None
+    if not status.is_cuda or status.element_size() != 4 or status.numel() < 1:
+        raise ValueError("status must be a 32-bit device word")
+    return status.data_ptr()
+
+
+def qk_norm_rope(q: torch.Tensor, k: torch.Tensor, q_weight: torch.Tensor | None, k_weight: torch.Tensor | None,
+                 cos_sin: torch.Tensor, positions: torch.Tensor, *, eps: float = 1e-6,
+                 adjacent_pairs: bool = False, out: tuple | None = None,
+                 status: torch.Tensor | None = None) -> tuple:
+    """RMS norm of every query and key head and the rotation of its first
+    cos_sin.shape[1] channels by position: (q [tokens, hq, d], k [tokens, hkv, d])
+    -> the same shapes, contiguous.  q and k may be strided views of a fused
+    projection; cos_sin is fp32 [max_pos, rot], the cosines of a position
+    before its sines."""
+    tokens, hq, d = _heads(q, "q")
+    _, hkv, _ = _heads(k, "k")
+    if k.shape[0] != tokens or k.shape[2] != d:
+        raise ValueError("q and k must have the same tokens and channels")
+    _dev(cos_sin, "cos_sin", torch.float32, 2)
+    _dev(positions, "positions", torch.int32, 1)
+    if positions.shape[0] != tokens:
+        raise ValueError("positions must be [tokens]")
+    for name, w in (("q_weight", q_weight), ("k_weight", k_weight)):
+        if w is not None:
+            _dev(w, name, torch.bfloat16, 1)
+            if w.shape[0] != d:
+                raise ValueError(f"{name} must be [d]")
+    _same_device(q.device, k=k, q_weight=q_weight, k_weight=k_weight, cos_sin=cos_sin, positions=positions,
+                 status=status)
+    if out is None:
+        q_out = torch.empty((tokens, hq, d), dtype=torch.bfloat16, device=q.device)
+        k_out = torch.empty((tokens, hkv, d), dtype=torch.bfloat16, device=q.device)
+    else:
+        q_out, k_out = out
+        _dev(q_out, "out[0]", torch.bfloat16, 3)
+        _dev(k_out, "out[1]", torch.bfloat16, 3)
+        if q_out.shape != q.shape or k_out.shape != k.shape:
+            raise ValueError("out must have the shapes of q and k")
+    st = lib.qg_qk_norm_rope(q.data_ptr(), q.stride(0), q.stride(1), k.data_ptr(), k.stride(0), k.stride(1), tokens,
+                             hq, hkv, d, _ptr(q_weight), _ptr(k_weight), cos_sin.data_ptr(), cos_sin.shape[0],
+                             cos_sin.shape[1], int(adjacent_pairs), positions.data_ptr(), eps, q_out.data_ptr(),
+                             k_out.data_ptr(), _flags(status), _stream(q.device))
+    _check(st, "qg_qk_norm_rope")
+    return q_out, k_out
+
+
+def kv8_empty(pages: int, hkv: int, d: int, device) -> tuple:
+    """(codes, scales) of an empty 8-bit key/value cache of `pages` pages of 64 tokens."""
+    return (torch.zeros((pages, hkv, 2, KV8_PAGE * d), dtype=torch.int8, device=device),
+            torch.zeros((pages, hkv, 2, KV8_PAGE // KV8_BLOCK), dtype=torch.float32, device=device))
+
+
+def _cache(codes, scales, block_table, lens) -> tuple:
+    """Checks a cache and its table; (pages, hkv, d, b, table width)."""
+    _dev(codes, "codes", torch.int8, 4)
+    _dev(scales, "scales", torch.float32, 4)
+    _dev(block_table, "block_table", torch.int32, 2)
+    _dev(lens, "lens", torch.int32, 1)
+    pages, hkv, two, bytes_ = codes.shape
+    if two != 2 or bytes_ % KV8_PAGE != 0:
+        raise ValueError("codes must be int8 [pages, hkv, 2, 64 * d]")
+    if scales.shape != (pages, hkv, 2, KV8_PAGE // KV8_BLOCK):
+        raise ValueError("scales must be float32 [pages, hkv, 2, 4]")
+    b, width = block_table.shape
+    if lens.shape[0] != b:
+        raise ValueError("block_table must be [b, width] and lens [b]")
+    _same_device(codes.device, scales=scales, block_table=block_table, lens=lens)
+    return pages, hkv, bytes_ // KV8_PAGE, b, width
+
+
+def _starts(cu: torch.Tensor | None, b: int, rows: int, most: int | None, device) -> int:
+    """Checks the row offsets; the bound of a sequence's rows."""
+    if cu is not None:
+        _dev(cu, "cu", torch.int32, 1)
+        if cu.shape[0] != b + 1:
+            raise ValueError("cu must be [b + 1]")
+        _same_device(device, cu=cu)
+        return rows if most is None else most
+    if rows % b != 0:
+        raise ValueError("without cu every sequence has the same number of rows")
+    return rows // b
+
+
+def kv8_append(k: torch.Tensor, v: torch.Tensor, codes: torch.Tensor, scales: torch.Tensor,
+               block_table: torch.Tensor, lens: torch.Tensor, *, cu: torch.Tensor | None = None,
+               max_new: int | None = None, status: torch.Tensor | None = None) -> None:
+    """Quantizes new keys and values [rows, hkv, d] into the cache as the last
+    tokens of the sequences (lens counts them).  Rows of sequence b are
+    cu[b]..cu[b + 1] (cu given), or rows / b each; max_new bounds a sequence's
+    rows (default: all of them, which launches more workgroups than needed)."""
+    pages, hkv, d, b, width = _cache(codes, scales, block_table, lens)
+    rows = _heads(k, "k")[0]
+    if tuple(k.shape) != (rows, hkv, d) or tuple(_heads(v, "v")) != (rows, hkv, d):
+        raise ValueError("k and v must be [rows, hkv, d] of the cache's heads")
+    most = _starts(cu, b, rows, max_new, codes.device)
+    _same_device(codes.device, k=k, v=v, status=status)
+    st = lib.qg_kv8_append(k.data_ptr(), k.stride(0), k.stride(1), v.data_ptr(), v.stride(0), v.stride(1), rows,
+                           codes.data_ptr(), scales.data_ptr(), pages, hkv, d, block_table.data_ptr(), width,
+                           lens.data_ptr(), _ptr(cu), b, most, _flags(status), _stream(codes.device))
+    _check(st, "qg_kv8_append")
+
+
+def kv8_read(codes: torch.Tensor, scales: torch.Tensor, block_table: torch.Tensor, lens: torch.Tensor,
+             max_len: int, *, out_dtype: torch.dtype = torch.bfloat16, out: tuple | None = None) -> tuple:
+    """The sequences' keys and values as [b, max_len, hkv, d]; zero past a length."""
+    pages, hkv, d, b, width = _cache(codes, scales, block_table, lens)
+    if out_dtype not in (torch.bfloat16, torch.float32):
+        raise ValueError("out_dtype must be torch.bfloat16 or torch.float32")
+    shape = (b, max_len, hkv, d)
+    if out is None:
+        out = tuple(torch.empty(shape, dtype=out_dtype, device=codes.device) for _ in range(2))
+    for i, t in enumerate(out):
+        _dev(t, f"out[{i}]", out_dtype, 4)
+        if tuple(t.shape) != shape:
+            raise ValueError("out must be two [b, max_len, hkv, d]")
+    _same_device(codes.device, k=out[0], v=out[1])
+    st = lib.qg_kv8_read(codes.data_ptr(), scales.data_ptr(), pages, hkv, d, block_table.data_ptr(), width,
+                         lens.data_ptr(), b, max_len, out[0].data_ptr(), out[1].data_ptr(),
+                         QG_F32 if out_dtype == torch.float32 else QG_BF16, _stream(codes.device))
+    _check(st, "qg_kv8_read")
+    return tuple(out)
+
+
+def attn_kv8_workspace_bytes(b: int, rows: int, hq: int, hkv: int, d: int, max_q: int, max_len: int, *,
+                             window: int = 0, splits: int = 0) -> int:
+    v = int(lib.qg_attn_kv8_workspace_bytes(b, rows, hq, hkv, d, max_q, max_len, window, splits))
+    _check(min(v, 0), "qg_attn_kv8_workspace_bytes")
+    return v
+
+
+def attn_kv8(q: torch.Tensor, codes: torch.Tensor, scales: torch.Tensor, block_table: torch.Tensor,
+             lens: torch.Tensor, *, cu: torch.Tensor | None = None, max_q: int | None = None,
+             max_len: int | None = None, window: int = 0, scale: float | None = None, splits: int = 0,
+             out_dtype: torch.dtype = torch.bfloat16, out: torch.Tensor | None = None,
+             workspace: torch.Tensor | None = None, status: torch.Tensor | None = None) -> torch.Tensor:
+    """Causal attention of query rows [rows, hq, d] (a sequence's last tokens)
+    over the cache -> [rows, hq, d].  scale defaults to d ** -0.5, max_len (an
+    upper bound of lens, for the choice of the split) to the table's width."""
+    pages, hkv, d, b, width = _cache(codes, scales, block_table, lens)
+    rows, hq, dq = _heads(q, "q")
+    if dq != d:
+        raise ValueError("q must have the cache's channels")
+    most = _starts(cu, b, rows, max_q, codes.device)
+    if max_len is None:
+        max_len = width * KV8_PAGE
+    if out_dtype not in (torch.bfloat16, torch.float32):
+        raise ValueError("out_dtype must be torch.bfloat16 or torch.float32")
+    if out is None:
+        out = torch.empty((rows, hq, d), dtype=out_dtype, device=q.device)
+    else:
+        _dev(out, "out", out_dtype, 3)
+        if out.shape != q.shape:
+            raise ValueError("out must have the shape of q")
+    _same_device(codes.device, q=q, out=out, workspace=workspace, status=status)
+    if rows == 0:
+        return out
+    need = int(lib.qg_attn_kv8_workspace_bytes(b, rows, hq, hkv, d, most, max_len, window, splits))
+    _check(min(need, 0), "qg_attn_kv8")
+    if need and workspace is None:
+        workspace = torch.empty(need, dtype=torch.uint8, device=q.device)
+    ws_bytes = 0 if workspace is None else workspace.numel() * workspace.element_size()
+    st = lib.qg_attn_kv8(q.data_ptr(), q.stride(0), q.stride(1), rows, hq, codes.data_ptr(), scales.data_ptr(), pages,
+                         hkv, d, block_table.data_ptr(), width, lens.data_ptr(), _ptr(cu), b, most, max_len, window,
+                         d ** -0.5 if scale is None else scale, out.data_ptr(),
+                         QG_F32 if out_dtype == torch.float32 else QG_BF16, splits, _ptr(workspace), ws_bytes,
+                         _flags(status), _stream(q.device))
+    _check(st, "qg_attn_kv8")
+    return out

@@ -137,6 +137,8 @@ const char* qg_status_string(int32_t s) {
     case QG_E_SCRATCH:
       return "the split needs more partial-sum space than the library's static scratch holds "
              "(split * m * n * 4 > QG_SCRATCH_BYTES); pass a smaller split_k or use qgemm_w4a16";
+    case QG_E_HEADS: return "a head size, head count or rotated width that this operator does not take";
+    case QG_E_STRIDE: return "strides must be multiples of 8 elements and at least a row of the tensor";
     default: return "unknown qgemm status";
   }
 }

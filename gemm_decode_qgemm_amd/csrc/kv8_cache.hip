@@ -1,0 +1,317 @@
+// kv8_cache.hip -- the paged key/value cache held in 8 bits: appending new
+// tokens (kv8_append) and reading sequences back (kv8_read).
+//
+// A page holds 64 tokens of every key/value head as int8 codes, with one fp32
+// scale per 16 tokens, head and keys / values (layout: include/qgemm.h).  For a
+// block of 16 tokens that receives new ones, with s_held its scale (0 where
+// the block holds no earlier token) and a = max |x| over its new tokens,
+//   s = max(s_held, a * (1/127)),
+//   held codes  q <- rint(q * (s_held / s))   where s grew,
+//   new codes   q  = clamp(rint(x / s), -127, 127)
+// in binary32: a block's scale only grows while it holds tokens, so a token is
+// requantized at most when a larger one joins its 16.
+//
+// Mapping of the append: a workgroup owns one page of one head of a sequence
+// (nobody else writes it), wave w its block w, so a block's maximum is a
+// butterfly within a wave.  Keys: a lane converts 8 channels of one token per
+// 16-byte load and stores 8 bytes.  Values are stored channel-major: a lane
+// loads the same 8 channels of 4 neighbouring tokens, and has then whole
+// dwords (4 tokens of a channel) to store.  A page whose four blocks are all
+// written gathers those dwords in LDS and stores 16 bytes per lane (a
+// channel's 64 bytes are one run); a page with fewer written blocks (a decode
+// step) stores the dwords where they are.
+#include "layer_common.h"
+
+namespace qg {
+
+struct AppendArgs {
+  Kv8Args c;
+  const uint16_t *k, *v;
+  int64_t k_ts, k_hs, v_ts, v_hs;
+  uint32_t* status;
+};
+
+__device__ __forceinline__ float absmax8(const u32x4_t& v, float m) {
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    m = fmaxf(m, fabsf(__uint_as_float(v[i] << 16)));
+    m = fmaxf(m, fabsf(__uint_as_float(v[i] & 0xffff0000u)));
+  }
+  return m;
+}
+
+// Whether any of the 8 bf16 values is an infinity or a NaN.
+__device__ __forceinline__ bool nonfinite8(const u32x4_t& v) {
+  bool bad = false;
+#pragma unroll
+  for (int i = 0; i < 4; ++i)
+    bad |= (v[i] & 0x7f80u) == 0x7f80u || (v[i] & 0x7f800000u) == 0x7f800000u;
+  return bad;
+}
+
+__device__ __forceinline__ uint32_t code_of(float x, float s) {
+  float q = s > 0.0f ? rintf(x / s) : 0.0f;   // s = 0 or NaN: code 0
+  q = fminf(fmaxf(q, -127.0f), 127.0f);
+  return (uint32_t)(int)q & 0xffu;
+}
+
+__device__ __forceinline__ uint32_t rescale4(uint32_t w, float f) {
+  uint32_t o = 0;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) o |= ((uint32_t)(int)rintf((float)(int8_t)(w >> (8 * i)) * f) & 0xffu) << (8 * i);
+  return o;
+}
+
+// The block's new scale from its lanes' maxima; NaN once anything that is not
+// finite has joined it.  `f` is what the held codes are multiplied by.
+__device__ __forceinline__ float grow(float mx, bool bad, float held, float& f) {
+#pragma unroll
+  for (int o = 1; o < 64; o *= 2) mx = fmaxf(mx, __shfl_xor(mx, o));
+  const float s = fmaxf(held, mx * (1.0f / 127.0f));
+  if (__ballot(bad) != 0 || held != held) {
+    f = 1.0f;
+    return __uint_as_float(0x7fc00000u);
+  }
+  f = s > held ? held / s : 1.0f;
+  return s;
+}
+
+template <int D>
+__global__ __launch_bounds__(256) void kv8_append_kernel(AppendArgs a) {
+  constexpr int NK = D / 32;            // 16-byte chunks of keys per lane
+  constexpr int CH = D / 8;             // chunks per token
+  constexpr int NV = (CH * 4 + 63) / 64;
+  __shared__ uint32_t vt[D * 16];       // [channel][quad][block]
+  const int lane = threadIdx.x & 63;
+  const int w = wave_id_uniform();      // block of the page
+  const int b = blockIdx.x / a.c.hkv, h = blockIdx.x % a.c.hkv;
+  int64_t r0, n;
+  kv8_rows(a.c.cu, a.c.rows, a.c.b, b, r0, n);
+  const int64_t len = a.c.lens[b];
+  if (n <= 0 || len <= 0) return;
+  const int64_t first = len > n ? len - n : 0;   // first token written
+  const int64_t shift = r0 - (len - n);          // row of token j: j + shift
+  const int64_t pi = first / kPage + blockIdx.y;
+  if (pi * kPage >= len) return;
+  const int page = kv8_page(a.c.table + (size_t)b * a.c.width, a.c.width, a.c.pages, pi);
+  if (page < 0) {
+    if (a.status && threadIdx.x == 0) atomicOr(a.status, QG_FLAG_PAGE);
+    return;
+  }
+  int8_t* const kc = a.c.codes + kv8_base(page, a.c.hkv, h, D);
+  uint32_t* const vc = reinterpret_cast<uint32_t*>(kc + kPage * D);
+  float* const sc = a.c.scales + ((size_t)page * a.c.hkv + h) * 8 + w;
+
+  const int64_t t0 = pi * kPage + w * kBlock;    // first token of this wave's block
+  const bool touched = t0 < len && t0 + kBlock > first;
+  // all four blocks written: the last one is, and the first has no token to leave alone
+  const bool whole = pi * kPage >= first / kBlock * kBlock && pi * kPage + 3 * kBlock < len;
+  const int lo = first > t0 ? (int)(first - t0) : 0;              // new tokens of the block: [lo, hi)
+  const int hi = len - t0 < kBlock ? (int)(len - t0) : kBlock;
+
+  if (touched) {
+    // all loads first: new keys, new values, held codes
+    u32x4_t kx[NK], vx[NV][4];
+    bool bad_k = false, bad_v = false;
+    float mk = 0.0f, mv = 0.0f;
+#pragma unroll
+    for (int i = 0; i < NK; ++i) {
+      const int c = lane + 64 * i, tok = c / CH;
+      kx[i] = u32x4_t{0u, 0u, 0u, 0u};
+      if (tok >= lo && tok < hi)
+        kx[i] = *reinterpret_cast<const u32x4_t*>(a.k + (t0 + tok + shift) * a.k_ts + h * a.k_hs + c % CH * 8);
+    }
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+      const int c = lane + 64 * i, quad = c & 3, ch = c >> 2;
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        const int tok = 4 * quad + e;
+        vx[i][e] = u32x4_t{0u, 0u, 0u, 0u};
+        if (ch < CH && tok >= lo && tok < hi)
+          vx[i][e] = *reinterpret_cast<const u32x4_t*>(a.v + (t0 + tok + shift) * a.v_ts + h * a.v_hs + ch * 8);
+      }
+    }
+#pragma unroll
+    for (int i = 0; i < NK; ++i) {
+      mk = absmax8(kx[i], mk);
+      bad_k |= nonfinite8(kx[i]);
+    }
+#pragma unroll
+    for (int i = 0; i < NV; ++i)
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        mv = absmax8(vx[i][e], mv);
+        bad_v |= nonfinite8(vx[i][e]);
+      }
+    float fk, fv;
+    const float sk = grow(mk, bad_k, lo > 0 ? sc[0] : 0.0f, fk);
+    const float sv = grow(mv, bad_v, lo > 0 ? sc[4] : 0.0f, fv);
+    if (lane == 0) {
+      if (a.status && (sk != sk || sv != sv)) atomicOr(a.status, QG_FLAG_NONFINITE);
+    }
+    // Keys: held tokens are rewritten only where the scale grew; the rest of
+    // a block that held nothing becomes zero.
+#pragma unroll
+    for (int i = 0; i < NK; ++i) {
+      const int c = lane + 64 * i, tok = c / CH;
+      u32x2_t* p = reinterpret_cast<u32x2_t*>(kc + (w * kBlock + tok) * D + c % CH * 8);
+      if (tok < lo) {
+        if (fk != 1.0f) {
+          const u32x2_t old = *p;
+          *p = u32x2_t{rescale4(old.x, fk), rescale4(old.y, fk)};
+        }
+      } else if (tok < hi || lo == 0) {
+        u32x2_t o{0u, 0u};
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          const uint32_t two = code_of(__uint_as_float(kx[i][e] << 16), sk) |
+                               code_of(__uint_as_float(kx[i][e] & 0xffff0000u), sk) << 8;
+          o[e >> 1] |= two << (16 * (e & 1));
+        }
+        *p = o;
+      }
+    }
+    // Values: dword (channel, quad) = tokens 4 quad .. + 3 of the block.
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+      const int c = lane + 64 * i, quad = c & 3, ch = c >> 2;
+      if (ch >= CH) continue;
+      // bytes of the dword that are new (or zeroed) / that hold an earlier token
+      const int q0 = 4 * quad;
+      const int keep = lo > q0 ? (lo - q0 < 4 ? lo - q0 : 4) : 0;   // its first `keep` tokens are held
+      const bool fresh = (lo < q0 + 4 && hi > q0) || lo == 0;
+      if (!whole && !fresh && fv == 1.0f) continue;   // nothing of it changes
+      const uint32_t mask = keep == 4 ? 0xffffffffu : (1u << (8 * keep)) - 1u;
+#pragma unroll
+      for (int e = 0; e < 8; ++e) {
+        const int d = 8 * ch + e;
+        uint32_t* p = vc + d * 16 + quad * 4 + w;
+        uint32_t o = 0;
+#pragma unroll
+        for (int u = 0; u < 4; ++u) {
+          const uint32_t x = vx[i][u][e >> 1];
+          o |= code_of(__uint_as_float((e & 1) ? x & 0xffff0000u : x << 16), sv) << (8 * u);
+        }
+        if (keep) o = (o & ~mask) | (rescale4(*p, fv) & mask);
+        if (whole) vt[d * 16 + quad * 4 + w] = o;
+        else *p = o;
+      }
+    }
+    if (lane == 0) {
+      sc[0] = sk;
+      sc[4] = sv;
+    }
+  }
+  if (!whole) return;                    // uniform over the workgroup
+  __syncthreads();
+  for (int p = threadIdx.x; p < D * 4; p += 256)
+    reinterpret_cast<u32x4_t*>(vc)[p] = reinterpret_cast<const u32x4_t*>(vt)[p];
+}
+
+struct ReadArgs {
+  Kv8Args c;
+  int64_t max_len;
+  void *k, *v;
+};
+
+template <bool F32>
+__device__ __forceinline__ void store4(void* out, size_t at, uint32_t w, float s) {
+  const float x0 = (float)(int8_t)w * s, x1 = (float)(int8_t)(w >> 8) * s, x2 = (float)(int8_t)(w >> 16) * s,
+              x3 = (float)(int8_t)(w >> 24) * s;
+  if constexpr (F32)
+    *reinterpret_cast<f32x4_t*>(static_cast<float*>(out) + at) = f32x4_t{x0, x1, x2, x3};
+  else
+    *reinterpret_cast<u32x2_t*>(static_cast<uint16_t*>(out) + at) = u32x2_t{pack_bf16(x0, x1), pack_bf16(x2, x3)};
+}
+
+// A workgroup reads one page of one head.  Keys: 16 codes per lane.  Values:
+// a lane loads 16 bytes (its quad's tokens of all four blocks) of 4
+// neighbouring channels, and byte permutes turn each 4 x 4 square round, so
+// that 16 lanes store whole 128-byte lines of a token's row.
+template <int D, bool F32>
+__global__ __launch_bounds__(256) void kv8_read_kernel(ReadArgs a) {
+  const int b = blockIdx.x / a.c.hkv, h = blockIdx.x % a.c.hkv;
+  const int64_t t0 = (int64_t)blockIdx.y * kPage;
+  const int64_t len = a.c.lens[b];
+  const int left = (int)(a.max_len - t0 < kPage ? a.max_len - t0 : kPage);              // rows to write
+  const int have = len - t0 >= left ? left : len > t0 ? (int)(len - t0) : 0;            // of them with a token
+  const int page = have > 0 ? kv8_page(a.c.table + (size_t)b * a.c.width, a.c.width, a.c.pages, blockIdx.y) : 0;
+  const size_t row0 = ((size_t)b * a.max_len + t0) * a.c.hkv + h;   // output row of token t: row0 + t hkv
+  const float nan = __uint_as_float(0x7fc00000u);
+  const int8_t* const kc = a.c.codes + kv8_base(page < 0 ? 0 : page, a.c.hkv, h, D);
+  const float* const sc = a.c.scales + ((size_t)(page < 0 ? 0 : page) * a.c.hkv + h) * 8;
+
+  for (int c = threadIdx.x; c < kPage * D / 16; c += 256) {
+    const int tok = c / (D / 16), ch = c % (D / 16) * 16;
+    if (tok >= left) continue;
+    u32x4_t q{0u, 0u, 0u, 0u};
+    float s = 0.0f;
+    if (tok < have) {
+      q = *reinterpret_cast<const u32x4_t*>(kc + tok * D + ch);
+      s = page < 0 ? nan : sc[tok / kBlock];
+    }
+    const size_t at = (row0 + (size_t)tok * a.c.hkv) * D + ch;
+#pragma unroll
+    for (int e = 0; e < 4; ++e) store4<F32>(a.k, at + 4 * e, q[e], s);
+  }
+  for (int c = threadIdx.x; c < D; c += 256) {   // (channel quad, token quad)
+    const int quad = c & 3, d = c >> 2 << 2;
+    u32x4_t v[4];
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      v[e] = u32x4_t{0u, 0u, 0u, 0u};
+      if (have > 0) v[e] = *reinterpret_cast<const u32x4_t*>(kc + kPage * D + (d + e) * 64 + quad * 16);
+    }
+#pragma unroll
+    for (int blk = 0; blk < 4; ++blk) {
+      const float s = page < 0 ? nan : kBlock * blk < have ? sc[4 + blk] : 0.0f;
+      // a, b: tokens 0, 1 / 2, 3 of channels 0, 1 and 2, 3
+      const uint32_t a01 = __builtin_amdgcn_perm(v[1][blk], v[0][blk], 0x05010400u);   // t0c0 t0c1 t1c0 t1c1
+      const uint32_t a23 = __builtin_amdgcn_perm(v[1][blk], v[0][blk], 0x07030602u);
+      const uint32_t b01 = __builtin_amdgcn_perm(v[3][blk], v[2][blk], 0x05010400u);
+      const uint32_t b23 = __builtin_amdgcn_perm(v[3][blk], v[2][blk], 0x07030602u);
+      const uint32_t o[4] = {__builtin_amdgcn_perm(b01, a01, 0x05040100u), __builtin_amdgcn_perm(b01, a01, 0x07060302u),
+                             __builtin_amdgcn_perm(b23, a23, 0x05040100u), __builtin_amdgcn_perm(b23, a23, 0x07060302u)};
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        const int tok = kBlock * blk + 4 * quad + e;
+        if (tok < left)
+          store4<F32>(a.v, (row0 + (size_t)tok * a.c.hkv) * D + d, tok < have ? o[e] : 0u, tok < have ? s : 0.0f);
+      }
+    }
+  }
+}
+
+hipError_t launch_kv8_append(const Kv8Args& c, const void* k, int64_t k_ts, int64_t k_hs, const void* v, int64_t v_ts,
+                             int64_t v_hs, int64_t max_new, uint32_t* status, hipStream_t stream) {
+  const AppendArgs a{c, static_cast<const uint16_t*>(k), static_cast<const uint16_t*>(v), k_ts, k_hs, v_ts, v_hs, status};
+  // max_new tokens that start anywhere in a page reach at most this many pages
+  const dim3 grid((uint32_t)(c.b * c.hkv), (uint32_t)((max_new + kPage - 2) / kPage + 1));
+  switch (c.d) {
+#define QG_APP(D) \
+  case D: hipLaunchKernelGGL((kv8_append_kernel<D>), grid, dim3(256), 0, stream, a); break;
+    QG_APP(64) QG_APP(128) QG_APP(192) QG_APP(256)
+#undef QG_APP
+    default: return hipErrorInvalidValue;
+  }
+  return hipGetLastError();
+}
+
+hipError_t launch_kv8_read(const Kv8Args& c, int64_t max_len, void* k, void* v, int f32, hipStream_t stream) {
+  const ReadArgs a{c, max_len, k, v};
+  const dim3 grid((uint32_t)(c.b * c.hkv), (uint32_t)((max_len + kPage - 1) / kPage));
+  switch (c.d) {
+#define QG_READ(D)                                                                                      \
+  case D:                                                                                               \
+    if (f32) hipLaunchKernelGGL((kv8_read_kernel<D, true>), grid, dim3(256), 0, stream, a);             \
+    else hipLaunchKernelGGL((kv8_read_kernel<D, false>), grid, dim3(256), 0, stream, a);                \
+    break;
+    QG_READ(64) QG_READ(128) QG_READ(192) QG_READ(256)
+#undef QG_READ
+    default: return hipErrorInvalidValue;
+  }
+  return hipGetLastError();
+}
+
+}  // namespace qg

@@ -96,12 +96,16 @@ enum qg_status {
     QG_E_DTYPE = -8,       /* y_dtype is not QG_BF16 / QG_F32 */
     QG_E_HIP = -9,         /* a HIP launch failed */
     QG_E_BITS = -10,       /* a code width other than 5 or 6 (INT5 / INT6 entry points) */
-    QG_E_SCRATCH = -11     /* qgemm_w4a16_noalloc: the split's partial sums exceed QG_SCRATCH_BYTES */
+    QG_E_SCRATCH = -11,    /* qgemm_w4a16_noalloc: the split's partial sums exceed QG_SCRATCH_BYTES */
+    QG_E_HEADS = -12,      /* a head size, head count or rotated width the decoder-layer operators do not take */
+    QG_E_STRIDE = -13      /* a stride that is no multiple of 8 elements, or is too small */
 };
 
 /* status_dev flag bits */
 #define QG_FLAG_NONFINITE 1u   /* a weight group/row held Inf or NaN */
 #define QG_FLAG_OVERFLOW 2u    /* an INT4 group's range exceeded 15 * 65504 */
+#define QG_FLAG_POSITION 4u    /* qg_qk_norm_rope: a position outside the table */
+#define QG_FLAG_PAGE 8u        /* the cache calls: a page that the table or the cache does not hold */
 
 /* Human-readable name of a qg_status value (static string). */
 const char *qg_status_string(int32_t status);
@@ -356,6 +360,116 @@ int32_t qgemm_w4a8_dq(const void *x_bf16, int64_t m, int64_t k, const void *pack
 int32_t qgemm_w4a8_g32_dq(const void *x_bf16, int64_t m, int64_t k, const void *packed,
                           int64_t packed_bytes, int64_t n, void *y, int32_t y_dtype,
                           int32_t split_k, void *ws, int64_t ws_bytes, void *stream);
+
+/* ==========================================================================
+ * Operators of a decoder layer around the quantized linears.  They follow the
+ * conventions above (device pointers, caller's stream and buffers, checks
+ * before any launch, bit-identical repeats).  They are this library's own:
+ * the pages it implements stop at the linear layer.
+ * ======================================================================= */
+
+/* ---- qg_qk_norm_rope -----------------------------------------------------
+ * RMS norm of every query and key head and the rotation of its first `rot`
+ * channels by position, in one pass, fp32, rounded once to bf16:
+ *   x' = x * rsqrt(mean(x^2) + eps) * w
+ *   (a, b) -> (a cos - b sin, b cos + a sin)
+ * with (a, b) = channels (i, rot/2 + i), or (2i, 2i + 1) where adjacent_pairs
+ * is not 0, and cos, sin = cos_sin[position][i], cos_sin[position][rot/2 + i].
+ *   q, k       in : bf16 [tokens, hq, d] and [tokens, hkv, d]; strides in
+ *                   elements per token and per head (multiples of 8; channels
+ *                   contiguous), so both may be columns of one projection
+ *   q_w, k_w   in : bf16 [d], or NULL for a norm without weights
+ *   cos_sin    in : fp32 [max_pos, rot]       positions in : int32 [tokens]
+ *   q_out      out: bf16 [tokens, hq, d], k_out bf16 [tokens, hkv, d]
+ *   status_dev    : QG_FLAG_POSITION where a position is outside [0, max_pos)
+ *                   (that token's heads become NaN); may be NULL
+ * d: a multiple of 16 up to 512; rot: a multiple of 16 up to d (0: no
+ * rotation).  tokens = 0 is fine; so are hq = 0 or hkv = 0 with their
+ * pointers NULL.
+ * Errors: QG_E_NULL, QG_E_SHAPE, QG_E_HEADS, QG_E_STRIDE, QG_E_ALIGN. */
+int32_t qg_qk_norm_rope(const void *q, int64_t q_token_stride, int64_t q_head_stride, const void *k,
+                        int64_t k_token_stride, int64_t k_head_stride, int64_t tokens, int32_t hq,
+                        int32_t hkv, int32_t d, const void *q_w, const void *k_w, const float *cos_sin,
+                        int64_t max_pos, int32_t rot, int32_t adjacent_pairs, const int32_t *positions,
+                        float eps, void *q_out, void *k_out, uint32_t *status_dev, void *stream);
+
+/* ---- the 8-bit key/value cache -------------------------------------------
+ * Pages of 64 tokens of every key/value head, as int8 codes with one fp32
+ * scale per block of 16 tokens, head, and keys / values; a value is code *
+ * scale.  d is 64, 128, 192 or 256.
+ *   codes  int8 [pages, hkv, 2, 64 d]: keys, then values.  Channel c of token
+ *          t of the page: keys at t d + c; values at
+ *          64 c + 16 ((t % 16) / 4) + 4 (t / 16) + t % 4
+ *          (a channel's 64 tokens together, in the order in which one lane of
+ *          the attention kernel needs them).
+ *   scales fp32 [pages, hkv, 2, 4]: block t / 16.
+ * A sequence's tokens [64 i, 64 i + 64) are in page block_table[b][i] (int32
+ * [b, table_width]; entries past its length are not read).  lens: int32 [b],
+ * tokens of each sequence.  Rows of new tokens or queries lie one sequence
+ * after another: sequence b has rows cu[b] .. cu[b + 1] - 1 (int32 [b + 1]),
+ * or rows / b each where cu is NULL (rows a multiple of b); they are its last
+ * tokens, so the last row is token lens[b] - 1.  Rows before token 0 (more
+ * rows than tokens) are skipped by the append and see nothing.
+ * A page that is not there (a table column past table_width, or an entry
+ * outside [0, pages)) is never read or written: its tokens are lost to an
+ * append and NaN to a read or an attention; QG_FLAG_PAGE is set. */
+#define QG_KV8_PAGE 64
+#define QG_KV8_BLOCK 16
+
+/* Quantizes rows of new keys and values into the cache.  For a block of 16
+ * tokens, s_held its scale where it holds a token from before this call (else
+ * 0), a = max |x| over its new tokens, in binary32:
+ *   s = max(s_held, a * (1/127));  held codes q <- rint(q * (s_held / s))
+ *   where s > s_held;  new codes q = clamp(rint(x / s), -127, 127), 0 for s = 0.
+ * A new value that is an infinity or a NaN makes its block's scale NaN.
+ * Codes after the last token of a written block are unspecified.  Writing the
+ * same rows again changes nothing.  A page belongs to one sequence of a call.
+ *   k, v       in : bf16 [rows, hkv, d], strides as qg_qk_norm_rope
+ *   lens       in : lengths with the new tokens counted
+ *   max_new    in : no sequence has more new rows (later ones are not written)
+ *   status_dev    : QG_FLAG_NONFINITE, QG_FLAG_PAGE; may be NULL
+ * Errors: QG_E_NULL, QG_E_SHAPE, QG_E_HEADS, QG_E_STRIDE, QG_E_ALIGN. */
+int32_t qg_kv8_append(const void *k, int64_t k_token_stride, int64_t k_head_stride, const void *v,
+                      int64_t v_token_stride, int64_t v_head_stride, int64_t rows, int8_t *codes,
+                      float *scales, int64_t pages, int32_t hkv, int32_t d, const int32_t *block_table,
+                      int64_t table_width, const int32_t *lens, const int32_t *cu, int64_t b,
+                      int64_t max_new, uint32_t *status_dev, void *stream);
+
+/* Reads sequences back: k_out, v_out [b, max_len, hkv, d] in bf16 or fp32
+ * (out_dtype); tokens at or past a sequence's length are zero. */
+int32_t qg_kv8_read(const int8_t *codes, const float *scales, int64_t pages, int32_t hkv, int32_t d,
+                    const int32_t *block_table, int64_t table_width, const int32_t *lens, int64_t b,
+                    int64_t max_len, void *k_out, void *v_out, int32_t out_dtype, void *stream);
+
+/* ---- qg_attn_kv8 ---------------------------------------------------------
+ * Attention of every query row over its sequence in the cache:
+ *   out[r, h] = sum_j softmax_j(scale * q[r, h] . k_j) v_j
+ * over the tokens j <= p (the row's own token p) and, where window > 0,
+ * j > p - window; head h of hq reads key/value head h / (hq / hkv).  A row
+ * that sees no token (length 0, or a row before token 0) is zero.  Softmax and
+ * sums are fp32; the products' operands are bf16: q, the codes (exact), and
+ * probability times value scale (rounded once).
+ *   q        in : bf16 [rows, hq, d], strides as qg_qk_norm_rope
+ *   max_q    in : no sequence has more query rows (later ones are not written)
+ *   max_len  in : an upper bound of lens, for the choice of the split only
+ *   out      out: [rows, hq, d], bf16 or fp32 (out_dtype)
+ *   splits   in : workgroups that share a sequence's pages, 1..256; 0 lets
+ *                 the library choose
+ *   ws          : qg_attn_kv8_workspace_bytes(...) bytes, NULL allowed for 0
+ *   status_dev  : QG_FLAG_PAGE; may be NULL
+ * Rows are query tokens of decode: 1 for a step, a few for the verification of
+ * drafted tokens.  Longer chunks are right, but every 32 of a head's rows read
+ * the cache anew.
+ * Errors: QG_E_NULL, QG_E_SHAPE, QG_E_HEADS, QG_E_STRIDE, QG_E_ALIGN,
+ * QG_E_DTYPE, QG_E_SPLIT, QG_E_BUFFER. */
+int64_t qg_attn_kv8_workspace_bytes(int64_t b, int64_t rows, int32_t hq, int32_t hkv, int32_t d,
+                                    int64_t max_q, int64_t max_len, int32_t window, int32_t splits);
+int32_t qg_attn_kv8(const void *q, int64_t q_token_stride, int64_t q_head_stride, int64_t rows, int32_t hq,
+                    const int8_t *codes, const float *scales, int64_t pages, int32_t hkv, int32_t d,
+                    const int32_t *block_table, int64_t table_width, const int32_t *lens, const int32_t *cu,
+                    int64_t b, int64_t max_q, int64_t max_len, int32_t window, float scale, void *out,
+                    int32_t out_dtype, int32_t splits, void *ws, int64_t ws_bytes, uint32_t *status_dev,
+                    void *stream);
 
 /* ---- qg_stream_read (measurement helper, not part of the layer) ---------
  * Reads `bytes` bytes of device memory at `src` once, with one 16-byte

@@ -1,0 +1,209 @@
+"""qg_attn_kv8 against attention in 64 bits over the cache's values.
+
+Tolerance per output, with A = sum of p |v| in 64 bits: the products' operands
+round p * scale to bf16 (2^-8 of each term at most), scores carry binary32
+rounding (below 2^-12 of p for these inputs: 256 products of magnitude about
+10 in all), so |err| <= (2^-8 + 2^-11) A, plus half a bf16 unit where the
+output is bf16."""
+from __future__ import annotations
+
+import numpy as np
+import pytest
+import torch
+
+import layer_reference as ref
+
+import gemm_decode_qgemm_amd as qg
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(scope="module")
+def dev():
+    assert torch.cuda.is_available(), "GPU tests need a HIP device"
+    return torch.device("cuda:0")
+
+
+class Filled:
+    """A cache with random codes and scales for sequences of the given lengths;
+    blocks past a length hold scales of NaN, as memory never written may."""
+
+    def __init__(self, dev, lens, hkv, d, seed, spare=1):
+        g = torch.Generator().manual_seed(seed)
+        width = max(1, -(-max(lens) // 64)) + spare
+        need = [-(-n // 64) for n in lens]
+        pages = sum(need) + 3
+        order = torch.randperm(pages, generator=g).to(torch.int32)
+        self.table = torch.full((len(lens), width), -1, dtype=torch.int32)
+        at = 0
+        for b, n in enumerate(need):
+            self.table[b, :n] = order[at:at + n]
+            at += n
+        self.host = ref.Cache(pages, hkv, d, self.table.numpy())
+        self.host.codes[:] = torch.randint(-127, 128, self.host.codes.shape, generator=g).numpy()
+        self.host.scales[:] = np.nan
+        for b, n in enumerate(lens):
+            for blk in range(-(-n // 16)):
+                p = self.table[b, blk // 4].item()
+                self.host.scales[p, :, :, blk % 4] = (0.01 + 0.03 * torch.rand(hkv, 2, generator=g)).numpy()
+        self.codes, self.scales = torch.from_numpy(self.host.codes).to(dev), torch.from_numpy(self.host.scales).to(dev)
+        self.table_d = self.table.to(dev)
+        self.lens = lens
+        self.lens_d = torch.tensor(lens, dtype=torch.int32, device=dev)
+        self.args = (self.codes, self.scales, self.table_d, self.lens_d)
+        self.values = None
+
+    def reference(self, q, counts, scale, window):
+        if self.values is None:
+            self.values = [(self.host.values(b, n, 0), self.host.values(b, n, 1)) for b, n in enumerate(self.lens)]
+        out, mass, at = [], [], 0
+        for b, c in enumerate(counts):
+            o, a = ref.attention(q[at:at + c], *self.values[b], self.lens[b], scale, window)
+            at += c
+            out.append(o)
+            mass.append(a)
+        return np.concatenate(out), np.concatenate(mass)
+
+
+def check(y, want, mass):
+    got = ref.f64(y)
+    assert np.isfinite(got).all()
+    tol = mass * (2.0 ** -8 + 2.0 ** -11) + 1e-30
+    if y.dtype == torch.bfloat16:
+        tol = tol + ref.half_ulp_bf16(np.abs(want) + tol)
+    err = np.abs(got - want)
+    assert (err <= tol).all(), float((err / tol).max())
+    assert not got[mass.sum(-1) == 0].any()
+
+
+def cu_of(counts, dev):
+    return torch.tensor(np.cumsum([0] + counts), dtype=torch.int32, device=dev)
+
+
+@pytest.mark.parametrize("hq,hkv,d", [(4, 4, 64), (8, 1, 64), (12, 2, 128), (32, 1, 128), (5, 1, 192), (17, 1, 192),
+                                      (4, 2, 256), (24, 1, 256)])
+@pytest.mark.parametrize("window", [0, 40])
+def test_one_query_row_over_every_length(dev, hq, hkv, d, window):
+    lens = [0, 1, 15, 16, 17, 63, 64, 65, 129, 200, 383, 2]
+    f = Filled(dev, lens, hkv, d, d + hq)
+    torch.manual_seed(d)
+    q = torch.randn(len(lens), hq, d).bfloat16()
+    want, mass = f.reference(ref.f64(q), [1] * len(lens), d ** -0.5, window)
+    for splits in (0, 1, 2, 5):
+        for dt in (torch.float32, torch.bfloat16):
+            check(qg.attn_kv8(q.to(dev), *f.args, window=window, splits=splits, out_dtype=dt), want, mass)
+
+
+@pytest.mark.parametrize("hq,hkv,d", [(6, 1, 64), (8, 2, 128), (3, 3, 192), (2, 1, 256)])
+@pytest.mark.parametrize("window", [0, 1, 70])
+def test_several_query_rows_ragged_and_uniform(dev, hq, hkv, d, window):
+    lens, counts = [0, 3, 64, 70, 150, 5, 130], [2, 5, 1, 7, 0, 5, 64]   # more rows than tokens among them
+    f = Filled(dev, lens, hkv, d, d)
+    torch.manual_seed(hq)
+    q = torch.randn(sum(counts), hq, d).bfloat16()
+    want, mass = f.reference(ref.f64(q), counts, 0.2, window)
+    cu = cu_of(counts, dev)
+    for splits in (0, 1, 3):
+        check(qg.attn_kv8(q.to(dev), *f.args, cu=cu, max_q=64, window=window, scale=0.2, splits=splits), want, mass)
+    check(qg.attn_kv8(q.to(dev), *f.args, cu=cu, window=window, scale=0.2, out_dtype=torch.float32), want, mass)
+    counts = [9] * len(lens)
+    q = torch.randn(sum(counts), hq, d).bfloat16()
+    want, mass = f.reference(ref.f64(q), counts, d ** -0.5, window)
+    for splits in (0, 2):
+        check(qg.attn_kv8(q.to(dev), *f.args, window=window, splits=splits), want, mass)
+
+
+def test_long_cache_many_splits_and_repeatability(dev):
+    lens = [5000, 1]
+    f = Filled(dev, lens, 1, 128, 5)
+    torch.manual_seed(5)
+    q = torch.randn(2, 20, 128).bfloat16()
+    want, mass = f.reference(ref.f64(q), [1, 1], 128 ** -0.5, 0)
+    for splits in (0, 1, 79, 256):
+        a = qg.attn_kv8(q.to(dev), *f.args, splits=splits, out_dtype=torch.float32)
+        check(a, want, mass)
+        for _ in range(3):
+            assert torch.equal(a, qg.attn_kv8(q.to(dev), *f.args, splits=splits, out_dtype=torch.float32))
+
+
+def test_large_scores_keep_the_softmax_in_range(dev):
+    """Scores of several thousand: the maximum moves at almost every page."""
+    f = Filled(dev, [700], 2, 64, 6)
+    torch.manual_seed(6)
+    q = (torch.randn(1, 4, 64) * 300).bfloat16()
+    # binary32 scores of 10^4 carry 2^-10: p is off by up to that, besides the bf16 operand
+    want, mass = f.reference(ref.f64(q), [1], 1.0, 0)
+    got = ref.f64(qg.attn_kv8(q.to(dev), *f.args, scale=1.0, out_dtype=torch.float32))
+    tol = mass * (2.0 ** -8 + 2.0 ** -7) + 1e-30
+    assert (np.abs(got - want) <= tol).all()
+
+
+def test_a_nan_block_reaches_only_the_rows_that_see_it(dev):
+    f = Filled(dev, [100], 1, 64, 7)
+    page = f.table[0, 1].item()
+    q = torch.randn(40, 2, 64, device=dev).bfloat16()       # rows at tokens 60 .. 99
+    for which in (0, 1):
+        scales = f.scales.clone()
+        scales[page, 0, which, 1] = float("nan")             # tokens 80 .. 95
+        for splits in (1, 2):
+            y = qg.attn_kv8(q, f.codes, scales, f.table_d, f.lens_d, splits=splits)
+            bad = y.isnan().any(2).any(1).tolist()
+            assert bad == [t >= 80 for t in range(60, 100)]
+
+
+def test_pages_that_are_not_there_are_nan_and_flagged(dev):
+    f = Filled(dev, [100, 100, 30], 1, 64, 8, spare=0)
+    q = torch.randn(3, 2, 64, device=dev).bfloat16()
+    flag = torch.zeros(1, dtype=torch.int32, device=dev)
+    want = qg.attn_kv8(q, *f.args, status=flag)
+    assert flag.item() == 0 and not want.isnan().any()
+    table = f.table_d.clone()
+    table[0, 0] = f.codes.shape[0]
+    lens = f.lens_d.clone()
+    lens[1] = 2_000_000_000                                   # far past the table's two columns
+    for splits in (1, 3):
+        y = qg.attn_kv8(q, f.codes, f.scales, table, lens, status=flag, splits=splits)
+        assert y[0].isnan().all() and y[1].isnan().all()
+        assert flag.item() == qg.FLAG_PAGE
+    assert torch.equal(qg.attn_kv8(q, f.codes, f.scales, table, lens, splits=1)[2],
+                       qg.attn_kv8(q, *f.args, splits=1)[2])
+
+
+def test_negative_lengths_and_rows_of_no_sequence(dev):
+    f = Filled(dev, [20, 20], 1, 64, 9)
+    q = torch.randn(7, 2, 64, device=dev).bfloat16()
+    lens = torch.tensor([-5, 20], dtype=torch.int32, device=dev)
+    out = torch.full((7, 2, 64), 3.0, dtype=torch.bfloat16, device=dev)
+    cu = torch.tensor([1, 3, 5], dtype=torch.int32, device=dev)
+    for splits in (1, 2):
+        out.fill_(3.0)
+        qg.attn_kv8(q, f.codes, f.scales, f.table_d, lens, cu=cu, max_q=2, out=out, splits=splits)
+        assert (out[[0, 5, 6]] == 3.0).all() and not out[1:3].any() and out[3:5].any()
+
+
+def test_strided_queries_side_stream_and_graph(dev):
+    torch.manual_seed(10)
+    lens = [300, 77, 0]
+    f = Filled(dev, lens, 2, 128, 10)
+    fused = torch.randn(3, 10 * 128, device=dev).bfloat16()
+    q = fused[:, :1024].unflatten(1, (8, 128))
+    for splits in (1, 3):
+        want = qg.attn_kv8(q.contiguous(), *f.args, splits=splits)
+        out = torch.empty_like(want)
+        s = torch.cuda.Stream()
+        s.wait_stream(torch.cuda.current_stream())
+        with torch.cuda.stream(s):
+            qg.attn_kv8(q, *f.args, out=out, splits=splits)
+        s.synchronize()
+        assert torch.equal(out, want)
+        ws = torch.empty(qg.attn_kv8_workspace_bytes(3, 3, 8, 2, 128, 1, 300, splits=splits) + 16, dtype=torch.uint8, device=dev)
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            qg.attn_kv8(q, *f.args, out=out, splits=splits, workspace=ws)
+        for i in range(3):
+            out.fill_(9.0)
+            ws.fill_(255)                                     # whatever the workspace held
+            torch.cuda.synchronize()
+            g.replay()
+            torch.cuda.synchronize()
+            assert torch.equal(out, want)
