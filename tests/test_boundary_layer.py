@@ -67,7 +67,7 @@ def test_cache_refusals(call, kw, want):
 
 @pytest.mark.parametrize("kw,want", [
     (dict(k=None), E_NULL), (dict(v=None), E_NULL), (dict(rows=-1), E_SHAPE), (dict(rows=3), E_SHAPE), (dict(max_new=-1), E_SHAPE),
-    (dict(max_new=1 << 40), E_SHAPE), (dict(kts=128), E_STRIDE), (dict(vhs=64), E_STRIDE), (dict(kts=260), E_STRIDE),
+    (dict(max_new=1 << 40), E_SHAPE), (dict(kts=64), E_STRIDE), (dict(vhs=64), E_STRIDE), (dict(kts=260), E_STRIDE),
     (dict(k=U), E_ALIGN), (dict(v=U), E_ALIGN), (dict(cu=A + 2), E_ALIGN), (dict(status=A + 2), E_ALIGN),
     (dict(rows=0, k=None, v=None), OK), (dict(max_new=0), OK)])
 def test_append_refusals(kw, want):
@@ -86,7 +86,7 @@ def test_read_refusals(kw, want):
     (dict(max_len=-1), E_SHAPE), (dict(window=-1), E_SHAPE), (dict(scale=float("nan")), E_SHAPE), (dict(scale=float("inf")), E_SHAPE),
     (dict(hq=7), E_HEADS), (dict(hq=0), E_HEADS), (dict(dt=7), E_DTYPE), (dict(splits=-1), E_SPLIT), (dict(splits=257), E_SPLIT),
     (dict(splits=2), E_NULL), (dict(splits=2, ws=A, ws_bytes=2 * 4 * 8 * 130 * 4 - 1), E_BUF), (dict(ws=U), E_ALIGN),
-    (dict(qts=512), E_STRIDE), (dict(qhs=12), E_STRIDE), (dict(q=U), E_ALIGN), (dict(out=U), E_ALIGN), (dict(status=A + 2), E_ALIGN),
+    (dict(qts=64), E_STRIDE), (dict(qhs=12), E_STRIDE), (dict(q=U), E_ALIGN), (dict(out=U), E_ALIGN), (dict(status=A + 2), E_ALIGN),
     (dict(rows=0), OK)])
 def test_attn_refusals(kw, want):
     assert attn(**kw) == want
