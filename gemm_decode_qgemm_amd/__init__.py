@@ -26,6 +26,8 @@ from .binding import (  # noqa: F401
     kv8_append,
     kv8_empty,
     kv8_read,
+    moe_w4a16,
+    moe_w4a16_workspace_bytes,
     qgemm_w4a8,
     qgemm_w4a8_dq,
     qgemm_w4a8_g32,

@@ -74,6 +74,8 @@ def _load() -> ctypes.CDLL:
         "qg_attn_kv8_workspace_bytes": (I64, [I64, I64, I32, I32, I32, I64, I64, I32, I32]),
         "qg_attn_kv8": (I32, [P, I64, I64, I64, I32, P, P, I64, I32, I32, P, I64, P, P, I64, I64, I64, I32,
                               ctypes.c_float, P, I32, I32, P, I64, P, P]),
+        "qg_moe_w4a16_workspace_bytes": (I64, [I64, I64, I64, I64, I64]),
+        "qg_moe_w4a16": (I32, [P, I64, I64, P, I64, P, I64, P, I64, I64, I64, I32, P, I32, P, I64, P]),
     }
     for name, (res, args) in sigs.items():
         fn = getattr(lib, name)
@@ -562,3 +564,39 @@ def attn_kv8(q: torch.Tensor, codes: torch.Tensor, scales: torch.Tensor, block_t
                          _flags(status), _stream(q.device))
     _check(st, "qg_attn_kv8")
     return out
+
+
+def moe_w4a16_workspace_bytes(t: int, h: int, e: int, inter: int, top_k: int) -> int:
+    v = int(lib.qg_moe_w4a16_workspace_bytes(t, h, e, inter, top_k))
+    _check(min(v, 0), "qg_moe_w4a16_workspace_bytes")
+    return v
+
+
+def moe_w4a16(x: torch.Tensor, router: torch.Tensor, gate_up: torch.Tensor, down: torch.Tensor, inter: int,
+              top_k: int, *, renormalize: bool = True, out_dtype: torch.dtype = torch.bfloat16,
+              out: torch.Tensor | None = None, workspace: torch.Tensor | None = None) -> torch.Tensor:
+    """A mixture-of-experts layer for up to 64 tokens: x [t, h], router [e, h]
+    (bf16), gate_up and down uint8 [e, bytes] of quantize_int4_g32 weights
+    (2 inter x h, gate rows first; h x inter) -> y [t, h]."""
+    _dev(x, "x", torch.bfloat16, 2)
+    _dev(router, "router", torch.bfloat16, 2)
+    _dev(gate_up, "gate_up", torch.uint8, 2)
+    _dev(down, "down", torch.uint8, 2)
+    t, h = x.shape
+    e = router.shape[0]
+    if router.shape[1] != h or gate_up.shape[0] != e or down.shape[0] != e:
+        raise ValueError("router must be [e, h], gate_up and down [e, bytes]")
+    need = moe_w4a16_workspace_bytes(t, h, e, inter, top_k)
+    if gate_up.shape[1] != int4_packed_bytes(2 * inter, h) or down.shape[1] != int4_packed_bytes(h, inter):
+        raise ValueError("gate_up must hold packed 2 inter x h weights and down packed h x inter ones")
+    y, yd = _out(t, h, out_dtype, x.device, out)
+    if tuple(y.shape) != (t, h):
+        raise ValueError("out must be [t, h]")
+    if workspace is None:
+        workspace = torch.empty(need, dtype=torch.uint8, device=x.device)
+    _same_device(x.device, router=router, gate_up=gate_up, down=down, out=y, workspace=workspace)
+    st = lib.qg_moe_w4a16(x.data_ptr(), t, h, router.data_ptr(), e, gate_up.data_ptr(), gate_up.numel(), down.data_ptr(),
+                          down.numel(), inter, top_k, int(renormalize), y.data_ptr(), yd, workspace.data_ptr(),
+                          workspace.numel() * workspace.element_size(), _stream(x.device))
+    _check(st, "qg_moe_w4a16")
+    return y

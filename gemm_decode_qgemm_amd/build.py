@@ -26,7 +26,8 @@ OBJDIR = os.path.join(PKG, "_build")
 
 SOURCES = ["api.hip", "quantize.hip", "gemv_w4a16.hip", "gemv_w8a16.hip", "gemv_w4a8.hip",
            "gemm_w4a16_mfma.hip", "gemv_w4a16_mx4.hip", "stream_read.hip",
-           "gemm_w8a16_mfma.hip", "api_layer.hip", "qk_norm_rope.hip", "kv8_cache.hip", "attn_kv8.hip"]
+           "gemm_w8a16_mfma.hip", "api_layer.hip", "qk_norm_rope.hip", "kv8_cache.hip", "attn_kv8.hip",
+           "moe_w4a16.hip"]
 
 HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")
 FLAGS = [
@@ -46,7 +47,8 @@ SOURCE_FLAGS = {"gemm_w4a16_mfma.hip": ["-mllvm", "-amdgpu-mfma-vgpr-form"],
                 "gemv_w4a16_mx4.hip": ["-mllvm", "-amdgpu-mfma-vgpr-form"],
                 "gemv_w4a8.hip": ["-mllvm", "-amdgpu-mfma-vgpr-form"],
                 "gemm_w8a16_mfma.hip": ["-mllvm", "-amdgpu-mfma-vgpr-form"],
-                "attn_kv8.hip": ["-mllvm", "-amdgpu-mfma-vgpr-form"]}
+                "attn_kv8.hip": ["-mllvm", "-amdgpu-mfma-vgpr-form"],
+                "moe_w4a16.hip": ["-mllvm", "-amdgpu-mfma-vgpr-form"]}
 
 
 def _compile(src: str, extra: list[str], objdir: str) -> str:

@@ -16,6 +16,10 @@ int attn_kv8_splits(int64_t b, int hkv, int64_t rows_per_head, int64_t max_len, 
 hipError_t launch_attn_kv8(const Kv8Args& c, const void* q, int64_t q_ts, int64_t q_hs, int hq, int max_q, int window,
                            float scale, void* out, int out_f32, int splits, float* part, uint32_t* status,
                            hipStream_t stream);
+int64_t moe_ws_bytes(int64_t t, int64_t h, int64_t e, int64_t inter, int64_t k);
+hipError_t launch_moe_w4a16(const void* x, int t, int h, const void* router, int e, const void* gate_up,
+                            int64_t gate_up_bytes, const void* down, int64_t down_bytes, int inter, int k, int renorm,
+                            void* y, int y_f32, void* ws, hipStream_t stream);
 }  // namespace qg
 
 namespace {
@@ -24,6 +28,7 @@ constexpr int64_t kMaxRows = (int64_t)1 << 30;   // tokens, positions, lengths
 constexpr int64_t kMaxGrid = 65535;              // the y and z extents of a grid
 constexpr int32_t kMaxHeads = 4096;
 constexpr int32_t kMaxSplits = 256;
+constexpr int64_t kMaxDim = (int64_t)1 << 20;    // channels and hidden columns of an expert
 
 bool aligned(const void* p, uintptr_t n) { return ((uintptr_t)p & (n - 1)) == 0; }
 
@@ -76,6 +81,16 @@ int32_t attn_shape(int64_t b, int64_t rows, int32_t hq, int32_t hkv, int32_t d, 
 
 int64_t attn_ws(int64_t rows, int32_t hq, int32_t d, int splits) {
   return splits > 1 ? (int64_t)splits * rows * hq * (d + 2) * 4 : 0;
+}
+
+constexpr int64_t kMaxExperts = 512, kMaxPicks = 32;
+
+// The shape rules of qg_moe_w4a16.
+int32_t moe_shape(int64_t t, int64_t h, int64_t e, int64_t inter, int64_t k) {
+  if (t < 0 || h < 1 || inter < 1 || h > kMaxDim || inter > kMaxDim) return QG_E_SHAPE;
+  if (e < 1 || e > kMaxExperts || k < 1 || k > kMaxPicks || k > e) return QG_E_SHAPE;
+  if (h % QG_TILE_K != 0 || inter % QG_TILE_K != 0) return QG_E_K_MULTIPLE;
+  return t > QG_MAX_M ? QG_E_M_RANGE : QG_OK;
 }
 
 }  // namespace
@@ -177,6 +192,30 @@ int32_t qg_attn_kv8(const void* q, int64_t q_ts, int64_t q_hs, int64_t rows, int
   const qg::Kv8Args c = cache_args(codes, scales, pages, hkv, d, block_table, table_width, lens, cu, rows, b);
   return hip_status(qg::launch_attn_kv8(c, q, q_ts, q_hs, hq, (int)max_q, window, scale, out, out_dtype == QG_F32, s,
                                         static_cast<float*>(ws), status_dev, static_cast<hipStream_t>(stream)));
+}
+
+int64_t qg_moe_w4a16_workspace_bytes(int64_t t, int64_t h, int64_t e, int64_t inter, int64_t top_k) {
+  const int32_t st = moe_shape(t, h, e, inter, top_k);
+  return st != QG_OK ? st : qg::moe_ws_bytes(t, h, e, inter, top_k);
+}
+
+int32_t qg_moe_w4a16(const void* x_bf16, int64_t t, int64_t h, const void* router_bf16, int64_t e, const void* gate_up,
+                     int64_t gate_up_bytes, const void* down, int64_t down_bytes, int64_t inter, int64_t top_k,
+                     int32_t renormalize, void* y, int32_t y_dtype, void* ws, int64_t ws_bytes, void* stream) {
+  const int32_t st = moe_shape(t, h, e, inter, top_k);
+  if (st != QG_OK) return st;
+  if (y_dtype != QG_BF16 && y_dtype != QG_F32) return QG_E_DTYPE;
+  const int64_t gu = qg_int4_packed_bytes(2 * inter, h), dn = qg_int4_packed_bytes(h, inter);
+  if (gate_up_bytes < e * gu || down_bytes < e * dn) return QG_E_BUFFER;
+  if (!aligned(x_bf16, 16) || !aligned(router_bf16, 16) || !aligned(gate_up, 16) || !aligned(down, 16) ||
+      !aligned(y, 16) || !aligned(ws, 16))
+    return QG_E_ALIGN;
+  if (t == 0) return QG_OK;
+  if (!x_bf16 || !router_bf16 || !gate_up || !down || !y || !ws) return QG_E_NULL;
+  if (ws_bytes < qg::moe_ws_bytes(t, h, e, inter, top_k)) return QG_E_BUFFER;
+  return hip_status(qg::launch_moe_w4a16(x_bf16, (int)t, (int)h, router_bf16, (int)e, gate_up, gu, down, dn,
+                                         (int)inter, (int)top_k, renormalize != 0, y, y_dtype == QG_F32, ws,
+                                         static_cast<hipStream_t>(stream)));
 }
 
 }  // extern "C"

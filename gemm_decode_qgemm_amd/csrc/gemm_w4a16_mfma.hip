@@ -39,18 +39,6 @@
 namespace qg {
 
 
-// (row r, register j) -> (row j, register r) over the wave's four 16-lane rows:
-// v_permlane32_swap exchanges the upper 32 lanes of its first operand with the
-// lower 32 of its second, v_permlane16_swap the odd 16-lane rows of the first
-// with the even rows of the second (both checked on MI355X).
-__device__ __forceinline__ void transpose_rows4(u32x4_t& v) {
-  const auto s02 = __builtin_amdgcn_permlane32_swap(v.x, v.z, false, false);
-  const auto s13 = __builtin_amdgcn_permlane32_swap(v.y, v.w, false, false);
-  const auto t01 = __builtin_amdgcn_permlane16_swap(s02[0], s13[0], false, false);
-  const auto t23 = __builtin_amdgcn_permlane16_swap(s02[1], s13[1], false, false);
-  v = u32x4_t{t01[0], t01[1], t23[0], t23[1]};
-}
-
 // bf16 pairs (128 + q) of nibbles 2e, 2e+1 of a code dword, in plain C: the
 // result feeds an MFMA source operand, and the compiler must see the VALU op
 // that writes it to insert the wait states the MFMA read needs (an inline-asm

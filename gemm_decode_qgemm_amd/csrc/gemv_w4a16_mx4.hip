@@ -43,21 +43,6 @@
 
 namespace qg {
 
-typedef short s16x4_t __attribute__((ext_vector_type(4)));
-
-__device__ __forceinline__ f32x4_t mfma_4x4x4(u32x2_t a, u32x2_t b, f32x4_t c) {
-  return __builtin_amdgcn_mfma_f32_4x4x4bf16_1k(__builtin_bit_cast(s16x4_t, a),
-                                                __builtin_bit_cast(s16x4_t, b), c, 0, 0, 0);
-}
-
-// Two codes as the bf16 pair (128 + q(8d+2e), 128 + q(8d+2e+1)) in plain C:
-// the matrix instruction reads it, and an inline-asm VALU write ahead of a
-// matrix-instruction read hides the dependency from the compiler's hazard
-// tracking.  mask_s = 0x000F000F (an SGPR), magic_v = 0x43004300 (a VGPR).
-__device__ __forceinline__ uint32_t code_pair(uint32_t w, int e, uint32_t mask_s, uint32_t magic_v) {
-  return ((w >> (4 * e)) & mask_s) | magic_v;
-}
-
 // x rows in a wave's LDS slot: 288 bytes apart, groups 2-3 of a half tile 16
 // bytes after groups 0-1.  An A-operand read (fixed group and k-step) touches
 // at most 8 distinct 16-byte chunks, (row i, group pair) at 288 i + 144 pair

@@ -212,6 +212,33 @@ __device__ __forceinline__ void split_range(int tiles, int split, int s, int& t0
   t1 = t0 + base + (s < rem ? 1 : 0);
 }
 
+// (row r, register j) -> (row j, register r) over the wave's four 16-lane rows:
+// v_permlane32_swap exchanges the upper 32 lanes of its first operand with the
+// lower 32 of its second, v_permlane16_swap the odd 16-lane rows of the first
+// with the even rows of the second (both checked on MI355X).
+__device__ __forceinline__ void transpose_rows4(u32x4_t& v) {
+  const auto s02 = __builtin_amdgcn_permlane32_swap(v.x, v.z, false, false);
+  const auto s13 = __builtin_amdgcn_permlane32_swap(v.y, v.w, false, false);
+  const auto t01 = __builtin_amdgcn_permlane16_swap(s02[0], s13[0], false, false);
+  const auto t23 = __builtin_amdgcn_permlane16_swap(s02[1], s13[1], false, false);
+  v = u32x4_t{t01[0], t01[1], t23[0], t23[1]};
+}
+
+typedef short s16x4_t __attribute__((ext_vector_type(4)));
+
+__device__ __forceinline__ f32x4_t mfma_4x4x4(u32x2_t a, u32x2_t b, f32x4_t c) {
+  return __builtin_amdgcn_mfma_f32_4x4x4bf16_1k(__builtin_bit_cast(s16x4_t, a),
+                                                __builtin_bit_cast(s16x4_t, b), c, 0, 0, 0);
+}
+
+// Two codes as the bf16 pair (128 + q(8d+2e), 128 + q(8d+2e+1)) in plain C:
+// the matrix instruction reads it, and an inline-asm VALU write ahead of a
+// matrix-instruction read hides the dependency from the compiler's hazard
+// tracking.  mask_s = 0x000F000F (an SGPR), magic_v = 0x43004300 (a VGPR).
+__device__ __forceinline__ uint32_t code_pair(uint32_t w, int e, uint32_t mask_s, uint32_t magic_v) {
+  return ((w >> (4 * e)) & mask_s) | magic_v;
+}
+
 template <int CTRL>
 __device__ __forceinline__ float dpp_mov(float v) {
   return __builtin_bit_cast(float, __builtin_amdgcn_update_dpp(0, __builtin_bit_cast(int, v),

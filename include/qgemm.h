@@ -471,6 +471,30 @@ int32_t qg_attn_kv8(const void *q, int64_t q_token_stride, int64_t q_head_stride
                     int32_t out_dtype, int32_t splits, void *ws, int64_t ws_bytes, uint32_t *status_dev,
                     void *stream);
 
+/* ---- qg_moe_w4a16 --------------------------------------------------------
+ * A whole mixture-of-experts layer for t <= 64 tokens on packed INT4 experts:
+ *   l = x . router^T;  the top_k experts of a token by l (ties go to the
+ *   lowest index; a NaN counts as the largest);
+ *   p = softmax of l over the picked experts (renormalize not 0) or over all;
+ *   y = sum over the picked e of p_e * down_e . (silu(gate_e x) * (up_e x)).
+ * Each expert's products are qgemm_w4a16's on its weight; the hidden
+ * activation is rounded to bf16 as the second product's operand, all sums,
+ * logits and weights are fp32, the picks are added in order of rank.
+ *   x        in : bf16 [t, h]          router in : bf16 [e, h]
+ *   gate_up  in : e packed weights of 2 inter x h (quantize_int4_g32), one
+ *                 after another: gate rows 0 .. inter - 1, then up rows
+ *   down     in : e packed weights of h x inter
+ *   y        out: [t, h], bf16 or fp32 (y_dtype)
+ *   ws          : qg_moe_w4a16_workspace_bytes(...) bytes; contents unspecified
+ * h, inter: multiples of 256; e <= 512; top_k <= 32.  t = 0 is fine.
+ * Errors: QG_E_NULL, QG_E_SHAPE, QG_E_K_MULTIPLE, QG_E_M_RANGE, QG_E_BUFFER,
+ * QG_E_ALIGN, QG_E_DTYPE. */
+int64_t qg_moe_w4a16_workspace_bytes(int64_t t, int64_t h, int64_t e, int64_t inter, int64_t top_k);
+int32_t qg_moe_w4a16(const void *x_bf16, int64_t t, int64_t h, const void *router_bf16, int64_t e,
+                     const void *gate_up, int64_t gate_up_bytes, const void *down, int64_t down_bytes,
+                     int64_t inter, int64_t top_k, int32_t renormalize, void *y, int32_t y_dtype, void *ws,
+                     int64_t ws_bytes, void *stream);
+
 /* ---- qg_stream_read (measurement helper, not part of the layer) ---------
  * Reads `bytes` bytes of device memory at `src` once, with one 16-byte
  * non-temporal load per lane per step over `blocks` workgroups of 256 lanes

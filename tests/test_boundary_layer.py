@@ -104,6 +104,26 @@ def test_attn_workspace():
         assert "unknown" not in qg.status_string(status)
 
 
+def moe(**kw):
+    a = dict(x=A, t=3, h=512, router=A, e=8, gu=A, gu_bytes=8 * 2 * 256 // 64 * 2 * 9472, dn=A, dn_bytes=8 * 8 * 9472, inter=256, k=2,
+             renorm=1, y=A, dt=0, ws=A, ws_bytes=1 << 30, stream=None)
+    assert set(kw) <= set(a)
+    return lib.qg_moe_w4a16(*(a | kw).values())
+
+
+@pytest.mark.parametrize("kw,want", [
+    (dict(x=None), E_NULL), (dict(router=None), E_NULL), (dict(gu=None), E_NULL), (dict(dn=None), E_NULL), (dict(y=None), E_NULL),
+    (dict(ws=None), E_NULL), (dict(t=-1), E_SHAPE), (dict(t=65), -4), (dict(h=0), E_SHAPE), (dict(h=500), -3), (dict(inter=128), -3),
+    (dict(inter=0), E_SHAPE), (dict(e=0), E_SHAPE), (dict(e=513), E_SHAPE), (dict(k=0), E_SHAPE), (dict(k=9), E_SHAPE),
+    (dict(e=64, k=33), E_SHAPE), (dict(dt=3), E_DTYPE), (dict(gu_bytes=8 * 8 * 2 * 9472 - 1), E_BUF), (dict(dn_bytes=8 * 8 * 9472 - 1), E_BUF),
+    (dict(ws_bytes=100), E_BUF), (dict(x=U), E_ALIGN), (dict(router=U), E_ALIGN), (dict(gu=U), E_ALIGN), (dict(dn=U), E_ALIGN),
+    (dict(y=U), E_ALIGN), (dict(ws=U), E_ALIGN), (dict(t=0), OK)])
+def test_moe_refusals(kw, want):
+    assert moe(**kw) == want
+    with pytest.raises(qg.QGemmError):
+        qg.moe_w4a16_workspace_bytes(65, 512, 8, 256, 2)
+
+
 def test_wrappers_refuse_host_tensors_and_wrong_types():
     x = torch.zeros(2, 4, 64, dtype=torch.bfloat16)
     with pytest.raises(ValueError, match="device"):

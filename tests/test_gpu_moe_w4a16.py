@@ -1,0 +1,185 @@
+"""qg_moe_w4a16 against the layer in 64 bits on the oracle's own quantization.
+
+Tolerance per output, with B = sum over picks of p |W2| |silu(g) u| in 64 bits:
+the hidden activation is rounded to bf16 (2^-8 of each term at most), the fp32
+sums and the routing weights add less than 2^-11 of the terms at these sizes
+(sums of at most 2048 products; a cancelled gate or up sum enters B with its own
+terms' rounding, covered by 2^-16 of the largest row of |W| |x|), so
+|err| <= (2^-8 + 2^-10) B + 2^-16 max B, plus half a bf16 unit for bf16 output."""
+from __future__ import annotations
+
+import functools
+
+import numpy as np
+import pytest
+import torch
+
+import layer_reference as ref
+import oracle
+import synthetic_inputs as si
+
+import gemm_decode_qgemm_amd as qg
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(scope="module")
+def dev():
+    assert torch.cuda.is_available(), "GPU tests need a HIP device"
+    return torch.device("cuda:0")
+
+
+@functools.lru_cache(maxsize=4)
+def experts(e, h, inter, seed):
+    """(packed gate_up, packed down, their values in 64 bits)."""
+    g = torch.Generator().manual_seed(seed)
+    out = []
+    for n, k in ((2 * inter, h), (h, inter)):
+        packed, values = [], []
+        for _ in range(e):
+            w = (torch.randn(n, k, generator=g) * k ** -0.5).bfloat16()
+            codes, scales, zeros, _ = oracle.quantize_int4_g32(si.bf16_bits(w))
+            packed.append(torch.from_numpy(oracle.pack_int4(codes, scales, zeros)))
+            q = codes.reshape(n, k // 32, 32).astype(np.float64) - zeros.reshape(n, k // 32, 1)
+            values.append((q * scales.reshape(n, k // 32, 1).view(np.float16).astype(np.float64)).reshape(n, k))
+        out.append((torch.stack(packed), values))
+    return out[0][0], out[1][0], out[0][1], out[1][1]
+
+
+def check(y, want, bound):
+    got = ref.f64(y)
+    assert np.isfinite(got).all()
+    tol = bound * (2.0 ** -8 + 2.0 ** -10) + bound.max(-1, keepdims=True) * 2.0 ** -16
+    if y.dtype == torch.bfloat16:
+        tol = tol + ref.half_ulp_bf16(np.abs(want) + tol)
+    err = np.abs(got - want)
+    assert (err <= tol).all(), float((err / tol).max())
+
+
+def case(dev, t, e, k, h, inter, renorm, seed, dtypes=(torch.float32, torch.bfloat16), x=None, router=None):
+    gu, dn, gu_v, dn_v = experts(e, h, inter, e + h + inter)
+    g = torch.Generator().manual_seed(seed)
+    x = torch.randn(t, h, generator=g).bfloat16() if x is None else x
+    router = (torch.randn(e, h, generator=g) * 2 * h ** -0.5).bfloat16() if router is None else router
+    want, bound = ref.moe(ref.f64(x), ref.f64(router), gu_v, dn_v, inter, k, renorm)
+    args = (x.to(dev), router.to(dev), gu.to(dev), dn.to(dev), inter, k)
+    for dt in dtypes:
+        y = qg.moe_w4a16(*args, renormalize=renorm, out_dtype=dt)
+        assert y.shape == (t, h) and y.dtype == dt
+        check(y, want, bound)
+    return args, want
+
+
+@pytest.mark.parametrize("t", [1, 2, 3, 4, 5, 16, 17, 33, 64])
+@pytest.mark.parametrize("e,k,h,inter,renorm", [(8, 2, 512, 256, True), (16, 4, 256, 768, False)])
+def test_every_token_count(dev, t, e, k, h, inter, renorm):
+    case(dev, t, e, k, h, inter, renorm, 100 * t + e)
+
+
+@pytest.mark.parametrize("t,e,k,h,inter", [
+    (1, 1, 1, 256, 256), (7, 1, 1, 256, 256), (64, 2, 2, 256, 256), (3, 5, 5, 256, 512), (2, 64, 6, 256, 256), (9, 70, 3, 256, 256),
+    (20, 128, 8, 256, 256), (1, 160, 32, 256, 256), (30, 3, 1, 2048, 1280)])
+@pytest.mark.parametrize("renorm", [True, False])
+def test_expert_counts_and_sizes(dev, t, e, k, h, inter, renorm):
+    case(dev, t, e, k, h, inter, renorm, t + e + k, (torch.bfloat16,))
+
+
+def test_all_tokens_on_the_same_experts(dev):
+    """64 tokens on two experts of eight: units of 64 tokens next to empty ones."""
+    e, h = 8, 512
+    g = torch.Generator().manual_seed(3)
+    x = (torch.randn(64, h, generator=g) * 0.2 + 1).bfloat16()
+    router = torch.zeros(e, h).bfloat16()
+    router[5], router[2] = 0.02, 0.01
+    case(dev, 64, e, 2, h, 256, True, 0, x=x, router=router)
+    case(dev, 3, e, 2, h, 256, False, 0, x=x[:3], router=router)
+
+
+def test_ties_go_to_the_lowest_index(dev):
+    """Equal logits everywhere: the first k experts, with equal weights."""
+    e, h = 16, 256
+    x = torch.randn(6, h, generator=torch.Generator().manual_seed(5)).bfloat16()
+    router = torch.zeros(e, h).bfloat16()
+    for t in (1, 2, 6):
+        case(dev, t, e, 4, h, 768, True, 0, x=x[:t], router=router)
+    router[3:9] = torch.randn(h, generator=torch.Generator().manual_seed(6)).bfloat16() * 0.05   # six equal rows
+    case(dev, 6, e, 4, h, 768, False, 0, x=x, router=router)
+
+
+def test_wide_logits_and_zero_tokens(dev):
+    e, h = 8, 512
+    g = torch.Generator().manual_seed(7)
+    x = torch.randn(5, h, generator=g).bfloat16()
+    x[2] = 0.0
+    router = (torch.randn(e, h, generator=g) * 30).bfloat16()      # one expert has all the weight
+    case(dev, 5, e, 2, h, 256, True, 0, x=x, router=router)
+    case(dev, 5, e, 2, h, 256, False, 0, x=x, router=router)
+
+
+def test_a_nan_token_leaves_the_others_alone(dev):
+    args, want = case(dev, 20, 8, 2, 512, 256, True, 11, (torch.float32,))
+    clean = qg.moe_w4a16(*args, out_dtype=torch.float32)
+    x = args[0].clone()
+    x[7, 100] = float("nan")
+    y = qg.moe_w4a16(x, *args[1:], out_dtype=torch.float32)
+    assert y[7].isnan().all()
+    keep = [t for t in range(20) if t != 7]
+    assert not y[keep].isnan().any()
+    assert torch.allclose(y[keep], clean[keep], rtol=1e-4, atol=1e-5)
+
+
+def test_repeats_streams_graphs_and_stale_workspace(dev):
+    for t in (1, 3, 17, 40):
+        args, _ = case(dev, t, 16, 4, 256, 768, False, 13 + t, (torch.bfloat16,))
+        want = qg.moe_w4a16(*args, renormalize=False)
+        ws = torch.full((qg.moe_w4a16_workspace_bytes(t, 256, 16, 768, 4),), 255, dtype=torch.uint8, device=dev)
+        out = torch.empty_like(want)
+        s = torch.cuda.Stream()
+        s.wait_stream(torch.cuda.current_stream())
+        with torch.cuda.stream(s):
+            qg.moe_w4a16(*args, renormalize=False, out=out, workspace=ws)
+        s.synchronize()
+        assert torch.equal(out, want)
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            qg.moe_w4a16(*args, renormalize=False, out=out, workspace=ws)
+        for _ in range(3):
+            out.fill_(5.0)
+            ws.fill_(255)
+            torch.cuda.synchronize()
+            g.replay()
+            torch.cuda.synchronize()
+            assert torch.equal(out, want)
+
+
+def test_packed_weights_of_the_library_and_the_linear_layer(dev):
+    """One expert with weight one is two qgemm_w4a16 calls with silu between."""
+    h, inter, t = 512, 256, 6
+    torch.manual_seed(17)
+    w1, w2 = (torch.randn(2 * inter, h) * 0.05).bfloat16().to(dev), (torch.randn(h, inter) * 0.05).bfloat16().to(dev)
+    gu, dn = qg.quantize_int4_g32(w1), qg.quantize_int4_g32(w2)
+    x = torch.randn(t, h).bfloat16().to(dev)
+    y = qg.moe_w4a16(x, torch.zeros(1, h, dtype=torch.bfloat16, device=dev), gu[None], dn[None], inter, 1, out_dtype=torch.float32)
+    z = qg.qgemm_w4a16(x, gu, 2 * inter, out_dtype=torch.float32)
+    a = (torch.nn.functional.silu(z[:, :inter]) * z[:, inter:]).bfloat16()
+    want = qg.qgemm_w4a16(a, dn, h, out_dtype=torch.float32)
+    # a hidden value may round the other way where silu differs in its last bits: 2^-8 of one term in 256
+    assert (y - want).abs().max() <= 2.0 ** -8 * want.abs().max()
+
+
+def test_experts_past_4_gib(dev):
+    """Offsets of the last experts need 64 bits."""
+    e, h, inter = 512, 2048, 4096
+    n1, n2 = qg.int4_packed_bytes(2 * inter, h), qg.int4_packed_bytes(h, inter)
+    assert (e - 1) * n1 > 1 << 32
+    gu = torch.zeros(e, n1, dtype=torch.uint8, device=dev)
+    dn = torch.zeros(e, n2, dtype=torch.uint8, device=dev)
+    torch.manual_seed(19)
+    one = [qg.quantize_int4_g32((torch.randn(n, k, device=dev) * 0.02).bfloat16()) for n, k in ((2 * inter, h), (h, inter))]
+    gu[-1], dn[-1] = one
+    x = torch.randn(2, h, device=dev).bfloat16()
+    router = torch.zeros(e, h, dtype=torch.bfloat16, device=dev)
+    router[-1] = x[0] * 0.01
+    y = qg.moe_w4a16(x[:1], router, gu, dn, inter, 1)
+    z = qg.moe_w4a16(x[:1], router[-1:], one[0][None], one[1][None], inter, 1)
+    assert torch.equal(y, z) and y.any()
