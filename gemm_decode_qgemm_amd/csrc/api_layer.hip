@@ -13,9 +13,9 @@ hipError_t launch_kv8_append(const Kv8Args& c, const void* k, int64_t k_ts, int6
                              int64_t v_hs, int64_t max_new, uint32_t* status, hipStream_t stream);
 hipError_t launch_kv8_read(const Kv8Args& c, int64_t max_len, void* k, void* v, int f32, hipStream_t stream);
 int attn_kv8_splits(int64_t b, int hkv, int64_t rows_per_head, int64_t max_len, int window, int64_t max_q);
-hipError_t launch_attn_kv8(const Kv8Args& c, const void* q, int64_t q_ts, int64_t q_hs, int hq, int max_q, int window,
-                           float scale, void* out, int out_f32, int splits, float* part, uint32_t* status,
-                           hipStream_t stream);
+hipError_t launch_attn_kv8(const Kv8Args& c, const void* q, int64_t q_ts, int64_t q_hs, int hq, int max_q,
+                           int64_t max_len, int window, float scale, void* out, int out_f32, int splits, float* part,
+                           uint32_t* status, hipStream_t stream);
 int64_t moe_ws_bytes(int64_t t, int64_t h, int64_t e, int64_t inter, int64_t k);
 hipError_t launch_moe_w4a16(const void* x, int t, int h, const void* router, int e, const void* gate_up,
                             int64_t gate_up_bytes, const void* down, int64_t down_bytes, int inter, int k, int renorm,
@@ -190,7 +190,8 @@ int32_t qg_attn_kv8(const void* q, int64_t q_ts, int64_t q_hs, int64_t rows, int
   const int64_t need = attn_ws(rows, hq, d, s);
   if (need > 0 && (!ws || ws_bytes < need)) return ws ? QG_E_BUFFER : QG_E_NULL;
   const qg::Kv8Args c = cache_args(codes, scales, pages, hkv, d, block_table, table_width, lens, cu, rows, b);
-  return hip_status(qg::launch_attn_kv8(c, q, q_ts, q_hs, hq, (int)max_q, window, scale, out, out_dtype == QG_F32, s,
+  return hip_status(qg::launch_attn_kv8(c, q, q_ts, q_hs, hq, (int)max_q, max_len, window, scale, out,
+                                        out_dtype == QG_F32, s,
                                         static_cast<float*>(ws), status_dev, static_cast<hipStream_t>(stream)));
 }
 

@@ -9,10 +9,21 @@
 //   m' = max(m, max s), p = 2^(s - m'), l = l 2^(m - m') + sum p,
 //   O  = O 2^(m - m') + sum p v,       o = O / l
 // (scores in units of log 2), everything but the products' operands in fp32.
-// Operands are bf16: q as given, codes exactly (|q| <= 127), and p * vs
-// rounded once, which costs 2^-9 of each term and needs no further pass.
+// Operands are fp16, which costs fewer instructions than bf16 and rounds less:
+//  * a code q becomes 1024 + (q + 128) by one byte permute a pair (0x6400 |
+//    byte), exactly.  Keys stay so: the accumulator starts at -1152 sum(q) of the
+//    row, and the rounding this costs (2^-24 of 1152 |sum q| against a score of
+//    some 40 sqrt(d) |q|) is below 2^-17 of the score.  Values, which are summed
+//    over a whole cache, have the 1152 taken off again, exactly (packed add);
+//  * a query row is scaled by a power of two to a largest channel in [2^7,
+//    2^8), where its 8 significant bits fit exactly;
+//  * p * vs is taken relative to the largest exponent of a value scale seen so
+//    far and put at 2^13, so it keeps 11 bits down to 2^-27 of the largest.
+// As bf16 the same products took 1.5 instructions per code and p * vs had to be
+// two operands for this accuracy: 32 sequences of 4096 tokens on 32 / 8 heads of
+// 128 ran 60 us, now 46 us (5.85 TB/s).
 //
-// Mapping (gfx950, wave64, v_mfma_f32_16x16x32_bf16):
+// Mapping (gfx950, wave64, v_mfma_f32_16x16x32_f16):
 //  * the rows of one key/value head are its query rows times its query heads;
 //    a wave takes 16 NT of them and whole pages, 64 tokens x (K, V), straight
 //    from memory to registers, no LDS: S^T = K Q^T, so lane (i, a) =
@@ -24,10 +35,7 @@
 //    partner.  Neither P nor V crosses lanes;
 //  * m and l of a row are the same lane column as its O, so rescaling is one
 //    factor per lane; it is skipped while no maximum of the wave moved;
-//  * a block's scales are wave-uniform (scalar loads);
-//  * codes become bf16 by a byte-selecting convert each and one byte permute a
-//    pair: 1.5 instructions per code, about a third of the time HBM takes to
-//    deliver them at 16 rows.
+//  * a block's scales are wave-uniform and read by scalar loads.
 // A workgroup's waves take pages in turn and join (m, l, O) through LDS; the
 // pages of a sequence are further split over workgroups when there are few,
 // the partial (m, l, O) joined by a second kernel in a fixed order.
@@ -39,13 +47,24 @@ struct AttnArgs {
   Kv8Args c;
   const uint16_t* q;
   int64_t q_ts, q_hs;
-  int hq, group, max_q, window, splits, row_tiles;
+  int hq, group, max_q, window, splits, chunk, row_tiles;
+  uint32_t magic;                   // floor(2^32 / group)
   float scale_log2;                 // scale * log2(e)
   void* out;
   int out_f32;
   float *part_o, *part_ml;          // [splits][rows * hq][d], [splits][rows * hq][2]
   uint32_t* status;
 };
+
+// r / group for 0 <= r < 2^31: the product with floor(2^32 / group) is at most
+// one short.
+__device__ __forceinline__ int group_of(const AttnArgs& a, int r) {
+  if (a.group == 1) return r;       // (2^32 does not fit the word)
+  const int q = (int)__umulhi((uint32_t)r, a.magic);
+  return q + (r - q * a.group >= a.group ? 1 : 0);
+}
+
+constexpr int kMinExp = 20;         // value scales below 2^-107 are taken relative to that
 
 // Value of lane ^ 32, then of lane ^ 16, folded with f.
 template <class F>
@@ -56,40 +75,74 @@ __device__ __forceinline__ float fold_quads(float v, F f) {
   return f(__uint_as_float(y[0]), __uint_as_float(y[1]));
 }
 
-// 8 int8 codes as 8 bf16 (exact: the low half of the fp32 value is zero).
-__device__ __forceinline__ bf16x8_t codes8(uint32_t lo, uint32_t hi) {
+typedef _Float16 f16x2_t __attribute__((ext_vector_type(2)));
+typedef _Float16 f16x8_t __attribute__((ext_vector_type(8)));
+
+// 8 int8 codes as fp16, plus 1152 where BIAS: with the sign bit flipped a code
+// q is the byte q + 128, and 0x6400 | byte is 1024 + byte exactly.
+template <bool BIAS>
+__device__ __forceinline__ f16x8_t codes8(uint32_t lo, uint32_t hi) {
   u32x4_t o;
+  lo ^= 0x80808080u;
+  hi ^= 0x80808080u;
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
-    const uint32_t w = i < 2 ? lo : hi;
-    const float x = (float)(int8_t)(w >> (16 * (i & 1))), y = (float)(int8_t)(w >> (16 * (i & 1) + 8));
-    o[i] = __builtin_amdgcn_perm(__float_as_uint(y), __float_as_uint(x), 0x07060302u);
+    // (a bit cast of a vector's element would read its first one: scalars)
+    uint32_t two = __builtin_amdgcn_perm(0x64646464u, i < 2 ? lo : hi, (i & 1) ? 0x04030402u : 0x04010400u);
+    if constexpr (!BIAS) {
+      const f16x2_t c = {(_Float16)1152.0f, (_Float16)1152.0f};
+      const f16x2_t v = __builtin_bit_cast(f16x2_t, two) - c;
+      two = __builtin_bit_cast(uint32_t, v);
+    }
+    o[i] = two;
   }
-  return __builtin_bit_cast(bf16x8_t, o);
+  return __builtin_bit_cast(f16x8_t, o);
 }
 
+__device__ __forceinline__ uint32_t pack_f16(float lo, float hi) {
+  f16x2_t v;
+  v[0] = (_Float16)lo;
+  v[1] = (_Float16)hi;
+  return __builtin_bit_cast(uint32_t, v);
+}
+
+// Wave-uniform words through scalar loads (a store or an atomic in the kernel
+// keeps the compiler from choosing them by itself; as vector loads they would
+// queue behind a page's 16 KB and everything that needs them with it).
+typedef const __attribute__((address_space(4))) int32_t* const_i32;
+typedef const __attribute__((address_space(4))) float* const_f32;
+
 constexpr float kNegInf = -__builtin_inff();
+constexpr int kMaxSplits = 256;   // a lane per split in the join
 
 template <int D, int NT, int W>
 __global__ __launch_bounds__(64 * W) void attn_kv8_kernel(AttnArgs a) {
   constexpr int KC = D / 64;        // 64-channel chunks of a key
   constexpr int DT = D / 16;        // 16-channel tiles of a value
+  constexpr bool kEarlyV = D <= 192 && D * NT <= 256;   // values in flight with the keys, where registers allow
   __shared__ float sm_m[W][16 * NT], sm_l[W][16 * NT];
   __shared__ f32x4_t sm_o[W][DT][64];
   const int lane = threadIdx.x & 63, i = lane & 15, qd = lane >> 4;
   const int wave = wave_id_uniform();
-  const int split = blockIdx.x;
-  const int h = blockIdx.y / a.row_tiles, rt = blockIdx.y % a.row_tiles, b = blockIdx.z;
+  // Splits slowest: workgroups go to the 8 XCDs in turn, and the late splits
+  // of short sequences, which are empty, must not all fall to the same ones.
+  const int h = blockIdx.x / a.row_tiles, rt = blockIdx.x % a.row_tiles, b = blockIdx.y, split = blockIdx.z;
+  const const_i32 trow = (const_i32)(a.c.table + (size_t)b * a.c.width);
+  const int width = (int)a.c.width;
+  // Without a window the first page does not depend on the length: its table
+  // entry is on its way together with the length.
+  const int guess = (int)min((int64_t)split * a.chunk + wave, (int64_t)width - 1);
+  const int guessed = trow[guess];
+  const int len = max(((const_i32)a.c.lens)[b], 0);
   int64_t r0, n64;
   kv8_rows(a.c.cu, a.c.rows, a.c.b, b, r0, n64);
   const int nq = (int)(n64 < a.max_q ? n64 : a.max_q);
   const int nrows = nq * a.group;
   const int row0 = rt * 16 * NT;
   if (row0 >= nrows) return;
-  const int len = max(a.c.lens[b], 0);
   // The last query row is the sequence's last token.
   const int shift = len - (int)n64;                  // position of query row t: shift + t
-  const int t_lo = row0 / a.group, t_hi = min(row0 + 16 * NT - 1, nrows - 1) / a.group;
+  const int t_lo = group_of(a, row0), t_hi = group_of(a, min(row0 + 16 * NT - 1, nrows - 1));
   const int pos_hi = shift + t_hi, pos_lo = shift + t_lo;
   const int tok_end = pos_hi + 1;                    // tokens [tok_beg, tok_end) are seen by some row
   const int tok_beg = a.window > 0 ? max(0, pos_lo - a.window + 1) : 0;
@@ -97,34 +150,72 @@ __global__ __launch_bounds__(64 * W) void attn_kv8_kernel(AttnArgs a) {
   if (tok_end > tok_beg) {
     const int first = tok_beg / kPage;
     // a length beyond the table costs one page that is not there
-    const int last = (int)min((int64_t)((tok_end - 1) / kPage), a.c.width);
-    const int count = last >= first ? last - first + 1 : 0;
-    p_beg = first + (int)((int64_t)count * split / a.splits);
-    p_end = first + (int)((int64_t)count * (split + 1) / a.splits);
+    const int last = min((tok_end - 1) / kPage, width);
+    // `chunk` pages a split, the last one what is left: equal work for every
+    // workgroup whatever the lengths
+    p_beg = (int)min(first + (int64_t)split * a.chunk, (int64_t)last + 1);
+    p_end = split + 1 < a.splits ? (int)min((int64_t)p_beg + a.chunk, (int64_t)last + 1) : last + 1;
   }
 
-  // Rows of this lane: t = query row, g = head of the group.
+  if (p_beg >= p_end && a.splits > 1) {              // nothing here: say so to the join, and no more
+    const int r = row0 + (int)threadIdx.x;
+    if ((int)threadIdx.x < 16 * NT && r < nrows) {
+      const int t = group_of(a, r), g = r - t * a.group;
+      float* const ml = a.part_ml + ((size_t)split * a.c.rows * a.hq + (r0 + t) * a.hq + h * a.group + g) * 2;
+      ml[0] = kNegInf;
+      ml[1] = 0.0f;
+    }
+    return;
+  }
+
+  // Rows of this lane, as fp16 q 2^(8 - e) with 2^e just above the row's
+  // largest channel: exact but for channels 2^-21 of that one.  The keys'
+  // bias of 1152 comes off in the accumulator's first value.
   int pos[NT];
-  bf16x8_t qf[NT][2 * KC];
+  float rscale[NT], corr[NT];
+  f16x8_t qf[NT][2 * KC];
 #pragma unroll
   for (int n = 0; n < NT; ++n) {
     const int r = row0 + 16 * n + i;
     const bool on = r < nrows;
-    const int t = r / a.group, g = r - t * a.group;
+    const int t = group_of(a, r), g = r - t * a.group;
     pos[n] = on ? shift + t : -1;
     const uint16_t* src = a.q + (r0 + t) * a.q_ts + (int64_t)(h * a.group + g) * a.q_hs + 16 * qd;
+    u32x4_t raw[2 * KC];
+    float mx = 0.0f;
 #pragma unroll
-    for (int c = 0; c < KC; ++c)
+    for (int c = 0; c < 2 * KC; ++c) {
+      raw[c] = u32x4_t{0u, 0u, 0u, 0u};
+      if (on) raw[c] = *reinterpret_cast<const u32x4_t*>(src + 64 * (c >> 1) + 8 * (c & 1));
+    }
 #pragma unroll
-      for (int e = 0; e < 2; ++e) {
-        u32x4_t v{0u, 0u, 0u, 0u};
-        if (on) v = *reinterpret_cast<const u32x4_t*>(src + 64 * c + 8 * e);
-        qf[n][2 * c + e] = __builtin_bit_cast(bf16x8_t, v);
+    for (int c = 0; c < 2 * KC; ++c)
+#pragma unroll
+      for (int e = 0; e < 4; ++e)
+        mx = fmaxf(mx, fmaxf(fabsf(__uint_as_float(raw[c][e] << 16)), fabsf(__uint_as_float(raw[c][e] & 0xffff0000u))));
+    mx = fold_quads(mx, [](float x, float y) { return fmaxf(x, y); });
+    const int ex = mx > 0.0f && mx < __builtin_inff() ? __builtin_amdgcn_frexp_expf(mx) : 8;
+    float sum = 0.0f;
+#pragma unroll
+    for (int c = 0; c < 2 * KC; ++c) {
+      u32x4_t o;
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        const uint32_t two = pack_f16(__builtin_ldexpf(__uint_as_float(raw[c][e] << 16), 8 - ex),
+                                      __builtin_ldexpf(__uint_as_float(raw[c][e] & 0xffff0000u), 8 - ex));
+        const f16x2_t v = __builtin_bit_cast(f16x2_t, two);
+        sum += (float)v[0] + (float)v[1];
+        o[e] = two;
       }
+      qf[n][c] = __builtin_bit_cast(f16x8_t, o);
+    }
+    corr[n] = -1152.0f * fold_quads(sum, [](float x, float y) { return x + y; });
+    rscale[n] = __builtin_ldexpf(a.scale_log2, ex - 8);
   }
 
   float m[NT], l[NT];
   f32x4_t o[NT][DT];
+  int ve = kMinExp;                 // o holds O 2^(140 - ve), ve the largest biased exponent of a value scale so far
 #pragma unroll
   for (int n = 0; n < NT; ++n) {
     m[n] = kNegInf;
@@ -133,14 +224,17 @@ __global__ __launch_bounds__(64 * W) void attn_kv8_kernel(AttnArgs a) {
     for (int t = 0; t < DT; ++t) o[n][t] = f32x4_t{0.0f, 0.0f, 0.0f, 0.0f};
   }
 
-  const int32_t* const trow = a.c.table + (size_t)b * a.c.width;
-  int next = p_beg + wave < p_end ? kv8_page(trow, a.c.width, a.c.pages, p_beg + wave) : 0;
+  auto entry = [&](int p) {         // the page, or -1
+    const int e = p == guess ? guessed : p < width ? trow[p] : -1;
+    return p < width && e >= 0 && e < a.c.pages ? e : -1;
+  };
+  bool missing = false;
+  int next = p_beg + wave < p_end ? entry(p_beg + wave) : 0;
   for (int p = p_beg + wave; p < p_end; p += W) {
-    const int page = __builtin_amdgcn_readfirstlane(next);
-    if (p + W < p_end) next = kv8_page(trow, a.c.width, a.c.pages, p + W);
+    const int page = next;
     const int held = page < 0 ? 0 : page;            // reads stay inside; its scales become NaN below
     const int8_t* const kc = a.c.codes + kv8_base(held, a.c.hkv, h, D);
-    const float* const sc = a.c.scales + ((size_t)held * a.c.hkv + h) * 8;
+    const const_f32 sc = (const_f32)(a.c.scales + ((size_t)held * a.c.hkv + h) * 8);
     u32x4_t kr[4][KC], vr[DT];
 #pragma unroll
     for (int blk = 0; blk < 4; ++blk)
@@ -148,16 +242,21 @@ __global__ __launch_bounds__(64 * W) void attn_kv8_kernel(AttnArgs a) {
       for (int c = 0; c < KC; ++c)
         kr[blk][c] = __builtin_nontemporal_load(
             reinterpret_cast<const u32x4_t*>(kc + (16 * blk + i) * D + 64 * c + 16 * qd));
+    auto load_v = [&] {
 #pragma unroll
-    for (int t = 0; t < DT; ++t)
-      vr[t] = __builtin_nontemporal_load(reinterpret_cast<const u32x4_t*>(kc + kPage * D + 1024 * t + 64 * i + 16 * qd));
+      for (int t = 0; t < DT; ++t)
+        vr[t] = __builtin_nontemporal_load(
+            reinterpret_cast<const u32x4_t*>(kc + kPage * D + 1024 * t + 64 * i + 16 * qd));
+    };
+    if constexpr (kEarlyV) load_v();
     float ks[4], vs[4];
 #pragma unroll
     for (int blk = 0; blk < 4; ++blk) {
-      ks[blk] = page < 0 ? __uint_as_float(0x7fc00000u) : sc[blk] * a.scale_log2;
+      ks[blk] = sc[blk];
       vs[blk] = sc[4 + blk];
     }
-    if (page < 0 && a.status && lane == 0) atomicOr(a.status, QG_FLAG_PAGE);
+    if (p + W < p_end) next = entry(p + W);
+    missing |= page < 0;
     const int j0 = p * kPage;
     const bool edge = j0 + kPage - 1 > pos_lo || (a.window > 0 && j0 <= pos_hi - a.window);   // uniform
 
@@ -165,26 +264,53 @@ __global__ __launch_bounds__(64 * W) void attn_kv8_kernel(AttnArgs a) {
 #pragma unroll
     for (int blk = 0; blk < 4; ++blk) {
 #pragma unroll
-      for (int n = 0; n < NT; ++n) s[n][blk] = f32x4_t{0.0f, 0.0f, 0.0f, 0.0f};
+      for (int n = 0; n < NT; ++n) s[n][blk] = f32x4_t{corr[n], corr[n], corr[n], corr[n]};
 #pragma unroll
       for (int c = 0; c < KC; ++c) {
-        const bf16x8_t k0 = codes8(kr[blk][c][0], kr[blk][c][1]), k1 = codes8(kr[blk][c][2], kr[blk][c][3]);
+        const f16x8_t k0 = codes8<true>(kr[blk][c][0], kr[blk][c][1]), k1 = codes8<true>(kr[blk][c][2], kr[blk][c][3]);
 #pragma unroll
         for (int n = 0; n < NT; ++n) {
-          s[n][blk] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(k0, qf[n][2 * c], s[n][blk], 0, 0, 0);
-          s[n][blk] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(k1, qf[n][2 * c + 1], s[n][blk], 0, 0, 0);
+          s[n][blk] = __builtin_amdgcn_mfma_f32_16x16x32_f16(k0, qf[n][2 * c], s[n][blk], 0, 0, 0);
+          s[n][blk] = __builtin_amdgcn_mfma_f32_16x16x32_f16(k1, qf[n][2 * c + 1], s[n][blk], 0, 0, 0);
         }
       }
     }
-    bf16x8_t pf[NT][2];
+    if constexpr (!kEarlyV) load_v();
+
+    // The exponent that value scales are taken relative to (uniform): of the
+    // blocks that some row sees, infinities and NaN aside.
+    int top = 0;
+#pragma unroll
+    for (int blk = 0; blk < 4; ++blk) {
+      const int ex = (int)(__float_as_uint(vs[blk]) >> 23 & 0xff);
+      const bool seen = j0 + 16 * blk < tok_end && j0 + 16 * blk + kBlock > tok_beg;
+      if (seen && ex < 255 && ex > top) top = ex;
+      if (page < 0) ks[blk] = __uint_as_float(0x7fc00000u);
+    }
+    if (top > ve) {
+      const float f = __builtin_ldexpf(1.0f, ve - top);
+#pragma unroll
+      for (int n = 0; n < NT; ++n)
+#pragma unroll
+        for (int t = 0; t < DT; ++t)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) o[n][t][e] *= f;
+      ve = top;
+    }
+    const float vmul = __uint_as_float((uint32_t)(267 - ve) << 23);   // 2^(140 - ve)
+#pragma unroll
+    for (int blk = 0; blk < 4; ++blk) vs[blk] *= vmul;
+
+    f16x8_t pf[NT][2];
 #pragma unroll
     for (int n = 0; n < NT; ++n) {
       float mx = kNegInf;
 #pragma unroll
-      for (int blk = 0; blk < 4; ++blk)
+      for (int blk = 0; blk < 4; ++blk) {
+        const float f = ks[blk] * rscale[n];
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
-          float v = s[n][blk][e] * ks[blk];
+          float v = s[n][blk][e] * f;
           if (edge) {
             const int j = j0 + 16 * blk + 4 * qd + e;
             v = j <= pos[n] && (a.window <= 0 || j > pos[n] - a.window) ? v : kNegInf;
@@ -192,6 +318,7 @@ __global__ __launch_bounds__(64 * W) void attn_kv8_kernel(AttnArgs a) {
           s[n][blk][e] = v;
           mx = fmaxf(mx, v);
         }
+      }
       mx = fold_quads(mx, [](float x, float y) { return fmaxf(x, y); });
       const float m_new = fmaxf(m[n], mx);
       const float base = m_new == kNegInf ? 0.0f : m_new;   // nothing seen yet: every p is 0
@@ -217,23 +344,25 @@ __global__ __launch_bounds__(64 * W) void attn_kv8_kernel(AttnArgs a) {
           // a scale that holds a NaN, or was never written, stays out of rows that do not see its block
           if (edge) pv[e] = s[n][blk][e] == kNegInf ? 0.0f : pv[e];
         }
-        w[blk >> 1][2 * (blk & 1)] = pack_bf16(pv[0], pv[1]);
-        w[blk >> 1][2 * (blk & 1) + 1] = pack_bf16(pv[2], pv[3]);
+        w[blk >> 1][2 * (blk & 1)] = pack_f16(pv[0], pv[1]);
+        w[blk >> 1][2 * (blk & 1) + 1] = pack_f16(pv[2], pv[3]);
       }
       l[n] += sum;
-      pf[n][0] = __builtin_bit_cast(bf16x8_t, w[0]);
-      pf[n][1] = __builtin_bit_cast(bf16x8_t, w[1]);
+      pf[n][0] = __builtin_bit_cast(f16x8_t, w[0]);
+      pf[n][1] = __builtin_bit_cast(f16x8_t, w[1]);
     }
 #pragma unroll
     for (int t = 0; t < DT; ++t) {
-      const bf16x8_t v0 = codes8(vr[t][0], vr[t][1]), v1 = codes8(vr[t][2], vr[t][3]);
+      const f16x8_t v0 = codes8<false>(vr[t][0], vr[t][1]), v1 = codes8<false>(vr[t][2], vr[t][3]);
 #pragma unroll
       for (int n = 0; n < NT; ++n) {
-        o[n][t] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(v0, pf[n][0], o[n][t], 0, 0, 0);
-        o[n][t] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(v1, pf[n][1], o[n][t], 0, 0, 0);
+        o[n][t] = __builtin_amdgcn_mfma_f32_16x16x32_f16(v0, pf[n][0], o[n][t], 0, 0, 0);
+        o[n][t] = __builtin_amdgcn_mfma_f32_16x16x32_f16(v1, pf[n][1], o[n][t], 0, 0, 0);
       }
     }
   }
+  if (missing && a.status && lane == 0) atomicOr(a.status, QG_FLAG_PAGE);
+  const float vback = __uint_as_float((uint32_t)(ve - 13) << 23);     // 2^(ve - 140)
 
   // Join the waves: M = max m, each wave's O and l times 2^(m - M), added in wave order.
 #pragma unroll
@@ -253,14 +382,14 @@ __global__ __launch_bounds__(64 * W) void attn_kv8_kernel(AttnArgs a) {
     const float base = mm == kNegInf ? 0.0f : mm;
 #pragma unroll
     for (int w = 0; w < W; ++w) ll += sm_l[w][16 * n + i] * __builtin_amdgcn_exp2f(sm_m[w][16 * n + i] - base);
-    const float f = __builtin_amdgcn_exp2f(m[n] - base);
+    const float f = __builtin_amdgcn_exp2f(m[n] - base) * vback;
     if (n > 0) __syncthreads();
 #pragma unroll
     for (int t = 0; t < DT; ++t)
       sm_o[wave][t][lane] = f32x4_t{o[n][t][0] * f, o[n][t][1] * f, o[n][t][2] * f, o[n][t][3] * f};
     __syncthreads();
     const int r = row0 + 16 * n + i;
-    const int t = r / a.group, g = r - t * a.group;
+    const int t = group_of(a, r), g = r - t * a.group;
     const int64_t row = (r0 + t) * a.hq + h * a.group + g;     // row of the output
     const bool on = r < nrows;
     for (int dt = wave; dt < DT; dt += W) {
@@ -293,97 +422,171 @@ __global__ __launch_bounds__(64 * W) void attn_kv8_kernel(AttnArgs a) {
   }
 }
 
-// The splits of one row and head: a workgroup of 4 waves, each a quarter of
-// the splits, joined in order.  Rows that belong to no sequence are left as
-// they are.
+// The splits of one row and head, joined in a fixed order: the factors
+// 2^(m_s - M) first (a lane per split), then O.  A workgroup takes 32 channels,
+// 32 groups of 8 lanes taking splits in turn, so that with many splits all
+// their loads are in flight at once.  Splits that saw nothing wrote no O and
+// are not read.
 template <int D>
 __global__ __launch_bounds__(256) void attn_kv8_join_kernel(AttnArgs a) {
-  constexpr int E = D / 64;
-  __shared__ float sm_m[4], sm_l[4], sm_o[4][D];
-  const int lane = threadIdx.x & 63, wave = wave_id_uniform();
-  // (sequence, query row, head)
-  const int b = blockIdx.z, t = blockIdx.y, hd = blockIdx.x;
+  __shared__ float sm_f[kMaxSplits], sm_w[4], sm_l[4];
+  __shared__ f32x4_t sm_o[32][8];
+  const int tid = threadIdx.x, lane = tid & 63, wave = wave_id_uniform();
+  const int b = blockIdx.z, t = blockIdx.y, hd = blockIdx.x / (D / 32), d0 = blockIdx.x % (D / 32) * 32;
   int64_t r0, n;
   kv8_rows(a.c.cu, a.c.rows, a.c.b, b, r0, n);
   if (t >= n) return;
   const size_t total = (size_t)a.c.rows * a.hq, row = (size_t)(r0 + t) * a.hq + hd;
-  float m = kNegInf, l = 0.0f, o[E];
-#pragma unroll
-  for (int e = 0; e < E; ++e) o[e] = 0.0f;
-  const int s0 = a.splits * wave / 4, s1 = a.splits * (wave + 1) / 4;
-  for (int s = s0; s < s1; ++s) {
-    const float* ml = a.part_ml + ((size_t)s * total + row) * 2;
-    const float ms = ml[0], ls = ml[1];
-    if (ms == kNegInf && ls == 0.0f) continue;           // the split saw nothing and wrote no O
-    const float* po = a.part_o + ((size_t)s * total + row) * D + lane * E;
-    const float m_new = fmaxf(m, ms), base = m_new == kNegInf ? 0.0f : m_new;
-    const float f = __builtin_amdgcn_exp2f(m - base), g = __builtin_amdgcn_exp2f(ms - base);
-    m = m_new;
-    l = l * f + ls * g;
-#pragma unroll
-    for (int e = 0; e < E; ++e) o[e] = o[e] * f + po[e] * g;
+  float m = kNegInf, l = 0.0f;
+  if (tid < a.splits) {
+    const float* const ml = a.part_ml + ((size_t)tid * total + row) * 2;
+    m = ml[0];
+    l = ml[1];
   }
-  if (lane == 0) {
-    sm_m[wave] = m;
-    sm_l[wave] = l;
-  }
+  float mm = m;
 #pragma unroll
-  for (int e = 0; e < E; ++e) sm_o[wave][lane * E + e] = o[e];
+  for (int o = 1; o < 64; o *= 2) mm = fmaxf(mm, __shfl_xor(mm, o));
+  if (lane == 0) sm_w[wave] = mm;
   __syncthreads();
-  if ((int)threadIdx.x >= D) return;
-  float mm = kNegInf, ll = 0.0f, v = 0.0f;
+  mm = fmaxf(fmaxf(sm_w[0], sm_w[1]), fmaxf(sm_w[2], sm_w[3]));
+  const float f = mm == kNegInf ? 0.0f : __builtin_amdgcn_exp2f(m - mm);
+  float ll = mm == kNegInf ? l : l * f;      // nothing seen: l is 0, or NaN
 #pragma unroll
-  for (int w = 0; w < 4; ++w) mm = fmaxf(mm, sm_m[w]);
-  const float base = mm == kNegInf ? 0.0f : mm;
+  for (int o = 1; o < 64; o *= 2) ll += __shfl_xor(ll, o);
+  if (lane == 0) sm_l[wave] = ll;
+  sm_f[tid] = f;
+  __syncthreads();
+  ll = (sm_l[0] + sm_l[1]) + (sm_l[2] + sm_l[3]);
+  const int g = tid >> 3, c = tid & 7;
+  f32x4_t v = {0.0f, 0.0f, 0.0f, 0.0f};
+  const float* const po = a.part_o + row * D + d0 + 4 * c;
 #pragma unroll
-  for (int w = 0; w < 4; ++w) {
-    const float f = __builtin_amdgcn_exp2f(sm_m[w] - base);
-    ll += sm_l[w] * f;
-    v += sm_o[w][threadIdx.x] * f;
+  for (int u = 0; u < kMaxSplits / 32; ++u) {
+    const int s = g + 32 * u;
+    const float w = sm_f[s];
+    f32x4_t x = {0.0f, 0.0f, 0.0f, 0.0f};
+    if (s < a.splits && w != 0.0f) x = *reinterpret_cast<const f32x4_t*>(po + (size_t)s * total * D);
+#pragma unroll
+    for (int e = 0; e < 4; ++e) v[e] = __builtin_fmaf(w, x[e], v[e]);
   }
-  v = ll == 0.0f ? 0.0f : v / ll;
+  sm_o[g][c] = v;
+  __syncthreads();
+  if (tid >= 32) return;
+  float y = 0.0f;
+#pragma unroll
+  for (int u = 0; u < 32; ++u) y += sm_o[u][tid >> 2][tid & 3];
+  y *= ll == 0.0f ? 0.0f : 1.0f / ll;
+  const size_t at = row * D + d0 + tid;
   if (a.out_f32)
-    static_cast<float*>(a.out)[row * D + threadIdx.x] = v;
+    static_cast<float*>(a.out)[at] = y;
   else
-    static_cast<uint16_t*>(a.out)[row * D + threadIdx.x] = (uint16_t)f32_to_bf16_rne(v);
+    static_cast<uint16_t*>(a.out)[at] = (uint16_t)f32_to_bf16_rne(y);
+}
+
+// The same for few splits: a lane takes 4 channels of a row through all of
+// them, a workgroup 256 / (D / 4) heads.
+constexpr int kFewSplits = 16;
+template <int D>
+__global__ __launch_bounds__(256) void attn_kv8_join_few_kernel(AttnArgs a) {
+  constexpr int C = D / 4, R = 256 / C;
+  const int g = threadIdx.x / C, c = threadIdx.x % C;
+  const int b = blockIdx.z, t = blockIdx.y, hd = blockIdx.x * R + g;
+  int64_t r0, n;
+  kv8_rows(a.c.cu, a.c.rows, a.c.b, b, r0, n);
+  if (t >= n || g >= R || hd >= a.hq) return;
+  const size_t total = (size_t)a.c.rows * a.hq, row = (size_t)(r0 + t) * a.hq + hd;
+  float m[kFewSplits], l[kFewSplits], mm = kNegInf;
+#pragma unroll
+  for (int s = 0; s < kFewSplits; ++s) {
+    m[s] = kNegInf;
+    l[s] = 0.0f;
+    if (s < a.splits) {
+      const float* const ml = a.part_ml + (s * total + row) * 2;
+      m[s] = ml[0];
+      l[s] = ml[1];
+    }
+  }
+#pragma unroll
+  for (int s = 0; s < kFewSplits; ++s) mm = fmaxf(mm, m[s]);
+  f32x4_t y = {0.0f, 0.0f, 0.0f, 0.0f};
+  float ll = 0.0f;
+#pragma unroll
+  for (int s = 0; s < kFewSplits; ++s) {
+    const float f = mm == kNegInf ? 0.0f : __builtin_amdgcn_exp2f(m[s] - mm);
+    ll += mm == kNegInf ? l[s] : l[s] * f;    // nothing seen: 0, or NaN
+    f32x4_t x = {0.0f, 0.0f, 0.0f, 0.0f};
+    if (s < a.splits && f != 0.0f) x = *reinterpret_cast<const f32x4_t*>(a.part_o + (s * total + row) * D + 4 * c);
+#pragma unroll
+    for (int e = 0; e < 4; ++e) y[e] = __builtin_fmaf(f, x[e], y[e]);
+  }
+  const float inv = ll == 0.0f ? 0.0f : 1.0f / ll;
+#pragma unroll
+  for (int e = 0; e < 4; ++e) y[e] *= inv;
+  if (a.out_f32)
+    *reinterpret_cast<f32x4_t*>(static_cast<float*>(a.out) + row * D + 4 * c) = y;
+  else
+    *reinterpret_cast<u32x2_t*>(static_cast<uint16_t*>(a.out) + row * D + 4 * c) =
+        u32x2_t{pack_bf16(y[0], y[1]), pack_bf16(y[2], y[3])};
 }
 
 // Row tiles a wave takes at once: two where a head has more than 16 rows, so
 // that a page's codes are converted once for both.
 int attn_kv8_nt(int64_t rows_per_head) { return rows_per_head > 16 ? 2 : 1; }
 
-// Splits of a sequence's pages over workgroups.
+// Pages that a sequence's rows can see.
+static int64_t seen_pages(int64_t max_len, int window, int64_t max_q) {
+  int64_t seen = max_len;
+  if (window > 0 && window + max_q + kPage < seen) seen = window + max_q + kPage;
+  return (seen + kPage - 1) / kPage;
+}
+
+// Waves of a workgroup, one page each at a time.  Eight instead of four halve
+// the partial results of a split, but fewer workgroups fit a CU (48 sequences of
+// 0..4095 tokens, 32 / 8 heads of 128: 48 us against 57 at 3 splits; 131071
+// tokens on one head: 19.6 against 19.9 at 256).
+constexpr int kWaves = 4;
+
+// Splits of a sequence's pages over workgroups: two workgroups per CU, a page
+// for every wave at most.  More pay for few long sequences only (8 of 32768 on
+// 8 heads: 91 us at 8, 89 at 12 and 16), fewer only where the lengths are equal
+// (32 of 4096 on 8 heads: 47 us at 1, 51 at 2; 48 of 0..4095: 49.8 at 1, 46.5 at 2
+// and 47 up to 8).
 int attn_kv8_splits(int64_t b, int hkv, int64_t rows_per_head, int64_t max_len, int window, int64_t max_q) {
   const int nt = attn_kv8_nt(rows_per_head);
   const int64_t units = b * hkv * ((rows_per_head + 16 * nt - 1) / (16 * nt));
-  int64_t seen = max_len;
-  if (window > 0 && window + max_q < seen) seen = window + max_q;
-  const int64_t pages = (seen + kPage - 1) / kPage;
+  const int64_t pages = seen_pages(max_len, window, max_q);
   int64_t s = (2 * kCUs + units - 1) / units;
-  const int64_t most = (pages + 3) / 4;                 // a page for every wave
+  const int64_t most = (pages + kWaves - 1) / kWaves;
   if (s > most) s = most;
-  return (int)(s < 1 ? 1 : s > 256 ? 256 : s);
+  return (int)(s < 1 ? 1 : s > kMaxSplits ? kMaxSplits : s);
 }
 
 template <int D, int NT>
 static hipError_t launch_attn_t(const AttnArgs& a, hipStream_t stream) {
-  constexpr int W = 4;
-  hipLaunchKernelGGL((attn_kv8_kernel<D, NT, W>), dim3(a.splits, a.row_tiles * a.c.hkv, a.c.b), dim3(64 * W), 0,
+  constexpr int W = kWaves;
+  hipLaunchKernelGGL((attn_kv8_kernel<D, NT, W>), dim3(a.row_tiles * a.c.hkv, a.c.b, a.splits), dim3(64 * W), 0,
                      stream, a);
   hipError_t e = hipGetLastError();
   if (e != hipSuccess || a.splits == 1) return e;
-  hipLaunchKernelGGL((attn_kv8_join_kernel<D>), dim3(a.hq, a.max_q, a.c.b), dim3(256), 0, stream, a);
+  constexpr int R = 256 / (D / 4);
+  if (a.splits <= kFewSplits)
+    hipLaunchKernelGGL((attn_kv8_join_few_kernel<D>), dim3((a.hq + R - 1) / R, a.max_q, a.c.b), dim3(256), 0, stream, a);
+  else
+    hipLaunchKernelGGL((attn_kv8_join_kernel<D>), dim3(a.hq * (D / 32), a.max_q, a.c.b), dim3(256), 0, stream, a);
   return hipGetLastError();
 }
 
-hipError_t launch_attn_kv8(const Kv8Args& c, const void* q, int64_t q_ts, int64_t q_hs, int hq, int max_q, int window,
-                           float scale, void* out, int out_f32, int splits, float* part, uint32_t* status,
-                           hipStream_t stream) {
+hipError_t launch_attn_kv8(const Kv8Args& c, const void* q, int64_t q_ts, int64_t q_hs, int hq, int max_q,
+                           int64_t max_len, int window, float scale, void* out, int out_f32, int splits, float* part,
+                           uint32_t* status, hipStream_t stream) {
   const int group = hq / c.hkv;
   const int64_t rows_per_head = (int64_t)max_q * group;
   const int nt = attn_kv8_nt(rows_per_head);
-  AttnArgs a{c, static_cast<const uint16_t*>(q), q_ts, q_hs, hq, group, max_q, window, splits,
-             (int)((rows_per_head + 16 * nt - 1) / (16 * nt)), scale * 1.44269504088896340736f, out, out_f32,
+  const int64_t pages = seen_pages(max_len, window, max_q);
+  const int chunk = pages > splits ? (int)((pages + splits - 1) / splits) : 1;
+  AttnArgs a{c, static_cast<const uint16_t*>(q), q_ts, q_hs, hq, group, max_q, window, splits, chunk,
+             (int)((rows_per_head + 16 * nt - 1) / (16 * nt)), group > 1 ? (uint32_t)(((uint64_t)1 << 32) / group) : 0u,
+             scale * 1.44269504088896340736f, out, out_f32,
              part, part ? part + (size_t)splits * c.rows * hq * c.d : nullptr, status};
   switch (c.d * 4 + nt) {
 #define QG_ATTN(D, NT) \

@@ -447,8 +447,9 @@ int32_t qg_kv8_read(const int8_t *codes, const float *scales, int64_t pages, int
  * over the tokens j <= p (the row's own token p) and, where window > 0,
  * j > p - window; head h of hq reads key/value head h / (hq / hkv).  A row
  * that sees no token (length 0, or a row before token 0) is zero.  Softmax and
- * sums are fp32; the products' operands are bf16: q, the codes (exact), and
- * probability times value scale (rounded once).
+ * sums are fp32; the products' operands are fp16: q scaled by a power of two
+ * per row, the codes (exact), and probability times value scale, rounded once
+ * to 11 bits.
  *   q        in : bf16 [rows, hq, d], strides as qg_qk_norm_rope
  *   max_q    in : no sequence has more query rows (later ones are not written)
  *   max_len  in : an upper bound of lens, for the choice of the split only
