@@ -9,26 +9,29 @@
 // of x applied per group in fp32.  The hidden activation is rounded to bf16
 // once, as the second product's operand; all else is fp32.
 //
-// Four launches, no atomics (bit-identical repeats):
-//  1. router: logits in fp32.
-//  2. gate and up: a workgroup owns 32 hidden columns of one expert: four
-//     waves the 32 gate rows, four the 32 up rows, each a quarter of K; the
-//     two sums meet in LDS and leave as silu(g) u per (token, pick).
-//  3. down: the same kernel on two neighbouring 32-row blocks, fp32 results
-//     per (token, pick).
-//  4. combine: the weighted sum over a token's picks, in order of rank.
-// No launch plans the routing: each workgroup of 2 and 3 ranks the logits it
-// needs (a few KB from L2).  The rank of expert e for a token is the number of
-// experts before it, so "which tokens picked e" takes one ballot per 64
-// experts and token, and a token's pick number is that rank.  The grid has
-// min(t k, e) units: one per pick, where a pick that shares its expert with
-// an earlier token leaves at once, or one per expert.
+// Launches, with no atomics between workgroups (bit-identical repeats):
+//   router      logits in fp32
+//   route       above 4 tokens: the tokens of every expert
+//   gate and up the two products of 32 or 64 hidden columns of one expert, and
+//               silu(g) u of its tokens
+//   down        above 1 token: fp32 results per (token, pick); for 1 token
+//               the weighted sum over its picks as well
+//   combine     above 1 token: the weighted sum, in order of rank
+// The rank of expert e for a token is the number of experts before it, so "which
+// tokens picked e" takes one ballot per 64 experts and token, and a token's pick
+// number is that rank.  Up to 4 tokens each workgroup of the gate and up launch
+// ranks the logits itself (a few KB; 1 us less than another launch) and leaves
+// what it found to the down launch.  Its units are the picks: where an earlier
+// token picked the same expert a unit leaves at once, and the earlier one
+// takes all their tokens, so an expert is read once.
 //
-// Two forms of the product, chosen by the tokens the workgroup finds:
-//  * up to 4: the 4x4x4 sixteen-block matrix instruction with lane = weight row
-//    (the mapping of gemv_w4a16_mx4.hip);
-//  * more: 16x16x32 with 16 MT tokens at a time (the mapping of the register
-//    form of gemm_w4a16_mfma.hip), weights read again per 16 MT tokens (L2).
+// Three forms of the product:
+//  * up to 4 tokens of an expert: the 4x4x4 sixteen-block matrix instruction
+//    with lane = weight row (the mapping of gemv_w4a16_mx4.hip), K split over
+//    waves and summed in LDS;
+//  * more: 16x16x32 with the tokens staged in LDS, one wave per 16 weight rows
+//    through all of K (the mapping of the LDS form of gemm_w4a16_mfma.hip),
+//    MT = 1 or 2 tiles of 16 tokens at a time.
 #include "layer_common.h"
 #include "w4_common.h"
 
@@ -38,16 +41,19 @@ struct MoeArgs {
   const uint16_t *x, *router;
   const uint8_t *gate_up, *down;
   size_t gate_up_bytes, down_bytes;   // per expert
-  int t, h, e, inter, k, renorm, by_pick;
+  int t, h, e, inter, k, renorm;
   float* logits;                      // [t, e]
   float* picked;                      // [t * k] logits in order of rank
+  int32_t* unit;                      // up to 4 tokens: [t * k][8] expert, count, picks
+  int32_t* count;                     // above: [e] tokens of an expert
+  int32_t* list;                      // [e][64] their picks, t k + rank
   uint16_t* hidden;                   // [t * k, inter]
   float* part;                        // [t * k, h]
   void* y;
   int y_f32;
 };
 
-// ---- 1: router ---------------------------------------------------------------
+// ---- router ---------------------------------------------------------------
 
 // Up to 4 tokens: a wave per expert.
 __global__ __launch_bounds__(256) void moe_router_gemv_kernel(MoeArgs a) {
@@ -115,84 +121,160 @@ __device__ __forceinline__ uint32_t order_key(float l) {
   return (u & 0x80000000u) ? ~u : u | 0x80000000u;
 }
 
+// Up to 4 tokens: the expert of a pick and the tokens that picked it.
 struct MoePlan {
-  uint32_t key[512];
+  uint32_t key[4][512];
   int count[512];
-  int rank[64];
-  int tok[64], slot[64];   // tokens of the expert in order, and their picks t k + rank
+  int rank[4];
   int expert;
 };
 
-// The expert of this workgroup's unit and its tokens; returns how many (0:
-// nothing to do).  Workgroups of 512 threads.
-__device__ int moe_plan(const MoeArgs& a, int unit, MoePlan& p) {
+// Returns how many tokens the unit has (0: nothing to do), its picks in
+// `slot`, in order.  Workgroups of 1024 threads.
+__device__ int moe_plan(const MoeArgs& a, int unit, MoePlan& p, int (&slot)[4]) {
   const int tid = threadIdx.x, lane = tid & 63, wave = wave_id_uniform();
-  int first = -1, expert = unit;
-  if (a.by_pick) {
-    first = unit / a.k;
-    const int want = unit - first * a.k;
-    if (tid < a.e) p.key[tid] = order_key(a.logits[(size_t)first * a.e + tid]);
-    p.count[tid] = 0;
-    __syncthreads();
-    int width = 64;
-    while (width < a.e) width *= 2;
-    const int parts = 512 / width, e = tid & (width - 1), part = tid / width;
-    if (e < a.e) {
-      const uint32_t mine = p.key[e];
-      int c = 0;
-      for (int o = a.e * part / parts; o < a.e * (part + 1) / parts; ++o)
-        c += p.key[o] > mine || (p.key[o] == mine && o < e);
-      atomicAdd(&p.count[e], c);
-    }
-    __syncthreads();
-    if (tid < a.e && p.count[tid] == want) p.expert = tid;
-    __syncthreads();
-    expert = p.expert;
+  const int first = unit / a.k, want = unit - first * a.k;
+  for (int c = tid; c < a.t * a.e; c += 1024) {
+    const int t = c / a.e;
+    p.key[t][c - t * a.e] = order_key(a.logits[c]);
   }
-  for (int t = wave; t < a.t; t += 8) {
-    const float* row = a.logits + (size_t)t * a.e;
-    const uint32_t mine = order_key(row[expert]);
+  if (tid < 512) p.count[tid] = 0;
+  __syncthreads();
+  // expert with rank `want` of token `first`: 1024 / width lanes per expert
+  int width = 64;
+  while (width < a.e) width *= 2;
+  const int parts = 1024 / width, e = tid & (width - 1), part = tid / width;
+  if (e < a.e) {
+    const uint32_t mine = p.key[first][e];
+    int c = 0;
+#pragma unroll 8
+    for (int o = a.e * part / parts; o < a.e * (part + 1) / parts; ++o) {
+      const uint32_t u = p.key[first][o];
+      c += u > mine || (u == mine && o < e);
+    }
+    atomicAdd(&p.count[e], c);     // integers in LDS: no order to depend on
+  }
+  __syncthreads();
+  if (tid < a.e && p.count[tid] == want) p.expert = tid;
+  __syncthreads();
+  const int expert = p.expert;
+  if (wave < a.t) {
+    const uint32_t mine = p.key[wave][expert];
     int c = 0;
     for (int o = lane; o - lane < a.e; o += 64) {
-      const uint32_t u = o < a.e ? order_key(row[o]) : 0u;
+      const uint32_t u = o < a.e ? p.key[wave][o] : 0u;
       c += __popcll(__ballot(o < a.e && (u > mine || (u == mine && o < expert))));
     }
-    if (lane == 0) p.rank[t] = c;
+    if (lane == 0) p.rank[wave] = c;
   }
   __syncthreads();
-  const bool sel = lane < a.t && p.rank[lane < a.t ? lane : 0] < a.k;
-  const uint64_t mask = __ballot(sel);
-  const int n = __popcll(mask);
-  if (wave == 0 && sel) {
-    const int at = __popcll(mask & (((uint64_t)1 << lane) - 1));
-    p.tok[at] = lane;
-    p.slot[at] = lane * a.k + p.rank[lane];
+  int n = 0, before = 0;
+#pragma unroll
+  for (int t = 0; t < 4; ++t) {
+    if (t < a.t && p.rank[t] < a.k) {
+#pragma unroll
+      for (int u = 0; u < 4; ++u)
+        if (u == n) slot[u] = t * a.k + p.rank[t];
+      ++n;
+      before |= t < first;
+    }
   }
-  if (tid == 0) p.expert = expert;
-  __syncthreads();
-  return a.by_pick && n > 0 && p.tok[0] != first ? 0 : n;
+#pragma unroll
+  for (int u = 1; u < 4; ++u)
+    if (u >= n) slot[u] = slot[u - 1];
+  return before ? 0 : n;
 }
 
-// ---- 2 and 3: the experts' products ------------------------------------------
+// Above 4 tokens: a workgroup per expert ranks it for every token.
+__global__ __launch_bounds__(512) void moe_route_kernel(MoeArgs a) {
+  __shared__ int rank[64];
+  const int tid = threadIdx.x, lane = tid & 63, wave = wave_id_uniform();
+  const int expert = blockIdx.x;
+  // wave w: tokens w, w + 8, ..., all their loads of 64 experts in flight together
+  uint32_t mine[8];
+  int c[8];
+#pragma unroll
+  for (int u = 0; u < 8; ++u) {
+    const int t = wave + 8 * u;
+    mine[u] = t < a.t ? order_key(a.logits[(size_t)t * a.e + expert]) : 0u;
+    c[u] = 0;
+  }
+  for (int o0 = 0; o0 < a.e; o0 += 64) {
+    const int o = o0 + lane;
+    uint32_t key[8];
+#pragma unroll
+    for (int u = 0; u < 8; ++u) {
+      const int t = wave + 8 * u;
+      key[u] = t < a.t && o < a.e ? order_key(a.logits[(size_t)t * a.e + o]) : 0u;
+    }
+#pragma unroll
+    for (int u = 0; u < 8; ++u)
+      c[u] += __popcll(__ballot(o < a.e && (key[u] > mine[u] || (key[u] == mine[u] && o < expert))));
+  }
+#pragma unroll
+  for (int u = 0; u < 8; ++u)
+    if (lane == 0 && wave + 8 * u < a.t) rank[wave + 8 * u] = c[u];
+  __syncthreads();
+  if (wave != 0) return;
+  const bool sel = lane < a.t && rank[lane < a.t ? lane : 0] < a.k;
+  const uint64_t mask = __ballot(sel);
+  if (lane == 0) a.count[expert] = __popcll(mask);
+  if (sel) {
+    const int slot = lane * a.k + rank[lane];
+    a.list[expert * 64 + __popcll(mask & (((uint64_t)1 << lane) - 1))] = slot;
+    a.picked[slot] = a.logits[(size_t)lane * a.e + expert];
+  }
+}
+
+// The expert of a unit above 4 tokens: the unit-th that has tokens, or -1.
+__device__ __forceinline__ int moe_active(const MoeArgs& a, int unit, int& n) {
+  const int lane = threadIdx.x & 63;
+  int cnt[8], expert = -1, seen = 0;
+#pragma unroll
+  for (int u = 0; u < 8; ++u) cnt[u] = 64 * u + lane < a.e ? a.count[64 * u + lane] : 0;
+  n = 0;
+#pragma unroll
+  for (int u = 0; u < 8; ++u) {
+    const uint64_t mask = __ballot(cnt[u] > 0);
+    const bool me = cnt[u] > 0 && __popcll(mask & (((uint64_t)1 << lane) - 1)) == unit - seen;
+    const uint64_t hit = __ballot(me);
+    if (hit != 0) {
+      const int at = __builtin_ctzll(hit);
+      expert = 64 * u + at;
+      n = __builtin_amdgcn_readlane(cnt[u], at);
+    }
+    seen += __popcll(mask);
+  }
+  return expert;
+}
+
+// ---- the experts' products -----------------------------------------------------
 
 constexpr int kMoeXRow = 288;     // LDS bytes of a token's 128 k (two runs of 128, 16 apart)
 constexpr int kMoeXPair = 144;
 
-union MoeShared {
-  struct {
-    uint8_t x[8][4 * kMoeXRow];
-    float sum[8][4][4];           // group sums of x: [wave][group][token]
-  } s;
-  f32x4_t red[8][2][64];
-  float red4[8][4][64];
+struct MoeSlot {                  // of one wave
+  uint8_t x[4 * kMoeXRow];
+  float sum[4][4];                // group sums of x: [group][token]
 };
 
-// acc[m] += dequant(W)[row] . x_m over this wave's half tiles, for up to 4 rows
-// of activations; lane l holds row l & 31 and the group pair l >> 5.
-__device__ __forceinline__ void moe_mx4(float (&acc)[4], const uint8_t* tiles, int row, int halves, int kw,
-                                        const uint16_t* xrow, uint8_t* slot, float (*sums)[4]) {
+// A half tile (128 k) of a wave's 32 weight rows and the activations it meets.
+struct MoeHalf {
+  const uint8_t* tile;
+  int half;
+  const uint16_t* x;              // this lane's activation row, its first k
+  float p;                        // weight of the result
+};
+
+// acc[m] += p dequant(W)[row] . x_m over the wave's units u0, u0 + step, ...
+// below `units`, for up to 4 rows of activations; at(u) names unit u.  Lane l
+// holds row l & 31 of the half block `hb` and the group pair l >> 5, and copies
+// 8 k of activation row l >> 4.
+template <bool WEIGHTED, class At>
+__device__ __forceinline__ void moe_mx4(float (&acc)[4], int hb, int u0, int units, int step, MoeSlot& slot, At at) {
   using L = W4Layout<false>;
   const int lane = threadIdx.x & 63, lg = lane >> 5, sm = lane >> 4, sc = lane & 15;
+  const int row = 32 * hb + (lane & 31);
   const int swr = sm * kMoeXRow + 16 * sc + (sc >= 8 ? 16 : 0);
   const int srd = (lane & 3) * kMoeXRow + lg * kMoeXPair;
   const uint32_t mask_s = __builtin_amdgcn_readfirstlane(0x000F000Fu);
@@ -200,11 +282,13 @@ __device__ __forceinline__ void moe_mx4(float (&acc)[4], const uint8_t* tiles, i
   asm volatile("" : "+v"(magic_v));
   uint32_t ones_v = 0x3f803f80u;
   asm volatile("" : "+v"(ones_v));
-  auto load = [&](Half32Regs& r, u32x4_t& xv, int hs) {
-    L::load(r, tiles + (size_t)(hs >> 1) * L::kTile, hs & 1, lg, row);
-    xv = *reinterpret_cast<const u32x4_t*>(xrow + (size_t)hs * 128 + 8 * sc);
+  auto load = [&](Half32Regs& r, u32x4_t& xv, float& p, int u) {
+    const MoeHalf h = at(u);
+    L::load(r, h.tile, h.half, lg, row);
+    xv = *reinterpret_cast<const u32x4_t*>(h.x + 8 * sc);
+    p = h.p;
   };
-  auto compute = [&](const Half32Regs& r, const u32x4_t& xv) {
+  auto compute = [&](const Half32Regs& r, const u32x4_t& xv, float p) {
     float xp = dot2_bf16(xv.x, ones_v, 0.0f);
     xp = dot2_bf16(xv.y, ones_v, xp);
     xp = dot2_bf16(xv.z, ones_v, xp);
@@ -214,8 +298,8 @@ __device__ __forceinline__ void moe_mx4(float (&acc)[4], const uint8_t* tiles, i
     // wave-private slot: a wave's LDS operations complete in order
     __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
     __builtin_amdgcn_wave_barrier();
-    *reinterpret_cast<u32x4_t*>(slot + swr) = xv;
-    if ((sc & 3) == 0) sums[sc >> 2][sm] = xp;
+    *reinterpret_cast<u32x4_t*>(slot.x + swr) = xv;
+    if ((sc & 3) == 0) slot.sum[sc >> 2][sm] = xp;
     __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
     __builtin_amdgcn_wave_barrier();
     __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
@@ -223,7 +307,7 @@ __device__ __forceinline__ void moe_mx4(float (&acc)[4], const uint8_t* tiles, i
     for (int jj = 0; jj < 2; ++jj) {
       u32x4_t xa[4];
 #pragma unroll
-      for (int q = 0; q < 4; ++q) xa[q] = *reinterpret_cast<const u32x4_t*>(slot + srd + 64 * jj + 16 * q);
+      for (int q = 0; q < 4; ++q) xa[q] = *reinterpret_cast<const u32x4_t*>(slot.x + srd + 64 * jj + 16 * q);
       f32x4_t d = {0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
       for (int t = 0; t < 8; ++t) {
@@ -232,122 +316,33 @@ __device__ __forceinline__ void moe_mx4(float (&acc)[4], const uint8_t* tiles, i
         const u32x4_t xq = xa[t >> 1];
         d = mfma_4x4x4((t & 1) ? u32x2_t{xq.z, xq.w} : u32x2_t{xq.x, xq.y}, b, d);
       }
-      const float s = L::scale(r.sc, jj, 1.0f);
-      const f32x4_t xg = *reinterpret_cast<const f32x4_t*>(&sums[2 * lg + jj][0]);
+      const float s = WEIGHTED ? p * L::scale(r.sc, jj, 1.0f) : L::scale(r.sc, jj, 1.0f);
+      const f32x4_t xg = *reinterpret_cast<const f32x4_t*>(&slot.sum[2 * lg + jj][0]);
       const float zb = (float)(L::zero(r, jj) | 0x80u);
 #pragma unroll
       for (int m = 0; m < 4; ++m) acc[m] = __builtin_fmaf(s, __builtin_fmaf(-zb, xg[m], d[m]), acc[m]);
     }
   };
-  // two register sets in turn: the next half tile's loads in flight while
-  // this one computes
-  int hs = kw;
-  if (hs >= halves) return;
+  // two register sets in turn: the next unit's loads in flight while this
+  // one computes
+  int u = u0;
+  if (u >= units) return;
   Half32Regs ra, rb;
   u32x4_t xa, xb;
-  load(ra, xa, hs);
+  float pa, pb;
+  load(ra, xa, pa, u);
   __builtin_amdgcn_sched_barrier(0);
   while (true) {
-    if (hs + 4 >= halves) { compute(ra, xa); break; }
-    load(rb, xb, hs + 4);
+    if (u + step >= units) { compute(ra, xa, pa); break; }
+    load(rb, xb, pb, u + step);
     __builtin_amdgcn_sched_barrier(0);
-    compute(ra, xa);
-    hs += 4;
-    if (hs + 4 >= halves) { compute(rb, xb); break; }
-    load(ra, xa, hs + 4);
+    compute(ra, xa, pa);
+    u += step;
+    if (u + step >= units) { compute(rb, xb, pb); break; }
+    load(ra, xa, pa, u + step);
     __builtin_amdgcn_sched_barrier(0);
-    compute(rb, xb);
-    hs += 4;
-  }
-}
-
-template <int MT>
-struct MoeUnit {
-  u32x4_t w[2];           // chunk of group a, row 16t + i
-  u32x2_t sc;             // row l & 31: the half tile's 4 scales
-  uint32_t zw;            // and zero points
-  u32x4_t x[MT][4];       // x[token 16 mt + i][32 g + 8 a ..]
-};
-
-// Two copies of a register whose 16-lane rows hold (r0, r1, r0, r1): row 0 and row 1 of it in every lane row.
-__device__ __forceinline__ u32x2_t spread2(uint32_t v) {
-  const auto s = __builtin_amdgcn_permlane16_swap(v, v, false, false);
-  return u32x2_t{s[0], s[1]};
-}
-
-// The same for 16 MT rows of activations: acc[t][mt][e] is weight row 16t + i
-// and activation row 16 mt + 4a + e.
-template <int MT>
-__device__ __forceinline__ void moe_mx16(f32x4_t (&acc)[2][MT], const uint8_t* tiles, int hb, int halves, int kw,
-                                         const uint16_t* const (&xrow)[MT]) {
-  const int lane = threadIdx.x & 63, i = lane & 15, a = lane >> 4, row = 32 * hb + (lane & 31);
-  const uint32_t mask_s = __builtin_amdgcn_readfirstlane(0x000F000Fu);
-  uint32_t magic_v = 0x43004300u;
-  asm volatile("" : "+v"(magic_v));
-  uint32_t one2 = 0x3f803f80u;
-  asm volatile("" : "+v"(one2));
-  const bf16x8_t ones = __builtin_bit_cast(bf16x8_t, u32x4_t{one2, one2, one2, one2});
-  const f32x4_t zero4 = {0.0f, 0.0f, 0.0f, 0.0f};
-  auto load = [&](MoeUnit<MT>& u, int hs) {
-    const BufView v(tiles + (size_t)(hs >> 1) * kTileBytes, kTileBytes);
-    const int half = hs & 1;
-#pragma unroll
-    for (int t = 0; t < 2; ++t)
-      u.w[t] = v.b128<true>((uint32_t)((4 * half + a) * kTileRows + 32 * hb + 16 * t + i) * 16u);
-    u.sc = v.b64((uint32_t)(kScaleOff + row * 16 + 8 * half));
-    u.zw = v.b16((uint32_t)(kZeroOff + row * 4 + 2 * half));
-#pragma unroll
-    for (int mt = 0; mt < MT; ++mt)
-#pragma unroll
-      for (int g = 0; g < 4; ++g)
-        u.x[mt][g] = *reinterpret_cast<const u32x4_t*>(xrow[mt] + (size_t)hs * 128 + 32 * g + 8 * a);
-  };
-  auto compute = [&](MoeUnit<MT>& u) {
-    transpose_rows4(u.w[0]);
-    transpose_rows4(u.w[1]);
-    const u32x2_t s0 = spread2(u.sc.x), s1 = spread2(u.sc.y), zz = spread2(u.zw);
-#pragma unroll
-    for (int g = 0; g < 4; ++g) {
-      f32x4_t xg[MT];
-#pragma unroll
-      for (int mt = 0; mt < MT; ++mt)
-        xg[mt] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8_t, u.x[mt][g]), ones, zero4, 0, 0, 0);
-#pragma unroll
-      for (int t = 0; t < 2; ++t) {
-        u32x4_t bp;
-#pragma unroll
-        for (int e = 0; e < 4; ++e) bp[e] = code_pair(u.w[t][g], e, mask_s, magic_v);
-        const uint32_t sw = g < 2 ? s0[t] : s1[t];
-        const float s = fp16_to_f32((sw >> (16 * (g & 1))) & 0xffffu);
-        const float zb = (float)(((zz[t] >> (4 * g)) & 15u) | 0x80u);
-#pragma unroll
-        for (int mt = 0; mt < MT; ++mt) {
-          const f32x4_t p = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8_t, u.x[mt][g]),
-                                                                    __builtin_bit_cast(bf16x8_t, bp), zero4, 0, 0, 0);
-#pragma unroll
-          for (int e = 0; e < 4; ++e)
-            acc[t][mt][e] = __builtin_fmaf(s, __builtin_fmaf(-zb, xg[mt][e], p[e]), acc[t][mt][e]);
-        }
-      }
-      __builtin_amdgcn_sched_barrier(0);   // a group's products are not all live at once
-    }
-  };
-  int hs = kw;
-  if (hs >= halves) return;
-  MoeUnit<MT> ua, ub;
-  load(ua, hs);
-  __builtin_amdgcn_sched_barrier(0);
-  while (true) {
-    if (hs + 4 >= halves) { compute(ua); break; }
-    load(ub, hs + 4);
-    __builtin_amdgcn_sched_barrier(0);
-    compute(ua);
-    hs += 4;
-    if (hs + 4 >= halves) { compute(ub); break; }
-    load(ua, hs + 4);
-    __builtin_amdgcn_sched_barrier(0);
-    compute(ub);
-    hs += 4;
+    compute(rb, xb, pb);
+    u += step;
   }
 }
 
@@ -356,129 +351,344 @@ __device__ __forceinline__ uint16_t silu_mul(float g, float u) {
   return (uint16_t)f32_to_bf16_rne(g / (1.0f + __builtin_amdgcn_exp2f(-1.44269504088896340736f * g)) * u);
 }
 
-// SMALL: no expert has more than 4 tokens (at most 4 tokens in all).
-template <bool DOWN, bool SMALL>
-__global__ __launch_bounds__(512) void moe_expert_kernel(MoeArgs a) {
-  __shared__ MoePlan plan;
-  __shared__ __attribute__((aligned(16))) MoeShared sh;
-  const int n = moe_plan(a, blockIdx.y, plan);
-  if (n == 0) return;                        // uniform over the workgroup
+// Up to 4 tokens.  A workgroup of 16 waves owns two blocks of 32 weight rows
+// (gate and up rows of 32 hidden columns; two neighbouring blocks of the down
+// matrix), 8 waves each, K split over them.
+template <bool DOWN>
+__global__ __launch_bounds__(1024) void moe_small_kernel(MoeArgs a) {
+  union Shared {
+    MoePlan plan;
+    MoeSlot slot[16];
+    float red[16][4][64];
+  };
+  __shared__ __attribute__((aligned(16))) Shared sh;
   const int tid = threadIdx.x, lane = tid & 63, wave = wave_id_uniform();
-  const int blk = wave >> 2, kw = wave & 3;
-  const int tile = blockIdx.x, expert = plan.expert;
-  if (!DOWN && tile == 0 && tid < n) {
-    const int t = plan.tok[tid];
-    a.picked[plan.slot[tid]] = a.logits[(size_t)t * a.e + expert];
+  const int blk = wave >> 3, kw = wave & 7;
+  const int tile = blockIdx.x, unit = blockIdx.y;
+  int n, expert, slot[4];
+  if constexpr (DOWN) {
+    const int32_t* const u = a.unit + unit * 8;
+    expert = u[0];
+    n = u[1];
+#pragma unroll
+    for (int m = 0; m < 4; ++m) slot[m] = u[2 + m];
+  } else {
+    n = moe_plan(a, unit, sh.plan, slot);
+    expert = sh.plan.expert;
+    if (tile == 0 && tid == 0) {
+      int32_t* const u = a.unit + unit * 8;
+      u[0] = expert;
+      u[1] = n;
+#pragma unroll
+      for (int m = 0; m < 4; ++m) {
+        u[2 + m] = slot[m];
+        if (m < n) a.picked[slot[m]] = a.logits[(size_t)(slot[m] / a.k) * a.e + expert];
+      }
+    }
+    __syncthreads();                 // the plan's LDS becomes the waves' slots
   }
-  const int kdim = DOWN ? a.inter : a.h, halves = kdim >> 7;
-  // gate_up: gate rows 32 tile.. and up rows inter + 32 tile..; down: rows
-  // 64 tile.. and 64 tile + 32..
+  if (n == 0) return;                // uniform over the workgroup
+  const int kdim = DOWN ? a.inter : a.h;
   const int rb = DOWN ? tile : (tile >> 1) + blk * (a.inter >> 6);
   const int hb = DOWN ? blk : tile & 1;
   const uint8_t* const tiles = (DOWN ? a.down + expert * a.down_bytes : a.gate_up + expert * a.gate_up_bytes) +
                                (size_t)rb * (kdim >> 8) * kTileBytes;
-  auto source = [&](int m) {                 // activation row of the expert's m-th token
-    m = m < n ? m : n - 1;
-    return DOWN ? a.hidden + (size_t)plan.slot[m] * a.inter : a.x + (size_t)plan.tok[m] * a.h;
-  };
-  // Row r (of 32) of block b for the m-th token: v0, v1 the sums of both blocks.
-  auto store = [&](int m, int r, float v0, float v1) {
-    const size_t slot = plan.slot[m];
+  const int sm = lane >> 4;
+  const int mine = sm == 0 ? slot[0] : sm == 1 ? slot[1] : sm == 2 ? slot[2] : slot[3];
+  const uint16_t* const x = DOWN ? a.hidden + (size_t)mine * a.inter : a.x + (size_t)(mine / a.k) * a.h;
+  float acc[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+  moe_mx4<false>(acc, hb, kw, kdim >> 7, 8, sh.slot[wave], [&](int u) {
+    return MoeHalf{tiles + (size_t)(u >> 1) * kTileBytes, u & 1, x + (size_t)u * 128, 1.0f};
+  });
+  __syncthreads();
+#pragma unroll
+  for (int m = 0; m < 4; ++m) sh.red[wave][m][lane] = acc[m];
+  __syncthreads();
+  if (tid < 32 * n) {
+    const int m = tid >> 5, r = tid & 31;
+    const size_t s = m == 0 ? slot[0] : m == 1 ? slot[1] : m == 2 ? slot[2] : slot[3];
+    float v[2];
+#pragma unroll
+    for (int b = 0; b < 2; ++b) {
+      v[b] = 0.0f;
+#pragma unroll
+      for (int w = 0; w < 8; ++w) v[b] += sh.red[8 * b + w][m][r] + sh.red[8 * b + w][m][r + 32];
+    }
     if constexpr (DOWN) {
-      float* const o = a.part + slot * a.h + 64 * tile + r;
-      o[0] = v0;
-      o[32] = v1;
+      a.part[s * a.h + 64 * tile + r] = v[0];
+      a.part[s * a.h + 64 * tile + 32 + r] = v[1];
     } else {
-      a.hidden[slot * a.inter + 32 * tile + r] = silu_mul(v0, v1);
-    }
-  };
-
-  if (SMALL || n <= 4) {
-    float acc[4] = {0.0f, 0.0f, 0.0f, 0.0f};
-    moe_mx4(acc, tiles, 32 * hb + (lane & 31), halves, kw, source(lane >> 4), sh.s.x[wave], sh.s.sum[wave]);
-    __syncthreads();
-#pragma unroll
-    for (int m = 0; m < 4; ++m) sh.red4[wave][m][lane] = acc[m];
-    __syncthreads();
-    if (tid < 32 * n) {
-      const int m = tid >> 5, r = tid & 31;
-      float v[2];
-#pragma unroll
-      for (int b = 0; b < 2; ++b) {
-        v[b] = 0.0f;
-#pragma unroll
-        for (int w = 0; w < 4; ++w) v[b] += sh.red4[4 * b + w][m][r] + sh.red4[4 * b + w][m][r + 32];
-      }
-      store(m, r, v[0], v[1]);
-    }
-    return;
-  }
-  if constexpr (!SMALL) {
-    const int i = lane & 15;
-    auto finish = [&](const f32x4_t (&acc0)[2], int m0) {   // tokens m0 .. m0 + 15
-      __syncthreads();
-#pragma unroll
-      for (int t = 0; t < 2; ++t) sh.red[wave][t][lane] = acc0[t];
-      __syncthreads();
-      if (tid < 128) {
-        const int t = tid >> 6, l = tid & 63;
-        f32x4_t v[2];
-#pragma unroll
-        for (int b = 0; b < 2; ++b) {
-          v[b] = sh.red[4 * b][t][l];
-#pragma unroll
-          for (int w = 1; w < 4; ++w) {
-            const f32x4_t u = sh.red[4 * b + w][t][l];
-            v[b] = f32x4_t{v[b][0] + u[0], v[b][1] + u[1], v[b][2] + u[2], v[b][3] + u[3]};
-          }
-        }
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          const int m = m0 + 4 * (l >> 4) + e;
-          if (m < n) store(m, 16 * t + (l & 15), v[0][e], v[1][e]);
-        }
-      }
-    };
-    if (n <= 16) {
-      f32x4_t acc[2][1] = {};
-      const uint16_t* const rows[1] = {source(i)};
-      moe_mx16<1>(acc, tiles, hb, halves, kw, rows);
-      const f32x4_t one[2] = {acc[0][0], acc[1][0]};
-      finish(one, 0);
-    } else {
-      for (int m0 = 0; m0 < n; m0 += 32) {
-        f32x4_t acc[2][2] = {};
-        const uint16_t* const rows[2] = {source(m0 + i), source(m0 + 16 + i)};
-        moe_mx16<2>(acc, tiles, hb, halves, kw, rows);
-#pragma unroll
-        for (int mt = 0; mt < 2; ++mt) {
-          const f32x4_t one[2] = {acc[0][mt], acc[1][mt]};
-          finish(one, m0 + 16 * mt);
-        }
-      }
+      a.hidden[s * a.inter + 32 * tile + r] = silu_mul(v[0], v[1]);
     }
   }
 }
 
-// ---- 4: combine ----------------------------------------------------------------
-
-__global__ __launch_bounds__(256) void moe_combine_kernel(MoeArgs a) {
-  const int t = blockIdx.y, c = blockIdx.x * 1024 + threadIdx.x * 4;
-  const int lane = threadIdx.x & 63;
-  const float* const l = a.picked + (size_t)t * a.k;
-  const float top = l[0];                      // rank 0: the largest
+// The softmax denominator of a token's picks, relative to its first logit.
+__device__ __forceinline__ float moe_total(const MoeArgs& a, int t, const float* l) {
   float total = 0.0f;
   if (a.renorm) {
-    for (int j = 0; j < a.k; ++j) total += expf(l[j] - top);
+    for (int j = 0; j < a.k; ++j) total += expf(l[j] - l[0]);
   } else {
-    for (int e = lane; e < a.e; e += 64) total += expf(a.logits[(size_t)t * a.e + e] - top);
+    for (int e = threadIdx.x & 63; e < a.e; e += 64) total += expf(a.logits[(size_t)t * a.e + e] - l[0]);
 #pragma unroll
     for (int o = 1; o < 64; o *= 2) total += __shfl_xor(total, o);
   }
+  return total;
+}
+
+// One token: 32 rows of the output through all its picks, 16 waves taking half
+// tiles of the picks in turn, the picks' weights applied with the group scales.
+__global__ __launch_bounds__(1024) void moe_down_one_kernel(MoeArgs a) {
+  union Shared {
+    MoeSlot slot[16];
+    float red[16][64];
+  };
+  __shared__ __attribute__((aligned(16))) Shared sh;
+  __shared__ float p[32];
+  __shared__ int expert[32];
+  const int tid = threadIdx.x, lane = tid & 63, wave = wave_id_uniform();
+  const int tile = blockIdx.x;
+  const float total = moe_total(a, 0, a.picked);
+  if (tid < a.k) {
+    p[tid] = expf(a.picked[tid] - a.picked[0]) / total;
+    expert[tid] = a.unit[tid * 8];
+  }
+  __syncthreads();
+  const int halves = a.inter >> 7;
+  const size_t block = (size_t)(tile >> 1) * (a.inter >> 8) * kTileBytes;
+  float acc[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+  moe_mx4<true>(acc, tile & 1, wave, a.k * halves, 16, sh.slot[wave], [&](int u) {
+    const int j = __builtin_amdgcn_readfirstlane(u / halves), hs = u - j * halves;
+    return MoeHalf{a.down + __builtin_amdgcn_readfirstlane(expert[j]) * a.down_bytes + block + (size_t)(hs >> 1) * kTileBytes,
+                   hs & 1, a.hidden + (size_t)j * a.inter + (size_t)hs * 128, p[j]};
+  });
+  __syncthreads();
+  sh.red[wave][lane] = acc[0];
+  __syncthreads();
+  if (tid >= 32) return;
+  float v = 0.0f;
+#pragma unroll
+  for (int w = 0; w < 16; ++w) v += sh.red[w][tid] + sh.red[w][tid + 32];
+  if (a.y_f32)
+    static_cast<float*>(a.y)[32 * tile + tid] = v;
+  else
+    static_cast<uint16_t*>(a.y)[32 * tile + tid] = (uint16_t)f32_to_bf16_rne(v);
+}
+
+// A barrier for LDS alone: loads from memory stay in flight across it.
+__device__ __forceinline__ void lds_barrier() {
+  __builtin_amdgcn_fence(__ATOMIC_RELEASE, "workgroup", "local");
+  __builtin_amdgcn_s_barrier();
+  __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "workgroup", "local");
+}
+
+struct MoeTile {                  // one 256-k tile of a wave's 16 rows: lane (i, a)
+  u32x4_t c0, c1;                 // chunks of groups a and 4 + a, row 16t + i
+  u32x4_t sc;                     // the row's 8 scales
+  uint32_t zw;                    // and zero points
+};
+
+// acc[mt][e] += row 16t + i of the block times activation row 16 mt + 4a + e,
+// over all of K.  The workgroup's 512 threads copy the 16 MT activation rows of
+// a 256-k tile into one of two LDS buffers: 16-byte piece c of row r at 32 r +
+// (c ^ (r & 15)), so that the operand reads of 16 lanes, one row each, fall on
+// distinct banks; xr: this thread's rows tid / 32 + 16 j.  Codes go two tiles
+// ahead, activations one (through registers).
+template <int MT>
+__device__ __forceinline__ void moe_mx16(f32x4_t (&acc)[MT], const uint8_t* tiles, int t, int kt_count,
+                                         const uint16_t* const (&xr)[MT], uint8_t* xs) {
+  const int tid = threadIdx.x, lane = tid & 63, i = lane & 15, a = lane >> 4;
+  const uint32_t mask_s = __builtin_amdgcn_readfirstlane(0x000F000Fu);
+  uint32_t magic_v = 0x43004300u;
+  asm volatile("" : "+v"(magic_v));
+  const f32x4_t zero4 = {0.0f, 0.0f, 0.0f, 0.0f};
+  const int pc = tid & 31, pr = tid >> 5;
+  auto load_w = [&](MoeTile& w, int kt) {
+    const BufView v(tiles + (size_t)kt * kTileBytes, kTileBytes);
+    const uint32_t row = (uint32_t)(16 * t + i), r0 = (uint32_t)a * kTileRows + row;
+    w.c0 = v.b128<true>(r0 * 16u);
+    w.c1 = v.b128<true>((r0 + 4 * kTileRows) * 16u);
+    w.sc = v.b128<false>(kScaleOff + row * 16u);
+    w.zw = v.b32(kZeroOff + row * 4u);
+  };
+  auto load_x = [&](u32x4_t (&x)[MT], int kt) {
+#pragma unroll
+    for (int j = 0; j < MT; ++j) x[j] = *reinterpret_cast<const u32x4_t*>(xr[j] + (size_t)kt * 256 + 8 * pc);
+  };
+  auto store_x = [&](const u32x4_t (&x)[MT], int buf) {
+#pragma unroll
+    for (int j = 0; j < MT; ++j)
+      *reinterpret_cast<u32x4_t*>(xs + buf * (MT * 8192) + 16 * (32 * (pr + 16 * j) + (pc ^ pr))) = x[j];
+  };
+  auto compute = [&](MoeTile& w, int buf) {
+    transpose_rows4(w.c0);
+    transpose_rows4(w.c1);
+    const uint8_t* const xb = xs + buf * (MT * 8192);
+#pragma unroll
+    for (int g = 0; g < 8; ++g) {
+      const uint32_t dw = g < 4 ? w.c0[g] : w.c1[g - 4];
+      u32x4_t bp;
+#pragma unroll
+      for (int e = 0; e < 4; ++e) bp[e] = code_pair(dw, e, mask_s, magic_v);
+      const uint32_t z = (w.zw >> (4 * g)) & 15u;
+      const uint32_t zn = (z | (z << 16)) | 0xC300C300u;     // bf16 pair -(128 + zp)
+      const u32x4_t zz = {zn, zn, zn, zn};
+      const float s = fp16_to_f32((w.sc[g >> 1] >> (16 * (g & 1))) & 0xffffu);
+      bf16x8_t av[MT];
+      f32x4_t d[MT];
+#pragma unroll
+      for (int mt = 0; mt < MT; ++mt) {
+        const u32x4_t x = *reinterpret_cast<const u32x4_t*>(xb + 16 * (32 * (16 * mt + i) + ((4 * g + a) ^ i)));
+        av[mt] = __builtin_bit_cast(bf16x8_t, x);
+        d[mt] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(av[mt], __builtin_bit_cast(bf16x8_t, bp), zero4, 0, 0, 0);
+      }
+#pragma unroll
+      for (int mt = 0; mt < MT; ++mt)
+        d[mt] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(av[mt], __builtin_bit_cast(bf16x8_t, zz), d[mt], 0, 0, 0);
+#pragma unroll
+      for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) acc[mt][e] = __builtin_fmaf(s, d[mt][e], acc[mt][e]);
+    }
+  };
+  MoeTile w0, w1;
+  u32x4_t x[MT];
+  load_x(x, 0);
+  load_w(w0, 0);
+  store_x(x, 0);
+  const int last = kt_count - 1;
+  load_x(x, min(1, last));
+  load_w(w1, min(1, last));
+  lds_barrier();
+  // tile kt in LDS buffer kt & 1 and set 0 (even) or 1 (odd); the loads past the
+  // end read the last tile again and are not used
+  for (int kt = 0;;) {
+    store_x(x, (kt + 1) & 1);
+    load_x(x, min(kt + 2, last));
+    compute(w0, kt & 1);
+    load_w(w0, min(kt + 2, last));
+    lds_barrier();
+    if (++kt > last) break;
+    store_x(x, (kt + 1) & 1);
+    load_x(x, min(kt + 2, last));
+    compute(w1, kt & 1);
+    load_w(w1, min(kt + 2, last));
+    lds_barrier();
+    if (++kt > last) break;
+  }
+}
+
+// Above 4 tokens.  A workgroup of 8 waves owns two 64-row blocks (gate and up
+// rows of 64 hidden columns; two neighbouring blocks of the down matrix).
+template <bool DOWN>
+__global__ __launch_bounds__(512) void moe_expert_kernel(MoeArgs a) {
+  union Shared {
+    MoeSlot slot[8];
+    float red[8][4][64];
+    uint8_t x[2 * 2 * 8192];
+    f32x4_t up[4][2][64];
+  };
+  __shared__ __attribute__((aligned(16))) Shared sh;
+  __shared__ int slots[64];
+  const int tid = threadIdx.x, lane = tid & 63, wave = wave_id_uniform();
+  int n;
+  const int expert = moe_active(a, blockIdx.y, n);
+  if (expert < 0) return;                    // uniform over the workgroup
+  if (tid < n) slots[tid] = a.list[expert * 64 + tid];
+  __syncthreads();
+  const int blk = wave >> 2, tile = blockIdx.x;
+  const int kdim = DOWN ? a.inter : a.h;
+  const int rb = DOWN ? 2 * tile + blk : tile + blk * (a.inter >> 6);
+  const uint8_t* const tiles = (DOWN ? a.down + expert * a.down_bytes : a.gate_up + expert * a.gate_up_bytes) +
+                               (size_t)rb * (kdim >> 8) * kTileBytes;
+  auto source = [&](int m) {                 // activation row of the expert's m-th token
+    const int s = slots[m < n ? m : n - 1];
+    return DOWN ? a.hidden + (size_t)s * a.inter : a.x + (size_t)(s / a.k) * a.h;
+  };
+
+  if (n <= 4) {
+    const int hb = (wave >> 1) & 1, kw = wave & 1;
+    const uint16_t* const x = source(lane >> 4);
+    float acc[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+    moe_mx4<false>(acc, hb, kw, kdim >> 7, 2, sh.slot[wave], [&](int u) {
+      return MoeHalf{tiles + (size_t)(u >> 1) * kTileBytes, u & 1, x + (size_t)u * 128, 1.0f};
+    });
+    __syncthreads();
+#pragma unroll
+    for (int m = 0; m < 4; ++m) sh.red[wave][m][lane] = acc[m];
+    __syncthreads();
+    if (tid < 64 * n) {
+      const int m = tid >> 6, r = tid & 63, w = 2 * (r >> 5), l = r & 31;
+      const size_t s = slots[m];
+      float v[2];
+#pragma unroll
+      for (int b = 0; b < 2; ++b)
+        v[b] = (sh.red[4 * b + w][m][l] + sh.red[4 * b + w][m][l + 32]) +
+               (sh.red[4 * b + w + 1][m][l] + sh.red[4 * b + w + 1][m][l + 32]);
+      if constexpr (DOWN) {
+        a.part[s * a.h + 128 * tile + r] = v[0];
+        a.part[s * a.h + 128 * tile + 64 + r] = v[1];
+      } else {
+        a.hidden[s * a.inter + 64 * tile + r] = silu_mul(v[0], v[1]);
+      }
+    }
+    return;
+  }
+
+  const int t = wave & 3, i = lane & 15;
+  // acc0: 16 tokens m0 .. of this wave's 16 rows
+  auto finish = [&](const f32x4_t (&acc0)[2], int tiles_of_16, int m0) {
+    if constexpr (!DOWN) {
+      __syncthreads();
+      if (blk == 1)
+        for (int mt = 0; mt < tiles_of_16; ++mt) sh.up[t][mt][lane] = acc0[mt];
+      __syncthreads();
+      if (blk == 1) return;
+    }
+#pragma unroll
+    for (int mt = 0; mt < 2; ++mt) {
+      if (mt >= tiles_of_16) continue;
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        const int m = m0 + 16 * mt + 4 * (lane >> 4) + e;
+        if (m < n) {
+          const size_t s = slots[m];
+          if constexpr (DOWN)
+            a.part[s * a.h + 128 * tile + 64 * blk + 16 * t + i] = acc0[mt][e];
+          else
+            a.hidden[s * a.inter + 64 * tile + 16 * t + i] = silu_mul(acc0[mt][e], sh.up[t][mt][lane][e]);
+        }
+      }
+    }
+  };
+  const int row = tid >> 5;
+  if (n <= 16) {
+    f32x4_t acc[1] = {};
+    const uint16_t* const xr[1] = {source(row)};
+    moe_mx16<1>(acc, tiles, t, kdim >> 8, xr, sh.x);
+    const f32x4_t both[2] = {acc[0], acc[0]};
+    finish(both, 1, 0);
+  } else {
+    for (int m0 = 0; m0 < n; m0 += 32) {
+      f32x4_t acc[2] = {};
+      const uint16_t* const xr[2] = {source(m0 + row), source(m0 + 16 + row)};
+      if (m0 > 0) __syncthreads();             // the LDS of the tokens before is done with
+      moe_mx16<2>(acc, tiles, t, kdim >> 8, xr, sh.x);
+      finish(acc, 2, m0);
+    }
+  }
+}
+
+// ---- combine ----------------------------------------------------------------
+
+__global__ __launch_bounds__(256) void moe_combine_kernel(MoeArgs a) {
+  const int t = blockIdx.y, c = blockIdx.x * 1024 + threadIdx.x * 4;
+  const float* const l = a.picked + (size_t)t * a.k;
+  const float total = moe_total(a, t, l);
   if (c >= a.h) return;
   f32x4_t y = {0.0f, 0.0f, 0.0f, 0.0f};
   for (int j = 0; j < a.k; ++j) {
-    const float p = expf(l[j] - top) / total;
+    const float p = expf(l[j] - l[0]) / total;
     const f32x4_t v = *reinterpret_cast<const f32x4_t*>(a.part + ((size_t)t * a.k + j) * a.h + c);
 #pragma unroll
     for (int e = 0; e < 4; ++e) y[e] = __builtin_fmaf(p, v[e], y[e]);
@@ -490,11 +700,12 @@ __global__ __launch_bounds__(256) void moe_combine_kernel(MoeArgs a) {
     *reinterpret_cast<u32x2_t*>(static_cast<uint16_t*>(a.y) + at) = u32x2_t{pack_bf16(y[0], y[1]), pack_bf16(y[2], y[3])};
 }
 
-// Workspace: logits, picked logits, hidden, partial results, each on 256 bytes.
+// Workspace: each part on 256 bytes.
 static int64_t up256(int64_t n) { return (n + 255) & ~(int64_t)255; }
 
 int64_t moe_ws_bytes(int64_t t, int64_t h, int64_t e, int64_t inter, int64_t k) {
-  return up256(t * e * 4) + up256(t * k * 4) + up256(t * k * inter * 2) + up256(t * k * h * 4);
+  return up256(t * e * 4) + up256(t * k * 4) + up256(t * k * inter * 2) + up256(t * k * h * 4) +
+         (t <= 4 ? up256(t * k * 32) : up256(e * 4) + up256(e * 256));
 }
 
 hipError_t launch_moe_w4a16(const void* x, int t, int h, const void* router, int e, const void* gate_up,
@@ -507,36 +718,49 @@ hipError_t launch_moe_w4a16(const void* x, int t, int h, const void* router, int
   a.down = static_cast<const uint8_t*>(down);
   a.gate_up_bytes = gate_up_bytes, a.down_bytes = down_bytes;
   a.t = t, a.h = h, a.e = e, a.inter = inter, a.k = k, a.renorm = renorm;
-  a.by_pick = t * k < e;
   char* w = static_cast<char*>(ws);
-  a.logits = reinterpret_cast<float*>(w);
-  w += up256((int64_t)t * e * 4);
-  a.picked = reinterpret_cast<float*>(w);
-  w += up256((int64_t)t * k * 4);
-  a.hidden = reinterpret_cast<uint16_t*>(w);
-  w += up256((int64_t)t * k * inter * 2);
-  a.part = reinterpret_cast<float*>(w);
+  auto take = [&](int64_t bytes) {
+    char* const p = w;
+    w += up256(bytes);
+    return p;
+  };
+  a.logits = reinterpret_cast<float*>(take((int64_t)t * e * 4));
+  a.picked = reinterpret_cast<float*>(take((int64_t)t * k * 4));
+  a.hidden = reinterpret_cast<uint16_t*>(take((int64_t)t * k * inter * 2));
+  a.part = reinterpret_cast<float*>(take((int64_t)t * k * h * 4));
+  if (t <= 4) {
+    a.unit = reinterpret_cast<int32_t*>(take((int64_t)t * k * 32));
+  } else {
+    a.count = reinterpret_cast<int32_t*>(take((int64_t)e * 4));
+    a.list = reinterpret_cast<int32_t*>(take((int64_t)e * 256));
+  }
   a.y = y, a.y_f32 = y_f32;
 
-  if (t <= 4)
-    hipLaunchKernelGGL(moe_router_gemv_kernel, dim3((e + 3) / 4), dim3(256), 0, stream, a);
-  else
-    hipLaunchKernelGGL(moe_router_mfma_kernel, dim3((e + 15) / 16, (t + 15) / 16), dim3(1024), 0, stream, a);
-  hipError_t st = hipGetLastError();
-  if (st != hipSuccess) return st;
-  const int units = a.by_pick ? t * k : e;
-  const dim3 g1(inter / 32, units), g2(h / 64, units);
+  hipError_t st = hipSuccess;
+  auto ok = [&] { return (st = hipGetLastError()) == hipSuccess; };
+  const dim3 combine((h + 1023) / 1024, t);
   if (t <= 4) {
-    hipLaunchKernelGGL((moe_expert_kernel<false, true>), g1, dim3(512), 0, stream, a);
-    if ((st = hipGetLastError()) != hipSuccess) return st;
-    hipLaunchKernelGGL((moe_expert_kernel<true, true>), g2, dim3(512), 0, stream, a);
+    hipLaunchKernelGGL(moe_router_gemv_kernel, dim3((e + 3) / 4), dim3(256), 0, stream, a);
+    if (!ok()) return st;
+    hipLaunchKernelGGL((moe_small_kernel<false>), dim3(inter / 32, t * k), dim3(1024), 0, stream, a);
+    if (!ok()) return st;
+    if (t == 1) {
+      hipLaunchKernelGGL(moe_down_one_kernel, dim3(h / 32), dim3(1024), 0, stream, a);
+      return hipGetLastError();
+    }
+    hipLaunchKernelGGL((moe_small_kernel<true>), dim3(h / 64, t * k), dim3(1024), 0, stream, a);
   } else {
-    hipLaunchKernelGGL((moe_expert_kernel<false, false>), g1, dim3(512), 0, stream, a);
-    if ((st = hipGetLastError()) != hipSuccess) return st;
-    hipLaunchKernelGGL((moe_expert_kernel<true, false>), g2, dim3(512), 0, stream, a);
+    const int units = t * k < e ? t * k : e;
+    hipLaunchKernelGGL(moe_router_mfma_kernel, dim3((e + 15) / 16, (t + 15) / 16), dim3(1024), 0, stream, a);
+    if (!ok()) return st;
+    hipLaunchKernelGGL(moe_route_kernel, dim3(e), dim3(512), 0, stream, a);
+    if (!ok()) return st;
+    hipLaunchKernelGGL((moe_expert_kernel<false>), dim3(inter / 64, units), dim3(512), 0, stream, a);
+    if (!ok()) return st;
+    hipLaunchKernelGGL((moe_expert_kernel<true>), dim3(h / 128, units), dim3(512), 0, stream, a);
   }
-  if ((st = hipGetLastError()) != hipSuccess) return st;
-  hipLaunchKernelGGL(moe_combine_kernel, dim3((h + 1023) / 1024, t), dim3(256), 0, stream, a);
+  if (!ok()) return st;
+  hipLaunchKernelGGL(moe_combine_kernel, combine, dim3(256), 0, stream, a);
   return hipGetLastError();
 }
 
