@@ -11,22 +11,21 @@
 //
 // Launches, with no atomics between workgroups (bit-identical repeats):
 //   router      logits in fp32
-//   route       above 4 tokens: the tokens of every expert
-//   gate and up the two products of 32 or 64 hidden columns of one expert, and
+//   route       above one token: the tokens of every expert
+//   gate and up the two products of a few hidden columns of one expert, and
 //               silu(g) u of its tokens
-//   down        above 1 token: fp32 results per (token, pick); for 1 token
-//               the weighted sum over its picks as well
-//   combine     above 1 token: the weighted sum, in order of rank
+//   down        one token: the weighted sum over its picks; above: fp32 results
+//               per (token, pick)
+//   combine     above one token: the weighted sum, in order of rank
 // The rank of expert e for a token is the number of experts before it, so "which
 // tokens picked e" takes one ballot per 64 experts and token, and a token's pick
-// number is that rank.  Up to 4 tokens each workgroup of the gate and up launch
-// ranks the logits itself (a few KB; 1 us less than another launch) and leaves
-// what it found to the down launch.  Its units are the picks: where an earlier
-// token picked the same expert a unit leaves at once, and the earlier one
-// takes all their tokens, so an expert is read once.
+// number is that rank.  For one token each workgroup of the gate and up launch
+// ranks the logits itself (a few KB), which is a launch less; with more, or with
+// more tokens, that work costs more than the launch (4 tokens, 6 of 160 experts of
+// 768 x 2048: 46 us of which half was ranking).
 //
-// Three forms of the product:
-//  * up to 4 tokens of an expert: the 4x4x4 sixteen-block matrix instruction
+// Two forms of the product:
+//  * one to 4 tokens of an expert: the 4x4x4 sixteen-block matrix instruction
 //    with lane = weight row (the mapping of gemv_w4a16_mx4.hip), K split over
 //    waves and summed in LDS;
 //  * more: 16x16x32 with the tokens staged in LDS, one wave per 16 weight rows
@@ -44,9 +43,8 @@ struct MoeArgs {
   int t, h, e, inter, k, renorm;
   float* logits;                      // [t, e]
   float* picked;                      // [t * k] logits in order of rank
-  int32_t* unit;                      // up to 4 tokens: [t * k][8] expert, count, picks
-  int32_t* count;                     // above: [e] tokens of an expert
-  int32_t* list;                      // [e][64] their picks, t k + rank
+  int32_t* count;                     // [e] tokens of an expert
+  int32_t* list;                      // [e][64] their picks, t k + rank; one token: [k] experts
   uint16_t* hidden;                   // [t * k, inter]
   float* part;                        // [t * k, h]
   void* y;
@@ -55,18 +53,17 @@ struct MoeArgs {
 
 // ---- router ---------------------------------------------------------------
 
-// Up to 4 tokens: a wave per expert.
+// Up to 4 tokens: a workgroup per expert, summed over its lanes in a fixed order.
 __global__ __launch_bounds__(256) void moe_router_gemv_kernel(MoeArgs a) {
-  const int lane = threadIdx.x & 63;
-  const int e = blockIdx.x * 4 + wave_id_uniform();
-  if (e >= a.e) return;
+  __shared__ float red[4][4];
+  const int tid = threadIdx.x, lane = tid & 63, wave = wave_id_uniform();
+  const int e = blockIdx.x;
   float acc[4] = {0.0f, 0.0f, 0.0f, 0.0f};
-  for (int c = lane * 8; c < a.h; c += 512) {
+  for (int c = tid * 8; c < a.h; c += 2048) {
     const u32x4_t w = *reinterpret_cast<const u32x4_t*>(a.router + (size_t)e * a.h + c);
 #pragma unroll
     for (int m = 0; m < 4; ++m) {
-      if (m >= a.t) continue;
-      const u32x4_t x = *reinterpret_cast<const u32x4_t*>(a.x + (size_t)m * a.h + c);
+      const u32x4_t x = *reinterpret_cast<const u32x4_t*>(a.x + (size_t)min(m, a.t - 1) * a.h + c);
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
         acc[m] = __builtin_fmaf(__uint_as_float(x[i] << 16), __uint_as_float(w[i] << 16), acc[m]);
@@ -78,8 +75,10 @@ __global__ __launch_bounds__(256) void moe_router_gemv_kernel(MoeArgs a) {
   for (int m = 0; m < 4; ++m) {
 #pragma unroll
     for (int o = 1; o < 64; o *= 2) acc[m] += __shfl_xor(acc[m], o);
-    if (m < a.t && lane == 0) a.logits[(size_t)m * a.e + e] = acc[m];
+    if (lane == 0) red[wave][m] = acc[m];
   }
+  __syncthreads();
+  if (tid < a.t) a.logits[(size_t)tid * a.e + e] = (red[0][tid] + red[1][tid]) + (red[2][tid] + red[3][tid]);
 }
 
 // 16 experts x 16 tokens per workgroup, its 16 waves taking 32 k in turn.
@@ -121,71 +120,38 @@ __device__ __forceinline__ uint32_t order_key(float l) {
   return (u & 0x80000000u) ? ~u : u | 0x80000000u;
 }
 
-// Up to 4 tokens: the expert of a pick and the tokens that picked it.
+// One token: the expert of rank `want`.  Workgroups of 1024 threads.
 struct MoePlan {
-  uint32_t key[4][512];
+  uint32_t key[512];
   int count[512];
-  int rank[4];
   int expert;
 };
 
-// Returns how many tokens the unit has (0: nothing to do), its picks in
-// `slot`, in order.  Workgroups of 1024 threads.
-__device__ int moe_plan(const MoeArgs& a, int unit, MoePlan& p, int (&slot)[4]) {
-  const int tid = threadIdx.x, lane = tid & 63, wave = wave_id_uniform();
-  const int first = unit / a.k, want = unit - first * a.k;
-  for (int c = tid; c < a.t * a.e; c += 1024) {
-    const int t = c / a.e;
-    p.key[t][c - t * a.e] = order_key(a.logits[c]);
-  }
+__device__ int moe_plan(const MoeArgs& a, int want, MoePlan& p) {
+  const int tid = threadIdx.x;
+  if (tid < a.e) p.key[tid] = order_key(a.logits[tid]);
   if (tid < 512) p.count[tid] = 0;
   __syncthreads();
-  // expert with rank `want` of token `first`: 1024 / width lanes per expert
-  int width = 64;
+  int width = 64;                    // lanes for the experts, 1024 / width parts of the comparison
   while (width < a.e) width *= 2;
   const int parts = 1024 / width, e = tid & (width - 1), part = tid / width;
   if (e < a.e) {
-    const uint32_t mine = p.key[first][e];
+    const uint32_t mine = p.key[e];
     int c = 0;
 #pragma unroll 8
     for (int o = a.e * part / parts; o < a.e * (part + 1) / parts; ++o) {
-      const uint32_t u = p.key[first][o];
+      const uint32_t u = p.key[o];
       c += u > mine || (u == mine && o < e);
     }
-    atomicAdd(&p.count[e], c);     // integers in LDS: no order to depend on
+    atomicAdd(&p.count[e], c);       // integers in LDS: no order to depend on
   }
   __syncthreads();
   if (tid < a.e && p.count[tid] == want) p.expert = tid;
   __syncthreads();
-  const int expert = p.expert;
-  if (wave < a.t) {
-    const uint32_t mine = p.key[wave][expert];
-    int c = 0;
-    for (int o = lane; o - lane < a.e; o += 64) {
-      const uint32_t u = o < a.e ? p.key[wave][o] : 0u;
-      c += __popcll(__ballot(o < a.e && (u > mine || (u == mine && o < expert))));
-    }
-    if (lane == 0) p.rank[wave] = c;
-  }
-  __syncthreads();
-  int n = 0, before = 0;
-#pragma unroll
-  for (int t = 0; t < 4; ++t) {
-    if (t < a.t && p.rank[t] < a.k) {
-#pragma unroll
-      for (int u = 0; u < 4; ++u)
-        if (u == n) slot[u] = t * a.k + p.rank[t];
-      ++n;
-      before |= t < first;
-    }
-  }
-#pragma unroll
-  for (int u = 1; u < 4; ++u)
-    if (u >= n) slot[u] = slot[u - 1];
-  return before ? 0 : n;
+  return __builtin_amdgcn_readfirstlane(p.expert);
 }
 
-// Above 4 tokens: a workgroup per expert ranks it for every token.
+// Above one token: a workgroup per expert ranks it for every token.
 __global__ __launch_bounds__(512) void moe_route_kernel(MoeArgs a) {
   __shared__ int rank[64];
   const int tid = threadIdx.x, lane = tid & 63, wave = wave_id_uniform();
@@ -226,7 +192,7 @@ __global__ __launch_bounds__(512) void moe_route_kernel(MoeArgs a) {
   }
 }
 
-// The expert of a unit above 4 tokens: the unit-th that has tokens, or -1.
+// The expert of a unit above one token: the unit-th that has tokens, or -1.
 __device__ __forceinline__ int moe_active(const MoeArgs& a, int unit, int& n) {
   const int lane = threadIdx.x & 63;
   int cnt[8], expert = -1, seen = 0;
@@ -263,15 +229,14 @@ struct MoeHalf {
   const uint8_t* tile;
   int half;
   const uint16_t* x;              // this lane's activation row, its first k
-  float p;                        // weight of the result
 };
 
-// acc[m] += p dequant(W)[row] . x_m over the wave's units u0, u0 + step, ...
-// below `units`, for up to 4 rows of activations; at(u) names unit u.  Lane l
+// acc[m] += dequant(W)[row] . x_m over the wave's units u0, u0 + step, ...
+// below `units`, for M rows of activations (lanes copy 4); at(u) names unit u.  Lane l
 // holds row l & 31 of the half block `hb` and the group pair l >> 5, and copies
 // 8 k of activation row l >> 4.
-template <bool WEIGHTED, class At>
-__device__ __forceinline__ void moe_mx4(float (&acc)[4], int hb, int u0, int units, int step, MoeSlot& slot, At at) {
+template <int M, bool PF, class At>
+__device__ __forceinline__ void moe_mx4(float (&acc)[M], int hb, int u0, int units, int step, MoeSlot& slot, At at) {
   using L = W4Layout<false>;
   const int lane = threadIdx.x & 63, lg = lane >> 5, sm = lane >> 4, sc = lane & 15;
   const int row = 32 * hb + (lane & 31);
@@ -282,13 +247,12 @@ __device__ __forceinline__ void moe_mx4(float (&acc)[4], int hb, int u0, int uni
   asm volatile("" : "+v"(magic_v));
   uint32_t ones_v = 0x3f803f80u;
   asm volatile("" : "+v"(ones_v));
-  auto load = [&](Half32Regs& r, u32x4_t& xv, float& p, int u) {
+  auto load = [&](Half32Regs& r, u32x4_t& xv, int u) {
     const MoeHalf h = at(u);
     L::load(r, h.tile, h.half, lg, row);
     xv = *reinterpret_cast<const u32x4_t*>(h.x + 8 * sc);
-    p = h.p;
   };
-  auto compute = [&](const Half32Regs& r, const u32x4_t& xv, float p) {
+  auto compute = [&](const Half32Regs& r, const u32x4_t& xv) {
     float xp = dot2_bf16(xv.x, ones_v, 0.0f);
     xp = dot2_bf16(xv.y, ones_v, xp);
     xp = dot2_bf16(xv.z, ones_v, xp);
@@ -316,32 +280,40 @@ __device__ __forceinline__ void moe_mx4(float (&acc)[4], int hb, int u0, int uni
         const u32x4_t xq = xa[t >> 1];
         d = mfma_4x4x4((t & 1) ? u32x2_t{xq.z, xq.w} : u32x2_t{xq.x, xq.y}, b, d);
       }
-      const float s = WEIGHTED ? p * L::scale(r.sc, jj, 1.0f) : L::scale(r.sc, jj, 1.0f);
+      const float s = L::scale(r.sc, jj, 1.0f);
       const f32x4_t xg = *reinterpret_cast<const f32x4_t*>(&slot.sum[2 * lg + jj][0]);
       const float zb = (float)(L::zero(r, jj) | 0x80u);
 #pragma unroll
-      for (int m = 0; m < 4; ++m) acc[m] = __builtin_fmaf(s, __builtin_fmaf(-zb, xg[m], d[m]), acc[m]);
+      for (int m = 0; m < M; ++m) acc[m] = __builtin_fmaf(s, __builtin_fmaf(-zb, xg[m], d[m]), acc[m]);
     }
   };
-  // two register sets in turn: the next unit's loads in flight while this
+  if constexpr (!PF) {
+    for (int u = u0; u < units; u += step) {
+      Half32Regs r;
+      u32x4_t xv;
+      load(r, xv, u);
+      compute(r, xv);
+    }
+    return;
+  }
+  // PF: two register sets in turn, the next unit's loads in flight while this
   // one computes
   int u = u0;
   if (u >= units) return;
   Half32Regs ra, rb;
   u32x4_t xa, xb;
-  float pa, pb;
-  load(ra, xa, pa, u);
+  load(ra, xa, u);
   __builtin_amdgcn_sched_barrier(0);
   while (true) {
-    if (u + step >= units) { compute(ra, xa, pa); break; }
-    load(rb, xb, pb, u + step);
+    if (u + step >= units) { compute(ra, xa); break; }
+    load(rb, xb, u + step);
     __builtin_amdgcn_sched_barrier(0);
-    compute(ra, xa, pa);
+    compute(ra, xa);
     u += step;
-    if (u + step >= units) { compute(rb, xb, pb); break; }
-    load(ra, xa, pa, u + step);
+    if (u + step >= units) { compute(rb, xb); break; }
+    load(ra, xa, u + step);
     __builtin_amdgcn_sched_barrier(0);
-    compute(rb, xb, pb);
+    compute(rb, xb);
     u += step;
   }
 }
@@ -351,76 +323,39 @@ __device__ __forceinline__ uint16_t silu_mul(float g, float u) {
   return (uint16_t)f32_to_bf16_rne(g / (1.0f + __builtin_amdgcn_exp2f(-1.44269504088896340736f * g)) * u);
 }
 
-// Up to 4 tokens.  A workgroup of 16 waves owns two blocks of 32 weight rows
-// (gate and up rows of 32 hidden columns; two neighbouring blocks of the down
-// matrix), 8 waves each, K split over them.
-template <bool DOWN>
-__global__ __launch_bounds__(1024) void moe_small_kernel(MoeArgs a) {
+// One token.  A workgroup of 16 waves owns the gate and up rows of 32 hidden
+// columns of one pick, 8 waves each, K split over them.  Two workgroups per CU
+// (64 VGPRs) rather than a second register set.
+__global__ __launch_bounds__(1024) __attribute__((amdgpu_waves_per_eu(8))) void moe_gate_up_one_kernel(MoeArgs a) {
   union Shared {
     MoePlan plan;
     MoeSlot slot[16];
-    float red[16][4][64];
+    float red[16][64];
   };
   __shared__ __attribute__((aligned(16))) Shared sh;
   const int tid = threadIdx.x, lane = tid & 63, wave = wave_id_uniform();
   const int blk = wave >> 3, kw = wave & 7;
-  const int tile = blockIdx.x, unit = blockIdx.y;
-  int n, expert, slot[4];
-  if constexpr (DOWN) {
-    const int32_t* const u = a.unit + unit * 8;
-    expert = u[0];
-    n = u[1];
-#pragma unroll
-    for (int m = 0; m < 4; ++m) slot[m] = u[2 + m];
-  } else {
-    n = moe_plan(a, unit, sh.plan, slot);
-    expert = sh.plan.expert;
-    if (tile == 0 && tid == 0) {
-      int32_t* const u = a.unit + unit * 8;
-      u[0] = expert;
-      u[1] = n;
-#pragma unroll
-      for (int m = 0; m < 4; ++m) {
-        u[2 + m] = slot[m];
-        if (m < n) a.picked[slot[m]] = a.logits[(size_t)(slot[m] / a.k) * a.e + expert];
-      }
-    }
-    __syncthreads();                 // the plan's LDS becomes the waves' slots
+  const int tile = blockIdx.x, pick = blockIdx.y;
+  const int expert = moe_plan(a, pick, sh.plan);
+  if (tile == 0 && tid == 0) {
+    a.list[pick] = expert;
+    a.picked[pick] = a.logits[expert];
   }
-  if (n == 0) return;                // uniform over the workgroup
-  const int kdim = DOWN ? a.inter : a.h;
-  const int rb = DOWN ? tile : (tile >> 1) + blk * (a.inter >> 6);
-  const int hb = DOWN ? blk : tile & 1;
-  const uint8_t* const tiles = (DOWN ? a.down + expert * a.down_bytes : a.gate_up + expert * a.gate_up_bytes) +
-                               (size_t)rb * (kdim >> 8) * kTileBytes;
-  const int sm = lane >> 4;
-  const int mine = sm == 0 ? slot[0] : sm == 1 ? slot[1] : sm == 2 ? slot[2] : slot[3];
-  const uint16_t* const x = DOWN ? a.hidden + (size_t)mine * a.inter : a.x + (size_t)(mine / a.k) * a.h;
-  float acc[4] = {0.0f, 0.0f, 0.0f, 0.0f};
-  moe_mx4<false>(acc, hb, kw, kdim >> 7, 8, sh.slot[wave], [&](int u) {
-    return MoeHalf{tiles + (size_t)(u >> 1) * kTileBytes, u & 1, x + (size_t)u * 128, 1.0f};
+  __syncthreads();                   // the plan's LDS becomes the waves' slots
+  const int rb = (tile >> 1) + blk * (a.inter >> 6);
+  const uint8_t* const tiles = a.gate_up + expert * a.gate_up_bytes + (size_t)rb * (a.h >> 8) * kTileBytes;
+  float acc[1] = {0.0f};
+  moe_mx4<1, false>(acc, tile & 1, kw, a.h >> 7, 8, sh.slot[wave], [&](int u) {
+    return MoeHalf{tiles + (size_t)(u >> 1) * kTileBytes, u & 1, a.x + (size_t)u * 128};
   });
   __syncthreads();
-#pragma unroll
-  for (int m = 0; m < 4; ++m) sh.red[wave][m][lane] = acc[m];
+  sh.red[wave][lane] = acc[0];
   __syncthreads();
-  if (tid < 32 * n) {
-    const int m = tid >> 5, r = tid & 31;
-    const size_t s = m == 0 ? slot[0] : m == 1 ? slot[1] : m == 2 ? slot[2] : slot[3];
-    float v[2];
+  if (tid >= 32) return;
+  float v[2] = {0.0f, 0.0f};
 #pragma unroll
-    for (int b = 0; b < 2; ++b) {
-      v[b] = 0.0f;
-#pragma unroll
-      for (int w = 0; w < 8; ++w) v[b] += sh.red[8 * b + w][m][r] + sh.red[8 * b + w][m][r + 32];
-    }
-    if constexpr (DOWN) {
-      a.part[s * a.h + 64 * tile + r] = v[0];
-      a.part[s * a.h + 64 * tile + 32 + r] = v[1];
-    } else {
-      a.hidden[s * a.inter + 32 * tile + r] = silu_mul(v[0], v[1]);
-    }
-  }
+  for (int w = 0; w < 16; ++w) v[w >> 3] += sh.red[w][tid] + sh.red[w][tid + 32];
+  a.hidden[(size_t)pick * a.inter + 32 * tile + tid] = silu_mul(v[0], v[1]);
 }
 
 // The softmax denominator of a token's picks, relative to its first logit.
@@ -436,43 +371,91 @@ __device__ __forceinline__ float moe_total(const MoeArgs& a, int t, const float*
   return total;
 }
 
-// One token: 32 rows of the output through all its picks, 16 waves taking half
-// tiles of the picks in turn, the picks' weights applied with the group scales.
-__global__ __launch_bounds__(1024) void moe_down_one_kernel(MoeArgs a) {
-  union Shared {
-    MoeSlot slot[16];
-    float red[16][64];
+// One token: 16 rows of the output through all its picks, 16 waves taking 256-k
+// tiles of the picks in turn, the picks' weights applied with the group
+// scales.  Lane (i, a) holds row i of the 16 and groups a and 4 + a of the tile:
+// half the rows of the mapping above and twice the workgroups (2 picks of 14336 x
+// 4096, down: 21 us with 32 rows and 128 workgroups).
+__global__ __launch_bounds__(1024) __attribute__((amdgpu_waves_per_eu(8))) void moe_down_one_kernel(MoeArgs a) {
+  struct Slot {
+    uint8_t x[512];
+    float sum[8];
   };
-  __shared__ __attribute__((aligned(16))) Shared sh;
+  __shared__ __attribute__((aligned(16))) Slot slots[16];
+  __shared__ float red[16][64];
   __shared__ float p[32];
   __shared__ int expert[32];
   const int tid = threadIdx.x, lane = tid & 63, wave = wave_id_uniform();
-  const int tile = blockIdx.x;
+  const int i = lane & 15, q = lane >> 4, c = lane & 31;
+  const int row = 16 * (blockIdx.x & 3) + i;             // of the 64-row block
   const float total = moe_total(a, 0, a.picked);
   if (tid < a.k) {
     p[tid] = expf(a.picked[tid] - a.picked[0]) / total;
-    expert[tid] = a.unit[tid * 8];
+    expert[tid] = a.list[tid];
   }
   __syncthreads();
-  const int halves = a.inter >> 7;
-  const size_t block = (size_t)(tile >> 1) * (a.inter >> 8) * kTileBytes;
-  float acc[4] = {0.0f, 0.0f, 0.0f, 0.0f};
-  moe_mx4<true>(acc, tile & 1, wave, a.k * halves, 16, sh.slot[wave], [&](int u) {
-    const int j = __builtin_amdgcn_readfirstlane(u / halves), hs = u - j * halves;
-    return MoeHalf{a.down + __builtin_amdgcn_readfirstlane(expert[j]) * a.down_bytes + block + (size_t)(hs >> 1) * kTileBytes,
-                   hs & 1, a.hidden + (size_t)j * a.inter + (size_t)hs * 128, p[j]};
-  });
-  __syncthreads();
-  sh.red[wave][lane] = acc[0];
-  __syncthreads();
-  if (tid >= 32) return;
-  float v = 0.0f;
+  const int kt_count = a.inter >> 8;
+  const size_t block = (size_t)(blockIdx.x >> 2) * kt_count * kTileBytes;
+  const uint32_t mask_s = __builtin_amdgcn_readfirstlane(0x000F000Fu);
+  uint32_t magic_v = 0x43004300u;
+  asm volatile("" : "+v"(magic_v));
+  uint32_t ones_v = 0x3f803f80u;
+  asm volatile("" : "+v"(ones_v));
+  Slot& slot = slots[wave];
+  float acc = 0.0f;
+  for (int u = wave; u < a.k * kt_count; u += 16) {
+    const int j = __builtin_amdgcn_readfirstlane(u / kt_count), kt = u - j * kt_count;
+    const BufView v(a.down + __builtin_amdgcn_readfirstlane(expert[j]) * a.down_bytes + block + (size_t)kt * kTileBytes,
+                    kTileBytes);
+    u32x4_t w[2];
+    uint32_t sc[2];
 #pragma unroll
-  for (int w = 0; w < 16; ++w) v += sh.red[w][tid] + sh.red[w][tid + 32];
+    for (int g = 0; g < 2; ++g) {
+      w[g] = v.b128<true>((uint32_t)((4 * g + q) * kTileRows + row) * 16u);
+      sc[g] = v.b16((uint32_t)(kScaleOff + row * 16 + 8 * g + 2 * q));
+    }
+    const uint32_t zw = v.b32((uint32_t)(kZeroOff + row * 4));
+    const u32x4_t xv = *reinterpret_cast<const u32x4_t*>(a.hidden + (size_t)j * a.inter + (size_t)kt * 256 + 8 * c);
+    float xp = dot2_bf16(xv.x, ones_v, 0.0f);
+    xp = dot2_bf16(xv.y, ones_v, xp);
+    xp = dot2_bf16(xv.z, ones_v, xp);
+    xp = dot2_bf16(xv.w, ones_v, xp);
+    xp += dpp_mov<0xB1>(xp);
+    xp += dpp_mov<0x4E>(xp);
+    // wave-private slot: a wave's LDS operations complete in order
+    __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
+    __builtin_amdgcn_wave_barrier();
+    if (lane < 32) {
+      *reinterpret_cast<u32x4_t*>(slot.x + 16 * c) = xv;
+      if ((c & 3) == 0) slot.sum[c >> 2] = xp;
+    }
+    __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
+    __builtin_amdgcn_wave_barrier();
+    __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
+#pragma unroll
+    for (int g = 0; g < 2; ++g) {
+      f32x4_t d = {0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+      for (int t = 0; t < 8; ++t) {
+        const u32x2_t xa = *reinterpret_cast<const u32x2_t*>(slot.x + 64 * (4 * g + q) + 8 * t);
+        const u32x2_t b = {code_pair(w[g][t >> 1], 2 * (t & 1), mask_s, magic_v),
+                           code_pair(w[g][t >> 1], 2 * (t & 1) + 1, mask_s, magic_v)};
+        d = mfma_4x4x4(xa, b, d);
+      }
+      const float zb = (float)((zw >> (16 * g + 4 * q) & 15u) | 0x80u);
+      acc = __builtin_fmaf(p[j] * fp16_to_f32(sc[g]), __builtin_fmaf(-zb, slot.sum[4 * g + q], d[0]), acc);
+    }
+  }
+  red[wave][lane] = acc;
+  __syncthreads();
+  if (tid >= 16) return;
+  float y = 0.0f;
+#pragma unroll
+  for (int u = 0; u < 16; ++u) y += (red[u][tid] + red[u][tid + 16]) + (red[u][tid + 32] + red[u][tid + 48]);
   if (a.y_f32)
-    static_cast<float*>(a.y)[32 * tile + tid] = v;
+    static_cast<float*>(a.y)[16 * blockIdx.x + tid] = y;
   else
-    static_cast<uint16_t*>(a.y)[32 * tile + tid] = (uint16_t)f32_to_bf16_rne(v);
+    static_cast<uint16_t*>(a.y)[16 * blockIdx.x + tid] = (uint16_t)f32_to_bf16_rne(y);
 }
 
 // A barrier for LDS alone: loads from memory stay in flight across it.
@@ -489,15 +472,17 @@ struct MoeTile {                  // one 256-k tile of a wave's 16 rows: lane (i
 };
 
 // acc[mt][e] += row 16t + i of the block times activation row 16 mt + 4a + e,
-// over all of K.  The workgroup's 512 threads copy the 16 MT activation rows of
-// a 256-k tile into one of two LDS buffers: 16-byte piece c of row r at 32 r +
-// (c ^ (r & 15)), so that the operand reads of 16 lanes, one row each, fall on
-// distinct banks; xr: this thread's rows tid / 32 + 16 j.  Codes go two tiles
-// ahead, activations one (through registers).
-template <int MT>
-__device__ __forceinline__ void moe_mx16(f32x4_t (&acc)[MT], const uint8_t* tiles, int t, int kt_count,
-                                         const uint16_t* const (&xr)[MT], uint8_t* xs) {
-  const int tid = threadIdx.x, lane = tid & 63, i = lane & 15, a = lane >> 4;
+// over the tiles kt0 .. kt0 + count - 1 of K.  TH threads (`tid` among them)
+// copy the 16 MT activation rows of a 256-k tile into one of two LDS buffers at
+// xs: 16-byte piece c of row r at 32 r + (c ^ (r & 15)), so that the operand
+// reads of 16 lanes, one row each, fall on distinct banks; xr: this thread's
+// rows tid / 32 + (TH / 32) j.  Codes go two tiles ahead, activations one (through
+// registers).  The workgroup's waves pass `steps` >= count barriers together.
+template <int MT, int TH>
+__device__ __forceinline__ void moe_mx16(f32x4_t (&acc)[MT], const uint8_t* tiles, int t, int kt0, int count, int steps,
+                                         const uint16_t* (&xr)[MT * 512 / TH], int tid, uint8_t* xs) {
+  constexpr int NP = MT * 512 / TH;
+  const int lane = tid & 63, i = lane & 15, a = lane >> 4;
   const uint32_t mask_s = __builtin_amdgcn_readfirstlane(0x000F000Fu);
   uint32_t magic_v = 0x43004300u;
   asm volatile("" : "+v"(magic_v));
@@ -511,14 +496,16 @@ __device__ __forceinline__ void moe_mx16(f32x4_t (&acc)[MT], const uint8_t* tile
     w.sc = v.b128<false>(kScaleOff + row * 16u);
     w.zw = v.b32(kZeroOff + row * 4u);
   };
-  auto load_x = [&](u32x4_t (&x)[MT], int kt) {
+  auto load_x = [&](u32x4_t (&x)[NP], int kt) {
 #pragma unroll
-    for (int j = 0; j < MT; ++j) x[j] = *reinterpret_cast<const u32x4_t*>(xr[j] + (size_t)kt * 256 + 8 * pc);
+    for (int j = 0; j < NP; ++j) x[j] = *reinterpret_cast<const u32x4_t*>(xr[j] + (size_t)kt * 256 + 8 * pc);
   };
-  auto store_x = [&](const u32x4_t (&x)[MT], int buf) {
+  auto store_x = [&](const u32x4_t (&x)[NP], int buf) {
 #pragma unroll
-    for (int j = 0; j < MT; ++j)
-      *reinterpret_cast<u32x4_t*>(xs + buf * (MT * 8192) + 16 * (32 * (pr + 16 * j) + (pc ^ pr))) = x[j];
+    for (int j = 0; j < NP; ++j) {
+      const int r = pr + TH / 32 * j;
+      *reinterpret_cast<u32x4_t*>(xs + buf * (MT * 8192) + 16 * (32 * r + (pc ^ (r & 15)))) = x[j];
+    }
   };
   auto compute = [&](MoeTile& w, int buf) {
     transpose_rows4(w.c0);
@@ -549,131 +536,151 @@ __device__ __forceinline__ void moe_mx16(f32x4_t (&acc)[MT], const uint8_t* tile
       for (int mt = 0; mt < MT; ++mt)
 #pragma unroll
         for (int e = 0; e < 4; ++e) acc[mt][e] = __builtin_fmaf(s, d[mt][e], acc[mt][e]);
+      __builtin_amdgcn_sched_barrier(0);
     }
   };
-  MoeTile w0, w1;
-  u32x4_t x[MT];
-  load_x(x, 0);
-  load_w(w0, 0);
+  MoeTile w0, w1, w2;
+  u32x4_t x[NP];
+  const int last = kt0 + max(count, 1) - 1;    // (no tile: the first one is read and not used)
+  load_x(x, kt0);
+  load_w(w0, kt0);
   store_x(x, 0);
-  const int last = kt_count - 1;
-  load_x(x, min(1, last));
-  load_w(w1, min(1, last));
+  load_w(w1, min(kt0 + 1, last));
+  load_x(x, min(kt0 + 1, last));
   lds_barrier();
-  // tile kt in LDS buffer kt & 1 and set 0 (even) or 1 (odd); the loads past the
-  // end read the last tile again and are not used
-  for (int kt = 0;;) {
-    store_x(x, (kt + 1) & 1);
-    load_x(x, min(kt + 2, last));
-    compute(w0, kt & 1);
-    load_w(w0, min(kt + 2, last));
+  // Tile kt0 + k in LDS buffer k & 1 and set k % 3; the loads past the end
+  // read the last tile again and are not used.
+  auto step = [&](int k, MoeTile& now, MoeTile& later) {
+    load_w(later, min(kt0 + k + 2, last));
+    __builtin_amdgcn_sched_barrier(0);
+    store_x(x, (k + 1) & 1);
+    load_x(x, min(kt0 + k + 2, last));
+    __builtin_amdgcn_sched_barrier(0);
+    if (k < count) compute(now, k & 1);        // uniform
     lds_barrier();
-    if (++kt > last) break;
-    store_x(x, (kt + 1) & 1);
-    load_x(x, min(kt + 2, last));
-    compute(w1, kt & 1);
-    load_w(w1, min(kt + 2, last));
-    lds_barrier();
-    if (++kt > last) break;
+  };
+  for (int k = 0;;) {
+    step(k, w0, w2);
+    if (++k >= steps) break;
+    step(k, w1, w0);
+    if (++k >= steps) break;
+    step(k, w2, w1);
+    if (++k >= steps) break;
   }
 }
 
-// Above 4 tokens.  A workgroup of 8 waves owns two 64-row blocks (gate and up
-// rows of 64 hidden columns; two neighbouring blocks of the down matrix).
-template <bool DOWN>
-__global__ __launch_bounds__(512) void moe_expert_kernel(MoeArgs a) {
+// Above one token, 8 waves.  kGateUp: a workgroup owns the gate and up rows of
+// 64 hidden columns, four waves each.  kDownWide: two neighbouring 64-row blocks
+// of the down matrix, four waves each.  kDownDeep: one block, four waves on each
+// half of K: twice the workgroups with half the work each, for grids that
+// would leave CUs idle otherwise.
+enum MoeForm { kGateUp, kDownWide, kDownDeep };
+
+template <MoeForm F>
+__global__ __launch_bounds__(512) __attribute__((amdgpu_waves_per_eu(4))) void moe_expert_kernel(MoeArgs a) {
+  constexpr bool DOWN = F != kGateUp, DEEP = F == kDownDeep;
   union Shared {
     MoeSlot slot[8];
     float red[8][4][64];
-    uint8_t x[2 * 2 * 8192];
-    f32x4_t up[4][2][64];
+    uint8_t x[DEEP ? 2 : 1][2 * 2 * 8192];
+    f32x4_t other[4][2][64];                 // results of the waves 4 .. 7
   };
   __shared__ __attribute__((aligned(16))) Shared sh;
-  __shared__ int slots[64];
   const int tid = threadIdx.x, lane = tid & 63, wave = wave_id_uniform();
   int n;
   const int expert = moe_active(a, blockIdx.y, n);
   if (expert < 0) return;                    // uniform over the workgroup
-  if (tid < n) slots[tid] = a.list[expert * 64 + tid];
-  __syncthreads();
+  const int pick = a.list[expert * 64 + min(lane, n - 1)];   // lane m: the expert's m-th pick
   const int blk = wave >> 2, tile = blockIdx.x;
-  const int kdim = DOWN ? a.inter : a.h;
-  const int rb = DOWN ? 2 * tile + blk : tile + blk * (a.inter >> 6);
+  const int kdim = DOWN ? a.inter : a.h, kt_count = kdim >> 8;
+  const int rb = F == kGateUp ? tile + blk * (a.inter >> 6) : DEEP ? tile : 2 * tile + blk;
   const uint8_t* const tiles = (DOWN ? a.down + expert * a.down_bytes : a.gate_up + expert * a.gate_up_bytes) +
-                               (size_t)rb * (kdim >> 8) * kTileBytes;
-  auto source = [&](int m) {                 // activation row of the expert's m-th token
-    const int s = slots[m < n ? m : n - 1];
+                               (size_t)rb * kt_count * kTileBytes;
+  auto source = [&](int m) {                 // activation row of the m-th pick (the last one past it)
+    const int s = __shfl(pick, m < n ? m : n - 1);
     return DOWN ? a.hidden + (size_t)s * a.inter : a.x + (size_t)(s / a.k) * a.h;
   };
 
   if (n <= 4) {
-    const int hb = (wave >> 1) & 1, kw = wave & 1;
+    // (block, 32-row half, one of 2 parts of K), or (half, one of 4) in the deep form
+    constexpr int KP = DEEP ? 4 : 2;
+    const int hb = DEEP ? wave >> 2 : (wave >> 1) & 1, kw = wave & (KP - 1);
     const uint16_t* const x = source(lane >> 4);
     float acc[4] = {0.0f, 0.0f, 0.0f, 0.0f};
-    moe_mx4<false>(acc, hb, kw, kdim >> 7, 2, sh.slot[wave], [&](int u) {
-      return MoeHalf{tiles + (size_t)(u >> 1) * kTileBytes, u & 1, x + (size_t)u * 128, 1.0f};
+    moe_mx4<4, true>(acc, hb, kw, kdim >> 7, KP, sh.slot[wave], [&](int u) {
+      return MoeHalf{tiles + (size_t)(u >> 1) * kTileBytes, u & 1, x + (size_t)u * 128};
     });
     __syncthreads();
 #pragma unroll
     for (int m = 0; m < 4; ++m) sh.red[wave][m][lane] = acc[m];
     __syncthreads();
-    if (tid < 64 * n) {
-      const int m = tid >> 6, r = tid & 63, w = 2 * (r >> 5), l = r & 31;
-      const size_t s = slots[m];
-      float v[2];
+    if (wave < n) {                          // wave m: the m-th pick, lane = row of the block
+      const size_t s = __builtin_amdgcn_readlane(pick, wave);
+      const int l = lane & 31, w = KP * (lane >> 5);
+      float v[2] = {0.0f, 0.0f};
 #pragma unroll
-      for (int b = 0; b < 2; ++b)
-        v[b] = (sh.red[4 * b + w][m][l] + sh.red[4 * b + w][m][l + 32]) +
-               (sh.red[4 * b + w + 1][m][l] + sh.red[4 * b + w + 1][m][l + 32]);
-      if constexpr (DOWN) {
-        a.part[s * a.h + 128 * tile + r] = v[0];
-        a.part[s * a.h + 128 * tile + 64 + r] = v[1];
+      for (int b = 0; b < (DEEP ? 1 : 2); ++b)
+#pragma unroll
+        for (int u = 0; u < KP; ++u) v[b] += sh.red[4 * b + w + u][wave][l] + sh.red[4 * b + w + u][wave][l + 32];
+      if constexpr (F == kGateUp) {
+        a.hidden[s * a.inter + 64 * tile + lane] = silu_mul(v[0], v[1]);
       } else {
-        a.hidden[s * a.inter + 64 * tile + r] = silu_mul(v[0], v[1]);
+        float* const o = a.part + s * a.h + (DEEP ? 64 : 128) * tile + lane;
+        o[0] = v[0];
+        if constexpr (!DEEP) o[64] = v[1];
       }
     }
     return;
   }
 
   const int t = wave & 3, i = lane & 15;
-  // acc0: 16 tokens m0 .. of this wave's 16 rows
-  auto finish = [&](const f32x4_t (&acc0)[2], int tiles_of_16, int m0) {
-    if constexpr (!DOWN) {
+  auto finish = [&](const f32x4_t (&acc)[2], int count, int m0) {
+    if constexpr (F != kDownWide) {          // the second four waves hand their sums over: up, or half of K
       __syncthreads();
       if (blk == 1)
-        for (int mt = 0; mt < tiles_of_16; ++mt) sh.up[t][mt][lane] = acc0[mt];
+        for (int mt = 0; mt < count; ++mt) sh.other[t][mt][lane] = acc[mt];
       __syncthreads();
       if (blk == 1) return;
     }
 #pragma unroll
     for (int mt = 0; mt < 2; ++mt) {
-      if (mt >= tiles_of_16) continue;
+      if (mt >= count) continue;
 #pragma unroll
       for (int e = 0; e < 4; ++e) {
         const int m = m0 + 16 * mt + 4 * (lane >> 4) + e;
-        if (m < n) {
-          const size_t s = slots[m];
-          if constexpr (DOWN)
-            a.part[s * a.h + 128 * tile + 64 * blk + 16 * t + i] = acc0[mt][e];
-          else
-            a.hidden[s * a.inter + 64 * tile + 16 * t + i] = silu_mul(acc0[mt][e], sh.up[t][mt][lane][e]);
-        }
+        const size_t s = __shfl(pick, m < n ? m : n - 1);
+        if (m >= n) continue;
+        if constexpr (F == kGateUp)
+          a.hidden[s * a.inter + 64 * tile + 16 * t + i] = silu_mul(acc[mt][e], sh.other[t][mt][lane][e]);
+        else if constexpr (DEEP)
+          a.part[s * a.h + 64 * tile + 16 * t + i] = acc[mt][e] + sh.other[t][mt][lane][e];
+        else
+          a.part[s * a.h + 128 * tile + 64 * blk + 16 * t + i] = acc[mt][e];
       }
     }
   };
-  const int row = tid >> 5;
+  constexpr int TH = DEEP ? 256 : 512;
+  const int th = DEEP ? tid & 255 : tid, row = th >> 5;
+  const int steps = DEEP ? (kt_count + 1) >> 1 : kt_count;
+  const int count = DEEP && blk == 1 ? kt_count - steps : steps;
+  const int kt0 = DEEP && blk == 1 ? min(steps, kt_count - 1) : 0;
+  uint8_t* const xs = sh.x[DEEP ? blk : 0];
   if (n <= 16) {
     f32x4_t acc[1] = {};
-    const uint16_t* const xr[1] = {source(row)};
-    moe_mx16<1>(acc, tiles, t, kdim >> 8, xr, sh.x);
+    const uint16_t* xr[512 / TH];
+#pragma unroll
+    for (int j = 0; j < 512 / TH; ++j) xr[j] = source(row + TH / 32 * j);
+    moe_mx16<1, TH>(acc, tiles, t, kt0, count, steps, xr, th, xs);
     const f32x4_t both[2] = {acc[0], acc[0]};
     finish(both, 1, 0);
   } else {
     for (int m0 = 0; m0 < n; m0 += 32) {
       f32x4_t acc[2] = {};
-      const uint16_t* const xr[2] = {source(m0 + row), source(m0 + 16 + row)};
+      const uint16_t* xr[1024 / TH];
+#pragma unroll
+      for (int j = 0; j < 1024 / TH; ++j) xr[j] = source(m0 + row + TH / 32 * j);
       if (m0 > 0) __syncthreads();             // the LDS of the tokens before is done with
-      moe_mx16<2>(acc, tiles, t, kdim >> 8, xr, sh.x);
+      moe_mx16<2, TH>(acc, tiles, t, kt0, count, steps, xr, th, xs);
       finish(acc, 2, m0);
     }
   }
@@ -705,7 +712,7 @@ static int64_t up256(int64_t n) { return (n + 255) & ~(int64_t)255; }
 
 int64_t moe_ws_bytes(int64_t t, int64_t h, int64_t e, int64_t inter, int64_t k) {
   return up256(t * e * 4) + up256(t * k * 4) + up256(t * k * inter * 2) + up256(t * k * h * 4) +
-         (t <= 4 ? up256(t * k * 32) : up256(e * 4) + up256(e * 256));
+         up256(e * 4) + up256(e * 256);
 }
 
 hipError_t launch_moe_w4a16(const void* x, int t, int h, const void* router, int e, const void* gate_up,
@@ -728,39 +735,38 @@ hipError_t launch_moe_w4a16(const void* x, int t, int h, const void* router, int
   a.picked = reinterpret_cast<float*>(take((int64_t)t * k * 4));
   a.hidden = reinterpret_cast<uint16_t*>(take((int64_t)t * k * inter * 2));
   a.part = reinterpret_cast<float*>(take((int64_t)t * k * h * 4));
-  if (t <= 4) {
-    a.unit = reinterpret_cast<int32_t*>(take((int64_t)t * k * 32));
-  } else {
-    a.count = reinterpret_cast<int32_t*>(take((int64_t)e * 4));
-    a.list = reinterpret_cast<int32_t*>(take((int64_t)e * 256));
-  }
+  a.count = reinterpret_cast<int32_t*>(take((int64_t)e * 4));
+  a.list = reinterpret_cast<int32_t*>(take((int64_t)e * 256));
   a.y = y, a.y_f32 = y_f32;
 
   hipError_t st = hipSuccess;
   auto ok = [&] { return (st = hipGetLastError()) == hipSuccess; };
-  const dim3 combine((h + 1023) / 1024, t);
-  if (t <= 4) {
-    hipLaunchKernelGGL(moe_router_gemv_kernel, dim3((e + 3) / 4), dim3(256), 0, stream, a);
-    if (!ok()) return st;
-    hipLaunchKernelGGL((moe_small_kernel<false>), dim3(inter / 32, t * k), dim3(1024), 0, stream, a);
-    if (!ok()) return st;
-    if (t == 1) {
-      hipLaunchKernelGGL(moe_down_one_kernel, dim3(h / 32), dim3(1024), 0, stream, a);
-      return hipGetLastError();
-    }
-    hipLaunchKernelGGL((moe_small_kernel<true>), dim3(h / 64, t * k), dim3(1024), 0, stream, a);
-  } else {
-    const int units = t * k < e ? t * k : e;
+  if (t <= 4)
+    hipLaunchKernelGGL(moe_router_gemv_kernel, dim3(e), dim3(256), 0, stream, a);
+  else
     hipLaunchKernelGGL(moe_router_mfma_kernel, dim3((e + 15) / 16, (t + 15) / 16), dim3(1024), 0, stream, a);
-    if (!ok()) return st;
-    hipLaunchKernelGGL(moe_route_kernel, dim3(e), dim3(512), 0, stream, a);
-    if (!ok()) return st;
-    hipLaunchKernelGGL((moe_expert_kernel<false>), dim3(inter / 64, units), dim3(512), 0, stream, a);
-    if (!ok()) return st;
-    hipLaunchKernelGGL((moe_expert_kernel<true>), dim3(h / 128, units), dim3(512), 0, stream, a);
-  }
   if (!ok()) return st;
-  hipLaunchKernelGGL(moe_combine_kernel, combine, dim3(256), 0, stream, a);
+  if (t == 1) {
+    hipLaunchKernelGGL(moe_gate_up_one_kernel, dim3(inter / 32, k), dim3(1024), 0, stream, a);
+    if (!ok()) return st;
+    hipLaunchKernelGGL(moe_down_one_kernel, dim3(h / 16), dim3(1024), 0, stream, a);
+    return hipGetLastError();
+  }
+  const int units = t * k < e ? t * k : e;
+  hipLaunchKernelGGL(moe_route_kernel, dim3(e), dim3(512), 0, stream, a);
+  if (!ok()) return st;
+  hipLaunchKernelGGL((moe_expert_kernel<kGateUp>), dim3(inter / 64, units), dim3(512), 0, stream, a);
+  if (!ok()) return st;
+  // Down in the deep form up to a workgroup per CU (8 of 8 experts of 14336 x 4096
+  // hit by 8 tokens, 256 workgroups: 150 us against 170 wide; 16 of 5888 x 1024,
+  // 128: 47 against 56); above it the wide form copies each activation row for
+  // twice the weight rows (128 experts of 768 x 2048: 64 us against 71 deep).
+  if (h / 128 * units <= kCUs)
+    hipLaunchKernelGGL((moe_expert_kernel<kDownDeep>), dim3(h / 64, units), dim3(512), 0, stream, a);
+  else
+    hipLaunchKernelGGL((moe_expert_kernel<kDownWide>), dim3(h / 128, units), dim3(512), 0, stream, a);
+  if (!ok()) return st;
+  hipLaunchKernelGGL(moe_combine_kernel, dim3((h + 1023) / 1024, t), dim3(256), 0, stream, a);
   return hipGetLastError();
 }
 
