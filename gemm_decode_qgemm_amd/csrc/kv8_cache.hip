@@ -20,6 +20,8 @@
 // written gathers those dwords in LDS and stores 16 bytes per lane (a
 // channel's 64 bytes are one run); a page with fewer written blocks (a decode
 // step) stores the dwords where they are.
+#include <type_traits>
+
 #include "layer_common.h"
 
 namespace qg {
@@ -31,28 +33,43 @@ struct AppendArgs {
   uint32_t* status;
 };
 
-__device__ __forceinline__ float absmax8(const u32x4_t& v, float m) {
+typedef uint16_t u16x2_t __attribute__((ext_vector_type(2)));
+
+// The larger of `m` and the magnitudes in 8 bf16 values, as bf16 patterns in both
+// halves: without the sign they order as whole numbers, infinities and NaN last.
+__device__ __forceinline__ uint32_t absmax8(const u32x4_t& v, uint32_t m) {
+  u16x2_t t = __builtin_bit_cast(u16x2_t, m);
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
-    m = fmaxf(m, fabsf(__uint_as_float(v[i] << 16)));
-    m = fmaxf(m, fabsf(__uint_as_float(v[i] & 0xffff0000u)));
+    const uint32_t w = v[i] & 0x7fff7fffu;
+    t = __builtin_elementwise_max(t, __builtin_bit_cast(u16x2_t, w));
   }
-  return m;
+  return __builtin_bit_cast(uint32_t, t);
 }
 
-// Whether any of the 8 bf16 values is an infinity or a NaN.
-__device__ __forceinline__ bool nonfinite8(const u32x4_t& v) {
-  bool bad = false;
+// Codes of four values, packed.  The quotient x / s, correctly rounded, as
+// q1 = x y, q = q1 + (x - q1 s) y with y the correctly rounded 1 / s (Markstein's
+// step: exact residual by fma); adding 1.5 2^23 rounds it to a whole number, half
+// to even, whose low byte is the code.  |x / s| stays below 127.5 since s >= a / 127
+// to within 2^-23.  Five instructions a code against about fifteen with the
+// divide; scales outside 2^-100 .. 2^100, where a step could leave the normal
+// numbers, and NaN (code 0) take that.
+template <bool FAST>
+__device__ __forceinline__ uint32_t codes4(float x0, float x1, float x2, float x3, float s, float y) {
+  const float x[4] = {x0, x1, x2, x3};
+  uint32_t b[4];
 #pragma unroll
-  for (int i = 0; i < 4; ++i)
-    bad |= (v[i] & 0x7f80u) == 0x7f80u || (v[i] & 0x7f800000u) == 0x7f800000u;
-  return bad;
-}
-
-__device__ __forceinline__ uint32_t code_of(float x, float s) {
-  float q = s > 0.0f ? rintf(x / s) : 0.0f;   // s = 0 or NaN: code 0
-  q = fminf(fmaxf(q, -127.0f), 127.0f);
-  return (uint32_t)(int)q & 0xffu;
+  for (int i = 0; i < 4; ++i) {
+    if constexpr (FAST) {
+      const float q1 = x[i] * y;
+      b[i] = __float_as_uint(__builtin_fmaf(__builtin_fmaf(-q1, s, x[i]), y, q1) + 12582912.0f);
+    } else {
+      const float q = s > 0.0f ? rintf(x[i] / s) : 0.0f;
+      b[i] = (uint32_t)(int)fminf(fmaxf(q, -127.0f), 127.0f);
+    }
+  }
+  return __builtin_amdgcn_perm(__builtin_amdgcn_perm(b[3], b[2], 0x0c0c0400u),
+                               __builtin_amdgcn_perm(b[1], b[0], 0x0c0c0400u), 0x05040100u);
 }
 
 __device__ __forceinline__ uint32_t rescale4(uint32_t w, float f) {
@@ -62,17 +79,18 @@ __device__ __forceinline__ uint32_t rescale4(uint32_t w, float f) {
   return o;
 }
 
-// The block's new scale from its lanes' maxima; NaN once anything that is not
-// finite has joined it.  `f` is what the held codes are multiplied by.
-__device__ __forceinline__ float grow(float mx, bool bad, float held, float& f) {
+// The block's new scale from its lanes' maxima (absmax8), the same for the whole
+// wave; NaN once anything that is not finite has joined it.  `f` is what the held
+// codes are multiplied by.
+__device__ __forceinline__ float grow(uint32_t mx, float held, float& f) {
+  mx = max(mx & 0xffffu, mx >> 16);
 #pragma unroll
-  for (int o = 1; o < 64; o *= 2) mx = fmaxf(mx, __shfl_xor(mx, o));
-  const float s = fmaxf(held, mx * (1.0f / 127.0f));
-  if (__ballot(bad) != 0 || held != held) {
-    f = 1.0f;
-    return __uint_as_float(0x7fc00000u);
-  }
-  f = s > held ? held / s : 1.0f;
+  for (int o = 1; o < 64; o *= 2) mx = max(mx, (uint32_t)__shfl_xor((int)mx, o));
+  mx = __builtin_amdgcn_readfirstlane(mx);
+  f = 1.0f;
+  if (mx >= 0x7f80u || held != held) return __uint_as_float(0x7fc00000u);
+  const float s = fmaxf(held, bf16_to_f32(mx) * (1.0f / 127.0f));
+  if (s > held) f = held / s;
   return s;
 }
 
@@ -81,7 +99,10 @@ __global__ __launch_bounds__(256) void kv8_append_kernel(AppendArgs a) {
   constexpr int NK = D / 32;            // 16-byte chunks of keys per lane
   constexpr int CH = D / 8;             // chunks per token
   constexpr int NV = (CH * 4 + 63) / 64;
-  __shared__ uint32_t vt[D * 16];       // [channel][quad][block]
+  // [channel][quad][block], 16 dwords more per 8 channels: the lanes of a store
+  // are 8 channels apart, 128 dwords without that
+  __shared__ __attribute__((aligned(16))) uint32_t vt[D * 18];
+  auto at_vt = [](int d) { return d * 16 + (d >> 3) * 16; };
   const int lane = threadIdx.x & 63;
   const int w = wave_id_uniform();      // block of the page
   const int b = blockIdx.x / a.c.hkv, h = blockIdx.x % a.c.hkv;
@@ -110,10 +131,9 @@ __global__ __launch_bounds__(256) void kv8_append_kernel(AppendArgs a) {
   const int hi = len - t0 < kBlock ? (int)(len - t0) : kBlock;
 
   if (touched) {
-    // all loads first: new keys, new values, held codes
+    const float held_k = lo > 0 ? sc[0] : 0.0f, held_v = lo > 0 ? sc[4] : 0.0f;
     u32x4_t kx[NK], vx[NV][4];
-    bool bad_k = false, bad_v = false;
-    float mk = 0.0f, mv = 0.0f;
+    uint32_t mk = 0, mv = 0;
 #pragma unroll
     for (int i = 0; i < NK; ++i) {
       const int c = lane + 64 * i, tok = c / CH;
@@ -133,71 +153,75 @@ __global__ __launch_bounds__(256) void kv8_append_kernel(AppendArgs a) {
       }
     }
 #pragma unroll
-    for (int i = 0; i < NK; ++i) {
-      mk = absmax8(kx[i], mk);
-      bad_k |= nonfinite8(kx[i]);
-    }
+    for (int i = 0; i < NK; ++i) mk = absmax8(kx[i], mk);
 #pragma unroll
     for (int i = 0; i < NV; ++i)
 #pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        mv = absmax8(vx[i][e], mv);
-        bad_v |= nonfinite8(vx[i][e]);
-      }
+      for (int e = 0; e < 4; ++e) mv = absmax8(vx[i][e], mv);
     float fk, fv;
-    const float sk = grow(mk, bad_k, lo > 0 ? sc[0] : 0.0f, fk);
-    const float sv = grow(mv, bad_v, lo > 0 ? sc[4] : 0.0f, fv);
-    if (lane == 0) {
-      if (a.status && (sk != sk || sv != sv)) atomicOr(a.status, QG_FLAG_NONFINITE);
-    }
+    const float sk = grow(mk, held_k, fk), sv = grow(mv, held_v, fv);
+    if (a.status && lane == 0 && (sk != sk || sv != sv)) atomicOr(a.status, QG_FLAG_NONFINITE);
+
     // Keys: held tokens are rewritten only where the scale grew; the rest of
     // a block that held nothing becomes zero.
+    auto keys = [&](auto fast) {
+      const float y = 1.0f / sk;
 #pragma unroll
-    for (int i = 0; i < NK; ++i) {
-      const int c = lane + 64 * i, tok = c / CH;
-      u32x2_t* p = reinterpret_cast<u32x2_t*>(kc + (w * kBlock + tok) * D + c % CH * 8);
-      if (tok < lo) {
-        if (fk != 1.0f) {
+      for (int i = 0; i < NK; ++i) {
+        const int c = lane + 64 * i, tok = c / CH;
+        auto four = [&](uint32_t a, uint32_t b) {
+          return codes4<decltype(fast)::value>(__uint_as_float(a << 16), __uint_as_float(a & 0xffff0000u),
+                                               __uint_as_float(b << 16), __uint_as_float(b & 0xffff0000u), sk, y);
+        };
+        u32x2_t* p = reinterpret_cast<u32x2_t*>(kc + (w * kBlock + tok) * D + c % CH * 8);
+        if (tok >= lo && (tok < hi || lo == 0)) *p = u32x2_t{four(kx[i].x, kx[i].y), four(kx[i].z, kx[i].w)};
+      }
+    };
+    if (sk >= 0x1p-100f && sk <= 0x1p100f) keys(std::true_type{});
+    else keys(std::false_type{});
+    if (fk != 1.0f) {
+#pragma unroll
+      for (int i = 0; i < NK; ++i) {
+        const int c = lane + 64 * i, tok = c / CH;
+        u32x2_t* p = reinterpret_cast<u32x2_t*>(kc + (w * kBlock + tok) * D + c % CH * 8);
+        if (tok < lo) {
           const u32x2_t old = *p;
           *p = u32x2_t{rescale4(old.x, fk), rescale4(old.y, fk)};
         }
-      } else if (tok < hi || lo == 0) {
-        u32x2_t o{0u, 0u};
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          const uint32_t two = code_of(__uint_as_float(kx[i][e] << 16), sk) |
-                               code_of(__uint_as_float(kx[i][e] & 0xffff0000u), sk) << 8;
-          o[e >> 1] |= two << (16 * (e & 1));
-        }
-        *p = o;
       }
     }
     // Values: dword (channel, quad) = tokens 4 quad .. + 3 of the block.
+    auto values = [&](auto fast) {
+      const float y = 1.0f / sv;
 #pragma unroll
-    for (int i = 0; i < NV; ++i) {
-      const int c = lane + 64 * i, quad = c & 3, ch = c >> 2;
-      if (ch >= CH) continue;
-      // bytes of the dword that are new (or zeroed) / that hold an earlier token
-      const int q0 = 4 * quad;
-      const int keep = lo > q0 ? (lo - q0 < 4 ? lo - q0 : 4) : 0;   // its first `keep` tokens are held
-      const bool fresh = (lo < q0 + 4 && hi > q0) || lo == 0;
-      if (!whole && !fresh && fv == 1.0f) continue;   // nothing of it changes
-      const uint32_t mask = keep == 4 ? 0xffffffffu : (1u << (8 * keep)) - 1u;
+      for (int i = 0; i < NV; ++i) {
+        const int c = lane + 64 * i, quad = c & 3, ch = c >> 2;
+        if (ch >= CH) continue;
+        // its first `keep` tokens are held, the others new (or zeroed)
+        const int q0 = 4 * quad;
+        const int keep = lo > q0 ? (lo - q0 < 4 ? lo - q0 : 4) : 0;
+        const bool fresh = (lo < q0 + 4 && hi > q0) || lo == 0;
+        if (!whole && !fresh && fv == 1.0f) continue;   // nothing of it changes
+        const uint32_t mask = keep == 4 ? 0xffffffffu : (1u << (8 * keep)) - 1u;
 #pragma unroll
-      for (int e = 0; e < 8; ++e) {
-        const int d = 8 * ch + e;
-        uint32_t* p = vc + d * 16 + quad * 4 + w;
-        uint32_t o = 0;
+        for (int e = 0; e < 8; ++e) {
+          const int d = 8 * ch + e;
+          float x[4];
 #pragma unroll
-        for (int u = 0; u < 4; ++u) {
-          const uint32_t x = vx[i][u][e >> 1];
-          o |= code_of(__uint_as_float((e & 1) ? x & 0xffff0000u : x << 16), sv) << (8 * u);
+          for (int u = 0; u < 4; ++u) {
+            const uint32_t two = vx[i][u][e >> 1];
+            x[u] = __uint_as_float((e & 1) ? two & 0xffff0000u : two << 16);
+          }
+          uint32_t* const p = vc + d * 16 + quad * 4 + w;
+          uint32_t o = codes4<decltype(fast)::value>(x[0], x[1], x[2], x[3], sv, y);
+          if (lo > 0 && keep) o = (o & ~mask) | (rescale4(*p, fv) & mask);
+          if (whole) vt[at_vt(d) + quad * 4 + w] = o;
+          else *p = o;
         }
-        if (keep) o = (o & ~mask) | (rescale4(*p, fv) & mask);
-        if (whole) vt[d * 16 + quad * 4 + w] = o;
-        else *p = o;
       }
-    }
+    };
+    if (sv >= 0x1p-100f && sv <= 0x1p100f) values(std::true_type{});
+    else values(std::false_type{});
     if (lane == 0) {
       sc[0] = sk;
       sc[4] = sv;
@@ -206,7 +230,7 @@ __global__ __launch_bounds__(256) void kv8_append_kernel(AppendArgs a) {
   if (!whole) return;                    // uniform over the workgroup
   __syncthreads();
   for (int p = threadIdx.x; p < D * 4; p += 256)
-    reinterpret_cast<u32x4_t*>(vc)[p] = reinterpret_cast<const u32x4_t*>(vt)[p];
+    reinterpret_cast<u32x4_t*>(vc)[p] = *reinterpret_cast<const u32x4_t*>(&vt[at_vt(p >> 2) + (p & 3) * 4]);
 }
 
 struct ReadArgs {
