@@ -100,6 +100,14 @@ def _stream(device: torch.device) -> int:
     return torch.cuda.current_stream(device).cuda_stream
 
 
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+
+
+def _stream_of(index: int) -> int:
+    """The current stream of a device by its index, without a Stream object (2 us less a call)."""
+    return _raw_stream(index) if _raw_stream is not None else torch.cuda.current_stream(index).cuda_stream
+
+
 def _ptr(t: torch.Tensor | None) -> int | None:
     return None if t is None else t.data_ptr()
 
@@ -375,6 +383,13 @@ def qgemm_w4a8_g32_dq(x: torch.Tensor, packed: torch.Tensor, n: int, *, split_k:
 
 
 # ---- operators of a decoder layer around the linears -------------------------
+#
+# A decode step's kernels run a few microseconds, so the wrappers check their
+# arguments in one expression; where it fails, the _refuse function of the
+# operator finds out what is wrong and raises.
+
+_BF16, _F32, _I32 = torch.bfloat16, torch.float32, torch.int32
+
 
 def _heads(t: torch.Tensor, name: str) -> tuple:
     """[rows, heads, d] bf16 with contiguous channels, any row and head stride."""
@@ -393,25 +408,18 @@ def _same_device(device: torch.device, **tensors) -> None:
             raise ValueError(f"{name} must be on {device}, got {t.device}")
 
 
-def _flags(status: torch.Tensor | None) -> int | None:
-    if status is None:
-        return None
-    if not status.is_cuda or status.element_size() != 4 or status.numel() < 1:
+def _flags_ok(status: torch.Tensor | None, dev: int) -> bool:
+    return status is None or (status.get_device() == dev and status.element_size() == 4 and status.numel() >= 1)
+
+
+def _refuse_flags(status: torch.Tensor | None) -> None:
+    if status is not None and (not status.is_cuda or status.element_size() != 4 or status.numel() < 1):
         raise ValueError("status must be a 32-bit device word")
-    return status.data_ptr()
 
 
-def qk_norm_rope(q: torch.Tensor, k: torch.Tensor, q_weight: torch.Tensor | None, k_weight: torch.Tensor | None,
-                 cos_sin: torch.Tensor, positions: torch.Tensor, *, eps: float = 1e-6,
-                 adjacent_pairs: bool = False, out: tuple | None = None,
-                 status: torch.Tensor | None = None) -> tuple:
-    """RMS norm of every query and key head and the rotation of its first
-    cos_sin.shape[1] channels by position: (q [tokens, hq, d], k [tokens, hkv, d])
-    -> the same shapes, contiguous.  q and k may be strided views of a fused
-    projection; cos_sin is fp32 [max_pos, rot], the cosines of a position
-    before its sines."""
-    tokens, hq, d = _heads(q, "q")
-    _, hkv, _ = _heads(k, "k")
+def _refuse_norm_rope(q, k, q_weight, k_weight, cos_sin, positions, out, status) -> None:
+    tokens, _, d = _heads(q, "q")
+    _heads(k, "k")
     if k.shape[0] != tokens or k.shape[2] != d:
         raise ValueError("q and k must have the same tokens and channels")
     _dev(cos_sin, "cos_sin", torch.float32, 2)
@@ -423,22 +431,50 @@ def qk_norm_rope(q: torch.Tensor, k: torch.Tensor, q_weight: torch.Tensor | None
             _dev(w, name, torch.bfloat16, 1)
             if w.shape[0] != d:
                 raise ValueError(f"{name} must be [d]")
+    if out is not None:
+        for i, (t, like) in enumerate(zip(out, (q, k))):
+            _dev(t, f"out[{i}]", torch.bfloat16, 3)
+            if t.shape != like.shape:
+                raise ValueError("out must have the shapes of q and k")
+        _same_device(q.device, q_out=out[0], k_out=out[1])
+    _refuse_flags(status)
     _same_device(q.device, k=k, q_weight=q_weight, k_weight=k_weight, cos_sin=cos_sin, positions=positions,
                  status=status)
-    if out is None:
-        q_out = torch.empty((tokens, hq, d), dtype=torch.bfloat16, device=q.device)
-        k_out = torch.empty((tokens, hkv, d), dtype=torch.bfloat16, device=q.device)
-    else:
-        q_out, k_out = out
-        _dev(q_out, "out[0]", torch.bfloat16, 3)
-        _dev(k_out, "out[1]", torch.bfloat16, 3)
-        if q_out.shape != q.shape or k_out.shape != k.shape:
-            raise ValueError("out must have the shapes of q and k")
-    st = lib.qg_qk_norm_rope(q.data_ptr(), q.stride(0), q.stride(1), k.data_ptr(), k.stride(0), k.stride(1), tokens,
-                             hq, hkv, d, _ptr(q_weight), _ptr(k_weight), cos_sin.data_ptr(), cos_sin.shape[0],
-                             cos_sin.shape[1], int(adjacent_pairs), positions.data_ptr(), eps, q_out.data_ptr(),
-                             k_out.data_ptr(), _flags(status), _stream(q.device))
-    _check(st, "qg_qk_norm_rope")
+    raise ValueError("qk_norm_rope: arguments that do not fit together")
+
+
+def qk_norm_rope(q: torch.Tensor, k: torch.Tensor, q_weight: torch.Tensor | None, k_weight: torch.Tensor | None,
+                 cos_sin: torch.Tensor, positions: torch.Tensor, *, eps: float = 1e-6,
+                 adjacent_pairs: bool = False, out: tuple | None = None,
+                 status: torch.Tensor | None = None) -> tuple:
+    """RMS norm of every query and key head and the rotation of its first
+    cos_sin.shape[1] channels by position: (q [tokens, hq, d], k [tokens, hkv, d])
+    -> the same shapes, contiguous.  q and k may be strided views of a fused
+    projection; cos_sin is fp32 [max_pos, rot], the cosines of a position
+    before its sines."""
+    dev, qs, ks, cs = q.get_device(), q.shape, k.shape, cos_sin.shape
+    if not (dev >= 0 and len(qs) == 3 and len(ks) == 3 and q.dtype is _BF16 and k.dtype is _BF16 and
+            k.get_device() == dev and ks[0] == qs[0] and ks[2] == qs[2] and q.stride(2) == 1 and k.stride(2) == 1 and
+            len(cs) == 2 and cos_sin.dtype is _F32 and cos_sin.get_device() == dev and cos_sin.is_contiguous() and
+            positions.dtype is _I32 and positions.get_device() == dev and positions.shape == qs[:1] and
+            positions.is_contiguous() and
+            (q_weight is None or (q_weight.dtype is _BF16 and q_weight.get_device() == dev and
+                                  q_weight.shape == qs[2:] and q_weight.is_contiguous())) and
+            (k_weight is None or (k_weight.dtype is _BF16 and k_weight.get_device() == dev and
+                                  k_weight.shape == qs[2:] and k_weight.is_contiguous())) and
+            (out is None or (out[0].dtype is _BF16 and out[1].dtype is _BF16 and out[0].shape == qs and
+                             out[1].shape == ks and out[0].is_contiguous() and out[1].is_contiguous() and
+                             out[0].get_device() == dev and out[1].get_device() == dev)) and
+            _flags_ok(status, dev)):
+        _refuse_norm_rope(q, k, q_weight, k_weight, cos_sin, positions, out, status)
+    q_out, k_out = out if out is not None else (torch.empty(qs, dtype=_BF16, device=q.device),
+                                                torch.empty(ks, dtype=_BF16, device=q.device))
+    st = lib.qg_qk_norm_rope(q.data_ptr(), q.stride(0), q.stride(1), k.data_ptr(), k.stride(0), k.stride(1), qs[0],
+                             qs[1], ks[1], qs[2], _ptr(q_weight), _ptr(k_weight), cos_sin.data_ptr(), cs[0], cs[1],
+                             adjacent_pairs, positions.data_ptr(), eps, q_out.data_ptr(), k_out.data_ptr(),
+                             _ptr(status), _stream_of(dev))
+    if st:
+        _check(st, "qg_qk_norm_rope")
     return q_out, k_out
 
 
@@ -448,31 +484,40 @@ def kv8_empty(pages: int, hkv: int, d: int, device) -> tuple:
             torch.zeros((pages, hkv, 2, KV8_PAGE // KV8_BLOCK), dtype=torch.float32, device=device))
 
 
-def _cache(codes, scales, block_table, lens) -> tuple:
-    """Checks a cache and its table; (pages, hkv, d, b, table width)."""
+def _refuse_cache(codes, scales, block_table, lens) -> None:
     _dev(codes, "codes", torch.int8, 4)
     _dev(scales, "scales", torch.float32, 4)
     _dev(block_table, "block_table", torch.int32, 2)
     _dev(lens, "lens", torch.int32, 1)
-    pages, hkv, two, bytes_ = codes.shape
-    if two != 2 or bytes_ % KV8_PAGE != 0:
+    pages, hkv, two, size = codes.shape
+    if two != 2 or size % KV8_PAGE != 0:
         raise ValueError("codes must be int8 [pages, hkv, 2, 64 * d]")
     if scales.shape != (pages, hkv, 2, KV8_PAGE // KV8_BLOCK):
         raise ValueError("scales must be float32 [pages, hkv, 2, 4]")
-    b, width = block_table.shape
-    if lens.shape[0] != b:
-        raise ValueError("block_table must be [b, width] and lens [b]")
+    if lens.shape[0] != block_table.shape[0] or lens.shape[0] < 1:
+        raise ValueError("block_table must be [b, width] and lens [b], b >= 1")
     _same_device(codes.device, scales=scales, block_table=block_table, lens=lens)
-    return pages, hkv, bytes_ // KV8_PAGE, b, width
+    raise ValueError("a cache whose parts do not fit together")
 
 
-def _starts(cu: torch.Tensor | None, b: int, rows: int, most: int | None, device) -> int:
+def _cache(codes, scales, block_table, lens) -> tuple:
+    """Checks a cache and its table; (device index, pages, hkv, d, b, table width)."""
+    dev, cs, ts = codes.get_device(), codes.shape, block_table.shape
+    if not (dev >= 0 and len(cs) == 4 and len(ts) == 2 and codes.dtype is torch.int8 and scales.dtype is _F32 and
+            block_table.dtype is _I32 and lens.dtype is _I32 and cs[2] == 2 and cs[3] % KV8_PAGE == 0 and
+            scales.shape == (cs[0], cs[1], 2, 4) and lens.shape == ts[:1] and ts[0] >= 1 and
+            scales.get_device() == dev and block_table.get_device() == dev and lens.get_device() == dev and
+            codes.is_contiguous() and scales.is_contiguous() and block_table.is_contiguous() and lens.is_contiguous()):
+        _refuse_cache(codes, scales, block_table, lens)
+    return dev, cs[0], cs[1], cs[3] // KV8_PAGE, ts[0], ts[1]
+
+
+def _starts(cu: torch.Tensor | None, b: int, rows: int, most: int | None, dev: int) -> int:
     """Checks the row offsets; the bound of a sequence's rows."""
     if cu is not None:
-        _dev(cu, "cu", torch.int32, 1)
-        if cu.shape[0] != b + 1:
-            raise ValueError("cu must be [b + 1]")
-        _same_device(device, cu=cu)
+        if cu.dtype is not _I32 or cu.shape != (b + 1,) or cu.get_device() != dev or not cu.is_contiguous():
+            _dev(cu, "cu", torch.int32, 1)
+            raise ValueError("cu must be [b + 1], on the cache's device")
         return rows if most is None else most
     if rows % b != 0:
         raise ValueError("without cu every sequence has the same number of rows")
@@ -486,37 +531,54 @@ def kv8_append(k: torch.Tensor, v: torch.Tensor, codes: torch.Tensor, scales: to
     tokens of the sequences (lens counts them).  Rows of sequence b are
     cu[b]..cu[b + 1] (cu given), or rows / b each; max_new bounds a sequence's
     rows (default: all of them, which launches more workgroups than needed)."""
-    pages, hkv, d, b, width = _cache(codes, scales, block_table, lens)
-    rows = _heads(k, "k")[0]
-    if tuple(k.shape) != (rows, hkv, d) or tuple(_heads(v, "v")) != (rows, hkv, d):
-        raise ValueError("k and v must be [rows, hkv, d] of the cache's heads")
-    most = _starts(cu, b, rows, max_new, codes.device)
-    _same_device(codes.device, k=k, v=v, status=status)
+    dev, pages, hkv, d, b, width = _cache(codes, scales, block_table, lens)
+    shape = k.shape
+    if not (len(shape) == 3 and shape[1] == hkv and shape[2] == d and v.shape == shape and k.dtype is _BF16 and
+            v.dtype is _BF16 and k.get_device() == dev and v.get_device() == dev and k.stride(2) == 1 and
+            v.stride(2) == 1 and _flags_ok(status, dev)):
+        rows = _heads(k, "k")[0]
+        if tuple(k.shape) != (rows, hkv, d) or tuple(_heads(v, "v")) != (rows, hkv, d):
+            raise ValueError("k and v must be [rows, hkv, d] of the cache's heads")
+        _refuse_flags(status)
+        _same_device(codes.device, k=k, v=v, status=status)
+        raise ValueError("kv8_append: arguments that do not fit together")
+    rows = shape[0]
     st = lib.qg_kv8_append(k.data_ptr(), k.stride(0), k.stride(1), v.data_ptr(), v.stride(0), v.stride(1), rows,
                            codes.data_ptr(), scales.data_ptr(), pages, hkv, d, block_table.data_ptr(), width,
-                           lens.data_ptr(), _ptr(cu), b, most, _flags(status), _stream(codes.device))
-    _check(st, "qg_kv8_append")
+                           lens.data_ptr(), _ptr(cu), b, _starts(cu, b, rows, max_new, dev), _ptr(status),
+                           _stream_of(dev))
+    if st:
+        _check(st, "qg_kv8_append")
+
+
+def _out_type(out_dtype: torch.dtype) -> int:
+    if out_dtype is _BF16:
+        return QG_BF16
+    if out_dtype is not _F32:
+        raise ValueError("out_dtype must be torch.bfloat16 or torch.float32")
+    return QG_F32
 
 
 def kv8_read(codes: torch.Tensor, scales: torch.Tensor, block_table: torch.Tensor, lens: torch.Tensor,
              max_len: int, *, out_dtype: torch.dtype = torch.bfloat16, out: tuple | None = None) -> tuple:
     """The sequences' keys and values as [b, max_len, hkv, d]; zero past a length."""
-    pages, hkv, d, b, width = _cache(codes, scales, block_table, lens)
-    if out_dtype not in (torch.bfloat16, torch.float32):
-        raise ValueError("out_dtype must be torch.bfloat16 or torch.float32")
-    shape = (b, max_len, hkv, d)
+    dev, pages, hkv, d, b, width = _cache(codes, scales, block_table, lens)
+    od, shape = _out_type(out_dtype), (b, max_len, hkv, d)
     if out is None:
-        out = tuple(torch.empty(shape, dtype=out_dtype, device=codes.device) for _ in range(2))
-    for i, t in enumerate(out):
-        _dev(t, f"out[{i}]", out_dtype, 4)
-        if tuple(t.shape) != shape:
-            raise ValueError("out must be two [b, max_len, hkv, d]")
-    _same_device(codes.device, k=out[0], v=out[1])
+        k, v = (torch.empty(shape, dtype=out_dtype, device=codes.device),
+                torch.empty(shape, dtype=out_dtype, device=codes.device))
+    else:
+        k, v = out
+        for i, t in enumerate(out):
+            _dev(t, f"out[{i}]", out_dtype, 4)
+            if tuple(t.shape) != shape:
+                raise ValueError("out must be two [b, max_len, hkv, d]")
+        _same_device(codes.device, k=k, v=v)
     st = lib.qg_kv8_read(codes.data_ptr(), scales.data_ptr(), pages, hkv, d, block_table.data_ptr(), width,
-                         lens.data_ptr(), b, max_len, out[0].data_ptr(), out[1].data_ptr(),
-                         QG_F32 if out_dtype == torch.float32 else QG_BF16, _stream(codes.device))
-    _check(st, "qg_kv8_read")
-    return tuple(out)
+                         lens.data_ptr(), b, max_len, k.data_ptr(), v.data_ptr(), od, _stream_of(dev))
+    if st:
+        _check(st, "qg_kv8_read")
+    return k, v
 
 
 def attn_kv8_workspace_bytes(b: int, rows: int, hq: int, hkv: int, d: int, max_q: int, max_len: int, *,
@@ -534,35 +596,45 @@ def attn_kv8(q: torch.Tensor, codes: torch.Tensor, scales: torch.Tensor, block_t
     """Causal attention of query rows [rows, hq, d] (a sequence's last tokens)
     over the cache -> [rows, hq, d].  scale defaults to d ** -0.5, max_len (an
     upper bound of lens, for the choice of the split) to the table's width."""
-    pages, hkv, d, b, width = _cache(codes, scales, block_table, lens)
-    rows, hq, dq = _heads(q, "q")
-    if dq != d:
-        raise ValueError("q must have the cache's channels")
-    most = _starts(cu, b, rows, max_q, codes.device)
+    dev, pages, hkv, d, b, width = _cache(codes, scales, block_table, lens)
+    shape, od = q.shape, _out_type(out_dtype)
+    if not (len(shape) == 3 and shape[2] == d and q.dtype is _BF16 and q.get_device() == dev and q.stride(2) == 1 and
+            (out is None or (out.dtype is out_dtype and out.shape == shape and out.get_device() == dev and
+                             out.is_contiguous())) and
+            (workspace is None or (workspace.get_device() == dev and workspace.is_contiguous())) and
+            _flags_ok(status, dev)):
+        if _heads(q, "q")[2] != d:
+            raise ValueError("q must have the cache's channels")
+        if out is not None:
+            _dev(out, "out", out_dtype, 3)
+            if out.shape != shape:
+                raise ValueError("out must have the shape of q")
+        _refuse_flags(status)
+        _same_device(codes.device, q=q, out=out, workspace=workspace, status=status)
+        raise ValueError("attn_kv8: arguments that do not fit together")
+    rows, hq = shape[0], shape[1]
+    most = _starts(cu, b, rows, max_q, dev)
     if max_len is None:
         max_len = width * KV8_PAGE
-    if out_dtype not in (torch.bfloat16, torch.float32):
-        raise ValueError("out_dtype must be torch.bfloat16 or torch.float32")
     if out is None:
-        out = torch.empty((rows, hq, d), dtype=out_dtype, device=q.device)
-    else:
-        _dev(out, "out", out_dtype, 3)
-        if out.shape != q.shape:
-            raise ValueError("out must have the shape of q")
-    _same_device(codes.device, q=q, out=out, workspace=workspace, status=status)
+        out = torch.empty(shape, dtype=out_dtype, device=q.device)
     if rows == 0:
         return out
-    need = int(lib.qg_attn_kv8_workspace_bytes(b, rows, hq, hkv, d, most, max_len, window, splits))
-    _check(min(need, 0), "qg_attn_kv8")
-    if need and workspace is None:
-        workspace = torch.empty(need, dtype=torch.uint8, device=q.device)
-    ws_bytes = 0 if workspace is None else workspace.numel() * workspace.element_size()
+    ws_bytes = 0
+    if workspace is None:
+        ws_bytes = lib.qg_attn_kv8_workspace_bytes(b, rows, hq, hkv, d, most, max_len, window, splits)
+        if ws_bytes > 0:
+            workspace = torch.empty(ws_bytes, dtype=torch.uint8, device=q.device)
+        elif ws_bytes < 0:
+            _check(ws_bytes, "qg_attn_kv8")
+    else:
+        ws_bytes = workspace.numel() * workspace.element_size()
     st = lib.qg_attn_kv8(q.data_ptr(), q.stride(0), q.stride(1), rows, hq, codes.data_ptr(), scales.data_ptr(), pages,
                          hkv, d, block_table.data_ptr(), width, lens.data_ptr(), _ptr(cu), b, most, max_len, window,
-                         d ** -0.5 if scale is None else scale, out.data_ptr(),
-                         QG_F32 if out_dtype == torch.float32 else QG_BF16, splits, _ptr(workspace), ws_bytes,
-                         _flags(status), _stream(q.device))
-    _check(st, "qg_attn_kv8")
+                         d ** -0.5 if scale is None else scale, out.data_ptr(), od, splits, _ptr(workspace), ws_bytes,
+                         _ptr(status), _stream_of(dev))
+    if st:
+        _check(st, "qg_attn_kv8")
     return out
 
 
@@ -572,31 +644,58 @@ def moe_w4a16_workspace_bytes(t: int, h: int, e: int, inter: int, top_k: int) ->
     return v
 
 
+def _refuse_moe(x, router, gate_up, down, inter, out, out_dtype, workspace) -> None:
+    _dev(x, "x", torch.bfloat16, 2)
+    _dev(router, "router", torch.bfloat16, 2)
+    _dev(gate_up, "gate_up", torch.uint8, 2)
+    _dev(down, "down", torch.uint8, 2)
+    e, h = router.shape[0], x.shape[1]
+    if router.shape[1] != h or gate_up.shape[0] != e or down.shape[0] != e:
+        raise ValueError("router must be [e, h], gate_up and down [e, bytes]")
+    if gate_up.shape[1] != int4_packed_bytes(2 * inter, h) or down.shape[1] != int4_packed_bytes(h, inter):
+        raise ValueError("gate_up must hold packed 2 inter x h weights and down packed h x inter ones")
+    if out is not None:
+        _dev(out, "out", out_dtype, 2)
+        if out.shape != x.shape:
+            raise ValueError("out must be [t, h]")
+    _same_device(x.device, router=router, gate_up=gate_up, down=down, out=out, workspace=workspace)
+    raise ValueError("moe_w4a16: arguments that do not fit together")
+
+
 def moe_w4a16(x: torch.Tensor, router: torch.Tensor, gate_up: torch.Tensor, down: torch.Tensor, inter: int,
               top_k: int, *, renormalize: bool = True, out_dtype: torch.dtype = torch.bfloat16,
               out: torch.Tensor | None = None, workspace: torch.Tensor | None = None) -> torch.Tensor:
     """A mixture-of-experts layer for up to 64 tokens: x [t, h], router [e, h]
     (bf16), gate_up and down uint8 [e, bytes] of quantize_int4_g32 weights
     (2 inter x h, gate rows first; h x inter) -> y [t, h]."""
-    _dev(x, "x", torch.bfloat16, 2)
-    _dev(router, "router", torch.bfloat16, 2)
-    _dev(gate_up, "gate_up", torch.uint8, 2)
-    _dev(down, "down", torch.uint8, 2)
-    t, h = x.shape
-    e = router.shape[0]
-    if router.shape[1] != h or gate_up.shape[0] != e or down.shape[0] != e:
-        raise ValueError("router must be [e, h], gate_up and down [e, bytes]")
-    need = moe_w4a16_workspace_bytes(t, h, e, inter, top_k)
-    if gate_up.shape[1] != int4_packed_bytes(2 * inter, h) or down.shape[1] != int4_packed_bytes(h, inter):
-        raise ValueError("gate_up must hold packed 2 inter x h weights and down packed h x inter ones")
-    y, yd = _out(t, h, out_dtype, x.device, out)
-    if tuple(y.shape) != (t, h):
-        raise ValueError("out must be [t, h]")
+    dev, xs, rs, gs, ds = x.get_device(), x.shape, router.shape, gate_up.shape, down.shape
+    od = _out_type(out_dtype)
+    if not (dev >= 0 and len(xs) == 2 and len(rs) == 2 and len(gs) == 2 and len(ds) == 2 and x.dtype is _BF16 and
+            router.dtype is _BF16 and gate_up.dtype is torch.uint8 and down.dtype is torch.uint8 and
+            rs[1] == xs[1] and gs[0] == rs[0] and ds[0] == rs[0] and inter > 0 and
+            gs[1] == 2 * inter // TILE_ROWS * (xs[1] // TILE_K) * TILE_BYTES and
+            ds[1] == xs[1] // TILE_ROWS * (inter // TILE_K) * TILE_BYTES and
+            router.get_device() == dev and gate_up.get_device() == dev and down.get_device() == dev and
+            x.is_contiguous() and router.is_contiguous() and gate_up.is_contiguous() and down.is_contiguous() and
+            (out is None or (out.dtype is out_dtype and out.shape == xs and out.get_device() == dev and
+                             out.is_contiguous())) and
+            (workspace is None or (workspace.get_device() == dev and workspace.is_contiguous()))):
+        if dev >= 0:
+            moe_w4a16_workspace_bytes(xs[0], xs[-1], rs[0], inter, top_k)   # sizes that no call takes
+        _refuse_moe(x, router, gate_up, down, inter, out, out_dtype, workspace)
+    t, h, e = xs[0], xs[1], rs[0]
     if workspace is None:
-        workspace = torch.empty(need, dtype=torch.uint8, device=x.device)
-    _same_device(x.device, router=router, gate_up=gate_up, down=down, out=y, workspace=workspace)
+        ws_bytes = lib.qg_moe_w4a16_workspace_bytes(t, h, e, inter, top_k)
+        if ws_bytes < 0:
+            _check(ws_bytes, "qg_moe_w4a16")
+        workspace = torch.empty(ws_bytes, dtype=torch.uint8, device=x.device)
+    else:
+        ws_bytes = workspace.numel() * workspace.element_size()
+    if out is None:
+        out = torch.empty(xs, dtype=out_dtype, device=x.device)
     st = lib.qg_moe_w4a16(x.data_ptr(), t, h, router.data_ptr(), e, gate_up.data_ptr(), gate_up.numel(), down.data_ptr(),
-                          down.numel(), inter, top_k, int(renormalize), y.data_ptr(), yd, workspace.data_ptr(),
-                          workspace.numel() * workspace.element_size(), _stream(x.device))
-    _check(st, "qg_moe_w4a16")
-    return y
+                          down.numel(), inter, top_k, renormalize, out.data_ptr(), od, workspace.data_ptr(), ws_bytes,
+                          _stream_of(dev))
+    if st:
+        _check(st, "qg_moe_w4a16")
+    return out
