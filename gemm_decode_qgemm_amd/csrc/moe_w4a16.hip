@@ -7,7 +7,8 @@
 // with the products of qgemm_w4a16: exact bf16 (128 + q) times bf16
 // activations, fp32 sums, the group scale and -(128 + zp) times the group sum
 // of x applied per group in fp32.  The hidden activation is rounded to bf16
-// once, as the second product's operand; all else is fp32.
+// once, as the second product's operand (for one token it is the sum of two bf16,
+// which costs nothing there); all else is fp32.
 //
 // Launches, with no atomics between workgroups (bit-identical repeats):
 //   router      logits in fp32
@@ -45,7 +46,7 @@ struct MoeArgs {
   float* picked;                      // [t * k] logits in order of rank
   int32_t* count;                     // [e] tokens of an expert
   int32_t* list;                      // [e][64] their picks, t k + rank; one token: [k] experts
-  uint16_t* hidden;                   // [t * k, inter]
+  uint16_t* hidden;                   // [t * k, inter]; one token: [2][k, inter], a sum of two
   float* part;                        // [t * k, h]
   void* y;
   int y_f32;
@@ -318,9 +319,8 @@ __device__ __forceinline__ void moe_mx4(float (&acc)[M], int hb, int u0, int uni
   }
 }
 
-// silu(g) u as bf16.
-__device__ __forceinline__ uint16_t silu_mul(float g, float u) {
-  return (uint16_t)f32_to_bf16_rne(g / (1.0f + __builtin_amdgcn_exp2f(-1.44269504088896340736f * g)) * u);
+__device__ __forceinline__ float silu_mul(float g, float u) {
+  return g / (1.0f + __builtin_amdgcn_exp2f(-1.44269504088896340736f * g)) * u;
 }
 
 // One token.  A workgroup of 16 waves owns the gate and up rows of 32 hidden
@@ -355,7 +355,13 @@ __global__ __launch_bounds__(1024) __attribute__((amdgpu_waves_per_eu(8))) void 
   float v[2] = {0.0f, 0.0f};
 #pragma unroll
   for (int w = 0; w < 16; ++w) v[w >> 3] += sh.red[w][tid] + sh.red[w][tid + 32];
-  a.hidden[(size_t)pick * a.inter + 32 * tile + tid] = silu_mul(v[0], v[1]);
+  // the hidden value as a sum of two bf16: the second is free in the down
+  // launch, whose matrix instruction has four rows for one token
+  const float f = silu_mul(v[0], v[1]);
+  const uint32_t hi = f32_to_bf16_rne(f);
+  const size_t at = (size_t)pick * a.inter + 32 * tile + tid;
+  a.hidden[at] = (uint16_t)hi;
+  a.hidden[(size_t)a.k * a.inter + at] = (uint16_t)f32_to_bf16_rne(f - bf16_to_f32(hi));
 }
 
 // The softmax denominator of a token's picks, relative to its first logit.
@@ -377,16 +383,16 @@ __device__ __forceinline__ float moe_total(const MoeArgs& a, int t, const float*
 // half the rows of the mapping above and twice the workgroups (2 picks of 14336 x
 // 4096, down: 21 us with 32 rows and 128 workgroups).
 __global__ __launch_bounds__(1024) __attribute__((amdgpu_waves_per_eu(8))) void moe_down_one_kernel(MoeArgs a) {
-  struct Slot {
-    uint8_t x[512];
-    float sum[8];
+  struct Slot {                      // of one wave: both parts of the hidden values of a tile
+    uint8_t x[2][512 + 16];          // (16 bytes apart: the operand reads of lanes 4j and 4j + 1 on other banks)
+    float sum[2][8];                 // their group sums
   };
   __shared__ __attribute__((aligned(16))) Slot slots[16];
   __shared__ float red[16][64];
   __shared__ float p[32];
   __shared__ int expert[32];
   const int tid = threadIdx.x, lane = tid & 63, wave = wave_id_uniform();
-  const int i = lane & 15, q = lane >> 4, c = lane & 31;
+  const int i = lane & 15, q = lane >> 4, c = lane & 31, part = lane >> 5;
   const int row = 16 * (blockIdx.x & 3) + i;             // of the 64-row block
   const float total = moe_total(a, 0, a.picked);
   if (tid < a.k) {
@@ -415,7 +421,7 @@ __global__ __launch_bounds__(1024) __attribute__((amdgpu_waves_per_eu(8))) void 
       sc[g] = v.b16((uint32_t)(kScaleOff + row * 16 + 8 * g + 2 * q));
     }
     const uint32_t zw = v.b32((uint32_t)(kZeroOff + row * 4));
-    const u32x4_t xv = *reinterpret_cast<const u32x4_t*>(a.hidden + (size_t)j * a.inter + (size_t)kt * 256 + 8 * c);
+    const u32x4_t xv = *reinterpret_cast<const u32x4_t*>(a.hidden + (size_t)(j + part * a.k) * a.inter + (size_t)kt * 256 + 8 * c);
     float xp = dot2_bf16(xv.x, ones_v, 0.0f);
     xp = dot2_bf16(xv.y, ones_v, xp);
     xp = dot2_bf16(xv.z, ones_v, xp);
@@ -425,10 +431,8 @@ __global__ __launch_bounds__(1024) __attribute__((amdgpu_waves_per_eu(8))) void 
     // wave-private slot: a wave's LDS operations complete in order
     __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
     __builtin_amdgcn_wave_barrier();
-    if (lane < 32) {
-      *reinterpret_cast<u32x4_t*>(slot.x + 16 * c) = xv;
-      if ((c & 3) == 0) slot.sum[c >> 2] = xp;
-    }
+    *reinterpret_cast<u32x4_t*>(slot.x[part] + 16 * c) = xv;
+    if ((c & 3) == 0) slot.sum[part][c >> 2] = xp;
     __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
     __builtin_amdgcn_wave_barrier();
     __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
@@ -437,13 +441,14 @@ __global__ __launch_bounds__(1024) __attribute__((amdgpu_waves_per_eu(8))) void 
       f32x4_t d = {0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
       for (int t = 0; t < 8; ++t) {
-        const u32x2_t xa = *reinterpret_cast<const u32x2_t*>(slot.x + 64 * (4 * g + q) + 8 * t);
+        const u32x2_t xa = *reinterpret_cast<const u32x2_t*>(slot.x[lane & 1] + 64 * (4 * g + q) + 8 * t);
         const u32x2_t b = {code_pair(w[g][t >> 1], 2 * (t & 1), mask_s, magic_v),
                            code_pair(w[g][t >> 1], 2 * (t & 1) + 1, mask_s, magic_v)};
         d = mfma_4x4x4(xa, b, d);
       }
       const float zb = (float)((zw >> (16 * g + 4 * q) & 15u) | 0x80u);
-      acc = __builtin_fmaf(p[j] * fp16_to_f32(sc[g]), __builtin_fmaf(-zb, slot.sum[4 * g + q], d[0]), acc);
+      const float x = slot.sum[0][4 * g + q] + slot.sum[1][4 * g + q];
+      acc = __builtin_fmaf(p[j] * fp16_to_f32(sc[g]), __builtin_fmaf(-zb, x, d[0] + d[1]), acc);
     }
   }
   red[wave][lane] = acc;
@@ -623,7 +628,7 @@ __global__ __launch_bounds__(512) __attribute__((amdgpu_waves_per_eu(4))) void m
 #pragma unroll
         for (int u = 0; u < KP; ++u) v[b] += sh.red[4 * b + w + u][wave][l] + sh.red[4 * b + w + u][wave][l + 32];
       if constexpr (F == kGateUp) {
-        a.hidden[s * a.inter + 64 * tile + lane] = silu_mul(v[0], v[1]);
+        a.hidden[s * a.inter + 64 * tile + lane] = (uint16_t)f32_to_bf16_rne(silu_mul(v[0], v[1]));
       } else {
         float* const o = a.part + s * a.h + (DEEP ? 64 : 128) * tile + lane;
         o[0] = v[0];
@@ -651,7 +656,8 @@ __global__ __launch_bounds__(512) __attribute__((amdgpu_waves_per_eu(4))) void m
         const size_t s = __shfl(pick, m < n ? m : n - 1);
         if (m >= n) continue;
         if constexpr (F == kGateUp)
-          a.hidden[s * a.inter + 64 * tile + 16 * t + i] = silu_mul(acc[mt][e], sh.other[t][mt][lane][e]);
+          a.hidden[s * a.inter + 64 * tile + 16 * t + i] =
+              (uint16_t)f32_to_bf16_rne(silu_mul(acc[mt][e], sh.other[t][mt][lane][e]));
         else if constexpr (DEEP)
           a.part[s * a.h + 64 * tile + 16 * t + i] = acc[mt][e] + sh.other[t][mt][lane][e];
         else
@@ -711,7 +717,7 @@ __global__ __launch_bounds__(256) void moe_combine_kernel(MoeArgs a) {
 static int64_t up256(int64_t n) { return (n + 255) & ~(int64_t)255; }
 
 int64_t moe_ws_bytes(int64_t t, int64_t h, int64_t e, int64_t inter, int64_t k) {
-  return up256(t * e * 4) + up256(t * k * 4) + up256(t * k * inter * 2) + up256(t * k * h * 4) +
+  return up256(t * e * 4) + up256(t * k * 4) + up256(t * k * inter * (t == 1 ? 4 : 2)) + up256(t * k * h * 4) +
          up256(e * 4) + up256(e * 256);
 }
 
@@ -733,7 +739,7 @@ hipError_t launch_moe_w4a16(const void* x, int t, int h, const void* router, int
   };
   a.logits = reinterpret_cast<float*>(take((int64_t)t * e * 4));
   a.picked = reinterpret_cast<float*>(take((int64_t)t * k * 4));
-  a.hidden = reinterpret_cast<uint16_t*>(take((int64_t)t * k * inter * 2));
+  a.hidden = reinterpret_cast<uint16_t*>(take((int64_t)t * k * inter * (t == 1 ? 4 : 2)));
   a.part = reinterpret_cast<float*>(take((int64_t)t * k * h * 4));
   a.count = reinterpret_cast<int32_t*>(take((int64_t)e * 4));
   a.list = reinterpret_cast<int32_t*>(take((int64_t)e * 256));
