@@ -478,19 +478,28 @@ struct MoeTile {                  // one 256-k tile of a wave's 16 rows: lane (i
 
 // acc[mt][e] += row 16t + i of the block times activation row 16 mt + 4a + e,
 // over the tiles kt0 .. kt0 + count - 1 of K.  TH threads (`tid` among them)
-// copy the 16 MT activation rows of a 256-k tile into one of two LDS buffers at
-// xs: 16-byte piece c of row r at 32 r + (c ^ (r & 15)), so that the operand
-// reads of 16 lanes, one row each, fall on distinct banks; xr: this thread's
-// rows tid / 32 + (TH / 32) j.  Codes go two tiles ahead, activations one (through
+// copy the 16 MT activation rows of a 256-k tile into one of two LDS buffers:
+// 16-byte piece c of row r at 32 r + (c ^ (r & 15)), so that the operand reads of
+// 16 lanes, one row each, fall on distinct banks; xr: this thread's rows
+// tid / 32 + (TH / 32) j.  Codes go two tiles ahead, activations one (through
 // registers).  The workgroup's waves pass `steps` >= count barriers together.
+//
+// Each group is as short as it goes: the zero point is taken off four codes at
+// a time, as whole bytes 16 + q - zp; one byte permute each then gives the bf16
+// pairs 144 + (q - zp), exactly; a product of x with -144 in every slot (a
+// constant operand) takes the 144 off again, so that one multiply-add per output
+// is left.  -(128 + zp) as the second operand instead took 26 vector
+// instructions a group where this takes 18, and -144 X through LDS as the
+// first value of the accumulator made LDS the bound at 32 rows.
 template <int MT, int TH>
 __device__ __forceinline__ void moe_mx16(f32x4_t (&acc)[MT], const uint8_t* tiles, int t, int kt0, int count, int steps,
                                          const uint16_t* (&xr)[MT * 512 / TH], int tid, uint8_t* xs) {
   constexpr int NP = MT * 512 / TH;
   const int lane = tid & 63, i = lane & 15, a = lane >> 4;
-  const uint32_t mask_s = __builtin_amdgcn_readfirstlane(0x000F000Fu);
-  uint32_t magic_v = 0x43004300u;
-  asm volatile("" : "+v"(magic_v));
+  uint32_t m144 = 0xc310c310u;     // bf16 pair (-144, -144), kept in registers
+  asm volatile("" : "+v"(m144));
+  const u32x4_t minus4 = {m144, m144, m144, m144};
+  const bf16x8_t minus = __builtin_bit_cast(bf16x8_t, minus4);
   const f32x4_t zero4 = {0.0f, 0.0f, 0.0f, 0.0f};
   const int pc = tid & 31, pr = tid >> 5;
   auto load_w = [&](MoeTile& w, int kt) {
@@ -516,15 +525,17 @@ __device__ __forceinline__ void moe_mx16(f32x4_t (&acc)[MT], const uint8_t* tile
     transpose_rows4(w.c0);
     transpose_rows4(w.c1);
     const uint8_t* const xb = xs + buf * (MT * 8192);
+    // bytes 16 - zp of groups 0, 2, 4, 6 and 1, 3, 5, 7
+    const uint32_t z0 = 0x10101010u - (w.zw & 0x0F0F0F0Fu), z1 = 0x10101010u - ((w.zw >> 4) & 0x0F0F0F0Fu);
 #pragma unroll
     for (int g = 0; g < 8; ++g) {
       const uint32_t dw = g < 4 ? w.c0[g] : w.c1[g - 4];
-      u32x4_t bp;
-#pragma unroll
-      for (int e = 0; e < 4; ++e) bp[e] = code_pair(dw, e, mask_s, magic_v);
-      const uint32_t z = (w.zw >> (4 * g)) & 15u;
-      const uint32_t zn = (z | (z << 16)) | 0xC300C300u;     // bf16 pair -(128 + zp)
-      const u32x4_t zz = {zn, zn, zn, zn};
+      const uint32_t z = __builtin_amdgcn_perm(0u, (g & 1) ? z1 : z0, 0x01010101u * (uint32_t)(g >> 1));
+      const uint32_t lo = (dw & 0x0F0F0F0Fu) + z, hi = ((dw >> 4) & 0x0F0F0F0Fu) + z;   // bytes 16 + q - zp
+      const u32x4_t bp = {__builtin_amdgcn_perm(0x43434343u, lo, 0x04020400u),
+                          __builtin_amdgcn_perm(0x43434343u, hi, 0x04020400u),
+                          __builtin_amdgcn_perm(0x43434343u, lo, 0x04030401u),
+                          __builtin_amdgcn_perm(0x43434343u, hi, 0x04030401u)};
       const float s = fp16_to_f32((w.sc[g >> 1] >> (16 * (g & 1))) & 0xffffu);
       bf16x8_t av[MT];
       f32x4_t d[MT];
@@ -532,11 +543,11 @@ __device__ __forceinline__ void moe_mx16(f32x4_t (&acc)[MT], const uint8_t* tile
       for (int mt = 0; mt < MT; ++mt) {
         const u32x4_t x = *reinterpret_cast<const u32x4_t*>(xb + 16 * (32 * (16 * mt + i) + ((4 * g + a) ^ i)));
         av[mt] = __builtin_bit_cast(bf16x8_t, x);
-        d[mt] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(av[mt], __builtin_bit_cast(bf16x8_t, bp), zero4, 0, 0, 0);
+        d[mt] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(av[mt], minus, zero4, 0, 0, 0);
       }
 #pragma unroll
       for (int mt = 0; mt < MT; ++mt)
-        d[mt] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(av[mt], __builtin_bit_cast(bf16x8_t, zz), d[mt], 0, 0, 0);
+        d[mt] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(av[mt], __builtin_bit_cast(bf16x8_t, bp), d[mt], 0, 0, 0);
 #pragma unroll
       for (int mt = 0; mt < MT; ++mt)
 #pragma unroll
@@ -578,7 +589,7 @@ __device__ __forceinline__ void moe_mx16(f32x4_t (&acc)[MT], const uint8_t* tile
 // 64 hidden columns, four waves each.  kDownWide: two neighbouring 64-row blocks
 // of the down matrix, four waves each.  kDownDeep: one block, four waves on each
 // half of K: twice the workgroups with half the work each, for grids that
-// would leave CUs idle otherwise.
+// would leave CUs idle otherwise (up to 16 tokens in all).
 enum MoeForm { kGateUp, kDownWide, kDownDeep };
 
 template <MoeForm F>
@@ -587,7 +598,7 @@ __global__ __launch_bounds__(512) __attribute__((amdgpu_waves_per_eu(4))) void m
   union Shared {
     MoeSlot slot[8];
     float red[8][4][64];
-    uint8_t x[DEEP ? 2 : 1][2 * 2 * 8192];
+    uint8_t x[2][2 * 8192];                  // deep: a half of K each; else one piece
     f32x4_t other[4][2][64];                 // results of the waves 4 .. 7
   };
   __shared__ __attribute__((aligned(16))) Shared sh;
@@ -670,8 +681,8 @@ __global__ __launch_bounds__(512) __attribute__((amdgpu_waves_per_eu(4))) void m
   const int steps = DEEP ? (kt_count + 1) >> 1 : kt_count;
   const int count = DEEP && blk == 1 ? kt_count - steps : steps;
   const int kt0 = DEEP && blk == 1 ? min(steps, kt_count - 1) : 0;
-  uint8_t* const xs = sh.x[DEEP ? blk : 0];
-  if (n <= 16) {
+  uint8_t* const xs = sh.x[DEEP ? blk : 0];    // 16 rows a buffer (deep), up to 32
+  if (DEEP || n <= 16) {                       // (deep: n <= t <= 16)
     f32x4_t acc[1] = {};
     const uint16_t* xr[512 / TH];
 #pragma unroll
@@ -679,8 +690,9 @@ __global__ __launch_bounds__(512) __attribute__((amdgpu_waves_per_eu(4))) void m
     moe_mx16<1, TH>(acc, tiles, t, kt0, count, steps, xr, th, xs);
     const f32x4_t both[2] = {acc[0], acc[0]};
     finish(both, 1, 0);
-  } else {
-    for (int m0 = 0; m0 < n; m0 += 32) {
+  }
+  if constexpr (!DEEP) {
+    for (int m0 = n <= 16 ? n : 0; m0 < n; m0 += 32) {
       f32x4_t acc[2] = {};
       const uint16_t* xr[1024 / TH];
 #pragma unroll
@@ -763,11 +775,12 @@ hipError_t launch_moe_w4a16(const void* x, int t, int h, const void* router, int
   if (!ok()) return st;
   hipLaunchKernelGGL((moe_expert_kernel<kGateUp>), dim3(inter / 64, units), dim3(512), 0, stream, a);
   if (!ok()) return st;
-  // Down in the deep form up to a workgroup per CU (8 of 8 experts of 14336 x 4096
+  // Down in the deep form for up to 16 tokens (it holds one tile of them) and
+  // up to a workgroup per CU (8 of 8 experts of 14336 x 4096
   // hit by 8 tokens, 256 workgroups: 150 us against 170 wide; 16 of 5888 x 1024,
   // 128: 47 against 56); above it the wide form copies each activation row for
   // twice the weight rows (128 experts of 768 x 2048: 64 us against 71 deep).
-  if (h / 128 * units <= kCUs)
+  if (t <= 16 && h / 128 * units <= kCUs)
     hipLaunchKernelGGL((moe_expert_kernel<kDownDeep>), dim3(h / 64, units), dim3(512), 0, stream, a);
   else
     hipLaunchKernelGGL((moe_expert_kernel<kDownWide>), dim3(h / 128, units), dim3(512), 0, stream, a);
