@@ -467,8 +467,8 @@ def qk_norm_rope(q: torch.Tensor, k: torch.Tensor, q_weight: torch.Tensor | None
                              out[0].get_device() == dev and out[1].get_device() == dev)) and
             _flags_ok(status, dev)):
         _refuse_norm_rope(q, k, q_weight, k_weight, cos_sin, positions, out, status)
-    q_out, k_out = out if out is not None else (torch.empty(qs, dtype=_BF16, device=q.device),
-                                                torch.empty(ks, dtype=_BF16, device=q.device))
+    q_out, k_out = out if out is not None else (torch.empty_like(q, memory_format=torch.contiguous_format),
+                                                torch.empty_like(k, memory_format=torch.contiguous_format))
     st = lib.qg_qk_norm_rope(q.data_ptr(), q.stride(0), q.stride(1), k.data_ptr(), k.stride(0), k.stride(1), qs[0],
                              qs[1], ks[1], qs[2], _ptr(q_weight), _ptr(k_weight), cos_sin.data_ptr(), cs[0], cs[1],
                              adjacent_pairs, positions.data_ptr(), eps, q_out.data_ptr(), k_out.data_ptr(),
@@ -565,8 +565,8 @@ def kv8_read(codes: torch.Tensor, scales: torch.Tensor, block_table: torch.Tenso
     dev, pages, hkv, d, b, width = _cache(codes, scales, block_table, lens)
     od, shape = _out_type(out_dtype), (b, max_len, hkv, d)
     if out is None:
-        k, v = (torch.empty(shape, dtype=out_dtype, device=codes.device),
-                torch.empty(shape, dtype=out_dtype, device=codes.device))
+        k = torch.empty(shape, dtype=out_dtype, device=codes.device)
+        v = torch.empty_like(k)
     else:
         k, v = out
         for i, t in enumerate(out):
@@ -617,7 +617,7 @@ def attn_kv8(q: torch.Tensor, codes: torch.Tensor, scales: torch.Tensor, block_t
     if max_len is None:
         max_len = width * KV8_PAGE
     if out is None:
-        out = torch.empty(shape, dtype=out_dtype, device=q.device)
+        out = torch.empty_like(q, dtype=out_dtype, memory_format=torch.contiguous_format)
     if rows == 0:
         return out
     ws_bytes = 0
@@ -692,7 +692,7 @@ def moe_w4a16(x: torch.Tensor, router: torch.Tensor, gate_up: torch.Tensor, down
     else:
         ws_bytes = workspace.numel() * workspace.element_size()
     if out is None:
-        out = torch.empty(xs, dtype=out_dtype, device=x.device)
+        out = torch.empty_like(x, dtype=out_dtype)
     st = lib.qg_moe_w4a16(x.data_ptr(), t, h, router.data_ptr(), e, gate_up.data_ptr(), gate_up.numel(), down.data_ptr(),
                           down.numel(), inter, top_k, renormalize, out.data_ptr(), od, workspace.data_ptr(), ws_bytes,
                           _stream_of(dev))

@@ -7,7 +7,7 @@
 // with the products of qgemm_w4a16: exact bf16 (128 + q) times bf16
 // activations, fp32 sums, the group scale and -(128 + zp) times the group sum
 // of x applied per group in fp32.  The hidden activation is rounded to bf16
-// once, as the second product's operand (for one token it is the sum of two bf16,
+// once, as the second product's operand (up to 4 tokens it is the sum of two bf16,
 // which costs nothing there); all else is fp32.
 //
 // Launches, with no atomics between workgroups (bit-identical repeats):
@@ -15,9 +15,9 @@
 //   route       above one token: the tokens of every expert
 //   gate and up the two products of a few hidden columns of one expert, and
 //               silu(g) u of its tokens
-//   down        one token: the weighted sum over its picks; above: fp32 results
-//               per (token, pick)
-//   combine     above one token: the weighted sum, in order of rank
+//   down        up to 4 tokens: the weighted sum over a token's picks; above: fp32
+//               results per (token, pick)
+//   combine     above 4 tokens: the weighted sum, in order of rank
 // The rank of expert e for a token is the number of experts before it, so "which
 // tokens picked e" takes one ballot per 64 experts and token, and a token's pick
 // number is that rank.  For one token each workgroup of the gate and up launch
@@ -37,6 +37,8 @@
 
 namespace qg {
 
+constexpr int kFewTokens = 4;         // up to these, the down launch adds a token's picks itself
+
 struct MoeArgs {
   const uint16_t *x, *router;
   const uint8_t *gate_up, *down;
@@ -45,8 +47,9 @@ struct MoeArgs {
   float* logits;                      // [t, e]
   float* picked;                      // [t * k] logits in order of rank
   int32_t* count;                     // [e] tokens of an expert
-  int32_t* list;                      // [e][64] their picks, t k + rank; one token: [k] experts
-  uint16_t* hidden;                   // [t * k, inter]; one token: [2][k, inter], a sum of two
+  int32_t* list;                      // [e][64] their picks, t k + rank
+  int32_t* expert_of;                 // [t * k] experts in order of rank
+  uint16_t* hidden;                   // [t * k, inter]; up to 4 tokens: [2][t * k, inter], a sum of two
   float* part;                        // [t * k, h]
   void* y;
   int y_f32;
@@ -91,11 +94,21 @@ __global__ __launch_bounds__(1024) void moe_router_mfma_kernel(MoeArgs a) {
   const uint16_t* const w = a.router + (size_t)min(e0 + i, a.e - 1) * a.h + 8 * q;
   const uint16_t* const x = a.x + (size_t)min(t0 + i, a.t - 1) * a.h + 8 * q;
   f32x4_t acc = {0.0f, 0.0f, 0.0f, 0.0f};
-#pragma unroll 4
-  for (int c = wave * 32; c < a.h; c += 512)
-    acc = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8_t, *reinterpret_cast<const u32x4_t*>(x + c)),
-                                                  __builtin_bit_cast(bf16x8_t, *reinterpret_cast<const u32x4_t*>(w + c)),
-                                                  acc, 0, 0, 0);
+  for (int c = wave * 32; c < a.h; c += 2048) {      // four steps' loads in flight together
+    u32x4_t xv[4], wv[4];
+#pragma unroll
+    for (int u = 0; u < 4; ++u) {
+      xv[u] = wv[u] = u32x4_t{0u, 0u, 0u, 0u};
+      if (c + 512 * u < a.h) {
+        xv[u] = *reinterpret_cast<const u32x4_t*>(x + c + 512 * u);
+        wv[u] = *reinterpret_cast<const u32x4_t*>(w + c + 512 * u);
+      }
+    }
+#pragma unroll
+    for (int u = 0; u < 4; ++u)
+      acc = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8_t, xv[u]), __builtin_bit_cast(bf16x8_t, wv[u]),
+                                                    acc, 0, 0, 0);
+  }
   red[wave][lane] = acc;
   __syncthreads();
   if (threadIdx.x >= 64) return;
@@ -190,6 +203,7 @@ __global__ __launch_bounds__(512) void moe_route_kernel(MoeArgs a) {
     const int slot = lane * a.k + rank[lane];
     a.list[expert * 64 + __popcll(mask & (((uint64_t)1 << lane) - 1))] = slot;
     a.picked[slot] = a.logits[(size_t)lane * a.e + expert];
+    a.expert_of[slot] = expert;
   }
 }
 
@@ -323,6 +337,14 @@ __device__ __forceinline__ float silu_mul(float g, float u) {
   return g / (1.0f + __builtin_amdgcn_exp2f(-1.44269504088896340736f * g)) * u;
 }
 
+// A hidden value as a sum of two bf16, for the down launch of a few tokens: its
+// matrix instruction has four rows for one token.
+__device__ __forceinline__ void store_hidden2(const MoeArgs& a, size_t at, float f) {
+  const uint32_t hi = f32_to_bf16_rne(f);
+  a.hidden[at] = (uint16_t)hi;
+  a.hidden[(size_t)a.t * a.k * a.inter + at] = (uint16_t)f32_to_bf16_rne(f - bf16_to_f32(hi));
+}
+
 // One token.  A workgroup of 16 waves owns the gate and up rows of 32 hidden
 // columns of one pick, 8 waves each, K split over them.  Two workgroups per CU
 // (64 VGPRs) rather than a second register set.
@@ -338,7 +360,7 @@ __global__ __launch_bounds__(1024) __attribute__((amdgpu_waves_per_eu(8))) void 
   const int tile = blockIdx.x, pick = blockIdx.y;
   const int expert = moe_plan(a, pick, sh.plan);
   if (tile == 0 && tid == 0) {
-    a.list[pick] = expert;
+    a.expert_of[pick] = expert;
     a.picked[pick] = a.logits[expert];
   }
   __syncthreads();                   // the plan's LDS becomes the waves' slots
@@ -355,13 +377,7 @@ __global__ __launch_bounds__(1024) __attribute__((amdgpu_waves_per_eu(8))) void 
   float v[2] = {0.0f, 0.0f};
 #pragma unroll
   for (int w = 0; w < 16; ++w) v[w >> 3] += sh.red[w][tid] + sh.red[w][tid + 32];
-  // the hidden value as a sum of two bf16: the second is free in the down
-  // launch, whose matrix instruction has four rows for one token
-  const float f = silu_mul(v[0], v[1]);
-  const uint32_t hi = f32_to_bf16_rne(f);
-  const size_t at = (size_t)pick * a.inter + 32 * tile + tid;
-  a.hidden[at] = (uint16_t)hi;
-  a.hidden[(size_t)a.k * a.inter + at] = (uint16_t)f32_to_bf16_rne(f - bf16_to_f32(hi));
+  store_hidden2(a, (size_t)pick * a.inter + 32 * tile + tid, silu_mul(v[0], v[1]));
 }
 
 // The softmax denominator of a token's picks, relative to its first logit.
@@ -377,12 +393,15 @@ __device__ __forceinline__ float moe_total(const MoeArgs& a, int t, const float*
   return total;
 }
 
-// One token: 16 rows of the output through all its picks, 16 waves taking 256-k
-// tiles of the picks in turn, the picks' weights applied with the group
-// scales.  Lane (i, a) holds row i of the 16 and groups a and 4 + a of the tile:
+// Up to 4 tokens: 16 rows of a token's output through all its picks, 16 waves
+// taking 256-k tiles of the picks in turn, the picks' weights applied with the
+// group scales, so that neither results per pick nor a combining launch are
+// needed.  Lane (i, a) holds row i of the 16 and groups a and 4 + a of the tile:
 // half the rows of the mapping above and twice the workgroups (2 picks of 14336 x
-// 4096, down: 21 us with 32 rows and 128 workgroups).
-__global__ __launch_bounds__(1024) __attribute__((amdgpu_waves_per_eu(8))) void moe_down_one_kernel(MoeArgs a) {
+// 4096: 14 us against 21 with 32 rows and 128 workgroups).  Tokens that share
+// an expert read it once each, from L2 the second time (a row block's
+// workgroups of all tokens go to the same XCD where h / 16 is a multiple of 8).
+__global__ __launch_bounds__(1024) __attribute__((amdgpu_waves_per_eu(8))) void moe_down_few_kernel(MoeArgs a) {
   struct Slot {                      // of one wave: both parts of the hidden values of a tile
     uint8_t x[2][512 + 16];          // (16 bytes apart: the operand reads of lanes 4j and 4j + 1 on other banks)
     float sum[2][8];                 // their group sums
@@ -394,14 +413,17 @@ __global__ __launch_bounds__(1024) __attribute__((amdgpu_waves_per_eu(8))) void 
   const int tid = threadIdx.x, lane = tid & 63, wave = wave_id_uniform();
   const int i = lane & 15, q = lane >> 4, c = lane & 31, part = lane >> 5;
   const int row = 16 * (blockIdx.x & 3) + i;             // of the 64-row block
-  const float total = moe_total(a, 0, a.picked);
+  const int token = blockIdx.y;
+  const float* const picked = a.picked + token * a.k;
+  const float total = moe_total(a, token, picked);
   if (tid < a.k) {
-    p[tid] = expf(a.picked[tid] - a.picked[0]) / total;
-    expert[tid] = a.list[tid];
+    p[tid] = expf(picked[tid] - picked[0]) / total;
+    expert[tid] = a.expert_of[token * a.k + tid];
   }
   __syncthreads();
   const int kt_count = a.inter >> 8;
   const size_t block = (size_t)(blockIdx.x >> 2) * kt_count * kTileBytes;
+  const uint16_t* const hidden = a.hidden + (size_t)(part * a.t + token) * a.k * a.inter + 8 * c;
   const uint32_t mask_s = __builtin_amdgcn_readfirstlane(0x000F000Fu);
   uint32_t magic_v = 0x43004300u;
   asm volatile("" : "+v"(magic_v));
@@ -421,7 +443,7 @@ __global__ __launch_bounds__(1024) __attribute__((amdgpu_waves_per_eu(8))) void 
       sc[g] = v.b16((uint32_t)(kScaleOff + row * 16 + 8 * g + 2 * q));
     }
     const uint32_t zw = v.b32((uint32_t)(kZeroOff + row * 4));
-    const u32x4_t xv = *reinterpret_cast<const u32x4_t*>(a.hidden + (size_t)(j + part * a.k) * a.inter + (size_t)kt * 256 + 8 * c);
+    const u32x4_t xv = *reinterpret_cast<const u32x4_t*>(hidden + (size_t)j * a.inter + (size_t)kt * 256);
     float xp = dot2_bf16(xv.x, ones_v, 0.0f);
     xp = dot2_bf16(xv.y, ones_v, xp);
     xp = dot2_bf16(xv.z, ones_v, xp);
@@ -457,10 +479,11 @@ __global__ __launch_bounds__(1024) __attribute__((amdgpu_waves_per_eu(8))) void 
   float y = 0.0f;
 #pragma unroll
   for (int u = 0; u < 16; ++u) y += (red[u][tid] + red[u][tid + 16]) + (red[u][tid + 32] + red[u][tid + 48]);
+  const size_t at = (size_t)token * a.h + 16 * blockIdx.x + tid;
   if (a.y_f32)
-    static_cast<float*>(a.y)[16 * blockIdx.x + tid] = y;
+    static_cast<float*>(a.y)[at] = y;
   else
-    static_cast<uint16_t*>(a.y)[16 * blockIdx.x + tid] = (uint16_t)f32_to_bf16_rne(y);
+    static_cast<uint16_t*>(a.y)[at] = (uint16_t)f32_to_bf16_rne(y);
 }
 
 // A barrier for LDS alone: loads from memory stay in flight across it.
@@ -639,7 +662,9 @@ __global__ __launch_bounds__(512) __attribute__((amdgpu_waves_per_eu(4))) void m
 #pragma unroll
         for (int u = 0; u < KP; ++u) v[b] += sh.red[4 * b + w + u][wave][l] + sh.red[4 * b + w + u][wave][l + 32];
       if constexpr (F == kGateUp) {
-        a.hidden[s * a.inter + 64 * tile + lane] = (uint16_t)f32_to_bf16_rne(silu_mul(v[0], v[1]));
+        const float f = silu_mul(v[0], v[1]);
+        if (a.t <= kFewTokens) store_hidden2(a, s * a.inter + 64 * tile + lane, f);
+        else a.hidden[s * a.inter + 64 * tile + lane] = (uint16_t)f32_to_bf16_rne(f);
       } else {
         float* const o = a.part + s * a.h + (DEEP ? 64 : 128) * tile + lane;
         o[0] = v[0];
@@ -709,12 +734,24 @@ __global__ __launch_bounds__(512) __attribute__((amdgpu_waves_per_eu(4))) void m
 __global__ __launch_bounds__(256) void moe_combine_kernel(MoeArgs a) {
   const int t = blockIdx.y, c = blockIdx.x * 1024 + threadIdx.x * 4;
   const float* const l = a.picked + (size_t)t * a.k;
+  const float* const part = a.part + (size_t)t * a.k * a.h + min(c, a.h - 4);
+  f32x4_t first[8];                      // on their way while the weights are formed
+#pragma unroll
+  for (int j = 0; j < 8; ++j)
+    first[j] = j < a.k ? *reinterpret_cast<const f32x4_t*>(part + (size_t)j * a.h) : f32x4_t{0.0f, 0.0f, 0.0f, 0.0f};
   const float total = moe_total(a, t, l);
   if (c >= a.h) return;
   f32x4_t y = {0.0f, 0.0f, 0.0f, 0.0f};
-  for (int j = 0; j < a.k; ++j) {
+#pragma unroll
+  for (int j = 0; j < 8; ++j) {
+    if (j >= a.k) continue;
     const float p = expf(l[j] - l[0]) / total;
-    const f32x4_t v = *reinterpret_cast<const f32x4_t*>(a.part + ((size_t)t * a.k + j) * a.h + c);
+#pragma unroll
+    for (int e = 0; e < 4; ++e) y[e] = __builtin_fmaf(p, first[j][e], y[e]);
+  }
+  for (int j = 8; j < a.k; ++j) {
+    const float p = expf(l[j] - l[0]) / total;
+    const f32x4_t v = *reinterpret_cast<const f32x4_t*>(part + (size_t)j * a.h);
 #pragma unroll
     for (int e = 0; e < 4; ++e) y[e] = __builtin_fmaf(p, v[e], y[e]);
   }
@@ -729,8 +766,9 @@ __global__ __launch_bounds__(256) void moe_combine_kernel(MoeArgs a) {
 static int64_t up256(int64_t n) { return (n + 255) & ~(int64_t)255; }
 
 int64_t moe_ws_bytes(int64_t t, int64_t h, int64_t e, int64_t inter, int64_t k) {
-  return up256(t * e * 4) + up256(t * k * 4) + up256(t * k * inter * (t == 1 ? 4 : 2)) + up256(t * k * h * 4) +
-         up256(e * 4) + up256(e * 256);
+  const bool few = t <= kFewTokens;
+  return up256(t * e * 4) + 2 * up256(t * k * 4) + up256(t * k * inter * (few ? 4 : 2)) +
+         (few ? 0 : up256(t * k * h * 4)) + up256(e * 4) + up256(e * 256);
 }
 
 hipError_t launch_moe_w4a16(const void* x, int t, int h, const void* router, int e, const void* gate_up,
@@ -751,15 +789,17 @@ hipError_t launch_moe_w4a16(const void* x, int t, int h, const void* router, int
   };
   a.logits = reinterpret_cast<float*>(take((int64_t)t * e * 4));
   a.picked = reinterpret_cast<float*>(take((int64_t)t * k * 4));
-  a.hidden = reinterpret_cast<uint16_t*>(take((int64_t)t * k * inter * (t == 1 ? 4 : 2)));
-  a.part = reinterpret_cast<float*>(take((int64_t)t * k * h * 4));
+  a.expert_of = reinterpret_cast<int32_t*>(take((int64_t)t * k * 4));
+  const bool few = t <= kFewTokens;
+  a.hidden = reinterpret_cast<uint16_t*>(take((int64_t)t * k * inter * (few ? 4 : 2)));
+  if (!few) a.part = reinterpret_cast<float*>(take((int64_t)t * k * h * 4));
   a.count = reinterpret_cast<int32_t*>(take((int64_t)e * 4));
   a.list = reinterpret_cast<int32_t*>(take((int64_t)e * 256));
   a.y = y, a.y_f32 = y_f32;
 
   hipError_t st = hipSuccess;
   auto ok = [&] { return (st = hipGetLastError()) == hipSuccess; };
-  if (t <= 4)
+  if (t <= 4)   // (its sums hold four tokens)
     hipLaunchKernelGGL(moe_router_gemv_kernel, dim3(e), dim3(256), 0, stream, a);
   else
     hipLaunchKernelGGL(moe_router_mfma_kernel, dim3((e + 15) / 16, (t + 15) / 16), dim3(1024), 0, stream, a);
@@ -767,7 +807,7 @@ hipError_t launch_moe_w4a16(const void* x, int t, int h, const void* router, int
   if (t == 1) {
     hipLaunchKernelGGL(moe_gate_up_one_kernel, dim3(inter / 32, k), dim3(1024), 0, stream, a);
     if (!ok()) return st;
-    hipLaunchKernelGGL(moe_down_one_kernel, dim3(h / 16), dim3(1024), 0, stream, a);
+    hipLaunchKernelGGL(moe_down_few_kernel, dim3(h / 16), dim3(1024), 0, stream, a);
     return hipGetLastError();
   }
   const int units = t * k < e ? t * k : e;
@@ -775,6 +815,10 @@ hipError_t launch_moe_w4a16(const void* x, int t, int h, const void* router, int
   if (!ok()) return st;
   hipLaunchKernelGGL((moe_expert_kernel<kGateUp>), dim3(inter / 64, units), dim3(512), 0, stream, a);
   if (!ok()) return st;
+  if (few) {
+    hipLaunchKernelGGL(moe_down_few_kernel, dim3(h / 16, t), dim3(1024), 0, stream, a);
+    return hipGetLastError();
+  }
   // Down in the deep form for up to 16 tokens (it holds one tile of them) and
   // up to a workgroup per CU (8 of 8 experts of 14336 x 4096
   // hit by 8 tokens, 256 workgroups: 150 us against 170 wide; 16 of 5888 x 1024,

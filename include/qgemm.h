@@ -479,9 +479,9 @@ int32_t qg_attn_kv8(const void *q, int64_t q_token_stride, int64_t q_head_stride
  *   p = softmax of l over the picked experts (renormalize not 0) or over all;
  *   y = sum over the picked e of p_e * down_e . (silu(gate_e x) * (up_e x)).
  * Each expert's products are qgemm_w4a16's on its weight; the hidden
- * activation is rounded to bf16 as the second product's operand (t = 1: kept as
- * the sum of two bf16), all sums, logits and weights are fp32; t > 1 adds the
- * picks in order of rank.
+ * activation is rounded to bf16 as the second product's operand (t <= 4: kept as
+ * the sum of two bf16), all sums, logits and weights are fp32; above 4 tokens
+ * the picks are added in order of rank.
  *   x        in : bf16 [t, h]          router in : bf16 [e, h]
  *   gate_up  in : e packed weights of 2 inter x h (quantize_int4_g32), one
  *                 after another: gate rows 0 .. inter - 1, then up rows
