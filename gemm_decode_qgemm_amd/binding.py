@@ -615,7 +615,7 @@ def attn_kv8(q: torch.Tensor, codes: torch.Tensor, scales: torch.Tensor, block_t
     rows, hq = shape[0], shape[1]
     most = _starts(cu, b, rows, max_q, dev)
     if max_len is None:
-        max_len = width * KV8_PAGE
+        max_len = min(width * KV8_PAGE, 2**31 - 1)
     if out is None:
         out = torch.empty_like(q, dtype=out_dtype, memory_format=torch.contiguous_format)
     if rows == 0:

@@ -26,6 +26,7 @@ namespace {
 
 constexpr int64_t kMaxRows = (int64_t)1 << 30;   // tokens, positions, lengths
 constexpr int64_t kMaxGrid = 65535;              // the y and z extents of a grid
+constexpr int64_t kMaxBlocks = ((int64_t)1 << 24) - 1;   // its x extent: below 2^32 threads at 256
 constexpr int32_t kMaxHeads = 4096;
 constexpr int32_t kMaxSplits = 256;
 constexpr int64_t kMaxDim = (int64_t)1 << 20;    // channels and hidden columns of an expert
@@ -49,6 +50,7 @@ int32_t check_cache(const void* codes, const void* scales, int64_t pages, int32_
   if (!codes || !scales || !table || !lens) return QG_E_NULL;
   if (pages < 1 || pages > 0x7fffffff || width < 1 || width > kMaxRows || b < 1 || b > kMaxGrid) return QG_E_SHAPE;
   if (hkv < 1 || hkv > kMaxHeads || !cache_d(d)) return QG_E_HEADS;
+  if (b * hkv > kMaxBlocks) return QG_E_SHAPE;
   if (!aligned(codes, 16) || !aligned(scales, 16) || !aligned(table, 4) || !aligned(lens, 4)) return QG_E_ALIGN;
   return QG_OK;
 }
@@ -69,7 +71,8 @@ qg::Kv8Args cache_args(const int8_t* codes, const float* scales, int64_t pages, 
 int32_t attn_shape(int64_t b, int64_t rows, int32_t hq, int32_t hkv, int32_t d, int64_t max_q, int64_t max_len,
                    int32_t window, int32_t splits, int* out) {
   if (b < 1 || b > kMaxGrid || rows < 0 || rows > kMaxRows || max_q < 1 || max_q > kMaxGrid || max_len < 0 ||
-      max_len > 0x7fffffff || window < 0)
+      max_len > 0x7fffffff || window < 0 ||
+      window > kMaxRows)
     return QG_E_SHAPE;
   if (hkv < 1 || hkv > kMaxHeads || hq < 1 || hq > kMaxHeads || hq % hkv != 0 || !cache_d(d)) return QG_E_HEADS;
   const int64_t per_head = max_q * (hq / hkv);
@@ -102,7 +105,7 @@ int32_t qg_qk_norm_rope(const void* q, int64_t q_ts, int64_t q_hs, const void* k
                         const float* cos_sin, int64_t max_pos, int32_t rot, int32_t adjacent_pairs,
                         const int32_t* positions, float eps, void* q_out, void* k_out, uint32_t* status_dev,
                         void* stream) {
-  if (tokens < 0 || tokens > kMaxRows || max_pos < 1 || max_pos > 0x7fffffff) return QG_E_SHAPE;
+  if (tokens < 0 || tokens > 4 * kMaxBlocks || max_pos < 1 || max_pos > 0x7fffffff) return QG_E_SHAPE;
   if (hq < 0 || hkv < 0 || hq > kMaxHeads || hkv > kMaxHeads || hq + hkv < 1) return QG_E_HEADS;
   if (d < 16 || d > 512 || d % 16 != 0 || rot < 0 || rot > d || rot % 16 != 0) return QG_E_HEADS;
   if (!(eps >= 0.0f) || std::isinf(eps)) return QG_E_SHAPE;

@@ -444,8 +444,8 @@ int32_t qg_kv8_read(const int8_t *codes, const float *scales, int64_t pages, int
 /* ---- qg_attn_kv8 ---------------------------------------------------------
  * Attention of every query row over its sequence in the cache:
  *   out[r, h] = sum_j softmax_j(scale * q[r, h] . k_j) v_j
- * over the tokens j <= p (the row's own token p) and, where window > 0,
- * j > p - window; head h of hq reads key/value head h / (hq / hkv).  A row
+ * over the tokens j <= p (the row's own token p) and, where window > 0 (up to
+ * 2^30), j > p - window; head h of hq reads key/value head h / (hq / hkv).  A row
  * that sees no token (length 0, or a row before token 0) is zero.  Softmax and
  * sums are fp32; the products' operands are fp16: q scaled by a power of two
  * per row, the codes (exact), and probability times value scale, rounded once

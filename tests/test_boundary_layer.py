@@ -22,7 +22,7 @@ def norm_rope(**kw):
 
 @pytest.mark.parametrize("kw,want", [
     (dict(q=None), E_NULL), (dict(k=None), E_NULL), (dict(qo=None), E_NULL), (dict(ko=None), E_NULL), (dict(pos=None), E_NULL),
-    (dict(cs=None), E_NULL), (dict(tokens=-1), E_SHAPE), (dict(tokens=1 << 31), E_SHAPE), (dict(max_pos=0), E_SHAPE),
+    (dict(cs=None), E_NULL), (dict(tokens=-1), E_SHAPE), (dict(tokens=1 << 31), E_SHAPE), (dict(tokens=(1 << 26) - 3), E_SHAPE), (dict(max_pos=0), E_SHAPE),
     (dict(eps=-1.0), E_SHAPE), (dict(eps=float("nan")), E_SHAPE), (dict(eps=float("inf")), E_SHAPE),
     (dict(hq=-1), E_HEADS), (dict(hq=0, hkv=0), E_HEADS), (dict(hq=5000), E_HEADS), (dict(d=120), E_HEADS), (dict(d=0), E_HEADS),
     (dict(d=528), E_HEADS), (dict(rot=24), E_HEADS), (dict(rot=144), E_HEADS), (dict(rot=-16), E_HEADS),
@@ -59,7 +59,7 @@ def attn(**kw):
 @pytest.mark.parametrize("kw,want", [
     (dict(codes=None), E_NULL), (dict(scales=None), E_NULL), (dict(table=None), E_NULL), (dict(lens=None), E_NULL),
     (dict(pages=0), E_SHAPE), (dict(pages=1 << 31), E_SHAPE), (dict(width=0), E_SHAPE), (dict(b=0), E_SHAPE), (dict(b=1 << 16), E_SHAPE),
-    (dict(hkv=0), E_HEADS), (dict(d=96), E_HEADS), (dict(d=320), E_HEADS),
+    (dict(b=65535, hkv=257), E_SHAPE), (dict(hkv=0), E_HEADS), (dict(d=96), E_HEADS), (dict(d=320), E_HEADS),
     (dict(codes=U), E_ALIGN), (dict(scales=U), E_ALIGN), (dict(table=A + 2), E_ALIGN), (dict(lens=A + 1), E_ALIGN)])
 def test_cache_refusals(call, kw, want):
     assert call(**kw) == want
@@ -83,7 +83,7 @@ def test_read_refusals(kw, want):
 
 @pytest.mark.parametrize("kw,want", [
     (dict(q=None), E_NULL), (dict(out=None), E_NULL), (dict(rows=5), E_SHAPE), (dict(max_q=0), E_SHAPE), (dict(max_q=70000), E_SHAPE),
-    (dict(max_len=-1), E_SHAPE), (dict(window=-1), E_SHAPE), (dict(scale=float("nan")), E_SHAPE), (dict(scale=float("inf")), E_SHAPE),
+    (dict(max_len=-1), E_SHAPE), (dict(window=-1), E_SHAPE), (dict(window=(1 << 30) + 1), E_SHAPE), (dict(scale=float("nan")), E_SHAPE), (dict(scale=float("inf")), E_SHAPE),
     (dict(hq=7), E_HEADS), (dict(hq=0), E_HEADS), (dict(dt=7), E_DTYPE), (dict(splits=-1), E_SPLIT), (dict(splits=257), E_SPLIT),
     (dict(splits=2), E_NULL), (dict(splits=2, ws=A, ws_bytes=2 * 4 * 8 * 130 * 4 - 1), E_BUF), (dict(ws=U), E_ALIGN),
     (dict(qts=64), E_STRIDE), (dict(qhs=12), E_STRIDE), (dict(q=U), E_ALIGN), (dict(out=U), E_ALIGN), (dict(status=A + 2), E_ALIGN),
