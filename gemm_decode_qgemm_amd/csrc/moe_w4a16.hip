@@ -44,6 +44,7 @@ struct MoeArgs {
   const uint8_t *gate_up, *down;
   size_t gate_up_bytes, down_bytes;   // per expert
   int t, h, e, inter, k, renorm;
+  int direct;                         // units of the expert launches: experts, with tokens or not
   float* logits;                      // [t, e]
   float* picked;                      // [t * k] logits in order of rank
   int32_t* count;                     // [e] tokens of an expert
@@ -626,10 +627,17 @@ __global__ __launch_bounds__(512) __attribute__((amdgpu_waves_per_eu(4))) void m
   };
   __shared__ __attribute__((aligned(16))) Shared sh;
   const int tid = threadIdx.x, lane = tid & 63, wave = wave_id_uniform();
-  int n;
-  const int expert = moe_active(a, blockIdx.y, n);
-  if (expert < 0) return;                    // uniform over the workgroup
-  const int pick = a.list[expert * 64 + min(lane, n - 1)];   // lane m: the expert's m-th pick
+  int n, expert, pick;                       // lane m of pick: the expert's m-th pick
+  if (a.direct) {
+    expert = blockIdx.y;
+    pick = a.list[expert * 64 + lane];
+    n = ((const __attribute__((address_space(4))) int*)a.count)[expert];
+    if (n == 0) return;                      // uniform over the workgroup
+  } else {
+    expert = moe_active(a, blockIdx.y, n);
+    if (expert < 0) return;
+    pick = a.list[expert * 64 + min(lane, n - 1)];
+  }
   const int blk = wave >> 2, tile = blockIdx.x;
   const int kdim = DOWN ? a.inter : a.h, kt_count = kdim >> 8;
   const int rb = F == kGateUp ? tile + blk * (a.inter >> 6) : DEEP ? tile : 2 * tile + blk;
@@ -810,7 +818,11 @@ hipError_t launch_moe_w4a16(const void* x, int t, int h, const void* router, int
     hipLaunchKernelGGL(moe_down_few_kernel, dim3(h / 16), dim3(1024), 0, stream, a);
     return hipGetLastError();
   }
-  const int units = t * k < e ? t * k : e;
+  // Units by experts once few of these are left without tokens: a workgroup then
+  // knows its expert without looking for it (17 tokens, 6 of 64 experts of 1024 x
+  // 2048: 56 us against 58.7; 16 tokens, 8 of 128: 66 against 63).
+  a.direct = 2 * t * k >= 3 * e;
+  const int units = a.direct || t * k > e ? e : t * k;
   hipLaunchKernelGGL(moe_route_kernel, dim3(e), dim3(512), 0, stream, a);
   if (!ok()) return st;
   hipLaunchKernelGGL((moe_expert_kernel<kGateUp>), dim3(inter / 64, units), dim3(512), 0, stream, a);
