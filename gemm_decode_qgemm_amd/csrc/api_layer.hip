@@ -12,9 +12,10 @@ hipError_t launch_qk_norm_rope(NormRopeArgs a, hipStream_t stream);
 hipError_t launch_kv8_append(const Kv8Args& c, const void* k, int64_t k_ts, int64_t k_hs, const void* v, int64_t v_ts,
                              int64_t v_hs, int64_t max_new, uint32_t* status, hipStream_t stream);
 hipError_t launch_kv8_read(const Kv8Args& c, int64_t max_len, void* k, void* v, int f32, hipStream_t stream);
-int attn_kv8_splits(int64_t b, int hkv, int64_t rows_per_head, int64_t max_len, int window, int64_t max_q);
+AttnSplit attn_kv8_split(int64_t b, int64_t rows, int hkv, int d, int64_t rows_per_head, int64_t max_len, int window,
+                         int64_t max_q);
 hipError_t launch_attn_kv8(const Kv8Args& c, const void* q, int64_t q_ts, int64_t q_hs, int hq, int max_q,
-                           int64_t max_len, int window, float scale, void* out, int out_f32, int splits, float* part,
+                           int64_t max_len, int window, float scale, void* out, int out_f32, AttnSplit by, float* part,
                            uint32_t* status, hipStream_t stream);
 int64_t moe_ws_bytes(int64_t t, int64_t h, int64_t e, int64_t inter, int64_t k);
 hipError_t launch_moe_w4a16(const void* x, int t, int h, const void* router, int e, const void* gate_up,
@@ -69,7 +70,7 @@ qg::Kv8Args cache_args(const int8_t* codes, const float* scales, int64_t pages, 
 
 // The shape rules of qg_attn_kv8 and the split it will use.
 int32_t attn_shape(int64_t b, int64_t rows, int32_t hq, int32_t hkv, int32_t d, int64_t max_q, int64_t max_len,
-                   int32_t window, int32_t splits, int* out) {
+                   int32_t window, int32_t splits, qg::AttnSplit* out) {
   if (b < 1 || b > kMaxGrid || rows < 0 || rows > kMaxRows || max_q < 1 || max_q > kMaxGrid || max_len < 0 ||
       max_len > 0x7fffffff || window < 0 ||
       window > kMaxRows)
@@ -78,12 +79,13 @@ int32_t attn_shape(int64_t b, int64_t rows, int32_t hq, int32_t hkv, int32_t d, 
   const int64_t per_head = max_q * (hq / hkv);
   if ((per_head + 15) / 16 * hkv > kMaxGrid) return QG_E_SHAPE;
   if (splits < 0 || splits > kMaxSplits) return QG_E_SPLIT;
-  *out = splits ? splits : qg::attn_kv8_splits(b, hkv, per_head, max_len, window, max_q);
+  *out = splits ? qg::AttnSplit{splits, 0} : qg::attn_kv8_split(b, rows, hkv, d, per_head, max_len, window, max_q);
   return QG_OK;
 }
 
-int64_t attn_ws(int64_t rows, int32_t hq, int32_t d, int splits) {
-  return splits > 1 ? (int64_t)splits * rows * hq * (d + 2) * 4 : 0;
+int64_t attn_ws(int64_t b, int64_t rows, int32_t hq, int32_t d, int64_t max_q, qg::AttnSplit by) {
+  if (by.slots > 0) return by.slots * max_q * hq * (d + 2) * 4 + b * 8;
+  return by.splits > 1 ? (int64_t)by.splits * rows * hq * (d + 2) * 4 : 0;
 }
 
 constexpr int64_t kMaxExperts = 512, kMaxPicks = 32;
@@ -168,9 +170,9 @@ int32_t qg_kv8_read(const int8_t* codes, const float* scales, int64_t pages, int
 
 int64_t qg_attn_kv8_workspace_bytes(int64_t b, int64_t rows, int32_t hq, int32_t hkv, int32_t d, int64_t max_q,
                                     int64_t max_len, int32_t window, int32_t splits) {
-  int s;
-  const int32_t st = attn_shape(b, rows, hq, hkv, d, max_q, max_len, window, splits, &s);
-  return st != QG_OK ? st : attn_ws(rows, hq, d, s);
+  qg::AttnSplit by;
+  const int32_t st = attn_shape(b, rows, hq, hkv, d, max_q, max_len, window, splits, &by);
+  return st != QG_OK ? st : attn_ws(b, rows, hq, d, max_q, by);
 }
 
 int32_t qg_attn_kv8(const void* q, int64_t q_ts, int64_t q_hs, int64_t rows, int32_t hq, const int8_t* codes,
@@ -181,8 +183,8 @@ int32_t qg_attn_kv8(const void* q, int64_t q_ts, int64_t q_hs, int64_t rows, int
   int32_t st = check_cache(codes, scales, pages, hkv, d, block_table, table_width, lens, b);
   if (st == QG_OK) st = check_rows(rows, cu, b);
   if (st != QG_OK) return st;
-  int s;
-  st = attn_shape(b, rows, hq, hkv, d, max_q, max_len, window, splits, &s);
+  qg::AttnSplit by;
+  st = attn_shape(b, rows, hq, hkv, d, max_q, max_len, window, splits, &by);
   if (st != QG_OK) return st;
   if (out_dtype != QG_BF16 && out_dtype != QG_F32) return QG_E_DTYPE;
   if (std::isnan(scale) || std::isinf(scale)) return QG_E_SHAPE;
@@ -190,11 +192,11 @@ int32_t qg_attn_kv8(const void* q, int64_t q_ts, int64_t q_hs, int64_t rows, int
   if (rows == 0) return QG_OK;
   if (!q || !out) return QG_E_NULL;
   if (!strides_ok(q_ts, q_hs, rows, hq, d)) return QG_E_STRIDE;
-  const int64_t need = attn_ws(rows, hq, d, s);
+  const int64_t need = attn_ws(b, rows, hq, d, max_q, by);
   if (need > 0 && (!ws || ws_bytes < need)) return ws ? QG_E_BUFFER : QG_E_NULL;
   const qg::Kv8Args c = cache_args(codes, scales, pages, hkv, d, block_table, table_width, lens, cu, rows, b);
   return hip_status(qg::launch_attn_kv8(c, q, q_ts, q_hs, hq, (int)max_q, max_len, window, scale, out,
-                                        out_dtype == QG_F32, s,
+                                        out_dtype == QG_F32, by,
                                         static_cast<float*>(ws), status_dev, static_cast<hipStream_t>(stream)));
 }
 

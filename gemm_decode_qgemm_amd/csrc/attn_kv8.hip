@@ -13,7 +13,7 @@
 //  * a code q becomes 1024 + (q + 128) by one byte permute a pair (0x6400 |
 //    byte), exactly.  Keys stay so: the accumulator starts at -1152 sum(q) of the
 //    row, and the rounding this costs (2^-24 of 1152 |sum q| against a score of
-//    some 40 sqrt(d) |q|) is below 2^-17 of the score.  Values, which are summed
+//    some 40 sqrt(d) |q|) is below 2^-15 of the score.  Values, which are summed
 //    over a whole cache, have the 1152 taken off again, exactly (packed add);
 //  * a query row is scaled by a power of two to a largest channel in [2^7,
 //    2^8), where its 8 significant bits fit exactly;
@@ -39,6 +39,8 @@
 // A workgroup's waves take pages in turn and join (m, l, O) through LDS; the
 // pages of a sequence are further split over workgroups when there are few,
 // the partial (m, l, O) joined by a second kernel in a fixed order.
+#include <algorithm>
+
 #include "layer_common.h"
 
 namespace qg {
@@ -52,7 +54,9 @@ struct AttnArgs {
   float scale_log2;                 // scale * log2(e)
   void* out;
   int out_f32;
-  float *part_o, *part_ml;          // [splits][rows * hq][d], [splits][rows * hq][2]
+  float *part_o, *part_ml;          // [splits][rows * hq][d], [splits][rows * hq][2]; balanced: see slots
+  int slots;                        // > 0: splits are shared out by length, [slots][max_q * hq] partial results
+  int32_t* plan;                    // then [b][2]: a sequence's first slot and their number
   uint32_t* status;
 };
 
@@ -114,8 +118,91 @@ typedef const __attribute__((address_space(4))) float* const_f32;
 
 constexpr float kNegInf = -__builtin_inff();
 constexpr int kMaxSplits = 256;   // a lane per split in the join
+// Waves of a workgroup, one page each at a time.  Eight instead of four halve
+// the partial results of a split, but fewer workgroups fit a CU (48 sequences of
+// 0..4095 tokens, 32 / 8 heads of 128: 48 us against 57 at 3 splits; 131071
+// tokens on one head: 19.6 against 19.9 at 256).
+constexpr int kWaves = 4;
 
-template <int D, int NT, int W>
+// Inclusive sum over the wave's lanes.
+__device__ __forceinline__ int wave_scan(int v) {
+  v += __builtin_amdgcn_update_dpp(0, v, 0x111, 0xf, 0xf, false);   // row_shr 1, 2, 4, 8
+  v += __builtin_amdgcn_update_dpp(0, v, 0x112, 0xf, 0xf, false);
+  v += __builtin_amdgcn_update_dpp(0, v, 0x114, 0xf, 0xf, false);
+  v += __builtin_amdgcn_update_dpp(0, v, 0x118, 0xf, 0xf, false);
+  v += __builtin_amdgcn_update_dpp(0, v, 0x142, 0xa, 0xf, false);   // row_bcast 15, 31
+  v += __builtin_amdgcn_update_dpp(0, v, 0x143, 0xc, 0xf, false);
+  return v;
+}
+
+// Pages that the rows of sequence s see: their number, and the first.
+__device__ __forceinline__ int pages_of(const AttnArgs& a, int s, int& first) {
+  const int len = a.c.lens[s];
+  int64_t r0, n;
+  kv8_rows(a.c.cu, a.c.rows, a.c.b, s, r0, n);
+  first = 0;
+  if (len <= 0 || n <= 0) return 0;
+  if (a.window > 0) {
+    const int64_t beg = len - n - a.window + 1;
+    first = beg > 0 ? (int)(beg / kPage) : 0;
+  }
+  return min((len - 1) / kPage, max((int)a.c.width, first)) - first + 1;   // (beyond the table: one page, missing)
+}
+
+// The sequence b that slot j works for, its share k of n and the pages it has.
+// Every wave works it out from the lengths alone: pages per slot C so that
+// sum ceil(pages / C) fits the slots, slots in order of the sequences.  Lane l
+// looks at the sequences per * l, ...  False: no work for the slot.
+__device__ __forceinline__ bool attn_plan(const AttnArgs& a, int j, bool tell, int& b, int& k, int& n) {
+  constexpr int kMost = 1 << 14;   // (a sum of such stays in range; longer is split in kMaxSplits anyway)
+  const int lane = threadIdx.x & 63, nb = a.c.b, per = (nb + 63) >> 6, mine = lane * per;
+  auto pages = [&](int s) {
+    int first;
+    return s < nb ? min(pages_of(a, s, first), kMost) : 0;
+  };
+  auto parts = [](int p, int c) { return min((int)((uint32_t)(p + c - 1) / (uint32_t)c), kMaxSplits); };
+  const int p0 = pages(mine);
+  int sum = p0;
+  for (int u = 1; u < per; ++u) sum += pages(mine + u);
+  const int total = __builtin_amdgcn_readlane(wave_scan(sum), 63);
+  const int busy = min(nb, per * (int)__popcll(__ballot(sum > 0)));
+  // each sequence leaves half a C of its last slot unused
+  const int room = a.slots - (busy >> 1);
+  int c = max(kWaves, (total + room - 1) / room), cnt, incl;
+  while (true) {
+    cnt = parts(p0, c);
+    for (int u = 1; u < per; ++u) cnt += parts(pages(mine + u), c);
+    incl = wave_scan(cnt);
+    if (__builtin_amdgcn_readlane(incl, 63) <= a.slots) break;   // at the latest when c is the longest: slots >= b
+    c += 1 + (c >> 4);
+  }
+  if (tell) {
+    int at = incl - cnt;
+    for (int u = 0; u < per && mine + u < nb; ++u) {
+      const int parts_u = parts(u == 0 ? p0 : pages(mine + u), c);
+      a.plan[2 * (mine + u)] = at;
+      a.plan[2 * (mine + u) + 1] = parts_u;
+      at += parts_u;
+    }
+  }
+  const uint64_t mask = __ballot(incl > j);
+  if (mask == 0) return false;
+  const int at = __builtin_ctzll(mask);
+  int base = __builtin_amdgcn_readlane(incl - cnt, at);
+  b = at * per;
+  n = parts(__builtin_amdgcn_readlane(p0, at), c);
+  while (j >= base + n) {          // within the lane's sequences, which hold slot j
+    base += n;
+    ++b;
+    n = parts(pages(b), c);
+  }
+  b = __builtin_amdgcn_readfirstlane(b);
+  n = __builtin_amdgcn_readfirstlane(n);
+  k = __builtin_amdgcn_readfirstlane(j - base);
+  return true;
+}
+
+template <int D, int NT, bool SHARED, int W = kWaves>   // SHARED: a.slots > 0
 __global__ __launch_bounds__(64 * W) void attn_kv8_kernel(AttnArgs a) {
   constexpr int KC = D / 64;        // 64-channel chunks of a key
   constexpr int DT = D / 16;        // 16-channel tiles of a value
@@ -126,12 +213,17 @@ __global__ __launch_bounds__(64 * W) void attn_kv8_kernel(AttnArgs a) {
   const int wave = wave_id_uniform();
   // Splits slowest: workgroups go to the 8 XCDs in turn, and the late splits
   // of short sequences, which are empty, must not all fall to the same ones.
-  const int h = blockIdx.x / a.row_tiles, rt = blockIdx.x % a.row_tiles, b = blockIdx.y, split = blockIdx.z;
+  const int h = blockIdx.x / a.row_tiles, rt = blockIdx.x % a.row_tiles;
+  int b = blockIdx.y, split = blockIdx.z, splits = a.splits;
+  if constexpr (SHARED) {
+    const bool tell = blockIdx.x == 0 && blockIdx.y == 0 && wave == 0;
+    if (!attn_plan(a, blockIdx.y, tell, b, split, splits)) return;
+  }
   const const_i32 trow = (const_i32)(a.c.table + (size_t)b * a.c.width);
   const int width = (int)a.c.width;
   // Without a window the first page does not depend on the length: its table
   // entry is on its way together with the length.
-  const int guess = (int)min((int64_t)split * a.chunk + wave, (int64_t)width - 1);
+  const int guess = SHARED ? 0 : (int)min((int64_t)split * a.chunk + wave, (int64_t)width - 1);
   const int guessed = trow[guess];
   const int len = max(((const_i32)a.c.lens)[b], 0);
   int64_t r0, n64;
@@ -151,17 +243,28 @@ __global__ __launch_bounds__(64 * W) void attn_kv8_kernel(AttnArgs a) {
     const int first = tok_beg / kPage;
     // a length beyond the table costs one page that is not there
     const int last = min((tok_end - 1) / kPage, width);
-    // `chunk` pages a split, the last one what is left: equal work for every
-    // workgroup whatever the lengths
-    p_beg = (int)min(first + (int64_t)split * a.chunk, (int64_t)last + 1);
-    p_end = split + 1 < a.splits ? (int)min((int64_t)p_beg + a.chunk, (int64_t)last + 1) : last + 1;
+    if constexpr (SHARED) {
+      // even shares of the pages that the whole sequence sees
+      int from;
+      const int all = pages_of(a, b, from), share = all / splits, more = all % splits;
+      const int beg = from + split * share + min(split, more);
+      p_beg = max(beg, first);
+      p_end = min(beg + share + (split < more ? 1 : 0), last + 1);
+    } else {
+      // `chunk` pages a split, the last one what is left: equal work for every
+      // workgroup whatever the lengths
+      p_beg = (int)min(first + (int64_t)split * a.chunk, (int64_t)last + 1);
+      p_end = split + 1 < splits ? (int)min((int64_t)p_beg + a.chunk, (int64_t)last + 1) : last + 1;
+    }
   }
+  // row t of the partial results
+  const size_t part0 = SHARED ? (size_t)blockIdx.y * a.max_q : (size_t)split * a.c.rows + r0;
 
-  if (p_beg >= p_end && a.splits > 1) {              // nothing here: say so to the join, and no more
+  if (p_beg >= p_end && splits > 1) {                // nothing here: say so to the join, and no more
     const int r = row0 + (int)threadIdx.x;
     if ((int)threadIdx.x < 16 * NT && r < nrows) {
       const int t = group_of(a, r), g = r - t * a.group;
-      float* const ml = a.part_ml + ((size_t)split * a.c.rows * a.hq + (r0 + t) * a.hq + h * a.group + g) * 2;
+      float* const ml = a.part_ml + ((part0 + t) * a.hq + h * a.group + g) * 2;
       ml[0] = kNegInf;
       ml[1] = 0.0f;
     }
@@ -391,6 +494,7 @@ __global__ __launch_bounds__(64 * W) void attn_kv8_kernel(AttnArgs a) {
     const int r = row0 + 16 * n + i;
     const int t = group_of(a, r), g = r - t * a.group;
     const int64_t row = (r0 + t) * a.hq + h * a.group + g;     // row of the output
+    const size_t prow = (part0 + t) * a.hq + h * a.group + g;
     const bool on = r < nrows;
     for (int dt = wave; dt < DT; dt += W) {
       f32x4_t v = sm_o[0][dt][lane];
@@ -401,9 +505,9 @@ __global__ __launch_bounds__(64 * W) void attn_kv8_kernel(AttnArgs a) {
       }
       if (!on) continue;
       const int d = 16 * dt + 4 * qd;
-      if (a.splits > 1) {
+      if (splits > 1) {
         if (mm != kNegInf || ll != 0.0f)
-          *reinterpret_cast<f32x4_t*>(a.part_o + ((size_t)split * a.c.rows * a.hq + row) * D + d) = v;
+          *reinterpret_cast<f32x4_t*>(a.part_o + prow * D + d) = v;
       } else {
         const float inv = ll == 0.0f ? 0.0f : 1.0f / ll;
         const f32x4_t y{v[0] * inv, v[1] * inv, v[2] * inv, v[3] * inv};
@@ -414,11 +518,27 @@ __global__ __launch_bounds__(64 * W) void attn_kv8_kernel(AttnArgs a) {
               u32x2_t{pack_bf16(y[0], y[1]), pack_bf16(y[2], y[3])};
       }
     }
-    if (a.splits > 1 && on && wave == 0 && qd == 0) {
-      float* const ml = a.part_ml + ((size_t)split * a.c.rows * a.hq + row) * 2;
+    if (splits > 1 && on && wave == 0 && qd == 0) {
+      float* const ml = a.part_ml + prow * 2;
       ml[0] = mm;
       ml[1] = ll;
     }
+  }
+}
+
+// Where the partial results of a row are: split s of head hd in row at(s, hd).
+struct JoinParts {
+  int n, hq;
+  size_t first, step;
+  __device__ __forceinline__ size_t at(int s, int hd) const { return (first + s * step) * hq + hd; }
+};
+template <bool SHARED>
+__device__ __forceinline__ JoinParts join_parts(const AttnArgs& a, int b, int64_t row, int t) {
+  if constexpr (SHARED) {
+    const const_i32 plan = (const_i32)(a.plan + 2 * (size_t)b);
+    return {plan[1], a.hq, (size_t)plan[0] * a.max_q + t, (size_t)a.max_q};
+  } else {
+    return {a.splits, a.hq, (size_t)row, (size_t)a.c.rows};
   }
 }
 
@@ -427,7 +547,7 @@ __global__ __launch_bounds__(64 * W) void attn_kv8_kernel(AttnArgs a) {
 // 32 groups of 8 lanes taking splits in turn, so that with many splits all
 // their loads are in flight at once.  Splits that saw nothing wrote no O and
 // are not read.
-template <int D>
+template <int D, bool SHARED>
 __global__ __launch_bounds__(256) void attn_kv8_join_kernel(AttnArgs a) {
   __shared__ float sm_f[kMaxSplits], sm_w[4], sm_l[4];
   __shared__ f32x4_t sm_o[32][8];
@@ -436,10 +556,12 @@ __global__ __launch_bounds__(256) void attn_kv8_join_kernel(AttnArgs a) {
   int64_t r0, n;
   kv8_rows(a.c.cu, a.c.rows, a.c.b, b, r0, n);
   if (t >= n) return;
-  const size_t total = (size_t)a.c.rows * a.hq, row = (size_t)(r0 + t) * a.hq + hd;
+  const JoinParts parts = join_parts<SHARED>(a, b, r0 + t, t);
+  if (SHARED && parts.n == 1) return;
+  const size_t row = (size_t)(r0 + t) * a.hq + hd;
   float m = kNegInf, l = 0.0f;
-  if (tid < a.splits) {
-    const float* const ml = a.part_ml + ((size_t)tid * total + row) * 2;
+  if (tid < parts.n) {
+    const float* const ml = a.part_ml + parts.at(tid, hd) * 2;
     m = ml[0];
     l = ml[1];
   }
@@ -459,13 +581,13 @@ __global__ __launch_bounds__(256) void attn_kv8_join_kernel(AttnArgs a) {
   ll = (sm_l[0] + sm_l[1]) + (sm_l[2] + sm_l[3]);
   const int g = tid >> 3, c = tid & 7;
   f32x4_t v = {0.0f, 0.0f, 0.0f, 0.0f};
-  const float* const po = a.part_o + row * D + d0 + 4 * c;
+  const float* const po = a.part_o + d0 + 4 * c;
 #pragma unroll
   for (int u = 0; u < kMaxSplits / 32; ++u) {
     const int s = g + 32 * u;
     const float w = sm_f[s];
     f32x4_t x = {0.0f, 0.0f, 0.0f, 0.0f};
-    if (s < a.splits && w != 0.0f) x = *reinterpret_cast<const f32x4_t*>(po + (size_t)s * total * D);
+    if (s < parts.n && w != 0.0f) x = *reinterpret_cast<const f32x4_t*>(po + parts.at(s, hd) * D);
 #pragma unroll
     for (int e = 0; e < 4; ++e) v[e] = __builtin_fmaf(w, x[e], v[e]);
   }
@@ -484,40 +606,49 @@ __global__ __launch_bounds__(256) void attn_kv8_join_kernel(AttnArgs a) {
 }
 
 // The same for few splits: a lane takes 4 channels of a row through all of
-// them, a workgroup 256 / (D / 4) heads.
+// them, 16 at a time, a workgroup 256 / (D / 4) heads.
+typedef float f32x2_t __attribute__((ext_vector_type(2)));
 constexpr int kFewSplits = 16;
-template <int D>
+template <int D, bool SHARED>
 __global__ __launch_bounds__(256) void attn_kv8_join_few_kernel(AttnArgs a) {
   constexpr int C = D / 4, R = 256 / C;
   const int g = threadIdx.x / C, c = threadIdx.x % C;
   const int b = blockIdx.z, t = blockIdx.y, hd = blockIdx.x * R + g;
-  int64_t r0, n;
-  kv8_rows(a.c.cu, a.c.rows, a.c.b, b, r0, n);
-  if (t >= n || g >= R || hd >= a.hq) return;
-  const size_t total = (size_t)a.c.rows * a.hq, row = (size_t)(r0 + t) * a.hq + hd;
-  float m[kFewSplits], l[kFewSplits], mm = kNegInf;
-#pragma unroll
-  for (int s = 0; s < kFewSplits; ++s) {
-    m[s] = kNegInf;
-    l[s] = 0.0f;
-    if (s < a.splits) {
-      const float* const ml = a.part_ml + (s * total + row) * 2;
-      m[s] = ml[0];
-      l[s] = ml[1];
-    }
-  }
-#pragma unroll
-  for (int s = 0; s < kFewSplits; ++s) mm = fmaxf(mm, m[s]);
+  int64_t r0, rows;
+  kv8_rows(a.c.cu, a.c.rows, a.c.b, b, r0, rows);
+  if (t >= rows) return;
+  const JoinParts parts = join_parts<SHARED>(a, b, r0 + t, t);
+  if (SHARED && parts.n == 1) return;          // written by the workgroup that did it all
+  if (g >= R || hd >= a.hq) return;
+  const size_t row = (size_t)(r0 + t) * a.hq + hd;
+  float mm = kNegInf, ll = 0.0f;
   f32x4_t y = {0.0f, 0.0f, 0.0f, 0.0f};
-  float ll = 0.0f;
+  for (int s0 = 0; s0 < parts.n; s0 += kFewSplits) {
+    f32x2_t ml[kFewSplits];
+    float top = mm;
 #pragma unroll
-  for (int s = 0; s < kFewSplits; ++s) {
-    const float f = mm == kNegInf ? 0.0f : __builtin_amdgcn_exp2f(m[s] - mm);
-    ll += mm == kNegInf ? l[s] : l[s] * f;    // nothing seen: 0, or NaN
-    f32x4_t x = {0.0f, 0.0f, 0.0f, 0.0f};
-    if (s < a.splits && f != 0.0f) x = *reinterpret_cast<const f32x4_t*>(a.part_o + (s * total + row) * D + 4 * c);
+    for (int s = 0; s < kFewSplits; ++s) {
+      ml[s] = f32x2_t{kNegInf, 0.0f};
+      if (s0 + s < parts.n) ml[s] = *reinterpret_cast<const f32x2_t*>(a.part_ml + parts.at(s0 + s, hd) * 2);
+    }
 #pragma unroll
-    for (int e = 0; e < 4; ++e) y[e] = __builtin_fmaf(f, x[e], y[e]);
+    for (int s = 0; s < kFewSplits; ++s) top = fmaxf(top, ml[s][0]);
+    const float base = top == kNegInf ? 0.0f : top, back = __builtin_amdgcn_exp2f(mm - base);
+    ll *= back;
+#pragma unroll
+    for (int e = 0; e < 4; ++e) y[e] *= back;
+#pragma unroll
+    for (int s = 0; s < kFewSplits; ++s) {
+      const float f = __builtin_amdgcn_exp2f(ml[s][0] - base);
+      ll += ml[s][1] * f;                      // (nothing seen: 0, or NaN)
+      f32x4_t x = {0.0f, 0.0f, 0.0f, 0.0f};
+      if (s0 + s < parts.n && f != 0.0f)
+        x = *reinterpret_cast<const f32x4_t*>(a.part_o + parts.at(s0 + s, hd) * D + 4 * c);
+#pragma unroll
+      for (int e = 0; e < 4; ++e) y[e] = __builtin_fmaf(f, x[e], y[e]);
+    }
+    mm = top;
+    if constexpr (!SHARED) break;              // (at most 16)
   }
   const float inv = ll == 0.0f ? 0.0f : 1.0f / ll;
 #pragma unroll
@@ -540,18 +671,12 @@ static int64_t seen_pages(int64_t max_len, int window, int64_t max_q) {
   return (seen + kPage - 1) / kPage;
 }
 
-// Waves of a workgroup, one page each at a time.  Eight instead of four halve
-// the partial results of a split, but fewer workgroups fit a CU (48 sequences of
-// 0..4095 tokens, 32 / 8 heads of 128: 48 us against 57 at 3 splits; 131071
-// tokens on one head: 19.6 against 19.9 at 256).
-constexpr int kWaves = 4;
-
 // Splits of a sequence's pages over workgroups: two workgroups per CU, a page
 // for every wave at most.  More pay for few long sequences only (8 of 32768 on
 // 8 heads: 91 us at 8, 89 at 12 and 16), fewer only where the lengths are equal
 // (32 of 4096 on 8 heads: 47 us at 1, 51 at 2; 48 of 0..4095: 49.8 at 1, 46.5 at 2
 // and 47 up to 8).
-int attn_kv8_splits(int64_t b, int hkv, int64_t rows_per_head, int64_t max_len, int window, int64_t max_q) {
+static int attn_splits(int64_t b, int hkv, int64_t rows_per_head, int64_t max_len, int window, int64_t max_q) {
   const int nt = attn_kv8_nt(rows_per_head);
   const int64_t units = b * hkv * ((rows_per_head + 16 * nt - 1) / (16 * nt));
   const int64_t pages = seen_pages(max_len, window, max_q);
@@ -561,36 +686,66 @@ int attn_kv8_splits(int64_t b, int hkv, int64_t rows_per_head, int64_t max_len, 
   return (int)(s < 1 ? 1 : s > kMaxSplits ? kMaxSplits : s);
 }
 
-template <int D, int NT>
+// How a call's pages are split: each sequence's in `splits`, or, where slots > 0,
+// over `slots` workgroups per head and row tile by the sequences' lengths, which
+// only the GPU knows.  Sharing out is for splits of many pages: a workgroup finds
+// its sequence first (about 1 us), and equal splits of up to four pages a wave
+// leave little to gain (1 sequence of 60000 tokens and 31 of 100..600, 32 / 8
+// heads of 128: 40 us against 416; 48 of 10..4095 in any order: 45 against 60;
+// 16 of 10..8192 on 64 / 8: 31 against 42; 32 equal ones of 4096: 52 against 50).
+// As many slots as workgroups are resident at once: with 2 a CU instead of 3 the
+// 48 take 52 us, with 4 they take 47.
+AttnSplit attn_kv8_split(int64_t b, int64_t rows, int hkv, int d, int64_t rows_per_head, int64_t max_len, int window,
+                         int64_t max_q) {
+  const int s = attn_splits(b, hkv, rows_per_head, max_len, window, max_q);
+  const int nt = attn_kv8_nt(rows_per_head);
+  const int64_t units = hkv * ((rows_per_head + 16 * nt - 1) / (16 * nt));
+  const int wide = d * nt, resident = wide <= 64 ? 4 : wide <= 128 ? 3 : wide <= 256 ? 2 : 1;   // per CU, by registers
+  const int64_t slots = std::max((resident * kCUs + units - 1) / units, b + b / 2);
+  if (b == 1 || max_q * b > 2 * rows || seen_pages(max_len, window, max_q) <= 4 * kWaves * s || slots > 65535)
+    return {s, 0};
+  return {1, (int)slots};
+}
+
+template <int D, int NT, bool SHARED>
 static hipError_t launch_attn_t(const AttnArgs& a, hipStream_t stream) {
-  constexpr int W = kWaves;
-  hipLaunchKernelGGL((attn_kv8_kernel<D, NT, W>), dim3(a.row_tiles * a.c.hkv, a.c.b, a.splits), dim3(64 * W), 0,
-                     stream, a);
+  const int x = a.row_tiles * a.c.hkv;
+  const dim3 grid = SHARED ? dim3(x, a.slots) : dim3(x, a.c.b, a.splits);
+  hipLaunchKernelGGL((attn_kv8_kernel<D, NT, SHARED>), grid, dim3(64 * kWaves), 0, stream, a);
   hipError_t e = hipGetLastError();
-  if (e != hipSuccess || a.splits == 1) return e;
+  if (e != hipSuccess || (!SHARED && a.splits == 1)) return e;
   constexpr int R = 256 / (D / 4);
-  if (a.splits <= kFewSplits)
-    hipLaunchKernelGGL((attn_kv8_join_few_kernel<D>), dim3((a.hq + R - 1) / R, a.max_q, a.c.b), dim3(256), 0, stream, a);
+  if (SHARED ? a.slots <= kFewSplits * a.c.b : a.splits <= kFewSplits)
+    hipLaunchKernelGGL((attn_kv8_join_few_kernel<D, SHARED>), dim3((a.hq + R - 1) / R, a.max_q, a.c.b), dim3(256), 0,
+                       stream, a);
   else
-    hipLaunchKernelGGL((attn_kv8_join_kernel<D>), dim3(a.hq * (D / 32), a.max_q, a.c.b), dim3(256), 0, stream, a);
+    hipLaunchKernelGGL((attn_kv8_join_kernel<D, SHARED>), dim3(a.hq * (D / 32), a.max_q, a.c.b), dim3(256), 0, stream,
+                       a);
   return hipGetLastError();
 }
 
 hipError_t launch_attn_kv8(const Kv8Args& c, const void* q, int64_t q_ts, int64_t q_hs, int hq, int max_q,
-                           int64_t max_len, int window, float scale, void* out, int out_f32, int splits, float* part,
+                           int64_t max_len, int window, float scale, void* out, int out_f32, AttnSplit by, float* part,
                            uint32_t* status, hipStream_t stream) {
   const int group = hq / c.hkv;
   const int64_t rows_per_head = (int64_t)max_q * group;
   const int nt = attn_kv8_nt(rows_per_head);
   const int64_t pages = seen_pages(max_len, window, max_q);
+  const int splits = by.splits;
   const int chunk = pages > splits ? (int)((pages + splits - 1) / splits) : 1;
   AttnArgs a{c, static_cast<const uint16_t*>(q), q_ts, q_hs, hq, group, max_q, window, splits, chunk,
              (int)((rows_per_head + 16 * nt - 1) / (16 * nt)), group > 1 ? (uint32_t)(((uint64_t)1 << 32) / group) : 0u,
              scale * 1.44269504088896340736f, out, out_f32,
-             part, part ? part + (size_t)splits * c.rows * hq * c.d : nullptr, status};
+             part, nullptr, by.slots, nullptr, status};
+  if (part) {
+    const size_t partial = (by.slots > 0 ? (size_t)by.slots * max_q : (size_t)splits * c.rows) * hq;
+    a.part_ml = part + partial * c.d;
+    a.plan = reinterpret_cast<int32_t*>(a.part_ml + partial * 2);
+  }
   switch (c.d * 4 + nt) {
 #define QG_ATTN(D, NT) \
-  case D * 4 + NT: return launch_attn_t<D, NT>(a, stream);
+  case D * 4 + NT:          \
+    return by.slots > 0 ? launch_attn_t<D, NT, true>(a, stream) : launch_attn_t<D, NT, false>(a, stream);
     QG_ATTN(64, 1) QG_ATTN(64, 2) QG_ATTN(128, 1) QG_ATTN(128, 2) QG_ATTN(192, 1) QG_ATTN(192, 2)
     QG_ATTN(256, 1) QG_ATTN(256, 2)
 #undef QG_ATTN

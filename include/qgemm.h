@@ -455,7 +455,7 @@ int32_t qg_kv8_read(const int8_t *codes, const float *scales, int64_t pages, int
  *   max_len  in : an upper bound of lens, for the choice of the split only
  *   out      out: [rows, hq, d], bf16 or fp32 (out_dtype)
  *   splits   in : workgroups that share a sequence's pages, 1..256; 0 lets
- *                 the library choose
+ *                 the library choose, by the sequences' lengths where that pays
  *   ws          : qg_attn_kv8_workspace_bytes(...) bytes, NULL allowed for 0
  *   status_dev  : QG_FLAG_PAGE; may be NULL
  * Rows are query tokens of decode: 1 for a step, a few for the verification of

@@ -137,3 +137,12 @@ def test_wrappers_refuse_host_tensors_and_wrong_types():
         qg.kv8_read(codes, scales, table, lens, 4)
     with pytest.raises(ValueError, match="device"):
         qg.attn_kv8(x, codes, scales, table, lens)
+
+
+def test_attn_workspace_of_shared_out_splits():
+    # 16 sequences on 8 heads, tables of 8192 tokens: 96 partial results a row and 8 bytes a sequence
+    assert qg.attn_kv8_workspace_bytes(16, 16, 32, 8, 128, 1, 8192) == 96 * 32 * 130 * 4 + 16 * 8
+    assert qg.attn_kv8_workspace_bytes(16, 16, 32, 8, 128, 1, 8192, splits=2) == 2 * 16 * 32 * 130 * 4
+    # few pages a split, or rows so ragged that their bound says little: equal splits
+    assert qg.attn_kv8_workspace_bytes(16, 16, 32, 8, 128, 1, 4096) == 4 * 16 * 32 * 130 * 4
+    assert qg.attn_kv8_workspace_bytes(16, 17, 32, 8, 128, 4, 8192) == 4 * 17 * 32 * 130 * 4

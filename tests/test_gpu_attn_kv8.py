@@ -207,3 +207,48 @@ def test_strided_queries_side_stream_and_graph(dev):
             g.replay()
             torch.cuda.synchronize()
             assert torch.equal(out, want)
+
+
+@pytest.mark.parametrize("b,hq,hkv,d,rows,long,width", [
+    (2, 8, 8, 64, 1, 8320, 520),        # a sequence in more splits than one trip of the join takes
+    (70, 8, 4, 64, 1, 2200, 41),        # more sequences than lanes of a wave
+    (5, 192, 16, 64, 2, 700, 113),      # two row tiles of a head at once
+    (3, 32, 32, 128, 3, 500, 97),
+    (33, 16, 8, 256, 1, 1300, 37),
+])
+@pytest.mark.parametrize("window", [0, 300])
+def test_one_long_sequence_among_short_ones(dev, b, hq, hkv, d, rows, long, width, window):
+    """Lengths far apart under a wide table: the splits are shared out by length."""
+    short = [0, 1, 63, 64, 65, 130, 17, 200]
+    lens = [short[i % len(short)] for i in range(b)]
+    lens[b // 2] = long
+    f = Filled(dev, lens, hkv, d, b + d, spare=width - -(-long // 64))
+    assert f.table.shape[1] == width
+    torch.manual_seed(b)
+    q = torch.randn(b * rows, hq, d).bfloat16()
+    want, mass = f.reference(ref.f64(q), [rows] * b, d ** -0.5, window)
+    need = qg.attn_kv8_workspace_bytes(b, b * rows, hq, hkv, d, rows, width * 64, window=window)
+    ws = torch.full((need + 16,), 255, dtype=torch.uint8, device=dev)
+    y = qg.attn_kv8(q.to(dev), *f.args, window=window, out_dtype=torch.float32, workspace=ws[:need])
+    check(y, want, mass)
+    assert (ws[need:] == 255).all()
+    assert torch.equal(y, qg.attn_kv8(q.to(dev), *f.args, window=window, out_dtype=torch.float32))
+    check(qg.attn_kv8(q.to(dev), *f.args, window=window), want, mass)
+
+
+def test_long_and_short_with_ragged_rows(dev):
+    lens, counts = [3, 900, 0, 64, 100, 2, 1500, 31] * 3, [2, 1, 2, 3, 0, 2, 3, 1] * 3
+    f = Filled(dev, lens, 8, 128, 5, spare=30)                  # 54 pages wide
+    torch.manual_seed(5)
+    q = torch.randn(sum(counts), 32, 128).bfloat16()
+    want, mass = f.reference(ref.f64(q), counts, 0.1, 0)
+    cu = cu_of(counts, dev)
+    y = qg.attn_kv8(q.to(dev), *f.args, cu=cu, max_q=3, scale=0.1)
+    check(y, want, mass)
+    graph, out, q = torch.cuda.CUDAGraph(), torch.empty_like(y), q.to(dev)
+    with torch.cuda.graph(graph):
+        qg.attn_kv8(q, *f.args, cu=cu, max_q=3, scale=0.1, out=out)
+    for _ in range(3):
+        out.zero_()
+        graph.replay()
+        assert torch.equal(out, y)
