@@ -613,7 +613,7 @@ __device__ __forceinline__ void moe_mx16(f32x4_t (&acc)[MT], const uint8_t* tile
 // 64 hidden columns, four waves each.  kDownWide: two neighbouring 64-row blocks
 // of the down matrix, four waves each.  kDownDeep: one block, four waves on each
 // half of K: twice the workgroups with half the work each, for grids that
-// would leave CUs idle otherwise (up to 16 tokens in all).
+// would leave CUs idle otherwise.
 enum MoeForm { kGateUp, kDownWide, kDownDeep };
 
 template <MoeForm F>
@@ -622,7 +622,7 @@ __global__ __launch_bounds__(512) __attribute__((amdgpu_waves_per_eu(4))) void m
   union Shared {
     MoeSlot slot[8];
     float red[8][4][64];
-    uint8_t x[2][2 * 8192];                  // deep: a half of K each; else one piece
+    uint8_t x[2][(DEEP ? 4 : 2) * 8192];     // deep: a half of K each; else one piece
     f32x4_t other[4][2][64];                 // results of the waves 4 .. 7
   };
   __shared__ __attribute__((aligned(16))) Shared sh;
@@ -714,8 +714,8 @@ __global__ __launch_bounds__(512) __attribute__((amdgpu_waves_per_eu(4))) void m
   const int steps = DEEP ? (kt_count + 1) >> 1 : kt_count;
   const int count = DEEP && blk == 1 ? kt_count - steps : steps;
   const int kt0 = DEEP && blk == 1 ? min(steps, kt_count - 1) : 0;
-  uint8_t* const xs = sh.x[DEEP ? blk : 0];    // 16 rows a buffer (deep), up to 32
-  if (DEEP || n <= 16) {                       // (deep: n <= t <= 16)
+  uint8_t* const xs = sh.x[DEEP ? blk : 0];    // two buffers of up to 32 rows
+  if (n <= 16) {
     f32x4_t acc[1] = {};
     const uint16_t* xr[512 / TH];
 #pragma unroll
@@ -724,16 +724,14 @@ __global__ __launch_bounds__(512) __attribute__((amdgpu_waves_per_eu(4))) void m
     const f32x4_t both[2] = {acc[0], acc[0]};
     finish(both, 1, 0);
   }
-  if constexpr (!DEEP) {
-    for (int m0 = n <= 16 ? n : 0; m0 < n; m0 += 32) {
-      f32x4_t acc[2] = {};
-      const uint16_t* xr[1024 / TH];
+  for (int m0 = n <= 16 ? n : 0; m0 < n; m0 += 32) {
+    f32x4_t acc[2] = {};
+    const uint16_t* xr[1024 / TH];
 #pragma unroll
-      for (int j = 0; j < 1024 / TH; ++j) xr[j] = source(m0 + row + TH / 32 * j);
-      if (m0 > 0) __syncthreads();             // the LDS of the tokens before is done with
-      moe_mx16<2, TH>(acc, tiles, t, kt0, count, steps, xr, th, xs);
-      finish(acc, 2, m0);
-    }
+    for (int j = 0; j < 1024 / TH; ++j) xr[j] = source(m0 + row + TH / 32 * j);
+    if (m0 > 0) __syncthreads();               // the LDS of the tokens before is done with
+    moe_mx16<2, TH>(acc, tiles, t, kt0, count, steps, xr, th, xs);
+    finish(acc, 2, m0);
   }
 }
 
@@ -831,12 +829,14 @@ hipError_t launch_moe_w4a16(const void* x, int t, int h, const void* router, int
     hipLaunchKernelGGL(moe_down_few_kernel, dim3(h / 16, t), dim3(1024), 0, stream, a);
     return hipGetLastError();
   }
-  // Down in the deep form for up to 16 tokens (it holds one tile of them) and
-  // up to a workgroup per CU (8 of 8 experts of 14336 x 4096
-  // hit by 8 tokens, 256 workgroups: 150 us against 170 wide; 16 of 5888 x 1024,
-  // 128: 47 against 56); above it the wide form copies each activation row for
-  // twice the weight rows (128 experts of 768 x 2048: 64 us against 71 deep).
-  if (t <= 16 && h / 128 * units <= kCUs)
+  // Down in the deep form up to one and a half workgroups per CU, whose second
+  // half of the slots the wide form would leave empty (8 of 8 experts of 14336 x 4096
+  // hit by 8 tokens, 256 wide workgroups: 150 us against 170 wide; 31 tokens on 8
+  // of 6912 x 2048, 128: 64 against 74; 54 on 16 of 6400 x 2560, 320: 134 against 141);
+  // above it the wide form copies each activation row for twice the weight rows (60
+  // on 16 of 3328 x 4096, 512: 121 us against 129 deep; 16 on 128 of 768 x 2048: 64
+  // against 71).
+  if (2 * (h / 128) * units <= 3 * kCUs)
     hipLaunchKernelGGL((moe_expert_kernel<kDownDeep>), dim3(h / 64, units), dim3(512), 0, stream, a);
   else
     hipLaunchKernelGGL((moe_expert_kernel<kDownWide>), dim3(h / 128, units), dim3(512), 0, stream, a);

@@ -95,6 +95,20 @@ def test_all_tokens_on_the_same_experts(dev):
     case(dev, 3, e, 2, h, 256, False, 0, x=x[:3], router=router)
 
 
+@pytest.mark.parametrize("t,k,same", [(17, 3, False), (64, 4, False), (64, 2, True), (5, 10, False)])
+def test_many_row_blocks_and_experts(dev, t, k, same):
+    """50 experts with 8 pairs of row blocks each in the down product: more than
+    the workgroups that halves of K are for; 64 tokens of one expert among them."""
+    e, h, inter = 50, 1024, 256
+    g = torch.Generator().manual_seed(t)
+    x = (torch.randn(t, h, generator=g) * 0.2 + 1).bfloat16() if same else None
+    router = None
+    if same:
+        router = torch.zeros(e, h).bfloat16()
+        router[31], router[7] = 0.02, 0.01
+    case(dev, t, e, k, h, inter, True, t, x=x, router=router)
+
+
 def test_ties_go_to_the_lowest_index(dev):
     """Equal logits everywhere: the first k experts, with equal weights."""
     e, h = 16, 256
