@@ -1,7 +1,7 @@
 """qg_attn_kv8 against attention in 64 bits over the cache's values.
 
 Tolerance per output, with A = sum of p |v| in 64 bits: the products' operands
-round p * scale to bf16 (2^-8 of each term at most), scores carry binary32
+hold p * scale in 8 bits or more (2^-8 of each term at most), scores carry binary32
 rounding (below 2^-12 of p for these inputs: 256 products of magnitude about
 10 in all), so |err| <= (2^-8 + 2^-11) A, plus half a bf16 unit where the
 output is bf16."""
