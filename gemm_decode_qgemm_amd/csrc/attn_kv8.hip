@@ -135,11 +135,8 @@ __device__ __forceinline__ int wave_scan(int v) {
   return v;
 }
 
-// Pages that the rows of sequence s see: their number, and the first.
-__device__ __forceinline__ int pages_of(const AttnArgs& a, int s, int& first) {
-  const int len = a.c.lens[s];
-  int64_t r0, n;
-  kv8_rows(a.c.cu, a.c.rows, a.c.b, s, r0, n);
+// Pages that the n rows of a sequence of len tokens see: their number, and the first.
+__device__ __forceinline__ int pages_of(const AttnArgs& a, int len, int64_t n, int& first) {
   first = 0;
   if (len <= 0 || n <= 0) return 0;
   if (a.window > 0) {
@@ -153,17 +150,20 @@ __device__ __forceinline__ int pages_of(const AttnArgs& a, int s, int& first) {
 // Every wave works it out from the lengths alone: pages per slot C so that
 // sum ceil(pages / C) fits the slots, slots in order of the sequences.  Lane l
 // looks at the sequences per * l, ...  False: no work for the slot.
-__device__ __forceinline__ bool attn_plan(const AttnArgs& a, int j, bool tell, int& b, int& k, int& n) {
+__device__ __forceinline__ bool attn_plan(const AttnArgs& a, int j, bool tell, int& b, int& k, int& n, int& len) {
   constexpr int kMost = 1 << 14;   // (a sum of such stays in range; longer is split in kMaxSplits anyway)
   const int lane = threadIdx.x & 63, nb = a.c.b, per = (nb + 63) >> 6, mine = lane * per;
-  auto pages = [&](int s) {
+  auto pages = [&](int s, int tokens) {
+    int64_t r0, rows;
     int first;
-    return s < nb ? min(pages_of(a, s, first), kMost) : 0;
+    kv8_rows(a.c.cu, a.c.rows, nb, s, r0, rows);
+    return min(pages_of(a, tokens, rows, first), kMost);
   };
+  auto more = [&](int u) { return mine + u < nb ? pages(mine + u, a.c.lens[mine + u]) : 0; };
   auto parts = [](int p, int c) { return min((int)((uint32_t)(p + c - 1) / (uint32_t)c), kMaxSplits); };
-  const int p0 = pages(mine);
+  const int len0 = mine < nb ? a.c.lens[mine] : 0, p0 = mine < nb ? pages(mine, len0) : 0;
   int sum = p0;
-  for (int u = 1; u < per; ++u) sum += pages(mine + u);
+  for (int u = 1; u < per; ++u) sum += more(u);
   const int total = __builtin_amdgcn_readlane(wave_scan(sum), 63);
   const int busy = min(nb, per * (int)__popcll(__ballot(sum > 0)));
   // each sequence leaves half a C of its last slot unused
@@ -171,7 +171,7 @@ __device__ __forceinline__ bool attn_plan(const AttnArgs& a, int j, bool tell, i
   int c = max(kWaves, (total + room - 1) / room), cnt, incl;
   while (true) {
     cnt = parts(p0, c);
-    for (int u = 1; u < per; ++u) cnt += parts(pages(mine + u), c);
+    for (int u = 1; u < per; ++u) cnt += parts(more(u), c);
     incl = wave_scan(cnt);
     if (__builtin_amdgcn_readlane(incl, 63) <= a.slots) break;   // at the latest when c is the longest: slots >= b
     c += 1 + (c >> 4);
@@ -179,7 +179,7 @@ __device__ __forceinline__ bool attn_plan(const AttnArgs& a, int j, bool tell, i
   if (tell) {
     int at = incl - cnt;
     for (int u = 0; u < per && mine + u < nb; ++u) {
-      const int parts_u = parts(u == 0 ? p0 : pages(mine + u), c);
+      const int parts_u = parts(u == 0 ? p0 : more(u), c);
       a.plan[2 * (mine + u)] = at;
       a.plan[2 * (mine + u) + 1] = parts_u;
       at += parts_u;
@@ -190,11 +190,12 @@ __device__ __forceinline__ bool attn_plan(const AttnArgs& a, int j, bool tell, i
   const int at = __builtin_ctzll(mask);
   int base = __builtin_amdgcn_readlane(incl - cnt, at);
   b = at * per;
+  len = __builtin_amdgcn_readlane(len0, at);
   n = parts(__builtin_amdgcn_readlane(p0, at), c);
   while (j >= base + n) {          // within the lane's sequences, which hold slot j
     base += n;
-    ++b;
-    n = parts(pages(b), c);
+    len = ((const_i32)a.c.lens)[++b];
+    n = parts(pages(b, len), c);
   }
   b = __builtin_amdgcn_readfirstlane(b);
   n = __builtin_amdgcn_readfirstlane(n);
@@ -214,10 +215,10 @@ __global__ __launch_bounds__(64 * W) void attn_kv8_kernel(AttnArgs a) {
   // Splits slowest: workgroups go to the 8 XCDs in turn, and the late splits
   // of short sequences, which are empty, must not all fall to the same ones.
   const int h = blockIdx.x / a.row_tiles, rt = blockIdx.x % a.row_tiles;
-  int b = blockIdx.y, split = blockIdx.z, splits = a.splits;
+  int b = blockIdx.y, split = blockIdx.z, splits = a.splits, len;
   if constexpr (SHARED) {
     const bool tell = blockIdx.x == 0 && blockIdx.y == 0 && wave == 0;
-    if (!attn_plan(a, blockIdx.y, tell, b, split, splits)) return;
+    if (!attn_plan(a, blockIdx.y, tell, b, split, splits, len)) return;
   }
   const const_i32 trow = (const_i32)(a.c.table + (size_t)b * a.c.width);
   const int width = (int)a.c.width;
@@ -225,7 +226,8 @@ __global__ __launch_bounds__(64 * W) void attn_kv8_kernel(AttnArgs a) {
   // entry is on its way together with the length.
   const int guess = SHARED ? 0 : (int)min((int64_t)split * a.chunk + wave, (int64_t)width - 1);
   const int guessed = trow[guess];
-  const int len = max(((const_i32)a.c.lens)[b], 0);
+  if constexpr (!SHARED) len = ((const_i32)a.c.lens)[b];
+  len = max(len, 0);
   int64_t r0, n64;
   kv8_rows(a.c.cu, a.c.rows, a.c.b, b, r0, n64);
   const int nq = (int)(n64 < a.max_q ? n64 : a.max_q);
@@ -246,7 +248,7 @@ __global__ __launch_bounds__(64 * W) void attn_kv8_kernel(AttnArgs a) {
     if constexpr (SHARED) {
       // even shares of the pages that the whole sequence sees
       int from;
-      const int all = pages_of(a, b, from), share = all / splits, more = all % splits;
+      const int all = pages_of(a, len, n64, from), share = all / splits, more = all % splits;
       const int beg = from + split * share + min(split, more);
       p_beg = max(beg, first);
       p_end = min(beg + share + (split < more ? 1 : 0), last + 1);
