@@ -12,18 +12,18 @@
 //
 // Launches, with no atomics between workgroups (bit-identical repeats):
 //   router      logits in fp32
-//   route       above one token: the tokens of every expert
+//   route       the tokens of every expert; up to 8 tokens the next launch
+//               finds them itself while its workgroups all run at once
 //   gate and up the two products of a few hidden columns of one expert, and
 //               silu(g) u of its tokens
 //   down        up to 4 tokens: the weighted sum over a token's picks; above: fp32
 //               results per (token, pick)
 //   combine     above 4 tokens: the weighted sum, in order of rank
 // The rank of expert e for a token is the number of experts before it, so "which
-// tokens picked e" takes one ballot per 64 experts and token, and a token's pick
-// number is that rank.  For one token each workgroup of the gate and up launch
-// ranks the logits itself (a few KB), which is a launch less; with more, or with
-// more tokens, that work costs more than the launch (4 tokens, 6 of 160 experts of
-// 768 x 2048: 46 us of which half was ranking).
+// tokens picked e" takes one ballot per 64 experts and token (route), and a token's
+// pick number is that rank.  A workgroup that ranks by itself takes the largest
+// logit left, once per pick; for one token it compares all of them at once in LDS,
+// with 16 waves (1 token, 8 of 128 experts of 768 x 2048: 15.9 us against 17.5).
 //
 // Two forms of the product:
 //  * one to 4 tokens of an expert: the 4x4x4 sixteen-block matrix instruction
@@ -54,6 +54,7 @@ struct MoeArgs {
   size_t gate_up_bytes, down_bytes;   // per expert
   int t, h, e, inter, k, renorm;
   int direct;                         // units of the expert launches: experts, with tokens or not
+  int own;                            // gate and up ranks the logits itself: no lists
   float* logits;                      // [t, e]
   float* picked;                      // [t * k] logits in order of rank
   int32_t* count;                     // [e] tokens of an expert
@@ -136,6 +137,18 @@ __global__ __launch_bounds__(1024) void moe_router_mfma_kernel(MoeArgs a) {
 
 // ---- routing -------------------------------------------------------------------
 
+// The largest of the wave's 64 values.
+__device__ __forceinline__ uint32_t wave_max(uint32_t v) {
+  auto step = [&](uint32_t o) { v = max(v, o); };
+  step((uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, 0x111, 0xf, 0xf, false));   // row_shr 1, 2, 4, 8
+  step((uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, 0x112, 0xf, 0xf, false));
+  step((uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, 0x114, 0xf, 0xf, false));
+  step((uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, 0x118, 0xf, 0xf, false));
+  step((uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, 0x142, 0xa, 0xf, false));   // row_bcast 15, 31
+  step((uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, 0x143, 0xc, 0xf, false));
+  return (uint32_t)__builtin_amdgcn_readlane((int)v, 63);
+}
+
 // A logit as an unsigned number of the same order; NaN is above all, -0 is 0.
 __device__ __forceinline__ uint32_t order_key(float l) {
   l += 0.0f;
@@ -175,7 +188,36 @@ __device__ int moe_plan(const MoeArgs& a, int want, MoePlan& p) {
   return __builtin_amdgcn_readfirstlane(p.expert);
 }
 
-// Above one token: a workgroup per expert ranks it for every token.
+// The first `upto` experts of token t in order of rank, by a wave: take(rank,
+// expert).  A round is the largest key of the wave, then the lowest expert that
+// has it (about 50 ns).
+template <class Take>
+__device__ __forceinline__ void moe_top(const MoeArgs& a, int t, int upto, Take take) {
+  const int lane = threadIdx.x & 63;
+  uint32_t key[8];                   // of expert 64 u + lane; no logit's key is 0
+#pragma unroll
+  for (int u = 0; u < 8; ++u) key[u] = 64 * u + lane < a.e ? order_key(a.logits[(size_t)t * a.e + 64 * u + lane]) : 0u;
+  for (int j = 0; j < upto; ++j) {
+    uint32_t m = 0u;
+#pragma unroll
+    for (int u = 0; u < 8; ++u) m = max(m, key[u]);
+    m = wave_max(m);
+    int at = -1;
+#pragma unroll
+    for (int u = 0; u < 8; ++u) {
+      if (64 * u >= a.e || at >= 0) continue;    // uniform
+      const uint64_t has = __ballot(key[u] == m);
+      if (has == 0) continue;
+      const int l = __builtin_ctzll(has);
+      at = 64 * u + l;
+      if (lane == l) key[u] = 0u;
+    }
+    take(j, at);
+  }
+}
+
+// Above one token, unless the gate and up launch does it: a workgroup per expert
+// ranks it for every token.
 __global__ __launch_bounds__(512) void moe_route_kernel(MoeArgs a) {
   __shared__ int rank[64];
   const int tid = threadIdx.x, lane = tid & 63, wave = wave_id_uniform();
@@ -217,7 +259,7 @@ __global__ __launch_bounds__(512) void moe_route_kernel(MoeArgs a) {
   }
 }
 
-// The expert of a unit above one token: the unit-th that has tokens, or -1.
+// The expert of a unit after the route launch: the unit-th that has tokens, or -1.
 __device__ __forceinline__ int moe_active(const MoeArgs& a, int unit, int& n) {
   const int lane = threadIdx.x & 63;
   int cnt[8], expert = -1, seen = 0;
@@ -236,6 +278,42 @@ __device__ __forceinline__ int moe_active(const MoeArgs& a, int unit, int& n) {
     }
     seen += __popcll(mask);
   }
+  return expert;
+}
+
+// Where the workgroups of the gate and up launch rank the logits themselves: of[u]
+// is the expert of slot 64 u + lane (t k + rank).  The expert of a unit and its
+// picks (lane m: the m-th, the last one past it), or -1: units are experts
+// (direct), or slots, of which the first with its expert works for all.
+constexpr int kOwnTokens = 8;
+constexpr int kOwnSlots = kOwnTokens * 32 / 64;
+
+__device__ __forceinline__ int moe_own(const MoeArgs& a, const int (&of)[kOwnSlots], int unit, int* list, int& n,
+                                       int& pick) {
+  const int lane = threadIdx.x & 63;
+  int expert = unit;
+  if (!a.direct) {
+#pragma unroll
+    for (int u = 0; u < kOwnSlots; ++u)
+      if (unit >> 6 == u) expert = __builtin_amdgcn_readlane(of[u], unit & 63);
+  }
+  n = 0;
+  int first = -1;
+#pragma unroll
+  for (int u = 0; u < kOwnSlots; ++u) {
+    const bool mine = of[u] == expert;
+    const uint64_t mask = __ballot(mine);
+    if (mask == 0) continue;
+    if (first < 0) first = 64 * u + __builtin_ctzll(mask);
+    if (mine) list[n + __popcll(mask & (((uint64_t)1 << lane) - 1))] = 64 * u + lane;
+    n += __popcll(mask);
+  }
+  if (n == 0 || (!a.direct && first != unit)) return -1;
+  // wave-private: a wave's LDS operations complete in order
+  __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
+  __builtin_amdgcn_wave_barrier();
+  __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
+  pick = list[min(lane, n - 1)];
   return expert;
 }
 
@@ -635,19 +713,41 @@ __global__ __launch_bounds__(512) __attribute__((amdgpu_waves_per_eu(4))) void m
     f32x4_t other[4][2][64];                 // results of the waves 4 .. 7
   };
   __shared__ __attribute__((aligned(16))) Shared sh;
-  const int tid = threadIdx.x, lane = tid & 63, wave = wave_id_uniform();
+  const int tid = threadIdx.x, lane = tid & 63, wave = wave_id_uniform(), tile = blockIdx.x;
+  __shared__ int slots[kOwnSlots * 64], lists[8][kOwnTokens];
   int n, expert, pick;                       // lane m of pick: the expert's m-th pick
-  if (a.direct) {
+  if (a.own) {
+    const int count = a.t * a.k;
+    if constexpr (F == kGateUp) {
+      if (wave < a.t) {
+        const bool tell = tile == 0 && blockIdx.y == 0;
+        moe_top(a, wave, a.k, [&](int j, int at) {
+          if (lane != 0) return;
+          slots[wave * a.k + j] = at;
+          if (!tell) return;
+          a.expert_of[wave * a.k + j] = at;
+          a.picked[wave * a.k + j] = a.logits[(size_t)wave * a.e + at];
+        });
+      }
+      __syncthreads();
+    }
+    int of[kOwnSlots];
+#pragma unroll
+    for (int u = 0; u < kOwnSlots; ++u)
+      of[u] = 64 * u + lane >= count ? -1 : F == kGateUp ? slots[64 * u + lane] : a.expert_of[64 * u + lane];
+    expert = moe_own(a, of, blockIdx.y, lists[wave], n, pick);
+    if (expert < 0) return;                  // uniform over the workgroup
+  } else if (a.direct) {
     expert = blockIdx.y;
     pick = a.list[expert * 64 + lane];
     n = ((const __attribute__((address_space(4))) int*)a.count)[expert];
-    if (n == 0) return;                      // uniform over the workgroup
+    if (n == 0) return;
   } else {
     expert = moe_active(a, blockIdx.y, n);
     if (expert < 0) return;
     pick = a.list[expert * 64 + min(lane, n - 1)];
   }
-  const int blk = wave >> 2, tile = blockIdx.x;
+  const int blk = wave >> 2;
   const int kdim = DOWN ? a.inter : a.h, kt_count = kdim >> 8;
   const int rb = F == kGateUp ? tile + blk * (a.inter >> 6) : DEEP ? tile : 2 * tile + blk;
   const uint8_t* const tiles = (DOWN ? a.down + expert * a.down_bytes : a.gate_up + expert * a.gate_up_bytes) +
@@ -829,9 +929,16 @@ hipError_t launch_moe_w4a16(const void* x, int t, int h, const void* router, int
   // knows its expert without looking for it (17 tokens, 6 of 64 experts of 1024 x
   // 2048: 56 us against 58.7; 16 tokens, 8 of 128: 66 against 63).
   a.direct = 2 * t * k >= 3 * e;
-  const int units = a.direct || t * k > e ? e : t * k;
-  hipLaunchKernelGGL(moe_route_kernel, dim3(e), dim3(512), 0, stream, a);
-  if (!ok()) return st;
+  // Up to kOwnTokens tokens, ranking takes a workgroup of the gate and up launch about
+  // 1 us, which is less than a launch while all of them run at once (4 tokens, 2 of 8
+  // of 3840 x 1024, 480 workgroups: 20.2 us against 22.6; 7 tokens, 8 of 128 of 768 x
+  // 4096, 672: 82 against 78; 5, 4 of 16 of 10496 x 2048, 2624: 112 against 102).
+  a.own = t <= kOwnTokens && (inter / 64) * (a.direct ? e : t * k) <= 2 * kCUs;
+  const int units = a.direct || (!a.own && t * k > e) ? e : t * k;
+  if (!a.own) {
+    hipLaunchKernelGGL(moe_route_kernel, dim3(e), dim3(512), 0, stream, a);
+    if (!ok()) return st;
+  }
   hipLaunchKernelGGL((moe_expert_kernel<kGateUp>), dim3(inter / 64, units), dim3(512), 0, stream, a);
   if (!ok()) return st;
   if (few) {

@@ -109,6 +109,27 @@ def test_many_row_blocks_and_experts(dev, t, k, same):
     case(dev, t, e, k, h, inter, True, t, x=x, router=router)
 
 
+@pytest.mark.parametrize("t,k", [(2, 30), (3, 17), (4, 16), (4, 20), (5, 10), (7, 11), (8, 7), (8, 32)])
+def test_few_tokens_on_many_workgroups(dev, t, k):
+    """Up to 8 tokens with more gate and up workgroups than run at once."""
+    case(dev, t, 50, k, 256, 768, t & 1 == 0, t + k, (torch.bfloat16,))
+
+
+@pytest.mark.parametrize("e,k", [(512, 32), (300, 5), (65, 3)])
+@pytest.mark.parametrize("t", [2, 8])
+def test_few_tokens_of_many_experts(dev, t, e, k):
+    """Routing alone: every expert one tile, its weights those of expert e % 8."""
+    h = inter = 256
+    gu, dn, gu_v, dn_v = experts(8, h, inter, 77)
+    which = [i % 8 for i in range(e)]
+    g = torch.Generator().manual_seed(e + t)
+    x = torch.randn(t, h, generator=g).bfloat16()
+    router = (torch.randn(e, h, generator=g) * 2 * h ** -0.5).bfloat16()
+    want, bound = ref.moe(ref.f64(x), ref.f64(router), [gu_v[i] for i in which], [dn_v[i] for i in which], inter, k, True)
+    y = qg.moe_w4a16(x.to(dev), router.to(dev), gu[which].to(dev), dn[which].to(dev), inter, k, out_dtype=torch.float32)
+    check(y, want, bound)
+
+
 def test_ties_go_to_the_lowest_index(dev):
     """Equal logits everywhere: the first k experts, with equal weights."""
     e, h = 16, 256
