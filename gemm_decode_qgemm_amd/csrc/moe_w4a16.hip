@@ -36,11 +36,13 @@
 // The least a call can do is read the weights of the experts that were picked, 37/64
 // byte each.  Measured, whole layer: 1 token, 8 of 128 experts of 768 x 2048, 15.9 us
 // (three launches that wait for each other; 3.4 us of bytes); 1 token, 2 of 8 of
-// 14336 x 4096, 46 us (4.4 TB/s); 17 tokens, 6 of 64 of 1024 x 2048, 56 us (3.4 TB/s:
-// 15 us of it the small launches, the rest short columns of K); 64 tokens, 2 of 8 of
+// 14336 x 4096, 46 us (4.4 TB/s); 17 tokens, 6 of 64 of 1024 x 2048, 50.5 us (3.7 TB/s:
+// 12 us of it the small launches, the rest short columns of K); 64 tokens, 2 of 8 of
 // 14336 x 4096, 222 us (3.7 TB/s): there the vector instructions that unpack codes
 // (74 % of issue) and the matrix instructions (33 %) of the waves of a SIMD add up;
 // exactly 16 tokens an expert, one tile, take 195 us, 22 to 32 take 260.
+#include <type_traits>
+
 #include "layer_common.h"
 #include "w4_common.h"
 
@@ -700,25 +702,38 @@ __device__ __forceinline__ void moe_mx16(f32x4_t (&acc)[MT], const uint8_t* tile
 // 64 hidden columns, four waves each.  kDownWide: two neighbouring 64-row blocks
 // of the down matrix, four waves each.  kDownDeep: one block, four waves on each
 // half of K: twice the workgroups with half the work each, for grids that
-// would leave CUs idle otherwise.
-enum MoeForm { kGateUp, kDownWide, kDownDeep };
+// would leave CUs idle otherwise.  kGateUpFew (32 hidden columns) and kDownFew (one
+// block): the matrix instruction of four tokens alone, an expert's tokens four at
+// a time with its weight read again (from L2) for each four, without LDS tiles or a
+// second register set, so that four workgroups fit a CU instead of two.
+enum MoeForm { kGateUp, kGateUpFew, kDownWide, kDownDeep, kDownFew };
+
+template <bool DEEP>
+union MoeShared {
+  MoeSlot slot[8];
+  float red[8][4][64];
+  uint8_t x[2][(DEEP ? 4 : 2) * 8192];       // deep: a half of K each; else one piece
+  f32x4_t other[4][2][64];                   // results of the waves 4 .. 7
+};
+union MoeSharedFew {
+  MoeSlot slot[8];
+  float red[8][4][64];
+};
+
+constexpr bool is_few(MoeForm f) { return f == kGateUpFew || f == kDownFew; }
 
 template <MoeForm F>
-__global__ __launch_bounds__(512) __attribute__((amdgpu_waves_per_eu(4))) void moe_expert_kernel(MoeArgs a) {
-  constexpr bool DOWN = F != kGateUp, DEEP = F == kDownDeep;
-  union Shared {
-    MoeSlot slot[8];
-    float red[8][4][64];
-    uint8_t x[2][(DEEP ? 4 : 2) * 8192];     // deep: a half of K each; else one piece
-    f32x4_t other[4][2][64];                 // results of the waves 4 .. 7
-  };
-  __shared__ __attribute__((aligned(16))) Shared sh;
+__global__ __launch_bounds__(512) __attribute__((amdgpu_waves_per_eu(is_few(F) ? 8 : 4))) void moe_expert_kernel(
+    MoeArgs a) {
+  constexpr bool FEW = is_few(F), UP = F == kGateUp || F == kGateUpFew, DOWN = !UP;
+  constexpr bool DEEP = F == kDownDeep || F == kDownFew;
+  __shared__ __attribute__((aligned(16))) std::conditional_t<FEW, MoeSharedFew, MoeShared<DEEP>> sh;
   const int tid = threadIdx.x, lane = tid & 63, wave = wave_id_uniform(), tile = blockIdx.x;
   __shared__ int slots[kOwnSlots * 64], lists[8][kOwnTokens];
   int n, expert, pick;                       // lane m of pick: the expert's m-th pick
   if (a.own) {
     const int count = a.t * a.k;
-    if constexpr (F == kGateUp) {
+    if constexpr (UP) {
       if (wave < a.t) {
         const bool tell = tile == 0 && blockIdx.y == 0;
         moe_top(a, wave, a.k, [&](int j, int at) {
@@ -734,7 +749,7 @@ __global__ __launch_bounds__(512) __attribute__((amdgpu_waves_per_eu(4))) void m
     int of[kOwnSlots];
 #pragma unroll
     for (int u = 0; u < kOwnSlots; ++u)
-      of[u] = 64 * u + lane >= count ? -1 : F == kGateUp ? slots[64 * u + lane] : a.expert_of[64 * u + lane];
+      of[u] = 64 * u + lane >= count ? -1 : UP ? slots[64 * u + lane] : a.expert_of[64 * u + lane];
     expert = moe_own(a, of, blockIdx.y, lists[wave], n, pick);
     if (expert < 0) return;                  // uniform over the workgroup
   } else if (a.direct) {
@@ -749,7 +764,7 @@ __global__ __launch_bounds__(512) __attribute__((amdgpu_waves_per_eu(4))) void m
   }
   const int blk = wave >> 2;
   const int kdim = DOWN ? a.inter : a.h, kt_count = kdim >> 8;
-  const int rb = F == kGateUp ? tile + blk * (a.inter >> 6) : DEEP ? tile : 2 * tile + blk;
+  const int rb = UP ? (FEW ? tile >> 1 : tile) + blk * (a.inter >> 6) : DEEP ? tile : 2 * tile + blk;
   const uint8_t* const tiles = (DOWN ? a.down + expert * a.down_bytes : a.gate_up + expert * a.gate_up_bytes) +
                                (size_t)rb * kt_count * kTileBytes;
   auto source = [&](int m) {                 // activation row of the m-th pick (the last one past it)
@@ -757,90 +772,99 @@ __global__ __launch_bounds__(512) __attribute__((amdgpu_waves_per_eu(4))) void m
     return DOWN ? a.hidden + (size_t)s * a.inter : a.x + (size_t)(s / a.k) * a.h;
   };
 
-  if (n <= 4) {
-    // (block, 32-row half, one of 2 parts of K), or (half, one of 4) in the deep form
-    constexpr int KP = DEEP ? 4 : 2;
-    const int hb = DEEP ? wave >> 2 : (wave >> 1) & 1, kw = wave & (KP - 1);
-    const uint16_t* const x = source(lane >> 4);
-    float acc[4] = {0.0f, 0.0f, 0.0f, 0.0f};
-    moe_mx4<4, true>(acc, hb, kw, kdim >> 7, KP, sh.slot[wave], [&](int u) {
-      return MoeHalf{tiles + (size_t)(u >> 1) * kTileBytes, u & 1, x + (size_t)u * 128};
-    });
-    __syncthreads();
+  if (FEW || n <= 4) {
+    // (block, 32-row half, one of 2 parts of K), or (half, one of 4) in the deep
+    // forms of down, (block, one of 4) in the few form of gate and up
+    constexpr bool HALF = F == kGateUpFew;
+    constexpr int KP = DEEP || HALF ? 4 : 2;
+    const int hb = HALF ? tile & 1 : DEEP ? wave >> 2 : (wave >> 1) & 1, kw = wave & (KP - 1);
+    for (int m0 = 0; m0 < (FEW ? n : 1); m0 += 4) {
+      const uint16_t* const x = source(m0 + (lane >> 4));
+      float acc[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+      if (m0 > 0) __syncthreads();
+      moe_mx4<4, !FEW>(acc, hb, kw, kdim >> 7, KP, sh.slot[wave], [&](int u) {
+        return MoeHalf{tiles + (size_t)(u >> 1) * kTileBytes, u & 1, x + (size_t)u * 128};
+      });
+      __syncthreads();
 #pragma unroll
-    for (int m = 0; m < 4; ++m) sh.red[wave][m][lane] = acc[m];
-    __syncthreads();
-    if (wave < n) {                          // wave m: the m-th pick, lane = row of the block
-      const size_t s = __builtin_amdgcn_readlane(pick, wave);
-      const int l = lane & 31, w = KP * (lane >> 5);
-      float v[2] = {0.0f, 0.0f};
+      for (int m = 0; m < 4; ++m) sh.red[wave][m][lane] = acc[m];
+      __syncthreads();
+      if (wave < n - m0 && wave < 4) {         // wave m: the m-th pick, lane = row of the block
+        const size_t s = __builtin_amdgcn_readlane(pick, m0 + wave);
+        const int l = lane & 31, w = HALF ? 0 : KP * (lane >> 5);
+        float v[2] = {0.0f, 0.0f};
 #pragma unroll
-      for (int b = 0; b < (DEEP ? 1 : 2); ++b)
+        for (int b = 0; b < (DEEP ? 1 : 2); ++b)
 #pragma unroll
-        for (int u = 0; u < KP; ++u) v[b] += sh.red[4 * b + w + u][wave][l] + sh.red[4 * b + w + u][wave][l + 32];
-      if constexpr (F == kGateUp) {
-        const float f = silu_mul(v[0], v[1]);
-        if (a.t <= kFewTokens) store_hidden2(a, s * a.inter + 64 * tile + lane, f);
-        else a.hidden[s * a.inter + 64 * tile + lane] = (uint16_t)f32_to_bf16_rne(f);
-      } else {
-        float* const o = a.part + s * a.h + (DEEP ? 64 : 128) * tile + lane;
-        o[0] = v[0];
-        if constexpr (!DEEP) o[64] = v[1];
+          for (int u = 0; u < KP; ++u) v[b] += sh.red[4 * b + w + u][wave][l] + sh.red[4 * b + w + u][wave][l + 32];
+        if constexpr (UP) {
+          const float f = silu_mul(v[0], v[1]);
+          const size_t at = s * a.inter + (HALF ? 32 : 64) * tile + lane;
+          if (!HALF || lane < 32) {
+            if (HALF && a.t <= kFewTokens) store_hidden2(a, at, f);
+            else a.hidden[at] = (uint16_t)f32_to_bf16_rne(f);
+          }
+        } else {
+          float* const o = a.part + s * a.h + (DEEP ? 64 : 128) * tile + lane;
+          o[0] = v[0];
+          if constexpr (!DEEP) o[64] = v[1];
+        }
       }
     }
     return;
   }
-
-  const int t = wave & 3, i = lane & 15;
-  auto finish = [&](const f32x4_t (&acc)[2], int count, int m0) {
-    if constexpr (F != kDownWide) {          // the second four waves hand their sums over: up, or half of K
-      __syncthreads();
-      if (blk == 1)
-        for (int mt = 0; mt < count; ++mt) sh.other[t][mt][lane] = acc[mt];
-      __syncthreads();
-      if (blk == 1) return;
-    }
-#pragma unroll
-    for (int mt = 0; mt < 2; ++mt) {
-      if (mt >= count) continue;
-#pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        const int m = m0 + 16 * mt + 4 * (lane >> 4) + e;
-        const size_t s = __shfl(pick, m < n ? m : n - 1);
-        if (m >= n) continue;
-        if constexpr (F == kGateUp)
-          a.hidden[s * a.inter + 64 * tile + 16 * t + i] =
-              (uint16_t)f32_to_bf16_rne(silu_mul(acc[mt][e], sh.other[t][mt][lane][e]));
-        else if constexpr (DEEP)
-          a.part[s * a.h + 64 * tile + 16 * t + i] = acc[mt][e] + sh.other[t][mt][lane][e];
-        else
-          a.part[s * a.h + 128 * tile + 64 * blk + 16 * t + i] = acc[mt][e];
+  if constexpr (!FEW) {
+    const int t = wave & 3, i = lane & 15;
+    auto finish = [&](const f32x4_t (&acc)[2], int count, int m0) {
+      if constexpr (F != kDownWide) {          // the second four waves hand their sums over: up, or half of K
+        __syncthreads();
+        if (blk == 1)
+          for (int mt = 0; mt < count; ++mt) sh.other[t][mt][lane] = acc[mt];
+        __syncthreads();
+        if (blk == 1) return;
       }
+#pragma unroll
+      for (int mt = 0; mt < 2; ++mt) {
+        if (mt >= count) continue;
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          const int m = m0 + 16 * mt + 4 * (lane >> 4) + e;
+          const size_t s = __shfl(pick, m < n ? m : n - 1);
+          if (m >= n) continue;
+          if constexpr (F == kGateUp)
+            a.hidden[s * a.inter + 64 * tile + 16 * t + i] =
+                (uint16_t)f32_to_bf16_rne(silu_mul(acc[mt][e], sh.other[t][mt][lane][e]));
+          else if constexpr (DEEP)
+            a.part[s * a.h + 64 * tile + 16 * t + i] = acc[mt][e] + sh.other[t][mt][lane][e];
+          else
+            a.part[s * a.h + 128 * tile + 64 * blk + 16 * t + i] = acc[mt][e];
+        }
+      }
+    };
+    constexpr int TH = DEEP ? 256 : 512;
+    const int th = DEEP ? tid & 255 : tid, row = th >> 5;
+    const int steps = DEEP ? (kt_count + 1) >> 1 : kt_count;
+    const int count = DEEP && blk == 1 ? kt_count - steps : steps;
+    const int kt0 = DEEP && blk == 1 ? min(steps, kt_count - 1) : 0;
+    uint8_t* const xs = sh.x[DEEP ? blk : 0];    // two buffers of up to 32 rows
+    if (n <= 16) {
+      f32x4_t acc[1] = {};
+      const uint16_t* xr[512 / TH];
+#pragma unroll
+      for (int j = 0; j < 512 / TH; ++j) xr[j] = source(row + TH / 32 * j);
+      moe_mx16<1, TH>(acc, tiles, t, kt0, count, steps, xr, th, xs);
+      const f32x4_t both[2] = {acc[0], acc[0]};
+      finish(both, 1, 0);
     }
-  };
-  constexpr int TH = DEEP ? 256 : 512;
-  const int th = DEEP ? tid & 255 : tid, row = th >> 5;
-  const int steps = DEEP ? (kt_count + 1) >> 1 : kt_count;
-  const int count = DEEP && blk == 1 ? kt_count - steps : steps;
-  const int kt0 = DEEP && blk == 1 ? min(steps, kt_count - 1) : 0;
-  uint8_t* const xs = sh.x[DEEP ? blk : 0];    // two buffers of up to 32 rows
-  if (n <= 16) {
-    f32x4_t acc[1] = {};
-    const uint16_t* xr[512 / TH];
+    for (int m0 = n <= 16 ? n : 0; m0 < n; m0 += 32) {
+      f32x4_t acc[2] = {};
+      const uint16_t* xr[1024 / TH];
 #pragma unroll
-    for (int j = 0; j < 512 / TH; ++j) xr[j] = source(row + TH / 32 * j);
-    moe_mx16<1, TH>(acc, tiles, t, kt0, count, steps, xr, th, xs);
-    const f32x4_t both[2] = {acc[0], acc[0]};
-    finish(both, 1, 0);
-  }
-  for (int m0 = n <= 16 ? n : 0; m0 < n; m0 += 32) {
-    f32x4_t acc[2] = {};
-    const uint16_t* xr[1024 / TH];
-#pragma unroll
-    for (int j = 0; j < 1024 / TH; ++j) xr[j] = source(m0 + row + TH / 32 * j);
-    if (m0 > 0) __syncthreads();               // the LDS of the tokens before is done with
-    moe_mx16<2, TH>(acc, tiles, t, kt0, count, steps, xr, th, xs);
-    finish(acc, 2, m0);
+      for (int j = 0; j < 1024 / TH; ++j) xr[j] = source(m0 + row + TH / 32 * j);
+      if (m0 > 0) __syncthreads();               // the LDS of the tokens before is done with
+      moe_mx16<2, TH>(acc, tiles, t, kt0, count, steps, xr, th, xs);
+      finish(acc, 2, m0);
+    }
   }
 }
 
@@ -929,17 +953,25 @@ hipError_t launch_moe_w4a16(const void* x, int t, int h, const void* router, int
   // knows its expert without looking for it (17 tokens, 6 of 64 experts of 1024 x
   // 2048: 56 us against 58.7; 16 tokens, 8 of 128: 66 against 63).
   a.direct = 2 * t * k >= 3 * e;
+  // Four tokens at a time where few experts have more: up to 2.5 picks per expert on
+  // average (17 tokens, 6 of 64 experts of 1024 x 2048: 50.5 us against 55; 7 tokens, 8
+  // of 128 of 768 x 4096: 68 against 78; at 2.1 and 2.5 per expert 67 and 71 against 70
+  // and 73, at 3 of 16 experts of 3840 x 2560 75.6 against 70.7).
+  const bool thin = few || 2 * t * k <= 5 * e;
   // Up to kOwnTokens tokens, ranking takes a workgroup of the gate and up launch about
   // 1 us, which is less than a launch while all of them run at once (4 tokens, 2 of 8
   // of 3840 x 1024, 480 workgroups: 20.2 us against 22.6; 7 tokens, 8 of 128 of 768 x
   // 4096, 672: 82 against 78; 5, 4 of 16 of 10496 x 2048, 2624: 112 against 102).
-  a.own = t <= kOwnTokens && (inter / 64) * (a.direct ? e : t * k) <= 2 * kCUs;
+  a.own = t <= kOwnTokens && inter / (thin ? 32 : 64) * (a.direct ? e : t * k) <= (thin ? 4 : 2) * kCUs;
   const int units = a.direct || (!a.own && t * k > e) ? e : t * k;
   if (!a.own) {
     hipLaunchKernelGGL(moe_route_kernel, dim3(e), dim3(512), 0, stream, a);
     if (!ok()) return st;
   }
-  hipLaunchKernelGGL((moe_expert_kernel<kGateUp>), dim3(inter / 64, units), dim3(512), 0, stream, a);
+  if (thin)
+    hipLaunchKernelGGL((moe_expert_kernel<kGateUpFew>), dim3(inter / 32, units), dim3(512), 0, stream, a);
+  else
+    hipLaunchKernelGGL((moe_expert_kernel<kGateUp>), dim3(inter / 64, units), dim3(512), 0, stream, a);
   if (!ok()) return st;
   if (few) {
     hipLaunchKernelGGL(moe_down_few_kernel, dim3(h / 16, t), dim3(1024), 0, stream, a);
@@ -952,7 +984,9 @@ hipError_t launch_moe_w4a16(const void* x, int t, int h, const void* router, int
   // above it the wide form copies each activation row for twice the weight rows (60
   // on 16 of 3328 x 4096, 512: 121 us against 129 deep; 16 on 128 of 768 x 2048: 64
   // against 71).
-  if (2 * (h / 128) * units <= 3 * kCUs)
+  if (thin)
+    hipLaunchKernelGGL((moe_expert_kernel<kDownFew>), dim3(h / 64, units), dim3(512), 0, stream, a);
+  else if (2 * (h / 128) * units <= 3 * kCUs)
     hipLaunchKernelGGL((moe_expert_kernel<kDownDeep>), dim3(h / 64, units), dim3(512), 0, stream, a);
   else
     hipLaunchKernelGGL((moe_expert_kernel<kDownWide>), dim3(h / 128, units), dim3(512), 0, stream, a);

@@ -93,9 +93,11 @@ def test_all_tokens_on_the_same_experts(dev):
     router[5], router[2] = 0.02, 0.01
     case(dev, 64, e, 2, h, 256, True, 0, x=x, router=router)
     case(dev, 3, e, 2, h, 256, False, 0, x=x[:3], router=router)
+    for t in (5, 6, 8, 9):
+        case(dev, t, e, 2, h, 256, False, 0, x=x[:t], router=router)
 
 
-@pytest.mark.parametrize("t,k,same", [(17, 3, False), (64, 4, False), (64, 2, True), (5, 10, False)])
+@pytest.mark.parametrize("t,k,same", [(17, 3, False), (64, 4, False), (64, 2, True), (60, 2, True), (5, 10, False)])
 def test_many_row_blocks_and_experts(dev, t, k, same):
     """50 experts with 8 pairs of row blocks each in the down product: more than
     the workgroups that halves of K are for; 64 tokens of one expert among them."""
