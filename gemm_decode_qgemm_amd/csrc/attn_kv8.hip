@@ -273,6 +273,8 @@ __global__ __launch_bounds__(64 * W) void attn_kv8_kernel(AttnArgs a) {
     return;
   }
 
+  const bool alone = p_end - p_beg <= 1;             // one wave has the only page
+
   // Rows of this lane, as fp16 q 2^(8 - e) with 2^e just above the row's
   // largest channel: exact but for channels 2^-21 of that one.  The keys'
   // bias of 1152 comes off in the accumulator's first value.
@@ -282,7 +284,7 @@ __global__ __launch_bounds__(64 * W) void attn_kv8_kernel(AttnArgs a) {
 #pragma unroll
   for (int n = 0; n < NT; ++n) {
     const int r = row0 + 16 * n + i;
-    const bool on = r < nrows;
+    const bool on = r < nrows && (!alone || wave == 0);
     const int t = group_of(a, r), g = r - t * a.group;
     pos[n] = on ? shift + t : -1;
     const uint16_t* src = a.q + (r0 + t) * a.q_ts + (int64_t)(h * a.group + g) * a.q_hs + 16 * qd;
@@ -489,9 +491,10 @@ __global__ __launch_bounds__(64 * W) void attn_kv8_kernel(AttnArgs a) {
     for (int w = 0; w < W; ++w) ll += sm_l[w][16 * n + i] * __builtin_amdgcn_exp2f(sm_m[w][16 * n + i] - base);
     const float f = __builtin_amdgcn_exp2f(m[n] - base) * vback;
     if (n > 0) __syncthreads();
+    if (!alone || wave == 0)
 #pragma unroll
-    for (int t = 0; t < DT; ++t)
-      sm_o[wave][t][lane] = f32x4_t{o[n][t][0] * f, o[n][t][1] * f, o[n][t][2] * f, o[n][t][3] * f};
+      for (int t = 0; t < DT; ++t)
+        sm_o[wave][t][lane] = f32x4_t{o[n][t][0] * f, o[n][t][1] * f, o[n][t][2] * f, o[n][t][3] * f};
     __syncthreads();
     const int r = row0 + 16 * n + i;
     const int t = group_of(a, r), g = r - t * a.group;
@@ -500,11 +503,12 @@ __global__ __launch_bounds__(64 * W) void attn_kv8_kernel(AttnArgs a) {
     const bool on = r < nrows;
     for (int dt = wave; dt < DT; dt += W) {
       f32x4_t v = sm_o[0][dt][lane];
+      if (!alone)
 #pragma unroll
-      for (int w = 1; w < W; ++w) {
-        const f32x4_t u = sm_o[w][dt][lane];
-        v = f32x4_t{v[0] + u[0], v[1] + u[1], v[2] + u[2], v[3] + u[3]};
-      }
+        for (int w = 1; w < W; ++w) {
+          const f32x4_t u = sm_o[w][dt][lane];
+          v = f32x4_t{v[0] + u[0], v[1] + u[1], v[2] + u[2], v[3] + u[3]};
+        }
       if (!on) continue;
       const int d = 16 * dt + 4 * qd;
       if (splits > 1) {
