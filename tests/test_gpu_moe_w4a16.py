@@ -118,8 +118,8 @@ def test_few_tokens_on_many_workgroups(dev, t, k):
 
 
 @pytest.mark.parametrize("e,k", [(512, 32), (300, 5), (65, 3)])
-@pytest.mark.parametrize("t", [2, 8])
-def test_few_tokens_of_many_experts(dev, t, e, k):
+@pytest.mark.parametrize("t", [2, 8, 63])
+def test_tokens_of_many_experts(dev, t, e, k):
     """Routing alone: every expert one tile, its weights those of expert e % 8."""
     h = inter = 256
     gu, dn, gu_v, dn_v = experts(8, h, inter, 77)
