@@ -70,6 +70,20 @@ def test_many_tokens_take_whole_tokens_per_wave(dev):
     check(yq[-3:], q[-3:], None, cs, pos[-3:], 1e-6, False)
 
 
+@pytest.mark.parametrize("t,hq,d,rot,pairs", [(200001, 1, 64, 64, False), (70000, 2, 80, 32, True)])
+def test_more_tokens_than_a_long_prompt(dev, t, hq, d, rot, pairs):
+    torch.manual_seed(t)
+    q, k = torch.randn(t, hq, d, device=dev).bfloat16(), torch.randn(t, 1, d, device=dev).bfloat16()
+    w = (1 + torch.randn(d) * 0.3).bfloat16()
+    cs, pos = table(4096, rot), torch.arange(t, device=dev, dtype=torch.int32) % 4096
+    yq, yk = qg.qk_norm_rope(q, k, w.to(dev), None, cs.to(dev), pos, adjacent_pairs=pairs)
+    assert yq.isfinite().all() and yk.isfinite().all()
+    for lo in (0, 32700, 65500, t - 100):
+        part = slice(lo, lo + 100)
+        check(yq[part], q[part], w, cs, pos[part], 1e-6, pairs)
+        check(yk[part], k[part], None, cs, pos[part], 1e-6, pairs)
+
+
 def test_no_weights_eps_zero_rows_and_extremes(dev):
     d = 64
     q = torch.zeros(4, 2, d, dtype=torch.bfloat16, device=dev)
