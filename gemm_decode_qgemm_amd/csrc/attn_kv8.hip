@@ -135,6 +135,14 @@ __device__ __forceinline__ int wave_scan(int v) {
   return v;
 }
 
+// The last page worth reading for rows that end before token `end`.  Beyond the
+// table: a page that is not there for every row that sees such a token, which is
+// the first one past the table or the first one of the row's window.
+__device__ __forceinline__ int last_page(const AttnArgs& a, int end) {
+  const int start = a.window > 0 ? max(0, end - a.window) / kPage : 0;   // of the last row's window
+  return min((end - 1) / kPage, max((int)a.c.width, start));
+}
+
 // Pages that the n rows of a sequence of len tokens see: their number, and the first.
 __device__ __forceinline__ int pages_of(const AttnArgs& a, int len, int64_t n, int& first) {
   first = 0;
@@ -143,7 +151,7 @@ __device__ __forceinline__ int pages_of(const AttnArgs& a, int len, int64_t n, i
     const int64_t beg = len - n - a.window + 1;
     first = beg > 0 ? (int)(beg / kPage) : 0;
   }
-  return min((len - 1) / kPage, max((int)a.c.width, first)) - first + 1;   // (beyond the table: one page, missing)
+  return last_page(a, len) - first + 1;
 }
 
 // The sequence b that slot j works for, its share k of n and the pages it has.
@@ -243,15 +251,14 @@ __global__ __launch_bounds__(64 * W) void attn_kv8_kernel(AttnArgs a) {
   int p_beg = 0, p_end = 0;
   if (tok_end > tok_beg) {
     const int first = tok_beg / kPage;
-    // a length beyond the table costs one page that is not there
-    const int last = min((tok_end - 1) / kPage, width);
+    const int last = last_page(a, tok_end);
     if constexpr (SHARED) {
       // even shares of the pages that the whole sequence sees
       int from;
       const int all = pages_of(a, len, n64, from), share = all / splits, more = all % splits;
       const int beg = from + split * share + min(split, more);
       p_beg = max(beg, first);
-      p_end = min(beg + share + (split < more ? 1 : 0), last + 1);
+      p_end = split + 1 < splits ? min(beg + share + (split < more ? 1 : 0), last + 1) : last + 1;
     } else {
       // `chunk` pages a split, the last one what is left: equal work for every
       // workgroup whatever the lengths

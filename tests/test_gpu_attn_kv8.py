@@ -263,3 +263,27 @@ def test_many_splits_of_many_rows(dev, splits):
     want, mass = f.reference(ref.f64(q), [2] * 3, 128 ** -0.5, 0)
     for dt in (torch.float32, torch.bfloat16):
         check(qg.attn_kv8(q.to(dev), *f.args, splits=splits, out_dtype=dt), want, mass)
+
+
+@pytest.mark.parametrize("width,splits", [(4, 0), (4, 1), (4, 3), (130, 0)])
+@pytest.mark.parametrize("window", [0, 33])
+def test_lengths_beyond_the_table(dev, width, splits, window):
+    """Rows that see a token past the table's pages are NaN and flagged, also
+    where a window sees nothing else; the others are not."""
+    hq, hkv, d, rows = 24, 8, 64, 70
+    lens = [100] * 12
+    f = Filled(dev, lens, hkv, d, 3, spare=width - 2)
+    end = 64 * width
+    for i in range(width):
+        f.table_d[:, i] = f.table_d[:, i % 2]
+    told = torch.tensor([100, end, end + 1, end + 64, end + 70, end + 1000] * 2, dtype=torch.int32, device=dev)
+    f.scales.nan_to_num_(0.02)
+    torch.manual_seed(width)
+    q = torch.randn(12 * rows, hq, d, device=dev).bfloat16()
+    flag = torch.zeros(1, dtype=torch.int32, device=dev)
+    y = qg.attn_kv8(q, *f.args[:3], told, window=window, splits=splits, status=flag).unflatten(0, (12, rows))
+    last = told[:, None] - rows + torch.arange(rows, device=dev)[None]
+    beyond = last >= end
+    assert torch.equal(y.isnan().all(3).all(2), beyond)
+    assert torch.equal(y.isnan().any(3).any(2), beyond)
+    assert flag.item() == qg.FLAG_PAGE
