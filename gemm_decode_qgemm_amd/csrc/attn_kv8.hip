@@ -18,7 +18,8 @@
 //  * a query row is scaled by a power of two to a largest channel in [2^7,
 //    2^8), where its 8 significant bits fit exactly;
 //  * p * vs is taken relative to the largest exponent of a value scale seen so
-//    far and put at 2^13, so it keeps 11 bits down to 2^-27 of the largest.
+//    far and put at 2^13, so it keeps 11 bits down to 2^-27 of the largest, and 2^-38
+//    of that below.
 // As bf16 the same products took 1.5 instructions per code and p * vs had to be
 // two operands for this accuracy: 32 sequences of 4096 tokens on 32 / 8 heads of
 // 128 ran 60 us, now 46 us (5.85 TB/s).
@@ -36,7 +37,8 @@
 //  * m and l of a row are the same lane column as its O, so rescaling is one
 //    factor per lane; it is skipped while no maximum of the wave moved;
 //  * a block's scales are wave-uniform and read by scalar loads.
-// A workgroup's waves take pages in turn and join (m, l, O) through LDS; the
+// A workgroup's waves take pages in turn and join (m, l, O) through LDS (or, with
+// many rows, each a row tile through all pages and join nothing); the
 // pages of a sequence are further split over workgroups when there are few,
 // the partial (m, l, O) joined by a second kernel in a fixed order.
 #include <algorithm>
@@ -211,18 +213,20 @@ __device__ __forceinline__ bool attn_plan(const AttnArgs& a, int j, bool tell, i
   return true;
 }
 
-template <int D, int NT, bool SHARED, int W = kWaves>   // SHARED: a.slots > 0
+// SHARED: a.slots > 0.  ROWS: each wave takes a row tile of its own through all
+// pages, and row_tiles counts fours of them (one split).
+template <int D, int NT, bool SHARED, bool ROWS, int W = kWaves>
 __global__ __launch_bounds__(64 * W) void attn_kv8_kernel(AttnArgs a) {
   constexpr int KC = D / 64;        // 64-channel chunks of a key
   constexpr int DT = D / 16;        // 16-channel tiles of a value
   constexpr bool kEarlyV = D <= 192 && D * NT <= 256;   // values in flight with the keys, where registers allow
-  __shared__ float sm_m[W][16 * NT], sm_l[W][16 * NT];
-  __shared__ f32x4_t sm_o[W][DT][64];
+  __shared__ float sm_m[ROWS ? 1 : W][16 * NT], sm_l[ROWS ? 1 : W][16 * NT];
+  __shared__ f32x4_t sm_o[ROWS ? 1 : W][DT][64];
   const int lane = threadIdx.x & 63, i = lane & 15, qd = lane >> 4;
   const int wave = wave_id_uniform();
   // Splits slowest: workgroups go to the 8 XCDs in turn, and the late splits
   // of short sequences, which are empty, must not all fall to the same ones.
-  const int h = blockIdx.x / a.row_tiles, rt = blockIdx.x % a.row_tiles;
+  const int h = blockIdx.x / a.row_tiles, rt = ROWS ? blockIdx.x % a.row_tiles * W + wave : blockIdx.x % a.row_tiles;
   int b = blockIdx.y, split = blockIdx.z, splits = a.splits, len;
   if constexpr (SHARED) {
     const bool tell = blockIdx.x == 0 && blockIdx.y == 0 && wave == 0;
@@ -232,7 +236,7 @@ __global__ __launch_bounds__(64 * W) void attn_kv8_kernel(AttnArgs a) {
   const int width = (int)a.c.width;
   // Without a window the first page does not depend on the length: its table
   // entry is on its way together with the length.
-  const int guess = SHARED ? 0 : (int)min((int64_t)split * a.chunk + wave, (int64_t)width - 1);
+  const int guess = SHARED || ROWS ? 0 : (int)min((int64_t)split * a.chunk + wave, (int64_t)width - 1);
   const int guessed = trow[guess];
   if constexpr (!SHARED) len = ((const_i32)a.c.lens)[b];
   len = max(len, 0);
@@ -280,7 +284,9 @@ __global__ __launch_bounds__(64 * W) void attn_kv8_kernel(AttnArgs a) {
     return;
   }
 
-  const bool alone = p_end - p_beg <= 1;             // one wave has the only page
+  const bool alone = !ROWS && p_end - p_beg <= 1;    // one wave has the only page
+  const int first_page = p_beg + (ROWS ? 0 : wave);
+  constexpr int kStep = ROWS ? 1 : W;
 
   // Rows of this lane, as fp16 q 2^(8 - e) with 2^e just above the row's
   // largest channel: exact but for channels 2^-21 of that one.  The keys'
@@ -343,8 +349,8 @@ __global__ __launch_bounds__(64 * W) void attn_kv8_kernel(AttnArgs a) {
     return p < width && e >= 0 && e < a.c.pages ? e : -1;
   };
   bool missing = false;
-  int next = p_beg + wave < p_end ? entry(p_beg + wave) : 0;
-  for (int p = p_beg + wave; p < p_end; p += W) {
+  int next = first_page < p_end ? entry(first_page) : 0;
+  for (int p = first_page; p < p_end; p += kStep) {
     const int page = next;
     const int held = page < 0 ? 0 : page;            // reads stay inside; its scales become NaN below
     const int8_t* const kc = a.c.codes + kv8_base(held, a.c.hkv, h, D);
@@ -369,7 +375,7 @@ __global__ __launch_bounds__(64 * W) void attn_kv8_kernel(AttnArgs a) {
       ks[blk] = sc[blk];
       vs[blk] = sc[4 + blk];
     }
-    if (p + W < p_end) next = entry(p + W);
+    if (p + kStep < p_end) next = entry(p + kStep);
     missing |= page < 0;
     const int j0 = p * kPage;
     const bool edge = j0 + kPage - 1 > pos_lo || (a.window > 0 && j0 <= pos_hi - a.window);   // uniform
@@ -478,6 +484,30 @@ __global__ __launch_bounds__(64 * W) void attn_kv8_kernel(AttnArgs a) {
   if (missing && a.status && lane == 0) atomicOr(a.status, QG_FLAG_PAGE);
   const float vback = __uint_as_float((uint32_t)(ve - 13) << 23);     // 2^(ve - 140)
 
+  auto store = [&](int64_t row, int d, const f32x4_t& v, float ll) {   // O / l of the output's row
+    const float inv = ll == 0.0f ? 0.0f : 1.0f / ll;
+    const f32x4_t y{v[0] * inv, v[1] * inv, v[2] * inv, v[3] * inv};
+    if (a.out_f32)
+      *reinterpret_cast<f32x4_t*>(static_cast<float*>(a.out) + (size_t)row * D + d) = y;
+    else
+      *reinterpret_cast<u32x2_t*>(static_cast<uint16_t*>(a.out) + (size_t)row * D + d) =
+          u32x2_t{pack_bf16(y[0], y[1]), pack_bf16(y[2], y[3])};
+  };
+  if constexpr (ROWS) {
+#pragma unroll
+    for (int n = 0; n < NT; ++n) {
+      l[n] = fold_quads(l[n], [](float x, float y) { return x + y; });
+      const int r = row0 + 16 * n + i;
+      if (r >= nrows) continue;
+      const int t = group_of(a, r), g = r - t * a.group;
+#pragma unroll
+      for (int dt = 0; dt < DT; ++dt)
+        store((r0 + t) * a.hq + h * a.group + g, 16 * dt + 4 * qd,
+              f32x4_t{o[n][dt][0] * vback, o[n][dt][1] * vback, o[n][dt][2] * vback, o[n][dt][3] * vback}, l[n]);
+    }
+    return;
+  }
+
   // Join the waves: M = max m, each wave's O and l times 2^(m - M), added in wave order.
 #pragma unroll
   for (int n = 0; n < NT; ++n) {
@@ -522,13 +552,7 @@ __global__ __launch_bounds__(64 * W) void attn_kv8_kernel(AttnArgs a) {
         if (mm != kNegInf || ll != 0.0f)
           *reinterpret_cast<f32x4_t*>(a.part_o + prow * D + d) = v;
       } else {
-        const float inv = ll == 0.0f ? 0.0f : 1.0f / ll;
-        const f32x4_t y{v[0] * inv, v[1] * inv, v[2] * inv, v[3] * inv};
-        if (a.out_f32)
-          *reinterpret_cast<f32x4_t*>(static_cast<float*>(a.out) + (size_t)row * D + d) = y;
-        else
-          *reinterpret_cast<u32x2_t*>(static_cast<uint16_t*>(a.out) + (size_t)row * D + d) =
-              u32x2_t{pack_bf16(y[0], y[1]), pack_bf16(y[2], y[3])};
+        store(row, d, v, ll);
       }
     }
     if (splits > 1 && on && wave == 0 && qd == 0) {
@@ -750,16 +774,19 @@ AttnSplit attn_kv8_split(int64_t b, int64_t rows, int hkv, int d, int64_t rows_p
   const int nt = attn_kv8_nt(rows_per_head);
   const int64_t units = hkv * ((rows_per_head + 16 * nt - 1) / (16 * nt));
   const int64_t slots = std::max((resident(d, nt) * kCUs + units - 1) / units, b + b / 2);
+  // (four times the row tiles that fill the card: 16 sequences of 3000 tokens, 64 rows on
+  // 64 / 8 heads of 128, 226 us with a row tile a wave against 280)
+  if (units * b >= 4 * resident(d, nt) * kCUs && rows_per_head > 16 * nt) return {1, 0};
   if (max_q * b > 2 * rows || seen_pages(max_len, window, max_q) <= 5 * kWaves * s || slots > 65535)
     return {s, 0};
   return {1, (int)slots};
 }
 
-template <int D, int NT, bool SHARED>
+template <int D, int NT, bool SHARED, bool ROWS = false>
 static hipError_t launch_attn_t(const AttnArgs& a, hipStream_t stream) {
   const int x = a.row_tiles * a.c.hkv;
   const dim3 grid = SHARED ? dim3(x, a.slots) : dim3(x, a.c.b, a.splits);
-  hipLaunchKernelGGL((attn_kv8_kernel<D, NT, SHARED>), grid, dim3(64 * kWaves), 0, stream, a);
+  hipLaunchKernelGGL((attn_kv8_kernel<D, NT, SHARED, ROWS>), grid, dim3(64 * kWaves), 0, stream, a);
   hipError_t e = hipGetLastError();
   if (e != hipSuccess || (!SHARED && a.splits == 1)) return e;
   // Many splits of few rows: a workgroup for 32 channels of a row; with many rows
@@ -794,9 +821,21 @@ hipError_t launch_attn_kv8(const Kv8Args& c, const void* q, int64_t q_ts, int64_
     a.part_ml = part + partial * c.d;
     a.plan = reinterpret_cast<int32_t*>(a.part_ml + partial * 2);
   }
-  switch (c.d * 4 + nt) {
+  // A row tile a wave instead of a page a wave: where there is hardly a second page,
+  // and where the row tiles fill the card one and a half times, there is nothing to
+  // join then and no wave waits (57 sequences of 17..45 tokens, 37 rows on 20 / 4 heads of 256: 30 us
+  // against 71; 16 of 1000, 64 on 64 / 8 of 128: 86 against 106; at half as many row
+  // tiles, 2 of 256: 17 against 11).  One tile at a time for up to two pages (12
+  // of 64, 61 on 40 / 8 of 64: 6.8 against 8.6), two above (86 against 134).
+  const int64_t units = (int64_t)a.row_tiles * c.hkv * c.b;
+  const bool rows = splits == 1 && by.slots == 0 && a.row_tiles > 1 &&
+                    (pages <= 2 || 2 * units >= 3 * resident(c.d, nt) * kCUs);
+  const int tall = rows && pages <= 2 ? 1 : nt;
+  if (rows) a.row_tiles = (int)((rows_per_head + 16 * tall * kWaves - 1) / (16 * tall * kWaves));
+  switch (c.d * 4 + tall) {
 #define QG_ATTN(D, NT) \
   case D * 4 + NT:          \
+    if (rows) return launch_attn_t<D, NT, false, true>(a, stream);                                          \
     return by.slots > 0 ? launch_attn_t<D, NT, true>(a, stream) : launch_attn_t<D, NT, false>(a, stream);
     QG_ATTN(64, 1) QG_ATTN(64, 2) QG_ATTN(128, 1) QG_ATTN(128, 2) QG_ATTN(192, 1) QG_ATTN(192, 2)
     QG_ATTN(256, 1) QG_ATTN(256, 2)

@@ -449,7 +449,7 @@ int32_t qg_kv8_read(const int8_t *codes, const float *scales, int64_t pages, int
  * that sees no token (length 0, or a row before token 0) is zero.  Softmax and
  * sums are fp32; the products' operands are fp16: q scaled by a power of two
  * per row, the codes (exact), and probability times value scale, rounded once
- * to 11 bits.
+ * to 11 bits (below 2^-27 of the row's largest: to 2^-38 of that).
  *   q        in : bf16 [rows, hq, d], strides as qg_qk_norm_rope
  *   max_q    in : no sequence has more query rows (later ones are not written)
  *   max_len  in : an upper bound of lens, for the choice of the split only

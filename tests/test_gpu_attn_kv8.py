@@ -287,3 +287,53 @@ def test_lengths_beyond_the_table(dev, width, splits, window):
     assert torch.equal(y.isnan().all(3).all(2), beyond)
     assert torch.equal(y.isnan().any(3).any(2), beyond)
     assert flag.item() == qg.FLAG_PAGE
+
+
+@pytest.mark.parametrize("hq,hkv,d", [(12, 2, 64), (8, 1, 128), (10, 2, 192), (5, 1, 256)])
+@pytest.mark.parametrize("window", [0, 1, 50])
+def test_many_rows_on_short_sequences(dev, request, hq, hkv, d, window):
+    """A row tile a wave: up to two pages, rows that end inside a tile, none at all, more than tokens."""
+    if (d, window) == (256, 50):
+        # One of 226560 outputs: the token that has nearly all of the weight holds a zero code there, so
+        # that its A is 2^-30 of the row's and smaller than what fp16 keeps of such weights; the
+        # bound that holds there is in test_weights_below_the_operands_range.
+        request.node.add_marker(pytest.mark.xfail(strict=True, reason="A below 2^-27 of the row's largest"))
+    lens, counts = [128, 0, 1, 64, 77, 20], [40, 3, 9, 0, 61, 64]
+    f = Filled(dev, lens, hkv, d, d, spare=0)
+    torch.manual_seed(d + window)
+    q = torch.randn(sum(counts), hq, d).bfloat16()
+    want, mass = f.reference(ref.f64(q), counts, 0.15, window)
+    for dt in (torch.float32, torch.bfloat16):
+        check(qg.attn_kv8(q.to(dev), *f.args, cu=cu_of(counts, dev), max_q=64, window=window, scale=0.15, out_dtype=dt),
+              want, mass)
+
+
+@pytest.mark.parametrize("b,rows,hq,hkv,d,longest", [(80, 16, 32, 8, 64, 260), (50, 9, 32, 8, 128, 200),
+                                                     (24, 10, 32, 8, 256, 330), (24, 9, 32, 8, 192, 330)])
+def test_row_tiles_that_fill_the_card(dev, b, rows, hq, hkv, d, longest):
+    lens = [(i * 37) % (longest + 1) for i in range(b - 1)] + [longest]
+    f = Filled(dev, lens, hkv, d, b)
+    torch.manual_seed(b)
+    q = torch.randn(b * rows, hq, d).bfloat16()
+    for window in (0, 90):
+        want, mass = f.reference(ref.f64(q), [rows] * b, d ** -0.5, window)
+        y = qg.attn_kv8(q.to(dev), *f.args, window=window)
+        check(y, want, mass)
+        assert torch.equal(y, qg.attn_kv8(q.to(dev), *f.args, window=window))
+
+
+@pytest.mark.parametrize("d,scale", [(64, 0.5), (128, 0.3), (256, 0.15)])
+def test_weights_below_the_operands_range(dev, d, scale):
+    """Sharp softmaxes.  A weight times its value scale is an fp16 operand with the largest value scale of
+    the row at 2^13: below 2^-14, that is 2^-27 of the largest, it is off by up to 2^-25, which
+    is 2^-38 of the largest scale for each token and code of up to 127."""
+    lens, rows = [20, 64, 128, 300], 5
+    f = Filled(dev, lens, 2, d, d + 1)
+    torch.manual_seed(d)
+    q = torch.randn(4 * rows, 8, d).bfloat16()
+    want, mass = f.reference(ref.f64(q), [rows] * 4, scale, 0)
+    n = np.repeat(np.array(lens), rows)[:, None, None]
+    for splits in (0, 1, 3):
+        got = ref.f64(qg.attn_kv8(q.to(dev), *f.args, scale=scale, splits=splits, out_dtype=torch.float32))
+        tol = mass * (2.0 ** -8 + 2.0 ** -11) + n * 127 * 0.04 * 2.0 ** -38 + 1e-30
+        assert (np.abs(got - want) <= tol).all(), float((np.abs(got - want) / tol).max())
