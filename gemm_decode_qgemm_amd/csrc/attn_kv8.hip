@@ -8,7 +8,8 @@
 // One pass with the running maximum m and sum l: for every page of 64 tokens
 //   m' = max(m, max s), p = 2^(s - m'), l = l 2^(m - m') + sum p,
 //   O  = O 2^(m - m') + sum p v,       o = O / l
-// (scores in units of log 2), everything but the products' operands in fp32.
+// (scores in units of log 2, m rounded up to a whole number so that every rescaling is
+// by a power of two), everything but the products' operands in fp32.
 // Operands are fp16, which costs fewer instructions than bf16 and rounds less:
 //  * a code q becomes 1024 + (q + 128) by one byte permute a pair (0x6400 |
 //    byte), exactly.  Keys stay so: the accumulator starts at -1152 sum(q) of the
@@ -17,9 +18,11 @@
 //    over a whole cache, have the 1152 taken off again, exactly (packed add);
 //  * a query row is scaled by a power of two to a largest channel in [2^7,
 //    2^8), where its 8 significant bits fit exactly;
-//  * p * vs is taken relative to the largest exponent of a value scale seen so
-//    far and put at 2^13, so it keeps 11 bits down to 2^-27 of the largest, and 2^-38
-//    of that below.
+//  * p * vs is taken relative to the largest one that the row itself has seen so far,
+//    put at 2^13 .. 2^15, so it keeps 11 bits down to 2^-27 of that, and 2^-38 of that
+//    below.  The power of two is a state of the row like m (one for all rows of a
+//    tile, from the scales alone, let a block that a row does not see, or hardly
+//    weighs, round the row's own products away).
 // As bf16 the same products took 1.5 instructions per code and p * vs had to be
 // two operands for this accuracy: 32 sequences of 4096 tokens on 32 / 8 heads of
 // 128 ran 60 us, now 46 us (5.85 TB/s).
@@ -70,7 +73,8 @@ __device__ __forceinline__ int group_of(const AttnArgs& a, int r) {
   return q + (r - q * a.group >= a.group ? 1 : 0);
 }
 
-constexpr int kMinExp = 20;         // value scales below 2^-107 are taken relative to that
+constexpr int kMinExp = -107;       // products p * vs below 2^-107 are taken relative to that
+constexpr int kTopExp = 14;         // the largest is put below 2^(kTopExp + 1)
 
 // Value of lane ^ 32, then of lane ^ 16, folded with f.
 template <class F>
@@ -118,7 +122,7 @@ __device__ __forceinline__ uint32_t pack_f16(float lo, float hi) {
 typedef const __attribute__((address_space(4))) int32_t* const_i32;
 typedef const __attribute__((address_space(4))) float* const_f32;
 
-constexpr float kNegInf = -__builtin_inff();
+constexpr float kNegInf = -__builtin_inff(), kMaxF32 = 0x1.fffffep127f;
 constexpr int kMaxSplits = 256;   // a lane per split in the join
 // Waves of a workgroup, one page each at a time.  Eight instead of four halve
 // the partial results of a split, but fewer workgroups fit a CU (48 sequences of
@@ -334,12 +338,14 @@ __global__ __launch_bounds__(64 * W) void attn_kv8_kernel(AttnArgs a) {
   }
 
   float m[NT], l[NT];
+  float pe[NT], pmul[NT];           // a whole number, p * vs < 2^(pe + 1) so far, and 2^(kTopExp - pe): o holds O * pmul
   f32x4_t o[NT][DT];
-  int ve = kMinExp;                 // o holds O 2^(140 - ve), ve the largest biased exponent of a value scale so far
 #pragma unroll
   for (int n = 0; n < NT; ++n) {
     m[n] = kNegInf;
     l[n] = 0.0f;
+    pe[n] = kMinExp;
+    pmul[n] = __builtin_ldexpf(1.0f, kTopExp - kMinExp);
 #pragma unroll
     for (int t = 0; t < DT; ++t) o[n][t] = f32x4_t{0.0f, 0.0f, 0.0f, 0.0f};
   }
@@ -397,37 +403,26 @@ __global__ __launch_bounds__(64 * W) void attn_kv8_kernel(AttnArgs a) {
     }
     if constexpr (!kEarlyV) load_v();
 
-    // The exponent that value scales are taken relative to (uniform): of the
-    // blocks that some row sees, infinities and NaN aside.
-    int top = 0;
+    // The exponents of the value scales (uniform).  A scale that is infinite or NaN and
+    // a page that is not there turn the scores into NaN, which reaches the rows that see it.
+    int vexp[4], vtop = kMinExp;
 #pragma unroll
     for (int blk = 0; blk < 4; ++blk) {
       const int ex = (int)(__float_as_uint(vs[blk]) >> 23 & 0xff);
-      const bool seen = j0 + 16 * blk < tok_end && j0 + 16 * blk + kBlock > tok_beg;
-      if (seen && ex < 255 && ex > top) top = ex;
-      if (page < 0) ks[blk] = __uint_as_float(0x7fc00000u);
+      vexp[blk] = ex < 255 ? max(ex - 127, kMinExp) : kMinExp;
+      vtop = max(vtop, vexp[blk]);
+      const bool bad = page < 0 || ex == 255 || (__float_as_uint(ks[blk]) >> 23 & 0xff) == 255;
+      if (bad) ks[blk] = __uint_as_float(0x7fc00000u);
     }
-    if (top > ve) {
-      const float f = __builtin_ldexpf(1.0f, ve - top);
-#pragma unroll
-      for (int n = 0; n < NT; ++n)
-#pragma unroll
-        for (int t = 0; t < DT; ++t)
-#pragma unroll
-          for (int e = 0; e < 4; ++e) o[n][t][e] *= f;
-      ve = top;
-    }
-    const float vmul = __uint_as_float((uint32_t)(267 - ve) << 23);   // 2^(140 - ve)
-#pragma unroll
-    for (int blk = 0; blk < 4; ++blk) vs[blk] *= vmul;
 
     f16x8_t pf[NT][2];
 #pragma unroll
     for (int n = 0; n < NT; ++n) {
-      float mx = kNegInf;
+      float top[4];                 // of the lane's scores in a block
 #pragma unroll
       for (int blk = 0; blk < 4; ++blk) {
         const float f = ks[blk] * rscale[n];
+        top[blk] = kNegInf;
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
           float v = s[n][blk][e] * f;
@@ -436,21 +431,38 @@ __global__ __launch_bounds__(64 * W) void attn_kv8_kernel(AttnArgs a) {
             v = j <= pos[n] && (a.window <= 0 || j > pos[n] - a.window) ? v : kNegInf;
           }
           s[n][blk][e] = v;
-          mx = fmaxf(mx, v);
+          top[blk] = fmaxf(top[blk], v);
         }
       }
-      mx = fold_quads(mx, [](float x, float y) { return fmaxf(x, y); });
-      const float m_new = fmaxf(m[n], mx);
+      auto larger = [](float x, float y) { return fmaxf(x, y); };
+      const float mx = fold_quads(fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3])), larger);
+      const float m_new = fmaxf(m[n], ceilf(mx));
       const float base = m_new == kNegInf ? 0.0f : m_new;   // nothing seen yet: every p is 0
-      if (__ballot(m_new > m[n]) != 0) {
-        const float f = __builtin_amdgcn_exp2f(m[n] - base);
-        l[n] *= f;
+      const float pe_old = pe[n] + (m[n] - base);           // relative to the new maximum
+      // Nothing to do while no maximum moved and the page's largest p with its largest
+      // scale stays below what the row has seen; else the largest p * vs counts, from
+      // the largest p of each block.
+      if (__ballot(m_new > m[n] || mx - base + (float)vtop > pe_old) != 0) {
+        float ptop = kNegInf;
+#pragma unroll
+        for (int blk = 0; blk < 4; ++blk) ptop = fmaxf(ptop, top[blk] - base + (float)vexp[blk]);
+        const float pe_new = fmaxf(fmaxf(pe_old, ceilf(fold_quads(ptop, larger))), (float)kMinExp);
+        const float f = __builtin_amdgcn_exp2f(pe_old - pe_new);
+        l[n] *= __builtin_amdgcn_exp2f(m[n] - base);
 #pragma unroll
         for (int t = 0; t < DT; ++t)
 #pragma unroll
           for (int e = 0; e < 4; ++e) o[n][t][e] *= f;
         m[n] = m_new;
+        pe[n] = pe_new;
+        pmul[n] = __builtin_ldexpf(1.0f, kTopExp - (int)pe_new);
       }
+      // Scales as the operands want them, finite so that a p of 0 stays 0: the bound only
+      // counts beside a scale that is 2^112 smaller, where p is below 2^-113, and for the
+      // blocks that are NaN or that the row does not see.
+      float vn[4];
+#pragma unroll
+      for (int blk = 0; blk < 4; ++blk) vn[blk] = __builtin_amdgcn_fmed3f(vs[blk] * pmul[n], -kMaxF32, kMaxF32);
       u32x4_t w[2];
       float sum = 0.0f;
 #pragma unroll
@@ -460,9 +472,7 @@ __global__ __launch_bounds__(64 * W) void attn_kv8_kernel(AttnArgs a) {
         for (int e = 0; e < 4; ++e) {
           const float x = __builtin_amdgcn_exp2f(s[n][blk][e] - base);
           sum += x;
-          pv[e] = x * vs[blk];
-          // a scale that holds a NaN, or was never written, stays out of rows that do not see its block
-          if (edge) pv[e] = s[n][blk][e] == kNegInf ? 0.0f : pv[e];
+          pv[e] = x * vn[blk];
         }
         w[blk >> 1][2 * (blk & 1)] = pack_f16(pv[0], pv[1]);
         w[blk >> 1][2 * (blk & 1) + 1] = pack_f16(pv[2], pv[3]);
@@ -482,7 +492,9 @@ __global__ __launch_bounds__(64 * W) void attn_kv8_kernel(AttnArgs a) {
     }
   }
   if (missing && a.status && lane == 0) atomicOr(a.status, QG_FLAG_PAGE);
-  const float vback = __uint_as_float((uint32_t)(ve - 13) << 23);     // 2^(ve - 140)
+  float vback[NT];
+#pragma unroll
+  for (int n = 0; n < NT; ++n) vback[n] = __builtin_ldexpf(1.0f, (int)pe[n] - kTopExp);
 
   auto store = [&](int64_t row, int d, const f32x4_t& v, float ll) {   // O / l of the output's row
     const float inv = ll == 0.0f ? 0.0f : 1.0f / ll;
@@ -503,7 +515,7 @@ __global__ __launch_bounds__(64 * W) void attn_kv8_kernel(AttnArgs a) {
 #pragma unroll
       for (int dt = 0; dt < DT; ++dt)
         store((r0 + t) * a.hq + h * a.group + g, 16 * dt + 4 * qd,
-              f32x4_t{o[n][dt][0] * vback, o[n][dt][1] * vback, o[n][dt][2] * vback, o[n][dt][3] * vback}, l[n]);
+              f32x4_t{o[n][dt][0] * vback[n], o[n][dt][1] * vback[n], o[n][dt][2] * vback[n], o[n][dt][3] * vback[n]}, l[n]);
     }
     return;
   }
@@ -526,7 +538,7 @@ __global__ __launch_bounds__(64 * W) void attn_kv8_kernel(AttnArgs a) {
     const float base = mm == kNegInf ? 0.0f : mm;
 #pragma unroll
     for (int w = 0; w < W; ++w) ll += sm_l[w][16 * n + i] * __builtin_amdgcn_exp2f(sm_m[w][16 * n + i] - base);
-    const float f = __builtin_amdgcn_exp2f(m[n] - base) * vback;
+    const float f = __builtin_amdgcn_exp2f(m[n] - base) * vback[n];
     if (n > 0) __syncthreads();
     if (!alone || wave == 0)
 #pragma unroll

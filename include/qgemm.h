@@ -449,7 +449,9 @@ int32_t qg_kv8_read(const int8_t *codes, const float *scales, int64_t pages, int
  * that sees no token (length 0, or a row before token 0) is zero.  Softmax and
  * sums are fp32; the products' operands are fp16: q scaled by a power of two
  * per row, the codes (exact), and probability times value scale, rounded once
- * to 11 bits (below 2^-27 of the row's largest: to 2^-38 of that).
+ * to 11 bits (where it is below 2^-27 of the largest that the row itself sees: to
+ * 2^-38 of that).  A key or value scale that is infinite or NaN makes the rows
+ * that see its block NaN, and no others.
  *   q        in : bf16 [rows, hq, d], strides as qg_qk_norm_rope
  *   max_q    in : no sequence has more query rows (later ones are not written)
  *   max_len  in : an upper bound of lens, for the choice of the split only

@@ -337,3 +337,120 @@ def test_weights_below_the_operands_range(dev, d, scale):
         got = ref.f64(qg.attn_kv8(q.to(dev), *f.args, scale=scale, splits=splits, out_dtype=torch.float32))
         tol = mass * (2.0 ** -8 + 2.0 ** -11) + n * 127 * 0.04 * 2.0 ** -38 + 1e-30
         assert (np.abs(got - want) <= tol).all(), float((np.abs(got - want) / tol).max())
+
+
+def operand_terms(f, q, counts, scale, window):
+    """Per output row and head in 64 bits: attention, sum p |v|, the largest p * value scale, the tokens
+    seen, and the largest |q| . |k|'s bound on a score's rounding (see operand_check)."""
+    hq, d = q.shape[1:]
+    hkv = f.host.hkv
+    group = hq // hkv
+    rows = sum(counts)
+    out, mass = np.zeros((rows, hq, d)), np.zeros((rows, hq, d))
+    top, seen, slip = np.zeros((rows, hq, 1)), np.zeros((rows, hq, 1)), np.zeros((rows, hq, 1))
+    at = 0
+    for b, (n, c) in enumerate(zip(f.lens, counts)):
+        k, v = f.host.values(b, n, 0), f.host.values(b, n, 1)
+        page = np.asarray(f.host.table[b])[np.arange(n) // 64]
+        sc = f.host.scales[page, :, :, np.arange(n) % 64 // 16].astype(np.float64)     # [n, hkv, 2]
+        for t in range(c):
+            end = n - c + t + 1
+            first = max(0, end - window) if window > 0 else 0
+            if end <= first:
+                continue
+            for h in range(hq):
+                g = h // group
+                s = k[first:end, g] @ q[at + t, h] * scale
+                p = np.exp(s - s.max())
+                p /= p.sum()
+                out[at + t, h], mass[at + t, h] = p @ v[first:end, g], p @ np.abs(v[first:end, g])
+                top[at + t, h], seen[at + t, h] = (p * sc[first:end, g, 1]).max(), end - first
+                size = np.abs(q[at + t, h]).sum() * sc[first:end, g, 0].max() * abs(scale)
+                slip[at + t, h] = d / 8 * 2.0 ** -24 * 1280 * size + 2.0 ** -22 * np.abs(s).max()
+        at += c
+    return out, mass, top, seen, slip
+
+
+def operand_check(y, terms, rows=slice(None)):
+    """fp32 output against the operands' promise, row by row.  p * scale is rounded once to 11 bits (2^-11 of
+    a term at most), and where that product is below 2^-27 of the row's largest, w, it is off by up to
+    2^-38 w for each token and code of up to 127.  A score is d / 8 sums of at most 1280 |q| in
+    binary32 (codes carry a bias of 1152), which moves numerator and denominator by its rounding each; the sums
+    over tokens add less than 2^-14 of the terms."""
+    out, mass, top, seen, slip = (t[rows] for t in terms)
+    got = ref.f64(y)[rows]
+    assert np.isfinite(got).all()
+    tol = mass * (2.0 ** -11 + 2.0 ** -14 + 2 * np.expm1(slip)) + seen * 127 * top * 2.0 ** -38
+    err = np.abs(got - out)
+    assert (err <= tol).all(), float((err / np.maximum(tol, 1e-300)).max())
+
+
+@pytest.mark.parametrize("d,hq,hkv", [(64, 4, 2), (128, 8, 1), (192, 2, 2), (256, 24, 1)])
+@pytest.mark.parametrize("rows,window", [(2, 0), (9, 0), (9, 7), (40, 30)])
+def test_a_large_value_block_leaves_rows_that_do_not_see_it_alone(dev, d, hq, hkv, rows, window):
+    """The value scale of one block is 2^40 times the others: rows before it, and rows whose window
+    has left it, keep every bit that they had without it."""
+    lens = [17, 50, 82, 131, 200]
+    f = Filled(dev, lens, hkv, d, d + rows)
+    for b, n in enumerate(lens):
+        blk = (n - 1) // 16 if window == 0 or b % 2 else max(0, n - rows - 3) // 16
+        f.host.scales[f.table[b, blk // 4].item(), :, 1, blk % 4] *= 2.0 ** 40
+    f.scales.copy_(torch.from_numpy(f.host.scales))
+    torch.manual_seed(rows + d)
+    q = torch.randn(len(lens) * rows, hq, d).bfloat16()
+    terms = operand_terms(f, ref.f64(q), [rows] * len(lens), 0.05, window)
+    for splits in (0, 1, 2):
+        operand_check(qg.attn_kv8(q.to(dev), *f.args, window=window, scale=0.05, splits=splits, out_dtype=torch.float32), terms)
+
+
+@pytest.mark.parametrize("d,hq,hkv", [(64, 4, 2), (128, 4, 1), (256, 17, 1)])
+@pytest.mark.parametrize("scale", [0.02, 1.0])
+def test_value_scales_of_any_size_beside_each_other(dev, d, hq, hkv, scale):
+    """Every block's value scale a different power of two: what a row needs is relative to its own largest
+    product of probability and scale, sharp softmaxes (scale 1) included."""
+    lens, rows = [1, 16, 40, 64, 150, 400], 3
+    f = Filled(dev, lens, hkv, d, d)
+    g = np.random.default_rng(d)
+    f.host.scales[:, :, 1] *= np.ldexp(1.0, g.integers(-60, 61, f.host.scales[:, :, 1].shape)).astype(np.float32)
+    f.scales.copy_(torch.from_numpy(f.host.scales))
+    torch.manual_seed(d)
+    q = torch.randn(len(lens) * rows, hq, d).bfloat16()
+    terms = operand_terms(f, ref.f64(q), [rows] * len(lens), scale, 0)
+    for splits in (0, 1, 3):
+        operand_check(qg.attn_kv8(q.to(dev), *f.args, scale=scale, splits=splits, out_dtype=torch.float32), terms)
+
+
+def test_a_missing_page_leaves_rows_that_do_not_see_it_alone(dev):
+    """Rows before the page that is not there, and rows whose window has left it, whatever page 0 holds."""
+    d, n, rows, window = 64, 420, 150, 205          # a wave has pages 1 and 5 of the same rows
+    f = Filled(dev, [n], 2, d, 31)
+    torch.manual_seed(31)
+    q = torch.randn(rows, 4, d).bfloat16()
+    terms = operand_terms(f, ref.f64(q), [rows], 0.05, window)
+    table = f.table_d.clone()
+    keep = table[0, 1].item()
+    table[0, 1] = -1
+    if 0 in table[0].tolist():                      # page 0 is this sequence's own: into the page left over
+        f.codes[keep], f.scales[keep] = f.codes[0].clone(), f.scales[0].clone()
+        table[0, table[0].tolist().index(0)] = keep
+    f.scales[0] = 2.0 ** 60
+    first = n - rows
+    sees = [first + t >= 64 and first + t - window + 1 <= 127 for t in range(rows)]
+    for splits in (0, 1, 2):
+        y = qg.attn_kv8(q.to(dev), f.codes, f.scales, table, f.lens_d, window=window, scale=0.05, splits=splits,
+                        out_dtype=torch.float32)
+        assert y.isnan().all(2).all(1).tolist() == sees
+        operand_check(y, terms, [t for t in range(rows) if not sees[t]])
+
+
+def test_an_infinite_scale_reaches_only_the_rows_that_see_it(dev):
+    f = Filled(dev, [100], 1, 128, 33)
+    page = f.table[0, 1].item()
+    q = torch.randn(40, 2, 128, device=dev).bfloat16()      # rows at tokens 60 .. 99
+    for which in (0, 1):
+        scales = f.scales.clone()
+        scales[page, 0, which, 1] = float("inf")             # tokens 80 .. 95
+        for splits in (1, 2):
+            y = qg.attn_kv8(q, f.codes, scales, f.table_d, f.lens_d, splits=splits)
+            assert y.isnan().all(2).all(1).tolist() == [t >= 80 for t in range(60, 100)]
+            assert not y[:20].isnan().any()
