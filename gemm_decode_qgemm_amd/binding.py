@@ -529,8 +529,9 @@ def kv8_append(k: torch.Tensor, v: torch.Tensor, codes: torch.Tensor, scales: to
                max_new: int | None = None, status: torch.Tensor | None = None) -> None:
     """Quantizes new keys and values [rows, hkv, d] into the cache as the last
     tokens of the sequences (lens counts them).  Rows of sequence b are
-    cu[b]..cu[b + 1] (cu given), or rows / b each; max_new bounds a sequence's
-    rows (default: all of them, which launches more workgroups than needed)."""
+    cu[b]..cu[b + 1] (cu given), or rows / b each; with cu, max_new bounds a
+    sequence's rows, and those from max_new on are not written (default: all
+    rows, which launches more workgroups than needed)."""
     dev, pages, hkv, d, b, width = _cache(codes, scales, block_table, lens)
     shape = k.shape
     if not (len(shape) == 3 and shape[1] == hkv and shape[2] == d and v.shape == shape and k.dtype is _BF16 and

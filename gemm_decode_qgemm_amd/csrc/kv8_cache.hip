@@ -35,6 +35,7 @@ struct AppendArgs {
   Kv8Args c;
   const uint16_t *k, *v;
   int64_t k_ts, k_hs, v_ts, v_hs;
+  int64_t max_new;
   uint32_t* status;
 };
 
@@ -113,10 +114,12 @@ __global__ __launch_bounds__(256) void kv8_append_kernel(AppendArgs a) {
   const int b = blockIdx.x / a.c.hkv, h = blockIdx.x % a.c.hkv;
   int64_t r0, n;
   kv8_rows(a.c.cu, a.c.rows, a.c.b, b, r0, n);
-  const int64_t len = a.c.lens[b];
-  if (n <= 0 || len <= 0) return;
-  const int64_t first = len > n ? len - n : 0;   // first token written
-  const int64_t shift = r0 - (len - n);          // row of token j: j + shift
+  const int64_t total = a.c.lens[b];
+  if (n <= 0 || total <= 0) return;
+  const int64_t first = total > n ? total - n : 0;   // first token written
+  const int64_t shift = r0 - (total - n);            // row of token j: j + shift
+  const int64_t len = total - n + min(n, a.max_new); // and the end of those written: rows past max_new are not
+  if (len <= first) return;
   const int64_t pi = first / kPage + blockIdx.y;
   if (pi * kPage >= len) return;
   const int page = kv8_page(a.c.table + (size_t)b * a.c.width, a.c.width, a.c.pages, pi);
@@ -334,7 +337,8 @@ __global__ __launch_bounds__(256) void kv8_read_kernel(ReadArgs a) {
 
 hipError_t launch_kv8_append(const Kv8Args& c, const void* k, int64_t k_ts, int64_t k_hs, const void* v, int64_t v_ts,
                              int64_t v_hs, int64_t max_new, uint32_t* status, hipStream_t stream) {
-  const AppendArgs a{c, static_cast<const uint16_t*>(k), static_cast<const uint16_t*>(v), k_ts, k_hs, v_ts, v_hs, status};
+  const AppendArgs a{c, static_cast<const uint16_t*>(k), static_cast<const uint16_t*>(v), k_ts, k_hs, v_ts, v_hs, max_new,
+                     status};
   // max_new tokens that start anywhere in a page reach at most this many pages
   const dim3 grid((uint32_t)(c.b * c.hkv), (uint32_t)((max_new + kPage - 2) / kPage + 1));
   switch (c.d) {

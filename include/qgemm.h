@@ -426,7 +426,8 @@ int32_t qg_qk_norm_rope(const void *q, int64_t q_token_stride, int64_t q_head_st
  * same rows again changes nothing.  A page belongs to one sequence of a call.
  *   k, v       in : bf16 [rows, hkv, d], strides as qg_qk_norm_rope
  *   lens       in : lengths with the new tokens counted
- *   max_new    in : no sequence has more new rows (later ones are not written)
+ *   max_new    in : no sequence has more new rows (a sequence's rows from
+ *                   max_new on are not written)
  *   status_dev    : QG_FLAG_NONFINITE, QG_FLAG_PAGE; may be NULL
  * Errors: QG_E_NULL, QG_E_SHAPE, QG_E_HEADS, QG_E_STRIDE, QG_E_ALIGN. */
 int32_t qg_kv8_append(const void *k, int64_t k_token_stride, int64_t k_head_stride, const void *v,

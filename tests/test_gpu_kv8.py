@@ -218,3 +218,50 @@ def test_offsets_past_32_bits(dev):
     assert torch.equal(qg.attn_kv8(q, codes, scales, far, lens), qg.attn_kv8(q, small, small_s, near, lens))
     a, b = qg.kv8_read(codes, scales, far, lens, 100), qg.kv8_read(small, small_s, near, lens, 100)
     assert torch.equal(a[0], b[0]) and torch.equal(a[1], b[1])
+
+
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("most", [1, 2, 15, 40, 64, 65])
+def test_rows_past_max_new_are_not_written(dev, d, most):
+    """Every sequence's first max_new rows and no more, wherever a page or a block begins."""
+    olds, counts = [0, 1, 30, 64, 100], [40, 200, 3, 130, 64]
+    p = Pair(dev, 5, 5, 2, d, d + most)
+    p.append(olds)
+    rows = torch.randn(sum(counts), 2, 2, d, generator=p.g).bfloat16()
+    before = p.codes.clone(), p.scales.clone()
+    cu = np.cumsum([0] + counts)
+    lens = torch.tensor([o + c for o, c in zip(olds, counts)], dtype=torch.int32, device=dev)
+    qg.kv8_append(rows[:, 0].to(dev), rows[:, 1].to(dev), p.codes, p.scales, p.table_d, lens,
+                  cu=torch.tensor(cu, dtype=torch.int32, device=dev), max_new=most, status=p.flag)
+    written = torch.zeros(p.scales.shape, dtype=torch.bool)
+    for b, (o, c) in enumerate(zip(olds, counts)):
+        n = min(c, most)
+        p.host.append(b, o, rows[cu[b]:cu[b] + n, 0].float().numpy(), rows[cu[b]:cu[b] + n, 1].float().numpy())
+        p.lens[b] = o + n
+        for blk in range(o // 16, (o + n + 15) // 16):
+            written[p.table[b, blk // 4], :, :, blk % 4] = True
+    p.check()
+    assert p.flag.item() == 0
+    written = written.to(dev)
+    assert torch.equal(p.scales[~written], before[1][~written])
+    keys = (p.codes[:, :, 0] != before[0][:, :, 0]).view(-1, 2, 4, 16, d).any(4).any(3)
+    values = (p.codes[:, :, 1] != before[0][:, :, 1]).view(-1, 2, d, 4, 4, 4).any(5).any(3).any(2)
+    assert not (keys & ~written[:, :, 0]).any() and not (values & ~written[:, :, 1]).any()
+
+
+def test_max_new_counts_rows_before_the_first_token_too(dev):
+    """40 rows of a sequence of 33 tokens: its first 7 rows are before token 0."""
+    p = Pair(dev, 1, 2, 1, 64, 6)
+    rows = torch.randn(40, 2, 1, 64, generator=p.g).bfloat16()
+    for most, n in ((7, 0), (10, 3), (39, 32)):
+        p.codes.zero_(), p.scales.zero_(), p.host.codes.fill(0), p.host.scales.fill(0)
+        lens = torch.tensor([33], dtype=torch.int32, device=dev)
+        qg.kv8_append(rows[:, 0].to(dev), rows[:, 1].to(dev), p.codes, p.scales, p.table_d, lens,
+                      cu=torch.tensor([0, 40], dtype=torch.int32, device=dev), max_new=most)
+        if n:
+            p.host.append(0, 0, rows[7:7 + n, 0].float().numpy(), rows[7:7 + n, 1].float().numpy())
+        p.lens = [n]
+        p.check()
+        fresh = torch.ones(8, dtype=torch.bool)              # blocks of the sequence's two pages
+        fresh[:(n + 15) // 16] = False
+        assert not p.scales[p.table[0].long()].permute(0, 3, 1, 2).flatten(0, 1)[fresh].any()
