@@ -98,20 +98,23 @@ __global__ __launch_bounds__(256) void qk_norm_rope_kernel(NormRopeArgs a) {
     }
 #pragma unroll
     for (int o = 1; o < LPH; o *= 2) ss += __shfl_xor(ss, o);
-    float r = 1.0f / sqrtf(ss * a.inv_d + a.eps);
-    if (__ballot(ss == __builtin_inff()) != 0) {
-      // Channels from 2^63 on: their squares leave binary32, so the sum is
-      // taken of x 2^-72 for the heads that overflowed (eps is nothing there).
-      float big = 0.0f;
+    const float mean = ss * a.inv_d + a.eps;
+    float r = 1.0f / sqrtf(mean);
+    // Channels from 2^63 on, and small ones where eps is no larger: their squares leave
+    // binary32, so such heads are taken times 2^-72 or 2^72, which the norm takes off again.
+    const float c = ss == __builtin_inff() ? 0x1p-72f : mean < 0x1p-90f ? 0x1p72f : 1.0f;
+    if (__ballot(c != 1.0f) != 0) {
+      ss = 0.0f;
 #pragma unroll
       for (int e = 0; e < 8; ++e) {
-        const float u = x0[e] * 0x1p-72f, v = x1[e] * 0x1p-72f;
-        big = __builtin_fmaf(u, u, big);
-        big = __builtin_fmaf(v, v, big);
+        x0[e] *= c;
+        x1[e] *= c;
+        ss = __builtin_fmaf(x0[e], x0[e], ss);
+        ss = __builtin_fmaf(x1[e], x1[e], ss);
       }
 #pragma unroll
-      for (int o = 1; o < LPH; o *= 2) big += __shfl_xor(big, o);
-      if (ss == __builtin_inff()) r = 0x1p-72f / sqrtf(big * a.inv_d);
+      for (int o = 1; o < LPH; o *= 2) ss += __shfl_xor(ss, o);
+      r = 1.0f / sqrtf(ss * a.inv_d + a.eps * c * c);
     }
     if (bad) r = __uint_as_float(0x7fc00000u);
 #pragma unroll

@@ -144,3 +144,34 @@ def test_side_stream_graph_and_empty_call(dev):
         assert torch.equal(out[0], want[0]) and torch.equal(out[1], want[1])
     e = qg.qk_norm_rope(q[:0], k[:0], None, None, cs, pos[:0])
     assert e[0].shape == (0, 8, 128)
+
+
+@pytest.mark.parametrize("d", [64, 128, 512])
+def test_channels_whose_squares_leave_binary32(dev, d):
+    """Heads of one magnitude from bf16's smallest normal numbers to its largest: the norm makes all of them
+    of size one.  Without eps where the channels are small, as any eps would be larger than they are."""
+    torch.manual_seed(d)
+    cs, pos = table(5, d), torch.tensor([0, 4, 2, 3], dtype=torch.int32, device=dev)
+    for size in (1e-37, 1e-30, 1e-24, 1e-20, 1e-18, 1e-10, 1.0, 1e10, 1e18, 3e18, 1e19, 1e30, 8e37):
+        q = (torch.randn(4, 3, d).clamp(-4, 4) * size).bfloat16()
+        for eps in ((0.0,) if size < 1e-9 else (0.0, 1e-6)):
+            yq, yk = qg.qk_norm_rope(q.to(dev), q[:, :1].contiguous().to(dev), None, None, cs.to(dev), pos, eps=eps)
+            check(yq, q, None, cs, pos, eps, False)
+            assert torch.equal(yk, yq[:, :1])
+    # one channel at the largest value of bf16 beside ordinary ones, in one head of three
+    q = torch.randn(4, 3, d).bfloat16()
+    q[:, 1, 3] = torch.finfo(torch.bfloat16).max
+    yq, _ = qg.qk_norm_rope(q.to(dev), q[:, :1].contiguous().to(dev), None, None, cs.to(dev), pos)
+    check(yq, q, None, cs, pos, 1e-6, False)
+
+
+def test_small_heads_beside_a_small_eps(dev):
+    """eps of the size of the mean square: both count."""
+    torch.manual_seed(9)
+    d = 128
+    cs, pos = table(3, d), torch.tensor([2, 1], dtype=torch.int32, device=dev)
+    for size, eps in ((1e-20, 1e-40), (1e-19, 1e-38), (1e-17, 1e-34), (1e-17, 0.0), (1e-14, 1e-28)):
+        q = (torch.randn(2, 2, d) * size).bfloat16()
+        yq, _ = qg.qk_norm_rope(q.to(dev), q[:, :1].contiguous().to(dev), None, None, cs.to(dev), pos, eps=eps)
+        e = float(torch.tensor(eps, dtype=torch.float32))        # as the call takes it
+        check(yq, q, None, cs, pos, e, False)
