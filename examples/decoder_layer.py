@@ -37,6 +37,8 @@ class DecoderLayer:
 
     def __init__(self, batch, max_len, *, hidden=1024, hq=16, hkv=4, d=64, experts=16, top_k=4, inter=512, seed=0,
                  device="cuda"):
+        if not 1 <= batch <= qg.binding.MAX_M:
+            raise ValueError(f"a step has a row for every sequence and the linears take 1 to {qg.binding.MAX_M}, got {batch}")
         g = torch.Generator(device=device).manual_seed(seed)
 
         def weight(n, k):

@@ -3,6 +3,9 @@ before anything is launched.  No call here reaches a kernel (each carries a
 definite argument error, or has nothing to do), so these run without a GPU."""
 from __future__ import annotations
 
+import importlib.util
+import os
+
 import pytest
 import torch
 
@@ -150,3 +153,14 @@ def test_attn_workspace_of_shared_out_splits():
     for n in (0, 1, 63, 64, 65, 257):
         assert qg.attn_kv8_workspace_bytes(3, 3, 8, 2, 64, 1, n) >= 0
         assert qg.attn_kv8_workspace_bytes(3, 3, 8, 2, 256, 1, n) >= 0
+
+
+@pytest.mark.parametrize("batch", [0, 65, 1000])
+def test_the_example_refuses_batches_that_no_step_takes(batch):
+    """Before any weight is made, not in the middle of a prompt."""
+    path = os.path.join(os.path.dirname(os.path.dirname(os.path.abspath(__file__))), "examples", "decoder_layer.py")
+    spec = importlib.util.spec_from_file_location("decoder_layer_example", path)
+    example = importlib.util.module_from_spec(spec)
+    spec.loader.exec_module(example)
+    with pytest.raises(ValueError, match="1 to 64"):
+        example.DecoderLayer(batch, 100, device="cpu")
