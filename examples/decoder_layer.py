@@ -100,6 +100,13 @@ class DecoderLayer:
         return torch.stack(last)
 
 
+def prompt_lengths(longest: int, batch: int) -> list:
+    """Ragged prompts of at least one token."""
+    if longest < 1:
+        raise ValueError("a prompt has at least one token")
+    return [max(1, longest - 3 * (b % 5)) for b in range(batch)]
+
+
 def main() -> None:
     p = argparse.ArgumentParser(description=__doc__, formatter_class=argparse.RawDescriptionHelpFormatter)
     p.add_argument("--batch", type=int, default=8)
@@ -110,7 +117,7 @@ def main() -> None:
     dev = torch.device("cuda")
     layer = DecoderLayer(a.batch, a.prompt + a.steps + 8)
     torch.manual_seed(1)
-    x = layer.prompts([torch.randn(a.prompt - 3 * (b % 5), layer.hidden, device=dev).bfloat16() for b in range(a.batch)])
+    x = layer.prompts([torch.randn(n, layer.hidden, device=dev).bfloat16() for n in prompt_lengths(a.prompt, a.batch)])
     one = torch.ones(a.batch, dtype=torch.int32, device=dev)
     step = lambda: x.copy_(rms(layer.forward(x, one, None, 1)))   # noqa: E731
     if a.graph:

@@ -155,12 +155,24 @@ def test_attn_workspace_of_shared_out_splits():
         assert qg.attn_kv8_workspace_bytes(3, 3, 8, 2, 256, 1, n) >= 0
 
 
+def example():
+    path = os.path.join(os.path.dirname(os.path.dirname(os.path.abspath(__file__))), "examples", "decoder_layer.py")
+    spec = importlib.util.spec_from_file_location("decoder_layer_example", path)
+    module = importlib.util.module_from_spec(spec)
+    spec.loader.exec_module(module)
+    return module
+
+
 @pytest.mark.parametrize("batch", [0, 65, 1000])
 def test_the_example_refuses_batches_that_no_step_takes(batch):
     """Before any weight is made, not in the middle of a prompt."""
-    path = os.path.join(os.path.dirname(os.path.dirname(os.path.abspath(__file__))), "examples", "decoder_layer.py")
-    spec = importlib.util.spec_from_file_location("decoder_layer_example", path)
-    example = importlib.util.module_from_spec(spec)
-    spec.loader.exec_module(example)
     with pytest.raises(ValueError, match="1 to 64"):
-        example.DecoderLayer(batch, 100, device="cpu")
+        example().DecoderLayer(batch, 100, device="cpu")
+
+
+def test_the_example_takes_short_prompts():
+    lengths = example().prompt_lengths
+    assert lengths(100, 7) == [100, 97, 94, 91, 88, 100, 97]
+    assert lengths(1, 6) == [1] * 6 and lengths(7, 5) == [7, 4, 1, 1, 1]
+    with pytest.raises(ValueError):
+        lengths(0, 3)
