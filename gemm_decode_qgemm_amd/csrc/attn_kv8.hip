@@ -25,7 +25,8 @@
 //    weighs, round the row's own products away).
 // As bf16 the same products took 1.5 instructions per code and p * vs had to be
 // two operands for this accuracy: 32 sequences of 4096 tokens on 32 / 8 heads of
-// 128 ran 60 us, now 46 us (5.85 TB/s).
+// 128 in two splits ran 60 us, and 46 once in fp16.  Today they take 48 us (5.6 TB/s),
+// 46 (5.85) in one split, which a caller who knows that they are equal can ask for.
 //
 // Mapping (gfx950, wave64, v_mfma_f32_16x16x32_f16):
 //  * the rows of one key/value head are its query rows times its query heads;
@@ -61,7 +62,8 @@ struct AttnArgs {
   int out_f32;
   float *part_o, *part_ml;          // [splits][rows * hq][d], [splits][rows * hq][2]; balanced: see slots
   int slots;                        // > 0: splits are shared out by length, [slots][max_q * hq] partial results
-  int32_t* plan;                    // then [b][2]: a sequence's first slot and their number
+  int even;                         // then: the splits of each sequence where all are about as long,
+  int32_t* plan;                    // and [b][2]: a sequence's first slot and their number
   uint32_t* status;
 };
 
@@ -141,6 +143,17 @@ __device__ __forceinline__ int wave_scan(int v) {
   return v;
 }
 
+// The largest of the wave's numbers, none of them negative.
+__device__ __forceinline__ int wave_top(int v) {
+  v = max(v, __builtin_amdgcn_update_dpp(0, v, 0x111, 0xf, 0xf, false));
+  v = max(v, __builtin_amdgcn_update_dpp(0, v, 0x112, 0xf, 0xf, false));
+  v = max(v, __builtin_amdgcn_update_dpp(0, v, 0x114, 0xf, 0xf, false));
+  v = max(v, __builtin_amdgcn_update_dpp(0, v, 0x118, 0xf, 0xf, false));
+  v = max(v, __builtin_amdgcn_update_dpp(0, v, 0x142, 0xa, 0xf, false));
+  v = max(v, __builtin_amdgcn_update_dpp(0, v, 0x143, 0xc, 0xf, false));
+  return __builtin_amdgcn_readlane(v, 63);
+}
+
 // The last page worth reading for rows that end before token `end`.  Beyond the
 // table: a page that is not there for every row that sees such a token, which is
 // the first one past the table or the first one of the row's window.
@@ -176,13 +189,21 @@ __device__ __forceinline__ bool attn_plan(const AttnArgs& a, int j, bool tell, i
   auto more = [&](int u) { return mine + u < nb ? pages(mine + u, a.c.lens[mine + u]) : 0; };
   auto parts = [](int p, int c) { return min((int)((uint32_t)(p + c - 1) / (uint32_t)c), kMaxSplits); };
   const int len0 = mine < nb ? a.c.lens[mine] : 0, p0 = mine < nb ? pages(mine, len0) : 0;
-  int sum = p0;
-  for (int u = 1; u < per; ++u) sum += more(u);
+  int sum = p0, most = p0;
+  for (int u = 1; u < per; ++u) {
+    const int p = more(u);
+    sum += p;
+    most = max(most, p);
+  }
+  most = wave_top(most);
   const int total = __builtin_amdgcn_readlane(wave_scan(sum), 63);
   const int busy = min(nb, per * (int)__popcll(__ballot(sum > 0)));
   // each sequence leaves half a C of its last slot unused
   const int room = a.slots - (busy >> 1);
   int c = max(kWaves, (total + room - 1) / room), cnt, incl;
+  // Lengths within an eighth of the longest: the even split, with fewer parts to join
+  // (32 sequences of 4096 tokens: 48 us against 52).
+  if ((int64_t)most * busy * 7 <= (int64_t)total * 8) c = max(c, (most + a.even - 1) / a.even);
   while (true) {
     cnt = parts(p0, c);
     for (int u = 1; u < per; ++u) cnt += parts(more(u), c);
@@ -777,7 +798,10 @@ static int attn_splits(int64_t b, int hkv, int d, int64_t rows_per_head, int64_t
 // its sequence first (about 1 us), and equal splits of up to five pages a wave
 // leave little to gain (1 sequence of 60000 tokens and 31 of 100..600, 32 / 8
 // heads of 128: 40 us against 416; 48 of 10..4095 in any order: 45 against 60;
-// 16 of 10..8192 on 64 / 8: 31 against 42; 32 equal ones of 4096: 52 against 50).
+// 16 of 10..8192 on 64 / 8: 31 against 42).  Sequences of about one length get the even
+// split all the same: 32 of 4096 take 48 us with the preparation and a join that finds
+// nothing, against 46 for one split from the start, which 32 of 10..4096 pay with 38
+// against 34.
 // As many slots as workgroups are resident at once: with 2 a CU instead of 3 the
 // 48 take 52 us, with 4 they take 47.
 AttnSplit attn_kv8_split(int64_t b, int64_t rows, int hkv, int d, int64_t rows_per_head, int64_t max_len, int window,
@@ -791,7 +815,7 @@ AttnSplit attn_kv8_split(int64_t b, int64_t rows, int hkv, int d, int64_t rows_p
   if (units * b >= 4 * resident(d, nt) * kCUs && rows_per_head > 16 * nt) return {1, 0};
   if (max_q * b > 2 * rows || seen_pages(max_len, window, max_q) <= 5 * kWaves * s || slots > 65535)
     return {s, 0};
-  return {1, (int)slots};
+  return {s, (int)slots};
 }
 
 template <int D, int NT, bool SHARED, bool ROWS = false>
@@ -822,12 +846,12 @@ hipError_t launch_attn_kv8(const Kv8Args& c, const void* q, int64_t q_ts, int64_
   const int64_t rows_per_head = (int64_t)max_q * group;
   const int nt = attn_kv8_nt(rows_per_head);
   const int64_t pages = seen_pages(max_len, window, max_q);
-  const int splits = by.splits;
+  const int splits = by.slots > 0 ? 1 : by.splits;
   const int chunk = pages > splits ? (int)((pages + splits - 1) / splits) : 1;
   AttnArgs a{c, static_cast<const uint16_t*>(q), q_ts, q_hs, hq, group, max_q, window, splits, chunk,
              (int)((rows_per_head + 16 * nt - 1) / (16 * nt)), group > 1 ? (uint32_t)(((uint64_t)1 << 32) / group) : 0u,
              scale * 1.44269504088896340736f, out, out_f32,
-             part, nullptr, by.slots, nullptr, status};
+             part, nullptr, by.slots, by.splits, nullptr, status};
   if (part) {
     const size_t partial = (by.slots > 0 ? (size_t)by.slots * max_q : (size_t)splits * c.rows) * hq;
     a.part_ml = part + partial * c.d;

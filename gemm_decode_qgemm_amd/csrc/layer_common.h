@@ -70,7 +70,9 @@ __device__ __forceinline__ void kv8_rows(const int32_t* cu, int64_t rows, int nb
   }
 }
 
-// How qg_attn_kv8 splits the pages of its sequences (attn_kv8.hip).
+// How qg_attn_kv8 splits the pages of its sequences (attn_kv8.hip): each in `splits`,
+// or over `slots` workgroups by their lengths where slots > 0 (`splits` where those
+// turn out to be about equal).
 struct AttnSplit {
   int splits, slots;
 };

@@ -454,3 +454,34 @@ def test_an_infinite_scale_reaches_only_the_rows_that_see_it(dev):
             y = qg.attn_kv8(q, f.codes, scales, f.table_d, f.lens_d, splits=splits)
             assert y.isnan().all(2).all(1).tolist() == [t >= 80 for t in range(60, 100)]
             assert not y[:20].isnan().any()
+
+
+@pytest.mark.parametrize("b,hq,hkv,d,rows,lo,hi,width", [
+    (33, 8, 8, 64, 1, 1400, 1400, 90),       # all of one length
+    (20, 16, 8, 128, 2, 900, 1000, 120),     # within an eighth
+    (20, 8, 8, 256, 1, 800, 1000, 60),       # just outside it, and too few pages to share out
+    (20, 8, 8, 256, 1, 800, 1000, 200),
+    (70, 8, 4, 64, 1, 640, 700, 120),        # two sequences to a lane that plans
+    (130, 4, 4, 64, 1, 130, 140, 200),
+])
+@pytest.mark.parametrize("window", [0, 500])
+def test_sequences_of_about_one_length_under_a_wide_table(dev, b, hq, hkv, d, rows, lo, hi, width, window):
+    """The splits are planned on the GPU, which finds the lengths to be about equal."""
+    lens = [lo + (hi - lo) * i // (b - 1) for i in range(b)]
+    f = Filled(dev, lens, hkv, d, b, spare=width - -(-hi // 64))
+    torch.manual_seed(b)
+    q = torch.randn(b * rows, hq, d).bfloat16()
+    want, mass = f.reference(ref.f64(q), [rows] * b, d ** -0.5, window)
+    need = qg.attn_kv8_workspace_bytes(b, b * rows, hq, hkv, d, rows, width * 64, window=window)
+    ws = torch.full((need + 16,), 255, dtype=torch.uint8, device=dev)
+    y = qg.attn_kv8(q.to(dev), *f.args, window=window, out_dtype=torch.float32, workspace=ws[:need])
+    check(y, want, mass)
+    assert (ws[need:] == 255).all()
+    if window == 0 and width > 60:
+        assert need % (hq * (d + 2) * 4) == b * 8            # the plan's bytes: this is the shared-out form
+    for keep in (1, b // 2):                                  # empty sequences among them
+        some = f.lens_d.clone()
+        some[keep:] = 0
+        z = qg.attn_kv8(q.to(dev), *f.args[:3], some, window=window, out_dtype=torch.float32)
+        check(z[:keep * rows], want[:keep * rows], mass[:keep * rows])
+        assert not z[keep * rows:].any()
