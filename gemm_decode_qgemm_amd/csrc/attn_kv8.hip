@@ -240,18 +240,18 @@ __device__ __forceinline__ bool attn_plan(const AttnArgs& a, int j, bool tell, i
 
 // SHARED: a.slots > 0.  ROWS: each wave takes a row tile of its own through all
 // pages, and row_tiles counts fours of them (one split).
-template <int D, int NT, bool SHARED, bool ROWS, int W = kWaves>
-__global__ __launch_bounds__(64 * W) void attn_kv8_kernel(AttnArgs a) {
+template <int D, int NT, bool SHARED, bool ROWS>
+__global__ __launch_bounds__(64 * kWaves) void attn_kv8_kernel(AttnArgs a) {
   constexpr int KC = D / 64;        // 64-channel chunks of a key
   constexpr int DT = D / 16;        // 16-channel tiles of a value
   constexpr bool kEarlyV = D <= 192 && D * NT <= 256;   // values in flight with the keys, where registers allow
-  __shared__ float sm_m[ROWS ? 1 : W][16 * NT], sm_l[ROWS ? 1 : W][16 * NT];
-  __shared__ f32x4_t sm_o[ROWS ? 1 : W][DT][64];
+  __shared__ float sm_m[ROWS ? 1 : kWaves][16 * NT], sm_l[ROWS ? 1 : kWaves][16 * NT];
+  __shared__ f32x4_t sm_o[ROWS ? 1 : kWaves][DT][64];
   const int lane = threadIdx.x & 63, i = lane & 15, qd = lane >> 4;
   const int wave = wave_id_uniform();
   // Splits slowest: workgroups go to the 8 XCDs in turn, and the late splits
   // of short sequences, which are empty, must not all fall to the same ones.
-  const int h = blockIdx.x / a.row_tiles, rt = ROWS ? blockIdx.x % a.row_tiles * W + wave : blockIdx.x % a.row_tiles;
+  const int h = blockIdx.x / a.row_tiles, rt = ROWS ? blockIdx.x % a.row_tiles * kWaves + wave : blockIdx.x % a.row_tiles;
   int b = blockIdx.y, split = blockIdx.z, splits = a.splits, len;
   if constexpr (SHARED) {
     const bool tell = blockIdx.x == 0 && blockIdx.y == 0 && wave == 0;
@@ -311,7 +311,7 @@ __global__ __launch_bounds__(64 * W) void attn_kv8_kernel(AttnArgs a) {
 
   const bool alone = !ROWS && p_end - p_beg <= 1;    // one wave has the only page
   const int first_page = p_beg + (ROWS ? 0 : wave);
-  constexpr int kStep = ROWS ? 1 : W;
+  constexpr int kStep = ROWS ? 1 : kWaves;
 
   // Rows of this lane, as fp16 q 2^(8 - e) with 2^e just above the row's
   // largest channel: exact but for channels 2^-21 of that one.  The keys'
@@ -555,10 +555,10 @@ __global__ __launch_bounds__(64 * W) void attn_kv8_kernel(AttnArgs a) {
   for (int n = 0; n < NT; ++n) {
     float mm = kNegInf, ll = 0.0f;
 #pragma unroll
-    for (int w = 0; w < W; ++w) mm = fmaxf(mm, sm_m[w][16 * n + i]);
+    for (int w = 0; w < kWaves; ++w) mm = fmaxf(mm, sm_m[w][16 * n + i]);
     const float base = mm == kNegInf ? 0.0f : mm;
 #pragma unroll
-    for (int w = 0; w < W; ++w) ll += sm_l[w][16 * n + i] * __builtin_amdgcn_exp2f(sm_m[w][16 * n + i] - base);
+    for (int w = 0; w < kWaves; ++w) ll += sm_l[w][16 * n + i] * __builtin_amdgcn_exp2f(sm_m[w][16 * n + i] - base);
     const float f = __builtin_amdgcn_exp2f(m[n] - base) * vback[n];
     if (n > 0) __syncthreads();
     if (!alone || wave == 0)
@@ -571,11 +571,11 @@ __global__ __launch_bounds__(64 * W) void attn_kv8_kernel(AttnArgs a) {
     const int64_t row = (r0 + t) * a.hq + h * a.group + g;     // row of the output
     const size_t prow = (part0 + t) * a.hq + h * a.group + g;
     const bool on = r < nrows;
-    for (int dt = wave; dt < DT; dt += W) {
+    for (int dt = wave; dt < DT; dt += kWaves) {
       f32x4_t v = sm_o[0][dt][lane];
       if (!alone)
 #pragma unroll
-        for (int w = 1; w < W; ++w) {
+        for (int w = 1; w < kWaves; ++w) {
           const f32x4_t u = sm_o[w][dt][lane];
           v = f32x4_t{v[0] + u[0], v[1] + u[1], v[2] + u[2], v[3] + u[3]};
         }
