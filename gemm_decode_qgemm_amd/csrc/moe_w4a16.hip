@@ -963,9 +963,11 @@ hipError_t launch_moe_w4a16(const void* x, int t, int h, const void* router, int
   // and 73, at 3 of 16 experts of 3840 x 2560 75.6 against 70.7).
   const bool thin = few || 2 * t * k <= 5 * e;
   // Up to kOwnTokens tokens, ranking takes a workgroup of the gate and up launch about
-  // 1 us, which is less than a launch while all of them run at once (4 tokens, 2 of 8
-  // of 3840 x 1024, 480 workgroups: 20.2 us against 22.6; 7 tokens, 8 of 128 of 768 x
-  // 4096, 672: 82 against 78; 5, 4 of 16 of 10496 x 2048, 2624: 112 against 102).
+  // 1 us, which is less than a launch while all of them run at once (thin: 4 tokens, 2 of
+  // 8 of 3840 x 1024, 960 workgroups: 18.3 us against 20.3; 6, 4 of 32 of 1280 x 2048, 960:
+  // 30.7 against 32.7; 7, 8 of 128 of 768 x 4096, 1344: 64.8 against 63.5; 5, 4 of 16 of
+  // 10496 x 2048, 6560: 107 against 89; else: 8, 4 of 8 of 4096 x 2048, 512: 38.1 against
+  // 39.3; of 5120, 640: 49.0 against 48.0).
   a.own = t <= kOwnTokens && inter / (thin ? 32 : 64) * (a.direct ? e : t * k) <= (thin ? 4 : 2) * kCUs;
   const int units = a.direct || (!a.own && t * k > e) ? e : t * k;
   if (!a.own) {
