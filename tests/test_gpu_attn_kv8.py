@@ -485,3 +485,38 @@ def test_sequences_of_about_one_length_under_a_wide_table(dev, b, hq, hkv, d, ro
         z = qg.attn_kv8(q.to(dev), *f.args[:3], some, window=window, out_dtype=torch.float32)
         check(z[:keep * rows], want[:keep * rows], mass[:keep * rows])
         assert not z[keep * rows:].any()
+
+
+@pytest.mark.parametrize("d,hq,hkv", [(64, 4, 4), (128, 8, 2), (192, 3, 1), (256, 6, 2)])
+def test_probability_times_scale_keeps_eleven_bits(dev, d, hq, hkv):
+    """One to three tokens, nearly equal weights: the operand's rounding is all there is, and no average hides
+    it.  The same product in the 8 bits of bf16 is outside the bound."""
+    lens = [1, 2, 3, 1, 2, 3, 17, 1]
+    f = Filled(dev, lens, hkv, d, 2 * d)
+    torch.manual_seed(d)
+    q = torch.randn(len(lens), hq, d).bfloat16()
+    terms = operand_terms(f, ref.f64(q), [1] * len(lens), 1e-3, 0)
+    for splits in (0, 1, 2):
+        operand_check(qg.attn_kv8(q.to(dev), *f.args, scale=1e-3, splits=splits, out_dtype=torch.float32), terms)
+    with pytest.raises(AssertionError):
+        coarse = f.host.scales.copy()
+        f.host.scales[:, :, 1] = torch.from_numpy(coarse[:, :, 1]).bfloat16().float().numpy()
+        rounded = operand_terms(f, ref.f64(q), [1] * len(lens), 1e-3, 0)[0]
+        operand_check(torch.from_numpy(rounded), terms)
+
+
+@pytest.mark.parametrize("hq,hkv,d", [(12, 2, 64), (8, 1, 128), (10, 2, 192), (5, 1, 256)])
+@pytest.mark.parametrize("window", [0, 1, 50])
+def test_every_output_of_many_rows_on_short_sequences(dev, hq, hkv, d, window):
+    """The sequences of test_many_rows_on_short_sequences with the operands' own bound, which also holds where a
+    token with nearly all of the weight has a zero code."""
+    lens, counts = [128, 0, 1, 64, 77, 20], [40, 3, 9, 0, 61, 64]
+    f = Filled(dev, lens, hkv, d, d, spare=0)
+    torch.manual_seed(d + window)
+    q = torch.randn(sum(counts), hq, d).bfloat16()
+    terms = operand_terms(f, ref.f64(q), counts, 0.15, window)
+    y = qg.attn_kv8(q.to(dev), *f.args, cu=cu_of(counts, dev), max_q=64, window=window, scale=0.15, out_dtype=torch.float32)
+    operand_check(y, terms)
+    assert not y[torch.from_numpy(terms[1].sum(-1) == 0).to(dev)].any()
+    z = qg.attn_kv8(q.to(dev), *f.args, cu=cu_of(counts, dev), max_q=64, window=window, scale=0.15)
+    assert torch.equal(z, y.bfloat16())
