@@ -220,3 +220,49 @@ def test_experts_past_4_gib(dev):
     y = qg.moe_w4a16(x[:1], router, gu, dn, inter, 1)
     z = qg.moe_w4a16(x[:1], router[-1:], one[0][None], one[1][None], inter, 1)
     assert torch.equal(y, z) and y.any()
+
+
+def one_term_weights(n, k, rows, cols, seed):
+    """A packed n x k weight whose row r has one value that is not zero, at cols[r] (rows alone), and its values
+    in 64 bits.  Codes of 8 with zero points of 8 are zeros; the others are 4 to 7 steps away from it."""
+    g = np.random.default_rng(seed)
+    codes, zeros = np.full((n, k), 8, np.uint8), np.full((n, k // 32), 8, np.uint8)
+    scales = (0.1 + 0.2 * g.random((n, k // 32))).astype(np.float16)
+    codes[rows, cols] = 8 + g.choice([-7, -6, -5, -4, 4, 5, 6, 7], len(rows))
+    values = (codes.astype(np.float64) - 8) * np.repeat(scales.astype(np.float64), 32, 1)
+    return torch.from_numpy(oracle.pack_int4(codes, scales.view(np.uint16), zeros)), values
+
+
+def bf16(a):
+    return torch.from_numpy(np.asarray(a)).float().bfloat16().double().numpy()
+
+
+@pytest.mark.parametrize("t", [1, 2, 3, 4])
+@pytest.mark.parametrize("e,k", [(2, 1), (2, 2), (5, 3)])
+def test_up_to_four_tokens_keep_the_hidden_values_as_two_bf16(dev, t, e, k):
+    """Weights with one term a row and one hidden value an expert, so that no sum rounds and what is left is
+    the rounding of the hidden value to the sum of two bf16 (2^-18 of it), silu in binary32 (its
+    exponential's argument of up to 16 carries 2^-20) and the last product (2^-24 of 272 / 4 of the term, from
+    the bias of 128 + 8 on a code at least 4 away from it): below 2^-15 of the terms in all.  The same
+    hidden values as one bf16 are outside it."""
+    h, inter, hot = 256, 256, 7 + 32 * ((t + e) % 8)
+    ks = 32 * np.arange(8) + 5                        # channels of x that are not zero
+    g = np.random.default_rng(10 * t + e)
+    gu, dn, gu_v, dn_v = [], [], [], []
+    for i in range(e):
+        w, v = one_term_weights(2 * inter, h, np.array([hot, inter + hot]), g.choice(ks, 2), 31 * i + e)
+        gu.append(w), gu_v.append(v)
+        w, v = one_term_weights(h, inter, np.arange(h), np.full(h, hot), 37 * i + e)
+        dn.append(w), dn_v.append(v)
+    x = torch.zeros(t, h, dtype=torch.bfloat16)
+    x[:, ks] = torch.from_numpy(1.5 * g.standard_normal((t, 8))).clamp(-4, 4).bfloat16()
+    router = torch.zeros(e, h, dtype=torch.bfloat16)
+    want, bound = ref.moe(ref.f64(x), ref.f64(router), gu_v, dn_v, inter, k, True)
+    y = qg.moe_w4a16(x.to(dev), router.to(dev), torch.stack(gu).to(dev), torch.stack(dn).to(dev), inter, k, out_dtype=torch.float32)
+    tol = bound * 2.0 ** -15 + 1e-30
+    assert (np.abs(ref.f64(y) - want) <= tol).all(), float((np.abs(ref.f64(y) - want) / tol).max())
+    once = np.zeros_like(want)                        # the first k experts, equal weights
+    for i in range(k):
+        gate, up = ref.f64(x) @ gu_v[i][:inter].T, ref.f64(x) @ gu_v[i][inter:].T
+        once += bf16(gate / (1 + np.exp(-gate)) * up) @ dn_v[i].T / k
+    assert (np.abs(once - want) > tol).any()
