@@ -596,7 +596,9 @@ def attn_kv8(q: torch.Tensor, codes: torch.Tensor, scales: torch.Tensor, block_t
              workspace: torch.Tensor | None = None, status: torch.Tensor | None = None) -> torch.Tensor:
     """Causal attention of query rows [rows, hq, d] (a sequence's last tokens)
     over the cache -> [rows, hq, d].  scale defaults to d ** -0.5, max_len (an
-    upper bound of lens, for the choice of the split) to the table's width."""
+    upper bound of lens, for the choice of the split) to the table's width.
+    Rows that no sequence of cu has, and a sequence's rows from max_q on, are
+    not written: give an `out` where that can happen."""
     dev, pages, hkv, d, b, width = _cache(codes, scales, block_table, lens)
     shape, od = q.shape, _out_type(out_dtype)
     if not (len(shape) == 3 and shape[2] == d and q.dtype is _BF16 and q.get_device() == dev and q.stride(2) == 1 and

@@ -36,11 +36,11 @@
 // The least a call can do is read the weights of the experts that were picked, 37/64
 // byte each.  Measured, whole layer: 1 token, 8 of 128 experts of 768 x 2048, 15.9 us
 // (three launches that wait for each other; 3.4 us of bytes); 1 token, 2 of 8 of
-// 14336 x 4096, 46 us (4.4 TB/s); 17 tokens, 6 of 64 of 1024 x 2048, 49.6 us (3.8 TB/s:
-// 10 us of it the small launches, the rest short columns of K); 64 tokens, 2 of 8 of
-// 14336 x 4096, 222 us (3.7 TB/s): there the vector instructions that unpack codes
-// (74 % of issue) and the matrix instructions (33 %) of the waves of a SIMD add up;
-// exactly 16 tokens an expert, one tile, take 195 us, 22 to 32 take 260.
+// 14336 x 4096, 46 us (4.4 TB/s); 17 tokens, 6 of 64 of 1024 x 2048, 46 to 56 us (10 us
+// of it the small launches, the rest short columns of K); 64 tokens, 2 of 8 of
+// 14336 x 4096, 214 to 232 us (3.5 to 3.8 TB/s): there the vector instructions that unpack
+// codes (62 % of a SIMD's issue without the matrix ones) and the matrix pipe (34 %)
+// take turns; exactly 16 tokens an expert, one tile, take 195 us, 22 to 32 take 260.
 #include <type_traits>
 
 #include "layer_common.h"

@@ -105,7 +105,7 @@ enum qg_status {
 #define QG_FLAG_NONFINITE 1u   /* a weight group/row held Inf or NaN */
 #define QG_FLAG_OVERFLOW 2u    /* an INT4 group's range exceeded 15 * 65504 */
 #define QG_FLAG_POSITION 4u    /* qg_qk_norm_rope: a position outside the table */
-#define QG_FLAG_PAGE 8u        /* the cache calls: a page that the table or the cache does not hold */
+#define QG_FLAG_PAGE 8u        /* kv8_append, attn_kv8: a page that the table or the cache does not hold */
 
 /* Human-readable name of a qg_status value (static string). */
 const char *qg_status_string(int32_t status);
@@ -412,7 +412,8 @@ int32_t qg_qk_norm_rope(const void *q, int64_t q_token_stride, int64_t q_head_st
  * rows than tokens) are skipped by the append and see nothing.
  * A page that is not there (a table column past table_width, or an entry
  * outside [0, pages)) is never read or written: its tokens are lost to an
- * append and NaN to a read or an attention; QG_FLAG_PAGE is set. */
+ * append and NaN to a read or an attention; the append and the attention set
+ * QG_FLAG_PAGE (a read has no status word). */
 #define QG_KV8_PAGE 64
 #define QG_KV8_BLOCK 16
 
