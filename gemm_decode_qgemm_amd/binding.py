@@ -27,6 +27,7 @@ FLAG_NONFINITE = 1
 FLAG_OVERFLOW = 2
 FLAG_POSITION = 4
 FLAG_PAGE = 8
+FLAG_INDEX = 16
 KV8_PAGE = 64                         # tokens of a cache page
 KV8_BLOCK = 16                        # tokens that share a scale
 
@@ -76,6 +77,16 @@ def _load() -> ctypes.CDLL:
                               ctypes.c_float, P, I32, I32, P, I64, P, P]),
         "qg_moe_w4a16_workspace_bytes": (I64, [I64, I64, I64, I64, I64]),
         "qg_moe_w4a16": (I32, [P, I64, I64, P, I64, P, I64, P, I64, I64, I64, I32, P, I32, P, I64, P]),
+    }
+    F32 = ctypes.c_float
+    sigs |= {
+        "qg_rms_norm": (I32, [P, I32, I64, P, I32, I64, I64, I64, P, F32, P, I32, P, P]),
+        "qg_rms_norm_q8": (I32, [P, I32, I64, P, I32, I64, I64, I64, P, F32, P, P, I32, P, P]),
+        "qg_lora_add_workspace_bytes": (I64, [I64, I64, I64, I64, I64]),
+        "qg_lora_add": (I32, [P, I64, I64, P, P, I64, I64, P, P, P, I32, I64, I64, P, I32, I64, P, I64, P, P]),
+        "qg_moe_route": (I32, [P, I32, I64, I64, I64, I32, P, I64, I64, I32, I32, F32, P, P, P]),
+        "qg_verify_drafts_workspace_bytes": (I64, [I64, I64, I64]),
+        "qg_verify_drafts": (I32, [P, P, I32, I64, I64, P, P, P, P, I64, P, P, P, P, I64, P, P]),
     }
     for name, (res, args) in sigs.items():
         fn = getattr(lib, name)
@@ -702,3 +713,313 @@ def moe_w4a16(x: torch.Tensor, router: torch.Tensor, gate_up: torch.Tensor, down
     if st:
         _check(st, "qg_moe_w4a16")
     return out
+
+
+# ---- operators of a serving step beside the linears ----------------------------
+
+def _on(dev: int, fn, *args) -> int:
+    """Calls into the library with `dev` as the current device, where its kernels launch."""
+    if torch.cuda.current_device() == dev:
+        return fn(*args, _stream_of(dev))
+    with torch.cuda.device(dev):
+        return fn(*args, _stream_of(dev))
+
+
+def _float_type(t: torch.Tensor) -> int:
+    """QG_BF16 or QG_F32, or -1."""
+    return QG_BF16 if t.dtype is _BF16 else QG_F32 if t.dtype is _F32 else -1
+
+
+def _refuse_norm(x, weight, residual, residual_out, outs) -> None:
+    for name, t in (("x", x), ("residual", residual)):
+        if t is None:
+            continue
+        if not t.is_cuda:
+            raise ValueError(f"{name} must be on a CUDA (HIP) device")
+        if _float_type(t) < 0 or t.dim() != 2:
+            raise ValueError(f"{name} must be bfloat16 or float32 [rows, h], got {t.dtype} of rank {t.dim()}")
+        if t.shape[1] > 1 and t.stride(1) != 1:
+            raise ValueError(f"{name}: the channels of a row must be contiguous")
+    if residual is not None and residual.shape != x.shape:
+        raise ValueError("residual must have the shape of x")
+    if weight is not None:
+        _dev(weight, "weight", torch.bfloat16, 1)
+        if weight.shape[0] != x.shape[1]:
+            raise ValueError("weight must be [h]")
+    if residual is None and residual_out is not None:
+        raise ValueError("residual_out without a residual")
+    if residual_out is not None:
+        _dev(residual_out, "residual_out", residual.dtype, 2)
+        if residual_out.shape != x.shape:
+            raise ValueError("residual_out must have the shape of x")
+    for name, t, dtype, shape in outs:
+        if t is not None:
+            _dev(t, name, dtype, len(shape))
+            if t.shape != shape:
+                raise ValueError(f"{name} must be {list(shape)}")
+    _same_device(x.device, weight=weight, residual=residual, residual_out=residual_out, **{o[0]: o[1] for o in outs})
+    raise ValueError("rms_norm: arguments that do not fit together")
+
+
+def _norm_args_ok(x, weight, residual, residual_out, dev) -> bool:
+    xs = x.shape
+    return (dev >= 0 and len(xs) == 2 and _float_type(x) >= 0 and (xs[1] <= 1 or x.stride(1) == 1) and
+            (weight is None or (weight.dtype is _BF16 and weight.shape == xs[1:] and weight.get_device() == dev and
+                                weight.is_contiguous())) and
+            (residual_out is None if residual is None else
+             _float_type(residual) >= 0 and residual.shape == xs and residual.get_device() == dev and
+             (xs[1] <= 1 or residual.stride(1) == 1) and
+             (residual_out is None or (residual_out.dtype is residual.dtype and residual_out.shape == xs and
+                                       residual_out.get_device() == dev and residual_out.is_contiguous()))))
+
+
+def _out_ok(t: torch.Tensor | None, dtype: torch.dtype, shape, dev: int) -> bool:
+    return t is None or (t.dtype is dtype and t.shape == shape and t.get_device() == dev and t.is_contiguous())
+
+
+def rms_norm(x: torch.Tensor, weight: torch.Tensor | None = None, *, residual: torch.Tensor | None = None,
+             eps: float = 1e-6, out_dtype: torch.dtype = torch.bfloat16, out: torch.Tensor | None = None,
+             residual_out: torch.Tensor | None = None):
+    """RMS norm of the rows of x [rows, h] (bf16 or fp32): y.  With a residual (bf16
+    or fp32) the norm of x + residual: (y, x + residual in the residual's type).
+    residual_out may be residual itself.  x and residual may be strided views."""
+    dev, od, shape = x.get_device(), _out_type(out_dtype), x.shape
+    if not (_norm_args_ok(x, weight, residual, residual_out, dev) and _out_ok(out, out_dtype, shape, dev)):
+        _refuse_norm(x, weight, residual, residual_out, [("out", out, out_dtype, shape)])
+    if out is None:
+        out = torch.empty(shape, dtype=out_dtype, device=x.device)
+    if residual is None:
+        st = _on(dev, lib.qg_rms_norm, x.data_ptr(), _float_type(x), x.stride(0), None, 0, 0, shape[0], shape[1], _ptr(weight), eps,
+                             out.data_ptr(), od, None)
+    else:
+        if residual_out is None:
+            residual_out = torch.empty(shape, dtype=residual.dtype, device=x.device)
+        st = _on(dev, lib.qg_rms_norm, x.data_ptr(), _float_type(x), x.stride(0), residual.data_ptr(), _float_type(residual),
+                             residual.stride(0), shape[0], shape[1], _ptr(weight), eps, out.data_ptr(), od,
+                             residual_out.data_ptr())
+    if st:
+        _check(st, "qg_rms_norm")
+    return out if residual is None else (out, residual_out)
+
+
+def rms_norm_q8(x: torch.Tensor, weight: torch.Tensor | None = None, *, residual: torch.Tensor | None = None,
+                eps: float = 1e-6, group_scales: bool = False, out: tuple | None = None,
+                residual_out: torch.Tensor | None = None) -> tuple:
+    """rms_norm with y as the 8-bit rows that qgemm_w4a8_rows takes: (codes int8
+    [rows, h], scales fp32 [rows], or [rows, h / 32] with group_scales), and with a
+    residual (codes, scales, x + residual)."""
+    dev, shape = x.get_device(), x.shape
+    wide = shape[:1] if not group_scales else (shape[0], shape[-1] // GROUP)
+    codes, scales = out if out is not None else (None, None)
+    if not (_norm_args_ok(x, weight, residual, residual_out, dev) and _out_ok(codes, torch.int8, shape, dev) and
+            _out_ok(scales, _F32, wide, dev)):
+        _refuse_norm(x, weight, residual, residual_out, [("codes", codes, torch.int8, shape),
+                                                         ("scales", scales, torch.float32, wide)])
+    if out is None:
+        codes = torch.empty(shape, dtype=torch.int8, device=x.device)
+        scales = torch.empty(wide, dtype=_F32, device=x.device)
+    if residual is not None and residual_out is None:
+        residual_out = torch.empty(shape, dtype=residual.dtype, device=x.device)
+    st = _on(dev, lib.qg_rms_norm_q8, x.data_ptr(), _float_type(x), x.stride(0), _ptr(residual),
+                            0 if residual is None else _float_type(residual),
+                            0 if residual is None else residual.stride(0), shape[0], shape[1], _ptr(weight), eps,
+                            codes.data_ptr(), scales.data_ptr(), group_scales, _ptr(residual_out))
+    if st:
+        _check(st, "qg_rms_norm_q8")
+    return (codes, scales) if residual is None else (codes, scales, residual_out)
+
+
+def lora_add_workspace_bytes(m: int, k: int, n: int, r: int, adapters: int) -> int:
+    v = int(lib.qg_lora_add_workspace_bytes(m, k, n, r, adapters))
+    _check(min(v, 0), "qg_lora_add_workspace_bytes")
+    return v
+
+
+def _refuse_lora(y, x, a, b, ids, scales, out, out_dtype, workspace, status) -> None:
+    _dev(x, "x", torch.bfloat16, 2)
+    _dev(a, "a", torch.bfloat16, 3)
+    _dev(b, "b", torch.bfloat16, 3)
+    _dev(ids, "ids", torch.int32, 1)
+    for name, t in (("y", y), ("out", out)):
+        if t is None:
+            continue
+        if not t.is_cuda or _float_type(t) < 0 or t.dim() != 2 or (t.shape[1] > 1 and t.stride(1) != 1):
+            raise ValueError(f"{name} must be bfloat16 or float32 [m, n] on a CUDA (HIP) device, columns contiguous")
+    if a.shape[2] != x.shape[1] or b.shape[0] != a.shape[0] or b.shape[2] != a.shape[1]:
+        raise ValueError("a must be [adapters, r, k] and b [adapters, n, r]")
+    if y.shape != (x.shape[0], b.shape[1]) or ids.shape[0] != x.shape[0]:
+        raise ValueError("y must be [m, n] and ids [m]")
+    if out is not None and (out.shape != y.shape or out.dtype != out_dtype):
+        raise ValueError("out must be [m, n] of out_dtype")
+    if out is not None and out.data_ptr() == y.data_ptr() and (out.dtype != y.dtype or out.stride() != y.stride()):
+        raise ValueError("out over y must have its type and strides")
+    if scales is not None:
+        _dev(scales, "scales", torch.float32, 1)
+        if scales.shape[0] != a.shape[0]:
+            raise ValueError("scales must be [adapters]")
+    _refuse_flags(status)
+    _same_device(x.device, y=y, a=a, b=b, ids=ids, scales=scales, out=out, workspace=workspace, status=status)
+    raise ValueError("lora_add: arguments that do not fit together")
+
+
+def lora_add(y: torch.Tensor, x: torch.Tensor, a: torch.Tensor, b: torch.Tensor, ids: torch.Tensor, *,
+             scales: torch.Tensor | None = None, out_dtype: torch.dtype | None = None, out: torch.Tensor | None = None,
+             workspace: torch.Tensor | None = None, status: torch.Tensor | None = None) -> torch.Tensor:
+    """y [m, n] + scales[i] * (x . a[i]^T) . b[i]^T with the adapter i = ids[row] of
+    each of up to 64 rows (none where negative): the adapters of many requests beside
+    a shared projection's output y (bf16 or fp32, rows any stride apart).  x bf16
+    [m, k], a bf16 [adapters, r, k], b bf16 [adapters, n, r].  out_dtype defaults to
+    y's; out may be y itself."""
+    dev, ys, xs, as_, bs = x.get_device(), y.shape, x.shape, a.shape, b.shape
+    if out_dtype is None:
+        out_dtype = y.dtype if out is None else out.dtype
+    if not (dev >= 0 and len(ys) == 2 and len(xs) == 2 and len(as_) == 3 and len(bs) == 3 and x.dtype is _BF16 and
+            a.dtype is _BF16 and b.dtype is _BF16 and ids.dtype is _I32 and _float_type(y) >= 0 and
+            as_[2] == xs[1] and bs[0] == as_[0] and bs[2] == as_[1] and ys == (xs[0], bs[1]) and ids.shape == xs[:1] and
+            (ys[1] <= 1 or y.stride(1) == 1) and y.get_device() == dev and a.get_device() == dev and
+            b.get_device() == dev and ids.get_device() == dev and x.is_contiguous() and a.is_contiguous() and
+            b.is_contiguous() and ids.is_contiguous() and
+            (scales is None or (scales.dtype is _F32 and scales.shape == as_[:1] and scales.get_device() == dev and
+                                scales.is_contiguous())) and
+            (out is None or (out.dtype is out_dtype and out.shape == ys and out.get_device() == dev and
+                             (ys[1] <= 1 or out.stride(1) == 1) and
+                             (out.data_ptr() != y.data_ptr() or (out.dtype is y.dtype and out.stride() == y.stride())))) and
+            (workspace is None or (workspace.get_device() == dev and workspace.is_contiguous())) and
+            _flags_ok(status, dev)):
+        _refuse_lora(y, x, a, b, ids, scales, out, out_dtype, workspace, status)
+    od, (m, k), (adapters, r) = _out_type(out_dtype), xs, as_[:2]
+    if workspace is None:
+        ws_bytes = lib.qg_lora_add_workspace_bytes(m, k, ys[1], r, adapters)
+        if ws_bytes < 0:
+            _check(ws_bytes, "qg_lora_add")
+        workspace = torch.empty(ws_bytes, dtype=torch.uint8, device=x.device)
+    else:
+        ws_bytes = workspace.numel() * workspace.element_size()
+    if out is None:
+        out = torch.empty(ys, dtype=out_dtype, device=x.device)
+    st = _on(dev, lib.qg_lora_add, x.data_ptr(), m, k, a.data_ptr(), b.data_ptr(), r, adapters, ids.data_ptr(), _ptr(scales),
+                         y.data_ptr(), _float_type(y), y.stride(0), ys[1], out.data_ptr(), od, out.stride(0),
+                         workspace.data_ptr(), ws_bytes, _ptr(status))
+    if st:
+        _check(st, "qg_lora_add")
+    return out
+
+
+def _refuse_route(logits, top_k, bias, out) -> None:
+    if not logits.is_cuda:
+        raise ValueError("logits must be on a CUDA (HIP) device")
+    if _float_type(logits) < 0 or logits.dim() != 2 or not logits.is_contiguous():
+        raise ValueError("logits must be contiguous bfloat16 or float32 [t, e]")
+    if bias is not None:
+        _dev(bias, "bias", torch.float32, 1)
+        if bias.shape[0] != logits.shape[1]:
+            raise ValueError("bias must be [e]")
+    if out is not None:
+        for name, t, dtype in (("ids", out[0], torch.int32), ("weights", out[1], torch.float32)):
+            _dev(t, name, dtype, 2)
+            if t.shape != (logits.shape[0], top_k):
+                raise ValueError("out must be two [t, top_k]")
+        _same_device(logits.device, ids=out[0], weights=out[1])
+    _same_device(logits.device, bias=bias)
+    raise ValueError("moe_route: arguments that do not fit together")
+
+
+def moe_route(logits: torch.Tensor, top_k: int, *, sigmoid: bool = False, bias: torch.Tensor | None = None,
+              groups: int = 1, top_groups: int = 1, group_best: int = 1, renormalize: bool = True, scale: float = 1.0,
+              out: tuple | None = None) -> tuple:
+    """The choice of experts from a router's logits [t, e] (bf16 or fp32): (ids int32
+    [t, top_k], weights fp32 [t, top_k]).  Softmax or sigmoid scores; `bias` (fp32
+    [e]) is added for the choice only; of `groups` equal groups the `top_groups` stay
+    whose best `group_best` (1 or 2) experts sum to most; weights are the picked
+    scores, over their sum where renormalized, times `scale`."""
+    dev, ls = logits.get_device(), logits.shape
+    shape = (ls[0], top_k)
+    ids, weights = out if out is not None else (None, None)
+    if not (dev >= 0 and len(ls) == 2 and _float_type(logits) >= 0 and logits.is_contiguous() and
+            (bias is None or (bias.dtype is _F32 and bias.shape == ls[1:] and bias.get_device() == dev and
+                              bias.is_contiguous())) and
+            _out_ok(ids, _I32, shape, dev) and _out_ok(weights, _F32, shape, dev)):
+        _refuse_route(logits, top_k, bias, out)
+    if out is None:
+        if top_k < 1:
+            _check(-2, "qg_moe_route")
+        ids = torch.empty(shape, dtype=_I32, device=logits.device)
+        weights = torch.empty(shape, dtype=_F32, device=logits.device)
+    st = _on(dev, lib.qg_moe_route, logits.data_ptr(), _float_type(logits), ls[0], ls[1], top_k, sigmoid, _ptr(bias), groups,
+                          top_groups, group_best, renormalize, scale, ids.data_ptr(), weights.data_ptr())
+    if st:
+        _check(st, "qg_moe_route")
+    return ids, weights
+
+
+def verify_drafts_workspace_bytes(rows: int, b: int, v: int) -> int:
+    n = int(lib.qg_verify_drafts_workspace_bytes(rows, b, v))
+    _check(min(n, 0), "qg_verify_drafts_workspace_bytes")
+    return n
+
+
+def _refuse_verify(target, draft, tokens, u, u_next, cu, lens, out, workspace, status) -> None:
+    if not target.is_cuda:
+        raise ValueError("target must be on a CUDA (HIP) device")
+    if _float_type(target) < 0 or target.dim() != 2 or not target.is_contiguous():
+        raise ValueError("target must be contiguous bfloat16 or float32 [rows, v]")
+    _dev(cu, "cu", torch.int32, 1)
+    b, (rows, v) = cu.shape[0] - 1, target.shape
+    if b < 0 or rows < b:
+        raise ValueError("cu must be [b + 1], and every sequence has a row of target at least")
+    if draft is not None:
+        _dev(draft, "draft", target.dtype, 2)
+        if draft.shape != (rows - b, v):
+            raise ValueError("draft must be [rows - b, v]")
+    for name, t, dtype, n in (("tokens", tokens, torch.int32, rows - b), ("u", u, torch.float32, rows - b),
+                              ("u_next", u_next, torch.float32, b), ("lens", lens, torch.int32, b),
+                              *((f"out[{i}]", t, torch.int32, b) for i, t in enumerate(out or ()))):
+        if t is not None:
+            _dev(t, name, dtype, 1)
+            if t.shape[0] != n:
+                raise ValueError(f"{name} must be [{n}]")
+            _same_device(target.device, **{name: t})
+    _refuse_flags(status)
+    _same_device(target.device, draft=draft, cu=cu, workspace=workspace, status=status)
+    raise ValueError("verify_drafts: arguments that do not fit together")
+
+
+def verify_drafts(target: torch.Tensor, draft: torch.Tensor | None, tokens: torch.Tensor, u: torch.Tensor,
+                  u_next: torch.Tensor, cu: torch.Tensor, *, lens: torch.Tensor | None = None, out: tuple | None = None,
+                  workspace: torch.Tensor | None = None, status: torch.Tensor | None = None) -> tuple:
+    """Drafted tokens against the target's probabilities: (accepted int32 [b], next
+    token int32 [b]).  Sequence b has rows cu[b]..cu[b + 1] of target [rows, v] (bf16 or
+    fp32), one per drafted token and one more, and one row fewer of draft
+    [rows - b, v] (None: drafts that are certain), tokens int32 and u fp32 [rows - b].
+    A draft is accepted while u * draft < target; the next token is drawn with u_next
+    fp32 [b].  lens (int32 [b]) loses the drafts that were not accepted."""
+    dev, ts, b = target.get_device(), target.shape, cu.shape[0] - 1
+    accepted, following = out if out is not None else (None, None)
+    if not (dev >= 0 and len(ts) == 2 and _float_type(target) >= 0 and target.is_contiguous() and cu.dtype is _I32 and
+            cu.dim() == 1 and 0 <= b <= ts[0] and cu.get_device() == dev and cu.is_contiguous() and
+            (draft is None or (draft.dtype is target.dtype and draft.shape == (ts[0] - b, ts[1]) and
+                               draft.get_device() == dev and draft.is_contiguous())) and
+            tokens.dtype is _I32 and tokens.shape == (ts[0] - b,) and tokens.get_device() == dev and
+            tokens.is_contiguous() and u.dtype is _F32 and u.shape == tokens.shape and u.get_device() == dev and
+            u.is_contiguous() and u_next.dtype is _F32 and u_next.shape == (b,) and u_next.get_device() == dev and
+            u_next.is_contiguous() and _out_ok(lens, _I32, (b,), dev) and _out_ok(accepted, _I32, (b,), dev) and
+            _out_ok(following, _I32, (b,), dev) and
+            (workspace is None or (workspace.get_device() == dev and workspace.is_contiguous())) and
+            _flags_ok(status, dev)):
+        _refuse_verify(target, draft, tokens, u, u_next, cu, lens, out, workspace, status)
+    if workspace is None:
+        ws_bytes = lib.qg_verify_drafts_workspace_bytes(ts[0], b, ts[1])
+        if ws_bytes < 0:
+            _check(ws_bytes, "qg_verify_drafts")
+        workspace = torch.empty(ws_bytes, dtype=torch.uint8, device=target.device)
+    else:
+        ws_bytes = workspace.numel() * workspace.element_size()
+    if out is None:
+        accepted = torch.empty(b, dtype=_I32, device=target.device)
+        following = torch.empty(b, dtype=_I32, device=target.device)
+    st = _on(dev, lib.qg_verify_drafts, target.data_ptr(), _ptr(draft), _float_type(target), ts[0], ts[1], tokens.data_ptr(),
+                              u.data_ptr(), u_next.data_ptr(), cu.data_ptr(), b, _ptr(lens), accepted.data_ptr(),
+                              following.data_ptr(), workspace.data_ptr(), ws_bytes, _ptr(status))
+    if st:
+        _check(st, "qg_verify_drafts")
+    return accepted, following

@@ -29,6 +29,7 @@
 //    the lane holding it (DPP row_newbcast), accumulating in int32; the zero
 //    point comes off as zp * (group sum of xq), also broadcast by DPP.
 #include "qg_common.h"
+#include "act_q8.h"
 #include "dispatch.h"
 #include "w4_common.h"
 
@@ -64,34 +65,6 @@ __device__ __forceinline__ void group_dot4(int& i0, int& i1, uint32_t xlo, uint3
 template <int CTRL>
 __device__ __forceinline__ int dpp_i(int v) {
   return __builtin_amdgcn_update_dpp(0, v, CTRL, 0xf, 0xf, true);
-}
-
-// The absmax keeps a NaN: nmax is the IEEE 754-2019 maximum (one
-// v_maximum3_f32 on gfx950), which returns NaN when either input is NaN,
-// where fmaxf would return the other input.  An infinity survives any max.
-__device__ __forceinline__ float nmax(float a, float b) { return __builtin_elementwise_maximum(a, b); }
-
-// A span whose absmax is not finite (it holds a NaN or an infinity) has no
-// finite scale: its absmax becomes NaN, which gives inv = 0 through
-// a > 0 ? 127 / a : 0 and sx = a / 127 = NaN, so every output the span
-// reaches is NaN.
-__device__ __forceinline__ float finite_or_nan(float a) {
-  return a < __builtin_inff() ? a : __builtin_nanf("");
-}
-
-// The span's scales from its absmax a (>= 0, or NaN as above): inv = 127 / a
-// and sx = a / 127, both correctly rounded binary32 divisions.  Where 127 / a
-// is not a finite binary32 number there is no inverse scale and inv = 0, so
-// every code is 0: for a == 0 and for a span so small that the quotient
-// overflows (a <= 127 * 2^-128), sx = 0 as well (a zero span, outputs 0); for
-// a NaN absmax sx stays NaN.
-__device__ __forceinline__ void span_scale(float a, float& inv, float& sx) {
-  inv = 127.0f / a;
-  sx = a / 127.0f;
-  if (!(inv <= __FLT_MAX__)) {
-    inv = 0.0f;
-    if (a == a) sx = 0.0f;
-  }
 }
 
 // Quantize 8 bf16 (one 16-byte load) to int8 with the row's inverse scale,
@@ -377,12 +350,6 @@ __global__ __launch_bounds__(WAVES * 64) void w4a8_gemv32_kernel(
 // rewrite.
 constexpr int kA8Chunk = 16;                 // half tiles per chunk
 constexpr int kA8Segs = kA8Chunk * 16;       // 8-k segments per chunk
-
-template <int CTRL>
-__device__ __forceinline__ float dpp_fa(float v) {
-  return __builtin_bit_cast(float, __builtin_amdgcn_update_dpp(0, __builtin_bit_cast(int, v),
-                                                               CTRL, 0xf, 0xf, true));
-}
 
 template <int M, bool DQ = false>
 __global__ __launch_bounds__(1024) void w4a8_gemv_lds_kernel(

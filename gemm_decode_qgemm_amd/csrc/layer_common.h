@@ -77,4 +77,55 @@ struct AttnSplit {
   int splits, slots;
 };
 
+// Residual addition and RMS norm (rms_norm.hip).
+enum RmsOut { kRmsBf16, kRmsF32, kRmsQ8Row, kRmsQ8Group };
+
+struct RmsNormArgs {
+  const void *x, *res;              // rows of h channels, strides in elements; res may be null
+  int64_t x_stride, res_stride, rows;
+  int h, x_f32, res_f32, out;       // out: RmsOut
+  float eps;
+  const uint16_t* w;                // bf16 [h] or null
+  void* y;                          // kRmsBf16, kRmsF32
+  int8_t* codes;                    // else
+  float* scales;
+  void* res_out;                    // in the residual's type
+};
+
+// Low-rank adapters (lora.hip).
+struct LoraArgs {
+  const uint16_t *x, *a, *b;        // bf16 [m, k], [adapters, r, k], [adapters, n, r]
+  const int32_t* ids;               // [m]
+  const float* scales;              // [adapters] or null
+  const void* y;                    // [m, n], rows y_stride apart
+  void* out;                        // rows out_stride apart
+  int64_t y_stride, out_stride;
+  int m, k, n, r, adapters, y_f32, out_f32, splits;
+  float* part;                      // [splits, m, r]
+  uint32_t* status;
+};
+
+// The choice of experts (moe_route.hip).
+struct RouteArgs {
+  const void* logits;               // [t, e]
+  const float* bias;                // [e] or null
+  int64_t t;
+  int e, k, half, sigmoid, groups, top_groups, best, renorm;
+  float scale;
+  int32_t* ids;                     // [t, k]
+  float* weights;                   // [t, k]
+};
+
+// Verification of drafted tokens (verify.hip).
+struct VerifyArgs {
+  const void *target, *draft;       // [rows, v], [rows - b, v] or null
+  const int32_t *tokens, *cu;
+  const float *u, *u_next;
+  int64_t rows, v;
+  int b, half, chunk, chunks;
+  int32_t *lens, *accepted, *next;
+  double* part;                     // [b, chunks, 2]
+  uint32_t* status;
+};
+
 }  // namespace qg

@@ -106,6 +106,7 @@ enum qg_status {
 #define QG_FLAG_OVERFLOW 2u    /* an INT4 group's range exceeded 15 * 65504 */
 #define QG_FLAG_POSITION 4u    /* qg_qk_norm_rope: a position outside the table */
 #define QG_FLAG_PAGE 8u        /* kv8_append, attn_kv8: a page that the table or the cache does not hold */
+#define QG_FLAG_INDEX 16u      /* an adapter, an expert, a token or row offsets outside what there is */
 
 /* Human-readable name of a qg_status value (static string). */
 const char *qg_status_string(int32_t status);
@@ -500,6 +501,118 @@ int32_t qg_moe_w4a16(const void *x_bf16, int64_t t, int64_t h, const void *route
                      const void *gate_up, int64_t gate_up_bytes, const void *down, int64_t down_bytes,
                      int64_t inter, int64_t top_k, int32_t renormalize, void *y, int32_t y_dtype, void *ws,
                      int64_t ws_bytes, void *stream);
+
+/* ==========================================================================
+ * Operators of a serving step beside the linears.  The conventions above
+ * hold.
+ * ======================================================================= */
+
+/* ---- qg_rms_norm / qg_rms_norm_q8 ----------------------------------------
+ * A sub-layer's output added to the residual stream, and the RMS norm of the sum:
+ *   r = x + residual;   y = r * rsqrt(mean(r^2) + eps) * w
+ * in binary32.  The norm takes the sum before it is rounded to the stream's type;
+ * y is rounded once, to y_dtype or to the 8-bit rows of qgemm_w4a8_rows:
+ *   a = max |y| of the row, or of each 32 channels where group_scales is not 0,
+ *   inv = 127/a, scale = a/127, code = clamp(rint(y * inv), -127, 127)
+ * with the rules of qgemm_w4a8 for spans that are zero, too small for 127/a, or
+ * not finite (scale NaN).
+ *   x            in : [rows, h], bf16 or fp32 (x_dtype), rows x_row_stride apart
+ *   residual     in : the same shape in either type, or NULL: r = x, not stored
+ *   w            in : bf16 [h], or NULL for a norm without weights
+ *   residual_out out: r [rows, h], contiguous, in the residual's type; NULL without
+ *                     a residual.  It may be `residual` itself (contiguous).
+ *   y            out: [rows, h], bf16 or fp32 (y_dtype)
+ *   codes        out: int8 [rows, h];   scales out: fp32 [rows] or [rows, h / 32]
+ * h: a multiple of 8 (group_scales: of 32) up to 32768; strides: multiples of 8.
+ * rows = 0 is fine.
+ * Errors: QG_E_NULL, QG_E_SHAPE, QG_E_STRIDE, QG_E_ALIGN, QG_E_DTYPE. */
+int32_t qg_rms_norm(const void *x, int32_t x_dtype, int64_t x_row_stride, const void *residual,
+                    int32_t residual_dtype, int64_t residual_row_stride, int64_t rows, int64_t h,
+                    const void *w, float eps, void *y, int32_t y_dtype, void *residual_out, void *stream);
+int32_t qg_rms_norm_q8(const void *x, int32_t x_dtype, int64_t x_row_stride, const void *residual,
+                       int32_t residual_dtype, int64_t residual_row_stride, int64_t rows, int64_t h,
+                       const void *w, float eps, int8_t *codes, float *scales, int32_t group_scales,
+                       void *residual_out, void *stream);
+
+/* ---- qg_lora_add ---------------------------------------------------------
+ * Low-rank adapters of many requests beside a shared projection:
+ *   out[m] = y[m] + s_i * (x[m] . A_i^T) . B_i^T,   i = ids[m];   out[m] = y[m] for i < 0
+ * for m <= 64 rows, as the linears take.  Sums are fp32; the inner value enters the
+ * second product with 24 bits.  Every adapter that a row names is read once.
+ *   x       in : bf16 [m, k]
+ *   a, b    in : bf16 [adapters, r, k] and [adapters, n, r]
+ *   ids     in : int32 [m]; one of `adapters` or more makes its row NaN and sets
+ *                QG_FLAG_INDEX
+ *   scales  in : fp32 [adapters], or NULL for 1
+ *   y       in : [m, n], bf16 or fp32, rows y_row_stride elements apart
+ *   out     out: [m, n], bf16 or fp32, rows out_row_stride apart; it may be y itself
+ *                (same type and stride)
+ *   ws         : qg_lora_add_workspace_bytes(...) bytes; contents unspecified
+ *   status_dev : QG_FLAG_INDEX; may be NULL
+ * r: a multiple of 8 up to 256 (lower ranks padded with zeros); k: a multiple of 8;
+ * n: any; both up to 2^20.  m = 0 is fine.
+ * Errors: QG_E_NULL, QG_E_SHAPE, QG_E_M_RANGE, QG_E_STRIDE, QG_E_ALIGN, QG_E_DTYPE,
+ * QG_E_BUFFER. */
+#define QG_LORA_MAX_RANK 256
+#define QG_LORA_MAX_DIM (1 << 20)
+int64_t qg_lora_add_workspace_bytes(int64_t m, int64_t k, int64_t n, int64_t r, int64_t adapters);
+int32_t qg_lora_add(const void *x_bf16, int64_t m, int64_t k, const void *a_bf16, const void *b_bf16,
+                    int64_t r, int64_t adapters, const int32_t *ids, const float *scales, const void *y,
+                    int32_t y_dtype, int64_t y_row_stride, int64_t n, void *out, int32_t out_dtype,
+                    int64_t out_row_stride, void *ws, int64_t ws_bytes, uint32_t *status_dev, void *stream);
+
+/* ---- qg_moe_route --------------------------------------------------------
+ * The choice of experts from a router's logits l [t, e]:
+ *   s = softmax(l) over the experts, or 1 / (1 + exp(-l)) (sigmoid not 0)
+ *   c = s + bias                     (it decides the choice and does not weigh)
+ *   groups > 1: the experts fall into equal groups one after another; a group
+ *   counts the sum of its group_best (1 or 2) largest c; the top_groups of them stay
+ *   ids = the top_k experts of those by c, largest first
+ *   weights = s of the picked, divided by their sum (renormalize not 0), times scale
+ * Ties go to the lowest index; a NaN counts as the largest.  Scores, sums and
+ * comparisons are in 64 bits, so that the choice is the exact one but for
+ * differences in the 16th digit; weights are rounded once.  An expert with a logit
+ * of -infinity has score 0 (it can be picked where too few others are left); where
+ * the picked scores sum to 0, renormalized weights are 0.
+ *   logits  in : [t, e], bf16 or fp32;   bias in : fp32 [e], or NULL
+ *   ids     out: int32 [t, top_k];       weights out: fp32 [t, top_k]
+ * e <= 512; top_k <= 32 and <= top_groups * e / groups; groups <= 64 divides e.
+ * t = 0 is fine.  Errors: QG_E_NULL, QG_E_SHAPE, QG_E_DTYPE, QG_E_ALIGN. */
+int32_t qg_moe_route(const void *logits, int32_t logits_dtype, int64_t t, int64_t e, int64_t top_k,
+                     int32_t sigmoid, const float *bias, int64_t groups, int64_t top_groups,
+                     int32_t group_best, int32_t renormalize, float scale, int32_t *ids, float *weights,
+                     void *stream);
+
+/* ---- qg_verify_drafts ----------------------------------------------------
+ * Drafted tokens against the target's probabilities, and the next token.
+ * Sequence b has rows cu[b] .. cu[b + 1] - 1 of `target`: one for each of its n
+ * drafted tokens and one more; and n rows of `draft`, `tokens` and `u`, which lie one
+ * sequence after another, from cu[b] - b on.  Draft i, token x, is accepted while
+ *   u * draft_i[x] < target_i[x]
+ * (draft NULL: the drafts are certain, u < target_i[x]).  At the first that is not, the
+ * next token is the first j whose running sum of max(target_i - draft_i, 0)
+ * exceeds u_next times the whole sum (draft NULL: of target_i without x); that of
+ * max(target_i, 0) where the whole sum is zero; and after the last draft that of the
+ * last row.  All in 64 bits.  Rows need not add up to one; a NaN counts as 0.
+ *   target     in : [rows, v], bf16 or fp32 (dtype)
+ *   draft      in : [rows - b, v] in the same type, or NULL
+ *   tokens, u  in : int32 and fp32 [rows - b]; u in [0, 1)
+ *   u_next     in : fp32 [b], in [0, 1);   cu in : int32 [b + 1]
+ *   lens       in/out: int32 [b], less the drafts that were not accepted (the
+ *                   lengths that a cache is left with); may be NULL
+ *   accepted, next out: int32 [b]
+ *   ws            : qg_verify_drafts_workspace_bytes(...) bytes; contents unspecified
+ *   status_dev    : may be NULL.  QG_FLAG_INDEX: a drafted token outside [0, v) (it is
+ *                   rejected), or offsets that are not in order (accepted 0, next -1,
+ *                   lens as it was); QG_FLAG_NONFINITE: a row to draw from without a
+ *                   finite sum above zero (next -1).
+ * b <= 65535; b = 0 is fine.
+ * Errors: QG_E_NULL, QG_E_SHAPE, QG_E_DTYPE, QG_E_ALIGN, QG_E_BUFFER. */
+int64_t qg_verify_drafts_workspace_bytes(int64_t rows, int64_t b, int64_t v);
+int32_t qg_verify_drafts(const void *target, const void *draft, int32_t dtype, int64_t rows, int64_t v,
+                         const int32_t *tokens, const float *u, const float *u_next, const int32_t *cu,
+                         int64_t b, int32_t *lens, int32_t *accepted, int32_t *next, void *ws,
+                         int64_t ws_bytes, uint32_t *status_dev, void *stream);
 
 /* ---- qg_stream_read (measurement helper, not part of the layer) ---------
  * Reads `bytes` bytes of device memory at `src` once, with one 16-byte

@@ -1,0 +1,133 @@
+"""The serving-step entry points on the host: every bad argument is refused before
+anything is launched.  No call here reaches a kernel, so these run without a GPU."""
+from __future__ import annotations
+
+import pytest
+import torch
+
+import gemm_decode_qgemm_amd as qg
+from gemm_decode_qgemm_amd.binding import lib
+
+A, U = 0x10000, 0x10008          # a 16-byte aligned and an 8-byte aligned fake address, never dereferenced
+OK, E_NULL, E_SHAPE, E_M, E_BUF, E_ALIGN, E_DTYPE, E_STRIDE = 0, -1, -2, -4, -6, -7, -8, -13
+NAN, INF = float("nan"), float("inf")
+
+
+def norm(**kw):
+    a = dict(x=A, xt=0, xs=512, res=A, rt=1, rs=512, rows=3, h=512, w=A, eps=1e-6, y=A, yt=0, ro=A, stream=None)
+    assert set(kw) <= set(a)
+    return lib.qg_rms_norm(*(a | kw).values())
+
+
+def norm_q8(**kw):
+    a = dict(x=A, xt=0, xs=512, res=A, rt=1, rs=512, rows=3, h=512, w=A, eps=1e-6, codes=A, scales=A, group=1, ro=A, stream=None)
+    assert set(kw) <= set(a)
+    return lib.qg_rms_norm_q8(*(a | kw).values())
+
+
+@pytest.mark.parametrize("call", [norm, norm_q8])
+@pytest.mark.parametrize("kw,want", [
+    (dict(x=None), E_NULL), (dict(ro=None), E_NULL), (dict(res=None), E_NULL), (dict(rows=-1), E_SHAPE), (dict(rows=1 << 22), E_SHAPE),
+    (dict(h=0), E_SHAPE), (dict(h=-8), E_SHAPE), (dict(h=516), E_SHAPE), (dict(h=32776, xs=40000, rs=40000), E_SHAPE), (dict(eps=-1.0), E_SHAPE),
+    (dict(eps=NAN), E_SHAPE), (dict(eps=INF), E_SHAPE), (dict(xt=2), E_DTYPE), (dict(rt=-1), E_DTYPE), (dict(xs=504), E_STRIDE), (dict(xs=516), E_STRIDE),
+    (dict(rs=8), E_STRIDE), (dict(rs=-512), E_STRIDE), (dict(xs=1 << 41), E_STRIDE), (dict(x=U), E_ALIGN), (dict(res=U), E_ALIGN), (dict(w=U), E_ALIGN),
+    (dict(ro=U), E_ALIGN), (dict(rows=0), OK), (dict(rows=0, x=None, res=None, ro=None), OK)])
+def test_norm_refusals(call, kw, want):
+    assert call(**kw) == want
+
+
+@pytest.mark.parametrize("kw,want", [(dict(y=None), E_NULL), (dict(y=U), E_ALIGN), (dict(yt=5), E_DTYPE)])
+def test_norm_output_refusals(kw, want):
+    assert norm(**kw) == want
+
+
+@pytest.mark.parametrize("kw,want", [
+    (dict(codes=None), E_NULL), (dict(scales=None), E_NULL), (dict(codes=A + 4), E_ALIGN), (dict(scales=A + 2), E_ALIGN),
+    (dict(h=520, xs=520, rs=520), E_SHAPE)])
+def test_norm_q8_output_refusals(kw, want):
+    assert norm_q8(**kw) == want
+
+
+def lora(**kw):
+    a = dict(x=A, m=3, k=512, a=A, b=A, r=16, adapters=5, ids=A, scales=None, y=A, yt=0, ys=300, n=300, out=A, ot=0, os=300, ws=A, ws_bytes=1 << 30,
+             status=None, stream=None)
+    assert set(kw) <= set(a)
+    return lib.qg_lora_add(*(a | kw).values())
+
+
+@pytest.mark.parametrize("kw,want", [
+    (dict(x=None), E_NULL), (dict(a=None), E_NULL), (dict(b=None), E_NULL), (dict(ids=None), E_NULL), (dict(y=None), E_NULL), (dict(out=None), E_NULL),
+    (dict(ws=None), E_NULL), (dict(m=-1), E_SHAPE), (dict(m=65), E_M), (dict(k=0), E_SHAPE), (dict(k=516), E_SHAPE), (dict(k=(1 << 20) + 8), E_SHAPE),
+    (dict(n=0), E_SHAPE), (dict(n=(1 << 20) + 1), E_SHAPE), (dict(r=0), E_SHAPE), (dict(r=12), E_SHAPE), (dict(r=264), E_SHAPE), (dict(adapters=0), E_SHAPE),
+    (dict(adapters=1 << 31), E_SHAPE), (dict(yt=2), E_DTYPE), (dict(ot=2), E_DTYPE), (dict(ys=299), E_STRIDE), (dict(os=0), E_STRIDE),
+    (dict(ys=1 << 41), E_STRIDE), (dict(ws_bytes=3 * 16 * 4 - 1), E_BUF), (dict(x=U), E_ALIGN), (dict(a=U), E_ALIGN), (dict(b=U), E_ALIGN),
+    (dict(ids=A + 2), E_ALIGN), (dict(scales=A + 2), E_ALIGN), (dict(y=A + 1), E_ALIGN), (dict(yt=1, y=A + 2), E_ALIGN), (dict(out=A + 1), E_ALIGN),
+    (dict(ws=U), E_ALIGN), (dict(status=A + 1), E_ALIGN), (dict(m=0), OK), (dict(m=0, x=None, ids=None, y=None, out=None, ws=None), OK)])
+def test_lora_refusals(kw, want):
+    assert lora(**kw) == want
+
+
+def test_lora_workspace():
+    assert qg.lora_add_workspace_bytes(0, 512, 300, 16, 5) == 0
+    n = qg.lora_add_workspace_bytes(3, 512, 300, 16, 5)
+    assert n > 0 and n % (3 * 16 * 4) == 0
+    for args in ((65, 512, 300, 16, 5), (3, 512, 300, 12, 5), (3, 511, 300, 16, 5)):
+        with pytest.raises(qg.QGemmError):
+            qg.lora_add_workspace_bytes(*args)
+
+
+def route(**kw):
+    a = dict(l=A, lt=1, t=3, e=256, k=8, sigmoid=1, bias=None, groups=8, top=4, best=2, renorm=1, scale=2.5, ids=A, w=A, stream=None)
+    assert set(kw) <= set(a)
+    return lib.qg_moe_route(*(a | kw).values())
+
+
+@pytest.mark.parametrize("kw,want", [
+    (dict(l=None), E_NULL), (dict(ids=None), E_NULL), (dict(w=None), E_NULL), (dict(t=-1), E_SHAPE), (dict(t=1 << 26), E_SHAPE), (dict(e=0), E_SHAPE),
+    (dict(e=520), E_SHAPE), (dict(k=0), E_SHAPE), (dict(k=33), E_SHAPE), (dict(groups=0), E_SHAPE), (dict(groups=7), E_SHAPE), (dict(groups=128), E_SHAPE),
+    (dict(top=0), E_SHAPE), (dict(top=9), E_SHAPE), (dict(best=0), E_SHAPE), (dict(best=3), E_SHAPE), (dict(e=8, groups=8, k=4), E_SHAPE),
+    (dict(e=16, k=9), E_SHAPE), (dict(scale=NAN), E_SHAPE), (dict(scale=INF), E_SHAPE), (dict(lt=3), E_DTYPE), (dict(l=A + 2), E_ALIGN),
+    (dict(bias=A + 2), E_ALIGN), (dict(ids=A + 2), E_ALIGN), (dict(w=A + 1), E_ALIGN), (dict(t=0), OK)])
+def test_route_refusals(kw, want):
+    assert route(**kw) == want
+
+
+def verify(**kw):
+    a = dict(p=A, q=A, dt=1, rows=9, v=1000, tokens=A, u=A, u_next=A, cu=A, b=3, lens=None, acc=A, nxt=A, ws=A, ws_bytes=1 << 20, status=None, stream=None)
+    assert set(kw) <= set(a)
+    return lib.qg_verify_drafts(*(a | kw).values())
+
+
+@pytest.mark.parametrize("kw,want", [
+    (dict(p=None), E_NULL), (dict(tokens=None), E_NULL), (dict(u=None), E_NULL), (dict(u_next=None), E_NULL), (dict(cu=None), E_NULL),
+    (dict(acc=None), E_NULL), (dict(nxt=None), E_NULL), (dict(ws=None), E_NULL), (dict(b=-1), E_SHAPE), (dict(b=65536, rows=70000), E_SHAPE),
+    (dict(rows=2), E_SHAPE), (dict(rows=1 << 31), E_SHAPE), (dict(v=0), E_SHAPE), (dict(v=1 << 31), E_SHAPE), (dict(dt=2), E_DTYPE), (dict(ws_bytes=47), E_BUF),
+    (dict(p=A + 2), E_ALIGN), (dict(dt=0, q=A + 1), E_ALIGN), (dict(tokens=A + 2), E_ALIGN), (dict(u=A + 1), E_ALIGN), (dict(u_next=A + 2), E_ALIGN),
+    (dict(cu=A + 2), E_ALIGN), (dict(lens=A + 2), E_ALIGN), (dict(acc=A + 2), E_ALIGN), (dict(nxt=A + 1), E_ALIGN), (dict(ws=U), E_ALIGN),
+    (dict(status=A + 2), E_ALIGN), (dict(b=0), OK), (dict(b=0, rows=0, p=None, ws=None, cu=None), OK)])
+def test_verify_refusals(kw, want):
+    assert verify(**kw) == want
+
+
+def test_verify_workspace():
+    assert qg.verify_drafts_workspace_bytes(9, 3, 1000) == 3 * 16
+    assert qg.verify_drafts_workspace_bytes(0, 0, 1000) == 0
+    assert 64 * 16 <= qg.verify_drafts_workspace_bytes(1, 1, 2 ** 31 - 1) <= 128 * 16
+    with pytest.raises(qg.QGemmError):
+        qg.verify_drafts_workspace_bytes(2, 3, 1000)
+
+
+def test_wrappers_refuse_host_tensors_and_wrong_types():
+    x, w = torch.zeros(2, 64, dtype=torch.bfloat16), torch.zeros(64, dtype=torch.bfloat16)
+    with pytest.raises(ValueError, match="device"):
+        qg.rms_norm(x, w)
+    with pytest.raises(ValueError, match="device"):
+        qg.rms_norm_q8(x, w, residual=x)
+    ids = torch.zeros(2, dtype=torch.int32)
+    with pytest.raises(ValueError, match="device"):
+        qg.lora_add(x, x, x[None], x[None], ids)
+    with pytest.raises(ValueError, match="device"):
+        qg.moe_route(x, 4)
+    f = torch.zeros(2)
+    with pytest.raises(ValueError, match="device"):
+        qg.verify_drafts(x, None, ids, f, f, ids)

@@ -1,0 +1,165 @@
+"""qg.lora_add against 64 bits.
+
+Tolerance: the inner value v is a sum of k exact products of bf16 in fp32, in
+chains of at most k / 128 matrix instructions of 32 products (counted as 32
+additions each, of which the partial sums' magnitude is at most the sum of the
+products' magnitudes), 4 waves and 16 splits: off by at most (k / 4 + 20) 2^-24
+times sum |a x|.  It enters the second product with 24 bits (2^-23 with the
+scale's rounding), whose 3 r terms are summed in fp32: (3 r + 3) 2^-24 times
+sum |b v|; then one addition and the rounding to the output's type."""
+from __future__ import annotations
+
+import numpy as np
+import pytest
+import torch
+
+import gemm_decode_qgemm_amd as qg
+import serving_reference as ref
+
+pytestmark = pytest.mark.gpu
+BF16, F32 = torch.bfloat16, torch.float32
+BITS = {BF16: 8, F32: 24}
+
+
+@pytest.fixture(scope="module")
+def dev():
+    assert torch.cuda.is_available(), "GPU tests need a HIP device"
+    return torch.device("cuda:0")
+
+
+def make(m, k, n, r, adapters, yt=BF16, seed=0):
+    g = torch.Generator().manual_seed(seed + m + 7 * k + 11 * n + 13 * r)
+    x = torch.randn(m, k, generator=g).bfloat16()
+    a = (torch.randn(adapters, r, k, generator=g) * k ** -0.5).bfloat16()
+    b = (torch.randn(adapters, n, r, generator=g) * r ** -0.5).bfloat16()
+    y = torch.randn(m, n, generator=g).to(yt)
+    scales = 0.2 + torch.rand(adapters, generator=g)
+    ids = torch.randint(-1, adapters, (m,), generator=g).to(torch.int32)
+    return y, x, a, b, ids, scales
+
+
+def check(out, y, x, a, b, ids, scales):
+    y, x, a, b = (ref.f64(t) for t in (y, x, a, b))
+    s = np.ones(a.shape[0]) if scales is None else ref.f64(scales)
+    k, r = x.shape[1], a.shape[1]
+    got, eps = ref.f64(out), 2.0 ** -24
+    for m, i in enumerate(ids.tolist()):
+        if i < 0:
+            want, tol = y[m], 0.0
+        else:
+            v = s[i] * (a[i] @ x[m])
+            dv = s[i] * (np.abs(a[i]) @ np.abs(x[m])) * (k / 4 + 20) * eps
+            want = y[m] + b[i] @ v
+            tol = np.abs(b[i]) @ (dv + np.abs(v) * (3 * r + 5) * eps) + np.abs(want) * 2 * eps
+        tol = tol + ref.half_step(np.abs(want) + tol, BITS[out.dtype]) * (i >= 0 or out.dtype == BF16)
+        bad = ~(np.abs(got[m] - want) <= tol)
+        assert not bad.any(), (m, i, np.argwhere(bad)[:3].ravel(), got[m][bad][:3], want[bad][:3])
+
+
+@pytest.mark.parametrize("m,k,n,r,adapters", [
+    (1, 8, 1, 8, 1), (1, 256, 256, 16, 4), (2, 264, 33, 24, 1), (3, 1000, 257, 16, 3), (5, 512, 1000, 32, 2), (16, 1024, 64, 40, 1),
+    (17, 768, 129, 64, 1), (33, 520, 300, 16, 2), (64, 256, 70, 8, 1), (64, 1280, 513, 64, 64), (64, 2048, 130, 128, 3),
+    (40, 512, 200, 256, 1), (64, 256, 65, 248, 2), (64, 6656, 256, 16, 7), (9, 19968, 100, 72, 20), (31, 4096, 2000, 16, 100)])
+@pytest.mark.parametrize("yt", [BF16, F32])
+def test_against_64_bits(dev, m, k, n, r, adapters, yt):
+    args = make(m, k, n, r, adapters, yt)
+    y, x, a, b, ids, scales = (t.to(dev) for t in args)
+    check(qg.lora_add(y, x, a, b, ids, scales=scales), *args)
+    check(qg.lora_add(y, x, a, b, ids, out_dtype=F32 if yt is BF16 else BF16), *args[:5], None)
+
+
+def test_every_row_has_its_own_result_whatever_the_batch(dev):
+    """The rows that share an adapter, and their order, change nothing."""
+    y, x, a, b, ids, scales = (t.to(dev) for t in make(64, 1024, 300, 16, 9))
+    want = qg.lora_add(y, x, a, b, ids, scales=scales)
+    order = torch.randperm(64, device=dev)
+    got = qg.lora_add(y[order].contiguous(), x[order].contiguous(), a, b, ids[order].contiguous(), scales=scales)
+    assert torch.equal(got, want[order])
+    same = torch.full_like(ids, 3)
+    all_of_one = qg.lora_add(y, x, a, b, same, scales=scales)
+    assert torch.equal(all_of_one[ids == 3], want[ids == 3])
+
+
+def test_in_place_views_and_rows_without_adapter(dev):
+    args = make(7, 512, 200, 16, 5)
+    y, x, a, b, ids, scales = (t.to(dev) for t in args)
+    ids[2] = ids[5] = -1
+    ids[3] = -(2 ** 31)
+    big = torch.full((7, 701), 3.0, dtype=BF16, device=dev)
+    view = big[:, 101:301]
+    view.copy_(y)
+    out = qg.lora_add(view, x, a, b, ids, scales=scales, out=view)
+    assert out.data_ptr() == view.data_ptr()
+    check(out, *args[:4], ids, args[5])
+    assert torch.equal(out[2], y[2]) and torch.equal(out[3], y[3])
+    assert bool((big[:, :101] == 3).all()) and bool((big[:, 301:] == 3).all())
+    none = torch.full_like(ids, -1)
+    assert torch.equal(qg.lora_add(y, x, a, b, none, scales=scales), y)
+    other = torch.full((7, 400), 3.0, dtype=F32, device=dev)
+    assert torch.equal(qg.lora_add(y, x, a, b, none, out=other[:, 100:300]), y.float()) and bool((other[:, :100] == 3).all())
+
+
+def test_adapters_outside_those_held(dev):
+    y, x, a, b, ids, scales = (t.to(dev) for t in make(6, 256, 70, 8, 3))
+    ids = torch.tensor([0, 3, -1, 2 ** 31 - 1, 2, 1], dtype=torch.int32, device=dev)
+    status = torch.zeros(1, dtype=torch.int32, device=dev)
+    out = qg.lora_add(y, x, a, b, ids, scales=scales, status=status)
+    assert status.item() == qg.FLAG_INDEX
+    assert bool(out[[1, 3]].isnan().all()) and bool(out[[0, 2, 4, 5]].isfinite().all()) and torch.equal(out[2], y[2])
+    status.zero_()
+    qg.lora_add(y, x, a, b, ids.clamp(-1, 2), scales=scales, status=status)
+    assert status.item() == 0
+    assert torch.equal(qg.lora_add(y[:2], x[:2], a, b, ids[:2]).isnan().all(1).cpu(), torch.tensor([False, True]))   # by rows
+
+
+def test_values_that_are_not_finite_stay_with_their_rows(dev):
+    y, x, a, b, ids, scales = (t.to(dev) for t in make(4, 256, 70, 8, 2))
+    ids = torch.tensor([0, 1, 1, -1], dtype=torch.int32, device=dev)
+    x[1, 9] = float("nan")
+    scales[0] = float("inf")
+    out = qg.lora_add(y, x, a, b, ids, scales=scales)
+    assert not bool(out[0].isfinite().any()) and bool(out[1].isnan().all()) and bool(out[2:].isfinite().all())
+
+
+def test_graphs_that_share_a_workspace_and_streams(dev):
+    m, k, n, r, adapters = 19, 2048, 777, 32, 6
+    y, x, a, b, ids, scales = (t.to(dev) for t in make(m, k, n, r, adapters))
+    ws = torch.empty(qg.lora_add_workspace_bytes(m, k, n, r, adapters), dtype=torch.uint8, device=dev)
+    outs = [torch.empty_like(y), torch.empty_like(y)]
+    other = ids.flip(0).contiguous()
+    graphs = [torch.cuda.CUDAGraph(), torch.cuda.CUDAGraph()]
+    qg.lora_add(y, x, a, b, ids, scales=scales, out=outs[0], workspace=ws)
+    for g, i, o in zip(graphs, (ids, other), outs):
+        with torch.cuda.graph(g):
+            qg.lora_add(y, x, a, b, i, scales=scales, out=o, workspace=ws)
+    for k_ in range(3):
+        x.copy_(torch.randn(m, k, device=dev))
+        want = [qg.lora_add(y, x, a, b, i, scales=scales) for i in (ids, other)]
+        for g in graphs:
+            g.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(outs[0], want[0]) and torch.equal(outs[1], want[1]), k_
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        got = qg.lora_add(y, x, a, b, ids, scales=scales)
+    torch.cuda.current_stream().wait_stream(side)
+    assert torch.equal(got, want[0])
+    assert qg.lora_add(y[:0], x[:0], a, b, ids[:0]).shape == (0, n)
+
+
+def test_the_largest_widths(dev):
+    """Offsets of an adapter past 2^31 elements."""
+    k, r, n = 2 ** 20, 64, 128
+    adapters = 34                               # 34 * 64 * 2^20 elements of A: 4.25 GiB
+    a = torch.zeros(adapters, r, k, dtype=BF16, device=dev)
+    a[33] = (torch.randn(r, k, device=dev) * k ** -0.5).bfloat16()
+    b = torch.randn(adapters, n, r, device=dev).bfloat16()
+    x = torch.randn(2, k, device=dev).bfloat16()
+    y = torch.randn(2, n, device=dev)
+    ids = torch.tensor([33, 0], dtype=torch.int32, device=dev)
+    out = qg.lora_add(y, x, a, b, ids)
+    v = torch.matmul(a[33].double(), x[0].double())
+    want = y[0].double() + torch.matmul(b[33].double(), v)
+    # the chain of 2^20 / 128 additions of positive and negative terms, far under its bound of (k / 4) 2^-24
+    assert float((out[0].double() - want).abs().max()) <= 1e-2 and torch.equal(out[1], y[1])

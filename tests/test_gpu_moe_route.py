@@ -1,0 +1,130 @@
+"""qg.moe_route against 64 bits: the same experts in the same order, weights within
+half a step of fp32 (plus the 64-bit errors of a sum over 512 scores: 2^-40)."""
+from __future__ import annotations
+
+import numpy as np
+import pytest
+import torch
+
+import gemm_decode_qgemm_amd as qg
+import serving_reference as ref
+
+pytestmark = pytest.mark.gpu
+BF16, F32 = torch.bfloat16, torch.float32
+
+
+@pytest.fixture(scope="module")
+def dev():
+    assert torch.cuda.is_available(), "GPU tests need a HIP device"
+    return torch.device("cuda:0")
+
+
+def check(dev, l, k, sigmoid=False, bias=None, groups=1, top_groups=1, best=1, renorm=True, scale=1.0):
+    ids, w = qg.moe_route(l.to(dev), k, sigmoid=sigmoid, bias=None if bias is None else bias.to(dev), groups=groups,
+                          top_groups=top_groups, group_best=best, renormalize=renorm, scale=scale)
+    want, weights = ref.route(ref.f64(l), k, sigmoid, None if bias is None else ref.f64(bias), groups, top_groups, best, renorm,
+                              float(torch.tensor(scale)))
+    assert ids.dtype == torch.int32 and w.dtype == F32
+    assert np.array_equal(ids.cpu().numpy(), want), np.argwhere(ids.cpu().numpy() != want)[:3]
+    tol = ref.half_step(np.abs(weights) * (1 + 2.0 ** -30), 24) + 2.0 ** -40 * np.abs(weights)
+    assert np.all(np.abs(ref.f64(w) - weights) <= tol)
+    return ids, w
+
+
+@pytest.mark.parametrize("t,e,k", [(1, 1, 1), (3, 2, 2), (5, 8, 2), (7, 16, 16), (9, 60, 6), (4, 64, 8), (130, 65, 3), (61, 128, 8), (33, 160, 6),
+                                   (17, 256, 8), (5, 257, 32), (11, 384, 10), (3, 512, 32), (1000, 64, 4)])
+@pytest.mark.parametrize("sigmoid,bias,renorm", [(False, False, True), (False, True, False), (True, True, True), (True, False, False)])
+@pytest.mark.parametrize("half", [False, True])
+def test_choice(dev, t, e, k, sigmoid, bias, renorm, half):
+    torch.manual_seed(t + e)
+    l = 2 * torch.randn(t, e)
+    check(dev, l.bfloat16() if half else l, k, sigmoid, 0.2 * torch.randn(e) if bias else None, renorm=renorm, scale=2.5)
+
+
+@pytest.mark.parametrize("e,groups,top,k", [(256, 8, 4, 8), (256, 8, 1, 8), (64, 64, 7, 5), (160, 8, 3, 6), (512, 4, 2, 32), (384, 8, 8, 9), (66, 6, 2, 11),
+                                            (128, 2, 1, 32)])
+@pytest.mark.parametrize("sigmoid,bias", [(False, False), (True, True), (True, False), (False, True)])
+def test_groups(dev, e, groups, top, k, sigmoid, bias):
+    torch.manual_seed(e + groups)
+    l = 2 * torch.randn(53, e)
+    for best in (1, 2) if e > groups else (1,):
+        check(dev, l, k, sigmoid, 0.2 * torch.randn(e) if bias else None, groups, top, best, renorm=best == 2)
+        check(dev, l.bfloat16(), k, sigmoid, 0.2 * torch.randn(e).bfloat16().float() if bias else None, groups, top, best)
+
+
+def test_ties_go_to_the_lowest_index(dev):
+    l = torch.zeros(3, 256)
+    l[1, 200:] = 1.0
+    l[2] = torch.arange(256) % 4
+    for sigmoid in (False, True):
+        for bias in (None, torch.zeros(256), torch.full((256,), 0.5)):
+            check(dev, l, 8, sigmoid, bias)
+            check(dev, l, 8, sigmoid, bias, 8, 3, 2)
+            check(dev, l, 8, sigmoid, bias, 8, 3, 1)
+    # an expert's bias makes up exactly for another's score
+    check(dev, torch.zeros(1, 4), 2, True, torch.tensor([0.25, 0.5, 0.25, 0.5]))
+
+
+def test_near_ties_that_32_bits_do_not_tell_apart(dev):
+    """Scores of logits that differ in the last bits, biased so that the scores' first digits are lost in 32 bits."""
+    torch.manual_seed(4)
+    l = (1 + torch.arange(512).flip(0) * 2.0 ** -23)[torch.randperm(512)].repeat(5, 1)
+    bias = torch.full((512,), 8.0)
+    check(dev, l, 16, True, bias)
+    check(dev, l, 16, False, bias)
+    check(dev, l, 16, True, bias, 8, 3, 2)
+    check(dev, l, 16, True, None)
+    # far along the sigmoid, where 32 bits hold a one
+    check(dev, 20 + 0.01 * torch.randn(9, 256), 8, True, torch.zeros(256))
+
+
+def test_masked_experts_and_rows_without_any(dev):
+    inf = float("inf")
+    l = torch.randn(6, 64)
+    l[0, 3:] = -inf                        # three experts left for four picks
+    l[1] = -inf
+    l[2, ::2] = torch.finfo(F32).min
+    l[3] = torch.finfo(F32).min
+    l[4, 10] = 80.0
+    l[5, 20] = torch.finfo(F32).max
+    for sigmoid in (False, True):
+        for renorm in (False, True):
+            for groups in (1, 8):
+                check(dev, l, 4, sigmoid, None, groups, 1 if groups == 1 else 4, renorm=renorm)
+    bias = torch.zeros(64)
+    bias[5] = -inf                         # an expert that the bias takes out
+    ids, _ = check(dev, l[2:5], 8, True, bias)
+    assert not bool((ids == 5).any())
+    ids, w = qg.moe_route(l[1:2].to(dev), 4)
+    assert ids.tolist() == [[0, 1, 2, 3]] and not bool(w.any())
+
+
+def test_nan_counts_as_the_largest(dev):
+    l = torch.randn(2, 128)
+    l[0, 77] = float("nan")
+    for kw in (dict(), dict(sigmoid=True, bias=torch.zeros(128, device=dev)), dict(sigmoid=True, groups=4, top_groups=1, group_best=2)):
+        ids, w = qg.moe_route(l.to(dev), 4, **kw)
+        assert ids[0, 0] == 77 and bool(w[1].isfinite().all()) and bool(w[0, 0].isnan())
+
+
+def test_long_prompts_graph_and_out(dev):
+    l = torch.randn(70001, 64, device=dev)
+    ids, w = qg.moe_route(l, 6, sigmoid=True, scale=0.5)
+    top = torch.sort(l, dim=1, descending=True, stable=True).indices[:, :6]
+    assert torch.equal(ids.long(), top)
+    l = torch.randn(37, 256, device=dev)
+    bias = 0.1 * torch.randn(256, device=dev)
+    kw = dict(sigmoid=True, bias=bias, groups=8, top_groups=4, group_best=2)
+    out = (torch.zeros(37, 8, dtype=torch.int32, device=dev), torch.zeros(37, 8, device=dev))
+    graph = torch.cuda.CUDAGraph()
+    qg.moe_route(l, 8, **kw)
+    with torch.cuda.graph(graph):
+        qg.moe_route(l, 8, **kw, out=out)
+    for k in range(3):
+        l.copy_(torch.randn(37, 256, device=dev))
+        graph.replay()
+        torch.cuda.synchronize()
+        want = qg.moe_route(l, 8, **kw)
+        assert torch.equal(out[0], want[0]) and torch.equal(out[1], want[1]), k
+    e = qg.moe_route(l[:0], 8, **kw)
+    assert e[0].shape == (0, 8) and e[1].shape == (0, 8)
