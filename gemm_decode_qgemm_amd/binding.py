@@ -717,12 +717,15 @@ def moe_w4a16(x: torch.Tensor, router: torch.Tensor, gate_up: torch.Tensor, down
 
 # ---- operators of a serving step beside the linears ----------------------------
 
-def _on(dev: int, fn, *args) -> int:
-    """Calls into the library with `dev` as the current device, where its kernels launch."""
-    if torch.cuda.current_device() == dev:
-        return fn(*args, _stream_of(dev))
-    with torch.cuda.device(dev):
-        return fn(*args, _stream_of(dev))
+_current = torch._C._cuda_getDevice
+
+
+def _elsewhere(dev: int, fn):
+    """`fn` with `dev` as the current device, where the library's kernels launch."""
+    def call(*args):
+        with torch.cuda.device(dev):
+            return fn(*args)
+    return call
 
 
 def _float_type(t: torch.Tensor) -> int:
@@ -787,16 +790,18 @@ def rms_norm(x: torch.Tensor, weight: torch.Tensor | None = None, *, residual: t
     if not (_norm_args_ok(x, weight, residual, residual_out, dev) and _out_ok(out, out_dtype, shape, dev)):
         _refuse_norm(x, weight, residual, residual_out, [("out", out, out_dtype, shape)])
     if out is None:
-        out = torch.empty(shape, dtype=out_dtype, device=x.device)
+        out = torch.empty_like(x, dtype=out_dtype, memory_format=torch.contiguous_format)
     if residual is None:
-        st = _on(dev, lib.qg_rms_norm, x.data_ptr(), _float_type(x), x.stride(0), None, 0, 0, shape[0], shape[1], _ptr(weight), eps,
-                             out.data_ptr(), od, None)
+        call = lib.qg_rms_norm if _current() == dev else _elsewhere(dev, lib.qg_rms_norm)
+        st = call(x.data_ptr(), _float_type(x), x.stride(0), None, 0, 0, shape[0], shape[1], _ptr(weight), eps,
+                  out.data_ptr(), od, None, _stream_of(dev))
     else:
         if residual_out is None:
-            residual_out = torch.empty(shape, dtype=residual.dtype, device=x.device)
-        st = _on(dev, lib.qg_rms_norm, x.data_ptr(), _float_type(x), x.stride(0), residual.data_ptr(), _float_type(residual),
-                             residual.stride(0), shape[0], shape[1], _ptr(weight), eps, out.data_ptr(), od,
-                             residual_out.data_ptr())
+            residual_out = torch.empty_like(residual, memory_format=torch.contiguous_format)
+        call = lib.qg_rms_norm if _current() == dev else _elsewhere(dev, lib.qg_rms_norm)
+        st = call(x.data_ptr(), _float_type(x), x.stride(0), residual.data_ptr(), _float_type(residual),
+                  residual.stride(0), shape[0], shape[1], _ptr(weight), eps, out.data_ptr(), od,
+                  residual_out.data_ptr(), _stream_of(dev))
     if st:
         _check(st, "qg_rms_norm")
     return out if residual is None else (out, residual_out)
@@ -816,14 +821,15 @@ def rms_norm_q8(x: torch.Tensor, weight: torch.Tensor | None = None, *, residual
         _refuse_norm(x, weight, residual, residual_out, [("codes", codes, torch.int8, shape),
                                                          ("scales", scales, torch.float32, wide)])
     if out is None:
-        codes = torch.empty(shape, dtype=torch.int8, device=x.device)
+        codes = torch.empty_like(x, dtype=torch.int8, memory_format=torch.contiguous_format)
         scales = torch.empty(wide, dtype=_F32, device=x.device)
     if residual is not None and residual_out is None:
         residual_out = torch.empty(shape, dtype=residual.dtype, device=x.device)
-    st = _on(dev, lib.qg_rms_norm_q8, x.data_ptr(), _float_type(x), x.stride(0), _ptr(residual),
-                            0 if residual is None else _float_type(residual),
-                            0 if residual is None else residual.stride(0), shape[0], shape[1], _ptr(weight), eps,
-                            codes.data_ptr(), scales.data_ptr(), group_scales, _ptr(residual_out))
+    call = lib.qg_rms_norm_q8 if _current() == dev else _elsewhere(dev, lib.qg_rms_norm_q8)
+    st = call(x.data_ptr(), _float_type(x), x.stride(0), _ptr(residual),
+              0 if residual is None else _float_type(residual), 0 if residual is None else residual.stride(0),
+              shape[0], shape[1], _ptr(weight), eps, codes.data_ptr(), scales.data_ptr(), group_scales,
+              _ptr(residual_out), _stream_of(dev))
     if st:
         _check(st, "qg_rms_norm_q8")
     return (codes, scales) if residual is None else (codes, scales, residual_out)
@@ -896,10 +902,11 @@ def lora_add(y: torch.Tensor, x: torch.Tensor, a: torch.Tensor, b: torch.Tensor,
     else:
         ws_bytes = workspace.numel() * workspace.element_size()
     if out is None:
-        out = torch.empty(ys, dtype=out_dtype, device=x.device)
-    st = _on(dev, lib.qg_lora_add, x.data_ptr(), m, k, a.data_ptr(), b.data_ptr(), r, adapters, ids.data_ptr(), _ptr(scales),
-                         y.data_ptr(), _float_type(y), y.stride(0), ys[1], out.data_ptr(), od, out.stride(0),
-                         workspace.data_ptr(), ws_bytes, _ptr(status))
+        out = torch.empty_like(y, dtype=out_dtype, memory_format=torch.contiguous_format)
+    call = lib.qg_lora_add if _current() == dev else _elsewhere(dev, lib.qg_lora_add)
+    st = call(x.data_ptr(), m, k, a.data_ptr(), b.data_ptr(), r, adapters, ids.data_ptr(), _ptr(scales), y.data_ptr(),
+              _float_type(y), y.stride(0), ys[1], out.data_ptr(), od, out.stride(0), workspace.data_ptr(), ws_bytes,
+              _ptr(status), _stream_of(dev))
     if st:
         _check(st, "qg_lora_add")
     return out
@@ -943,10 +950,10 @@ def moe_route(logits: torch.Tensor, top_k: int, *, sigmoid: bool = False, bias: 
     if out is None:
         if top_k < 1:
             _check(-2, "qg_moe_route")
-        ids = torch.empty(shape, dtype=_I32, device=logits.device)
-        weights = torch.empty(shape, dtype=_F32, device=logits.device)
-    st = _on(dev, lib.qg_moe_route, logits.data_ptr(), _float_type(logits), ls[0], ls[1], top_k, sigmoid, _ptr(bias), groups,
-                          top_groups, group_best, renormalize, scale, ids.data_ptr(), weights.data_ptr())
+        ids, weights = logits.new_empty(shape, dtype=_I32), logits.new_empty(shape, dtype=_F32)
+    call = lib.qg_moe_route if _current() == dev else _elsewhere(dev, lib.qg_moe_route)
+    st = call(logits.data_ptr(), _float_type(logits), ls[0], ls[1], top_k, sigmoid, _ptr(bias), groups, top_groups,
+              group_best, renormalize, scale, ids.data_ptr(), weights.data_ptr(), _stream_of(dev))
     if st:
         _check(st, "qg_moe_route")
     return ids, weights
@@ -1011,15 +1018,16 @@ def verify_drafts(target: torch.Tensor, draft: torch.Tensor | None, tokens: torc
         ws_bytes = lib.qg_verify_drafts_workspace_bytes(ts[0], b, ts[1])
         if ws_bytes < 0:
             _check(ws_bytes, "qg_verify_drafts")
-        workspace = torch.empty(ws_bytes, dtype=torch.uint8, device=target.device)
+        if ws_bytes > 0:
+            workspace = torch.empty(ws_bytes, dtype=torch.uint8, device=target.device)
     else:
         ws_bytes = workspace.numel() * workspace.element_size()
     if out is None:
-        accepted = torch.empty(b, dtype=_I32, device=target.device)
-        following = torch.empty(b, dtype=_I32, device=target.device)
-    st = _on(dev, lib.qg_verify_drafts, target.data_ptr(), _ptr(draft), _float_type(target), ts[0], ts[1], tokens.data_ptr(),
-                              u.data_ptr(), u_next.data_ptr(), cu.data_ptr(), b, _ptr(lens), accepted.data_ptr(),
-                              following.data_ptr(), workspace.data_ptr(), ws_bytes, _ptr(status))
+        accepted, following = torch.empty_like(u_next, dtype=_I32), torch.empty_like(u_next, dtype=_I32)
+    call = lib.qg_verify_drafts if _current() == dev else _elsewhere(dev, lib.qg_verify_drafts)
+    st = call(target.data_ptr(), _ptr(draft), _float_type(target), ts[0], ts[1], tokens.data_ptr(), u.data_ptr(),
+              u_next.data_ptr(), cu.data_ptr(), b, _ptr(lens), accepted.data_ptr(), following.data_ptr(),
+              _ptr(workspace), ws_bytes, _ptr(status), _stream_of(dev))
     if st:
         _check(st, "qg_verify_drafts")
     return accepted, following

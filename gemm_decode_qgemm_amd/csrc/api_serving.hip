@@ -11,10 +11,10 @@
 namespace qg {
 hipError_t launch_rms_norm(const RmsNormArgs& a, hipStream_t stream);
 int lora_splits(int64_t m, int64_t k, int64_t r, int64_t adapters);
-hipError_t launch_lora_add(const LoraArgs& a, hipStream_t stream);
-hipError_t launch_moe_route(const RouteArgs& a, hipStream_t stream);
-int verify_chunk(int64_t v);
-hipError_t launch_verify_drafts(const VerifyArgs& a, hipStream_t stream);
+hipError_t launch_lora_add(LoraArgs a, hipStream_t stream);
+hipError_t launch_moe_route(RouteArgs a, hipStream_t stream);
+int64_t verify_ws_bytes(int64_t b, int64_t v);
+hipError_t launch_verify_drafts(VerifyArgs a, hipStream_t stream);
 }  // namespace qg
 
 namespace {
@@ -68,11 +68,6 @@ int64_t lora_ws(int64_t m, int64_t k, int64_t r, int64_t adapters) {
 int32_t verify_shape(int64_t rows, int64_t b, int64_t v) {
   if (b < 0 || b > 65535 || rows < b || rows > 0x7fffffff || v < 1 || v > 0x7fffffff) return QG_E_SHAPE;
   return QG_OK;
-}
-
-int64_t verify_ws(int64_t b, int64_t v) {
-  const int64_t c = qg::verify_chunk(v);
-  return b * ((v + c - 1) / c) * 16;
 }
 
 }  // namespace
@@ -169,7 +164,7 @@ int32_t qg_moe_route(const void* logits, int32_t logits_dtype, int64_t t, int64_
 
 int64_t qg_verify_drafts_workspace_bytes(int64_t rows, int64_t b, int64_t v) {
   const int32_t st = verify_shape(rows, b, v);
-  return st != QG_OK ? st : verify_ws(b, v);
+  return st != QG_OK ? st : qg::verify_ws_bytes(b, v);
 }
 
 int32_t qg_verify_drafts(const void* target, const void* draft, int32_t dtype, int64_t rows, int64_t v,
@@ -185,13 +180,12 @@ int32_t qg_verify_drafts(const void* target, const void* draft, int32_t dtype, i
       !aligned(status_dev, 4))
     return QG_E_ALIGN;
   if (b == 0) return QG_OK;
-  if (!target || !u_next || !cu || !accepted || !next || !ws || (rows > b && (!tokens || !u))) return QG_E_NULL;
-  if (ws_bytes < verify_ws(b, v)) return QG_E_BUFFER;
+  if (!target || !u_next || !cu || !accepted || !next || (rows > b && (!tokens || !u))) return QG_E_NULL;
+  const int64_t need = qg::verify_ws_bytes(b, v);
+  if (need > 0 && (!ws || ws_bytes < need)) return ws ? QG_E_BUFFER : QG_E_NULL;
   qg::VerifyArgs a{};
   a.target = target, a.draft = draft, a.tokens = tokens, a.cu = cu, a.u = u, a.u_next = u_next;
   a.rows = rows, a.v = v, a.b = (int)b, a.half = dtype == QG_BF16;
-  a.chunk = qg::verify_chunk(v);
-  a.chunks = (int)((v + a.chunk - 1) / a.chunk);
   a.lens = lens, a.accepted = accepted, a.next = next;
   a.part = static_cast<double*>(ws);
   a.status = status_dev;

@@ -43,6 +43,13 @@ __device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
   return __builtin_bit_cast(uint32_t, v);
 }
 
+// A barrier for LDS alone: loads from memory stay in flight across it.
+__device__ __forceinline__ void lds_barrier() {
+  __builtin_amdgcn_fence(__ATOMIC_RELEASE, "workgroup", "local");
+  __builtin_amdgcn_s_barrier();
+  __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "workgroup", "local");
+}
+
 // First byte of the codes of (page, head): keys, then 64 d bytes of values.
 __device__ __forceinline__ size_t kv8_base(int64_t page, int hkv, int h, int d) {
   return ((size_t)page * hkv + h) * (2 * kPage) * (size_t)d;
@@ -100,7 +107,7 @@ struct LoraArgs {
   const void* y;                    // [m, n], rows y_stride apart
   void* out;                        // rows out_stride apart
   int64_t y_stride, out_stride;
-  int m, k, n, r, adapters, y_f32, out_f32, splits;
+  int m, k, n, r, adapters, y_f32, out_f32, splits, steps;
   float* part;                      // [splits, m, r]
   uint32_t* status;
 };
@@ -111,6 +118,7 @@ struct RouteArgs {
   const float* bias;                // [e] or null
   int64_t t;
   int e, k, half, sigmoid, groups, top_groups, best, renorm;
+  int whole, lanes, shift;          // set by the launcher (moe_route.hip)
   float scale;
   int32_t* ids;                     // [t, k]
   float* weights;                   // [t, k]
@@ -122,10 +130,12 @@ struct VerifyArgs {
   const int32_t *tokens, *cu;
   const float *u, *u_next;
   int64_t rows, v;
-  int b, half, chunk, chunks;
+  int b, half;
   int32_t *lens, *accepted, *next;
-  double* part;                     // [b, chunks, 2]
+  double* part;                     // [b, pieces]
   uint32_t* status;
+  int64_t piece;                    // set by the launcher, as what follows
+  int pieces, whole;                // whole: rows can be read 16 bytes at a time
 };
 
 }  // namespace qg

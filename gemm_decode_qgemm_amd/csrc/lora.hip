@@ -21,10 +21,13 @@
 #include <algorithm>
 
 #include "layer_common.h"
+#include "w4_common.h"
 
 namespace qg {
 
 constexpr int kLoraRows = QG_MAX_M;
+constexpr int kLoraSplits = 16;        // of K, at most
+constexpr int kLoraStep = 1024;        // k of a workgroup whose loads are all in flight together
 
 // The rows of unit `unit` as a mask, or 0 where it has none (or another unit
 // works for them); `adapter` is theirs.
@@ -54,7 +57,7 @@ __device__ __forceinline__ void lora_down(const LoraArgs& a, int adapter, int co
 #pragma unroll
   for (int t = 0; t < MT; ++t) x[t] = a.x + (size_t)rows[min(16 * t + i, count - 1)] * a.k + 8 * q;
   f32x4_t acc[MT] = {};
-  constexpr int U = MT == 1 ? 4 : 2;
+  constexpr int U = MT == 1 ? kLoraStep / 128 : MT == 2 ? 4 : 2;
   for (int c = k0 + 32 * wave; c < k1; c += 128 * U) {
     u32x4_t wv[U], xv[U][MT];
 #pragma unroll
@@ -79,10 +82,10 @@ __device__ __forceinline__ void lora_down(const LoraArgs& a, int adapter, int co
   // acc[t][e]: row 16 t + 4 q + e of the unit, rank r0 + i
 #pragma unroll
   for (int t = 0; t < MT; ++t) {
-    if (t > 0) __syncthreads();
+    if (t > 0) lds_barrier();
 #pragma unroll
     for (int e = 0; e < 4; ++e) red[wave][4 * q + e][i] = acc[t][e];
-    __syncthreads();
+    lds_barrier();
     const int m = threadIdx.x >> 4, r = threadIdx.x & 15;
     if (16 * t + m < count && r0 + r < a.r)
       a.part[((size_t)blockIdx.z * a.m + rows[16 * t + m]) * a.r + r0 + r] =
@@ -97,7 +100,7 @@ __global__ __launch_bounds__(256) void lora_down_kernel(LoraArgs a) {
   const uint64_t mask = lora_rows(a, blockIdx.y, adapter);
   if (mask == 0) return;             // the same in all waves
   lora_list(mask, rows);
-  __syncthreads();
+  lds_barrier();
   const int count = __popcll(mask);
   const int steps = (a.k + 127) >> 7;                    // of 128 k, shared out evenly
   const int k0 = 128 * (int)((int64_t)steps * blockIdx.z / a.splits);
@@ -110,40 +113,110 @@ __global__ __launch_bounds__(256) void lora_down_kernel(LoraArgs a) {
     lora_down<4>(a, adapter, count, rows, 16 * blockIdx.x, k0, k1, red);
 }
 
+template <bool Y32>
 __device__ __forceinline__ float lora_y(const LoraArgs& a, int row, int col) {
   const size_t at = (size_t)row * a.y_stride + col;
-  return a.y_f32 ? static_cast<const float*>(a.y)[at] : bf16_to_f32(static_cast<const uint16_t*>(a.y)[at]);
+  return Y32 ? static_cast<const float*>(a.y)[at] : bf16_to_f32(static_cast<const uint16_t*>(a.y)[at]);
 }
 
+template <bool OUT32>
 __device__ __forceinline__ void lora_store(const LoraArgs& a, int row, int col, float v) {
   const size_t at = (size_t)row * a.out_stride + col;
-  if (a.out_f32)
+  if constexpr (OUT32)
     static_cast<float*>(a.out)[at] = v;
   else
     static_cast<uint16_t*>(a.out)[at] = (uint16_t)f32_to_bf16_rne(v);
 }
 
-// RS steps of 32 ranks, NB tiles of 16 columns a wave.
+// The workgroup's columns of a row without an adapter, by a wave: y as it is; NaN for
+// an adapter that is not there.
+template <bool Y32, bool OUT32>
+__device__ __forceinline__ void lora_rest(const LoraArgs& a, int m) {
+  const int lane = threadIdx.x & 63;
+  if (m >= a.m) return;
+  const int id = a.ids[m];
+  const bool bad = id >= a.adapters;
+  if (id >= 0 && !bad) return;
+  if (bad && a.status && blockIdx.x == 0 && lane == 0) atomicOr(a.status, QG_FLAG_INDEX);
+  if (!bad && a.y == a.out) return;    // in place there is nothing to do
+  for (int c0 = blockIdx.x * 256; c0 < a.n; c0 += gridDim.x * 256) {
+    float v[4];
+#pragma unroll
+    for (int j = 0; j < 4; ++j)
+      v[j] = bad ? __uint_as_float(0x7fc00000u) : lora_y<Y32>(a, m, min(c0 + 64 * j + lane, a.n - 1));
+#pragma unroll
+    for (int j = 0; j < 4; ++j)
+      if (c0 + 64 * j + lane < a.n) lora_store<OUT32>(a, m, c0 + 64 * j + lane, v[j]);
+  }
+}
+
+// 64 columns of B, 4 tiles of 16, as a wave's operands; zeros past its view.
 template <int RS>
-__global__ __launch_bounds__(256) void lora_up_kernel(LoraArgs a) {
-  constexpr int NB = RS >= 4 ? 8 / RS : 4;
-  constexpr int COLS = 64 * NB;                  // of a workgroup
-  constexpr int ROWS = RS > 4 ? 32 : 64;         // at a time, for LDS
+struct LoraB {
+  u32x4_t w[4][RS];
+
+  __device__ __forceinline__ void load(const BufView& b, int r, int col) {
+    const int lane = threadIdx.x & 63, i = lane & 15, q = lane >> 4;
+    const uint32_t row = 2u * (uint32_t)r, at = (uint32_t)(col + i) * row + 16u * q;
+#pragma unroll
+    for (int s = 0; s < RS; ++s) {
+      const uint32_t from = 32 * s + 8 * q < r ? at + 64u * s : 0xfffffff0u - 64u * row;
+#pragma unroll
+      for (int t = 0; t < 4; ++t) w[t][s] = b.b128<false>(from + 16u * t * row);
+    }
+  }
+};
+
+// 4 rows of y or out as views of their n columns.
+struct LoraRows {
+  __amdgpu_buffer_rsrc_t row[4];
+  __device__ __forceinline__ LoraRows(const void* base, bool f32, int64_t stride, const int* rows, int part, int n) {
+#pragma unroll
+    for (int m = 0; m < 4; ++m) {
+      const int64_t at = (int64_t)__builtin_amdgcn_readfirstlane(rows[min(m, part - 1)]) * stride;
+      row[m] = __builtin_amdgcn_make_buffer_rsrc(
+          const_cast<char*>(static_cast<const char*>(base) + at * (f32 ? 4 : 2)), (short)0,
+          m < part ? n * (f32 ? 4 : 2) : 0, 0x00020000);
+    }
+  }
+  template <bool F32>
+  __device__ __forceinline__ float load(int m, int col) const {
+    if constexpr (F32) return __uint_as_float(__builtin_amdgcn_raw_buffer_load_b32(row[m], 4 * col, 0, 0));
+    return bf16_to_f32((uint16_t)__builtin_amdgcn_raw_buffer_load_b16(row[m], 2 * col, 0, 0));
+  }
+  template <bool F32>
+  __device__ __forceinline__ void store(int m, int col, float v) const {
+    if constexpr (F32)
+      __builtin_amdgcn_raw_buffer_store_b32(__float_as_uint(v), row[m], 4 * col, 0, 0);
+    else
+      __builtin_amdgcn_raw_buffer_store_b16((uint16_t)f32_to_bf16_rne(v), row[m], 2 * col, 0, 0);
+  }
+};
+
+// RS steps of 32 ranks.  A wave takes 64 columns at a time, B of the next ones in
+// flight, and 4 rows at a time: the operand repeats them, so that lane (i, q) has all
+// four for column i of every tile and takes tile q, 64 neighbouring columns a row.
+// (16 rows at a time would take a quarter of the matrix instructions, of which there
+// are plenty, and touch 16 columns of a row at a time.)
+#ifndef QG_LS
+#define QG_LS 4
+#define QG_LD 8
+#endif
+#ifdef QG_LW
+#define QG_WP __attribute__((amdgpu_waves_per_eu(QG_LW)))
+#else
+#define QG_WP
+#endif
+template <int RS, bool Y32, bool OUT32>
+__global__ __launch_bounds__(256) QG_WP void lora_up_kernel(LoraArgs a) {
   constexpr int LD = 32 * RS + 8;                // bf16 apart: operand reads on distinct banks
-  __shared__ __attribute__((aligned(16))) uint16_t low[3][ROWS][LD];
+  __shared__ __attribute__((aligned(16))) uint16_t low[3][16][LD];
   __shared__ int rows[kLoraRows];
   const int tid = threadIdx.x, lane = tid & 63, i = lane & 15, q = lane >> 4, wave = wave_id_uniform();
-  const int units = gridDim.y - 1;
-  const int n0 = blockIdx.x * COLS;
-  if ((int)blockIdx.y == units) {                // rows without an adapter
-    for (int m = 0; m < a.m; ++m) {
-      const int id = a.ids[m];
-      if (id >= 0 && id < a.adapters) continue;
-      const bool bad = id >= a.adapters;
-      if (bad && a.status && blockIdx.x == 0 && tid == 0) atomicOr(a.status, QG_FLAG_INDEX);
-      for (int c = n0 + tid; c < min(n0 + COLS, a.n); c += 256)
-        lora_store(a, m, c, bad ? __uint_as_float(0x7fc00000u) : lora_y(a, m, c));
-    }
+  const int units = min(a.m, a.adapters);
+  const int first = blockIdx.x * 256 + 64 * wave, stride = gridDim.x * 256;   // this wave's columns
+  if ((int)blockIdx.y >= units) {
+    lora_rest<Y32, OUT32>(a, 4 * ((int)blockIdx.y - units) + wave);
     return;
   }
   int adapter;
@@ -151,26 +224,35 @@ __global__ __launch_bounds__(256) void lora_up_kernel(LoraArgs a) {
   if (mask == 0) return;                         // the same in all waves
   const int count = __popcll(mask);
   lora_list(mask, rows);
-  u32x4_t w[NB][RS];                             // B, on its way while the partial sums are added
-#pragma unroll
-  for (int b = 0; b < NB; ++b)
-#pragma unroll
-    for (int s = 0; s < RS; ++s) {
-      const int col = min(n0 + 16 * (NB * wave + b) + i, a.n - 1), rank = 32 * s + 8 * q;
-      w[b][s] = u32x4_t{0u, 0u, 0u, 0u};
-      if (rank < a.r) w[b][s] = *reinterpret_cast<const u32x4_t*>(a.b + ((size_t)adapter * a.n + col) * a.r + rank);
-    }
-  __syncthreads();
+  const BufView b(a.b + (size_t)adapter * a.n * a.r, a.n * a.r * 2);
+  LoraB<RS> w0;
+  w0.load(b, a.r, first);                    // on its way while the first product's parts are added
+  lds_barrier();
   const float scale = a.scales ? a.scales[adapter] : 1.0f;
-  for (int m0 = 0; m0 < count; m0 += ROWS) {
-    if (m0 > 0) __syncthreads();
-    const int part = min(ROWS, count - m0);
+  for (int m0 = 0; m0 < count; m0 += 16) {
+    const int part = min(16, count - m0);
+    const int* const mine = rows + m0;
+    if (m0 > 0) {
+      lds_barrier();
+      w0.load(b, a.r, first);
+    }
+    const LoraRows y0(a.y, Y32, a.y_stride, mine, min(part, 4), a.n);
+    float y[4];
+#pragma unroll
+    for (int m = 0; m < 4; ++m) y[m] = y0.load<Y32>(m, first + lane);
+#pragma unroll 1
     for (int at = tid; at < part * 32 * RS; at += 256) {
       const int m = at / (32 * RS), r = at % (32 * RS);
       float v = 0.0f;
-      if (r < a.r)
-        for (int s = 0; s < a.splits; ++s) v += a.part[((size_t)s * a.m + rows[m0 + m]) * a.r + r];
-      v = r < a.r ? v * scale : 0.0f;
+      if (r < a.r) {
+        float t[kLoraSplits];                    // all on their way together
+        const float* const p = a.part + (size_t)mine[m] * a.r + r;
+#pragma unroll
+        for (int s = 0; s < kLoraSplits; ++s) t[s] = s < a.splits ? p[(size_t)s * a.m * a.r] : 0.0f;
+#pragma unroll
+        for (int s = 0; s < kLoraSplits; ++s) v += t[s];
+        v *= scale;
+      }
 #pragma unroll
       for (int u = 0; u < 3; ++u) {
         const uint32_t h = f32_to_bf16_rne(v);
@@ -178,52 +260,82 @@ __global__ __launch_bounds__(256) void lora_up_kernel(LoraArgs a) {
         v = (h & 0x7fffu) < 0x7f80u ? v - bf16_to_f32(h) : 0.0f;   // an infinity is whole in the first
       }
     }
-    __syncthreads();
-    for (int t = 0; t < part; t += 16) {
-      f32x4_t acc[NB] = {};
+    lds_barrier();
+    auto step = [&](const LoraB<RS>& w, int col) {
+      for (int g = 0; g < part; g += 4) {
+        const int some = min(part - g, 4);
+        const LoraRows ys(a.y, Y32, a.y_stride, mine + g, some, a.n);
+        if (g > 0) {
 #pragma unroll
-      for (int s = 0; s < RS; ++s)
-#pragma unroll
-        for (int u = 2; u >= 0; --u) {
-          const u32x4_t v = *reinterpret_cast<const u32x4_t*>(&low[u][min(t + i, part - 1)][32 * s + 8 * q]);
-#pragma unroll
-          for (int b = 0; b < NB; ++b)
-            acc[b] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8_t, v),
-                                                             __builtin_bit_cast(bf16x8_t, w[b][s]), acc[b], 0, 0, 0);
+          for (int m = 0; m < 4; ++m) y[m] = ys.load<Y32>(m, col + lane);
         }
+        f32x4_t acc[4] = {};
 #pragma unroll
-      for (int b = 0; b < NB; ++b)
+        for (int s = 0; s < RS; ++s)
 #pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          const int m = t + 4 * q + e, col = n0 + 16 * (NB * wave + b) + i;
-          if (m < part && col < a.n) lora_store(a, rows[m0 + m], col, lora_y(a, rows[m0 + m], col) + acc[b][e]);
+          for (int u = 2; u >= 0; --u) {
+            const u32x4_t v = *reinterpret_cast<const u32x4_t*>(&low[u][g + min(i & 3, some - 1)][32 * s + 8 * q]);
+#pragma unroll
+            for (int t = 0; t < 4; ++t)
+              acc[t] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8_t, v),
+                                                               __builtin_bit_cast(bf16x8_t, w.w[t][s]), acc[t], 0, 0, 0);
+          }
+        const LoraRows os(a.out, OUT32, a.out_stride, mine + g, some, a.n);
+#pragma unroll
+        for (int m = 0; m < 4; ++m) {
+          const float v = q < 2 ? (q == 0 ? acc[0][m] : acc[1][m]) : (q == 2 ? acc[2][m] : acc[3][m]);
+          os.store<OUT32>(m, col + lane, y[m] + v);
         }
+      }
+    };
+    for (int col = first; col < a.n; col += stride) {
+      const int next = col + stride;
+      if constexpr (RS <= 4) {
+        LoraB<RS> w1;
+        if (next < a.n) w1.load(b, a.r, next);
+        step(w0, col);
+        w0 = w1;
+      } else {                                   // B takes the registers of two: no next one in flight
+        step(w0, col);
+        if (next < a.n) w0.load(b, a.r, next);
+      }
+      if (next < a.n)
+#pragma unroll
+        for (int m = 0; m < 4; ++m) y[m] = y0.load<Y32>(m, next + lane);
     }
   }
 }
 
 int lora_splits(int64_t m, int64_t k, int64_t r, int64_t adapters) {
-  // Two workgroups a CU, of at least four steps of 128 k each.
-  const int64_t units = std::min(m, adapters) * ((r + 15) / 16), steps = (k + 127) / 128;
-  return (int)std::max<int64_t>(1, std::min<int64_t>({(2 * kCUs + units - 1) / units, (steps + 3) / 4, 16}));
+  (void)m, (void)r, (void)adapters;
+  return (int)std::min<int64_t>(kLoraSplits, (k + kLoraStep - 1) / kLoraStep);
 }
 
-hipError_t launch_lora_add(const LoraArgs& a, hipStream_t stream) {
+hipError_t launch_lora_add(LoraArgs a, hipStream_t stream) {
   const int units = std::min(a.m, a.adapters);
   hipLaunchKernelGGL(lora_down_kernel, dim3((a.r + 15) / 16, units, a.splits), dim3(256), 0, stream, a);
   const hipError_t st = hipGetLastError();
   if (st != hipSuccess) return st;
-#define QG_LORA(RS)                                                                                           \
-  hipLaunchKernelGGL((lora_up_kernel<RS>), dim3((a.n + 64 * (RS >= 4 ? 8 / RS : 4) - 1) / (64 * (RS >= 4 ? 8 / RS : 4)), \
-                                                units + 1), dim3(256), 0, stream, a)
+  // Steps a wave: up to 4 while eight workgroups a CU are left.
+  const int blocks = (a.n + 255) / 256;
+  a.steps = std::max(1, std::min(QG_LS, (int)((int64_t)units * blocks / (QG_LD * kCUs))));
+  const dim3 grid((blocks + a.steps - 1) / a.steps, units + (a.m + 3) / 4);
+  const int types = (a.y_f32 ? 2 : 0) + (a.out_f32 ? 1 : 0);
+#define QG_LORA(RS)                                                                                    \
+  switch (types) {                                                                                     \
+    case 0: hipLaunchKernelGGL((lora_up_kernel<RS, false, false>), grid, dim3(256), 0, stream, a); break; \
+    case 1: hipLaunchKernelGGL((lora_up_kernel<RS, false, true>), grid, dim3(256), 0, stream, a); break;  \
+    case 2: hipLaunchKernelGGL((lora_up_kernel<RS, true, false>), grid, dim3(256), 0, stream, a); break;  \
+    case 3: hipLaunchKernelGGL((lora_up_kernel<RS, true, true>), grid, dim3(256), 0, stream, a); break;   \
+  }
   if (a.r <= 32)
-    QG_LORA(1);
+    QG_LORA(1)
   else if (a.r <= 64)
-    QG_LORA(2);
+    QG_LORA(2)
   else if (a.r <= 128)
-    QG_LORA(4);
+    QG_LORA(4)
   else
-    QG_LORA(8);
+    QG_LORA(8)
 #undef QG_LORA
   return hipGetLastError();
 }

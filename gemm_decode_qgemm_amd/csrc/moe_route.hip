@@ -5,15 +5,26 @@
 //   best groups stay;   the top k experts by c among them, ties to the lowest index;
 //   w = s of the picked, over their sum where renormalized, times a scale
 //
-// A wave takes a token, lane l experts l, 64 + l, ...  Scores are formed in 64 bits:
-// which of two experts comes first is a comparison of computed numbers, and in 32
-// bits one choice in some thousands would go by rounding.  Where no bias and no sum
-// of two takes part the order is that of the logits, compared as they are.
+// A wave takes a token, lane l experts U l .. U l + U - 1.  Which of two experts comes
+// first is a comparison of computed numbers, and in 32 bits one choice in some
+// thousands would go by rounding.  So:
+//  * where no bias and no sum of two takes part, the order is that of the logits,
+//    which are compared as they are;
+//  * else c is formed in 32 bits with a bound on its error, and where all
+//    numbers that were compared are further apart than that, the choice is the
+//    exact one; a token where they are not (about one in a thousand) is done again
+//    in 64 bits.
+// Weights are formed in 64 bits from the picked logits, a lane each, by one wave for
+// several tokens.
+//
+// The k-th largest c is found by bisection: a ballot per register and step, from
+// the largest c down until exactly k are left above, about ten steps.
 #include "layer_common.h"
+#include "wave.h"
 
 namespace qg {
 
-// A number as an unsigned one of the same order; NaN is above all, -0 is 0, none is 0.
+// A number as an unsigned one of the same order; NaN is above all, -0 is 0, and none is 0.
 __device__ __forceinline__ uint64_t order64(double c) {
   c += 0.0;
   const uint64_t u = (uint64_t)__double_as_longlong(c);
@@ -21,81 +32,144 @@ __device__ __forceinline__ uint64_t order64(double c) {
   return (u >> 63) != 0 ? ~u : u | (uint64_t)1 << 63;
 }
 
-__device__ __forceinline__ uint32_t wave_max32(uint32_t v) {
-  auto step = [&](uint32_t o) { v = max(v, o); };
-  step((uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, 0x111, 0xf, 0xf, false));   // row_shr 1, 2, 4, 8
-  step((uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, 0x112, 0xf, 0xf, false));
-  step((uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, 0x114, 0xf, 0xf, false));
-  step((uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, 0x118, 0xf, 0xf, false));
-  step((uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, 0x142, 0xa, 0xf, false));   // row_bcast 15, 31
-  step((uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, 0x143, 0xc, 0xf, false));
-  return (uint32_t)__builtin_amdgcn_readlane((int)v, 63);
+// The same order for binary32 numbers, as steps of a bisection; and back.
+__device__ __forceinline__ uint32_t step_of(float c) {
+  const uint32_t u = __float_as_uint(c + 0.0f);
+  return (u & 0x80000000u) ? ~u : u | 0x80000000u;
+}
+__device__ __forceinline__ float step_to(uint32_t k) {
+  return __uint_as_float((k & 0x80000000u) ? k ^ 0x80000000u : ~k);
 }
 
-__device__ __forceinline__ double wave_sum64(double v) {
-#pragma unroll
-  for (int o = 1; o < 64; o *= 2) v += __shfl_xor(v, o);
-  return v;
+template <int CTRL>
+__device__ __forceinline__ float dpp_f(float v) {
+  return __uint_as_float((uint32_t)__builtin_amdgcn_update_dpp(0, (int)__float_as_uint(v), CTRL, 0xf, 0xf, true));
 }
 
-template <int U>   // experts a lane
-__global__ __launch_bounds__(256) void moe_route_top_kernel(RouteArgs a) {
-  __shared__ double choice_s[4][64 * U];
-  const int lane = threadIdx.x & 63, wave = wave_id_uniform();
-  const int64_t t = (int64_t)blockIdx.x * 4 + wave;
-  if (t >= a.t) return;              // a wave's LDS is its own
-  float l[U];
+// The value of lane l ^ O, where lanes of an O-aligned block hold the same value.
+template <int O>
+__device__ __forceinline__ float other_block(float v) {
+  if constexpr (O == 1) return dpp_f<0xB1>(v);         // quad_perm [1,0,3,2]
+  if constexpr (O == 2) return dpp_f<0x4E>(v);         // quad_perm [2,3,0,1]
+  if constexpr (O == 4) return dpp_f<0x141>(v);        // row_half_mirror
+  if constexpr (O == 8) return dpp_f<0x140>(v);        // row_mirror
+  return __shfl_xor(v, O);
+}
+
+// The best two over blocks of 2 O lanes from those of O.
+template <int O>
+__device__ __forceinline__ void best_two(int lanes, float& c1, float& c2) {
+  if (O >= lanes) return;              // uniform
+  const float d1 = other_block<O>(c1), d2 = other_block<O>(c2);
+  c2 = fmaxf(fminf(c1, d1), fmaxf(c2, d2));
+  c1 = fmaxf(c1, d1);
+}
+
+// A wave's own LDS: its operations complete in order.
+__device__ __forceinline__ void wave_fence() {
+  __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
+  __builtin_amdgcn_wave_barrier();
+  __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
+}
+
+struct __attribute__((aligned(16))) Pick {
+  float c, x;                          // what decides, and the logit
+  int id, pad;
+};
+
+constexpr int kRouteTokens = 8;        // of a workgroup, a wave each
+
+template <int U>
+struct RouteLds {
+  union {
+    double choice[64 * U];             // of the exact way: c of every expert, in 64 bits
+    Pick by_expert[32];
+  };
+};
+
+// U values from the lane's place on in a row of n, `none` past it.  `whole`: rows and
+// places are aligned to U values, and n is a multiple of U.
+template <int U>
+__device__ __forceinline__ void load_row(float (&v)[U], const void* row, bool half, bool whole, int n, float none) {
+  const int e = U * (int)(threadIdx.x & 63);
 #pragma unroll
-  for (int u = 0; u < U; ++u) {
-    const int e = 64 * u + lane;
-    l[u] = -__builtin_inff();
-    if (e < a.e)
-      l[u] = a.half ? bf16_to_f32(static_cast<const uint16_t*>(a.logits)[t * a.e + e])
-                    : static_cast<const float*>(a.logits)[t * a.e + e];
-  }
-  double s[U];
-  if (a.sigmoid) {
+  for (int u = 0; u < U; ++u) v[u] = none;
+  if (whole) {
+    if (e >= n) return;
+    if (half) {
+      struct __attribute__((aligned(2 * U))) Pack { uint16_t v[U]; };
+      const Pack p = *reinterpret_cast<const Pack*>(static_cast<const uint16_t*>(row) + e);
 #pragma unroll
-    for (int u = 0; u < U; ++u) s[u] = 1.0 / (1.0 + exp(-(double)l[u]));
-  } else {
-    float top = l[0];
+      for (int u = 0; u < U; ++u) v[u] = bf16_to_f32(p.v[u]);
+    } else {
+      struct __attribute__((aligned(U < 4 ? 4 * U : 16))) Pack { float v[U]; };
+      const Pack p = *reinterpret_cast<const Pack*>(static_cast<const float*>(row) + e);
 #pragma unroll
-    for (int u = 1; u < U; ++u) top = fmaxf(top, l[u]);
-#pragma unroll
-    for (int o = 1; o < 64; o *= 2) top = fmaxf(top, __shfl_xor(top, o));
-    double total = 0.0;
-#pragma unroll
-    for (int u = 0; u < U; ++u) {
-      // a token without a logit above -infinity has no scores; NaN stays NaN
-      s[u] = l[u] == -__builtin_inff() ? 0.0 : exp((double)l[u] - (double)top);
-      total += s[u];
+      for (int u = 0; u < U; ++u) v[u] = p.v[u];
     }
-    total = wave_sum64(total);
+  } else {
 #pragma unroll
-    for (int u = 0; u < U; ++u) s[u] = total == 0.0 ? 0.0 : s[u] / total;
+    for (int u = 0; u < U; ++u)
+      if (e + u < n) v[u] = half ? bf16_to_f32(static_cast<const uint16_t*>(row)[e + u]) : static_cast<const float*>(row)[e + u];
   }
-  // Keys in the order of c.
+}
+
+// exp(x - top) in 64 bits; 0 for -infinity (a token without a logit above it has no scores).
+__device__ __forceinline__ double route_exp(float x, float top) {
+  return x == -__builtin_inff() ? 0.0 : exp((double)x - (double)top);
+}
+
+template <int U>
+__device__ __forceinline__ double route_total(const float (&l)[U], float top) {
+  double total = 0.0;
+#pragma unroll
+  for (int u = 0; u < U; ++u) total += route_exp(l[u], top);
+  return wave_sum(total);
+}
+
+// Groups whose rank, by `mine` of lane g, is below top_groups.
+template <class T>
+__device__ __forceinline__ uint64_t open_groups(const RouteArgs& a, T mine, T (*read)(T, int)) {
+  const int lane = threadIdx.x & 63;
+  int before = 0;
+  for (int g = 0; g < a.groups; ++g) {
+    const T other = read(mine, g);
+    before += other > mine || (other == mine && g < lane);
+  }
+  return __ballot(lane < a.groups && before < a.top_groups);
+}
+
+// The whole choice in 64 bits: lane j's pick.  By k rounds: the largest key of the
+// wave, then the lowest expert that has it.
+template <int U>
+__device__ __forceinline__ int route_exact(const RouteArgs& a, const float (&l)[U], float top, RouteLds<U>& lds) {
+  const int lane = threadIdx.x & 63;
   uint64_t key[U];
   const bool by_logit = a.bias == nullptr && (a.groups == 1 || a.best == 1);
+  const double total = by_logit || a.sigmoid ? 0.0 : route_total(l, top);
 #pragma unroll
   for (int u = 0; u < U; ++u) {
-    const int e = 64 * u + lane;
-    double c = by_logit ? (double)l[u] : s[u];
-    if (a.bias && e < a.e) c += (double)a.bias[e];
+    const int e = U * lane + u;
+    double c = (double)l[u];
+    if (!by_logit) {
+      if (a.sigmoid)
+        c = 1.0 / (1.0 + exp(-c));
+      else
+        c = total == 0.0 ? 0.0 : route_exp(l[u], top) / total;
+      if (a.bias && e < a.e) c += (double)a.bias[e];
+    }
     key[u] = e < a.e ? order64(c) : 0;
-    if (a.groups > 1) choice_s[wave][e] = c;
+    lds.choice[e] = c;
   }
   if (a.groups > 1) {
-    __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
-    __builtin_amdgcn_wave_barrier();
-    __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
+    wave_fence();
     const int per = a.e / a.groups;
     uint64_t mine = 0;
-    if (lane < a.groups) {           // lane g: the best one or two of group g
+    if (lane < a.groups) {             // lane g: the best one or two of group g
       uint64_t k1 = 0, k2 = 0;
       double c1 = 0.0, c2 = 0.0;
       for (int i = 0; i < per; ++i) {
-        const double c = choice_s[wave][lane * per + i];
+        const double c = lds.choice[lane * per + i];
         const uint64_t k = order64(c);
         if (k > k1) {
           k2 = k1, c2 = c1;
@@ -106,60 +180,289 @@ __global__ __launch_bounds__(256) void moe_route_top_kernel(RouteArgs a) {
       }
       mine = a.best == 1 ? k1 : order64(c1 + c2);
     }
-    int before = 0;
-    for (int g = 0; g < a.groups; ++g) {
-      const uint64_t other = (uint64_t)(uint32_t)__builtin_amdgcn_readlane((int)(mine >> 32), g) << 32 |
-                             (uint32_t)__builtin_amdgcn_readlane((int)mine, g);
-      before += other > mine || (other == mine && g < lane);
-    }
-    const uint64_t open = __ballot(lane < a.groups && before < a.top_groups);
+    const uint64_t open = open_groups<uint64_t>(a, mine, [](uint64_t v, int g) {
+      return (uint64_t)(uint32_t)__builtin_amdgcn_readlane((int)(v >> 32), g) << 32 |
+             (uint32_t)__builtin_amdgcn_readlane((int)v, g);
+    });
 #pragma unroll
     for (int u = 0; u < U; ++u)
-      if ((open >> ((64 * u + lane) / per & 63) & 1) == 0) key[u] = 0;
+      if ((open >> ((U * lane + u) / per & 63) & 1) == 0) key[u] = 0;
   }
-  // k rounds: the largest key of the wave, then the lowest expert that has it.
-  double w = 0.0;                    // lane j: the j-th pick's score
   int id = 0;
   for (int j = 0; j < a.k; ++j) {
     uint64_t m = key[0];
 #pragma unroll
     for (int u = 1; u < U; ++u) m = max(m, key[u]);
-    const uint32_t hi = wave_max32((uint32_t)(m >> 32));
-    const uint32_t lo = wave_max32((uint32_t)(m >> 32) == hi ? (uint32_t)m : 0u);
-    m = (uint64_t)hi << 32 | lo;
-    bool found = false;
 #pragma unroll
-    for (int u = 0; u < U; ++u) {
-      if (found) continue;           // uniform
-      const uint64_t has = __ballot(key[u] == m);
-      if (has == 0) continue;
-      found = true;
-      const int at = __builtin_ctzll(has);
-      if (lane == at) key[u] = 0;
-      const double v = __shfl(s[u], at);
-      if (lane == j) w = v, id = 64 * u + at;
+    for (int o = 1; o < 64; o *= 2) m = max(m, (uint64_t)__shfl_xor((unsigned long long)m, o));
+    int first = U;                     // of this lane's experts that have it
+#pragma unroll
+    for (int u = U - 1; u >= 0; --u)
+      if (key[u] == m) first = u;
+    const int at = __builtin_ctzll(__ballot(first < U));
+#pragma unroll
+    for (int u = 0; u < U; ++u)
+      if (lane == at && u == first) key[u] = 0;
+    const int e = U * at + __builtin_amdgcn_readlane(first, at);
+    if (lane == j) id = e;
+  }
+  return id;
+}
+
+template <int U>
+__device__ __forceinline__ int count_from(const float (&c)[U], float from) {
+  int n = 0;
+#pragma unroll
+  for (int u = 0; u < U; ++u) n += __popcll(__ballot(c[u] >= from));
+  return n;
+}
+
+// Bits of the mask below this lane, added to n.
+__device__ __forceinline__ int bits_below(uint64_t mask, int n) {
+  return __builtin_amdgcn_mbcnt_hi((uint32_t)(mask >> 32), __builtin_amdgcn_mbcnt_lo((uint32_t)mask, n));
+}
+
+// A token's picks in order, `to`[0 .. k - 1], by a wave.
+template <int U>
+__device__ __forceinline__ void route_token(const RouteArgs& a, const float (&l)[U], const float (&b)[U], float top,
+                                            RouteLds<U>& lds, int* id_to, float* x_to) {
+  const int lane = threadIdx.x & 63;
+  // c as binary32, off by at most `most` 2^-19 + |c| 2^-22 (route_off): exponentials and
+  // reciprocals by 2^-21 of themselves with what the rounding of a logit's distance x
+  // to the largest adds (x e^-x < 0.4 of 2^-23), the sum and the quotient by
+  // 2^-21, the addition by 2^-24 of c.
+  const bool exact = a.bias == nullptr && (a.groups == 1 || a.best == 1);
+  float c[U];
+  float most = 1.0f;                   // the largest score, at most
+#pragma unroll
+  for (int u = 0; u < U; ++u) c[u] = l[u];
+  if (!exact) {
+    constexpr float kLog2e = 1.44269504088896340736f;
+    if (a.sigmoid) {
+#pragma unroll
+      for (int u = 0; u < U; ++u)
+        c[u] = b[u] + __builtin_amdgcn_rcpf(1.0f + __builtin_amdgcn_exp2f(-kLog2e * l[u]));
+    } else {
+      float total = 0.0f;
+#pragma unroll
+      for (int u = 0; u < U; ++u) {
+        c[u] = l[u] == -__builtin_inff() ? 0.0f : __builtin_amdgcn_exp2f(kLog2e * (l[u] - top));
+        total += c[u];
+      }
+      total = wave_sum(total);
+      most = total == 0.0f ? 0.0f : __builtin_amdgcn_rcpf(total);
+#pragma unroll
+      for (int u = 0; u < U; ++u) c[u] = b[u] + c[u] * most;
     }
   }
-  if (a.renorm) {
-    const double total = wave_sum64(w);
-    w = total == 0.0 ? 0.0 : w / total;
+  auto off = [&](float v) { return __builtin_fmaf(fabsf(v), 0x1p-22f, most * 0x1p-19f); };
+  bool near = false;                   // numbers that 32 bits do not tell apart, or a NaN
+#pragma unroll
+  for (int u = 0; u < U; ++u) near |= c[u] != c[u] && U * lane + u < a.e;
+  // From here on a NaN is an expert that is not there: no comparison holds.
+#pragma unroll
+  for (int u = 0; u < U; ++u)
+    if (U * lane + u >= a.e) c[u] = __builtin_nanf("");
+
+  if (a.groups > 1) {
+    near |= a.lanes == 0;
+    const int lanes = max(a.lanes, 1);
+    float c1 = c[0], c2 = -__builtin_inff();   // the best two of this lane, then of the group
+#pragma unroll
+    for (int u = 1; u < U; ++u) {
+      c2 = fmaxf(fminf(c1, c[u]), c2);
+      c1 = fmaxf(c1, c[u]);
+    }
+    best_two<1>(lanes, c1, c2);
+    best_two<2>(lanes, c1, c2);
+    best_two<4>(lanes, c1, c2);
+    best_two<8>(lanes, c1, c2);
+    best_two<16>(lanes, c1, c2);
+    best_two<32>(lanes, c1, c2);
+    const float value = a.best == 1 ? c1 : c1 + c2;
+    const int own = lane >> a.shift, first = lane & (lanes - 1);
+    const float far = 2.0f * (off(c1) + off(a.best == 1 ? c1 : c2));
+    float n = 0.0f;                    // groups before this one
+    // A group's lanes compare it with one other group each, in turn.
+    for (int g0 = 0; g0 < a.groups; g0 += lanes) {
+      const int g = g0 + first;
+      const float other = __shfl(value, min(g, a.groups - 1) << a.shift);
+      const bool is = g < a.groups && own < a.groups && g != own;
+      n += is && (other > value || (other == value && g < own)) ? 1.0f : 0.0f;
+      // (a pair is looked at from both sides: the larger of the two bounds counts)
+      if (!exact) near |= is && !(fabsf(other - value) > far);
+    }
+    if (lanes > 1) n += other_block<1>(n);
+    if (lanes > 2) n += other_block<2>(n);
+    if (lanes > 4) n += other_block<4>(n);
+    if (lanes > 8) n += other_block<8>(n);
+    if (lanes > 16) n += other_block<16>(n);
+    if (lanes > 32) n += other_block<32>(n);
+    if (n >= (float)a.top_groups)
+#pragma unroll
+      for (int u = 0; u < U; ++u) c[u] = __builtin_nanf("");
   }
-  if (lane < a.k) {
-    a.ids[t * a.k + lane] = id;
-    a.weights[t * a.k + lane] = (float)((double)a.scale * w);
+
+  bool sure = __ballot(near) == 0;
+  if (sure) {
+    float high = c[0];
+#pragma unroll
+    for (int u = 1; u < U; ++u) high = fmaxf(high, c[u]);
+    high = wave_max(high);
+    // From the largest down in strides until k are reached, then by halves: k or more
+    // from `lo` on, fewer from `hi` on.
+    const uint32_t least = step_of(-__builtin_inff());
+    uint32_t hi = step_of(high) + 1u, lo = hi;
+    int n = 0;
+    for (uint32_t d = 1u << 21; n < a.k; d <<= 2) {
+      hi = lo;
+      lo = lo - least > d && d != 0u ? lo - d : least;
+      n = count_from(c, step_to(lo));
+      if (lo == least) break;
+    }
+    while (n != a.k && hi - lo > 1u) {
+      const uint32_t mid = lo + (hi - lo) / 2;
+      const int m = count_from(c, step_to(mid));
+      if (m >= a.k)
+        lo = mid, n = m;
+      else
+        hi = mid;
+    }
+    const float from = step_to(lo);
+    bool mine[U];
+#pragma unroll
+    for (int u = 0; u < U; ++u) mine[u] = c[u] >= from;
+    if (n != a.k) {                    // several that are equal: of those the lowest, as many as are left
+      int left = a.k, before = 0;
+#pragma unroll
+      for (int u = 0; u < U; ++u) left -= __popcll(__ballot(c[u] > from));
+#pragma unroll
+      for (int u = 0; u < U; ++u) before = bits_below(__ballot(c[u] == from), before);
+#pragma unroll
+      for (int u = 0; u < U; ++u)
+        if (c[u] == from) mine[u] = before++ < left;
+    }
+    int place = 0;                     // among the picks, in order of experts
+#pragma unroll
+    for (int u = 0; u < U; ++u) place = bits_below(__ballot(mine[u]), place);
+#pragma unroll
+    for (int u = 0; u < U; ++u)
+      if (mine[u]) lds.by_expert[place++] = Pick{c[u], l[u], U * lane + u, 0};
+    wave_fence();
+    // Every pick against every other: 64 / `room` lanes a pick, one other each in turn.
+    const int room = a.k <= 8 ? 8 : a.k <= 16 ? 16 : 32, turn = 64 / room, at = lane / turn;
+    const Pick p = lds.by_expert[at];
+    const float far = 2.0f * off(p.c);
+    float rank = 0.0f;
+    for (int j = lane & (turn - 1); j < room; j += turn) {
+      const float other = lds.by_expert[j].c;
+      const bool is = j < a.k && at < a.k && j != at;
+      rank += is && (other > p.c || (other == p.c && j < at)) ? 1.0f : 0.0f;
+      if (!exact) near |= is && !(fabsf(other - p.c) > far);
+    }
+    rank += other_block<1>(rank);
+    if (turn > 2) rank += other_block<2>(rank);
+    if (turn > 4) rank += other_block<4>(rank);
+    if (!exact) {                      // and the last pick against the first that is none
+      const uint64_t last = __ballot(at < a.k && rank == (float)(a.k - 1));
+      const float v = lane_of(p.c, last != 0 ? __builtin_ctzll(last) : 0);
+      near |= count_from(c, __builtin_fmaf(-2.5f, off(v), v)) != a.k;
+      sure = __ballot(near) == 0;
+    }
+    if (sure && at < a.k && (lane & (turn - 1)) == 0) id_to[(int)rank] = p.id, x_to[(int)rank] = p.x;
+  }
+  if (!sure) {
+    wave_fence();
+    const int id = route_exact(a, l, top, lds);
+    if (lane >= a.k) return;
+    id_to[lane] = id;
+    // out of the registers of the lane that has it, by way of LDS, would take longer
+    const size_t at = (size_t)((int64_t)blockIdx.x * kRouteTokens + wave_id_uniform()) * a.e + id;
+    x_to[lane] = a.half ? bf16_to_f32(static_cast<const uint16_t*>(a.logits)[at]) : static_cast<const float*>(a.logits)[at];
   }
 }
 
-hipError_t launch_moe_route(const RouteArgs& a, hipStream_t stream) {
-  const dim3 grid((uint32_t)((a.t + 3) / 4));
-  if (a.e <= 64)
-    hipLaunchKernelGGL((moe_route_top_kernel<1>), grid, dim3(256), 0, stream, a);
-  else if (a.e <= 128)
-    hipLaunchKernelGGL((moe_route_top_kernel<2>), grid, dim3(256), 0, stream, a);
-  else if (a.e <= 256)
-    hipLaunchKernelGGL((moe_route_top_kernel<4>), grid, dim3(256), 0, stream, a);
+template <int U>   // experts a lane
+__global__ __launch_bounds__(64 * kRouteTokens) void moe_route_top_kernel(RouteArgs a) {
+  __shared__ RouteLds<U> lds_s[kRouteTokens];
+  __shared__ int id_s[kRouteTokens][32];
+  __shared__ float x_s[kRouteTokens][32], top_s[kRouteTokens];
+  __shared__ double total_s[kRouteTokens];
+  const int lane = threadIdx.x & 63, wave = wave_id_uniform();
+  const int64_t t0 = (int64_t)blockIdx.x * kRouteTokens, t = t0 + wave;
+  const int tokens = (int)min((int64_t)kRouteTokens, a.t - t0);
+  if (wave < tokens) {
+    float l[U], b[U];
+    const size_t row = (size_t)t * a.e;
+    load_row<U>(l, a.half ? (const void*)(static_cast<const uint16_t*>(a.logits) + row)
+                          : (const void*)(static_cast<const float*>(a.logits) + row),
+                a.half, a.whole, a.e, -__builtin_inff());
+    if (a.bias)
+      load_row<U>(b, a.bias, false, a.whole, a.e, 0.0f);
+    else
+#pragma unroll
+      for (int u = 0; u < U; ++u) b[u] = 0.0f;
+    float top = 0.0f;
+    if (!a.sigmoid) {
+      top = l[0];
+#pragma unroll
+      for (int u = 1; u < U; ++u) top = fmaxf(top, l[u]);
+      top = wave_max(top);
+      if (lane == 0) top_s[wave] = top;
+      if (!a.renorm) {
+        const double total = route_total(l, top);
+        if (lane == 0) total_s[wave] = total;
+      }
+    }
+    route_token<U>(a, l, b, top, lds_s[wave], id_s[wave], x_s[wave]);
+  }
+  __syncthreads();
+  // Weights: `room` lanes a token, a pick each.
+  const int room = a.k <= 8 ? 8 : a.k <= 16 ? 16 : 32;
+  const int mine = threadIdx.x / room, j = threadIdx.x & (room - 1);
+  if (wave * 64 >= tokens * room) return;
+  const bool on = mine < tokens && j < a.k;
+  const int from = on ? mine : 0, pick = on ? j : 0;
+  const double x = (double)x_s[from][pick];
+  double w;
+  if (a.sigmoid)
+    w = 1.0 / (1.0 + exp(-x));
   else
-    hipLaunchKernelGGL((moe_route_top_kernel<8>), grid, dim3(256), 0, stream, a);
+    w = route_exp((float)x, top_s[from]);
+  double total = 1.0;
+  if (a.renorm) {
+    total = on ? w : 0.0;
+    total += __shfl_xor(total, 1);
+    total += __shfl_xor(total, 2);
+    total += __shfl_xor(total, 4);
+    if (room > 8) total += __shfl_xor(total, 8);
+    if (room > 16) total += __shfl_xor(total, 16);
+  } else if (!a.sigmoid) {
+    total = total_s[from];
+  }
+  w = total == 0.0 ? 0.0 : w / total;
+  if (!on) return;
+  a.ids[(t0 + mine) * a.k + j] = id_s[from][pick];
+  a.weights[(t0 + mine) * a.k + j] = (float)((double)a.scale * w);
+}
+
+hipError_t launch_moe_route(RouteArgs a, hipStream_t stream) {
+  const int u = a.e <= 64 ? 1 : a.e <= 128 ? 2 : a.e <= 256 ? 4 : 8;
+  auto on = [](const void* p, int n) { return ((uintptr_t)p & (uintptr_t)(n - 1)) == 0; };
+  // The fast way takes groups of whole lanes, a power of two of them.
+  const int per = a.e / a.groups, lanes = per / u;
+  a.lanes = per % u == 0 && (lanes & (lanes - 1)) == 0 ? lanes : 0;
+  for (a.shift = 0; 1 << a.shift < a.lanes;) ++a.shift;
+  a.whole = a.e % u == 0 && on(a.logits, a.half ? 2 * u : u < 4 ? 4 * u : 16) && on(a.bias, u < 4 ? 4 * u : 16);
+  const dim3 grid((uint32_t)((a.t + kRouteTokens - 1) / kRouteTokens));
+  if (a.e <= 64)
+    hipLaunchKernelGGL((moe_route_top_kernel<1>), grid, dim3(64 * kRouteTokens), 0, stream, a);
+  else if (a.e <= 128)
+    hipLaunchKernelGGL((moe_route_top_kernel<2>), grid, dim3(64 * kRouteTokens), 0, stream, a);
+  else if (a.e <= 256)
+    hipLaunchKernelGGL((moe_route_top_kernel<4>), grid, dim3(64 * kRouteTokens), 0, stream, a);
+  else
+    hipLaunchKernelGGL((moe_route_top_kernel<8>), grid, dim3(64 * kRouteTokens), 0, stream, a);
   return hipGetLastError();
 }
 

@@ -576,13 +576,6 @@ __global__ __launch_bounds__(1024) __attribute__((amdgpu_waves_per_eu(8))) void 
     static_cast<uint16_t*>(a.y)[at] = (uint16_t)f32_to_bf16_rne(y);
 }
 
-// A barrier for LDS alone: loads from memory stay in flight across it.
-__device__ __forceinline__ void lds_barrier() {
-  __builtin_amdgcn_fence(__ATOMIC_RELEASE, "workgroup", "local");
-  __builtin_amdgcn_s_barrier();
-  __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "workgroup", "local");
-}
-
 struct MoeTile {                  // one 256-k tile of a wave's 16 rows: lane (i, a)
   u32x4_t c0, c1;                 // chunks of groups a and 4 + a, row 16t + i
   u32x4_t sc;                     // the row's 8 scales

@@ -44,7 +44,7 @@ __device__ __forceinline__ float row_reduce(float v, float* red) {
   }
   if constexpr (T > 64) {
     if ((threadIdx.x & 63) == 0) red[threadIdx.x >> 6] = v;
-    __syncthreads();
+    lds_barrier();
     v = red[0];
 #pragma unroll
     for (int w = 1; w < T / 64; ++w) v = MAX ? nmax(v, red[w]) : v + red[w];

@@ -8,18 +8,22 @@
 // whole sum.  So the tokens are distributed as if the target alone had drawn them.
 //
 // Sums are in 64 bits: a vocabulary's running sums in 32 would move a border
-// between tokens by a ten-thousandth of a likely token's share.
+// between tokens by a ten-thousandth of a likely token's share.  Where running
+// sums decide, they are sums of whole numbers (a share of 2^61): exact in any
+// order, so a token without a share is never drawn.
 //
-// Two launches over the one row that counts:
-//   sums  every workgroup finds the sequence's first rejected draft (a few loads)
-//         and adds up its 2048 or more tokens of that row; both the sum of
-//         max(p - q, 0) and that of p, which stands in where the first is zero
-//   draw  finds the part that holds the border, and the token in it
+// Only the one row that counts is read, but for a few values.  It falls into pieces of
+// 512 tokens or more, a wave's work: their sums first, then the piece with the
+// border in it, read again.
 #include "layer_common.h"
+#include "w4_common.h"
+#include "wave.h"
 
 namespace qg {
 
-constexpr int kVerifyThreads = 256;
+constexpr int kPiece = 512;            // tokens, 8 a lane
+constexpr int kMaxPieces = 1024;       // a row's; longer pieces where it has more
+constexpr int kVerifyOnePieces = 256;   // those whose sums one workgroup keeps in LDS
 
 template <bool HALF>
 __device__ __forceinline__ float prob(const void* p, size_t at) {
@@ -27,236 +31,356 @@ __device__ __forceinline__ float prob(const void* p, size_t at) {
   return static_cast<const float*>(p)[at];
 }
 
-struct Row {                         // where the next token of a sequence comes from
-  int64_t first, drafts;             // rows of the target: first .. first + drafts
+struct VerifyRow {                     // where the next token of a sequence comes from
+  int64_t first, drafts;               // rows of the target: first .. first + drafts
   int accepted;
-  int64_t p, q;                      // row of the target; of the draft, or -1
-  int without;                       // the rejected token where drafts have no probabilities, or -1
-  bool bad;                          // a drafted token outside the vocabulary
+  size_t p, q;                         // first element of the target's row, and of the draft's
+  bool two;                            // there is a draft's row
+  int without;                         // the rejected token where drafts are certain, or -1
+  bool bad;                            // a drafted token outside the vocabulary
 };
 
-// Rows of sequence b, clipped to what there is.
-__device__ __forceinline__ void verify_rows(const VerifyArgs& a, int b, int64_t& first, int64_t& drafts) {
-  first = a.cu[b];
+// Rows of sequence b; false where its offsets are not in order.
+__device__ __forceinline__ bool verify_rows(const VerifyArgs& a, int b, VerifyRow& r) {
+  r.bad = false;
+  r.first = a.cu[b];
   int64_t end = a.cu[b + 1];
-  first = first < 0 ? 0 : first;
+  r.first = r.first < 0 ? 0 : r.first;
   end = end > a.rows ? a.rows : end;
-  drafts = end - first - 1;          // -1: a sequence without a row
-  if (first - b < 0 || first - b + drafts > a.rows - a.b) drafts = -1;   // offsets that are not in order
+  r.drafts = end - r.first - 1;
+  return r.drafts >= 0 && r.first - b >= 0 && r.first - b + r.drafts <= a.rows - a.b;
 }
 
-// The row of the first rejected draft, or the one after the last; by whole waves.
-template <bool HALF>
-__device__ __forceinline__ void verify_at(const VerifyArgs& a, int b, int accepted, Row& r) {
+// The row behind `accepted` drafts.
+__device__ __forceinline__ void verify_at(const VerifyArgs& a, int b, int accepted, VerifyRow& r) {
   r.accepted = accepted;
-  r.p = r.first + accepted;
-  r.q = -1;
-  r.without = -1;
-  if (accepted < r.drafts) {
-    const int64_t d = r.first - b + accepted;
-    if (a.draft)
-      r.q = d;
-    else
-      r.without = a.tokens[d];
-  }
+  const int64_t d = r.first - b + accepted;
+  r.p = (size_t)(r.first + accepted) * a.v;
+  r.q = (size_t)d * a.v;
+  r.two = accepted < r.drafts && a.draft != nullptr;
+  r.without = accepted < r.drafts && !a.draft ? __builtin_amdgcn_readfirstlane(a.tokens[d]) : -1;
 }
 
+// The first rejected draft of sequence b, by a whole wave.
 template <bool HALF>
-__device__ __forceinline__ int verify_accepted(const VerifyArgs& a, int b, int64_t first, int64_t drafts, bool& bad) {
+__device__ __forceinline__ void verify_find(const VerifyArgs& a, int b, VerifyRow& r) {
   const int lane = threadIdx.x & 63;
-  bad = false;
-  for (int64_t i0 = 0; i0 < drafts; i0 += 64) {
-    const int64_t i = i0 + lane, d = first - b + i;
-    bool ok = i >= drafts, out = false;
-    if (i < drafts) {
+  int64_t accepted = r.drafts;
+  for (int64_t i0 = 0; i0 < r.drafts; i0 += 64) {
+    const int64_t i = i0 + lane, d = r.first - b + i;
+    bool ok = true, out = false;
+    if (i < r.drafts) {
       const int x = a.tokens[d];
+      const double u = (double)a.u[d];
       out = x < 0 || x >= a.v;
+      ok = false;
       if (!out) {
-        const double p = (double)prob<HALF>(a.target, (size_t)(first + i) * a.v + x);
+        const double p = (double)prob<HALF>(a.target, (size_t)(r.first + i) * a.v + x);
         const double q = a.draft ? (double)prob<HALF>(a.draft, (size_t)d * a.v + x) : 1.0;
-        ok = (double)a.u[d] * q < p;
+        ok = u * q < p;
       }
     }
     const uint64_t no = __ballot(!ok);
-    const int at = no ? __builtin_ctzll(no) : 64;
-    bad = (__ballot(out) & (at < 64 ? ((uint64_t)2 << at) - 1 : ~(uint64_t)0)) != 0;
-    if (no) return (int)(i0 + at);
+    if (no != 0) {
+      const int at = __builtin_ctzll(no);
+      r.bad = (__ballot(out) >> at & 1) != 0;
+      accepted = i0 + at;
+      break;
+    }
   }
-  return (int)(drafts < 0 ? 0 : drafts);
+  verify_at(a, b, __builtin_amdgcn_readfirstlane((int)accepted), r);
 }
 
-// What token j weighs: max(p - q, 0), where a NaN counts as 0; and max(p, 0).
-template <bool HALF>
-__device__ __forceinline__ void verify_weight(const VerifyArgs& a, const Row& r, int64_t j, double& left, double& whole) {
-  const double p = (double)prob<HALF>(a.target, (size_t)r.p * a.v + j);
-  const double q = r.q >= 0 ? (double)prob<HALF>(a.draft, (size_t)r.q * a.v + j) : 0.0;
-  whole = fmax(p, 0.0);
-  left = j == r.without ? 0.0 : fmax(p - q, 0.0);
+// What a token weighs: max(p - q, 0); a NaN counts as 0.
+__device__ __forceinline__ double verify_left(float p, float q) {
+  return fmax((double)p - (double)q, 0.0);
 }
 
-__device__ __forceinline__ double wave_add(double v) {
+// Eight tokens a lane of the 512 from j0 on: in order (lane l: 8 l ..) or, for
+// sums, as they are read best.  Tokens from v on weigh nothing (they are past the
+// end of the view), nor does the one that was rejected where drafts are certain.
+template <bool HALF, bool ORDER>
+__device__ __forceinline__ void verify_load(const VerifyArgs& a, const VerifyRow& r, int64_t j0, float (&p)[8], float (&q)[8]) {
+  constexpr int kSize = HALF ? 2 : 4;
+  const int lane = threadIdx.x & 63;
+  const int bytes = (int)min((int64_t)kPiece, a.v - j0) * kSize;
+  const BufView pv(static_cast<const char*>(a.target) + (r.p + j0) * kSize, bytes);
+  const BufView qv(static_cast<const char*>(r.two ? a.draft : a.target) + (r.two ? (r.q + j0) * kSize : 0), r.two ? bytes : 0);
+  const bool order = ORDER || a.whole;
+  if (a.whole) {                         // rows start on 16 bytes and end so: 16 bytes are all there or not
+    if constexpr (HALF) {
+      const u32x4_t w = pv.b128<false>(16 * lane), x = qv.b128<false>(16 * lane);
 #pragma unroll
-  for (int o = 1; o < 64; o *= 2) v += __shfl_xor(v, o);
-  return v;
-}
-
-template <bool HALF>
-__global__ __launch_bounds__(kVerifyThreads) void verify_sums_kernel(VerifyArgs a) {
-  __shared__ double red[2][4];
-  const int tid = threadIdx.x, b = blockIdx.y;
-  Row r;
-  verify_rows(a, b, r.first, r.drafts);
-  if (r.drafts < 0) return;          // the same for the whole workgroup
-  const int accepted = verify_accepted<HALF>(a, b, r.first, r.drafts, r.bad);
-  verify_at<HALF>(a, b, accepted, r);
-  double left = 0.0, whole = 0.0;
-  const int64_t j1 = min(a.v, (int64_t)(blockIdx.x + 1) * a.chunk);
-  for (int64_t j = (int64_t)blockIdx.x * a.chunk + tid; j < j1; j += kVerifyThreads) {
-    double l, w;
-    verify_weight<HALF>(a, r, j, l, w);
-    left += l;
-    whole += w;
+      for (int i = 0; i < 8; ++i) {
+        p[i] = __uint_as_float((i & 1) ? w[i >> 1] & 0xffff0000u : w[i >> 1] << 16);
+        q[i] = __uint_as_float((i & 1) ? x[i >> 1] & 0xffff0000u : x[i >> 1] << 16);
+      }
+    } else {
+      const u32x4_t w0 = pv.b128<false>(32 * lane), w1 = pv.b128<false>(32 * lane + 16);
+      const u32x4_t x0 = qv.b128<false>(32 * lane), x1 = qv.b128<false>(32 * lane + 16);
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        p[i] = __uint_as_float(i < 4 ? w0[i & 3] : w1[i & 3]);
+        q[i] = __uint_as_float(i < 4 ? x0[i & 3] : x1[i & 3]);
+      }
+    }
+  } else {                               // 64 neighbours at a time where the order is free
+    const uint32_t at = kSize * (ORDER ? 8 * lane : lane), step = kSize * (ORDER ? 1 : 64);
+    uint32_t w[8], x[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) w[i] = HALF ? pv.b16(at + i * step) << 16 : pv.b32(at + i * step);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) x[i] = HALF ? qv.b16(at + i * step) << 16 : qv.b32(at + i * step);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) p[i] = __uint_as_float(w[i]), q[i] = __uint_as_float(x[i]);
   }
-  left = wave_add(left);
-  whole = wave_add(whole);
-  if ((tid & 63) == 0) red[0][tid >> 6] = left, red[1][tid >> 6] = whole;
-  __syncthreads();
-  if (tid >= 2) return;
-  a.part[((size_t)b * a.chunks + blockIdx.x) * 2 + tid] = (red[tid][0] + red[tid][1]) + (red[tid][2] + red[tid][3]);
-  if (blockIdx.x == 0 && tid == 0) {
-    a.accepted[b] = accepted;
-    if (r.bad && a.status) atomicOr(a.status, QG_FLAG_INDEX);
+  if (r.without >= j0 && r.without < j0 + kPiece) {
+    const int not_it = (int)(r.without - j0);
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+      if ((order ? 8 * lane + i : 64 * i + lane) == not_it) p[i] = 0.0f;
   }
 }
 
+// The sum of a piece.
 template <bool HALF>
-__global__ __launch_bounds__(kVerifyThreads) void verify_draw_kernel(VerifyArgs a) {
-  __shared__ double base_s;
-  __shared__ int chunk_s, mode_s;
-  __shared__ uint64_t wave_s[4];
-  __shared__ int at_s[4];
-  const int tid = threadIdx.x, lane = tid & 63, wave = wave_id_uniform(), b = blockIdx.x;
-  Row r;
-  verify_rows(a, b, r.first, r.drafts);
-  if (r.drafts < 0) {                // nothing to verify, nothing to draw from
-    if (tid == 0) {
+__device__ __forceinline__ double verify_sum(const VerifyArgs& a, const VerifyRow& r, int64_t piece) {
+  double sum = 0.0;
+#pragma unroll 1
+  for (int64_t j0 = piece * a.piece; j0 < min(a.v, (piece + 1) * a.piece); j0 += kPiece) {
+    float p[8], q[8];
+    verify_load<HALF, false>(a, r, j0, p, q);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) sum += verify_left(p[i], q[i]);
+  }
+  return wave_sum(sum);
+}
+
+// x of a whole of which 2^e is a share of 2^61 or more; one at least.
+__device__ __forceinline__ uint64_t verify_count(double x, int e) {
+  return x > 0.0 ? max((uint64_t)1, (uint64_t)__builtin_amdgcn_ldexp(x, e)) : 0;
+}
+__device__ __forceinline__ uint64_t verify_border(double x, int e) {
+  const double y = __builtin_amdgcn_ldexp(x, e);
+  return y > 0.0 ? (y < 0x1p63 ? (uint64_t)y : (uint64_t)1 << 63) : 0;
+}
+
+// The token that u falls on, by a whole wave; part[i]: the sum of piece i.  -1 where
+// the row has no finite sum above zero.
+template <bool HALF>
+__device__ __forceinline__ int verify_draw(const VerifyArgs& a, VerifyRow& r, double u, double* part) {
+  const int lane = threadIdx.x & 63;
+  const int per = (a.pieces + 63) / 64, i0 = lane * per, i1 = min(a.pieces, i0 + per);
+  double own = 0.0;
+  for (int i = i0; i < i1; ++i) own += part[i];
+  double total = wave_sum(own);
+  if (total == 0.0 && (r.two || r.without >= 0)) {
+    // p nowhere above q: the token comes from p (rows that do not add up to one, or
+    // a draft rejected by rounding alone; so seldom that one wave may do it)
+    r.two = false;
+    r.without = -1;
+#pragma unroll 1
+    for (int i = 0; i < a.pieces; ++i) {
+      const double sum = verify_sum<HALF>(a, r, i);
+      if (i >= i0 && i < i1) part[i] = sum;
+    }
+    own = 0.0;
+    for (int i = i0; i < i1; ++i) own += part[i];
+    total = wave_sum(own);
+  }
+  const double border = u * total;
+  if (!(total > 0.0 && total < __builtin_inf())) return -1;
+  // the piece
+  int e = 62 - __builtin_amdgcn_frexp_exp(total);
+  uint64_t all, mine = 0;
+  int last = -1;
+  for (int i = i0; i < i1; ++i) {
+    const uint64_t c = verify_count(part[i], e);
+    mine += c;
+    if (c != 0) last = i;
+  }
+  constexpr uint64_t kLast = (uint64_t)1 << 63;   // u of 1 and more: the last token with a share
+  uint64_t want = u < 1.0 ? verify_border(border, e) : kLast;
+  uint64_t run = wave_before(mine, all);
+  int at = last;
+  double base = 0.0;                   // this lane's part of the sum before the piece
+  uint64_t hit;
+  if (want < all) {
+    const bool here = run <= want && want < run + mine;
+    hit = __ballot(here);
+    if (here) {
+      for (int i = i0; i < i1; ++i) {
+        run += verify_count(part[i], e);
+        at = i;
+        if (run > want) break;
+      }
+    }
+  } else {                             // by rounding, or kLast
+    const uint64_t some = __ballot(last >= 0);
+    hit = (uint64_t)1 << (63 - __builtin_clzll(some));
+  }
+  const int piece = __builtin_amdgcn_readlane(at, __builtin_ctzll(hit));
+  for (int i = i0; i < min(i1, piece); ++i) base += part[i];
+  const double rest = border - wave_sum(base);
+  // the token in it
+  e = 62 - __builtin_amdgcn_frexp_exp(part[piece]);
+  want = u < 1.0 ? verify_border(rest, e) : kLast;
+  uint64_t before = 0;
+  int token = -1;                      // this lane's last one with a share
+#pragma unroll 1
+  for (int64_t j0 = (int64_t)piece * a.piece; j0 < min(a.v, (int64_t)(piece + 1) * a.piece); j0 += kPiece) {
+    float p[8], q[8];
+    verify_load<HALF, true>(a, r, j0, p, q);
+    uint64_t c[8];
+    mine = 0;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      c[i] = verify_count(verify_left(p[i], q[i]), e);
+      mine += c[i];
+      if (c[i] != 0) token = (int)j0 + 8 * lane + i;
+    }
+    run = before + wave_before(mine, all);
+    const bool here = run <= want && want < run + mine;
+    hit = __ballot(here);
+    if (hit != 0) {
+      bool found = false;
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        run += c[i];
+        if (!found && run > want) token = (int)(j0 + 8 * lane + i), found = true;
+      }
+      return __builtin_amdgcn_readlane(token, __builtin_ctzll(hit));
+    }
+    before += all;
+  }
+  return (int)lane_of(wave_scan((uint32_t)(token + 1), 0u, [](uint32_t a, uint32_t b) { return max(a, b); }), 63) - 1;
+}
+
+__device__ __forceinline__ void verify_flag(const VerifyArgs& a, uint32_t flags) {
+  if (flags != 0 && a.status) atomicOr(a.status, flags);
+}
+
+__device__ __forceinline__ void verify_store(const VerifyArgs& a, int b, const VerifyRow& r, int token) {
+  a.next[b] = token;
+  if (a.lens) a.lens[b] -= (int)(r.drafts - r.accepted);
+  if (token < 0) verify_flag(a, QG_FLAG_NONFINITE);
+}
+
+// A workgroup a sequence.
+template <bool HALF>
+__global__ __launch_bounds__(1024) void verify_one_kernel(VerifyArgs a) {
+  __shared__ double part[kVerifyOnePieces];
+  const int wave = wave_id_uniform(), b = blockIdx.x;
+  const float u = a.u_next[b];
+  VerifyRow r;
+  if (!verify_rows(a, b, r)) {           // the same in all waves
+    if (threadIdx.x == 0) {              // nothing to verify, nothing to draw from
       a.accepted[b] = 0;
       a.next[b] = -1;
-      if (a.status) atomicOr(a.status, QG_FLAG_INDEX);
+      verify_flag(a, QG_FLAG_INDEX);
     }
     return;
   }
-  const int accepted = a.accepted[b];
-  verify_at<HALF>(a, b, accepted, r);
-  const double* const part = a.part + (size_t)b * a.chunks * 2;
-  const double u = (double)a.u_next[b];
-  if (tid == 0) {
-    // One after another: the running sums never fall, so the part that the border is in has a sum above zero.
-    int mode = 0;
-    double total = 0.0;
-    for (int s = 0; s < a.chunks; ++s) total += part[2 * s];
-    if (total == 0.0) {
-      mode = 1;
-      for (int s = 0; s < a.chunks; ++s) total += part[2 * s + 1];
-    }
-    int chunk = -1;
-    double base = 0.0, border = 0.0;
-    if (total > 0.0 && total < __builtin_inf()) {
-      border = u * total;
-      double sum = 0.0;
-      for (int s = 0; s < a.chunks; ++s) {
-        const double x = part[2 * s + mode];
-        if (x > 0.0) {               // the last one stays where u is 1 or more
-          chunk = s;
-          base = sum;
-          if (sum + x > border) break;
-        }
-        sum += x;
-      }
-    }
-    chunk_s = chunk;
-    mode_s = mode;
-    base_s = border - base;
+  verify_find<HALF>(a, b, r);
+#pragma unroll 1
+  for (int i = wave; i < a.pieces; i += 16) {
+    const double sum = verify_sum<HALF>(a, r, i);
+    if ((threadIdx.x & 63) == 0) part[i] = sum;
   }
   __syncthreads();
-  const int chunk = chunk_s;
-  if (a.lens && tid == 0) a.lens[b] -= (int)(r.drafts - accepted);
-  if (chunk < 0) {
-    if (tid == 0) {
+  if (wave != 0) return;
+  const int token = verify_draw<HALF>(a, r, (double)u, part);
+  if (threadIdx.x != 0) return;
+  a.accepted[b] = r.accepted;
+  if (r.bad) verify_flag(a, QG_FLAG_INDEX);
+  verify_store(a, b, r, token);
+}
+
+// Many workgroups a sequence, a piece or a few each wave; then a wave a sequence.
+template <bool HALF>
+__global__ __launch_bounds__(256) void verify_sums_kernel(VerifyArgs a) {
+  const int b = blockIdx.y;
+  const bool first = blockIdx.x == 0 && threadIdx.x == 0;
+  VerifyRow r;
+  if (!verify_rows(a, b, r)) {
+    if (first) a.accepted[b] = 0;
+    return;
+  }
+  verify_find<HALF>(a, b, r);
+  if (first) {
+    a.accepted[b] = r.accepted;
+    if (r.bad) verify_flag(a, QG_FLAG_INDEX);
+  }
+  const int step = gridDim.x * 4;
+#pragma unroll 1
+  for (int i = blockIdx.x * 4 + wave_id_uniform(); i < a.pieces; i += step) {
+    const double sum = verify_sum<HALF>(a, r, i);
+    if ((threadIdx.x & 63) == 0) a.part[(size_t)b * a.pieces + i] = sum;
+  }
+}
+
+template <bool HALF>
+__global__ __launch_bounds__(64) void verify_draw_kernel(VerifyArgs a) {
+  const int b = blockIdx.x;
+  const int accepted = __builtin_amdgcn_readfirstlane(a.accepted[b]);   // of the launch before, as the sums
+  const float u = a.u_next[b];
+  VerifyRow r;
+  if (!verify_rows(a, b, r)) {
+    if (threadIdx.x == 0) {
       a.next[b] = -1;
-      if (a.status) atomicOr(a.status, QG_FLAG_NONFINITE);
+      verify_flag(a, QG_FLAG_INDEX);
     }
     return;
   }
-  // Within the part, sums of whole numbers: exact, in any order.  A token counts
-  // 2^61 times its share of the part, and at least one.
-  const int mode = mode_s;
-  const double all = part[2 * chunk + mode];
-  const int e = 61 - ilogb(all);
-  const double rest = ldexp(base_s, e);
-  const uint64_t border = rest > 0.0 ? (rest < 0x1p63 ? (uint64_t)rest : (uint64_t)1 << 63) : 0;
-  const int64_t j0 = (int64_t)chunk * a.chunk, j1 = min(a.v, j0 + a.chunk);
-  const int per = (int)((a.chunk + kVerifyThreads - 1) / kVerifyThreads);
-  auto count = [&](int64_t j) -> uint64_t {
-    double l, w;
-    verify_weight<HALF>(a, r, j, l, w);
-    const double x = mode ? w : l;
-    return x > 0.0 ? max((uint64_t)1, (uint64_t)ldexp(x, e)) : 0;
-  };
-  uint64_t mine = 0;
-  int64_t last = -1;                 // this thread's last token with a share
-  const int64_t t0 = j0 + (int64_t)tid * per, t1 = min(j1, t0 + per);
-  for (int64_t j = t0; j < t1; ++j) {
-    const uint64_t c = count(j);
-    mine += c;
-    if (c) last = j;
-  }
-  uint64_t sum = mine;               // running over the threads
-#pragma unroll
-  for (int o = 1; o < 64; o *= 2) {
-    const uint64_t v = __shfl_up(sum, o);
-    if (lane >= o) sum += v;
-  }
-  if (lane == 63) wave_s[wave] = sum;
-  const uint64_t some = __ballot(last >= 0);
-  if (lane == 0) at_s[wave] = some ? 64 * wave + 63 - __builtin_clzll(some) : -1;
-  __syncthreads();
-  for (int w = 0; w < wave; ++w) sum += wave_s[w];
-  const uint64_t before = sum - mine;
-  const uint64_t end = wave_s[0] + wave_s[1] + wave_s[2] + wave_s[3];
-  if (border >= end) {               // by rounding, or u of 1 and more: the last token with a share
-    const int t = max(max(at_s[0], at_s[1]), max(at_s[2], at_s[3]));
-    if (tid == t) a.next[b] = (int)last;
-  } else if (before <= border && border < sum) {
-    uint64_t run = before;
-    for (int64_t j = t0; j < t1; ++j) {
-      run += count(j);
-      if (run > border) {
-        a.next[b] = (int)j;
-        break;
-      }
-    }
-  }
+  verify_at(a, b, accepted, r);
+  const int token = verify_draw<HALF>(a, r, (double)u, a.part + (size_t)b * a.pieces);
+  if (threadIdx.x == 0) verify_store(a, b, r, token);
 }
 
-// Tokens a workgroup adds up: 2048, more where a row would have over 128 parts.
-int verify_chunk(int64_t v) {
-  int64_t c = 2048;
-  while ((v + c - 1) / c > 128) c *= 2;
-  return (int)c;
+int64_t verify_piece(int64_t v) {
+  int64_t c = kPiece;
+  while ((v + c - 1) / c > kMaxPieces) c *= 2;
+  return c;
 }
 
-hipError_t launch_verify_drafts(const VerifyArgs& a, hipStream_t stream) {
+// Whether one workgroup a sequence does it all.
+bool verify_in_one(int64_t b, int64_t v) {
+  // Few tokens, or sequences for every second CU (one of 32000, 7.4 us against 6.7 and a second launch;
+  // 61 of 32768 in bf16, 8.8 against 7.8 and a launch; 64 of 131071, 25 against 18).
+  if ((v + kPiece - 1) / kPiece > kVerifyOnePieces) return false;
+  return v <= 40000 || b >= kCUs / 2;
+}
+
+int64_t verify_ws_bytes(int64_t b, int64_t v) {
+  const int64_t c = verify_piece(v);
+  return verify_in_one(b, v) ? 0 : b * ((v + c - 1) / c) * 8;
+}
+
+hipError_t launch_verify_drafts(VerifyArgs a, hipStream_t stream) {
+  a.piece = verify_piece(a.v);
+  a.pieces = (int)((a.v + a.piece - 1) / a.piece);
+  auto on16 = [](const void* p) { return ((uintptr_t)p & 15) == 0; };
+  a.whole = a.v % (a.half ? 8 : 4) == 0 && on16(a.target) && on16(a.draft);
+  if (verify_in_one(a.b, a.v)) {
+    if (a.half)
+      hipLaunchKernelGGL((verify_one_kernel<true>), dim3(a.b), dim3(1024), 0, stream, a);
+    else
+      hipLaunchKernelGGL((verify_one_kernel<false>), dim3(a.b), dim3(1024), 0, stream, a);
+    return hipGetLastError();
+  }
+  const int64_t waves = (int64_t)a.b * a.pieces / (16 * kCUs);   // pieces a wave, 16 waves a CU
+  const int per = (int)(waves < 1 ? 1 : waves > 4 ? 4 : waves);
+  const dim3 grid((a.pieces + 4 * per - 1) / (4 * per), a.b);
   if (a.half)
-    hipLaunchKernelGGL((verify_sums_kernel<true>), dim3(a.chunks, a.b), dim3(kVerifyThreads), 0, stream, a);
+    hipLaunchKernelGGL((verify_sums_kernel<true>), grid, dim3(256), 0, stream, a);
   else
-    hipLaunchKernelGGL((verify_sums_kernel<false>), dim3(a.chunks, a.b), dim3(kVerifyThreads), 0, stream, a);
+    hipLaunchKernelGGL((verify_sums_kernel<false>), grid, dim3(256), 0, stream, a);
   const hipError_t st = hipGetLastError();
   if (st != hipSuccess) return st;
   if (a.half)
-    hipLaunchKernelGGL((verify_draw_kernel<true>), dim3(a.b), dim3(kVerifyThreads), 0, stream, a);
+    hipLaunchKernelGGL((verify_draw_kernel<true>), dim3(a.b), dim3(64), 0, stream, a);
   else
-    hipLaunchKernelGGL((verify_draw_kernel<false>), dim3(a.b), dim3(kVerifyThreads), 0, stream, a);
+    hipLaunchKernelGGL((verify_draw_kernel<false>), dim3(a.b), dim3(64), 0, stream, a);
   return hipGetLastError();
 }
 

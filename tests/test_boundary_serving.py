@@ -93,7 +93,7 @@ def test_route_refusals(kw, want):
 
 
 def verify(**kw):
-    a = dict(p=A, q=A, dt=1, rows=9, v=1000, tokens=A, u=A, u_next=A, cu=A, b=3, lens=None, acc=A, nxt=A, ws=A, ws_bytes=1 << 20, status=None, stream=None)
+    a = dict(p=A, q=A, dt=1, rows=9, v=131071, tokens=A, u=A, u_next=A, cu=A, b=3, lens=None, acc=A, nxt=A, ws=A, ws_bytes=1 << 20, status=None, stream=None)
     assert set(kw) <= set(a)
     return lib.qg_verify_drafts(*(a | kw).values())
 
@@ -101,7 +101,7 @@ def verify(**kw):
 @pytest.mark.parametrize("kw,want", [
     (dict(p=None), E_NULL), (dict(tokens=None), E_NULL), (dict(u=None), E_NULL), (dict(u_next=None), E_NULL), (dict(cu=None), E_NULL),
     (dict(acc=None), E_NULL), (dict(nxt=None), E_NULL), (dict(ws=None), E_NULL), (dict(b=-1), E_SHAPE), (dict(b=65536, rows=70000), E_SHAPE),
-    (dict(rows=2), E_SHAPE), (dict(rows=1 << 31), E_SHAPE), (dict(v=0), E_SHAPE), (dict(v=1 << 31), E_SHAPE), (dict(dt=2), E_DTYPE), (dict(ws_bytes=47), E_BUF),
+    (dict(rows=2), E_SHAPE), (dict(rows=1 << 31), E_SHAPE), (dict(v=0), E_SHAPE), (dict(v=1 << 31), E_SHAPE), (dict(dt=2), E_DTYPE), (dict(ws_bytes=3 * 256 * 8 - 1), E_BUF),
     (dict(p=A + 2), E_ALIGN), (dict(dt=0, q=A + 1), E_ALIGN), (dict(tokens=A + 2), E_ALIGN), (dict(u=A + 1), E_ALIGN), (dict(u_next=A + 2), E_ALIGN),
     (dict(cu=A + 2), E_ALIGN), (dict(lens=A + 2), E_ALIGN), (dict(acc=A + 2), E_ALIGN), (dict(nxt=A + 1), E_ALIGN), (dict(ws=U), E_ALIGN),
     (dict(status=A + 2), E_ALIGN), (dict(b=0), OK), (dict(b=0, rows=0, p=None, ws=None, cu=None), OK)])
@@ -110,9 +110,11 @@ def test_verify_refusals(kw, want):
 
 
 def test_verify_workspace():
-    assert qg.verify_drafts_workspace_bytes(9, 3, 1000) == 3 * 16
+    assert qg.verify_drafts_workspace_bytes(9, 3, 1000) == 0              # a workgroup a sequence keeps its sums
+    assert qg.verify_drafts_workspace_bytes(9, 3, 131071) == 3 * 256 * 8
     assert qg.verify_drafts_workspace_bytes(0, 0, 1000) == 0
-    assert 64 * 16 <= qg.verify_drafts_workspace_bytes(1, 1, 2 ** 31 - 1) <= 128 * 16
+    assert 512 * 8 < qg.verify_drafts_workspace_bytes(1, 1, 2 ** 31 - 1) <= 1024 * 8
+    assert verify(v=1000, ws=None, ws_bytes=0, p=None) == E_NULL
     with pytest.raises(qg.QGemmError):
         qg.verify_drafts_workspace_bytes(2, 3, 1000)
 
