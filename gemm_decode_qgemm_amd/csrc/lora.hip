@@ -7,10 +7,10 @@
 // (24 bits), which costs matrix instructions only, of which there are plenty.
 //
 // Two launches, as the second product needs all of the first:
-//   down  a workgroup owns 16 ranks of one adapter and a part of K; its four
-//         waves take 32 k in turn and are summed in LDS; partial sums in fp32
-//   up    a workgroup owns columns of one adapter's B; it adds the partial sums
-//         of the adapter's rows, then its waves take 16 columns at a time
+//   down  a workgroup owns 16 ranks of one adapter and a part of K; its waves take
+//         64 k in turn and are summed in LDS; partial sums in fp32
+//   up    a wave owns 64 columns of one adapter's B; it adds the partial sums of the
+//         adapter's rows itself
 // A unit is an adapter, or the rows' adapters where a batch has fewer rows than
 // there are adapters: then the first row that names an adapter works for all of
 // its rows, so that every adapter in use is read once.
@@ -26,8 +26,9 @@
 namespace qg {
 
 constexpr int kLoraRows = QG_MAX_M;
-constexpr int kLoraSplits = 16;        // of K, at most
-constexpr int kLoraStep = 1024;        // k of a workgroup whose loads are all in flight together
+constexpr int kLoraSplits = 4;         // parts of K, at most
+constexpr int kLoraWaves = 8;          // of a workgroup of the first product
+constexpr int kLoraStep = 256 * kLoraWaves;   // k of a workgroup whose loads are all in flight together
 
 // The rows of unit `unit` as a mask, or 0 where it has none (or another unit
 // works for them); `adapter` is theirs.
@@ -57,15 +58,15 @@ __device__ __forceinline__ void lora_down(const LoraArgs& a, int adapter, int co
 #pragma unroll
   for (int t = 0; t < MT; ++t) x[t] = a.x + (size_t)rows[min(16 * t + i, count - 1)] * a.k + 8 * q;
   f32x4_t acc[MT] = {};
-  constexpr int U = MT == 1 ? kLoraStep / 128 : MT == 2 ? 4 : 2;
-  for (int c = k0 + 32 * wave; c < k1; c += 128 * U) {
+  constexpr int U = 8 / MT;
+  for (int c = k0 + 64 * wave; c < k1; c += 32 * kLoraWaves * U) {   // whole 128-byte lines a wave
     u32x4_t wv[U], xv[U][MT];
 #pragma unroll
     for (int u = 0; u < U; ++u) {
       wv[u] = u32x4_t{0u, 0u, 0u, 0u};
 #pragma unroll
       for (int t = 0; t < MT; ++t) xv[u][t] = u32x4_t{0u, 0u, 0u, 0u};
-      const int at = c + 128 * u;
+      const int at = c + 64 * kLoraWaves * (u >> 1) + 32 * (u & 1);
       if (at + 8 * q < k1) {         // k is a multiple of 8
         wv[u] = *reinterpret_cast<const u32x4_t*>(w + at);
 #pragma unroll
@@ -87,14 +88,17 @@ __device__ __forceinline__ void lora_down(const LoraArgs& a, int adapter, int co
     for (int e = 0; e < 4; ++e) red[wave][4 * q + e][i] = acc[t][e];
     lds_barrier();
     const int m = threadIdx.x >> 4, r = threadIdx.x & 15;
-    if (16 * t + m < count && r0 + r < a.r)
-      a.part[((size_t)blockIdx.z * a.m + rows[16 * t + m]) * a.r + r0 + r] =
-          (red[0][m][r] + red[1][m][r]) + (red[2][m][r] + red[3][m][r]);
+    if (m < 16 && 16 * t + m < count && r0 + r < a.r) {
+      float v = 0.0f;
+#pragma unroll
+      for (int w = 0; w < kLoraWaves; w += 2) v += red[w][m][r] + red[w + 1][m][r];
+      a.part[((size_t)blockIdx.z * a.m + rows[16 * t + m]) * a.r + r0 + r] = v;
+    }
   }
 }
 
-__global__ __launch_bounds__(256) void lora_down_kernel(LoraArgs a) {
-  __shared__ float red[4][16][17];
+__global__ __launch_bounds__(64 * kLoraWaves) void lora_down_kernel(LoraArgs a) {
+  __shared__ float red[kLoraWaves][16][17];
   __shared__ int rows[kLoraRows];
   int adapter;
   const uint64_t mask = lora_rows(a, blockIdx.y, adapter);
@@ -170,10 +174,10 @@ struct LoraB {
 // 4 rows of y or out as views of their n columns.
 struct LoraRows {
   __amdgpu_buffer_rsrc_t row[4];
-  __device__ __forceinline__ LoraRows(const void* base, bool f32, int64_t stride, const int* rows, int part, int n) {
+  __device__ __forceinline__ LoraRows(const void* base, bool f32, int64_t stride, const int (&rows)[4], int part, int n) {
 #pragma unroll
     for (int m = 0; m < 4; ++m) {
-      const int64_t at = (int64_t)__builtin_amdgcn_readfirstlane(rows[min(m, part - 1)]) * stride;
+      const int64_t at = (int64_t)rows[m] * stride;
       row[m] = __builtin_amdgcn_make_buffer_rsrc(
           const_cast<char*>(static_cast<const char*>(base) + at * (f32 ? 4 : 2)), (short)0,
           m < part ? n * (f32 ? 4 : 2) : 0, 0x00020000);
@@ -193,133 +197,114 @@ struct LoraRows {
   }
 };
 
-// RS steps of 32 ranks.  A wave takes 64 columns at a time, B of the next ones in
-// flight, and 4 rows at a time: the operand repeats them, so that lane (i, q) has all
-// four for column i of every tile and takes tile q, 64 neighbouring columns a row.
-// (16 rows at a time would take a quarter of the matrix instructions, of which there
-// are plenty, and touch 16 columns of a row at a time.)
-#ifndef QG_LS
-#define QG_LS 4
-#define QG_LD 8
-#endif
-#ifdef QG_LW
-#define QG_WP __attribute__((amdgpu_waves_per_eu(QG_LW)))
-#else
-#define QG_WP
-#endif
+// 8 ranks of the first product as the sum of three bf16 operands.
+struct LoraLow {
+  u32x4_t v[3];
+  __device__ __forceinline__ void split(float (&f)[8]) {
+    float most = 0.0f;
+#pragma unroll
+    for (int j = 0; j < 8; ++j) most = fmaxf(most, fabsf(f[j]));
+    const bool huge = __ballot(most > 0x1p127f) != 0;   // bf16's infinity, perhaps: all in the first
+#pragma unroll
+    for (int u = 0; u < 3; ++u)
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const uint32_t h = pack_bf16(f[2 * j], f[2 * j + 1]);
+        v[u][j] = h;
+        f[2 * j] = huge ? 0.0f : f[2 * j] - __uint_as_float(h << 16);
+        f[2 * j + 1] = huge ? 0.0f : f[2 * j + 1] - __uint_as_float(h & 0xffff0000u);
+      }
+  }
+};
+
+// RS steps of 32 ranks.  A wave takes 64 columns, and 4 rows at a time: the operand
+// repeats them, so that lane (i, q) has all four for column i of every tile and takes
+// tile q, 64 neighbouring columns a row.  (16 rows at a time would take a quarter of
+// the matrix instructions, of which there are plenty, and touch 16 columns of a row
+// at a time.)  Waves share nothing: once a wave knows its adapter, all it reads is
+// on its way together.
 template <int RS, bool Y32, bool OUT32>
-__global__ __launch_bounds__(256) QG_WP void lora_up_kernel(LoraArgs a) {
-  constexpr int LD = 32 * RS + 8;                // bf16 apart: operand reads on distinct banks
-  __shared__ __attribute__((aligned(16))) uint16_t low[3][16][LD];
-  __shared__ int rows[kLoraRows];
-  const int tid = threadIdx.x, lane = tid & 63, i = lane & 15, q = lane >> 4, wave = wave_id_uniform();
+__global__ __launch_bounds__(256) void lora_up_kernel(LoraArgs a) {
+  const int lane = threadIdx.x & 63, i = lane & 15, q = lane >> 4, wave = wave_id_uniform();
   const int units = min(a.m, a.adapters);
-  const int first = blockIdx.x * 256 + 64 * wave, stride = gridDim.x * 256;   // this wave's columns
   if ((int)blockIdx.y >= units) {
     lora_rest<Y32, OUT32>(a, 4 * ((int)blockIdx.y - units) + wave);
     return;
   }
+  const int col = blockIdx.x * 256 + 64 * wave;
   int adapter;
-  const uint64_t mask = lora_rows(a, blockIdx.y, adapter);
-  if (mask == 0) return;                         // the same in all waves
-  const int count = __popcll(mask);
-  lora_list(mask, rows);
-  const BufView b(a.b + (size_t)adapter * a.n * a.r, a.n * a.r * 2);
-  LoraB<RS> w0;
-  w0.load(b, a.r, first);                    // on its way while the first product's parts are added
-  lds_barrier();
+  uint64_t mask = lora_rows(a, blockIdx.y, adapter);
+  if (mask == 0 || col >= a.n) return;
+  const BufView bv(a.b + (size_t)adapter * a.n * a.r, a.n * a.r * 2);
+  const BufView pv(a.part, a.splits * a.m * a.r * 4);
+  LoraB<RS> b;
+  b.load(bv, a.r, col);
   const float scale = a.scales ? a.scales[adapter] : 1.0f;
-  for (int m0 = 0; m0 < count; m0 += 16) {
-    const int part = min(16, count - m0);
-    const int* const mine = rows + m0;
-    if (m0 > 0) {
-      lds_barrier();
-      w0.load(b, a.r, first);
+  do {
+    int rows[4], some = 0;
+#pragma unroll
+    for (int m = 0; m < 4; ++m) {
+      rows[m] = m > 0 ? rows[m - 1] : 0;
+      if (mask == 0) continue;
+      rows[m] = __builtin_ctzll(mask);
+      mask &= mask - 1;
+      ++some;
     }
-    const LoraRows y0(a.y, Y32, a.y_stride, mine, min(part, 4), a.n);
+    const LoraRows ys(a.y, Y32, a.y_stride, rows, some, a.n), os(a.out, OUT32, a.out_stride, rows, some, a.n);
     float y[4];
 #pragma unroll
-    for (int m = 0; m < 4; ++m) y[m] = y0.load<Y32>(m, first + lane);
-#pragma unroll 1
-    for (int at = tid; at < part * 32 * RS; at += 256) {
-      const int m = at / (32 * RS), r = at % (32 * RS);
-      float v = 0.0f;
-      if (r < a.r) {
-        float t[kLoraSplits];                    // all on their way together
-        const float* const p = a.part + (size_t)mine[m] * a.r + r;
+    for (int m = 0; m < 4; ++m) y[m] = ys.load<Y32>(m, col + lane);
+    const int mine = (i & 2) ? ((i & 1) ? rows[3] : rows[2]) : ((i & 1) ? rows[1] : rows[0]);
+    f32x4_t acc[4] = {};
 #pragma unroll
-        for (int s = 0; s < kLoraSplits; ++s) t[s] = s < a.splits ? p[(size_t)s * a.m * a.r] : 0.0f;
+    for (int s = 0; s < RS; ++s) {
+      const int rank = 32 * s + 8 * q;
+      uint32_t at = rank < a.r ? 4u * (uint32_t)(mine * a.r + rank) : 0xf0000000u;   // past the view: zeros
+      u32x4_t v[kLoraSplits][2] = {};
 #pragma unroll
-        for (int s = 0; s < kLoraSplits; ++s) v += t[s];
-        v *= scale;
+      for (int p = 0; p < kLoraSplits; p += 2) {
+        if (p > 0 && p >= a.splits) continue;    // uniform; a part past the last is past the view
+#pragma unroll
+        for (int o = 0; o < 2; ++o, at += 4u * (uint32_t)(a.m * a.r))
+          v[p + o][0] = pv.b128<false>(at), v[p + o][1] = pv.b128<false>(at + 16);
       }
+      float f[8];
 #pragma unroll
-      for (int u = 0; u < 3; ++u) {
-        const uint32_t h = f32_to_bf16_rne(v);
-        low[u][m][r] = (uint16_t)h;
-        v = (h & 0x7fffu) < 0x7f80u ? v - bf16_to_f32(h) : 0.0f;   // an infinity is whole in the first
+      for (int j = 0; j < 8; ++j) {
+        f[j] = __uint_as_float(v[0][j >> 2][j & 3]);
+#pragma unroll
+        for (int p = 1; p < kLoraSplits; ++p) f[j] += __uint_as_float(v[p][j >> 2][j & 3]);
+        f[j] *= scale;
       }
+      LoraLow low;
+      low.split(f);
+#pragma unroll
+      for (int u = 2; u >= 0; --u)
+#pragma unroll
+        for (int t = 0; t < 4; ++t)
+          acc[t] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8_t, low.v[u]),
+                                                           __builtin_bit_cast(bf16x8_t, b.w[t][s]), acc[t], 0, 0, 0);
     }
-    lds_barrier();
-    auto step = [&](const LoraB<RS>& w, int col) {
-      for (int g = 0; g < part; g += 4) {
-        const int some = min(part - g, 4);
-        const LoraRows ys(a.y, Y32, a.y_stride, mine + g, some, a.n);
-        if (g > 0) {
 #pragma unroll
-          for (int m = 0; m < 4; ++m) y[m] = ys.load<Y32>(m, col + lane);
-        }
-        f32x4_t acc[4] = {};
-#pragma unroll
-        for (int s = 0; s < RS; ++s)
-#pragma unroll
-          for (int u = 2; u >= 0; --u) {
-            const u32x4_t v = *reinterpret_cast<const u32x4_t*>(&low[u][g + min(i & 3, some - 1)][32 * s + 8 * q]);
-#pragma unroll
-            for (int t = 0; t < 4; ++t)
-              acc[t] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8_t, v),
-                                                               __builtin_bit_cast(bf16x8_t, w.w[t][s]), acc[t], 0, 0, 0);
-          }
-        const LoraRows os(a.out, OUT32, a.out_stride, mine + g, some, a.n);
-#pragma unroll
-        for (int m = 0; m < 4; ++m) {
-          const float v = q < 2 ? (q == 0 ? acc[0][m] : acc[1][m]) : (q == 2 ? acc[2][m] : acc[3][m]);
-          os.store<OUT32>(m, col + lane, y[m] + v);
-        }
-      }
-    };
-    for (int col = first; col < a.n; col += stride) {
-      const int next = col + stride;
-      if constexpr (RS <= 4) {
-        LoraB<RS> w1;
-        if (next < a.n) w1.load(b, a.r, next);
-        step(w0, col);
-        w0 = w1;
-      } else {                                   // B takes the registers of two: no next one in flight
-        step(w0, col);
-        if (next < a.n) w0.load(b, a.r, next);
-      }
-      if (next < a.n)
-#pragma unroll
-        for (int m = 0; m < 4; ++m) y[m] = y0.load<Y32>(m, next + lane);
+    for (int m = 0; m < 4; ++m) {
+      const float v = q < 2 ? (q == 0 ? acc[0][m] : acc[1][m]) : (q == 2 ? acc[2][m] : acc[3][m]);
+      os.store<OUT32>(m, col + lane, y[m] + v);
     }
-  }
+  } while (mask != 0);
 }
 
 int lora_splits(int64_t m, int64_t k, int64_t r, int64_t adapters) {
-  (void)m, (void)r, (void)adapters;
-  return (int)std::min<int64_t>(kLoraSplits, (k + kLoraStep - 1) / kLoraStep);
+  // Parts of K: a step each while that gives two workgroups a CU.
+  const int64_t units = std::min(m, adapters) * ((r + 15) / 16), steps = (k + kLoraStep - 1) / kLoraStep;
+  return (int)std::max<int64_t>(1, std::min<int64_t>({steps, kLoraSplits, (2 * kCUs + units - 1) / units}));
 }
 
 hipError_t launch_lora_add(LoraArgs a, hipStream_t stream) {
   const int units = std::min(a.m, a.adapters);
-  hipLaunchKernelGGL(lora_down_kernel, dim3((a.r + 15) / 16, units, a.splits), dim3(256), 0, stream, a);
+  hipLaunchKernelGGL(lora_down_kernel, dim3((a.r + 15) / 16, units, a.splits), dim3(64 * kLoraWaves), 0, stream, a);
   const hipError_t st = hipGetLastError();
   if (st != hipSuccess) return st;
-  // Steps a wave: up to 4 while eight workgroups a CU are left.
-  const int blocks = (a.n + 255) / 256;
-  a.steps = std::max(1, std::min(QG_LS, (int)((int64_t)units * blocks / (QG_LD * kCUs))));
-  const dim3 grid((blocks + a.steps - 1) / a.steps, units + (a.m + 3) / 4);
+  const dim3 grid((a.n + 255) / 256, units + (a.m + 3) / 4);
   const int types = (a.y_f32 ? 2 : 0) + (a.out_f32 ? 1 : 0);
 #define QG_LORA(RS)                                                                                    \
   switch (types) {                                                                                     \
