@@ -80,6 +80,7 @@ def _load() -> ctypes.CDLL:
     }
     F32 = ctypes.c_float
     sigs |= {
+        "qgemm_w4a8_rows": (I32, [P, P, I32, I64, I64, P, I64, I32, I64, P, I32, I32, P, I64, P]),
         "qg_rms_norm": (I32, [P, I32, I64, P, I32, I64, I64, I64, P, F32, P, I32, P, P]),
         "qg_rms_norm_q8": (I32, [P, I32, I64, P, I32, I64, I64, I64, P, F32, P, P, I32, P, P]),
         "qg_lora_add_workspace_bytes": (I64, [I64, I64, I64, I64, I64]),
@@ -391,6 +392,27 @@ def qgemm_w4a8_g32_dq(x: torch.Tensor, packed: torch.Tensor, n: int, *, split_k:
     """qgemm_w4a8_g32 (one activation scale per group of 32) on a scale-code packed weight (m <= 64)."""
     return _w4a8_call(lib.qgemm_w4a8_g32_dq, "qgemm_w4a8_g32_dq", x, packed, n, split_k, out_dtype, out,
                       workspace)
+
+
+def qgemm_w4a8_rows(codes: torch.Tensor, scales: torch.Tensor, packed: torch.Tensor, n: int, *, scale_codes: bool = False,
+                    split_k: int = 0, out_dtype: torch.dtype = torch.bfloat16, out: torch.Tensor | None = None,
+                    workspace: torch.Tensor | None = None) -> torch.Tensor:
+    """W4A8 on rows that come quantized (rms_norm_q8): codes int8 [m, k] with fp32
+    scales [m], or [m, k / 32] for one per group of 32; scale_codes for a weight of
+    quantize_int4_g32_dq."""
+    _dev(codes, "codes", torch.int8, 2)
+    m, k = codes.shape
+    groups = scales.dim() == 2
+    _dev(scales, "scales", torch.float32, 2 if groups else 1)
+    if tuple(scales.shape) != ((m, k // GROUP) if groups else (m,)):
+        raise ValueError("scales must be [m] or [m, k / 32]")
+    _same_device(codes.device, scales=scales, packed=packed, out=out, workspace=workspace)
+    y, yd = _out(m, n, out_dtype, codes.device, out)
+    ws, ws_bytes = _workspace(m, n, k, split_k, codes.device, workspace)
+    st = lib.qgemm_w4a8_rows(codes.data_ptr(), scales.data_ptr(), groups, m, k, packed.data_ptr(), packed.numel(),
+                             scale_codes, n, y.data_ptr(), yd, split_k, _ptr(ws), ws_bytes, _stream(codes.device))
+    _check(st, "qgemm_w4a8_rows")
+    return y
 
 
 # ---- operators of a decoder layer around the linears -------------------------

@@ -45,6 +45,9 @@ hipError_t launch_w4a8g_mfma(bool dq, int m, const void* xq, const float* act_sc
                              int k, void* y, int y_f32, float* partial, int split, hipStream_t stream);
 hipError_t launch_w4a8_actquant_bf16(int m, const void* x, int k, void* xq, float* sx,
                                      hipStream_t stream);
+hipError_t launch_w4a8_rows(int m, bool group_scales, bool dq, const void* xq, const float* sx, const void* packed, int n,
+                            int k, void* y, int y_f32, float* partial, int split, hipStream_t stream);
+hipError_t launch_w4a8_expand(int m, const int8_t* xq, int k, void* out, const float* sx, float* sxg, hipStream_t stream);
 hipError_t launch_w4a8_rowscale_reduce(const float* partial, int split, int m, int n, const float* sx,
                                        void* y, int y_f32, hipStream_t stream);
 hipError_t launch_w4a8_dq(int m, bool group_scales, const void* x, const void* packed, int n, int k,
@@ -583,6 +586,47 @@ int32_t qgemm_w4a8_g32_dq(const void* x_bf16, int64_t m, int64_t k, const void* 
                           void* ws, int64_t ws_bytes, void* stream) {
   return w4a8_common(x_bf16, m, k, packed, packed_bytes, n, y, y_dtype, split_k, ws, ws_bytes,
                      stream, true, true);
+}
+
+int32_t qgemm_w4a8_rows(const int8_t* xq, const float* scales, int32_t group_scales, int64_t m, int64_t k,
+                        const void* packed, int64_t packed_bytes, int32_t scale_codes, int64_t n, void* y,
+                        int32_t y_dtype, int32_t split_k, void* ws, int64_t ws_bytes, void* stream) {
+  if (!xq || !scales || !packed || !y) return QG_E_NULL;
+  int32_t st = check_mnk(m, n, k);
+  if (st != QG_OK) return st;
+  if (y_dtype != QG_BF16 && y_dtype != QG_F32) return QG_E_DTYPE;
+  const bool gs = group_scales != 0, dq = scale_codes != 0, f32 = y_dtype == QG_F32;
+  int32_t split;
+  st = resolve_split(m, n, k, split_k, &split, m > 4 && gs ? qg::SplitRule::kW4A8G32 : qg::SplitRule::kW4);
+  if (st != QG_OK) return st;
+  if (packed_bytes < (dq ? qg_int4_dq_packed_bytes(n, k) : qg_int4_packed_bytes(n, k))) return QG_E_BUFFER;
+  const int64_t need = m > 4 ? w4a8_mfma_ws(m, n, k, split) : split > 1 ? (int64_t)split * m * n * 4 : 0;
+  if (need > 0 && (!ws || ws_bytes < need)) return ws ? QG_E_BUFFER : QG_E_NULL;
+  if (!aligned16(xq) || !aligned16(packed) || !aligned16(y) || !aligned16(ws) || ((uintptr_t)scales & 3u))
+    return QG_E_ALIGN;
+  hipStream_t s = static_cast<hipStream_t>(stream);
+  if (m <= 4) {
+    float* const partial = split > 1 ? static_cast<float*>(ws) : nullptr;
+    st = hip_status(qg::launch_w4a8_rows((int)m, gs, dq, xq, scales, packed, (int)n, (int)k, y, f32, partial, split, s));
+    if (st != QG_OK || split == 1) return st;
+    return hip_status(qg::launch_splitk_reduce(partial, split, m * n, y, f32, s));
+  }
+  // As w4a8_common above 4 rows, from the codes on.
+  char* const w = static_cast<char*>(ws);
+  float* const sxg = reinterpret_cast<float*>(w + m * k * 2);
+  float* const partial = split > 1 ? reinterpret_cast<float*>(w + m * k * 2 + w4a8_scales_bytes(k)) : nullptr;
+  st = hip_status(qg::launch_w4a8_expand((int)m, xq, (int)k, w, gs ? scales : nullptr, sxg, s));
+  if (st != QG_OK) return st;
+  if (gs) {
+    st = hip_status(qg::launch_w4a8g_mfma(dq, (int)m, w, sxg, packed, (int)n, (int)k, y, f32, partial, split, s));
+    if (st != QG_OK || split == 1) return st;
+    return hip_status(qg::launch_splitk_reduce(partial, split, m * n, y, f32, s));
+  }
+  const float* const in_store = split == 1 ? scales : nullptr;
+  st = hip_status(dq ? qg::launch_w4a16_mfma_dq((int)m, w, packed, (int)n, (int)k, y, f32, partial, split, s, in_store)
+                     : qg::launch_w4a16_mfma((int)m, w, packed, (int)n, (int)k, y, f32, partial, split, s, in_store));
+  if (st != QG_OK || split == 1) return st;
+  return hip_status(qg::launch_w4a8_rowscale_reduce(partial, split, (int)m, (int)n, scales, y, f32, s));
 }
 
 int32_t qg_stream_read(const void* src, int64_t bytes, uint32_t* sink, int32_t blocks,

@@ -87,6 +87,16 @@ __device__ __forceinline__ void quant8(const u32x4_t& v, float inv, uint32_t& xl
   xhi = b(2) | (b(6) << 8) | (b(3) << 16) | (b(7) << 24);
 }
 
+// Rows that come quantized (Q8: qgemm_w4a8_rows): 8 codes as they lie in memory,
+// in the byte order of quant8.
+__device__ __forceinline__ void order8(const u32x2_t& v, uint32_t& xlo, uint32_t& xhi) {
+  xlo = __builtin_amdgcn_perm(v.y, v.x, 0x05010400u);
+  xhi = __builtin_amdgcn_perm(v.y, v.x, 0x07030602u);
+}
+__device__ __forceinline__ u32x2_t load_codes8(const uint16_t* x, size_t at) {
+  return *reinterpret_cast<const u32x2_t*>(reinterpret_cast<const int8_t*>(x) + at);
+}
+
 template <int M, int JJ>
 __device__ __forceinline__ void do_group_a8(float (&acc)[M], const HalfRegs& cur,
                                             const uint32_t (&xlo)[M], const uint32_t (&xhi)[M],
@@ -112,10 +122,10 @@ __device__ __forceinline__ void do_group_a8(float (&acc)[M], const HalfRegs& cur
   }
 }
 
-template <int M, int WAVES>
+template <int M, int WAVES, bool Q8 = false>
 __global__ __launch_bounds__(WAVES * 64) void w4a8_gemv_kernel(
     const uint16_t* __restrict__ x, const uint8_t* __restrict__ packed, int n, int k,
-    void* __restrict__ y, int y_f32, float* __restrict__ partial, int split) {
+    void* __restrict__ y, int y_f32, float* __restrict__ partial, int split, const float* __restrict__ act_scale) {
   __shared__ float red[WAVES * M * 64];
   __shared__ float amax_w[WAVES][M];
   const int lane = threadIdx.x & 63;
@@ -127,31 +137,36 @@ __global__ __launch_bounds__(WAVES * 64) void w4a8_gemv_kernel(
   split_range(kt_count, split, blockIdx.y, t0, t1);
   const uint8_t* tiles = packed + (size_t)rb * kt_count * kTileBytes;
 
-  // Per-row absmax of x over the whole K (every split needs the same scale).
-#pragma unroll
-  for (int m = 0; m < M; ++m) {
-    float a = 0.0f;
-    const u32x4_t* xr = reinterpret_cast<const u32x4_t*>(x + (size_t)m * k);
-    for (int i = threadIdx.x; i < (k >> 3); i += WAVES * 64) {
-      const u32x4_t v = xr[i];
-      const uint32_t w[4] = {v.x, v.y, v.z, v.w};
-#pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        a = nmax(a, fabsf(bf16_to_f32(w[j] & 0xffffu)));
-        a = nmax(a, fabsf(bf16_to_f32(w[j] >> 16)));
-      }
-    }
-#pragma unroll
-    for (int off = 32; off > 0; off >>= 1) a = nmax(a, __shfl_xor(a, off, 64));
-    if (lane == 0) amax_w[wave][m] = a;
-  }
-  __syncthreads();
   float inv[M], sx[M];
+  if constexpr (Q8) {
 #pragma unroll
-  for (int m = 0; m < M; ++m) {
-    float a = amax_w[0][m];
-    for (int ww = 1; ww < WAVES; ++ww) a = nmax(a, amax_w[ww][m]);
-    span_scale(finite_or_nan(a), inv[m], sx[m]);
+    for (int m = 0; m < M; ++m) sx[m] = act_scale[m];
+  } else {
+    // Per-row absmax of x over the whole K (every split needs the same scale).
+#pragma unroll
+    for (int m = 0; m < M; ++m) {
+      float a = 0.0f;
+      const u32x4_t* xr = reinterpret_cast<const u32x4_t*>(x + (size_t)m * k);
+      for (int i = threadIdx.x; i < (k >> 3); i += WAVES * 64) {
+        const u32x4_t v = xr[i];
+        const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          a = nmax(a, fabsf(bf16_to_f32(w[j] & 0xffffu)));
+          a = nmax(a, fabsf(bf16_to_f32(w[j] >> 16)));
+        }
+      }
+#pragma unroll
+      for (int off = 32; off > 0; off >>= 1) a = nmax(a, __shfl_xor(a, off, 64));
+      if (lane == 0) amax_w[wave][m] = a;
+    }
+    __syncthreads();
+#pragma unroll
+    for (int m = 0; m < M; ++m) {
+      float a = amax_w[0][m];
+      for (int ww = 1; ww < WAVES; ++ww) a = nmax(a, amax_w[ww][m]);
+      span_scale(finite_or_nan(a), inv[m], sx[m]);
+    }
   }
 
   const uint32_t nib_s = __builtin_amdgcn_readfirstlane(0x0F0F0F0Fu);
@@ -169,8 +184,10 @@ __global__ __launch_bounds__(WAVES * 64) void w4a8_gemv_kernel(
     int sxq[M];
 #pragma unroll
     for (int m = 0; m < M; ++m) {
-      const u32x4_t v = *reinterpret_cast<const u32x4_t*>(x + (size_t)m * k + (size_t)hs * 128 + li * 8);
-      quant8(v, inv[m], xlo[m], xhi[m]);
+      if constexpr (Q8)
+        order8(load_codes8(x, (size_t)m * k + (size_t)hs * 128 + li * 8), xlo[m], xhi[m]);
+      else
+        quant8(*reinterpret_cast<const u32x4_t*>(x + (size_t)m * k + (size_t)hs * 128 + li * 8), inv[m], xlo[m], xhi[m]);
       // sum of this lane's 8 xq, then over the 4 lanes of its group
       int p = __builtin_amdgcn_sdot4((int)xlo[m], (int)ones_v, 0, false);
       p = __builtin_amdgcn_sdot4((int)xhi[m], (int)ones_v, p, false);
@@ -235,10 +252,10 @@ __device__ __forceinline__ void do_group_a8_32(float (&acc)[M], const Half32Regs
   }
 }
 
-template <int M, int WAVES, bool DQ = false>
+template <int M, int WAVES, bool DQ = false, bool Q8 = false>
 __global__ __launch_bounds__(WAVES * 64) void w4a8_gemv32_kernel(
     const uint16_t* __restrict__ x, const uint8_t* __restrict__ packed, int n, int k,
-    void* __restrict__ y, int y_f32, float* __restrict__ partial, int split) {
+    void* __restrict__ y, int y_f32, float* __restrict__ partial, int split, const float* __restrict__ act_scale) {
   __shared__ float red[WAVES * M * 64];
   __shared__ float amax_w[WAVES][M];
   const int lane = threadIdx.x & 63;
@@ -254,31 +271,36 @@ __global__ __launch_bounds__(WAVES * 64) void w4a8_gemv32_kernel(
   float step;
   const uint8_t* tiles = L::tiles(packed, rb, kt_count, row, step);
 
-  // Per-row absmax of x over the whole K (every split needs the same scale).
-#pragma unroll
-  for (int m = 0; m < M; ++m) {
-    float a = 0.0f;
-    const u32x4_t* xr = reinterpret_cast<const u32x4_t*>(x + (size_t)m * k);
-    for (int i = threadIdx.x; i < (k >> 3); i += WAVES * 64) {
-      const u32x4_t v = xr[i];
-      const uint32_t w[4] = {v.x, v.y, v.z, v.w};
-#pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        a = nmax(a, fabsf(bf16_to_f32(w[j] & 0xffffu)));
-        a = nmax(a, fabsf(bf16_to_f32(w[j] >> 16)));
-      }
-    }
-#pragma unroll
-    for (int off = 32; off > 0; off >>= 1) a = nmax(a, __shfl_xor(a, off, 64));
-    if (lane == 0) amax_w[wave][m] = a;
-  }
-  __syncthreads();
   float inv[M], sx[M];
+  if constexpr (Q8) {
 #pragma unroll
-  for (int m = 0; m < M; ++m) {
-    float a = amax_w[0][m];
-    for (int ww = 1; ww < WAVES; ++ww) a = nmax(a, amax_w[ww][m]);
-    span_scale(finite_or_nan(a), inv[m], sx[m]);
+    for (int m = 0; m < M; ++m) sx[m] = act_scale[m];
+  } else {
+    // Per-row absmax of x over the whole K (every split needs the same scale).
+#pragma unroll
+    for (int m = 0; m < M; ++m) {
+      float a = 0.0f;
+      const u32x4_t* xr = reinterpret_cast<const u32x4_t*>(x + (size_t)m * k);
+      for (int i = threadIdx.x; i < (k >> 3); i += WAVES * 64) {
+        const u32x4_t v = xr[i];
+        const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          a = nmax(a, fabsf(bf16_to_f32(w[j] & 0xffffu)));
+          a = nmax(a, fabsf(bf16_to_f32(w[j] >> 16)));
+        }
+      }
+#pragma unroll
+      for (int off = 32; off > 0; off >>= 1) a = nmax(a, __shfl_xor(a, off, 64));
+      if (lane == 0) amax_w[wave][m] = a;
+    }
+    __syncthreads();
+#pragma unroll
+    for (int m = 0; m < M; ++m) {
+      float a = amax_w[0][m];
+      for (int ww = 1; ww < WAVES; ++ww) a = nmax(a, amax_w[ww][m]);
+      span_scale(finite_or_nan(a), inv[m], sx[m]);
+    }
   }
 
   const uint32_t nib_s = __builtin_amdgcn_readfirstlane(0x0F0F0F0Fu);
@@ -296,9 +318,11 @@ __global__ __launch_bounds__(WAVES * 64) void w4a8_gemv32_kernel(
     int sxq[M];
 #pragma unroll
     for (int m = 0; m < M; ++m) {
-      const u32x4_t v = *reinterpret_cast<const u32x4_t*>(x + (size_t)m * k + (size_t)hs * 128 +
-                                                          64 * lg + 8 * seg);
-      quant8(v, inv[m], xlo[m], xhi[m]);
+      const size_t at = (size_t)m * k + (size_t)hs * 128 + 64 * lg + 8 * seg;
+      if constexpr (Q8)
+        order8(load_codes8(x, at), xlo[m], xhi[m]);
+      else
+        quant8(*reinterpret_cast<const u32x4_t*>(x + at), inv[m], xlo[m], xhi[m]);
       // sum of this lane's 8 xq, then over the 4 lanes of its group
       int p = __builtin_amdgcn_sdot4((int)xlo[m], (int)ones_v, 0, false);
       p = __builtin_amdgcn_sdot4((int)xhi[m], (int)ones_v, p, false);
@@ -351,10 +375,10 @@ __global__ __launch_bounds__(WAVES * 64) void w4a8_gemv32_kernel(
 constexpr int kA8Chunk = 16;                 // half tiles per chunk
 constexpr int kA8Segs = kA8Chunk * 16;       // 8-k segments per chunk
 
-template <int M, bool DQ = false>
+template <int M, bool DQ = false, bool Q8 = false>
 __global__ __launch_bounds__(1024) void w4a8_gemv_lds_kernel(
     const uint16_t* __restrict__ x, const uint8_t* __restrict__ packed, int n, int k,
-    void* __restrict__ y, int y_f32, float* __restrict__ partial, int split) {
+    void* __restrict__ y, int y_f32, float* __restrict__ partial, int split, const float* __restrict__ act_scale) {
   constexpr int WAVES = 16;
   __shared__ u32x2_t xq_s[2][M][kA8Segs];
   __shared__ float sx_s[2][M][kA8Segs / 4];
@@ -393,19 +417,26 @@ __global__ __launch_bounds__(1024) void w4a8_gemv_lds_kernel(
     {
       const int m = tid >> 8, sg = tid & (kA8Segs - 1);
       if (m < M && sg < nh * 16) {
-        const u32x4_t v = *reinterpret_cast<const u32x4_t*>(x + (size_t)m * k + (size_t)cb * 128 + sg * 8);
-        const uint32_t w[4] = {v.x, v.y, v.z, v.w};
-        float a = 0.0f;
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          a = nmax(a, fabsf(bf16_to_f32(w[j] & 0xffffu)));
-          a = nmax(a, fabsf(bf16_to_f32(w[j] >> 16)));
-        }
-        a = nmax(a, dpp_fa<0xB1>(a));          // the lane quad holds one group of 32
-        float inv, sxv;
-        span_scale(finite_or_nan(nmax(a, dpp_fa<0x4E>(a))), inv, sxv);
+        const size_t at = (size_t)m * k + (size_t)cb * 128 + sg * 8;
         uint32_t lo, hi;
-        quant8(v, inv, lo, hi);
+        float sxv;
+        if constexpr (Q8) {
+          order8(load_codes8(x, at), lo, hi);
+          sxv = act_scale[at >> 5];
+        } else {
+          const u32x4_t v = *reinterpret_cast<const u32x4_t*>(x + at);
+          const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+          float a = 0.0f;
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            a = nmax(a, fabsf(bf16_to_f32(w[j] & 0xffffu)));
+            a = nmax(a, fabsf(bf16_to_f32(w[j] >> 16)));
+          }
+          a = nmax(a, dpp_fa<0xB1>(a));          // the lane quad holds one group of 32
+          float inv;
+          span_scale(finite_or_nan(nmax(a, dpp_fa<0x4E>(a))), inv, sxv);
+          quant8(v, inv, lo, hi);
+        }
         xq_s[buf][m][sg] = u32x2_t{lo, hi};
         if ((sg & 3) == 0) sx_s[buf][m][sg >> 2] = sxv;
       }
@@ -516,10 +547,10 @@ __device__ __forceinline__ float absmax8(const u32x4_t& v, float a) {
 // per CU, so 128 VGPRs and two register sets used in turn: the next half
 // tile's loads are in flight while the current one is computed (the grids it
 // is used on are in dispatch.h, gemv_shape).
-template <int M, bool GS, bool DQ = false, bool R64 = false>
+template <int M, bool GS, bool DQ = false, bool R64 = false, bool Q8 = false>
 __global__ __launch_bounds__(1024) __attribute__((amdgpu_waves_per_eu(R64 ? 4 : 8))) void w4a8_gemv_mx4_kernel(
     const uint16_t* __restrict__ x, const uint8_t* __restrict__ packed, int n, int k,
-    void* __restrict__ y, int y_f32, float* __restrict__ partial, int split) {
+    void* __restrict__ y, int y_f32, float* __restrict__ partial, int split, const float* __restrict__ act_scale) {
   constexpr int WAVES = 16;
   __shared__ __attribute__((aligned(16))) uint8_t xq_s[WAVES][M * kA8XRowBytes];
   __shared__ __attribute__((aligned(16))) int gsum_s[WAVES][4][4];          // [group][m]
@@ -555,11 +586,25 @@ __global__ __launch_bounds__(1024) __attribute__((amdgpu_waves_per_eu(R64 ? 4 : 
   };
   auto load_x = [&](int h) {
     u32x4_t v = {0u, 0u, 0u, 0u};
-    if (qlane) v = *reinterpret_cast<const u32x4_t*>(xsrc + (size_t)h * 128);
+    if constexpr (Q8) {                            // 8 codes, and the scale of their group
+      const size_t at = (size_t)qm * k + 8 * qs + (size_t)h * 128;
+      if (qlane) {
+        const u32x2_t c = load_codes8(x, at);
+        v = u32x4_t{c.x, c.y, GS ? __float_as_uint(act_scale[at >> 5]) : 0u, 0u};
+      }
+    } else {
+      if (qlane) v = *reinterpret_cast<const u32x4_t*>(xsrc + (size_t)h * 128);
+    }
     return v;
   };
   float inv_q = 0.0f, sx_row[M];
-  if constexpr (!GS) {
+  if constexpr (Q8) {
+    if (hs < h_end) load_w(r, hs);
+    if constexpr (!GS) {
+#pragma unroll
+      for (int m = 0; m < M; ++m) sx_row[m] = act_scale[m];
+    }
+  } else if constexpr (!GS) {
     // Per-row absmax over the whole row (the workgroup reads x once from L2).
     // The first pass of x loads goes out first, then the first half tile's
     // weight loads, so the wait for x does not wait for HBM and the weight
@@ -621,7 +666,9 @@ __global__ __launch_bounds__(1024) __attribute__((amdgpu_waves_per_eu(R64 ? 4 : 
   auto compute = [&](const Half32Regs (&rr)[NP], const u32x4_t& v) {
     // ---- quantize this lane's segment; the quad holds one group of 32.
     float inv = inv_q, sxv = 0.0f;
-    if constexpr (GS) {
+    if constexpr (Q8) {
+      sxv = __uint_as_float(v.z);
+    } else if constexpr (GS) {
       const uint32_t w[4] = {v.x, v.y, v.z, v.w};
       float a = 0.0f;
 #pragma unroll
@@ -633,7 +680,10 @@ __global__ __launch_bounds__(1024) __attribute__((amdgpu_waves_per_eu(R64 ? 4 : 
       span_scale(finite_or_nan(nmax(a, dpp_fa<0x4E>(a))), inv, sxv);
     }
     uint32_t lo, hi;
-    quant8(v, inv, lo, hi);
+    if constexpr (Q8)
+      order8(u32x2_t{v.x, v.y}, lo, hi);
+    else
+      quant8(v, inv, lo, hi);
     int p = __builtin_amdgcn_sdot4((int)lo, (int)ones_v, 0, false);
     p = __builtin_amdgcn_sdot4((int)hi, (int)ones_v, p, false);
     p += dpp_i<0xB1>(p);                           // group sum of xq over the quad
@@ -743,11 +793,11 @@ static hipError_t launch_w4a8_mx4_t(const void* x, const void* packed, int n, in
   if (gemv_shape(M, n, split).rows == 64)
     hipLaunchKernelGGL((w4a8_gemv_mx4_kernel<M, GS, DQ, true>), dim3(rbs, split), dim3(1024), 0, stream,
                        static_cast<const uint16_t*>(x), static_cast<const uint8_t*>(packed), n, k,
-                       y, y_f32, partial, split);
+                       y, y_f32, partial, split, nullptr);
   else
     hipLaunchKernelGGL((w4a8_gemv_mx4_kernel<M, GS, DQ>), dim3(2 * rbs, split), dim3(1024), 0, stream,
                        static_cast<const uint16_t*>(x), static_cast<const uint8_t*>(packed), n, k,
-                       y, y_f32, partial, split);
+                       y, y_f32, partial, split, nullptr);
   return hipGetLastError();
 }
 
@@ -769,7 +819,7 @@ static hipError_t launch_w4a8_lds_t(const void* x, const void* packed, int n, in
   const int rbs = (n + kTileRows - 1) / kTileRows;
   hipLaunchKernelGGL((w4a8_gemv_lds_kernel<M, DQ>), dim3(2 * rbs, split), dim3(1024), 0, stream,
                      static_cast<const uint16_t*>(x), static_cast<const uint8_t*>(packed), n, k,
-                     y, y_f32, partial, split);
+                     y, y_f32, partial, split, nullptr);
   return hipGetLastError();
 }
 
@@ -788,7 +838,7 @@ static hipError_t launch_w4a8_32_t(const void* x, const void* packed, int n, int
   const int rbs = (n + kTileRows - 1) / kTileRows;
   hipLaunchKernelGGL((w4a8_gemv32_kernel<M, WAVES, DQ>), dim3(2 * rbs, split), dim3(WAVES * 64), 0,
                      stream, static_cast<const uint16_t*>(x), static_cast<const uint8_t*>(packed),
-                     n, k, y, y_f32, partial, split);
+                     n, k, y, y_f32, partial, split, nullptr);
   return hipGetLastError();
 }
 
@@ -798,7 +848,7 @@ static hipError_t launch_w4a8_t(const void* x, const void* packed, int n, int k,
   const int rbs = (n + kTileRows - 1) / kTileRows;
   hipLaunchKernelGGL((w4a8_gemv_kernel<M, WAVES>), dim3(rbs, split), dim3(WAVES * 64), 0, stream,
                      static_cast<const uint16_t*>(x), static_cast<const uint8_t*>(packed), n, k,
-                     y, y_f32, partial, split);
+                     y, y_f32, partial, split, nullptr);
   return hipGetLastError();
 }
 
@@ -834,6 +884,49 @@ hipError_t launch_w4a8_dq(int m, bool group_scales, const void* x, const void* p
   return hipErrorInvalidValue;
 }
 
+
+// Rows that come quantized, M = 1..4: the kernels of the calls above on the codes.
+template <int M, bool GS, bool DQ>
+static void launch_w4a8_rows_t(const uint16_t* x, const float* sx, const uint8_t* w, int n, int k, void* y, int y_f32,
+                               float* partial, int split, hipStream_t stream) {
+  const int rbs = (n + kTileRows - 1) / kTileRows;
+  const bool r64 = gemv_shape(M, n, split).rows == 64;
+  const dim3 wide(rbs, split), half(2 * rbs, split), block(1024);
+  if constexpr (M == 1 && GS) {
+    hipLaunchKernelGGL((w4a8_gemv_lds_kernel<1, DQ, true>), half, block, 0, stream, x, w, n, k, y, y_f32, partial, split, sx);
+  } else if constexpr (M == 1) {
+    if constexpr (!DQ) {
+      if (r64) {
+        hipLaunchKernelGGL((w4a8_gemv_kernel<1, 16, true>), wide, block, 0, stream, x, w, n, k, y, y_f32, partial, split, sx);
+        return;
+      }
+    }
+    hipLaunchKernelGGL((w4a8_gemv32_kernel<1, 16, DQ, true>), half, block, 0, stream, x, w, n, k, y, y_f32, partial, split, sx);
+  } else {
+    if (r64)
+      hipLaunchKernelGGL((w4a8_gemv_mx4_kernel<M, GS, DQ, true, true>), wide, block, 0, stream, x, w, n, k, y, y_f32, partial,
+                         split, sx);
+    else
+      hipLaunchKernelGGL((w4a8_gemv_mx4_kernel<M, GS, DQ, false, true>), half, block, 0, stream, x, w, n, k, y, y_f32, partial,
+                         split, sx);
+  }
+}
+
+hipError_t launch_w4a8_rows(int m, bool group_scales, bool dq, const void* xq, const float* sx, const void* packed, int n,
+                            int k, void* y, int y_f32, float* partial, int split, hipStream_t stream) {
+  const uint16_t* const x = static_cast<const uint16_t*>(xq);
+  const uint8_t* const w = static_cast<const uint8_t*>(packed);
+#define QG_A8R(MM)                                                                                        \
+  if (m == MM) {                                                                                          \
+    if (group_scales && dq) launch_w4a8_rows_t<MM, true, true>(x, sx, w, n, k, y, y_f32, partial, split, stream);         \
+    else if (group_scales) launch_w4a8_rows_t<MM, true, false>(x, sx, w, n, k, y, y_f32, partial, split, stream);         \
+    else if (dq) launch_w4a8_rows_t<MM, false, true>(x, sx, w, n, k, y, y_f32, partial, split, stream);                   \
+    else launch_w4a8_rows_t<MM, false, false>(x, sx, w, n, k, y, y_f32, partial, split, stream);                          \
+  }
+  QG_A8R(1) QG_A8R(2) QG_A8R(3) QG_A8R(4)
+#undef QG_A8R
+  return hipGetLastError();
+}
 
 // ---------------------------------------------------------------------------
 // Per-row scales at 5..64 rows, on the bf16 matrix-core kernels.  xq is an
@@ -921,6 +1014,22 @@ __global__ __launch_bounds__(256) void w4a8_actquant_g32_bf16_kernel(const uint1
   if ((i & 3) == 0) sxg[(size_t)(i >> 2) * 64 + row] = sxv;
 }
 
+// Pass 1 for rows that come quantized: the codes as exact bf16 integers, 8 a thread,
+// and, with one scale per group of 32 (sx not null), the scales group-major.
+__global__ __launch_bounds__(256) void w4a8_expand_kernel(const int8_t* __restrict__ xq, int k, uint16_t* __restrict__ out,
+                                                           const float* __restrict__ sx, float* __restrict__ sxg) {
+  const int row = blockIdx.y, i = blockIdx.x * 256 + threadIdx.x;   // 8-byte piece of the row
+  if (i >= (k >> 3)) return;
+  const u32x2_t v = reinterpret_cast<const u32x2_t*>(xq + (size_t)row * k)[i];
+  uint32_t h[8];
+#pragma unroll
+  for (int j = 0; j < 8; ++j)
+    h[j] = __float_as_uint((float)(int)(int8_t)(v[j >> 2] >> (8 * (j & 3)) & 0xffu)) >> 16;
+  reinterpret_cast<u32x4_t*>(out + (size_t)row * k)[i] =
+      u32x4_t{h[0] | h[1] << 16, h[2] | h[3] << 16, h[4] | h[5] << 16, h[6] | h[7] << 16};
+  if (sx != nullptr && (i & 3) == 0) sxg[(size_t)(i >> 2) * 64 + row] = sx[(size_t)row * (k >> 5) + (i >> 2)];
+}
+
 // Pass 3: y[r, c] = sx[r] * sum over s (ascending) of partial[s, r, c]; a
 // workgroup per (256 columns, row).
 __global__ __launch_bounds__(256) void w4a8_rowscale_reduce_kernel(const float* __restrict__ partial,
@@ -953,6 +1062,12 @@ hipError_t launch_w4a8_actquant_g32_bf16(int m, const void* x, int k, void* xq, 
   const int chunks = ((k >> 3) + 255) / 256;
   hipLaunchKernelGGL(w4a8_actquant_g32_bf16_kernel, dim3(chunks, m), dim3(256), 0, stream,
                      static_cast<const uint16_t*>(x), k, static_cast<uint16_t*>(xq), sxg);
+  return hipGetLastError();
+}
+
+hipError_t launch_w4a8_expand(int m, const int8_t* xq, int k, void* out, const float* sx, float* sxg, hipStream_t stream) {
+  hipLaunchKernelGGL(w4a8_expand_kernel, dim3(((k >> 3) + 255) / 256, m), dim3(256), 0, stream, xq, k,
+                     static_cast<uint16_t*>(out), sx, sxg);
   return hipGetLastError();
 }
 

@@ -362,6 +362,18 @@ int32_t qgemm_w4a8_g32_dq(const void *x_bf16, int64_t m, int64_t k, const void *
                           int64_t packed_bytes, int64_t n, void *y, int32_t y_dtype,
                           int32_t split_k, void *ws, int64_t ws_bytes, void *stream);
 
+/* ---- qgemm_w4a8_rows -----------------------------------------------------
+ * The W4A8 calls above on rows that come quantized (qg_rms_norm_q8, or codes of the
+ * caller's): no pass over x for its scales.
+ *   xq       in : int8 [m, k];   scales in : fp32 [m], or [m, k / 32] with
+ *                 group_scales not 0; value = code * scale
+ *   packed   in : version 1, or version 2 with scale_codes not 0
+ * The sums are those of qgemm_w4a8 (qgemm_w4a8_g32) for the same codes and
+ * scales.  Other arguments, workspace and errors as there. */
+int32_t qgemm_w4a8_rows(const int8_t *xq, const float *scales, int32_t group_scales, int64_t m, int64_t k,
+                        const void *packed, int64_t packed_bytes, int32_t scale_codes, int64_t n, void *y,
+                        int32_t y_dtype, int32_t split_k, void *ws, int64_t ws_bytes, void *stream);
+
 /* ==========================================================================
  * Operators of a decoder layer around the quantized linears.  They follow the
  * conventions above (device pointers, caller's stream and buffers, checks

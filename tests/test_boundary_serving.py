@@ -119,6 +119,22 @@ def test_verify_workspace():
         qg.verify_drafts_workspace_bytes(2, 3, 1000)
 
 
+def rows(**kw):
+    a = dict(xq=A, scales=A, group=0, m=3, k=512, packed=A, bytes=2 * 2 * 9472, codes=0, n=128, y=A, dt=0, split=0, ws=A, ws_bytes=1 << 20, stream=None)
+    assert set(kw) <= set(a)
+    return lib.qgemm_w4a8_rows(*(a | kw).values())
+
+
+@pytest.mark.parametrize("kw,want", [
+    (dict(xq=None), E_NULL), (dict(scales=None), E_NULL), (dict(packed=None), E_NULL), (dict(y=None), E_NULL), (dict(m=0), E_SHAPE), (dict(m=65), E_M),
+    (dict(n=0), E_SHAPE), (dict(k=500), -3), (dict(split=3), -5), (dict(split=4), -5), (dict(dt=2), E_DTYPE), (dict(bytes=2 * 2 * 9472 - 1), E_BUF),
+    (dict(codes=1, bytes=2 * (128 + 2 * 8960) - 1), E_BUF), (dict(split=2, ws=None), E_NULL), (dict(split=2, ws_bytes=2 * 3 * 128 * 4 - 1), E_BUF),
+    (dict(m=9, split=1, ws=None), E_NULL), (dict(m=9, split=1, ws_bytes=9 * 512 * 2), E_BUF), (dict(xq=U), E_ALIGN), (dict(packed=U), E_ALIGN),
+    (dict(y=U), E_ALIGN), (dict(ws=U), E_ALIGN), (dict(scales=A + 2), E_ALIGN)])
+def test_w4a8_rows_refusals(kw, want):
+    assert rows(**kw) == want
+
+
 def test_wrappers_refuse_host_tensors_and_wrong_types():
     x, w = torch.zeros(2, 64, dtype=torch.bfloat16), torch.zeros(64, dtype=torch.bfloat16)
     with pytest.raises(ValueError, match="device"):
@@ -130,6 +146,8 @@ def test_wrappers_refuse_host_tensors_and_wrong_types():
         qg.lora_add(x, x, x[None], x[None], ids)
     with pytest.raises(ValueError, match="device"):
         qg.moe_route(x, 4)
+    with pytest.raises(ValueError, match="device"):
+        qg.qgemm_w4a8_rows(torch.zeros(2, 256, dtype=torch.int8), torch.zeros(2), torch.zeros(9472, dtype=torch.uint8), 64)
     f = torch.zeros(2)
     with pytest.raises(ValueError, match="device"):
         qg.verify_drafts(x, None, ids, f, f, ids)
