@@ -80,6 +80,7 @@ def _load() -> ctypes.CDLL:
     }
     F32 = ctypes.c_float
     sigs |= {
+        "qg_moe_w4a16_picked": (I32, [P, I64, I64, P, P, I64, P, I64, P, I64, I64, I64, P, I32, P, I64, P, P]),
         "qgemm_w4a8_rows": (I32, [P, P, I32, I64, I64, P, I64, I32, I64, P, I32, I32, P, I64, P]),
         "qg_rms_norm": (I32, [P, I32, I64, P, I32, I64, I64, I64, P, F32, P, I32, P, P]),
         "qg_rms_norm_q8": (I32, [P, I32, I64, P, I32, I64, I64, I64, P, F32, P, P, I32, P, P]),
@@ -1053,3 +1054,66 @@ def verify_drafts(target: torch.Tensor, draft: torch.Tensor | None, tokens: torc
     if st:
         _check(st, "qg_verify_drafts")
     return accepted, following
+
+
+def _refuse_picked(x, ids, weights, gate_up, down, inter, out, out_dtype, workspace, status) -> None:
+    _dev(x, "x", torch.bfloat16, 2)
+    _dev(ids, "ids", torch.int32, 2)
+    _dev(weights, "weights", torch.float32, 2)
+    _dev(gate_up, "gate_up", torch.uint8, 2)
+    _dev(down, "down", torch.uint8, 2)
+    if ids.shape != weights.shape or ids.shape[0] != x.shape[0]:
+        raise ValueError("ids and weights must be [t, top_k]")
+    h = x.shape[1]
+    if down.shape[0] != gate_up.shape[0]:
+        raise ValueError("gate_up and down must be [e, bytes]")
+    if gate_up.shape[1] != int4_packed_bytes(2 * inter, h) or down.shape[1] != int4_packed_bytes(h, inter):
+        raise ValueError("gate_up must hold packed 2 inter x h weights and down packed h x inter ones")
+    if out is not None:
+        _dev(out, "out", out_dtype, 2)
+        if out.shape != x.shape:
+            raise ValueError("out must be [t, h]")
+    _refuse_flags(status)
+    _same_device(x.device, ids=ids, weights=weights, gate_up=gate_up, down=down, out=out, workspace=workspace, status=status)
+    raise ValueError("moe_w4a16_picked: arguments that do not fit together")
+
+
+def moe_w4a16_picked(x: torch.Tensor, ids: torch.Tensor, weights: torch.Tensor, gate_up: torch.Tensor, down: torch.Tensor,
+                     inter: int, *, out_dtype: torch.dtype = torch.bfloat16, out: torch.Tensor | None = None,
+                     workspace: torch.Tensor | None = None, status: torch.Tensor | None = None) -> torch.Tensor:
+    """The experts of moe_w4a16 on picks and weights that moe_route (or the caller)
+    chose: x [t, h], ids int32 and weights fp32 [t, top_k] -> y [t, h].  A negative id
+    is no pick; one past the experts, or one a second time for a token, counts for
+    nothing."""
+    dev, xs, ks, gs, ds = x.get_device(), x.shape, ids.shape, gate_up.shape, down.shape
+    od = _out_type(out_dtype)
+    if not (dev >= 0 and len(xs) == 2 and len(ks) == 2 and len(gs) == 2 and len(ds) == 2 and x.dtype is _BF16 and
+            ids.dtype is _I32 and weights.dtype is _F32 and weights.shape == ks and ks[0] == xs[0] and
+            gate_up.dtype is torch.uint8 and down.dtype is torch.uint8 and ds[0] == gs[0] and inter > 0 and
+            gs[1] == 2 * inter // TILE_ROWS * (xs[1] // TILE_K) * TILE_BYTES and
+            ds[1] == xs[1] // TILE_ROWS * (inter // TILE_K) * TILE_BYTES and
+            ids.get_device() == dev and weights.get_device() == dev and gate_up.get_device() == dev and
+            down.get_device() == dev and x.is_contiguous() and ids.is_contiguous() and weights.is_contiguous() and
+            gate_up.is_contiguous() and down.is_contiguous() and _out_ok(out, out_dtype, xs, dev) and
+            (workspace is None or (workspace.get_device() == dev and workspace.is_contiguous())) and
+            _flags_ok(status, dev)):
+        if dev >= 0:
+            moe_w4a16_workspace_bytes(xs[0], xs[-1], gs[0], inter, ks[-1])   # sizes that no call takes
+        _refuse_picked(x, ids, weights, gate_up, down, inter, out, out_dtype, workspace, status)
+    (t, h), e, top_k = xs, gs[0], ks[1]
+    if workspace is None:
+        ws_bytes = lib.qg_moe_w4a16_workspace_bytes(t, h, e, inter, top_k)
+        if ws_bytes < 0:
+            _check(ws_bytes, "qg_moe_w4a16_picked")
+        workspace = torch.empty(ws_bytes, dtype=torch.uint8, device=x.device)
+    else:
+        ws_bytes = workspace.numel() * workspace.element_size()
+    if out is None:
+        out = torch.empty_like(x, dtype=out_dtype)
+    call = lib.qg_moe_w4a16_picked if _current() == dev else _elsewhere(dev, lib.qg_moe_w4a16_picked)
+    st = call(x.data_ptr(), t, h, ids.data_ptr(), weights.data_ptr(), e, gate_up.data_ptr(), gate_up.numel(),
+              down.data_ptr(), down.numel(), inter, top_k, out.data_ptr(), od, workspace.data_ptr(), ws_bytes,
+              _ptr(status), _stream_of(dev))
+    if st:
+        _check(st, "qg_moe_w4a16_picked")
+    return out

@@ -20,7 +20,8 @@ hipError_t launch_attn_kv8(const Kv8Args& c, const void* q, int64_t q_ts, int64_
 int64_t moe_ws_bytes(int64_t t, int64_t h, int64_t e, int64_t inter, int64_t k);
 hipError_t launch_moe_w4a16(const void* x, int t, int h, const void* router, int e, const void* gate_up,
                             int64_t gate_up_bytes, const void* down, int64_t down_bytes, int inter, int k, int renorm,
-                            void* y, int y_f32, void* ws, hipStream_t stream);
+                            void* y, int y_f32, void* ws, const int32_t* ids, const float* weights, uint32_t* status,
+                            hipStream_t stream);
 }  // namespace qg
 
 namespace {
@@ -96,6 +97,20 @@ int32_t moe_shape(int64_t t, int64_t h, int64_t e, int64_t inter, int64_t k) {
   if (e < 1 || e > kMaxExperts || k < 1 || k > kMaxPicks || k > e) return QG_E_SHAPE;
   if (h % QG_TILE_K != 0 || inter % QG_TILE_K != 0) return QG_E_K_MULTIPLE;
   return t > QG_MAX_M ? QG_E_M_RANGE : QG_OK;
+}
+
+// The rules that both layers share.
+int32_t moe_check(const void* x, int64_t t, int64_t h, int64_t e, const void* gate_up, int64_t gate_up_bytes,
+                  const void* down, int64_t down_bytes, int64_t inter, int64_t k, const void* y, int32_t y_dtype,
+                  const void* ws) {
+  const int32_t st = moe_shape(t, h, e, inter, k);
+  if (st != QG_OK) return st;
+  if (y_dtype != QG_BF16 && y_dtype != QG_F32) return QG_E_DTYPE;
+  if (gate_up_bytes < e * qg_int4_packed_bytes(2 * inter, h) || down_bytes < e * qg_int4_packed_bytes(h, inter))
+    return QG_E_BUFFER;
+  if (!aligned(x, 16) || !aligned(gate_up, 16) || !aligned(down, 16) || !aligned(y, 16) || !aligned(ws, 16))
+    return QG_E_ALIGN;
+  return QG_OK;
 }
 
 }  // namespace
@@ -208,19 +223,31 @@ int64_t qg_moe_w4a16_workspace_bytes(int64_t t, int64_t h, int64_t e, int64_t in
 int32_t qg_moe_w4a16(const void* x_bf16, int64_t t, int64_t h, const void* router_bf16, int64_t e, const void* gate_up,
                      int64_t gate_up_bytes, const void* down, int64_t down_bytes, int64_t inter, int64_t top_k,
                      int32_t renormalize, void* y, int32_t y_dtype, void* ws, int64_t ws_bytes, void* stream) {
-  const int32_t st = moe_shape(t, h, e, inter, top_k);
+  const int32_t st = moe_check(x_bf16, t, h, e, gate_up, gate_up_bytes, down, down_bytes, inter, top_k, y, y_dtype, ws);
   if (st != QG_OK) return st;
-  if (y_dtype != QG_BF16 && y_dtype != QG_F32) return QG_E_DTYPE;
-  const int64_t gu = qg_int4_packed_bytes(2 * inter, h), dn = qg_int4_packed_bytes(h, inter);
-  if (gate_up_bytes < e * gu || down_bytes < e * dn) return QG_E_BUFFER;
-  if (!aligned(x_bf16, 16) || !aligned(router_bf16, 16) || !aligned(gate_up, 16) || !aligned(down, 16) ||
-      !aligned(y, 16) || !aligned(ws, 16))
-    return QG_E_ALIGN;
+  if (!aligned(router_bf16, 16)) return QG_E_ALIGN;
   if (t == 0) return QG_OK;
   if (!x_bf16 || !router_bf16 || !gate_up || !down || !y || !ws) return QG_E_NULL;
   if (ws_bytes < qg::moe_ws_bytes(t, h, e, inter, top_k)) return QG_E_BUFFER;
-  return hip_status(qg::launch_moe_w4a16(x_bf16, (int)t, (int)h, router_bf16, (int)e, gate_up, gu, down, dn,
-                                         (int)inter, (int)top_k, renormalize != 0, y, y_dtype == QG_F32, ws,
+  return hip_status(qg::launch_moe_w4a16(x_bf16, (int)t, (int)h, router_bf16, (int)e, gate_up,
+                                         qg_int4_packed_bytes(2 * inter, h), down, qg_int4_packed_bytes(h, inter),
+                                         (int)inter, (int)top_k, renormalize != 0, y, y_dtype == QG_F32, ws, nullptr,
+                                         nullptr, nullptr, static_cast<hipStream_t>(stream)));
+}
+
+int32_t qg_moe_w4a16_picked(const void* x_bf16, int64_t t, int64_t h, const int32_t* ids, const float* weights,
+                            int64_t e, const void* gate_up, int64_t gate_up_bytes, const void* down,
+                            int64_t down_bytes, int64_t inter, int64_t top_k, void* y, int32_t y_dtype, void* ws,
+                            int64_t ws_bytes, uint32_t* status_dev, void* stream) {
+  const int32_t st = moe_check(x_bf16, t, h, e, gate_up, gate_up_bytes, down, down_bytes, inter, top_k, y, y_dtype, ws);
+  if (st != QG_OK) return st;
+  if (!aligned(ids, 4) || !aligned(weights, 4) || !aligned(status_dev, 4)) return QG_E_ALIGN;
+  if (t == 0) return QG_OK;
+  if (!x_bf16 || !ids || !weights || !gate_up || !down || !y || !ws) return QG_E_NULL;
+  if (ws_bytes < qg::moe_ws_bytes(t, h, e, inter, top_k)) return QG_E_BUFFER;
+  return hip_status(qg::launch_moe_w4a16(x_bf16, (int)t, (int)h, nullptr, (int)e, gate_up,
+                                         qg_int4_packed_bytes(2 * inter, h), down, qg_int4_packed_bytes(h, inter),
+                                         (int)inter, (int)top_k, 0, y, y_dtype == QG_F32, ws, ids, weights, status_dev,
                                          static_cast<hipStream_t>(stream)));
 }
 

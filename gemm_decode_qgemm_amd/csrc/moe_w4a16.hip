@@ -1,5 +1,6 @@
 // moe_w4a16.hip -- a whole mixture-of-experts layer for up to 64 tokens on
-// packed INT4 group-32 experts (qg_moe_w4a16).
+// packed INT4 group-32 experts (qg_moe_w4a16), or its experts' part alone, on picks and
+// weights that come with the call (qg_moe_w4a16_picked).
 //
 //   l = x Wr^T;  the top k experts of a token (ties: the lowest index);
 //   p = softmax over the picked logits, or over all of them;
@@ -66,6 +67,9 @@ struct MoeArgs {
   float* part;                        // [t * k, h]
   void* y;
   int y_f32;
+  const int32_t* ids;                 // [t * k] picks that come with the call, or null
+  const float* weights;               // [t * k] and their weights
+  uint32_t* status;
 };
 
 // ---- router ---------------------------------------------------------------
@@ -261,6 +265,44 @@ __global__ __launch_bounds__(512) void moe_route_kernel(MoeArgs a) {
   }
 }
 
+// Picks that come with the call, in place of the launch above; the last workgroup
+// goes over those that name no expert, or one that an earlier pick of the token
+// names: they get expert -1 and count for nothing.
+__device__ __forceinline__ bool moe_repeated(const MoeArgs& a, int t, int j, int id) {
+  for (int o = 0; o < j; ++o)
+    if (a.ids[t * a.k + o] == id) return true;
+  return false;
+}
+
+__global__ __launch_bounds__(512) void moe_given_kernel(MoeArgs a) {
+  __shared__ int rank[64];
+  const int tid = threadIdx.x, lane = tid & 63, wave = wave_id_uniform();
+  const int expert = blockIdx.x;
+  if (expert == a.e) {
+    for (int slot = tid; slot < a.t * a.k; slot += 512) {
+      const int t = slot / a.k, id = a.ids[slot];
+      const bool none = id < 0 || id >= a.e || moe_repeated(a, t, slot - t * a.k, id);
+      if (none) a.expert_of[slot] = -1;
+      if (none && id >= 0 && a.status) atomicOr(a.status, QG_FLAG_INDEX);
+    }
+    return;
+  }
+  for (int t = wave; t < a.t; t += 8) {
+    const uint64_t has = __ballot(lane < a.k && a.ids[t * a.k + min(lane, a.k - 1)] == expert);
+    if (lane == 0) rank[t] = has != 0 ? __builtin_ctzll(has) : a.k;
+  }
+  __syncthreads();
+  if (wave != 0) return;
+  const bool sel = lane < a.t && rank[lane < a.t ? lane : 0] < a.k;
+  const uint64_t mask = __ballot(sel);
+  if (lane == 0) a.count[expert] = __popcll(mask);
+  if (sel) {
+    const int slot = lane * a.k + rank[lane];
+    a.list[expert * 64 + __popcll(mask & (((uint64_t)1 << lane) - 1))] = slot;
+    a.expert_of[slot] = expert;
+  }
+}
+
 // The expert of a unit after the route launch: the unit-th that has tokens, or -1.
 __device__ __forceinline__ int moe_active(const MoeArgs& a, int unit, int& n) {
   const int lane = threadIdx.x & 63;
@@ -448,10 +490,22 @@ __global__ __launch_bounds__(1024) __attribute__((amdgpu_waves_per_eu(8))) void 
   const int tid = threadIdx.x, lane = tid & 63, wave = wave_id_uniform();
   const int blk = wave >> 3, kw = wave & 7;
   const int tile = blockIdx.x, pick = blockIdx.y;
-  const int expert = moe_plan(a, pick, sh.plan);
-  if (tile == 0 && tid == 0) {
-    a.expert_of[pick] = expert;
-    a.picked[pick] = a.logits[expert];
+  int expert;
+  if (a.ids) {
+    const int id = a.ids[pick];
+    const bool none = id < 0 || id >= a.e || moe_repeated(a, 0, pick, id);
+    expert = none ? -1 : id;
+    if (tile == 0 && tid == 0) {
+      a.expert_of[pick] = expert;
+      if (none && id >= 0 && a.status) atomicOr(a.status, QG_FLAG_INDEX);
+    }
+    if (none) return;                // uniform
+  } else {
+    expert = moe_plan(a, pick, sh.plan);
+    if (tile == 0 && tid == 0) {
+      a.expert_of[pick] = expert;
+      a.picked[pick] = a.logits[expert];
+    }
   }
   __syncthreads();                   // the plan's LDS becomes the waves' slots
   const int rb = (tile >> 1) + blk * (a.inter >> 6);
@@ -473,6 +527,7 @@ __global__ __launch_bounds__(1024) __attribute__((amdgpu_waves_per_eu(8))) void 
 // The softmax denominator of a token's picks, relative to its first logit.
 __device__ __forceinline__ float moe_total(const MoeArgs& a, int t, const float* l) {
   float total = 0.0f;
+  if (a.weights) return total;
   if (a.renorm) {
     for (int j = 0; j < a.k; ++j) total += expf(l[j] - l[0]);
   } else {
@@ -481,6 +536,11 @@ __device__ __forceinline__ float moe_total(const MoeArgs& a, int t, const float*
     for (int o = 1; o < 64; o *= 2) total += __shfl_xor(total, o);
   }
   return total;
+}
+
+// The weight of a token's j-th pick.
+__device__ __forceinline__ float moe_weight(const MoeArgs& a, int t, int j, const float* l, float total) {
+  return a.weights ? a.weights[t * a.k + j] : expf(l[j] - l[0]) / total;
 }
 
 // Up to 4 tokens: 16 rows of a token's output through all its picks, 16 waves
@@ -507,7 +567,7 @@ __global__ __launch_bounds__(1024) __attribute__((amdgpu_waves_per_eu(8))) void 
   const float* const picked = a.picked + token * a.k;
   const float total = moe_total(a, token, picked);
   if (tid < a.k) {
-    p[tid] = expf(picked[tid] - picked[0]) / total;
+    p[tid] = moe_weight(a, token, tid, picked, total);
     expert[tid] = a.expert_of[token * a.k + tid];
   }
   __syncthreads();
@@ -523,8 +583,9 @@ __global__ __launch_bounds__(1024) __attribute__((amdgpu_waves_per_eu(8))) void 
   float acc = 0.0f;
   for (int u = wave; u < a.k * kt_count; u += 16) {
     const int j = __builtin_amdgcn_readfirstlane(u / kt_count), kt = u - j * kt_count;
-    const BufView v(a.down + __builtin_amdgcn_readfirstlane(expert[j]) * a.down_bytes + block + (size_t)kt * kTileBytes,
-                    kTileBytes);
+    const int e = __builtin_amdgcn_readfirstlane(expert[j]);
+    if (e < 0) continue;             // a pick that counts for nothing
+    const BufView v(a.down + e * a.down_bytes + block + (size_t)kt * kTileBytes, kTileBytes);
     u32x4_t w[2];
     uint32_t sc[2];
 #pragma unroll
@@ -874,15 +935,17 @@ __global__ __launch_bounds__(256) void moe_combine_kernel(MoeArgs a) {
   const float total = moe_total(a, t, l);
   if (c >= a.h) return;
   f32x4_t y = {0.0f, 0.0f, 0.0f, 0.0f};
+  const int32_t* const of = a.expert_of + (size_t)t * a.k;
 #pragma unroll
   for (int j = 0; j < 8; ++j) {
-    if (j >= a.k) continue;
-    const float p = expf(l[j] - l[0]) / total;
+    if (j >= a.k || (a.ids && of[j] < 0)) continue;
+    const float p = moe_weight(a, t, j, l, total);
 #pragma unroll
     for (int e = 0; e < 4; ++e) y[e] = __builtin_fmaf(p, first[j][e], y[e]);
   }
   for (int j = 8; j < a.k; ++j) {
-    const float p = expf(l[j] - l[0]) / total;
+    if (a.ids && of[j] < 0) continue;
+    const float p = moe_weight(a, t, j, l, total);
     const f32x4_t v = *reinterpret_cast<const f32x4_t*>(part + (size_t)j * a.h);
 #pragma unroll
     for (int e = 0; e < 4; ++e) y[e] = __builtin_fmaf(p, v[e], y[e]);
@@ -905,8 +968,10 @@ int64_t moe_ws_bytes(int64_t t, int64_t h, int64_t e, int64_t inter, int64_t k) 
 
 hipError_t launch_moe_w4a16(const void* x, int t, int h, const void* router, int e, const void* gate_up,
                             int64_t gate_up_bytes, const void* down, int64_t down_bytes, int inter, int k, int renorm,
-                            void* y, int y_f32, void* ws, hipStream_t stream) {
+                            void* y, int y_f32, void* ws, const int32_t* ids, const float* weights, uint32_t* status,
+                            hipStream_t stream) {
   MoeArgs a{};
+  a.ids = ids, a.weights = weights, a.status = status;
   a.x = static_cast<const uint16_t*>(x);
   a.router = static_cast<const uint16_t*>(router);
   a.gate_up = static_cast<const uint8_t*>(gate_up);
@@ -935,9 +1000,9 @@ hipError_t launch_moe_w4a16(const void* x, int t, int h, const void* router, int
   // that a CU holds (64 tokens on 8 experts, h 4096: 48.2 us in all against 51.7; 17 on
   // 64, 2048: 50.6 against 52.8; 64 on 128, 2048 workgroups: 95 both; 64 on 160, 2560: 65
   // against 63.5).
-  if (e * ((t + 3) / 4) <= 8 * kCUs)
+  if (ids == nullptr && e * ((t + 3) / 4) <= 8 * kCUs)
     hipLaunchKernelGGL(moe_router_gemv_kernel, dim3(e, (t + 3) / 4), dim3(256), 0, stream, a);
-  else
+  else if (ids == nullptr)
     hipLaunchKernelGGL(moe_router_mfma_kernel, dim3((e + 15) / 16, (t + 15) / 16), dim3(1024), 0, stream, a);
   if (!ok()) return st;
   if (t == 1) {
@@ -961,9 +1026,13 @@ hipError_t launch_moe_w4a16(const void* x, int t, int h, const void* router, int
   // 30.7 against 32.7; 7, 8 of 128 of 768 x 4096, 1344: 64.8 against 63.5; 5, 4 of 16 of
   // 10496 x 2048, 6560: 107 against 89; else: 8, 4 of 8 of 4096 x 2048, 512: 38.1 against
   // 39.3; of 5120, 640: 49.0 against 48.0).
-  a.own = t <= kOwnTokens && inter / (thin ? 32 : 64) * (a.direct ? e : t * k) <= (thin ? 4 : 2) * kCUs;
+  // Picks that come with the call are listed by a launch, which the router's makes up for.
+  a.own = ids == nullptr && t <= kOwnTokens && inter / (thin ? 32 : 64) * (a.direct ? e : t * k) <= (thin ? 4 : 2) * kCUs;
   const int units = a.direct || (!a.own && t * k > e) ? e : t * k;
-  if (!a.own) {
+  if (ids != nullptr) {
+    hipLaunchKernelGGL(moe_given_kernel, dim3(e + 1), dim3(512), 0, stream, a);
+    if (!ok()) return st;
+  } else if (!a.own) {
     hipLaunchKernelGGL(moe_route_kernel, dim3(e), dim3(512), 0, stream, a);
     if (!ok()) return st;
   }

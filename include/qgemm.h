@@ -514,6 +514,20 @@ int32_t qg_moe_w4a16(const void *x_bf16, int64_t t, int64_t h, const void *route
                      int64_t inter, int64_t top_k, int32_t renormalize, void *y, int32_t y_dtype, void *ws,
                      int64_t ws_bytes, void *stream);
 
+/* ---- qg_moe_w4a16_picked -------------------------------------------------
+ * The experts' part of qg_moe_w4a16 on picks and weights that come with the call
+ * (qg_moe_route, or the caller's):
+ *   y = sum over the picks j of weights[t][j] * down_e . (silu(gate_e x) * (up_e x)),  e = ids[t][j]
+ *   ids      in : int32 [t, top_k];  weights in : fp32 [t, top_k]
+ *   status_dev  : QG_FLAG_INDEX; may be NULL
+ * A negative id is no pick.  One of e or more, or one that an earlier pick of the same
+ * token has, counts for nothing and sets QG_FLAG_INDEX.  Other arguments, workspace
+ * and errors as qg_moe_w4a16. */
+int32_t qg_moe_w4a16_picked(const void *x_bf16, int64_t t, int64_t h, const int32_t *ids, const float *weights,
+                            int64_t e, const void *gate_up, int64_t gate_up_bytes, const void *down,
+                            int64_t down_bytes, int64_t inter, int64_t top_k, void *y, int32_t y_dtype,
+                            void *ws, int64_t ws_bytes, uint32_t *status_dev, void *stream);
+
 /* ==========================================================================
  * Operators of a serving step beside the linears.  The conventions above
  * hold.

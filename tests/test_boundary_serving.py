@@ -135,6 +135,23 @@ def test_w4a8_rows_refusals(kw, want):
     assert rows(**kw) == want
 
 
+def picked(**kw):
+    a = dict(x=A, t=3, h=512, ids=A, weights=A, e=8, gu=A, gu_bytes=8 * 2 * 256 // 64 * 2 * 9472, dn=A, dn_bytes=8 * 8 * 9472, inter=256, k=2,
+             y=A, dt=0, ws=A, ws_bytes=1 << 30, status=None, stream=None)
+    assert set(kw) <= set(a)
+    return lib.qg_moe_w4a16_picked(*(a | kw).values())
+
+
+@pytest.mark.parametrize("kw,want", [
+    (dict(x=None), E_NULL), (dict(ids=None), E_NULL), (dict(weights=None), E_NULL), (dict(gu=None), E_NULL), (dict(dn=None), E_NULL), (dict(y=None), E_NULL),
+    (dict(ws=None), E_NULL), (dict(t=-1), E_SHAPE), (dict(t=65), E_M), (dict(h=500), -3), (dict(inter=128), -3), (dict(e=513), E_SHAPE), (dict(k=9), E_SHAPE),
+    (dict(dt=3), E_DTYPE), (dict(gu_bytes=8 * 8 * 2 * 9472 - 1), E_BUF), (dict(dn_bytes=8 * 8 * 9472 - 1), E_BUF), (dict(ws_bytes=100), E_BUF),
+    (dict(x=U), E_ALIGN), (dict(ids=A + 2), E_ALIGN), (dict(weights=A + 1), E_ALIGN), (dict(gu=U), E_ALIGN), (dict(dn=U), E_ALIGN), (dict(y=U), E_ALIGN),
+    (dict(ws=U), E_ALIGN), (dict(status=A + 2), E_ALIGN), (dict(t=0), OK)])
+def test_moe_picked_refusals(kw, want):
+    assert picked(**kw) == want
+
+
 def test_wrappers_refuse_host_tensors_and_wrong_types():
     x, w = torch.zeros(2, 64, dtype=torch.bfloat16), torch.zeros(64, dtype=torch.bfloat16)
     with pytest.raises(ValueError, match="device"):
