@@ -1,13 +1,21 @@
 """One decoder layer of quantized linears, from prompt to decode.
 
     python examples/decoder_layer.py [--batch 8] [--prompt 100] [--steps 16] [--graph]
+                                     [--adapters 3] [--groups 4] [--act8] [--drafts 3]
 
-Every step runs on this library: the INT4 linears around attention
-(qgemm_w4a16), the norm and rotation of query and key heads (qk_norm_rope), the
-8-bit paged cache and attention over it (kv8_append, attn_kv8), and an INT4
-mixture of experts (moe_w4a16).  Prompts are fed in chunks of at most 64 rows,
-then one token per sequence and step; with --graph the decode step is captured
-once and replayed.  Weights are random.
+Every step runs on this library: the norms with the residual's addition
+(rms_norm), the INT4 linears around attention (qgemm_w4a16), the norm and
+rotation of query and key heads (qk_norm_rope), the 8-bit paged cache and attention
+over it (kv8_append, attn_kv8), and an INT4 mixture of experts (moe_w4a16).
+Prompts are fed in chunks of at most 64 rows, then one token per sequence and step;
+with --graph the decode step is captured once and replayed.  Weights are random.
+
+--adapters: the sequences' own low-rank adapters beside both projections (lora_add),
+some sequences without one.  --groups: experts chosen by biased sigmoid scores
+within the best half of that many groups (moe_route, moe_w4a16_picked).  --act8: the
+first projection on 8-bit rows (rms_norm_q8, qgemm_w4a8_rows).  --drafts: every step
+verifies that many drafted tokens a sequence against the probabilities of an INT4
+head (verify_drafts), and the cache keeps the accepted ones.
 """
 from __future__ import annotations
 
@@ -35,8 +43,8 @@ def rotation_table(positions: int, rot: int, device) -> torch.Tensor:
 class DecoderLayer:
     """Weights, cache and buffers of one layer for `batch` sequences of up to `max_len` tokens."""
 
-    def __init__(self, batch, max_len, *, hidden=1024, hq=16, hkv=4, d=64, experts=16, top_k=4, inter=512, seed=0,
-                 device="cuda"):
+    def __init__(self, batch, max_len, *, hidden=1024, hq=16, hkv=4, d=64, experts=16, top_k=4, inter=512, adapters=0,
+                 rank=8, groups=1, act8=False, seed=0, device="cuda"):
         if not 1 <= batch <= qg.binding.MAX_M:
             raise ValueError(f"a step has a row for every sequence and the linears take 1 to {qg.binding.MAX_M}, got {batch}")
         g = torch.Generator(device=device).manual_seed(seed)
@@ -60,6 +68,19 @@ class DecoderLayer:
         self.table = torch.randperm(batch * width, generator=g, device=device).to(torch.int32).view(batch, width)
         self.lens = torch.zeros(batch, dtype=torch.int32, device=device)
         self.max_len = max_len
+        self.act8, self.groups = act8, groups
+        self.bias = 0.1 * torch.randn(experts, generator=g, device=device) if groups > 1 else None
+        self.lora, self.ids, self.lora_scales = {}, None, None
+        if adapters:
+            for name, n, k in (("qkv", (hq + 2 * hkv) * d, hidden), ("o", hidden, hq * d)):
+                self.lora[name] = (torch.stack([weight(rank, k) for _ in range(adapters)]),
+                                   torch.stack([weight(n, rank) for _ in range(adapters)]))
+            self.lora_scales = 0.5 + torch.rand(adapters, generator=g, device=device)
+            self.ids = (torch.arange(batch, device=device) % (adapters + 1) - 1).to(torch.int32)   # -1: without one
+
+    def _adapt(self, name: str, y: torch.Tensor, x: torch.Tensor, ids: torch.Tensor | None) -> torch.Tensor:
+        """The rows' adapters beside a projection, over its output."""
+        return y if ids is None else qg.lora_add(y, x, *self.lora[name], ids, scales=self.lora_scales, out=y)
 
     def forward(self, x: torch.Tensor, counts: torch.Tensor, cu: torch.Tensor | None, max_rows: int) -> torch.Tensor:
         """x [rows, hidden]: the next counts[b] tokens of every sequence, row offsets cu
@@ -70,16 +91,31 @@ class DecoderLayer:
         rows = x.shape[0]
         if cu is None:
             positions = (before[:, None] + torch.arange(rows // batch, device=x.device)).flatten().to(torch.int32)
+            ids = None if self.ids is None else self.ids.repeat_interleave(rows // batch)
         else:
             seq = torch.repeat_interleave(torch.arange(batch, device=x.device), counts.long(), output_size=rows)
             positions = (torch.arange(rows, device=x.device) - cu[seq] + before[seq]).to(torch.int32)
-        qkv = qg.qgemm_w4a16(rms(x), self.qkv, (self.hq + 2 * self.hkv) * self.d).unflatten(1, (-1, self.d))
+            ids = None if self.ids is None else self.ids[seq]
+        width = (self.hq + 2 * self.hkv) * self.d
+        if self.act8:
+            codes, scales = qg.rms_norm_q8(x, group_scales=True)
+            qkv = qg.qgemm_w4a8_rows(codes, scales, self.qkv, width)
+            normed = None if ids is None else qg.rms_norm(x)
+        else:
+            normed = qg.rms_norm(x)
+            qkv = qg.qgemm_w4a16(normed, self.qkv, width)
+        qkv = self._adapt("qkv", qkv, normed, ids).unflatten(1, (-1, self.d))
         q, k, v = qkv.split((self.hq, self.hkv, self.hkv), 1)
         q, k = qg.qk_norm_rope(q, k, self.q_norm, self.k_norm, self.cos_sin, positions)
         qg.kv8_append(k, v, self.codes, self.scales, self.table, self.lens, cu=cu, max_new=max_rows)
-        a = qg.attn_kv8(q, self.codes, self.scales, self.table, self.lens, cu=cu, max_q=max_rows, max_len=self.max_len)
-        x = x + qg.qgemm_w4a16(a.flatten(1), self.o, self.hidden)
-        return x + qg.moe_w4a16(rms(x), self.router, self.gate_up, self.down, self.inter, self.top_k)
+        a = qg.attn_kv8(q, self.codes, self.scales, self.table, self.lens, cu=cu, max_q=max_rows, max_len=self.max_len).flatten(1)
+        o = self._adapt("o", qg.qgemm_w4a16(a, self.o, self.hidden), a, ids)
+        normed, x = qg.rms_norm(o, residual=x)
+        if self.groups > 1:
+            chosen, weights = qg.moe_route(normed.float() @ self.router.float().t(), self.top_k, sigmoid=True, bias=self.bias,
+                                           groups=self.groups, top_groups=self.groups // 2, group_best=2)
+            return x + qg.moe_w4a16_picked(normed, chosen, weights, self.gate_up, self.down, self.inter)
+        return x + qg.moe_w4a16(normed, self.router, self.gate_up, self.down, self.inter, self.top_k)
 
     def prompts(self, x: list) -> torch.Tensor:
         """Feeds prompts [n_b, hidden] in chunks of at most 64 rows in all; the last output row of each."""
@@ -100,6 +136,36 @@ class DecoderLayer:
         return torch.stack(last)
 
 
+class Speculator:
+    """Drafted tokens verified by a layer with an embedding and an INT4 head."""
+
+    def __init__(self, layer: DecoderLayer, vocabulary: int = 4096, seed: int = 1):
+        device = layer.router.device
+        g = torch.Generator(device=device).manual_seed(seed)
+        self.layer, self.vocabulary, self.g = layer, vocabulary, g
+        self.embedding = torch.randn(vocabulary, layer.hidden, generator=g, device=device).bfloat16()
+        head = (torch.randn(vocabulary, layer.hidden, generator=g, device=device) * layer.hidden ** -0.5).bfloat16()
+        self.head = qg.quantize_int4_g32(head)
+
+    def probabilities(self, y: torch.Tensor) -> torch.Tensor:
+        return torch.softmax(qg.qgemm_w4a16(qg.rms_norm(y), self.head, self.vocabulary, out_dtype=torch.float32), 1)
+
+    def step(self, last: torch.Tensor, drafts: int) -> tuple:
+        """One step for every sequence: its last token and `drafts` drafted ones (drawn evenly
+        from the vocabulary here; a draft model's otherwise).  (accepted [b], next token [b]);
+        the cache is left with the accepted tokens."""
+        layer, device = self.layer, last.device
+        b, rows = last.shape[0], last.shape[0] * (drafts + 1)
+        tokens = torch.randint(0, self.vocabulary, (b, drafts), generator=self.g, device=device)
+        q = torch.full((b * drafts, self.vocabulary), 1 / self.vocabulary, device=device)
+        x = self.embedding[torch.cat([last[:, None].long(), tokens], 1).flatten()]
+        y = layer.forward(x, torch.full_like(layer.lens, drafts + 1), None, drafts + 1)
+        cu = torch.arange(0, rows + 1, drafts + 1, dtype=torch.int32, device=device)
+        u = torch.rand(b * drafts, generator=self.g, device=device)
+        return qg.verify_drafts(self.probabilities(y), q, tokens.flatten().to(torch.int32), u,
+                                torch.rand(b, generator=self.g, device=device), cu, lens=layer.lens)
+
+
 def prompt_lengths(longest: int, batch: int) -> list:
     """Ragged prompts of at least one token."""
     if longest < 1:
@@ -113,9 +179,15 @@ def main() -> None:
     p.add_argument("--prompt", type=int, default=100)
     p.add_argument("--steps", type=int, default=16)
     p.add_argument("--graph", action="store_true")
+    p.add_argument("--adapters", type=int, default=0)
+    p.add_argument("--groups", type=int, default=1)
+    p.add_argument("--act8", action="store_true")
+    p.add_argument("--drafts", type=int, default=0)
     a = p.parse_args()
+    if a.drafts and (a.graph or a.batch * (a.drafts + 1) > qg.binding.MAX_M):
+        p.error(f"--drafts takes no --graph, and at most {qg.binding.MAX_M} rows a step")
     dev = torch.device("cuda")
-    layer = DecoderLayer(a.batch, a.prompt + a.steps + 8)
+    layer = DecoderLayer(a.batch, a.prompt + a.steps * (a.drafts + 1) + 8, adapters=a.adapters, groups=a.groups, act8=a.act8)
     torch.manual_seed(1)
     x = layer.prompts([torch.randn(n, layer.hidden, device=dev).bfloat16() for n in prompt_lengths(a.prompt, a.batch)])
     one = torch.ones(a.batch, dtype=torch.int32, device=dev)
@@ -130,6 +202,10 @@ def main() -> None:
         with torch.cuda.graph(graph):
             step()
         step = graph.replay
+    if a.drafts:
+        speculator = Speculator(layer)
+        last = torch.zeros(a.batch, dtype=torch.int32, device=dev)
+        step = lambda: last.copy_(speculator.step(last, a.drafts)[1])   # noqa: E731
     step()
     torch.cuda.synchronize()
     t = time.perf_counter()
