@@ -22,7 +22,7 @@
 namespace qg {
 
 constexpr int kPiece = 512;            // tokens, 8 a lane
-constexpr int kMaxPieces = 1024;       // a row's; longer pieces where it has more
+constexpr int kMaxPieces = 1024;       // a row's, 16 a lane of the wave that draws; longer pieces where it has more
 constexpr int kVerifyOnePieces = 256;   // those whose sums one workgroup keeps in LDS
 
 template <bool HALF>
@@ -100,60 +100,81 @@ __device__ __forceinline__ double verify_left(float p, float q) {
 // sums, as they are read best.  Tokens from v on weigh nothing (they are past the
 // end of the view), nor does the one that was rejected where drafts are certain.
 template <bool HALF, bool ORDER>
-__device__ __forceinline__ void verify_load(const VerifyArgs& a, const VerifyRow& r, int64_t j0, float (&p)[8], float (&q)[8]) {
-  constexpr int kSize = HALF ? 2 : 4;
-  const int lane = threadIdx.x & 63;
-  const int bytes = (int)min((int64_t)kPiece, a.v - j0) * kSize;
-  const BufView pv(static_cast<const char*>(a.target) + (r.p + j0) * kSize, bytes);
-  const BufView qv(static_cast<const char*>(r.two ? a.draft : a.target) + (r.two ? (r.q + j0) * kSize : 0), r.two ? bytes : 0);
-  const bool order = ORDER || a.whole;
-  if (a.whole) {                         // rows start on 16 bytes and end so: 16 bytes are all there or not
-    if constexpr (HALF) {
-      const u32x4_t w = pv.b128<false>(16 * lane), x = qv.b128<false>(16 * lane);
+struct VerifyEight {
+  typedef uint32_t u32x8_t __attribute__((ext_vector_type(8)));
+  u32x8_t w = {}, x = {};                // p and q as they lie in memory: pairs of bf16 where `whole`
+  __device__ __forceinline__ void load(const VerifyArgs& a, const VerifyRow& r, int64_t j0) {
+    constexpr int kSize = HALF ? 2 : 4;
+    const int lane = threadIdx.x & 63;
+    const int bytes = (int)min((int64_t)kPiece, a.v - j0) * kSize;
+    const BufView pv(static_cast<const char*>(a.target) + (r.p + j0) * kSize, bytes);
+    const BufView qv(static_cast<const char*>(r.two ? a.draft : a.target) + (r.two ? (r.q + j0) * kSize : 0), r.two ? bytes : 0);
+    if (a.whole) {                       // rows start on 16 bytes and end so: 16 bytes are all there or not
 #pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        p[i] = __uint_as_float((i & 1) ? w[i >> 1] & 0xffff0000u : w[i >> 1] << 16);
-        q[i] = __uint_as_float((i & 1) ? x[i >> 1] & 0xffff0000u : x[i >> 1] << 16);
-      }
-    } else {
-      const u32x4_t w0 = pv.b128<false>(32 * lane), w1 = pv.b128<false>(32 * lane + 16);
-      const u32x4_t x0 = qv.b128<false>(32 * lane), x1 = qv.b128<false>(32 * lane + 16);
+      for (int h = 0; h < (HALF ? 1 : 2); ++h) {
+        const u32x4_t p = pv.b128<false>((HALF ? 16 : 32) * lane + 16 * h), q = qv.b128<false>((HALF ? 16 : 32) * lane + 16 * h);
 #pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        p[i] = __uint_as_float(i < 4 ? w0[i & 3] : w1[i & 3]);
-        q[i] = __uint_as_float(i < 4 ? x0[i & 3] : x1[i & 3]);
+        for (int i = 0; i < 4; ++i) w[4 * h + i] = p[i], x[4 * h + i] = q[i];
       }
+    } else {                             // 64 neighbours at a time where the order is free
+      const uint32_t at = kSize * (ORDER ? 8 * lane : lane), step = kSize * (ORDER ? 1 : 64);
+#pragma unroll
+      for (int i = 0; i < 8; ++i) w[i] = HALF ? pv.b16(at + i * step) : pv.b32(at + i * step);
+#pragma unroll
+      for (int i = 0; i < 8; ++i) x[i] = HALF ? qv.b16(at + i * step) : qv.b32(at + i * step);
     }
-  } else {                               // 64 neighbours at a time where the order is free
-    const uint32_t at = kSize * (ORDER ? 8 * lane : lane), step = kSize * (ORDER ? 1 : 64);
-    uint32_t w[8], x[8];
-#pragma unroll
-    for (int i = 0; i < 8; ++i) w[i] = HALF ? pv.b16(at + i * step) << 16 : pv.b32(at + i * step);
-#pragma unroll
-    for (int i = 0; i < 8; ++i) x[i] = HALF ? qv.b16(at + i * step) << 16 : qv.b32(at + i * step);
-#pragma unroll
-    for (int i = 0; i < 8; ++i) p[i] = __uint_as_float(w[i]), q[i] = __uint_as_float(x[i]);
   }
-  if (r.without >= j0 && r.without < j0 + kPiece) {
-    const int not_it = (int)(r.without - j0);
+  __device__ __forceinline__ void values(const VerifyArgs& a, const VerifyRow& r, int64_t j0, float (&p)[8], float (&q)[8]) const {
+    const int lane = threadIdx.x & 63;
+    const bool order = ORDER || a.whole;
+    // (bf16 in pairs are taken apart here: w[4 ..] is not loaded then)
+    const bool pairs = HALF && a.whole;
+    const uint32_t odd = 0xffff0000u;
 #pragma unroll
-    for (int i = 0; i < 8; ++i)
-      if ((order ? 8 * lane + i : 64 * i + lane) == not_it) p[i] = 0.0f;
+    for (int i = 0; i < 4; ++i) {
+      uint32_t w0 = w[2 * i], w1 = w[2 * i + 1], x0 = x[2 * i], x1 = x[2 * i + 1];
+      if constexpr (HALF) w0 <<= 16, w1 <<= 16, x0 <<= 16, x1 <<= 16;
+      if (pairs) w0 = w[i] << 16, w1 = w[i] & odd, x0 = x[i] << 16, x1 = x[i] & odd;
+      p[2 * i] = __uint_as_float(w0), p[2 * i + 1] = __uint_as_float(w1);
+      q[2 * i] = __uint_as_float(x0), q[2 * i + 1] = __uint_as_float(x1);
+    }
+    if (r.without >= j0 && r.without < j0 + kPiece) {
+      const int not_it = (int)(r.without - j0);
+#pragma unroll
+      for (int i = 0; i < 8; ++i)
+        if ((order ? 8 * lane + i : 64 * i + lane) == not_it) p[i] = 0.0f;
+    }
   }
-}
+};
 
-// The sum of a piece.
-template <bool HALF>
-__device__ __forceinline__ double verify_sum(const VerifyArgs& a, const VerifyRow& r, int64_t piece) {
+// The sums of the pieces first, first + step, ... below a.pieces, each given to
+// take(piece, sum); the loads of the next 512 tokens are in flight while these are added.
+template <bool HALF, class Take>
+__device__ __forceinline__ void verify_sums(const VerifyArgs& a, const VerifyRow& r, int first, int step, Take take) {
+  if (first >= a.pieces) return;
+  VerifyEight<HALF, false> now, next;
+  int64_t j0 = first * a.piece;
+  now.load(a, r, j0);
   double sum = 0.0;
 #pragma unroll 1
-  for (int64_t j0 = piece * a.piece; j0 < min(a.v, (piece + 1) * a.piece); j0 += kPiece) {
+  for (int i = first; i < a.pieces;) {
+    const int64_t end = min(a.v, (i + 1) * a.piece);
+    const bool last = j0 + kPiece >= end;
+    const int at = last ? i + step : i;
+    const int64_t then = last ? at * a.piece : j0 + kPiece;
+    if (at < a.pieces) next.load(a, r, then);
     float p[8], q[8];
-    verify_load<HALF, false>(a, r, j0, p, q);
+    now.values(a, r, j0, p, q);
 #pragma unroll
-    for (int i = 0; i < 8; ++i) sum += verify_left(p[i], q[i]);
+    for (int k = 0; k < 8; ++k) sum += verify_left(p[k], q[k]);
+    if (last) {
+      take(i, wave_sum(sum));
+      sum = 0.0;
+    }
+    i = at;
+    j0 = then;
+    now = next;
   }
-  return wave_sum(sum);
 }
 
 // x of a whole of which 2^e is a share of 2^61 or more; one at least.
@@ -165,28 +186,33 @@ __device__ __forceinline__ uint64_t verify_border(double x, int e) {
   return y > 0.0 ? (y < 0x1p63 ? (uint64_t)y : (uint64_t)1 << 63) : 0;
 }
 
-// The token that u falls on, by a whole wave; part[i]: the sum of piece i.  -1 where
-// the row has no finite sum above zero.
-template <bool HALF>
-__device__ __forceinline__ int verify_draw(const VerifyArgs& a, VerifyRow& r, double u, double* part) {
+// The token that u falls on, by a whole wave; part[i]: the sum of piece i, up to 64 PER
+// of them.  -1 where the row has no finite sum above zero.
+template <bool HALF, int PER>
+__device__ __forceinline__ int verify_draw(const VerifyArgs& a, VerifyRow& r, double u, const double* part) {
   const int lane = threadIdx.x & 63;
-  const int per = (a.pieces + 63) / 64, i0 = lane * per, i1 = min(a.pieces, i0 + per);
-  double own = 0.0;
-  for (int i = i0; i < i1; ++i) own += part[i];
-  double total = wave_sum(own);
+  const int per = (a.pieces + 63) / 64, i0 = lane * per;
+  double x[PER];                         // this lane's pieces i0 ..
+  auto add = [&] {
+    double own = 0.0;
+#pragma unroll
+    for (int i = 0; i < PER; ++i) own += x[i];
+    return wave_sum(own);
+  };
+#pragma unroll
+  for (int i = 0; i < PER; ++i) x[i] = i < per && i0 + i < a.pieces ? part[i0 + i] : 0.0;
+  double total = add();
   if (total == 0.0 && (r.two || r.without >= 0)) {
     // p nowhere above q: the token comes from p (rows that do not add up to one, or
     // a draft rejected by rounding alone; so seldom that one wave may do it)
     r.two = false;
     r.without = -1;
-#pragma unroll 1
-    for (int i = 0; i < a.pieces; ++i) {
-      const double sum = verify_sum<HALF>(a, r, i);
-      if (i >= i0 && i < i1) part[i] = sum;
-    }
-    own = 0.0;
-    for (int i = i0; i < i1; ++i) own += part[i];
-    total = wave_sum(own);
+    verify_sums<HALF>(a, r, 0, 1, [&](int piece, double sum) {
+#pragma unroll
+      for (int i = 0; i < PER; ++i)
+        if (i < per && piece == i0 + i) x[i] = sum;
+    });
+    total = add();
   }
   const double border = u * total;
   if (!(total > 0.0 && total < __builtin_inf())) return -1;
@@ -194,8 +220,9 @@ __device__ __forceinline__ int verify_draw(const VerifyArgs& a, VerifyRow& r, do
   int e = 62 - __builtin_amdgcn_frexp_exp(total);
   uint64_t all, mine = 0;
   int last = -1;
-  for (int i = i0; i < i1; ++i) {
-    const uint64_t c = verify_count(part[i], e);
+#pragma unroll
+  for (int i = 0; i < PER; ++i) {
+    const uint64_t c = verify_count(x[i], e);
     mine += c;
     if (c != 0) last = i;
   }
@@ -203,34 +230,38 @@ __device__ __forceinline__ int verify_draw(const VerifyArgs& a, VerifyRow& r, do
   uint64_t want = u < 1.0 ? verify_border(border, e) : kLast;
   uint64_t run = wave_before(mine, all);
   int at = last;
-  double base = 0.0;                   // this lane's part of the sum before the piece
   uint64_t hit;
   if (want < all) {
-    const bool here = run <= want && want < run + mine;
-    hit = __ballot(here);
-    if (here) {
-      for (int i = i0; i < i1; ++i) {
-        run += verify_count(part[i], e);
-        at = i;
-        if (run > want) break;
-      }
+    hit = __ballot(run <= want && want < run + mine);
+    bool found = false;
+#pragma unroll
+    for (int i = 0; i < PER; ++i) {
+      run += verify_count(x[i], e);
+      if (!found && run > want) at = i, found = true;
     }
-  } else {                             // by rounding, or kLast
-    const uint64_t some = __ballot(last >= 0);
-    hit = (uint64_t)1 << (63 - __builtin_clzll(some));
+  } else {                               // by rounding, or kLast
+    hit = (uint64_t)1 << (63 - __builtin_clzll(__ballot(last >= 0)));
   }
-  const int piece = __builtin_amdgcn_readlane(at, __builtin_ctzll(hit));
-  for (int i = i0; i < min(i1, piece); ++i) base += part[i];
+  const int winner = __builtin_ctzll(hit), place = __builtin_amdgcn_readlane(at, winner);
+  double base = 0.0, own = 0.0;          // the sum before the piece; the piece's
+#pragma unroll
+  for (int i = 0; i < PER; ++i) {
+    if (lane < winner || (lane == winner && i < place)) base += x[i];
+    if (i == place) own = x[i];
+  }
   const double rest = border - wave_sum(base);
   // the token in it
-  e = 62 - __builtin_amdgcn_frexp_exp(part[piece]);
+  e = 62 - __builtin_amdgcn_frexp_exp(lane_of(own, winner));
   want = u < 1.0 ? verify_border(rest, e) : kLast;
   uint64_t before = 0;
-  int token = -1;                      // this lane's last one with a share
+  int token = -1;                        // this lane's last one with a share
+  const int64_t piece = (int64_t)winner * per + place;
 #pragma unroll 1
-  for (int64_t j0 = (int64_t)piece * a.piece; j0 < min(a.v, (int64_t)(piece + 1) * a.piece); j0 += kPiece) {
+  for (int64_t j0 = piece * a.piece; j0 < min(a.v, (piece + 1) * a.piece); j0 += kPiece) {
+    VerifyEight<HALF, true> eight;
+    eight.load(a, r, j0);
     float p[8], q[8];
-    verify_load<HALF, true>(a, r, j0, p, q);
+    eight.values(a, r, j0, p, q);
     uint64_t c[8];
     mine = 0;
 #pragma unroll
@@ -240,14 +271,13 @@ __device__ __forceinline__ int verify_draw(const VerifyArgs& a, VerifyRow& r, do
       if (c[i] != 0) token = (int)j0 + 8 * lane + i;
     }
     run = before + wave_before(mine, all);
-    const bool here = run <= want && want < run + mine;
-    hit = __ballot(here);
+    hit = __ballot(run <= want && want < run + mine);
     if (hit != 0) {
       bool found = false;
 #pragma unroll
       for (int i = 0; i < 8; ++i) {
         run += c[i];
-        if (!found && run > want) token = (int)(j0 + 8 * lane + i), found = true;
+        if (!found && run > want) token = (int)j0 + 8 * lane + i, found = true;
       }
       return __builtin_amdgcn_readlane(token, __builtin_ctzll(hit));
     }
@@ -282,14 +312,12 @@ __global__ __launch_bounds__(1024) void verify_one_kernel(VerifyArgs a) {
     return;
   }
   verify_find<HALF>(a, b, r);
-#pragma unroll 1
-  for (int i = wave; i < a.pieces; i += 16) {
-    const double sum = verify_sum<HALF>(a, r, i);
-    if ((threadIdx.x & 63) == 0) part[i] = sum;
-  }
+  verify_sums<HALF>(a, r, wave, 16, [&](int piece, double sum) {
+    if ((threadIdx.x & 63) == 0) part[piece] = sum;
+  });
   __syncthreads();
   if (wave != 0) return;
-  const int token = verify_draw<HALF>(a, r, (double)u, part);
+  const int token = verify_draw<HALF, kVerifyOnePieces / 64>(a, r, (double)u, part);
   if (threadIdx.x != 0) return;
   a.accepted[b] = r.accepted;
   if (r.bad) verify_flag(a, QG_FLAG_INDEX);
@@ -311,15 +339,12 @@ __global__ __launch_bounds__(256) void verify_sums_kernel(VerifyArgs a) {
     a.accepted[b] = r.accepted;
     if (r.bad) verify_flag(a, QG_FLAG_INDEX);
   }
-  const int step = gridDim.x * 4;
-#pragma unroll 1
-  for (int i = blockIdx.x * 4 + wave_id_uniform(); i < a.pieces; i += step) {
-    const double sum = verify_sum<HALF>(a, r, i);
-    if ((threadIdx.x & 63) == 0) a.part[(size_t)b * a.pieces + i] = sum;
-  }
+  verify_sums<HALF>(a, r, blockIdx.x * 4 + wave_id_uniform(), gridDim.x * 4, [&](int piece, double sum) {
+    if ((threadIdx.x & 63) == 0) a.part[(size_t)b * a.pieces + piece] = sum;
+  });
 }
 
-template <bool HALF>
+template <bool HALF, int PER>
 __global__ __launch_bounds__(64) void verify_draw_kernel(VerifyArgs a) {
   const int b = blockIdx.x;
   const int accepted = __builtin_amdgcn_readfirstlane(a.accepted[b]);   // of the launch before, as the sums
@@ -333,7 +358,7 @@ __global__ __launch_bounds__(64) void verify_draw_kernel(VerifyArgs a) {
     return;
   }
   verify_at(a, b, accepted, r);
-  const int token = verify_draw<HALF>(a, r, (double)u, a.part + (size_t)b * a.pieces);
+  const int token = verify_draw<HALF, PER>(a, r, (double)u, a.part + (size_t)b * a.pieces);
   if (threadIdx.x == 0) verify_store(a, b, r, token);
 }
 
@@ -345,8 +370,10 @@ int64_t verify_piece(int64_t v) {
 
 // Whether one workgroup a sequence does it all.
 bool verify_in_one(int64_t b, int64_t v) {
-  // Few tokens, or sequences for every second CU (one of 32000, 7.4 us against 6.7 and a second launch;
-  // 61 of 32768 in bf16, 8.8 against 7.8 and a launch; 64 of 131071, 25 against 18).
+  // A short row, or sequences for every second CU: there one launch takes as long as the
+  // two or less (kernels alone, fp32: one sequence of 32000 7.1 us against 3.6 + 3.0, 64 of
+  // 40000 9.8 against 5.3 + 4.0; in bf16 61 of 32768 9.5 against 4.8 + 4.4; 128 of 131071
+  // 27.3 against 20.4 + 4.7, 256 44.6 against 41.0 + 4.0; but 64 of 131071 27 against 13 + 4).
   if ((v + kPiece - 1) / kPiece > kVerifyOnePieces) return false;
   return v <= 40000 || b >= kCUs / 2;
 }
@@ -377,10 +404,14 @@ hipError_t launch_verify_drafts(VerifyArgs a, hipStream_t stream) {
     hipLaunchKernelGGL((verify_sums_kernel<false>), grid, dim3(256), 0, stream, a);
   const hipError_t st = hipGetLastError();
   if (st != hipSuccess) return st;
-  if (a.half)
-    hipLaunchKernelGGL((verify_draw_kernel<true>), dim3(a.b), dim3(64), 0, stream, a);
+  if (a.half && a.pieces <= 256)
+    hipLaunchKernelGGL((verify_draw_kernel<true, 4>), dim3(a.b), dim3(64), 0, stream, a);
+  else if (a.half)
+    hipLaunchKernelGGL((verify_draw_kernel<true, 16>), dim3(a.b), dim3(64), 0, stream, a);
+  else if (a.pieces <= 256)
+    hipLaunchKernelGGL((verify_draw_kernel<false, 4>), dim3(a.b), dim3(64), 0, stream, a);
   else
-    hipLaunchKernelGGL((verify_draw_kernel<false>), dim3(a.b), dim3(64), 0, stream, a);
+    hipLaunchKernelGGL((verify_draw_kernel<false, 16>), dim3(a.b), dim3(64), 0, stream, a);
   return hipGetLastError();
 }
 
