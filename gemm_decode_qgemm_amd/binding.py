@@ -741,6 +741,8 @@ def moe_w4a16(x: torch.Tensor, router: torch.Tensor, gate_up: torch.Tensor, down
 # ---- operators of a serving step beside the linears ----------------------------
 
 _current = torch._C._cuda_getDevice
+_TYPES = {_BF16: QG_BF16, _F32: QG_F32}
+_DENSE = torch.contiguous_format
 
 
 def _elsewhere(dev: int, fn):
@@ -751,18 +753,13 @@ def _elsewhere(dev: int, fn):
     return call
 
 
-def _float_type(t: torch.Tensor) -> int:
-    """QG_BF16 or QG_F32, or -1."""
-    return QG_BF16 if t.dtype is _BF16 else QG_F32 if t.dtype is _F32 else -1
-
-
 def _refuse_norm(x, weight, residual, residual_out, outs) -> None:
     for name, t in (("x", x), ("residual", residual)):
         if t is None:
             continue
         if not t.is_cuda:
             raise ValueError(f"{name} must be on a CUDA (HIP) device")
-        if _float_type(t) < 0 or t.dim() != 2:
+        if t.dtype not in _TYPES or t.dim() != 2:
             raise ValueError(f"{name} must be bfloat16 or float32 [rows, h], got {t.dtype} of rank {t.dim()}")
         if t.shape[1] > 1 and t.stride(1) != 1:
             raise ValueError(f"{name}: the channels of a row must be contiguous")
@@ -787,20 +784,24 @@ def _refuse_norm(x, weight, residual, residual_out, outs) -> None:
     raise ValueError("rms_norm: arguments that do not fit together")
 
 
-def _norm_args_ok(x, weight, residual, residual_out, dev) -> bool:
-    xs = x.shape
-    return (dev >= 0 and len(xs) == 2 and _float_type(x) >= 0 and (xs[1] <= 1 or x.stride(1) == 1) and
-            (weight is None or (weight.dtype is _BF16 and weight.shape == xs[1:] and weight.get_device() == dev and
-                                weight.is_contiguous())) and
-            (residual_out is None if residual is None else
-             _float_type(residual) >= 0 and residual.shape == xs and residual.get_device() == dev and
-             (xs[1] <= 1 or residual.stride(1) == 1) and
-             (residual_out is None or (residual_out.dtype is residual.dtype and residual_out.shape == xs and
-                                       residual_out.get_device() == dev and residual_out.is_contiguous()))))
+def _norm_args_ok(dev, x, xs, weight, residual, residual_out) -> bool:
+    """The arguments that both norms share."""
+    if dev < 0 or len(xs) != 2 or x.dtype not in _TYPES or x.stride(1) != 1:
+        return False
+    if weight is not None and (weight.dtype is not _BF16 or weight.get_device() != dev or weight.shape != xs[1:] or
+                               not weight.is_contiguous()):
+        return False
+    if residual is None:
+        return residual_out is None
+    if (residual.dtype not in _TYPES or residual.get_device() != dev or residual.shape != xs or
+            residual.stride(1) != 1):
+        return False
+    return residual_out is None or (residual_out.dtype is residual.dtype and residual_out.get_device() == dev and
+                                    residual_out.shape == xs and residual_out.is_contiguous())
 
 
-def _out_ok(t: torch.Tensor | None, dtype: torch.dtype, shape, dev: int) -> bool:
-    return t is None or (t.dtype is dtype and t.shape == shape and t.get_device() == dev and t.is_contiguous())
+def _out_ok(t: torch.Tensor, dtype: torch.dtype, shape, dev: int) -> bool:
+    return t.dtype is dtype and t.shape == shape and t.get_device() == dev and t.is_contiguous()
 
 
 def rms_norm(x: torch.Tensor, weight: torch.Tensor | None = None, *, residual: torch.Tensor | None = None,
@@ -809,22 +810,22 @@ def rms_norm(x: torch.Tensor, weight: torch.Tensor | None = None, *, residual: t
     """RMS norm of the rows of x [rows, h] (bf16 or fp32): y.  With a residual (bf16
     or fp32) the norm of x + residual: (y, x + residual in the residual's type).
     residual_out may be residual itself.  x and residual may be strided views."""
-    dev, od, shape = x.get_device(), _out_type(out_dtype), x.shape
-    if not (_norm_args_ok(x, weight, residual, residual_out, dev) and _out_ok(out, out_dtype, shape, dev)):
+    dev, shape, od = x.get_device(), x.shape, _out_type(out_dtype)
+    if not (_norm_args_ok(dev, x, shape, weight, residual, residual_out) and
+            (out is None or _out_ok(out, out_dtype, shape, dev))):
         _refuse_norm(x, weight, residual, residual_out, [("out", out, out_dtype, shape)])
     if out is None:
-        out = torch.empty_like(x, dtype=out_dtype, memory_format=torch.contiguous_format)
+        out = torch.empty_like(x, dtype=out_dtype, memory_format=_DENSE)
+    call = lib.qg_rms_norm if _current() == dev else _elsewhere(dev, lib.qg_rms_norm)
+    w = None if weight is None else weight.data_ptr()
     if residual is None:
-        call = lib.qg_rms_norm if _current() == dev else _elsewhere(dev, lib.qg_rms_norm)
-        st = call(x.data_ptr(), _float_type(x), x.stride(0), None, 0, 0, shape[0], shape[1], _ptr(weight), eps,
-                  out.data_ptr(), od, None, _stream_of(dev))
+        st = call(x.data_ptr(), _TYPES[x.dtype], x.stride(0), None, 0, 0, *shape, w, eps, out.data_ptr(), od, None,
+                  _stream_of(dev))
     else:
         if residual_out is None:
-            residual_out = torch.empty_like(residual, memory_format=torch.contiguous_format)
-        call = lib.qg_rms_norm if _current() == dev else _elsewhere(dev, lib.qg_rms_norm)
-        st = call(x.data_ptr(), _float_type(x), x.stride(0), residual.data_ptr(), _float_type(residual),
-                  residual.stride(0), shape[0], shape[1], _ptr(weight), eps, out.data_ptr(), od,
-                  residual_out.data_ptr(), _stream_of(dev))
+            residual_out = torch.empty_like(residual, memory_format=_DENSE)
+        st = call(x.data_ptr(), _TYPES[x.dtype], x.stride(0), residual.data_ptr(), _TYPES[residual.dtype],
+                  residual.stride(0), *shape, w, eps, out.data_ptr(), od, residual_out.data_ptr(), _stream_of(dev))
     if st:
         _check(st, "qg_rms_norm")
     return out if residual is None else (out, residual_out)
@@ -839,20 +840,20 @@ def rms_norm_q8(x: torch.Tensor, weight: torch.Tensor | None = None, *, residual
     dev, shape = x.get_device(), x.shape
     wide = shape[:1] if not group_scales else (shape[0], shape[-1] // GROUP)
     codes, scales = out if out is not None else (None, None)
-    if not (_norm_args_ok(x, weight, residual, residual_out, dev) and _out_ok(codes, torch.int8, shape, dev) and
-            _out_ok(scales, _F32, wide, dev)):
+    if not (_norm_args_ok(dev, x, shape, weight, residual, residual_out) and
+            (out is None or (_out_ok(codes, torch.int8, shape, dev) and _out_ok(scales, _F32, wide, dev)))):
         _refuse_norm(x, weight, residual, residual_out, [("codes", codes, torch.int8, shape),
                                                          ("scales", scales, torch.float32, wide)])
     if out is None:
-        codes = torch.empty_like(x, dtype=torch.int8, memory_format=torch.contiguous_format)
-        scales = torch.empty(wide, dtype=_F32, device=x.device)
+        codes = torch.empty_like(x, dtype=torch.int8, memory_format=_DENSE)
+        scales = x.new_empty(wide, dtype=_F32)
     if residual is not None and residual_out is None:
-        residual_out = torch.empty(shape, dtype=residual.dtype, device=x.device)
+        residual_out = torch.empty_like(residual, memory_format=_DENSE)
     call = lib.qg_rms_norm_q8 if _current() == dev else _elsewhere(dev, lib.qg_rms_norm_q8)
-    st = call(x.data_ptr(), _float_type(x), x.stride(0), _ptr(residual),
-              0 if residual is None else _float_type(residual), 0 if residual is None else residual.stride(0),
-              shape[0], shape[1], _ptr(weight), eps, codes.data_ptr(), scales.data_ptr(), group_scales,
-              _ptr(residual_out), _stream_of(dev))
+    st = call(x.data_ptr(), _TYPES[x.dtype], x.stride(0), _ptr(residual),
+              0 if residual is None else _TYPES[residual.dtype], 0 if residual is None else residual.stride(0),
+              *shape, _ptr(weight), eps, codes.data_ptr(), scales.data_ptr(), group_scales, _ptr(residual_out),
+              _stream_of(dev))
     if st:
         _check(st, "qg_rms_norm_q8")
     return (codes, scales) if residual is None else (codes, scales, residual_out)
@@ -872,7 +873,7 @@ def _refuse_lora(y, x, a, b, ids, scales, out, out_dtype, workspace, status) -> 
     for name, t in (("y", y), ("out", out)):
         if t is None:
             continue
-        if not t.is_cuda or _float_type(t) < 0 or t.dim() != 2 or (t.shape[1] > 1 and t.stride(1) != 1):
+        if not t.is_cuda or t.dtype not in _TYPES or t.dim() != 2 or (t.shape[1] > 1 and t.stride(1) != 1):
             raise ValueError(f"{name} must be bfloat16 or float32 [m, n] on a CUDA (HIP) device, columns contiguous")
     if a.shape[2] != x.shape[1] or b.shape[0] != a.shape[0] or b.shape[2] != a.shape[1]:
         raise ValueError("a must be [adapters, r, k] and b [adapters, n, r]")
@@ -902,33 +903,32 @@ def lora_add(y: torch.Tensor, x: torch.Tensor, a: torch.Tensor, b: torch.Tensor,
     dev, ys, xs, as_, bs = x.get_device(), y.shape, x.shape, a.shape, b.shape
     if out_dtype is None:
         out_dtype = y.dtype if out is None else out.dtype
-    if not (dev >= 0 and len(ys) == 2 and len(xs) == 2 and len(as_) == 3 and len(bs) == 3 and x.dtype is _BF16 and
-            a.dtype is _BF16 and b.dtype is _BF16 and ids.dtype is _I32 and _float_type(y) >= 0 and
-            as_[2] == xs[1] and bs[0] == as_[0] and bs[2] == as_[1] and ys == (xs[0], bs[1]) and ids.shape == xs[:1] and
-            (ys[1] <= 1 or y.stride(1) == 1) and y.get_device() == dev and a.get_device() == dev and
+    if not (dev >= 0 and len(ys) == 2 and len(xs) == 2 and len(as_) == 3 and x.dtype is _BF16 and a.dtype is _BF16 and
+            b.dtype is _BF16 and ids.dtype is _I32 and y.dtype in _TYPES and as_[2] == xs[1] and
+            bs == (as_[0], ys[1], as_[1]) and ys[0] == xs[0] and ids.shape == xs[:1] and
+            (y.stride(1) == 1 or ys[1] <= 1) and y.get_device() == dev and a.get_device() == dev and
             b.get_device() == dev and ids.get_device() == dev and x.is_contiguous() and a.is_contiguous() and
             b.is_contiguous() and ids.is_contiguous() and
-            (scales is None or (scales.dtype is _F32 and scales.shape == as_[:1] and scales.get_device() == dev and
-                                scales.is_contiguous())) and
+            (scales is None or _out_ok(scales, _F32, as_[:1], dev)) and
             (out is None or (out.dtype is out_dtype and out.shape == ys and out.get_device() == dev and
-                             (ys[1] <= 1 or out.stride(1) == 1) and
+                             (out.stride(1) == 1 or ys[1] <= 1) and
                              (out.data_ptr() != y.data_ptr() or (out.dtype is y.dtype and out.stride() == y.stride())))) and
             (workspace is None or (workspace.get_device() == dev and workspace.is_contiguous())) and
-            _flags_ok(status, dev)):
+            (status is None or _flags_ok(status, dev))):
         _refuse_lora(y, x, a, b, ids, scales, out, out_dtype, workspace, status)
-    od, (m, k), (adapters, r) = _out_type(out_dtype), xs, as_[:2]
+    od, (m, k), (adapters, r, _), n = _out_type(out_dtype), xs, as_, ys[1]
     if workspace is None:
-        ws_bytes = lib.qg_lora_add_workspace_bytes(m, k, ys[1], r, adapters)
+        ws_bytes = lib.qg_lora_add_workspace_bytes(m, k, n, r, adapters)
         if ws_bytes < 0:
             _check(ws_bytes, "qg_lora_add")
-        workspace = torch.empty(ws_bytes, dtype=torch.uint8, device=x.device)
+        workspace = x.new_empty(ws_bytes, dtype=torch.uint8)
     else:
         ws_bytes = workspace.numel() * workspace.element_size()
     if out is None:
-        out = torch.empty_like(y, dtype=out_dtype, memory_format=torch.contiguous_format)
+        out = torch.empty_like(y, dtype=out_dtype, memory_format=_DENSE)
     call = lib.qg_lora_add if _current() == dev else _elsewhere(dev, lib.qg_lora_add)
     st = call(x.data_ptr(), m, k, a.data_ptr(), b.data_ptr(), r, adapters, ids.data_ptr(), _ptr(scales), y.data_ptr(),
-              _float_type(y), y.stride(0), ys[1], out.data_ptr(), od, out.stride(0), workspace.data_ptr(), ws_bytes,
+              _TYPES[y.dtype], y.stride(0), n, out.data_ptr(), od, out.stride(0), workspace.data_ptr(), ws_bytes,
               _ptr(status), _stream_of(dev))
     if st:
         _check(st, "qg_lora_add")
@@ -938,7 +938,7 @@ def lora_add(y: torch.Tensor, x: torch.Tensor, a: torch.Tensor, b: torch.Tensor,
 def _refuse_route(logits, top_k, bias, out) -> None:
     if not logits.is_cuda:
         raise ValueError("logits must be on a CUDA (HIP) device")
-    if _float_type(logits) < 0 or logits.dim() != 2 or not logits.is_contiguous():
+    if logits.dtype not in _TYPES or logits.dim() != 2 or not logits.is_contiguous():
         raise ValueError("logits must be contiguous bfloat16 or float32 [t, e]")
     if bias is not None:
         _dev(bias, "bias", torch.float32, 1)
@@ -963,20 +963,20 @@ def moe_route(logits: torch.Tensor, top_k: int, *, sigmoid: bool = False, bias: 
     whose best `group_best` (1 or 2) experts sum to most; weights are the picked
     scores, over their sum where renormalized, times `scale`."""
     dev, ls = logits.get_device(), logits.shape
-    shape = (ls[0], top_k)
-    ids, weights = out if out is not None else (None, None)
-    if not (dev >= 0 and len(ls) == 2 and _float_type(logits) >= 0 and logits.is_contiguous() and
-            (bias is None or (bias.dtype is _F32 and bias.shape == ls[1:] and bias.get_device() == dev and
-                              bias.is_contiguous())) and
-            _out_ok(ids, _I32, shape, dev) and _out_ok(weights, _F32, shape, dev)):
+    if not (dev >= 0 and len(ls) == 2 and logits.dtype in _TYPES and logits.is_contiguous() and
+            (bias is None or _out_ok(bias, _F32, ls[1:], dev)) and
+            (out is None or (_out_ok(out[0], _I32, (ls[0], top_k), dev) and _out_ok(out[1], _F32, (ls[0], top_k), dev)))):
         _refuse_route(logits, top_k, bias, out)
+    t, e = ls
     if out is None:
         if top_k < 1:
             _check(-2, "qg_moe_route")
-        ids, weights = logits.new_empty(shape, dtype=_I32), logits.new_empty(shape, dtype=_F32)
+        ids, weights = logits.new_empty((t, top_k), dtype=_I32), logits.new_empty((t, top_k), dtype=_F32)
+    else:
+        ids, weights = out
     call = lib.qg_moe_route if _current() == dev else _elsewhere(dev, lib.qg_moe_route)
-    st = call(logits.data_ptr(), _float_type(logits), ls[0], ls[1], top_k, sigmoid, _ptr(bias), groups, top_groups,
-              group_best, renormalize, scale, ids.data_ptr(), weights.data_ptr(), _stream_of(dev))
+    st = call(logits.data_ptr(), _TYPES[logits.dtype], t, e, top_k, sigmoid, _ptr(bias), groups, top_groups, group_best,
+              renormalize, scale, ids.data_ptr(), weights.data_ptr(), _stream_of(dev))
     if st:
         _check(st, "qg_moe_route")
     return ids, weights
@@ -991,7 +991,7 @@ def verify_drafts_workspace_bytes(rows: int, b: int, v: int) -> int:
 def _refuse_verify(target, draft, tokens, u, u_next, cu, lens, out, workspace, status) -> None:
     if not target.is_cuda:
         raise ValueError("target must be on a CUDA (HIP) device")
-    if _float_type(target) < 0 or target.dim() != 2 or not target.is_contiguous():
+    if target.dtype not in _TYPES or target.dim() != 2 or not target.is_contiguous():
         raise ValueError("target must be contiguous bfloat16 or float32 [rows, v]")
     _dev(cu, "cu", torch.int32, 1)
     b, (rows, v) = cu.shape[0] - 1, target.shape
@@ -1023,34 +1023,35 @@ def verify_drafts(target: torch.Tensor, draft: torch.Tensor | None, tokens: torc
     [rows - b, v] (None: drafts that are certain), tokens int32 and u fp32 [rows - b].
     A draft is accepted while u * draft < target; the next token is drawn with u_next
     fp32 [b].  lens (int32 [b]) loses the drafts that were not accepted."""
-    dev, ts, b = target.get_device(), target.shape, cu.shape[0] - 1
-    accepted, following = out if out is not None else (None, None)
-    if not (dev >= 0 and len(ts) == 2 and _float_type(target) >= 0 and target.is_contiguous() and cu.dtype is _I32 and
+    dev, ts, b, tt = target.get_device(), target.shape, cu.numel() - 1, target.dtype
+    if not (dev >= 0 and len(ts) == 2 and tt in _TYPES and target.is_contiguous() and cu.dtype is _I32 and
             cu.dim() == 1 and 0 <= b <= ts[0] and cu.get_device() == dev and cu.is_contiguous() and
-            (draft is None or (draft.dtype is target.dtype and draft.shape == (ts[0] - b, ts[1]) and
-                               draft.get_device() == dev and draft.is_contiguous())) and
+            (draft is None or (draft.dtype is tt and draft.shape == (ts[0] - b, ts[1]) and draft.get_device() == dev and
+                               draft.is_contiguous())) and
             tokens.dtype is _I32 and tokens.shape == (ts[0] - b,) and tokens.get_device() == dev and
             tokens.is_contiguous() and u.dtype is _F32 and u.shape == tokens.shape and u.get_device() == dev and
             u.is_contiguous() and u_next.dtype is _F32 and u_next.shape == (b,) and u_next.get_device() == dev and
-            u_next.is_contiguous() and _out_ok(lens, _I32, (b,), dev) and _out_ok(accepted, _I32, (b,), dev) and
-            _out_ok(following, _I32, (b,), dev) and
+            u_next.is_contiguous() and (lens is None or _out_ok(lens, _I32, (b,), dev)) and
+            (out is None or (_out_ok(out[0], _I32, (b,), dev) and _out_ok(out[1], _I32, (b,), dev))) and
             (workspace is None or (workspace.get_device() == dev and workspace.is_contiguous())) and
-            _flags_ok(status, dev)):
+            (status is None or _flags_ok(status, dev))):
         _refuse_verify(target, draft, tokens, u, u_next, cu, lens, out, workspace, status)
     if workspace is None:
         ws_bytes = lib.qg_verify_drafts_workspace_bytes(ts[0], b, ts[1])
         if ws_bytes < 0:
             _check(ws_bytes, "qg_verify_drafts")
         if ws_bytes > 0:
-            workspace = torch.empty(ws_bytes, dtype=torch.uint8, device=target.device)
+            workspace = target.new_empty(ws_bytes, dtype=torch.uint8)
     else:
         ws_bytes = workspace.numel() * workspace.element_size()
     if out is None:
         accepted, following = torch.empty_like(u_next, dtype=_I32), torch.empty_like(u_next, dtype=_I32)
+    else:
+        accepted, following = out
     call = lib.qg_verify_drafts if _current() == dev else _elsewhere(dev, lib.qg_verify_drafts)
-    st = call(target.data_ptr(), _ptr(draft), _float_type(target), ts[0], ts[1], tokens.data_ptr(), u.data_ptr(),
-              u_next.data_ptr(), cu.data_ptr(), b, _ptr(lens), accepted.data_ptr(), following.data_ptr(),
-              _ptr(workspace), ws_bytes, _ptr(status), _stream_of(dev))
+    st = call(target.data_ptr(), _ptr(draft), _TYPES[tt], *ts, tokens.data_ptr(), u.data_ptr(), u_next.data_ptr(),
+              cu.data_ptr(), b, _ptr(lens), accepted.data_ptr(), following.data_ptr(), _ptr(workspace), ws_bytes,
+              _ptr(status), _stream_of(dev))
     if st:
         _check(st, "qg_verify_drafts")
     return accepted, following
@@ -1094,7 +1095,7 @@ def moe_w4a16_picked(x: torch.Tensor, ids: torch.Tensor, weights: torch.Tensor, 
             ds[1] == xs[1] // TILE_ROWS * (inter // TILE_K) * TILE_BYTES and
             ids.get_device() == dev and weights.get_device() == dev and gate_up.get_device() == dev and
             down.get_device() == dev and x.is_contiguous() and ids.is_contiguous() and weights.is_contiguous() and
-            gate_up.is_contiguous() and down.is_contiguous() and _out_ok(out, out_dtype, xs, dev) and
+            gate_up.is_contiguous() and down.is_contiguous() and (out is None or _out_ok(out, out_dtype, xs, dev)) and
             (workspace is None or (workspace.get_device() == dev and workspace.is_contiguous())) and
             _flags_ok(status, dev)):
         if dev >= 0:
