@@ -118,7 +118,7 @@ struct RouteArgs {
   const float* bias;                // [e] or null
   int64_t t;
   int e, k, half, sigmoid, groups, top_groups, best, renorm;
-  int whole, lanes, shift;          // set by the launcher (moe_route.hip)
+  int whole, lanes, shift, lanes16, shift16;   // set by the launcher (moe_route.hip)
   float scale;
   int32_t* ids;                     // [t, k]
   float* weights;                   // [t, k]

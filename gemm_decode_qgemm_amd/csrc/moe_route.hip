@@ -32,6 +32,10 @@ __device__ __forceinline__ uint64_t order64(double c) {
   return (u >> 63) != 0 ? ~u : u | (uint64_t)1 << 63;
 }
 
+__device__ __forceinline__ double from64(uint64_t k) {
+  return __longlong_as_double((long long)((k >> 63) != 0 ? k ^ (uint64_t)1 << 63 : ~k));
+}
+
 // The same order for binary32 numbers, as steps of a bisection; and back.
 __device__ __forceinline__ uint32_t step_of(float c) {
   const uint32_t u = __float_as_uint(c + 0.0f);
@@ -82,7 +86,7 @@ constexpr int kRouteTokens = 8;        // of a workgroup, a wave each
 template <int U>
 struct RouteLds {
   union {
-    double choice[64 * U];             // of the exact way: c of every expert, in 64 bits
+    uint64_t choice[64 * U];           // of the exact way: every expert's key
     Pick by_expert[32];
   };
 };
@@ -114,9 +118,11 @@ __device__ __forceinline__ void load_row(float (&v)[U], const void* row, bool ha
   }
 }
 
-// exp(x - top) in 64 bits; 0 for -infinity (a token without a logit above it has no scores).
+// exp(x - top) in 64 bits; 0 for -infinity (a token without a logit above it has no
+// scores), and none beside an infinite one.
 __device__ __forceinline__ double route_exp(float x, float top) {
-  return x == -__builtin_inff() ? 0.0 : exp((double)x - (double)top);
+  const double d = top == __builtin_inff() ? (double)__builtin_nanf("") : (double)x - (double)top;
+  return x == -__builtin_inff() && !(top == __builtin_inff()) ? 0.0 : exp(d);
 }
 
 template <int U>
@@ -127,16 +133,17 @@ __device__ __forceinline__ double route_total(const float (&l)[U], float top) {
   return wave_sum(total);
 }
 
-// Groups whose rank, by `mine` of lane g, is below top_groups.
-template <class T>
-__device__ __forceinline__ uint64_t open_groups(const RouteArgs& a, T mine, T (*read)(T, int)) {
-  const int lane = threadIdx.x & 63;
-  int before = 0;
-  for (int g = 0; g < a.groups; ++g) {
-    const T other = read(mine, g);
-    before += other > mine || (other == mine && g < lane);
-  }
-  return __ballot(lane < a.groups && before < a.top_groups);
+template <int O>
+__device__ __forceinline__ uint64_t other_block64(uint64_t v) {
+  return (uint64_t)__float_as_uint(other_block<O>(__uint_as_float((uint32_t)(v >> 32)))) << 32 |
+         __float_as_uint(other_block<O>(__uint_as_float((uint32_t)v)));
+}
+template <int O>
+__device__ __forceinline__ void best_two64(int lanes, uint64_t& k1, uint64_t& k2) {
+  if (O >= lanes) return;              // uniform
+  const uint64_t d1 = other_block64<O>(k1), d2 = other_block64<O>(k2);
+  k2 = max(min(k1, d1), max(k2, d2));
+  k1 = max(k1, d1);
 }
 
 // The whole choice in 64 bits: lane j's pick.  By k rounds: the largest key of the
@@ -159,31 +166,49 @@ __device__ __forceinline__ int route_exact(const RouteArgs& a, const float (&l)[
       if (a.bias && e < a.e) c += (double)a.bias[e];
     }
     key[u] = e < a.e ? order64(c) : 0;
-    lds.choice[e] = c;
   }
-  if (a.groups > 1) {
+  if (a.groups > 1 && a.lanes > 0) {   // groups of whole lanes
+    uint64_t k1 = key[0], k2 = 0;      // the best two of this lane, then of the group
+#pragma unroll
+    for (int u = 1; u < U; ++u) {
+      k2 = max(min(k1, key[u]), k2);
+      k1 = max(k1, key[u]);
+    }
+    best_two64<1>(a.lanes, k1, k2);
+    best_two64<2>(a.lanes, k1, k2);
+    best_two64<4>(a.lanes, k1, k2);
+    best_two64<8>(a.lanes, k1, k2);
+    best_two64<16>(a.lanes, k1, k2);
+    best_two64<32>(a.lanes, k1, k2);
+    const uint64_t value = a.best == 1 ? k1 : order64(from64(k1) + from64(k2));
+    const int own = lane >> a.shift;
+    int before = 0;
+    for (int g = 0; g < a.groups; ++g) {
+      const uint64_t other = lane_of(value, g << a.shift);
+      before += other > value || (other == value && g < own);
+    }
+    if (before >= a.top_groups)
+#pragma unroll
+      for (int u = 0; u < U; ++u) key[u] = 0;
+  } else if (a.groups > 1) {
+#pragma unroll
+    for (int u = 0; u < U; ++u) lds.choice[U * lane + u] = key[u];
     wave_fence();
     const int per = a.e / a.groups;
-    uint64_t mine = 0;
-    if (lane < a.groups) {             // lane g: the best one or two of group g
-      uint64_t k1 = 0, k2 = 0;
-      double c1 = 0.0, c2 = 0.0;
+    uint64_t k1 = 0, k2 = 0;           // lane g: the best two of group g
+    if (lane < a.groups)
       for (int i = 0; i < per; ++i) {
-        const double c = lds.choice[lane * per + i];
-        const uint64_t k = order64(c);
-        if (k > k1) {
-          k2 = k1, c2 = c1;
-          k1 = k, c1 = c;
-        } else if (k > k2) {
-          k2 = k, c2 = c;
-        }
+        const uint64_t k = lds.choice[lane * per + i];
+        k2 = max(min(k1, k), k2);
+        k1 = max(k1, k);
       }
-      mine = a.best == 1 ? k1 : order64(c1 + c2);
+    const uint64_t mine = lane >= a.groups ? 0 : a.best == 1 ? k1 : order64(from64(k1) + from64(k2));
+    int before = 0;
+    for (int g = 0; g < a.groups; ++g) {
+      const uint64_t other = lane_of(mine, g);
+      before += other > mine || (other == mine && g < lane);
     }
-    const uint64_t open = open_groups<uint64_t>(a, mine, [](uint64_t v, int g) {
-      return (uint64_t)(uint32_t)__builtin_amdgcn_readlane((int)(v >> 32), g) << 32 |
-             (uint32_t)__builtin_amdgcn_readlane((int)v, g);
-    });
+    const uint64_t open = __ballot(lane < a.groups && before < a.top_groups);
 #pragma unroll
     for (int u = 0; u < U; ++u)
       if ((open >> ((U * lane + u) / per & 63) & 1) == 0) key[u] = 0;
@@ -193,8 +218,10 @@ __device__ __forceinline__ int route_exact(const RouteArgs& a, const float (&l)[
     uint64_t m = key[0];
 #pragma unroll
     for (int u = 1; u < U; ++u) m = max(m, key[u]);
-#pragma unroll
-    for (int o = 1; o < 64; o *= 2) m = max(m, (uint64_t)__shfl_xor((unsigned long long)m, o));
+    const auto larger = [](uint32_t x, uint32_t y) { return max(x, y); };
+    const uint32_t hi = lane_of(wave_scan((uint32_t)(m >> 32), 0u, larger), 63);
+    const uint32_t lo = lane_of(wave_scan((uint32_t)(m >> 32) == hi ? (uint32_t)m : 0u, 0u, larger), 63);
+    m = (uint64_t)hi << 32 | lo;
     int first = U;                     // of this lane's experts that have it
 #pragma unroll
     for (int u = U - 1; u >= 0; --u)
@@ -227,10 +254,11 @@ template <int U>
 __device__ __forceinline__ void route_token(const RouteArgs& a, const float (&l)[U], const float (&b)[U], float top,
                                             RouteLds<U>& lds, int* id_to, float* x_to) {
   const int lane = threadIdx.x & 63;
-  // c as binary32, off by at most `most` 2^-19 + |c| 2^-22 (route_off): exponentials and
-  // reciprocals by 2^-21 of themselves with what the rounding of a logit's distance x
-  // to the largest adds (x e^-x < 0.4 of 2^-23), the sum and the quotient by
-  // 2^-21, the addition by 2^-24 of c.
+  // c as binary32, off by at most `off`.  Sigmoid: an exponential is off by 2^-23 of
+  // itself and what the rounding of its argument adds, |l| 2^-24, of which s (1 - s) < 1/4
+  // and s (1 - s) |l| < 0.3 counts; a reciprocal by 2^-23: 2^-22 in all.  Softmax: likewise
+  // 2^-23 + 2.5 x 2^-24 of e^-x with x e^-x < 0.4, and the sum, up to 40 additions of
+  // 2^-24 one after another: 2^-18.5 of the largest score.  The last addition: 2^-24 of c.
   const bool exact = a.bias == nullptr && (a.groups == 1 || a.best == 1);
   float c[U];
   float most = 1.0f;                   // the largest score, at most
@@ -255,7 +283,8 @@ __device__ __forceinline__ void route_token(const RouteArgs& a, const float (&l)
       for (int u = 0; u < U; ++u) c[u] = b[u] + c[u] * most;
     }
   }
-  auto off = [&](float v) { return __builtin_fmaf(fabsf(v), 0x1p-22f, most * 0x1p-19f); };
+  const float least = a.sigmoid ? 0x1p-21f : most * 0x1p-18f;
+  auto off = [&](float v) { return __builtin_fmaf(fabsf(v), 0x1p-23f, least); };
   bool near = false;                   // numbers that 32 bits do not tell apart, or a NaN
 #pragma unroll
   for (int u = 0; u < U; ++u) near |= c[u] != c[u] && U * lane + u < a.e;
@@ -311,14 +340,14 @@ __device__ __forceinline__ void route_token(const RouteArgs& a, const float (&l)
     high = wave_max(high);
     // From the largest down in strides until k are reached, then by halves: k or more
     // from `lo` on, fewer from `hi` on.
-    const uint32_t least = step_of(-__builtin_inff());
+    const uint32_t lowest = step_of(-__builtin_inff());
     uint32_t hi = step_of(high) + 1u, lo = hi;
     int n = 0;
     for (uint32_t d = 1u << 21; n < a.k; d <<= 2) {
       hi = lo;
-      lo = lo - least > d && d != 0u ? lo - d : least;
+      lo = lo - lowest > d && d != 0u ? lo - d : lowest;
       n = count_from(c, step_to(lo));
-      if (lo == least) break;
+      if (lo == lowest) break;
     }
     while (n != a.k && hi - lo > 1u) {
       const uint32_t mid = lo + (hi - lo) / 2;
@@ -446,6 +475,251 @@ __global__ __launch_bounds__(64 * kRouteTokens) void moe_route_top_kernel(RouteA
   a.weights[(t0 + mine) * a.k + j] = (float)((double)a.scale * w);
 }
 
+// ---- many tokens, up to 8 picks of 128 experts ----------------------------------------
+//
+// Four tokens a wave, 16 lanes each, V experts a lane.  A lane keeps its experts as sorted
+// keys, so that a round of the choice is a maximum over 16 lanes and a shift in the
+// lane that had it, for four tokens at once and without scalar work (a wave a token
+// as above takes about 300 vector and 330 scalar instructions a token at 8 of 256
+// experts, and these take turns).
+//
+// A key is c's step with its last bits replaced: by the expert's place in the lane,
+// where c is computed or in 32 bits, which costs as much of c as the last bits are
+// worth and is added to its bound; by the whole expert's number, where logits of 16
+// bits are compared as they are, which makes keys unique, lower experts first.  Tokens
+// whose keys do not tell, or that have a NaN, are done again in 64 bits, by the
+// whole wave.  (With 16 experts a lane, four bits of c given up, so many tokens are that
+// it takes as long as a wave a token.)
+
+template <int CTRL>
+__device__ __forceinline__ uint32_t dpp_u(uint32_t v) {
+  return (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, CTRL, 0xf, 0xf, true);
+}
+__device__ __forceinline__ uint32_t row_max(uint32_t v) {   // of 16 lanes, in all of them
+  v = max(v, dpp_u<0x128>(v));           // row_ror 8, 4, 2, 1
+  v = max(v, dpp_u<0x124>(v));
+  v = max(v, dpp_u<0x122>(v));
+  return max(v, dpp_u<0x121>(v));
+}
+__device__ __forceinline__ float row_max(float v) {
+  v = fmaxf(v, dpp_f<0x128>(v));
+  v = fmaxf(v, dpp_f<0x124>(v));
+  v = fmaxf(v, dpp_f<0x122>(v));
+  return fmaxf(v, dpp_f<0x121>(v));
+}
+__device__ __forceinline__ float row_sum(float v) {
+  v += dpp_f<0x128>(v);
+  v += dpp_f<0x124>(v);
+  v += dpp_f<0x122>(v);
+  return v + dpp_f<0x121>(v);
+}
+__device__ __forceinline__ uint32_t med3_u(uint32_t a, uint32_t b, uint32_t c) {
+  return max(min(a, b), min(max(a, b), c));
+}
+
+// V values of a lane: 4 or 8.
+template <int V>
+__device__ __forceinline__ void load_lane(float (&v)[V], const void* row, bool half, int e) {
+  if (half) {
+    const uint16_t* const p = static_cast<const uint16_t*>(row) + e;
+#pragma unroll
+    for (int i = 0; i < V; i += 4) {
+      const u32x2_t w = *reinterpret_cast<const u32x2_t*>(p + i);
+#pragma unroll
+      for (int j = 0; j < 4; ++j) v[i + j] = __uint_as_float((j & 1) ? w[j >> 1] & 0xffff0000u : w[j >> 1] << 16);
+    }
+  } else {
+    const float* const p = static_cast<const float*>(row) + e;
+#pragma unroll
+    for (int i = 0; i < V; i += 4) {
+      const f32x4_t w = *reinterpret_cast<const f32x4_t*>(p + i);
+#pragma unroll
+      for (int j = 0; j < 4; ++j) v[i + j] = w[j];
+    }
+  }
+}
+
+template <int V>
+__global__ __launch_bounds__(256) void moe_route_rows_kernel(RouteArgs a) {
+  constexpr int U = V / 4;               // experts a lane where the whole wave takes a token
+  static_assert(V == 4 || V == 8, "experts a lane");
+  __shared__ RouteLds<U> lds_s[4];
+  __shared__ int fixed_s[4][4][8];
+  const int lane = threadIdx.x & 63, i = lane & 15, q = lane >> 4, wave = wave_id_uniform();
+  const int64_t t0 = ((int64_t)blockIdx.x * 4 + wave) * 4;
+  if (t0 >= a.t) return;                 // waves share nothing
+  const int64_t t = min(t0 + q, a.t - 1);
+  const bool live = V * i < a.e;         // e is a multiple of V
+  const int at = live ? V * i : 0;
+  float c[V];
+  const size_t row = (size_t)t * a.e;
+  load_lane<V>(c, a.half ? (const void*)(static_cast<const uint16_t*>(a.logits) + row)
+                         : (const void*)(static_cast<const float*>(a.logits) + row), a.half, at);
+  float top = 0.0f;
+  double total = 0.0;                    // of softmax scores that are not renormalized
+  if (!a.sigmoid) {
+    top = c[0];
+#pragma unroll
+    for (int u = 1; u < V; ++u) top = fmaxf(top, c[u]);
+    top = row_max(live ? top : -__builtin_inff());
+    if (!a.renorm) {
+#pragma unroll
+      for (int u = 0; u < V; ++u) total += route_exp(c[u], top);
+      total = live ? total : 0.0;
+      total += __shfl_xor(total, 1);
+      total += __shfl_xor(total, 2);
+      total += __shfl_xor(total, 4);
+      total += __shfl_xor(total, 8);
+    }
+  }
+  // c, and the bound on its error (route_token).
+  const bool exact = a.bias == nullptr && (a.groups == 1 || a.best == 1);
+  const bool whole_key = exact && a.half;
+  float most = 1.0f;                     // the largest score, at most
+  bool near = false;
+#pragma unroll
+  for (int u = 0; u < V; ++u) near |= c[u] != c[u];
+  if (!exact) {
+    constexpr float kLog2e = 1.44269504088896340736f;
+    float b[V];
+#pragma unroll
+    for (int u = 0; u < V; ++u) b[u] = 0.0f;
+    if (a.bias) load_lane<V>(b, a.bias, false, at);
+    if (a.sigmoid) {
+#pragma unroll
+      for (int u = 0; u < V; ++u) c[u] = b[u] + __builtin_amdgcn_rcpf(1.0f + __builtin_amdgcn_exp2f(-kLog2e * c[u]));
+    } else {
+      float sum = 0.0f;
+#pragma unroll
+      for (int u = 0; u < V; ++u) {
+        c[u] = c[u] == -__builtin_inff() ? 0.0f : __builtin_amdgcn_exp2f(kLog2e * (c[u] - top));
+        sum += c[u];
+      }
+      sum = row_sum(live ? sum : 0.0f);
+      most = sum == 0.0f ? 0.0f : __builtin_amdgcn_rcpf(sum);
+#pragma unroll
+      for (int u = 0; u < V; ++u) c[u] = b[u] + c[u] * most;
+    }
+#pragma unroll
+    for (int u = 0; u < V; ++u) near |= c[u] != c[u];   // a bias that is none
+  }
+  // (what the key's last bits leave out is below V units in the last place)
+  const float least = a.sigmoid ? 0x1p-21f : most * 0x1p-18f;
+  auto off = [&](float v) {
+    return whole_key ? 0.0f : __builtin_fmaf(fabsf(v), (float)(1 + V) * 0x1p-23f, exact ? 0.0f : least);
+  };
+  uint32_t k[V];
+#pragma unroll
+  for (int j = 0; j < V; ++j) k[j] = 0u;
+#pragma unroll
+  for (int u = 0; u < V; ++u) {
+    const uint32_t step = step_of(c[u]);
+    uint32_t x = whole_key ? (step & ~0x1ffu) | (uint32_t)(511 - (at + u)) : (step & ~(uint32_t)(V - 1)) | (uint32_t)(V - 1 - u);
+    x = live ? x : 0u;
+#pragma unroll
+    for (int j = V - 1; j > 0; --j) k[j] = med3_u(k[j - 1], k[j], x);
+    k[0] = max(k[0], x);
+  }
+  const uint32_t low = whole_key ? 0x1ffu : (uint32_t)(V - 1);
+  auto value_of = [&](uint32_t key) { return step_to(key & ~low); };
+
+  if (a.groups > 1) {
+    const int lanes = a.lanes16;
+    float c1 = value_of(k[0]), c2 = value_of(k[1]);
+    best_two<1>(lanes, c1, c2);
+    best_two<2>(lanes, c1, c2);
+    best_two<4>(lanes, c1, c2);
+    best_two<8>(lanes, c1, c2);
+    const float value = a.best == 1 ? c1 : c1 + c2;
+    const float far = 2.0f * (off(c1) + off(a.best == 1 ? c1 : c2));
+    const int own = i >> a.shift16;
+    int before = 0;
+    for (int g = 0; g < a.groups; ++g) {
+      const float other = __shfl(value, 16 * q + (g << a.shift16));
+      const bool is = g != own && live;
+      before += is && (other > value || (other == value && g < own));
+      if (!whole_key) near |= is && !(fabsf(other - value) > far);
+    }
+    if (before >= a.top_groups)
+#pragma unroll
+      for (int j = 0; j < V; ++j) k[j] = 0u;
+  }
+
+  // A round: the largest key of the 16 lanes, and in its lane the next one.
+  uint32_t mine = 0u, from = 0u;         // lane j: the j-th pick's key, and its lane
+  float last = 0.0f;
+  bool twice = false;                    // a key in two lanes
+  for (int j = 0; j < a.k; ++j) {
+    const uint32_t m = row_max(k[0]);
+    const bool it = k[0] == m;
+    const uint64_t has = __ballot(it);
+    twice |= __popcll(has) != 4;
+    if (!whole_key) {
+      const float v = value_of(m);
+      if (j > 0) near |= !(last - v > off(last) + off(v));
+      last = v;
+    }
+    const uint32_t lanes = (uint32_t)(q < 2 ? has : has >> 32) >> (16 * (q & 1)) & 0xffffu;
+    if (i == j) mine = m, from = (uint32_t)__builtin_ctz(lanes | 0x10000u);
+    if (it) {
+#pragma unroll
+      for (int o = 0; o + 1 < V; ++o) k[o] = k[o + 1];
+      k[V - 1] = 0u;
+    }
+  }
+  if (!whole_key) {                      // the last pick and the first that is none
+    const uint32_t m = row_max(k[0]);
+    const float v = value_of(m);
+    near |= m != 0u && !(last - v > off(last) + off(v));
+  }
+  int id = (int)(whole_key ? 511u - (mine & low) : (uint32_t)V * from + (uint32_t)(V - 1) - (mine & low));
+
+  uint64_t again = __ballot(near);
+  if (twice) again = ~(uint64_t)0;
+  if (again != 0) {
+    for (int r = 0; r < 4; ++r) {
+      if ((again >> (16 * r) & 0xffffu) == 0 || t0 + r >= a.t) continue;   // uniform
+      float l[U];
+      const size_t at_r = (size_t)(t0 + r) * a.e;
+      load_row<U>(l, a.half ? (const void*)(static_cast<const uint16_t*>(a.logits) + at_r)
+                            : (const void*)(static_cast<const float*>(a.logits) + at_r),
+                  a.half, a.whole, a.e, -__builtin_inff());
+      const int id_r = route_exact(a, l, lane_of(top, 16 * r), lds_s[wave]);
+      if (lane < a.k) fixed_s[wave][r][lane] = id_r;
+      wave_fence();
+    }
+    if ((again >> (16 * q) & 0xffffu) != 0) id = fixed_s[wave][q][i & 7];
+  }
+
+  const bool on = i < a.k;
+  const size_t pick = row + (on ? min(max(id, 0), a.e - 1) : 0);
+  const float x = a.half ? bf16_to_f32(static_cast<const uint16_t*>(a.logits)[pick]) : static_cast<const float*>(a.logits)[pick];
+  double w;
+  if (a.sigmoid)
+    w = 1.0 / (1.0 + exp(-(double)x));
+  else
+    w = route_exp(x, top);
+  if (a.renorm) {
+    total = on ? w : 0.0;
+    total += __shfl_xor(total, 1);
+    total += __shfl_xor(total, 2);
+    total += __shfl_xor(total, 4);
+  } else if (a.sigmoid) {
+    total = 1.0;
+  }
+  w = total == 0.0 ? 0.0 : w / total;
+  if (on && t0 + q < a.t) {
+    a.ids[t * a.k + i] = id;
+    a.weights[t * a.k + i] = (float)((double)a.scale * w);
+  }
+}
+
+// From here on, and from twice as many for more than 64 experts, four tokens a wave pay (64
+// experts: 4096 tokens 4.1 us against 4.9, 16385 5.4 against 10.0, 2048 4.0 both, 65536
+// with 8 experts 10 against 32; 128 experts: 4096 7.4 against 6.0, 16385 11.0 against 13.5,
+// 65536 28 against 43).
+constexpr int64_t kRouteRowsFrom = 4096;
+
 hipError_t launch_moe_route(RouteArgs a, hipStream_t stream) {
   const int u = a.e <= 64 ? 1 : a.e <= 128 ? 2 : a.e <= 256 ? 4 : 8;
   auto on = [](const void* p, int n) { return ((uintptr_t)p & (uintptr_t)(n - 1)) == 0; };
@@ -454,6 +728,18 @@ hipError_t launch_moe_route(RouteArgs a, hipStream_t stream) {
   a.lanes = per % u == 0 && (lanes & (lanes - 1)) == 0 ? lanes : 0;
   for (a.shift = 0; 1 << a.shift < a.lanes;) ++a.shift;
   a.whole = a.e % u == 0 && on(a.logits, a.half ? 2 * u : u < 4 ? 4 * u : 16) && on(a.bias, u < 4 ? 4 * u : 16);
+  const int v = 4 * u, lanes16 = per / v;
+  a.lanes16 = per % v == 0 && (lanes16 & (lanes16 - 1)) == 0 ? lanes16 : 0;
+  for (a.shift16 = 0; 1 << a.shift16 < a.lanes16;) ++a.shift16;
+  if (a.t >= kRouteRowsFrom * u && a.k <= 8 && u <= 2 && a.e % v == 0 && a.whole && on(a.logits, 16) && on(a.bias, 16) &&
+      (a.groups == 1 || a.lanes16 > 0)) {
+    const dim3 rows((uint32_t)((a.t + 15) / 16));
+    if (u == 1)
+      hipLaunchKernelGGL((moe_route_rows_kernel<4>), rows, dim3(256), 0, stream, a);
+    else
+      hipLaunchKernelGGL((moe_route_rows_kernel<8>), rows, dim3(256), 0, stream, a);
+    return hipGetLastError();
+  }
   const dim3 grid((uint32_t)((a.t + kRouteTokens - 1) / kRouteTokens));
   if (a.e <= 64)
     hipLaunchKernelGGL((moe_route_top_kernel<1>), grid, dim3(64 * kRouteTokens), 0, stream, a);

@@ -45,13 +45,14 @@ def route(l, k, sigmoid, bias, groups, top_groups, best, renorm, scale):
             else:
                 s = np.exp(l[i] - np.max(l[i]))
                 s = s / s.sum()
-        c = s if bias is None else s + bias
-        # sigmoid and softmax keep the order of the logits, which tell apart what 64 bits round together
-        pairs = [(c[j], l[i, j] if bias is None else 0.0, -j) for j in range(e)]
+        # sigmoid and softmax keep the order of the logits, which decide where neither a bias nor a sum takes part;
+        # a NaN (of an infinite logit in a softmax, too) is above all numbers
+        c = l[i] if bias is None and (groups == 1 or best == 1) else s if bias is None else s + bias
+        pairs = [(bool(np.isnan(c[j])), 0.0 if np.isnan(c[j]) else c[j], -j) for j in range(e)]
         value = []
         for g in range(groups):
             top = sorted(pairs[g * per:(g + 1) * per], reverse=True)[:best]
-            value.append((sum(p[0] for p in top), top[0][1] if best == 1 else 0.0, -g))
+            value.append((any(p[0] for p in top), sum(p[1] for p in top) if not any(p[0] for p in top) else 0.0, -g))
         kept = {-v[2] for v in sorted(value, reverse=True)[:top_groups]}
         order = sorted((p for p in pairs if -p[2] // per in kept), reverse=True)[:k]
         ids[i] = [-p[2] for p in order]

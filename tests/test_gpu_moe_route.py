@@ -27,7 +27,9 @@ def check(dev, l, k, sigmoid=False, bias=None, groups=1, top_groups=1, best=1, r
     assert ids.dtype == torch.int32 and w.dtype == F32
     assert np.array_equal(ids.cpu().numpy(), want), np.argwhere(ids.cpu().numpy() != want)[:3]
     tol = ref.half_step(np.abs(weights) * (1 + 2.0 ** -30), 24) + 2.0 ** -40 * np.abs(weights)
-    assert np.all(np.abs(ref.f64(w) - weights) <= tol)
+    got = ref.f64(w)
+    bad = ~((np.abs(got - weights) <= tol) | (np.isnan(got) & np.isnan(weights)))
+    assert not bad.any(), (np.argwhere(bad)[:3], got[bad][:3], weights[bad][:3])
     return ids, w
 
 
@@ -128,3 +130,86 @@ def test_long_prompts_graph_and_out(dev):
         assert torch.equal(out[0], want[0]) and torch.equal(out[1], want[1]), k
     e = qg.moe_route(l[:0], 8, **kw)
     assert e[0].shape == (0, 8) and e[1].shape == (0, 8)
+
+
+# ---- many tokens: four of them a wave, up to 128 experts and 8 picks ------------------
+
+def check_many(dev, l, k, **kw):
+    """A few hundred tokens, each many times over in any order, as many as that takes; the reference takes each once."""
+    n = l.shape[0]
+    order = torch.randint(0, n, (8195,), generator=torch.Generator().manual_seed(n))
+    order[:n] = torch.arange(n)
+    bias = kw.get("bias")
+    ids, w = qg.moe_route(l[order].to(dev), k, sigmoid=kw.get("sigmoid", False), bias=None if bias is None else bias.to(dev),
+                          groups=kw.get("groups", 1), top_groups=kw.get("top_groups", 1), group_best=kw.get("best", 1),
+                          renormalize=kw.get("renorm", True), scale=kw.get("scale", 1.0))
+    once = check(dev, l, k, **kw)
+    assert torch.equal(ids, once[0][order.to(dev)])
+    again = once[1][order.to(dev)]
+    # both within half a step of the same number, and a hair more: a step of the last place apart at most
+    assert bool(((w - again).abs() <= 2.0 ** -23 * again.abs()).logical_or(w.isnan() & again.isnan()).all())
+
+
+@pytest.mark.parametrize("e,k", [(4, 1), (8, 2), (60, 6), (64, 8), (72, 5), (100, 4), (128, 8), (256, 8)])
+@pytest.mark.parametrize("sigmoid,bias,renorm", [(False, False, True), (False, True, False), (True, True, True), (True, False, False)])
+@pytest.mark.parametrize("half", [False, True])
+def test_many_tokens(dev, e, k, sigmoid, bias, renorm, half):
+    torch.manual_seed(e + k)
+    l = 2 * torch.randn(203, e)
+    check_many(dev, l.bfloat16() if half else l, k, sigmoid=sigmoid, bias=0.2 * torch.randn(e) if bias else None, renorm=renorm, scale=2.5)
+
+
+@pytest.mark.parametrize("e,groups,top,k", [(128, 8, 4, 8), (128, 16, 1, 8), (64, 16, 7, 5), (64, 8, 3, 6), (96, 4, 2, 8), (32, 2, 1, 8), (256, 8, 4, 8),
+                                            (128, 2, 1, 8), (96, 6, 2, 4)])
+@pytest.mark.parametrize("sigmoid,bias", [(False, False), (True, True), (True, False), (False, True)])
+@pytest.mark.parametrize("half", [False, True])
+def test_many_tokens_in_groups(dev, e, groups, top, k, sigmoid, bias, half):
+    torch.manual_seed(e + groups)
+    l = 2 * torch.randn(150, e)
+    for best in (1, 2):
+        check_many(dev, l.bfloat16() if half else l, k, sigmoid=sigmoid, bias=0.2 * torch.randn(e) if bias else None, groups=groups,
+                   top_groups=top, best=best, renorm=best == 2)
+
+
+@pytest.mark.parametrize("e", [64, 128, 256])
+def test_many_tokens_with_ties_clusters_masks_and_nan(dev, e):
+    """Equal logits, the best experts side by side, experts masked out, tokens with nothing left, and NaN: token by token
+    beside ordinary ones."""
+    inf = float("inf")
+    torch.manual_seed(e)
+    l = torch.randn(160, e)
+    l[::8] = 0.0
+    l[1::8, 5:16] += 20.0
+    l[2::8] = torch.randint(0, 3, (20, e)).float()
+    l[3::8, 9:] = -inf
+    l[4::8] = -inf
+    l[5::16, e // 2] = torch.finfo(F32).max
+    l[6::8, 1::2] = torch.finfo(F32).min
+    l[7::8] = 1 + torch.arange(e).flip(0) * 2.0 ** -23
+    for sigmoid, bias in ((False, None), (True, None), (True, torch.zeros(e)), (False, torch.zeros(e)), (True, torch.full((e,), 8.0))):
+        for groups in (1, 4):
+            for half in (False, True):
+                check_many(dev, l.bfloat16() if half else l, 8, sigmoid=sigmoid, bias=bias, groups=groups, top_groups=max(1, groups // 2),
+                           best=1 if sigmoid or groups == 1 else 2)
+    l[13, 33] = float("nan")
+    l = l.repeat(52, 1)
+    for kw in (dict(), dict(sigmoid=True, bias=torch.zeros(e, device=dev)), dict(sigmoid=True, groups=4, top_groups=1, group_best=2)):
+        for x in (l, l.bfloat16()):
+            ids, w = qg.moe_route(x.to(dev), 4, **kw)
+            # (the largest binary32 number is an infinity in bf16, beside which a softmax has no scores)
+            others = (x < inf).all(1) | torch.tensor("sigmoid" in kw)
+            others[13::160] = False
+            assert bool((ids[13::160, 0] == 33).all()) and bool(w[13::160, 0].isnan().all()) and bool(w[others.to(dev)].isfinite().all())
+
+
+def test_many_tokens_at_addresses_that_are_not_aligned(dev):
+    """Logits and bias 4 bytes off: the other way, with the same result."""
+    torch.manual_seed(8)
+    l, bias = torch.randn(8500, 128), 0.1 * torch.randn(128)
+    want = qg.moe_route(l.to(dev), 8, sigmoid=True, bias=bias.to(dev))
+    room = torch.empty(8500 * 128 + 1, device=dev)
+    room[1:] = l.flatten().to(dev)
+    room_b = torch.empty(129, device=dev)
+    room_b[1:] = bias.to(dev)
+    got = qg.moe_route(room[1:].view(8500, 128), 8, sigmoid=True, bias=room_b[1:])
+    assert torch.equal(got[0], want[0]) and bool(((got[1] - want[1]).abs() <= 2.0 ** -23 * want[1]).all())
