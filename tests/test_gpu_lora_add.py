@@ -163,3 +163,30 @@ def test_the_largest_widths(dev):
     want = y[0].double() + torch.matmul(b[33].double(), v)
     # the chain of 2^20 / 128 additions of positive and negative terms, far under its bound of (k / 4) 2^-24
     assert float((out[0].double() - want).abs().max()) <= 1e-2 and torch.equal(out[1], y[1])
+
+
+def test_adapters_and_rows_that_no_one_names_are_not_read(dev):
+    y, x, a, b, ids, scales = (t.to(dev) for t in make(24, 520, 130, 24, 5))
+    ids = torch.tensor([0, 2, -1, 4] * 6, dtype=torch.int32, device=dev)
+    want = qg.lora_add(y, x, a, b, ids, scales=scales)
+    x[2::4] = float("nan")
+    for i in (1, 3):
+        a[i], b[i], scales[i] = float("nan"), float("nan"), float("nan")
+    assert torch.equal(qg.lora_add(y, x, a, b, ids, scales=scales), want)
+    few = slice(0, 4)                          # fewer rows than adapters
+    assert torch.equal(qg.lora_add(y[few], x[few], a, b, ids[few].contiguous(), scales=scales), want[few])
+
+
+def test_two_streams_at_once(dev):
+    """Calls that overlap, each with a workspace of its own."""
+    args = [tuple(t.to(dev) for t in make(33, 2048, 5000, 64, 20, seed=s)) for s in (0, 1)]
+    want = [qg.lora_add(*c[:5], scales=c[5]) for c in args]
+    streams = [torch.cuda.Stream(), torch.cuda.Stream()]
+    torch.cuda.synchronize()
+    got = [[], []]
+    for _ in range(10):
+        for i, s in enumerate(streams):
+            with torch.cuda.stream(s):
+                got[i].append(qg.lora_add(*args[i][:5], scales=args[i][5]))
+    torch.cuda.synchronize()
+    assert all(torch.equal(o, want[i]) for i in (0, 1) for o in got[i])

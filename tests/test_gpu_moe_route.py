@@ -213,3 +213,23 @@ def test_many_tokens_at_addresses_that_are_not_aligned(dev):
     room_b[1:] = bias.to(dev)
     got = qg.moe_route(room[1:].view(8500, 128), 8, sigmoid=True, bias=room_b[1:])
     assert torch.equal(got[0], want[0]) and bool(((got[1] - want[1]).abs() <= 2.0 ** -23 * want[1]).all())
+
+
+@pytest.mark.parametrize("e", [64, 512])           # four tokens a wave; one
+def test_logits_past_two_to_the_31_elements(dev, e):
+    t = 2 ** 31 // e + 5
+    l = torch.zeros(t, e, dtype=BF16, device=dev)
+    l[-7:] = torch.randn(7, e, device=dev)
+    ids, w = qg.moe_route(l, 6, sigmoid=True)
+    want = qg.moe_route(l[-7:].clone(), 6, sigmoid=True)
+    assert torch.equal(ids[-7:], want[0]) and bool(((w[-7:] - want[1]).abs() <= 2.0 ** -23 * want[1]).all())
+    assert torch.equal(ids[-8], torch.arange(6, dtype=torch.int32, device=dev))
+
+
+def test_sigmoid_scores_that_are_all_one(dev):
+    """Nothing is added to the scores, so the logits decide, also where 64 bits hold a one; infinite ones are equal."""
+    l = torch.zeros(2, 16)
+    l[0, 3], l[0, 9], l[0, 12] = 50.0, 60.0, 55.0
+    l[1, 7] = l[1, 5] = float("inf")
+    ids, w = qg.moe_route(l.to(dev), 3, sigmoid=True, renormalize=False)
+    assert ids.tolist() == [[9, 12, 3], [5, 7, 0]] and w.tolist() == [[1.0, 1.0, 1.0], [1.0, 1.0, 0.5]]

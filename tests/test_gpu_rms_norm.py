@@ -178,3 +178,24 @@ def test_a_device_that_is_not_the_current_one(dev, monkeypatch):
     want = qg.rms_norm(x)
     monkeypatch.setattr(qg.binding, "_current", lambda: -1)
     assert torch.equal(qg.rms_norm(x), want)
+
+
+@pytest.mark.parametrize("h", [128, 2056, 6656, 20000])
+def test_over_its_own_input(dev, h):
+    """y over x, and the sum over the residual, in one call."""
+    x, res, w = (t.to(dev) for t in inputs(9, h, BF16, BF16))
+    y, r = qg.rms_norm(x, w, residual=res)
+    got = qg.rms_norm(x, w, residual=res, out=x, residual_out=res)
+    assert got[0].data_ptr() == x.data_ptr() and torch.equal(got[0], y) and torch.equal(got[1], r)
+
+
+def test_rows_past_two_to_the_31_elements(dev):
+    t, h = 2 ** 19 + 3, 4096
+    x = torch.zeros(t, h, dtype=BF16, device=dev)
+    x[-5:] = torch.randn(5, h, device=dev)
+    y = qg.rms_norm(x)
+    codes, scales = qg.rms_norm_q8(x, group_scales=True)
+    few = x[-5:].clone()
+    assert torch.equal(y[-5:], qg.rms_norm(few)) and not bool(y[-6].any())
+    want = qg.rms_norm_q8(few, group_scales=True)
+    assert torch.equal(codes[-5:], want[0]) and torch.equal(scales[-5:], want[1]) and not bool(scales[-6].any())

@@ -201,3 +201,91 @@ def test_draws_follow_the_target(dev):
     first = torch.where(accepted.cpu() > 0, tokens, following.cpu())
     count = torch.bincount(first.long(), minlength=v)
     assert float((count - b * p).abs().max()) <= 6 * 71
+
+
+# ---- vocabularies whose sums are a launch of their own, and wide batches ----------------
+
+@pytest.mark.parametrize("v", [40008, 50001, 600001])       # whole rows of 16 bytes; odd; pieces of more than 512
+@pytest.mark.parametrize("dtype,sure,cut", [(F32, False, False), (BF16, False, True), (F32, True, True), (BF16, True, False)])
+def test_wide_vocabularies(dev, v, dtype, sure, cut):
+    check(dev, make([2, 0, 3, 1, 0], v, dtype, sure, cut))
+
+
+@pytest.mark.parametrize("dtype", [F32, BF16])
+def test_wide_batches_of_wide_vocabularies(dev, dtype):
+    """130 sequences of 60001: one workgroup each; the same outcome as 13 at a time."""
+    g = torch.Generator(device=dev).manual_seed(1)
+    b, v = 130, 60001
+    p = torch.softmax(2 * torch.randn(2 * b, v, generator=g, device=dev), 1).to(dtype)
+    q = torch.softmax(2 * torch.randn(b, v, generator=g, device=dev), 1).to(dtype)
+    tokens = torch.randint(0, v, (b,), generator=g, device=dev, dtype=torch.int32)
+    u, u_next = torch.rand(b, generator=g, device=dev), torch.rand(b, generator=g, device=dev)
+    got = qg.verify_drafts(p, q, tokens, u, u_next, 2 * torch.arange(b + 1, device=dev, dtype=torch.int32))
+    cu = 2 * torch.arange(14, device=dev, dtype=torch.int32)
+    for i in range(0, b, 13):
+        s = slice(i, i + 13)
+        part = qg.verify_drafts(p[2 * i:2 * i + 26], q[s], tokens[s], u[s], u_next[s], cu)
+        assert torch.equal(got[0][s], part[0]) and torch.equal(got[1][s], part[1]), i
+
+
+def test_wide_vocabularies_at_their_edges(dev):
+    """Nothing left over, nothing to draw from, tokens and offsets outside, lengths and flags: as for small ones."""
+    v = 50000
+    c = make([1, 1], v)
+    c["draft"] = c["target"][[0, 2]].clone()
+    c["target"] *= 0.5
+    c["u"].fill_(0.75)
+    assert check(dev, c)[0] == [0, 0]
+    c = make([1, 1, 1, 1], v)
+    status = torch.zeros(1, dtype=torch.int32, device=dev)
+    c["u"].fill_(0.999999)
+    c["draft"].scatter_(1, c["tokens"].long()[:, None], 1.0)
+    c["target"][0] = 0.0
+    c["target"][2, 7] = float("inf")
+    c["target"][4, 9] = float("nan")
+    accepted, following = run(dev, c, status=status)
+    w = want(c)
+    assert accepted.tolist() == w[0] and following.tolist() == w[1] and w[1][:2] == [-1, -1] and w[1][2] >= 0
+    assert status.item() == qg.FLAG_NONFINITE
+    c = make([2, 3, 1], v)
+    c["tokens"][0], c["tokens"][3] = v, -1
+    status.zero_()
+    accepted, following = run(dev, c, status=status)
+    assert accepted.tolist() == want(c)[0] and following.tolist() == want(c)[1] and status.item() == qg.FLAG_INDEX
+    status.zero_()
+    lens = torch.full((3,), 50, dtype=torch.int32, device=dev)
+    accepted, following = run(dev, make([2, 3, 1], v) | dict(cu=torch.tensor([0, 3, 2, 9], dtype=torch.int32)), status=status, lens=lens)
+    assert status.item() & qg.FLAG_INDEX and accepted[1].item() == 0 and following[1].item() == -1 and lens[1].item() == 50
+
+
+def test_captured_graphs_of_wide_vocabularies_share_a_workspace(dev):
+    first, second = ({k: t.to(dev) for k, t in make([4, 0, 6, 3, 2], 50001, seed=s).items()} for s in (0, 1))
+    ws = torch.empty(qg.verify_drafts_workspace_bytes(first["target"].shape[0], 5, 50001), dtype=torch.uint8, device=dev)
+    assert ws.numel() > 0
+    graphs, outs = [], []
+    for c in (first, second):
+        outs.append((torch.zeros(5, dtype=torch.int32, device=dev), torch.zeros(5, dtype=torch.int32, device=dev)))
+        graphs.append(torch.cuda.CUDAGraph())
+        with torch.cuda.graph(graphs[-1]):
+            qg.verify_drafts(*c.values(), out=outs[-1], workspace=ws)
+    for k in range(3):
+        for c in (first, second):
+            c["u"].uniform_()
+            c["u_next"].uniform_()
+        for g in graphs:
+            g.replay()
+        torch.cuda.synchronize()
+        for c, out in zip((first, second), outs):
+            want_ = qg.verify_drafts(*c.values())
+            assert torch.equal(out[0], want_[0]) and torch.equal(out[1], want_[1]), k
+
+
+def test_rows_past_two_to_the_31_elements(dev):
+    v, b = 131072, 16385                       # 2^31 elements and a row, 4 GiB
+    target = torch.zeros(b, v, dtype=BF16, device=dev)
+    hit = torch.arange(b, device=dev) * 7919 % v
+    target.scatter_(1, hit[:, None], 1.0)
+    none = torch.zeros(0, device=dev)
+    accepted, following = qg.verify_drafts(target, None, none.to(torch.int32), none, torch.rand(b, device=dev),
+                                           torch.arange(b + 1, dtype=torch.int32, device=dev))
+    assert not bool(accepted.any()) and torch.equal(following.long(), hit)
