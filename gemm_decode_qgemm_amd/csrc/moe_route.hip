@@ -475,21 +475,19 @@ __global__ __launch_bounds__(64 * kRouteTokens) void moe_route_top_kernel(RouteA
   a.weights[(t0 + mine) * a.k + j] = (float)((double)a.scale * w);
 }
 
-// ---- many tokens, up to 8 picks of 128 experts ----------------------------------------
+// ---- many tokens, up to 8 picks of 256 experts ----------------------------------------
 //
-// Four tokens a wave, 16 lanes each, V experts a lane.  A lane keeps its experts as sorted
-// keys, so that a round of the choice is a maximum over 16 lanes and a shift in the
-// lane that had it, for four tokens at once and without scalar work (a wave a token
+// Four tokens a wave, 16 lanes each, V experts a lane.  A lane keeps its best eight as
+// sorted keys, so that a round of the choice is a maximum over 16 lanes and a shift in
+// the lane that had it, for four tokens at once and without scalar work (a wave a token
 // as above takes about 300 vector and 330 scalar instructions a token at 8 of 256
 // experts, and these take turns).
 //
-// A key is c's step with its last bits replaced: by the expert's place in the lane,
-// where c is computed or in 32 bits, which costs as much of c as the last bits are
-// worth and is added to its bound; by the whole expert's number, where logits of 16
-// bits are compared as they are, which makes keys unique, lower experts first.  Tokens
-// whose keys do not tell, or that have a NaN, are done again in 64 bits, by the
-// whole wave.  (With 16 experts a lane, four bits of c given up, so many tokens are that
-// it takes as long as a wave a token.)
+// A key is c's step, and the expert it belongs to is looked up in the lane's c, which
+// lie in LDS, when all picks are known.  Where logits of 16 bits are compared as they are,
+// which are often equal, the last bits of a key are the expert's number, lower ones
+// first.  Tokens whose keys do not tell, or that have a NaN, are done again in 64
+// bits, by the whole wave.
 
 template <int CTRL>
 __device__ __forceinline__ uint32_t dpp_u(uint32_t v) {
@@ -513,11 +511,38 @@ __device__ __forceinline__ float row_sum(float v) {
   v += dpp_f<0x122>(v);
   return v + dpp_f<0x121>(v);
 }
-__device__ __forceinline__ uint32_t med3_u(uint32_t a, uint32_t b, uint32_t c) {
-  return max(min(a, b), min(max(a, b), c));
+// k[A] and k[B] in order, the larger first.
+template <int A, int B, int N>
+__device__ __forceinline__ void in_order(uint32_t (&k)[N]) {
+  const uint32_t a = max(k[A], k[B]), b = min(k[A], k[B]);
+  k[A] = a, k[B] = b;
+}
+// F .. F + 3 sorted, largest first; F .. F + 7 by an odd-even merge of two of these.
+template <int F, int N>
+__device__ __forceinline__ void sort4(uint32_t (&k)[N]) {
+  in_order<F, F + 1>(k), in_order<F + 2, F + 3>(k);
+  in_order<F, F + 2>(k), in_order<F + 1, F + 3>(k);
+  in_order<F + 1, F + 2>(k);
+}
+template <int F, int N>
+__device__ __forceinline__ void sort8(uint32_t (&k)[N]) {
+  sort4<F>(k), sort4<F + 4>(k);
+  in_order<F, F + 4>(k), in_order<F + 1, F + 5>(k), in_order<F + 2, F + 6>(k), in_order<F + 3, F + 7>(k);
+  in_order<F + 2, F + 4>(k), in_order<F + 3, F + 5>(k);
+  in_order<F + 1, F + 2>(k), in_order<F + 3, F + 4>(k), in_order<F + 5, F + 6>(k);
+}
+// The best 8 of 16 into k[0 .. 7], sorted: of two sorted eights the larger of each place and
+// its mirror, which rise and fall (or fall and rise) once, then their merge.
+__device__ __forceinline__ void best8(uint32_t (&k)[16]) {
+  sort8<0>(k), sort8<8>(k);
+#pragma unroll
+  for (int i = 0; i < 8; ++i) k[i] = max(k[i], k[15 - i]);
+  in_order<0, 4>(k), in_order<1, 5>(k), in_order<2, 6>(k), in_order<3, 7>(k);
+  in_order<0, 2>(k), in_order<1, 3>(k), in_order<4, 6>(k), in_order<5, 7>(k);
+  in_order<0, 1>(k), in_order<2, 3>(k), in_order<4, 5>(k), in_order<6, 7>(k);
 }
 
-// V values of a lane: 4 or 8.
+// V values of a lane: 4, 8 or 16.
 template <int V>
 __device__ __forceinline__ void load_lane(float (&v)[V], const void* row, bool half, int e) {
   if (half) {
@@ -542,8 +567,11 @@ __device__ __forceinline__ void load_lane(float (&v)[V], const void* row, bool h
 template <int V>
 __global__ __launch_bounds__(256) void moe_route_rows_kernel(RouteArgs a) {
   constexpr int U = V / 4;               // experts a lane where the whole wave takes a token
-  static_assert(V == 4 || V == 8, "experts a lane");
+  constexpr int K = V < 8 ? V : 8;       // keys a lane keeps
+  static_assert(V == 4 || V == 8 || V == 16, "experts a lane");
   __shared__ RouteLds<U> lds_s[4];
+  __shared__ __attribute__((aligned(16))) float c_s[4][64][V + 4];   // rows 16 bytes apart at least, off the same banks
+  __shared__ u32x2_t pick_s[4][4][8];
   __shared__ int fixed_s[4][4][8];
   const int lane = threadIdx.x & 63, i = lane & 15, q = lane >> 4, wave = wave_id_uniform();
   const int64_t t0 = ((int64_t)blockIdx.x * 4 + wave) * 4;
@@ -603,24 +631,24 @@ __global__ __launch_bounds__(256) void moe_route_rows_kernel(RouteArgs a) {
 #pragma unroll
     for (int u = 0; u < V; ++u) near |= c[u] != c[u];   // a bias that is none
   }
-  // (what the key's last bits leave out is below V units in the last place)
   const float least = a.sigmoid ? 0x1p-21f : most * 0x1p-18f;
-  auto off = [&](float v) {
-    return whole_key ? 0.0f : __builtin_fmaf(fabsf(v), (float)(1 + V) * 0x1p-23f, exact ? 0.0f : least);
-  };
+  auto off = [&](float v) { return exact ? 0.0f : __builtin_fmaf(fabsf(v), 0x1p-23f, least); };
   uint32_t k[V];
-#pragma unroll
-  for (int j = 0; j < V; ++j) k[j] = 0u;
 #pragma unroll
   for (int u = 0; u < V; ++u) {
     const uint32_t step = step_of(c[u]);
-    uint32_t x = whole_key ? (step & ~0x1ffu) | (uint32_t)(511 - (at + u)) : (step & ~(uint32_t)(V - 1)) | (uint32_t)(V - 1 - u);
-    x = live ? x : 0u;
-#pragma unroll
-    for (int j = V - 1; j > 0; --j) k[j] = med3_u(k[j - 1], k[j], x);
-    k[0] = max(k[0], x);
+    k[u] = !live ? 0u : whole_key ? (step & ~0x1ffu) | (uint32_t)(511 - (at + u)) : step;
   }
-  const uint32_t low = whole_key ? 0x1ffu : (uint32_t)(V - 1);
+  if (!whole_key)
+#pragma unroll
+    for (int u = 0; u < V; u += 4) *reinterpret_cast<f32x4_t*>(&c_s[wave][lane][u]) = f32x4_t{c[u], c[u + 1], c[u + 2], c[u + 3]};
+  if constexpr (V == 4)
+    sort4<0>(k);
+  else if constexpr (V == 8)
+    sort8<0>(k);
+  else
+    best8(k);
+  const uint32_t low = whole_key ? 0x1ffu : 0u;
   auto value_of = [&](uint32_t key) { return step_to(key & ~low); };
 
   if (a.groups > 1) {
@@ -632,47 +660,59 @@ __global__ __launch_bounds__(256) void moe_route_rows_kernel(RouteArgs a) {
     best_two<8>(lanes, c1, c2);
     const float value = a.best == 1 ? c1 : c1 + c2;
     const float far = 2.0f * (off(c1) + off(a.best == 1 ? c1 : c2));
-    const int own = i >> a.shift16;
-    int before = 0;
-    for (int g = 0; g < a.groups; ++g) {
-      const float other = __shfl(value, 16 * q + (g << a.shift16));
-      const bool is = g != own && live;
-      before += is && (other > value || (other == value && g < own));
+    const int own = i >> a.shift16, first = i & (lanes - 1);
+    float before = 0.0f;                 // groups before this one
+    // A group's lanes compare it with one other group each, in turn.
+    for (int g0 = 0; g0 < a.groups; g0 += lanes) {
+      const int g = g0 + first;
+      const float other = __shfl(value, 16 * q + (min(g, a.groups - 1) << a.shift16));
+      const bool is = g < a.groups && g != own && live;
+      before += is && (other > value || (other == value && g < own)) ? 1.0f : 0.0f;
       if (!whole_key) near |= is && !(fabsf(other - value) > far);
     }
-    if (before >= a.top_groups)
+    if (lanes > 1) before += other_block<1>(before);
+    if (lanes > 2) before += other_block<2>(before);
+    if (lanes > 4) before += other_block<4>(before);
+    if (lanes > 8) before += other_block<8>(before);
+    if (before >= (float)a.top_groups)
 #pragma unroll
-      for (int j = 0; j < V; ++j) k[j] = 0u;
+      for (int j = 0; j < K; ++j) k[j] = 0u;
   }
 
   // A round: the largest key of the 16 lanes, and in its lane the next one.
-  uint32_t mine = 0u, from = 0u;         // lane j: the j-th pick's key, and its lane
-  float last = 0.0f;
   bool twice = false;                    // a key in two lanes
   for (int j = 0; j < a.k; ++j) {
     const uint32_t m = row_max(k[0]);
     const bool it = k[0] == m;
-    const uint64_t has = __ballot(it);
-    twice |= __popcll(has) != 4;
-    if (!whole_key) {
-      const float v = value_of(m);
-      if (j > 0) near |= !(last - v > off(last) + off(v));
-      last = v;
-    }
-    const uint32_t lanes = (uint32_t)(q < 2 ? has : has >> 32) >> (16 * (q & 1)) & 0xffffu;
-    if (i == j) mine = m, from = (uint32_t)__builtin_ctz(lanes | 0x10000u);
+    twice |= __popcll(__ballot(it)) != 4;
     if (it) {
+      pick_s[wave][q][j] = u32x2_t{m, (uint32_t)i};
 #pragma unroll
-      for (int o = 0; o + 1 < V; ++o) k[o] = k[o + 1];
-      k[V - 1] = 0u;
+      for (int o = 0; o + 1 < K; ++o) k[o] = k[o + 1];
+      k[K - 1] = 0u;
     }
   }
-  if (!whole_key) {                      // the last pick and the first that is none
-    const uint32_t m = row_max(k[0]);
-    const float v = value_of(m);
-    near |= m != 0u && !(last - v > off(last) + off(v));
+  const uint32_t next = row_max(k[0]);
+  wave_fence();
+  const u32x2_t pick = pick_s[wave][q][i & 7];
+  const bool on = i < a.k;
+  const uint32_t mine = on ? pick[0] : 0u, from = on ? pick[1] & 15u : 0u;   // lane j: the j-th pick's key, and its lane
+  if (!whole_key) {                      // a pick and the one behind it, or the first that is none
+    uint32_t behind = dpp_u<0x101>(mine);   // row_shl 1
+    behind = i == a.k - 1 ? next : behind;
+    const float v = value_of(mine), w = value_of(behind);
+    near |= on && behind != 0u && !(v - w > off(v) + off(w));
   }
-  int id = (int)(whole_key ? 511u - (mine & low) : (uint32_t)V * from + (uint32_t)(V - 1) - (mine & low));
+  int id = (int)(511u - (mine & low));
+  if (!whole_key) {
+    wave_fence();
+    const float v = value_of(mine);
+    const float* const of = c_s[wave][16 * q + from];
+    int u_of = 0;
+#pragma unroll
+    for (int u = V - 1; u >= 0; --u) u_of = of[u] == v ? u : u_of;
+    id = V * (int)from + u_of;
+  }
 
   uint64_t again = __ballot(near);
   if (twice) again = ~(uint64_t)0;
@@ -691,9 +731,8 @@ __global__ __launch_bounds__(256) void moe_route_rows_kernel(RouteArgs a) {
     if ((again >> (16 * q) & 0xffffu) != 0) id = fixed_s[wave][q][i & 7];
   }
 
-  const bool on = i < a.k;
-  const size_t pick = row + (on ? min(max(id, 0), a.e - 1) : 0);
-  const float x = a.half ? bf16_to_f32(static_cast<const uint16_t*>(a.logits)[pick]) : static_cast<const float*>(a.logits)[pick];
+  const size_t of = row + (on ? min(max(id, 0), a.e - 1) : 0);
+  const float x = a.half ? bf16_to_f32(static_cast<const uint16_t*>(a.logits)[of]) : static_cast<const float*>(a.logits)[of];
   double w;
   if (a.sigmoid)
     w = 1.0 / (1.0 + exp(-(double)x));
@@ -714,10 +753,12 @@ __global__ __launch_bounds__(256) void moe_route_rows_kernel(RouteArgs a) {
   }
 }
 
-// From here on, and from twice as many for more than 64 experts, four tokens a wave pay (64
-// experts: 4096 tokens 4.1 us against 4.9, 16385 5.4 against 10.0, 2048 4.0 both, 65536
-// with 8 experts 10 against 32; 128 experts: 4096 7.4 against 6.0, 16385 11.0 against 13.5,
-// 65536 28 against 43).
+// From here on four tokens a wave pay, from twice as many for more than 64 experts and four
+// times for more than 128 (64 experts: 4096 tokens 3.8 us against 4.9, 16385 5.1 against
+// 10.0, 2048 4.0 both; 500000 of 8 64 against 194; 128 experts: 4096 6.5 against 6.0, 16385
+// 9.1 against 13.5, 65536 25 against 43; 256, grouped: 16385 15.1 against 17.2, 65536 39
+// against 48.  Of the 15.1 a wave lives for 8, 880 vector instructions one behind the
+// other with four waves a SIMD, and the few that end in 64 bits longer).
 constexpr int64_t kRouteRowsFrom = 4096;
 
 hipError_t launch_moe_route(RouteArgs a, hipStream_t stream) {
@@ -731,13 +772,15 @@ hipError_t launch_moe_route(RouteArgs a, hipStream_t stream) {
   const int v = 4 * u, lanes16 = per / v;
   a.lanes16 = per % v == 0 && (lanes16 & (lanes16 - 1)) == 0 ? lanes16 : 0;
   for (a.shift16 = 0; 1 << a.shift16 < a.lanes16;) ++a.shift16;
-  if (a.t >= kRouteRowsFrom * u && a.k <= 8 && u <= 2 && a.e % v == 0 && a.whole && on(a.logits, 16) && on(a.bias, 16) &&
+  if (a.t >= kRouteRowsFrom * u && a.k <= 8 && u <= 4 && a.e % v == 0 && a.whole && on(a.logits, 16) && on(a.bias, 16) &&
       (a.groups == 1 || a.lanes16 > 0)) {
     const dim3 rows((uint32_t)((a.t + 15) / 16));
     if (u == 1)
       hipLaunchKernelGGL((moe_route_rows_kernel<4>), rows, dim3(256), 0, stream, a);
-    else
+    else if (u == 2)
       hipLaunchKernelGGL((moe_route_rows_kernel<8>), rows, dim3(256), 0, stream, a);
+    else
+      hipLaunchKernelGGL((moe_route_rows_kernel<16>), rows, dim3(256), 0, stream, a);
     return hipGetLastError();
   }
   const dim3 grid((uint32_t)((a.t + kRouteTokens - 1) / kRouteTokens));

@@ -132,12 +132,12 @@ def test_long_prompts_graph_and_out(dev):
     assert e[0].shape == (0, 8) and e[1].shape == (0, 8)
 
 
-# ---- many tokens: four of them a wave, up to 128 experts and 8 picks ------------------
+# ---- many tokens: four of them a wave, up to 256 experts and 8 picks ------------------
 
 def check_many(dev, l, k, **kw):
     """A few hundred tokens, each many times over in any order, as many as that takes; the reference takes each once."""
     n = l.shape[0]
-    order = torch.randint(0, n, (8195,), generator=torch.Generator().manual_seed(n))
+    order = torch.randint(0, n, (16387,), generator=torch.Generator().manual_seed(n))
     order[:n] = torch.arange(n)
     bias = kw.get("bias")
     ids, w = qg.moe_route(l[order].to(dev), k, sigmoid=kw.get("sigmoid", False), bias=None if bias is None else bias.to(dev),
@@ -150,7 +150,7 @@ def check_many(dev, l, k, **kw):
     assert bool(((w - again).abs() <= 2.0 ** -23 * again.abs()).logical_or(w.isnan() & again.isnan()).all())
 
 
-@pytest.mark.parametrize("e,k", [(4, 1), (8, 2), (60, 6), (64, 8), (72, 5), (100, 4), (128, 8), (256, 8)])
+@pytest.mark.parametrize("e,k", [(4, 1), (8, 2), (60, 6), (64, 8), (72, 5), (100, 4), (128, 8), (256, 8), (144, 6), (512, 8), (8, 8), (256, 1)])
 @pytest.mark.parametrize("sigmoid,bias,renorm", [(False, False, True), (False, True, False), (True, True, True), (True, False, False)])
 @pytest.mark.parametrize("half", [False, True])
 def test_many_tokens(dev, e, k, sigmoid, bias, renorm, half):
@@ -160,7 +160,7 @@ def test_many_tokens(dev, e, k, sigmoid, bias, renorm, half):
 
 
 @pytest.mark.parametrize("e,groups,top,k", [(128, 8, 4, 8), (128, 16, 1, 8), (64, 16, 7, 5), (64, 8, 3, 6), (96, 4, 2, 8), (32, 2, 1, 8), (256, 8, 4, 8),
-                                            (128, 2, 1, 8), (96, 6, 2, 4)])
+                                            (128, 2, 1, 8), (96, 6, 2, 4), (256, 2, 1, 8), (192, 4, 2, 8), (256, 16, 2, 5)])
 @pytest.mark.parametrize("sigmoid,bias", [(False, False), (True, True), (True, False), (False, True)])
 @pytest.mark.parametrize("half", [False, True])
 def test_many_tokens_in_groups(dev, e, groups, top, k, sigmoid, bias, half):
@@ -192,7 +192,7 @@ def test_many_tokens_with_ties_clusters_masks_and_nan(dev, e):
                 check_many(dev, l.bfloat16() if half else l, 8, sigmoid=sigmoid, bias=bias, groups=groups, top_groups=max(1, groups // 2),
                            best=1 if sigmoid or groups == 1 else 2)
     l[13, 33] = float("nan")
-    l = l.repeat(52, 1)
+    l = l.repeat(103, 1)
     for kw in (dict(), dict(sigmoid=True, bias=torch.zeros(e, device=dev)), dict(sigmoid=True, groups=4, top_groups=1, group_best=2)):
         for x in (l, l.bfloat16()):
             ids, w = qg.moe_route(x.to(dev), 4, **kw)
@@ -205,13 +205,13 @@ def test_many_tokens_with_ties_clusters_masks_and_nan(dev, e):
 def test_many_tokens_at_addresses_that_are_not_aligned(dev):
     """Logits and bias 4 bytes off: the other way, with the same result."""
     torch.manual_seed(8)
-    l, bias = torch.randn(8500, 128), 0.1 * torch.randn(128)
+    l, bias = torch.randn(17000, 128), 0.1 * torch.randn(128)
     want = qg.moe_route(l.to(dev), 8, sigmoid=True, bias=bias.to(dev))
-    room = torch.empty(8500 * 128 + 1, device=dev)
+    room = torch.empty(17000 * 128 + 1, device=dev)
     room[1:] = l.flatten().to(dev)
     room_b = torch.empty(129, device=dev)
     room_b[1:] = bias.to(dev)
-    got = qg.moe_route(room[1:].view(8500, 128), 8, sigmoid=True, bias=room_b[1:])
+    got = qg.moe_route(room[1:].view(17000, 128), 8, sigmoid=True, bias=room_b[1:])
     assert torch.equal(got[0], want[0]) and bool(((got[1] - want[1]).abs() <= 2.0 ** -23 * want[1]).all())
 
 
