@@ -107,7 +107,7 @@ struct LoraArgs {
   const void* y;                    // [m, n], rows y_stride apart
   void* out;                        // rows out_stride apart
   int64_t y_stride, out_stride;
-  int m, k, n, r, adapters, y_f32, out_f32, splits, steps;
+  int m, k, n, r, adapters, y_f32, out_f32, splits;
   float* part;                      // [splits, m, r]
   uint32_t* status;
 };

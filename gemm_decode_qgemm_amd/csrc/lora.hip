@@ -217,13 +217,13 @@ struct LoraLow {
   }
 };
 
-// RS steps of 32 ranks.  A wave takes 64 columns, and 4 rows at a time: the operand
+// RS steps of 32 ranks.  A wave takes TILES times 64 columns, and 4 rows at a time: the operand
 // repeats them, so that lane (i, q) has all four for column i of every tile and takes
 // tile q, 64 neighbouring columns a row.  (16 rows at a time would take a quarter of
 // the matrix instructions, of which there are plenty, and touch 16 columns of a row
 // at a time.)  Waves share nothing: once a wave knows its adapter, all it reads is
 // on its way together.
-template <int RS, bool Y32, bool OUT32>
+template <int RS, int TILES, bool Y32, bool OUT32>
 __global__ __launch_bounds__(256) void lora_up_kernel(LoraArgs a) {
   const int lane = threadIdx.x & 63, i = lane & 15, q = lane >> 4, wave = wave_id_uniform();
   const int units = min(a.m, a.adapters);
@@ -231,14 +231,15 @@ __global__ __launch_bounds__(256) void lora_up_kernel(LoraArgs a) {
     lora_rest<Y32, OUT32>(a, 4 * ((int)blockIdx.y - units) + wave);
     return;
   }
-  const int col = blockIdx.x * 256 + 64 * wave;
+  const int col = TILES * (blockIdx.x * 256 + 64 * wave);
   int adapter;
   uint64_t mask = lora_rows(a, blockIdx.y, adapter);
   if (mask == 0 || col >= a.n) return;
   const BufView bv(a.b + (size_t)adapter * a.n * a.r, a.n * a.r * 2);
   const BufView pv(a.part, a.splits * a.m * a.r * 4);
-  LoraB<RS> b;
-  b.load(bv, a.r, col);
+  LoraB<RS> b[TILES];
+#pragma unroll
+  for (int c = 0; c < TILES; ++c) b[c].load(bv, a.r, col + 64 * c);
   const float scale = a.scales ? a.scales[adapter] : 1.0f;
   do {
     int rows[4], some = 0;
@@ -251,11 +252,13 @@ __global__ __launch_bounds__(256) void lora_up_kernel(LoraArgs a) {
       ++some;
     }
     const LoraRows ys(a.y, Y32, a.y_stride, rows, some, a.n), os(a.out, OUT32, a.out_stride, rows, some, a.n);
-    float y[4];
+    float y[TILES][4];
 #pragma unroll
-    for (int m = 0; m < 4; ++m) y[m] = ys.load<Y32>(m, col + lane);
+    for (int c = 0; c < TILES; ++c)
+#pragma unroll
+      for (int m = 0; m < 4; ++m) y[c][m] = ys.load<Y32>(m, col + 64 * c + lane);
     const int mine = (i & 2) ? ((i & 1) ? rows[3] : rows[2]) : ((i & 1) ? rows[1] : rows[0]);
-    f32x4_t acc[4] = {};
+    f32x4_t acc[TILES][4] = {};
 #pragma unroll
     for (int s = 0; s < RS; ++s) {
       const int rank = 32 * s + 8 * q;
@@ -279,17 +282,21 @@ __global__ __launch_bounds__(256) void lora_up_kernel(LoraArgs a) {
       LoraLow low;
       low.split(f);
 #pragma unroll
-      for (int u = 2; u >= 0; --u)
+      for (int c = 0; c < TILES; ++c)
 #pragma unroll
-        for (int t = 0; t < 4; ++t)
-          acc[t] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8_t, low.v[u]),
-                                                           __builtin_bit_cast(bf16x8_t, b.w[t][s]), acc[t], 0, 0, 0);
+        for (int u = 2; u >= 0; --u)
+#pragma unroll
+          for (int t = 0; t < 4; ++t)
+            acc[c][t] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8_t, low.v[u]),
+                                                                __builtin_bit_cast(bf16x8_t, b[c].w[t][s]), acc[c][t], 0, 0, 0);
     }
 #pragma unroll
-    for (int m = 0; m < 4; ++m) {
-      const float v = q < 2 ? (q == 0 ? acc[0][m] : acc[1][m]) : (q == 2 ? acc[2][m] : acc[3][m]);
-      os.store<OUT32>(m, col + lane, y[m] + v);
-    }
+    for (int c = 0; c < TILES; ++c)
+#pragma unroll
+      for (int m = 0; m < 4; ++m) {
+        const float v = q < 2 ? (q == 0 ? acc[c][0][m] : acc[c][1][m]) : (q == 2 ? acc[c][2][m] : acc[c][3][m]);
+        os.store<OUT32>(m, col + 64 * c + lane, y[c][m] + v);
+      }
   } while (mask != 0);
 }
 
@@ -304,23 +311,32 @@ hipError_t launch_lora_add(LoraArgs a, hipStream_t stream) {
   hipLaunchKernelGGL(lora_down_kernel, dim3((a.r + 15) / 16, units, a.splits), dim3(64 * kLoraWaves), 0, stream, a);
   const hipError_t st = hipGetLastError();
   if (st != hipSuccess) return st;
-  const dim3 grid((a.n + 255) / 256, units + (a.m + 3) / 4);
   const int types = (a.y_f32 ? 2 : 0) + (a.out_f32 ? 1 : 0);
-#define QG_LORA(RS)                                                                                    \
-  switch (types) {                                                                                     \
-    case 0: hipLaunchKernelGGL((lora_up_kernel<RS, false, false>), grid, dim3(256), 0, stream, a); break; \
-    case 1: hipLaunchKernelGGL((lora_up_kernel<RS, false, true>), grid, dim3(256), 0, stream, a); break;  \
-    case 2: hipLaunchKernelGGL((lora_up_kernel<RS, true, false>), grid, dim3(256), 0, stream, a); break;  \
-    case 3: hipLaunchKernelGGL((lora_up_kernel<RS, true, true>), grid, dim3(256), 0, stream, a); break;   \
+#define QG_LORA(RS, TILES)                                                                                \
+  {                                                                                                       \
+    const dim3 grid((a.n + 256 * TILES - 1) / (256 * TILES), units + (a.m + 3) / 4);                      \
+    switch (types) {                                                                                      \
+      case 0: hipLaunchKernelGGL((lora_up_kernel<RS, TILES, false, false>), grid, dim3(256), 0, stream, a); break; \
+      case 1: hipLaunchKernelGGL((lora_up_kernel<RS, TILES, false, true>), grid, dim3(256), 0, stream, a); break;  \
+      case 2: hipLaunchKernelGGL((lora_up_kernel<RS, TILES, true, false>), grid, dim3(256), 0, stream, a); break;  \
+      case 3: hipLaunchKernelGGL((lora_up_kernel<RS, TILES, true, true>), grid, dim3(256), 0, stream, a); break;   \
+    }                                                                                                     \
   }
-  if (a.r <= 32)
-    QG_LORA(1)
+  // Up to rank 16 half of a wave's lanes load nothing of 64 columns; where those make up four
+  // rounds of 16 waves a CU, a wave takes 256 (64 adapters: rank 8, 131072 columns 54 us
+  // against 68, rank 16 62 against 72, 16384 columns 12.9 against 13.6; 8192 columns 11.2
+  // against 10.9; rank 32, 131072 columns 104 against 100).
+  const bool wide = a.r <= 16 && (int64_t)units * ((a.n + 63) / 64) >= 4 * 16 * kCUs;
+  if (wide)
+    QG_LORA(1, 4)
+  else if (a.r <= 32)
+    QG_LORA(1, 1)
   else if (a.r <= 64)
-    QG_LORA(2)
+    QG_LORA(2, 1)
   else if (a.r <= 128)
-    QG_LORA(4)
+    QG_LORA(4, 1)
   else
-    QG_LORA(8)
+    QG_LORA(8, 1)
 #undef QG_LORA
   return hipGetLastError();
 }

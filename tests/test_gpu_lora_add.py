@@ -56,6 +56,15 @@ def check(out, y, x, a, b, ids, scales):
         assert not bad.any(), (m, i, np.argwhere(bad)[:3].ravel(), got[m][bad][:3], want[bad][:3])
 
 
+@pytest.mark.parametrize("yt", [BF16, F32])
+@pytest.mark.parametrize("m,k,n,r,adapters", [(64, 64, 16385, 8, 64), (40, 64, 30001, 16, 64), (64, 72, 131072, 16, 8)])
+def test_low_ranks_beside_wide_projections(dev, m, k, n, r, adapters, yt):
+    args = make(m, k, n, r, adapters, yt)
+    y, x, a, b, ids, scales = (t.to(dev) for t in args)
+    check(qg.lora_add(y, x, a, b, ids, scales=scales), *args)
+    check(qg.lora_add(y, x, a, b, ids, out_dtype=F32 if yt is BF16 else BF16), *args[:5], None)
+
+
 @pytest.mark.parametrize("m,k,n,r,adapters", [
     (1, 8, 1, 8, 1), (1, 256, 256, 16, 4), (2, 264, 33, 24, 1), (3, 1000, 257, 16, 3), (5, 512, 1000, 32, 2), (16, 1024, 64, 40, 1),
     (17, 768, 129, 64, 1), (33, 520, 300, 16, 2), (64, 256, 70, 8, 1), (64, 1280, 513, 64, 64), (64, 2048, 130, 128, 3),
