@@ -9,15 +9,19 @@
 // Two launches, as the second product needs all of the first:
 //   down  a workgroup owns 16 ranks of one adapter and a part of K; its waves take
 //         64 k in turn and are summed in LDS; partial sums in fp32
-//   up    a wave owns 64 columns of one adapter's B; it adds the partial sums of the
-//         adapter's rows itself
+//   up    a wave owns 64 columns of one adapter's B or more; its workgroup adds the
+//         partial sums of the adapter's rows
 // A unit is an adapter, or the rows' adapters where a batch has fewer rows than
 // there are adapters: then the first row that names an adapter works for all of
 // its rows, so that every adapter in use is read once.
 //
 // The matrix instruction (16x16x32) has the rows of an adapter on one side and up to
 // 16 rows of x on the other.  A single row wastes 15/16 of it, which is
-// nothing: the kernels are bound by reading A and B.
+// nothing: the kernels are bound by reading A and B, and where these are small by
+// latency.  Kernels alone, in bf16: one row, rank 16, 6656 to 256 columns 4.3 + 2.0 us; 41
+// rows of 24 adapters to 8448 columns 5.3 + 4.4; 64 adapters of rank 64, 6656 to 39936
+// columns 13.4 (54 MB, 4.1 TB/s) + 61.5 (337 MB, 5.5 TB/s; reads alone in this pattern
+// take 53).
 #include <algorithm>
 
 #include "layer_common.h"
@@ -154,19 +158,22 @@ __device__ __forceinline__ void lora_rest(const LoraArgs& a, int m) {
   }
 }
 
-// 64 columns of B, 4 tiles of 16, as a wave's operands; zeros past its view.
-template <int RS>
+// 64 columns of B, 4 tiles of 16, as a wave's operands; zeros past its view.  An operand
+// holds PACK tiles side by side where that many ranks are all there are: 16 or 8.
+template <int RS, int PACK>
 struct LoraB {
-  u32x4_t w[4][RS];
+  static constexpr int kOps = 4 / PACK;
+  u32x4_t w[kOps][RS];
 
+  static __device__ __forceinline__ int tile(int t) { return PACK * t + (threadIdx.x >> 4 & 3) / kOps; }   // of a lane
+  static __device__ __forceinline__ int rank(int s) { return 32 * s + 8 * ((threadIdx.x >> 4 & 3) % kOps); }
   __device__ __forceinline__ void load(const BufView& b, int r, int col) {
-    const int lane = threadIdx.x & 63, i = lane & 15, q = lane >> 4;
-    const uint32_t row = 2u * (uint32_t)r, at = (uint32_t)(col + i) * row + 16u * q;
+    const uint32_t row = 2u * (uint32_t)r, at = (uint32_t)(col + 16 * tile(0) + (threadIdx.x & 15)) * row;
 #pragma unroll
     for (int s = 0; s < RS; ++s) {
-      const uint32_t from = 32 * s + 8 * q < r ? at + 64u * s : 0xfffffff0u - 64u * row;
+      const uint32_t from = rank(s) < r ? at + 2u * rank(s) : 0xfffffff0u - 64u * row;
 #pragma unroll
-      for (int t = 0; t < 4; ++t) w[t][s] = b.b128<false>(from + 16u * t * row);
+      for (int t = 0; t < kOps; ++t) w[t][s] = b.b128<false>(from + 16u * PACK * t * row);
     }
   }
 };
@@ -197,34 +204,65 @@ struct LoraRows {
   }
 };
 
-// 8 ranks of the first product as the sum of three bf16 operands.
-struct LoraLow {
-  u32x4_t v[3];
-  __device__ __forceinline__ void split(float (&f)[8]) {
-    float most = 0.0f;
+// Four rows' first product, scaled, as sums of three bf16: LDS of a workgroup.
+template <int RS>
+struct LoraInner {
+  static constexpr int kRanks = 32 * RS, kRow = kRanks + 8;        // rows off the same banks
+  static constexpr int kEach = (4 * kRanks + 255) / 256;            // values a thread
+  uint16_t v[3][4][kRow];
+
+  struct Parts { float f[kEach][kLoraSplits]; };
+  static __device__ __forceinline__ void place(int j, int& m, int& rank) {
+    const int at = (int)threadIdx.x + 256 * j;
+    m = at / kRanks, rank = at % kRanks;
+  }
+  static __device__ __forceinline__ Parts load(const LoraArgs& a, const BufView& pv, const int (&rows)[4]) {
+    Parts p;
+    // (as registers: an array that is picked from would go to LDS)
+    const int r0 = __builtin_amdgcn_readfirstlane(rows[0]), r1 = __builtin_amdgcn_readfirstlane(rows[1]);
+    const int r2 = __builtin_amdgcn_readfirstlane(rows[2]), r3 = __builtin_amdgcn_readfirstlane(rows[3]);
 #pragma unroll
-    for (int j = 0; j < 8; ++j) most = fmaxf(most, fabsf(f[j]));
-    const bool huge = __ballot(most > 0x1p127f) != 0;   // bf16's infinity, perhaps: all in the first
+    for (int j = 0; j < kEach; ++j) {
+      int m, rank;
+      place(j, m, rank);
+      const int row = (m & 2) ? ((m & 1) ? r3 : r2) : ((m & 1) ? r1 : r0);
+      uint32_t at = rank < a.r ? 4u * (uint32_t)(row * a.r + rank) : 0xf0000000u;   // past the view: zeros
 #pragma unroll
-    for (int u = 0; u < 3; ++u)
+      for (int s = 0; s < kLoraSplits; ++s, at += 4u * (uint32_t)(a.m * a.r))
+        p.f[j][s] = s < a.splits ? __uint_as_float(pv.b32(at)) : 0.0f;   // uniform
+    }
+    return p;
+  }
+  __device__ __forceinline__ void store(const Parts& p, float scale) {
 #pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        const uint32_t h = pack_bf16(f[2 * j], f[2 * j + 1]);
-        v[u][j] = h;
-        f[2 * j] = huge ? 0.0f : f[2 * j] - __uint_as_float(h << 16);
-        f[2 * j + 1] = huge ? 0.0f : f[2 * j + 1] - __uint_as_float(h & 0xffff0000u);
+    for (int j = 0; j < kEach; ++j) {
+      int m, rank;
+      place(j, m, rank);
+      if (m >= 4) continue;
+      float f = p.f[j][0];
+#pragma unroll
+      for (int s = 1; s < kLoraSplits; ++s) f += p.f[j][s];
+      f *= scale;
+      const bool huge = fabsf(f) > 0x1p127f;   // bf16's infinity, perhaps: all in the first
+#pragma unroll
+      for (int u = 0; u < 3; ++u) {
+        const uint32_t h = f32_to_bf16_rne(f) & 0xffffu;
+        v[u][m][rank] = (uint16_t)h;
+        f = huge ? 0.0f : f - __uint_as_float(h << 16);
       }
+    }
   }
 };
 
-// RS steps of 32 ranks.  A wave takes TILES times 64 columns, and 4 rows at a time: the operand
-// repeats them, so that lane (i, q) has all four for column i of every tile and takes
-// tile q, 64 neighbouring columns a row.  (16 rows at a time would take a quarter of
+// RS steps of 32 ranks.  A wave takes TILES times 64 columns, and 4 rows at a time: the
+// operand repeats them, so that lane (i, q) has all four for column i of every tile and
+// takes tile q, 64 neighbouring columns a row.  (16 rows at a time would take a quarter of
 // the matrix instructions, of which there are plenty, and touch 16 columns of a row
-// at a time.)  Waves share nothing: once a wave knows its adapter, all it reads is
-// on its way together.
-template <int RS, int TILES, bool Y32, bool OUT32>
+// at a time.)  The waves of a workgroup share what they need of the first product, each
+// its part of the sums, by way of LDS; their loads of B are on the way meanwhile.
+template <int RS, int PACK, int TILES, bool Y32, bool OUT32>
 __global__ __launch_bounds__(256) void lora_up_kernel(LoraArgs a) {
+  __shared__ __attribute__((aligned(16))) LoraInner<RS> inner_s[2];   // in turn: a barrier each
   const int lane = threadIdx.x & 63, i = lane & 15, q = lane >> 4, wave = wave_id_uniform();
   const int units = min(a.m, a.adapters);
   if ((int)blockIdx.y >= units) {
@@ -234,15 +272,13 @@ __global__ __launch_bounds__(256) void lora_up_kernel(LoraArgs a) {
   const int col = TILES * (blockIdx.x * 256 + 64 * wave);
   int adapter;
   uint64_t mask = lora_rows(a, blockIdx.y, adapter);
-  if (mask == 0 || col >= a.n) return;
+  if (mask == 0) return;               // the same in all waves; one past the columns goes on, for the barriers
   const BufView bv(a.b + (size_t)adapter * a.n * a.r, a.n * a.r * 2);
   const BufView pv(a.part, a.splits * a.m * a.r * 4);
-  LoraB<RS> b[TILES];
-#pragma unroll
-  for (int c = 0; c < TILES; ++c) b[c].load(bv, a.r, col + 64 * c);
   const float scale = a.scales ? a.scales[adapter] : 1.0f;
-  do {
-    int rows[4], some = 0;
+  int rows[4], some;
+  auto next_rows = [&] {
+    some = 0;
 #pragma unroll
     for (int m = 0; m < 4; ++m) {
       rows[m] = m > 0 ? rows[m - 1] : 0;
@@ -251,53 +287,51 @@ __global__ __launch_bounds__(256) void lora_up_kernel(LoraArgs a) {
       mask &= mask - 1;
       ++some;
     }
+  };
+  next_rows();
+  typename LoraInner<RS>::Parts parts = LoraInner<RS>::load(a, pv, rows);   // first: waited for first
+  using Ops = LoraB<RS, PACK>;
+  Ops b[TILES];
+#pragma unroll
+  for (int c = 0; c < TILES; ++c) b[c].load(bv, a.r, col + 64 * c);
+  for (int turn = 0;; turn ^= 1) {
     const LoraRows ys(a.y, Y32, a.y_stride, rows, some, a.n), os(a.out, OUT32, a.out_stride, rows, some, a.n);
     float y[TILES][4];
 #pragma unroll
     for (int c = 0; c < TILES; ++c)
 #pragma unroll
       for (int m = 0; m < 4; ++m) y[c][m] = ys.load<Y32>(m, col + 64 * c + lane);
-    const int mine = (i & 2) ? ((i & 1) ? rows[3] : rows[2]) : ((i & 1) ? rows[1] : rows[0]);
-    f32x4_t acc[TILES][4] = {};
+    LoraInner<RS>& inner = inner_s[turn];
+    inner.store(parts, scale);
+    lds_barrier();
 #pragma unroll
-    for (int s = 0; s < RS; ++s) {
-      const int rank = 32 * s + 8 * q;
-      uint32_t at = rank < a.r ? 4u * (uint32_t)(mine * a.r + rank) : 0xf0000000u;   // past the view: zeros
-      u32x4_t v[kLoraSplits][2] = {};
+    for (int c = 0; c < TILES; ++c) {
+      f32x4_t acc[Ops::kOps] = {};
 #pragma unroll
-      for (int p = 0; p < kLoraSplits; p += 2) {
-        if (p > 0 && p >= a.splits) continue;    // uniform; a part past the last is past the view
+      for (int s = 0; s < RS; ++s)
 #pragma unroll
-        for (int o = 0; o < 2; ++o, at += 4u * (uint32_t)(a.m * a.r))
-          v[p + o][0] = pv.b128<false>(at), v[p + o][1] = pv.b128<false>(at + 16);
-      }
-      float f[8];
+        for (int u = 2; u >= 0; --u) {
+          const u32x4_t low = *reinterpret_cast<const u32x4_t*>(&inner.v[u][i & 3][Ops::rank(s)]);
 #pragma unroll
-      for (int j = 0; j < 8; ++j) {
-        f[j] = __uint_as_float(v[0][j >> 2][j & 3]);
-#pragma unroll
-        for (int p = 1; p < kLoraSplits; ++p) f[j] += __uint_as_float(v[p][j >> 2][j & 3]);
-        f[j] *= scale;
-      }
-      LoraLow low;
-      low.split(f);
-#pragma unroll
-      for (int c = 0; c < TILES; ++c)
-#pragma unroll
-        for (int u = 2; u >= 0; --u)
-#pragma unroll
-          for (int t = 0; t < 4; ++t)
-            acc[c][t] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8_t, low.v[u]),
-                                                                __builtin_bit_cast(bf16x8_t, b[c].w[t][s]), acc[c][t], 0, 0, 0);
-    }
-#pragma unroll
-    for (int c = 0; c < TILES; ++c)
+          for (int t = 0; t < Ops::kOps; ++t) {
+            // rows 4 T .. 4 T + 3 of the product are tile T's, which for the other tiles' ranks are zero
+            const u32x4_t x = PACK == 1 || i >> 2 == Ops::tile(t) ? low : u32x4_t{0u, 0u, 0u, 0u};
+            f32x4_t& to = acc[PACK == 1 ? t : 0];
+            to = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8_t, x),
+                                                         __builtin_bit_cast(bf16x8_t, b[c].w[t][s]), to, 0, 0, 0);
+          }
+        }
 #pragma unroll
       for (int m = 0; m < 4; ++m) {
-        const float v = q < 2 ? (q == 0 ? acc[c][0][m] : acc[c][1][m]) : (q == 2 ? acc[c][2][m] : acc[c][3][m]);
+        float v = acc[0][m];
+        if constexpr (PACK == 1) v = q < 2 ? (q == 0 ? v : acc[1][m]) : (q == 2 ? acc[2][m] : acc[3][m]);
         os.store<OUT32>(m, col + 64 * c + lane, y[c][m] + v);
       }
-  } while (mask != 0);
+    }
+    if (mask == 0) return;
+    next_rows();
+    parts = LoraInner<RS>::load(a, pv, rows);
+  }
 }
 
 int lora_splits(int64_t m, int64_t k, int64_t r, int64_t adapters) {
@@ -312,31 +346,39 @@ hipError_t launch_lora_add(LoraArgs a, hipStream_t stream) {
   const hipError_t st = hipGetLastError();
   if (st != hipSuccess) return st;
   const int types = (a.y_f32 ? 2 : 0) + (a.out_f32 ? 1 : 0);
-#define QG_LORA(RS, TILES)                                                                                \
+#define QG_LORA(RS, PACK, TILES)                                                                          \
   {                                                                                                       \
-    const dim3 grid((a.n + 256 * TILES - 1) / (256 * TILES), units + (a.m + 3) / 4);                      \
+    const dim3 grid((a.n + 256 * TILES - 1) / (256 * TILES), units + (a.m + 3) / 4), block(256);          \
     switch (types) {                                                                                      \
-      case 0: hipLaunchKernelGGL((lora_up_kernel<RS, TILES, false, false>), grid, dim3(256), 0, stream, a); break; \
-      case 1: hipLaunchKernelGGL((lora_up_kernel<RS, TILES, false, true>), grid, dim3(256), 0, stream, a); break;  \
-      case 2: hipLaunchKernelGGL((lora_up_kernel<RS, TILES, true, false>), grid, dim3(256), 0, stream, a); break;  \
-      case 3: hipLaunchKernelGGL((lora_up_kernel<RS, TILES, true, true>), grid, dim3(256), 0, stream, a); break;   \
+      case 0: hipLaunchKernelGGL((lora_up_kernel<RS, PACK, TILES, false, false>), grid, block, 0, stream, a); break; \
+      case 1: hipLaunchKernelGGL((lora_up_kernel<RS, PACK, TILES, false, true>), grid, block, 0, stream, a); break;  \
+      case 2: hipLaunchKernelGGL((lora_up_kernel<RS, PACK, TILES, true, false>), grid, block, 0, stream, a); break;  \
+      case 3: hipLaunchKernelGGL((lora_up_kernel<RS, PACK, TILES, true, true>), grid, block, 0, stream, a); break;   \
     }                                                                                                     \
   }
-  // Up to rank 16 half of a wave's lanes load nothing of 64 columns; where those make up four
-  // rounds of 16 waves a CU, a wave takes 256 (64 adapters: rank 8, 131072 columns 54 us
-  // against 68, rank 16 62 against 72, 16384 columns 12.9 against 13.6; 8192 columns 11.2
-  // against 10.9; rank 32, 131072 columns 104 against 100).
-  const bool wide = a.r <= 16 && (int64_t)units * ((a.n + 63) / 64) >= 4 * 16 * kCUs;
-  if (wide)
-    QG_LORA(1, 4)
+  // Ranks of 8 and 16, which most adapters have, fill an operand with neighbouring tiles
+  // (without: 64 adapters of 131072 columns, rank 8 66 us, rank 16 75).  Where 64
+  // columns a wave make up four rounds of 16 waves a CU, a wave takes 256 or 128 (rank 8: 31 us
+  // against 56, 16384 columns 11.0 against 11.9; rank 16: 52 against 62, 11.7 against
+  // 12.4; 8192 columns 11 all).  Larger operands take the registers that hide latency: at
+  // rank 64 128 columns a wave 65 us against 61 at 39936, at rank 128 125 against 116.
+  const bool many = (int64_t)units * ((a.n + 63) / 64) >= 4 * 16 * kCUs;
+  if (a.r == 8 && many)
+    QG_LORA(1, 4, 4)
+  else if (a.r == 8)
+    QG_LORA(1, 4, 1)
+  else if (a.r == 16 && many)
+    QG_LORA(1, 2, 2)
+  else if (a.r == 16)
+    QG_LORA(1, 2, 1)
   else if (a.r <= 32)
-    QG_LORA(1, 1)
+    QG_LORA(1, 1, 1)
   else if (a.r <= 64)
-    QG_LORA(2, 1)
+    QG_LORA(2, 1, 1)
   else if (a.r <= 128)
-    QG_LORA(4, 1)
+    QG_LORA(4, 1, 1)
   else
-    QG_LORA(8, 1)
+    QG_LORA(8, 1, 1)
 #undef QG_LORA
   return hipGetLastError();
 }

@@ -57,7 +57,8 @@ def check(out, y, x, a, b, ids, scales):
 
 
 @pytest.mark.parametrize("yt", [BF16, F32])
-@pytest.mark.parametrize("m,k,n,r,adapters", [(64, 64, 16385, 8, 64), (40, 64, 30001, 16, 64), (64, 72, 131072, 16, 8)])
+@pytest.mark.parametrize("m,k,n,r,adapters", [(64, 64, 16385, 8, 64), (40, 64, 30001, 16, 64), (64, 72, 131072, 16, 8), (64, 64, 131075, 8, 9),
+                                               (33, 512, 700, 8, 3), (50, 512, 700, 16, 6), (64, 128, 4099, 24, 64)])
 def test_low_ranks_beside_wide_projections(dev, m, k, n, r, adapters, yt):
     args = make(m, k, n, r, adapters, yt)
     y, x, a, b, ids, scales = (t.to(dev) for t in args)
