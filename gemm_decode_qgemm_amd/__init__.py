@@ -3,6 +3,10 @@
 y = x . dequant(W)^T (. per-row scale) for INT4 group-32 asymmetric weights
 (W4A16, W4A8; fp16 group scales, or uint8 scale codes with a per-row
 fp16 step as the pages store them), INT5 / INT6 group-32 weights and INT8 per-channel weights (W8A16), M = 1..64 activation rows.
+Between the linears of a decoder layer: norms (rms_norm, rms_norm_q8, qk_norm_rope),
+an 8-bit paged cache and its attention (kv8_*, attn_kv8), mixtures of experts
+(moe_w4a16; moe_route and moe_w4a16_picked), adapters (lora_add) and the verification
+of drafted tokens (verify_drafts).
 The computation runs in the HIP library libqgemm.so (C ABI: include/qgemm.h);
 this package only binds it.
 """

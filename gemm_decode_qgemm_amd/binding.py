@@ -809,7 +809,7 @@ def rms_norm(x: torch.Tensor, weight: torch.Tensor | None = None, *, residual: t
              residual_out: torch.Tensor | None = None):
     """RMS norm of the rows of x [rows, h] (bf16 or fp32): y.  With a residual (bf16
     or fp32) the norm of x + residual: (y, x + residual in the residual's type).
-    residual_out may be residual itself.  x and residual may be strided views."""
+    residual_out may be residual itself, out x.  x and residual may be strided views."""
     dev, shape, od = x.get_device(), x.shape, _out_type(out_dtype)
     if not (_norm_args_ok(dev, x, shape, weight, residual, residual_out) and
             (out is None or _out_ok(out, out_dtype, shape, dev))):

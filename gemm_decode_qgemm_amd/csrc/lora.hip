@@ -321,12 +321,43 @@ __global__ __launch_bounds__(256) void lora_up_kernel(LoraArgs a) {
                                                          __builtin_bit_cast(bf16x8_t, b[c].w[t][s]), to, 0, 0, 0);
           }
         }
+      f32x4_t v = acc[0];              // of tile q
+      if constexpr (PACK == 1)
 #pragma unroll
-      for (int m = 0; m < 4; ++m) {
-        float v = acc[0][m];
-        if constexpr (PACK == 1) v = q < 2 ? (q == 0 ? v : acc[1][m]) : (q == 2 ? acc[2][m] : acc[3][m]);
-        os.store<OUT32>(m, col + 64 * c + lane, y[c][m] + v);
+        for (int m = 0; m < 4; ++m) v[m] = q < 2 ? (q == 0 ? v[m] : acc[1][m]) : (q == 2 ? acc[2][m] : acc[3][m]);
+      bool none = false;
+#pragma unroll
+      for (int m = 0; m < 4; ++m) none |= v[m] != v[m];
+      // A NaN may come of a weight that is infinite, times an inner value's second or third
+      // part, or times the zeros between neighbouring tiles: every tile by itself, and a
+      // sum that is still none from the first parts alone.
+      if (__ballot(none) != 0) {
+#pragma unroll 1
+        for (int p = 0; p < PACK; ++p) {
+          const bool own = q / Ops::kOps == p;
+          const u32x4_t zero = {0u, 0u, 0u, 0u};
+#pragma unroll
+          for (int t = 0; t < Ops::kOps; ++t) {
+            f32x4_t one = {}, some_of_it = {};
+#pragma unroll
+            for (int s = 0; s < RS; ++s)
+#pragma unroll
+              for (int u = 2; u >= 0; --u) {
+                const u32x4_t low = *reinterpret_cast<const u32x4_t*>(&inner.v[u][i & 3][Ops::rank(s)]);
+                const bf16x8_t x = __builtin_bit_cast(bf16x8_t, PACK == 1 || own ? low : zero);
+                const bf16x8_t w = __builtin_bit_cast(bf16x8_t, PACK == 1 || own ? b[c].w[t][s] : zero);
+                one = __builtin_amdgcn_mfma_f32_16x16x32_bf16(x, w, one, 0, 0, 0);
+                if (u == 0) some_of_it = __builtin_amdgcn_mfma_f32_16x16x32_bf16(x, w, some_of_it, 0, 0, 0);
+                __builtin_amdgcn_sched_barrier(0);   // seldom here: no registers for it
+              }
+            if (q == PACK * t + p)
+#pragma unroll
+              for (int m = 0; m < 4; ++m) v[m] = one[m] != one[m] ? some_of_it[m] : one[m];
+          }
+        }
       }
+#pragma unroll
+      for (int m = 0; m < 4; ++m) os.store<OUT32>(m, col + 64 * c + lane, y[c][m] + v[m]);
     }
     if (mask == 0) return;
     next_rows();
@@ -358,8 +389,8 @@ hipError_t launch_lora_add(LoraArgs a, hipStream_t stream) {
   }
   // Ranks of 8 and 16, which most adapters have, fill an operand with neighbouring tiles
   // (without: 64 adapters of 131072 columns, rank 8 66 us, rank 16 75).  Where 64
-  // columns a wave make up four rounds of 16 waves a CU, a wave takes 256 or 128 (rank 8: 31 us
-  // against 56, 16384 columns 11.0 against 11.9; rank 16: 52 against 62, 11.7 against
+  // columns a wave make up four rounds of 16 waves a CU, a wave takes 256 or 128 (rank 8: 32 us
+  // against 56, 16384 columns 10.3 against 11.9; rank 16: 53 against 62, 11.7 to 12.9 against
   // 12.4; 8192 columns 11 all).  Larger operands take the registers that hide latency: at
   // rank 64 128 columns a wave 65 us against 61 at 39936, at rank 128 125 against 116.
   const bool many = (int64_t)units * ((a.n + 63) / 64) >= 4 * 16 * kCUs;

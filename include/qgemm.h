@@ -530,7 +530,9 @@ int32_t qg_moe_w4a16_picked(const void *x_bf16, int64_t t, int64_t h, const int3
 
 /* ==========================================================================
  * Operators of a serving step beside the linears.  The conventions above
- * hold.
+ * hold, but for alignment: ids, scales, y and out of qg_lora_add, all arrays of
+ * qg_moe_route, and those of qg_verify_drafts but its workspace need that of their
+ * elements only; codes of qg_rms_norm_q8 8 bytes, its scales 4.
  * ======================================================================= */
 
 /* ---- qg_rms_norm / qg_rms_norm_q8 ----------------------------------------
@@ -547,7 +549,8 @@ int32_t qg_moe_w4a16_picked(const void *x_bf16, int64_t t, int64_t h, const int3
  *   w            in : bf16 [h], or NULL for a norm without weights
  *   residual_out out: r [rows, h], contiguous, in the residual's type; NULL without
  *                     a residual.  It may be `residual` itself (contiguous).
- *   y            out: [rows, h], bf16 or fp32 (y_dtype)
+ *   y            out: [rows, h], bf16 or fp32 (y_dtype).  It may be x itself (contiguous,
+ *                     same type).
  *   codes        out: int8 [rows, h];   scales out: fp32 [rows] or [rows, h / 32]
  * h: a multiple of 8 (group_scales: of 32) up to 32768; strides: multiples of 8.
  * rows = 0 is fine.
@@ -595,11 +598,13 @@ int32_t qg_lora_add(const void *x_bf16, int64_t m, int64_t k, const void *a_bf16
  *   counts the sum of its group_best (1 or 2) largest c; the top_groups of them stay
  *   ids = the top_k experts of those by c, largest first
  *   weights = s of the picked, divided by their sum (renormalize not 0), times scale
- * Ties go to the lowest index; a NaN counts as the largest.  Scores, sums and
- * comparisons are in 64 bits, so that the choice is the exact one but for
- * differences in the 16th digit; weights are rounded once.  An expert with a logit
+ * Ties go to the lowest index; a NaN counts as the largest.  Where no bias and no sum
+ * of two takes part, experts are in the order of their logits; else scores, sums
+ * and comparisons are as in 64 bits, so that the choice is the exact one but for
+ * differences in the 16th digit.  Weights are rounded once.  An expert with a logit
  * of -infinity has score 0 (it can be picked where too few others are left); where
- * the picked scores sum to 0, renormalized weights are 0.
+ * the picked scores sum to 0, renormalized weights are 0; beside a logit of +infinity
+ * a softmax is NaN.
  *   logits  in : [t, e], bf16 or fp32;   bias in : fp32 [e], or NULL
  *   ids     out: int32 [t, top_k];       weights out: fp32 [t, top_k]
  * e <= 512; top_k <= 32 and <= top_groups * e / groups; groups <= 64 divides e.
@@ -619,7 +624,9 @@ int32_t qg_moe_route(const void *logits, int32_t logits_dtype, int64_t t, int64_
  * next token is the first j whose running sum of max(target_i - draft_i, 0)
  * exceeds u_next times the whole sum (draft NULL: of target_i without x); that of
  * max(target_i, 0) where the whole sum is zero; and after the last draft that of the
- * last row.  All in 64 bits.  Rows need not add up to one; a NaN counts as 0.
+ * last row.  All in 64 bits: sums of the 512 tokens of a piece or more in binary64, and
+ * running sums in whole numbers of 2^-61 of the whole, so that a token without a share is
+ * never drawn.  Rows need not add up to one; a NaN counts as 0.
  *   target     in : [rows, v], bf16 or fp32 (dtype)
  *   draft      in : [rows - b, v] in the same type, or NULL
  *   tokens, u  in : int32 and fp32 [rows - b]; u in [0, 1)
@@ -627,7 +634,8 @@ int32_t qg_moe_route(const void *logits, int32_t logits_dtype, int64_t t, int64_
  *   lens       in/out: int32 [b], less the drafts that were not accepted (the
  *                   lengths that a cache is left with); may be NULL
  *   accepted, next out: int32 [b]
- *   ws            : qg_verify_drafts_workspace_bytes(...) bytes; contents unspecified
+ *   ws            : qg_verify_drafts_workspace_bytes(...) bytes; contents unspecified;
+ *                   NULL where that is 0
  *   status_dev    : may be NULL.  QG_FLAG_INDEX: a drafted token outside [0, v) (it is
  *                   rejected), or offsets that are not in order (accepted 0, next -1,
  *                   lens as it was); QG_FLAG_NONFINITE: a row to draw from without a

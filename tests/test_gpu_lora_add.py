@@ -200,3 +200,26 @@ def test_two_streams_at_once(dev):
                 got[i].append(qg.lora_add(*args[i][:5], scales=args[i][5]))
     torch.cuda.synchronize()
     assert all(torch.equal(o, want[i]) for i in (0, 1) for o in got[i])
+
+
+@pytest.mark.parametrize("r", [8, 16, 24, 64])
+@pytest.mark.parametrize("n,adapters", [(300, 5), (20000, 64)])
+def test_weights_that_are_not_finite_stay_with_their_columns(dev, r, n, adapters):
+    """Infinities and NaN in B reach the columns that they weigh, of the rows with that adapter, and no other; an inner
+    value that is infinite is taken as it is."""
+    y, x, a, b, ids, scales = (t.to(dev) for t in make(64, 128, n, r, adapters))
+    ids = (torch.arange(64, device=dev) % 5).to(torch.int32)
+    want = qg.lora_add(y, x, a, b, ids, scales=scales)
+    inf, nan = float("inf"), float("nan")
+    b[1, 17, 3], b[1, 100, r - 1], b[3, 40, 0], b[3, 299, 5] = nan, inf, -inf, nan
+    got = qg.lora_add(y, x, a, b, ids, scales=scales)
+    bad = torch.zeros(64, n, dtype=torch.bool, device=dev)
+    bad[1::5, 17] = bad[1::5, 100] = bad[3::5, 40] = bad[3::5, 299] = True
+    assert torch.equal(got[~bad], want[~bad])
+    inner = [scales[i].double() * (x[i::5].double() @ a[i].double().t()) for i in (1, 3)]
+    assert bool(got[1::5, 17].isnan().all()) and bool(got[3::5, 299].isnan().all())
+    assert torch.equal(got[1::5, 100].double(), inner[0][:, r - 1] * inf) and torch.equal(got[3::5, 40].double(), inner[1][:, 0] * -inf)
+    scales[0] = inf                            # an inner value's sign times a weight's: infinite or, where they differ, NaN
+    ref_ = y.double()[0] + (scales[0].double() * (a[0].double() @ x[0].double())) @ b[0].double().t()
+    got = qg.lora_add(y, x, a, b, ids, scales=scales, out_dtype=F32)[0]
+    assert torch.equal(got.isnan(), ref_.isnan()) and torch.equal(got.isinf(), ref_.isinf())
