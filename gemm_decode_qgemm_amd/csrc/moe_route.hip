@@ -310,7 +310,6 @@ __device__ __forceinline__ void route_token(const RouteArgs& a, const float (&l)
     best_two<32>(lanes, c1, c2);
     const float value = a.best == 1 ? c1 : c1 + c2;
     const int own = lane >> a.shift, first = lane & (lanes - 1);
-    const float far = 2.0f * (off(c1) + off(a.best == 1 ? c1 : c2));
     float n = 0.0f;                    // groups before this one
     // A group's lanes compare it with one other group each, in turn.
     for (int g0 = 0; g0 < a.groups; g0 += lanes) {
@@ -318,8 +317,6 @@ __device__ __forceinline__ void route_token(const RouteArgs& a, const float (&l)
       const float other = __shfl(value, min(g, a.groups - 1) << a.shift);
       const bool is = g < a.groups && own < a.groups && g != own;
       n += is && (other > value || (other == value && g < own)) ? 1.0f : 0.0f;
-      // (a pair is looked at from both sides: the larger of the two bounds counts)
-      if (!exact) near |= is && !(fabsf(other - value) > far);
     }
     if (lanes > 1) n += other_block<1>(n);
     if (lanes > 2) n += other_block<2>(n);
@@ -327,7 +324,14 @@ __device__ __forceinline__ void route_token(const RouteArgs& a, const float (&l)
     if (lanes > 8) n += other_block<8>(n);
     if (lanes > 16) n += other_block<16>(n);
     if (lanes > 32) n += other_block<32>(n);
-    if (n >= (float)a.top_groups)
+    const bool stay = own < a.groups && n < (float)a.top_groups;
+    if (!exact) {                      // the last group that stays and the first that does not
+      const float e = 1.5f * (off(c1) + off(a.best == 1 ? c1 : c2));
+      const float stays = -wave_max(stay ? e - value : -__builtin_inff());
+      const float goes = wave_max(own < a.groups && !stay ? value + e : -__builtin_inff());
+      near |= !(stays > goes);
+    }
+    if (!stay)
 #pragma unroll
       for (int u = 0; u < U; ++u) c[u] = __builtin_nanf("");
   }
@@ -651,6 +655,7 @@ __global__ __launch_bounds__(256) void moe_route_rows_kernel(RouteArgs a) {
   const uint32_t low = whole_key ? 0x1ffu : 0u;
   auto value_of = [&](uint32_t key) { return step_to(key & ~low); };
 
+  bool open = live;                      // the lane's experts can be picked
   if (a.groups > 1) {
     const int lanes = a.lanes16;
     float c1 = value_of(k[0]), c2 = value_of(k[1]);
@@ -659,7 +664,6 @@ __global__ __launch_bounds__(256) void moe_route_rows_kernel(RouteArgs a) {
     best_two<4>(lanes, c1, c2);
     best_two<8>(lanes, c1, c2);
     const float value = a.best == 1 ? c1 : c1 + c2;
-    const float far = 2.0f * (off(c1) + off(a.best == 1 ? c1 : c2));
     const int own = i >> a.shift16, first = i & (lanes - 1);
     float before = 0.0f;                 // groups before this one
     // A group's lanes compare it with one other group each, in turn.
@@ -668,13 +672,19 @@ __global__ __launch_bounds__(256) void moe_route_rows_kernel(RouteArgs a) {
       const float other = __shfl(value, 16 * q + (min(g, a.groups - 1) << a.shift16));
       const bool is = g < a.groups && g != own && live;
       before += is && (other > value || (other == value && g < own)) ? 1.0f : 0.0f;
-      if (!whole_key) near |= is && !(fabsf(other - value) > far);
     }
     if (lanes > 1) before += other_block<1>(before);
     if (lanes > 2) before += other_block<2>(before);
     if (lanes > 4) before += other_block<4>(before);
     if (lanes > 8) before += other_block<8>(before);
-    if (before >= (float)a.top_groups)
+    open = live && before < (float)a.top_groups;
+    if (!exact) {                        // the last group that stays and the first that does not
+      const float e = 1.5f * (off(c1) + off(a.best == 1 ? c1 : c2));
+      const float stays = -row_max(open ? e - value : -__builtin_inff());
+      const float goes = row_max(live && !open ? value + e : -__builtin_inff());
+      near |= !(stays > goes);
+    }
+    if (!open)
 #pragma unroll
       for (int j = 0; j < K; ++j) k[j] = 0u;
   }
@@ -697,6 +707,7 @@ __global__ __launch_bounds__(256) void moe_route_rows_kernel(RouteArgs a) {
   const u32x2_t pick = pick_s[wave][q][i & 7];
   const bool on = i < a.k;
   const uint32_t mine = on ? pick[0] : 0u, from = on ? pick[1] & 15u : 0u;   // lane j: the j-th pick's key, and its lane
+  if (V > K && !whole_key) near |= open && k[0] == 0u;   // a lane that gave all it had kept, and has more
   if (!whole_key) {                      // a pick and the one behind it, or the first that is none
     uint32_t behind = dpp_u<0x101>(mine);   // row_shl 1
     behind = i == a.k - 1 ? next : behind;

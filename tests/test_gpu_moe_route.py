@@ -233,3 +233,17 @@ def test_sigmoid_scores_that_are_all_one(dev):
     l[1, 7] = l[1, 5] = float("inf")
     ids, w = qg.moe_route(l.to(dev), 3, sigmoid=True, renormalize=False)
     assert ids.tolist() == [[9, 12, 3], [5, 7, 0]] and w.tolist() == [[1.0, 1.0, 1.0], [1.0, 1.0, 0.5]]
+
+
+@pytest.mark.parametrize("best", [8, 9, 12, 16])
+def test_many_tokens_whose_best_are_side_by_side(dev, best):
+    """Up to 16 experts of one lane ahead of all others, equal or a hair apart from the eighth on."""
+    torch.manual_seed(best)
+    l = torch.randn(120, 256)
+    l[:, 16:16 + best] = 6 + torch.rand(120, best)
+    l[::3, 16:16 + best] = 6.0
+    l[1::3, 16:16 + best] = 6 + 2.0 ** -21 * torch.randint(0, 3, (40, best)).float()
+    for kw in (dict(), dict(sigmoid=True, bias=torch.zeros(256)), dict(sigmoid=True, bias=0.01 * torch.randn(256), groups=8, top_groups=4, best=2),
+               dict(bias=torch.zeros(256))):
+        check_many(dev, l, 8, **kw)
+        check_many(dev, l.bfloat16(), 8, **kw)
