@@ -96,6 +96,12 @@ __device__ __forceinline__ void order8(const u32x2_t& v, uint32_t& xlo, uint32_t
 __device__ __forceinline__ u32x2_t load_codes8(const uint16_t* x, size_t at) {
   return *reinterpret_cast<const u32x2_t*>(reinterpret_cast<const int8_t*>(x) + at);
 }
+// The scale of code `at` of `all`, by a view: a plain load is moved to its use, behind a
+// wait for the codes or the weights (39936 x 6656: one row 28.7 us against 24.1, four 34.1
+// against 25.8).
+__device__ __forceinline__ float group_scale(const float* scales, size_t at, size_t all) {
+  return __uint_as_float(BufView(scales, (int)(all >> 5) * 4).b32((uint32_t)(at >> 5) * 4u));
+}
 
 template <int M, int JJ>
 __device__ __forceinline__ void do_group_a8(float (&acc)[M], const HalfRegs& cur,
@@ -422,7 +428,7 @@ __global__ __launch_bounds__(1024) void w4a8_gemv_lds_kernel(
         float sxv;
         if constexpr (Q8) {
           order8(load_codes8(x, at), lo, hi);
-          sxv = act_scale[at >> 5];
+          sxv = group_scale(act_scale, at, (size_t)M * k);
         } else {
           const u32x4_t v = *reinterpret_cast<const u32x4_t*>(x + at);
           const uint32_t w[4] = {v.x, v.y, v.z, v.w};
@@ -438,7 +444,7 @@ __global__ __launch_bounds__(1024) void w4a8_gemv_lds_kernel(
           quant8(v, inv, lo, hi);
         }
         xq_s[buf][m][sg] = u32x2_t{lo, hi};
-        if ((sg & 3) == 0) sx_s[buf][m][sg >> 2] = sxv;
+        if (Q8 || (sg & 3) == 0) sx_s[buf][m][sg >> 2] = sxv;   // (Q8: the quad's is the same)
       }
     }
     __syncthreads();
@@ -590,7 +596,8 @@ __global__ __launch_bounds__(1024) __attribute__((amdgpu_waves_per_eu(R64 ? 4 : 
       const size_t at = (size_t)qm * k + 8 * qs + (size_t)h * 128;
       if (qlane) {
         const u32x2_t c = load_codes8(x, at);
-        v = u32x4_t{c.x, c.y, GS ? __float_as_uint(act_scale[at >> 5]) : 0u, 0u};
+        v = u32x4_t{c.x, c.y, GS ? __float_as_uint(group_scale(act_scale, at, (size_t)M * k)) : 0u, 0u};
+        __builtin_amdgcn_sched_barrier(0);
       }
     } else {
       if (qlane) v = *reinterpret_cast<const u32x4_t*>(xsrc + (size_t)h * 128);
