@@ -838,22 +838,31 @@ def rms_norm_q8(x: torch.Tensor, weight: torch.Tensor | None = None, *, residual
     [rows, h], scales fp32 [rows], or [rows, h / 32] with group_scales), and with a
     residual (codes, scales, x + residual)."""
     dev, shape = x.get_device(), x.shape
-    wide = shape[:1] if not group_scales else (shape[0], shape[-1] // GROUP)
-    codes, scales = out if out is not None else (None, None)
-    if not (_norm_args_ok(dev, x, shape, weight, residual, residual_out) and
-            (out is None or (_out_ok(codes, torch.int8, shape, dev) and _out_ok(scales, _F32, wide, dev)))):
+    if not _norm_args_ok(dev, x, shape, weight, residual, residual_out):
+        codes, scales = out or (None, None)
+        wide = (shape[0], shape[-1] // GROUP) if group_scales else shape[:1]
         _refuse_norm(x, weight, residual, residual_out, [("codes", codes, torch.int8, shape),
                                                          ("scales", scales, torch.float32, wide)])
+    t, h = shape
+    wide = (t, h // GROUP) if group_scales else (t,)
     if out is None:
-        codes = torch.empty_like(x, dtype=torch.int8, memory_format=_DENSE)
-        scales = x.new_empty(wide, dtype=_F32)
-    if residual is not None and residual_out is None:
-        residual_out = torch.empty_like(residual, memory_format=_DENSE)
+        codes, scales = torch.empty_like(x, dtype=torch.int8, memory_format=_DENSE), x.new_empty(wide, dtype=_F32)
+    else:
+        codes, scales = out
+        if not (_out_ok(codes, torch.int8, shape, dev) and _out_ok(scales, _F32, wide, dev)):
+            _refuse_norm(x, weight, residual, residual_out, [("codes", codes, torch.int8, shape),
+                                                             ("scales", scales, torch.float32, wide)])
     call = lib.qg_rms_norm_q8 if _current() == dev else _elsewhere(dev, lib.qg_rms_norm_q8)
-    st = call(x.data_ptr(), _TYPES[x.dtype], x.stride(0), _ptr(residual),
-              0 if residual is None else _TYPES[residual.dtype], 0 if residual is None else residual.stride(0),
-              *shape, _ptr(weight), eps, codes.data_ptr(), scales.data_ptr(), group_scales, _ptr(residual_out),
-              _stream_of(dev))
+    w = None if weight is None else weight.data_ptr()
+    if residual is None:
+        st = call(x.data_ptr(), _TYPES[x.dtype], x.stride(0), None, 0, 0, t, h, w, eps, codes.data_ptr(),
+                  scales.data_ptr(), group_scales, None, _stream_of(dev))
+    else:
+        if residual_out is None:
+            residual_out = torch.empty_like(residual, memory_format=_DENSE)
+        st = call(x.data_ptr(), _TYPES[x.dtype], x.stride(0), residual.data_ptr(), _TYPES[residual.dtype],
+                  residual.stride(0), t, h, w, eps, codes.data_ptr(), scales.data_ptr(), group_scales,
+                  residual_out.data_ptr(), _stream_of(dev))
     if st:
         _check(st, "qg_rms_norm_q8")
     return (codes, scales) if residual is None else (codes, scales, residual_out)
