@@ -653,7 +653,8 @@ __global__ __launch_bounds__(256) void moe_route_rows_kernel(RouteArgs a) {
   else
     best8(k);
   const uint32_t low = whole_key ? 0x1ffu : 0u;
-  auto value_of = [&](uint32_t key) { return step_to(key & ~low); };
+  // (the last bits of a negative number's step are ones)
+  auto value_of = [&](uint32_t key) { return step_to((key >> 31) != 0 ? key & ~low : key | low); };
 
   bool open = live;                      // the lane's experts can be picked
   if (a.groups > 1) {

@@ -247,3 +247,19 @@ def test_many_tokens_whose_best_are_side_by_side(dev, best):
                dict(bias=torch.zeros(256))):
         check_many(dev, l, 8, **kw)
         check_many(dev, l.bfloat16(), 8, **kw)
+
+
+@pytest.mark.parametrize("e,groups", [(64, 4), (128, 4), (256, 8)])
+def test_many_tokens_with_whole_groups_masked(dev, e, groups):
+    """Fewer experts left than picks, in one group: the rest of the picks are that group's, or the first group's beside it."""
+    l = torch.full((40, e), -float("inf"))
+    per = e // groups
+    for i in range(40):
+        at = (i % groups) * per
+        l[i, at + i % 3:at + 2 + i % 5] = torch.randn(2 + i % 5 - i % 3)
+    for top in (1, 2):
+        for sigmoid in (False, True):
+            for best in (1, 2):
+                check_many(dev, l, 8, sigmoid=sigmoid, groups=groups, top_groups=top, best=best)
+                check_many(dev, l.bfloat16(), 8, sigmoid=sigmoid, groups=groups, top_groups=top, best=best)
+                check(dev, l.bfloat16(), 8, sigmoid, None, groups, top, best)
