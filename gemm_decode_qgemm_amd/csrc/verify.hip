@@ -40,15 +40,14 @@ struct VerifyRow {                     // where the next token of a sequence com
   bool bad;                            // a drafted token outside the vocabulary
 };
 
-// Rows of sequence b; false where its offsets are not in order.
+// Rows of sequence b; false where its offsets are not in order, or where one of its rows, of
+// the target or of the drafts, is not there.
 __device__ __forceinline__ bool verify_rows(const VerifyArgs& a, int b, VerifyRow& r) {
   r.bad = false;
   r.first = a.cu[b];
-  int64_t end = a.cu[b + 1];
-  r.first = r.first < 0 ? 0 : r.first;
-  end = end > a.rows ? a.rows : end;
+  const int64_t end = a.cu[b + 1];
   r.drafts = end - r.first - 1;
-  return r.drafts >= 0 && r.first - b >= 0 && r.first - b + r.drafts <= a.rows - a.b;
+  return r.drafts >= 0 && end <= a.rows && r.first >= b && r.first - b + r.drafts <= a.rows - a.b;
 }
 
 // The row behind `accepted` drafts.

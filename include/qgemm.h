@@ -637,8 +637,9 @@ int32_t qg_moe_route(const void *logits, int32_t logits_dtype, int64_t t, int64_
  *   ws            : qg_verify_drafts_workspace_bytes(...) bytes; contents unspecified;
  *                   NULL where that is 0
  *   status_dev    : may be NULL.  QG_FLAG_INDEX: a drafted token outside [0, v) (it is
- *                   rejected), or offsets that are not in order (accepted 0, next -1,
- *                   lens as it was); QG_FLAG_NONFINITE: a row to draw from without a
+ *                   rejected), or a sequence whose offsets are not in order or reach
+ *                   past the rows (accepted 0, next -1, lens as it was; the others
+ *                   as ever); QG_FLAG_NONFINITE: a row to draw from without a
  *                   finite sum above zero (next -1).
  * b <= 65535; b = 0 is fine.
  * Errors: QG_E_NULL, QG_E_SHAPE, QG_E_DTYPE, QG_E_ALIGN, QG_E_BUFFER. */

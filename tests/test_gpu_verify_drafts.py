@@ -289,3 +289,22 @@ def test_rows_past_two_to_the_31_elements(dev):
     accepted, following = qg.verify_drafts(target, None, none.to(torch.int32), none, torch.rand(b, device=dev),
                                            torch.arange(b + 1, dtype=torch.int32, device=dev))
     assert not bool(accepted.any()) and torch.equal(following.long(), hit)
+
+
+@pytest.mark.parametrize("v", [300, 50000])        # one launch; the sums in one of their own
+@pytest.mark.parametrize("cu,bad", [([0, 3, 7, 10], 2), ([0, 3, 7, 700], 2), ([0, 3, 7, 2 ** 31 - 1], 2), ([-1, 3, 7, 9], 0), ([-5, 3, 7, 9], 0),
+                                    ([-2 ** 31, 3, 7, 9], 0), ([0, 3, 7, -1], 2)])
+def test_offsets_that_reach_past_the_rows(dev, v, cu, bad):
+    """The one sequence whose rows are not all there accepts nothing and draws nothing, its length stays, and the flag says so; the
+    others are as they are with the right offsets, 0 3 7 9."""
+    c = make([2, 3, 1], v)
+    status = torch.zeros(1, dtype=torch.int32, device=dev)
+    lens = torch.full((3,), 50, dtype=torch.int32, device=dev)
+    right = [t.tolist() for t in run(dev, c, lens=lens, status=status)]
+    want_lens = lens.tolist()
+    assert status.item() == 0
+    lens.fill_(50)
+    accepted, following = run(dev, c | dict(cu=torch.tensor(cu, dtype=torch.int32)), lens=lens, status=status)
+    right[0][bad], right[1][bad], want_lens[bad] = 0, -1, 50
+    assert accepted.tolist() == right[0] and following.tolist() == right[1] and lens.tolist() == want_lens
+    assert status.item() == qg.FLAG_INDEX
