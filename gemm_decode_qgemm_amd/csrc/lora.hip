@@ -233,7 +233,7 @@ struct LoraInner {
     }
     return p;
   }
-  __device__ __forceinline__ void store(const Parts& p, float scale) {
+  __device__ __forceinline__ void store(const Parts& p, int r, float scale) {
 #pragma unroll
     for (int j = 0; j < kEach; ++j) {
       int m, rank;
@@ -242,7 +242,7 @@ struct LoraInner {
       float f = p.f[j][0];
 #pragma unroll
       for (int s = 1; s < kLoraSplits; ++s) f += p.f[j][s];
-      f *= scale;
+      f = rank < r ? f * scale : 0.0f;         // (an infinite scale times no rank is no NaN)
       const bool huge = fabsf(f) > 0x1p127f;   // bf16's infinity, perhaps: all in the first
 #pragma unroll
       for (int u = 0; u < 3; ++u) {
@@ -302,7 +302,7 @@ __global__ __launch_bounds__(256) void lora_up_kernel(LoraArgs a) {
 #pragma unroll
       for (int m = 0; m < 4; ++m) y[c][m] = ys.load<Y32>(m, col + 64 * c + lane);
     LoraInner<RS>& inner = inner_s[turn];
-    inner.store(parts, scale);
+    inner.store(parts, a.r, scale);
     lds_barrier();
 #pragma unroll
     for (int c = 0; c < TILES; ++c) {

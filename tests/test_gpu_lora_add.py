@@ -223,3 +223,17 @@ def test_weights_that_are_not_finite_stay_with_their_columns(dev, r, n, adapters
     ref_ = y.double()[0] + (scales[0].double() * (a[0].double() @ x[0].double())) @ b[0].double().t()
     got = qg.lora_add(y, x, a, b, ids, scales=scales, out_dtype=F32)[0]
     assert torch.equal(got.isnan(), ref_.isnan()) and torch.equal(got.isinf(), ref_.isinf())
+
+
+@pytest.mark.parametrize("r", [8, 16, 24, 40, 64, 72, 136])
+@pytest.mark.parametrize("m", [1, 9])
+def test_an_infinite_scale_reaches_the_ranks_that_there_are(dev, m, r):
+    """Ranks that fill up a matrix operand are no part of the sums: positive products times an infinite scale are infinite."""
+    k, n = 72, 301
+    g = torch.Generator().manual_seed(r)
+    x, a, b = (0.5 + torch.rand(s, generator=g).bfloat16().to(dev) for s in ((m, k), (2, r, k), (2, n, r)))
+    y = torch.randn(m, n, generator=g).to(dev)
+    ids = torch.ones(m, dtype=torch.int32, device=dev)
+    for s in (float("inf"), -float("inf")):
+        out = qg.lora_add(y, x, a, b, ids, scales=torch.tensor([1.0, s], device=dev))
+        assert bool((out == s).all())
