@@ -243,12 +243,14 @@ struct LoraInner {
 #pragma unroll
       for (int s = 1; s < kLoraSplits; ++s) f += p.f[j][s];
       f = rank < r ? f * scale : 0.0f;         // (an infinite scale times no rank is no NaN)
-      const bool huge = fabsf(f) > 0x1p127f;   // bf16's infinity, perhaps: all in the first
+      // The first part is rounded towards zero where to nearest could give bf16's infinity: the
+      // 16 bits behind it fill the other two as the rest of a rounded one does.
+      const bool huge = fabsf(f) > 0x1p127f, inf = fabsf(f) == __builtin_inff();
 #pragma unroll
       for (int u = 0; u < 3; ++u) {
-        const uint32_t h = f32_to_bf16_rne(f) & 0xffffu;
+        const uint32_t h = u == 0 && huge ? __float_as_uint(f) >> 16 : f32_to_bf16_rne(f) & 0xffffu;
         v[u][m][rank] = (uint16_t)h;
-        f = huge ? 0.0f : f - __uint_as_float(h << 16);
+        f = inf ? 0.0f : f - __uint_as_float(h << 16);   // (infinite: all in the first)
       }
     }
   }

@@ -237,3 +237,23 @@ def test_an_infinite_scale_reaches_the_ranks_that_there_are(dev, m, r):
     for s in (float("inf"), -float("inf")):
         out = qg.lora_add(y, x, a, b, ids, scales=torch.tensor([1.0, s], device=dev))
         assert bool((out == s).all())
+
+
+@pytest.mark.parametrize("r", [8, 16, 40])
+def test_inner_values_next_to_the_largest_binary32(dev, r):
+    """An inner value keeps its 24 bits up to the largest binary32 number, where bf16 rounds to infinity.
+
+    One product a rank, exact in fp32: v = s c with c a power of two.  It enters the second product as a sum of three bf16,
+    which hold its 24 bits, b = 2^-20 is exact, and r equal terms are summed in fp32: off by (3 r + 2) 2^-24 at most."""
+    k, n = 8, 70
+    x = torch.zeros(3, k, dtype=BF16, device=dev)
+    x[:, 3] = 1.0
+    a = torch.zeros(3, r, k, dtype=BF16, device=dev)
+    a[:, :, 3] = 2.0 ** 100
+    b = torch.full((3, n, r), 2.0 ** -20, dtype=BF16, device=dev)
+    scales = torch.tensor([2.0 ** 28 * (1 - 2.0 ** -24), 2.0 ** 27 * (1 + 2.0 ** -12 + 2.0 ** -23), -(2.0 ** 28) * (1 - 2.0 ** -10 + 2.0 ** -24)],
+                          device=dev)
+    ids = torch.arange(3, dtype=torch.int32, device=dev)
+    out = qg.lora_add(torch.zeros(3, n, device=dev), x, a, b, ids, scales=scales)
+    want = r * 2.0 ** 80 * ref.f64(scales)[:, None]
+    assert np.all(np.abs(ref.f64(out) - want) <= (3 * r + 2) * 2.0 ** -24 * np.abs(want))
