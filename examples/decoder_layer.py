@@ -15,7 +15,7 @@ some sequences without one.  --groups: experts chosen by biased sigmoid scores
 within the best half of that many groups (moe_route, moe_w4a16_picked).  --act8: the
 first projection on 8-bit rows (rms_norm_q8, qgemm_w4a8_rows).  --drafts: every step
 verifies that many drafted tokens a sequence against the probabilities of an INT4
-head (verify_drafts), and the cache keeps the accepted ones.
+head (verify_drafts), and the cache is left as if only the accepted ones had been fed.
 """
 from __future__ import annotations
 
@@ -82,9 +82,10 @@ class DecoderLayer:
         """The rows' adapters beside a projection, over its output."""
         return y if ids is None else qg.lora_add(y, x, *self.lora[name], ids, scales=self.lora_scales, out=y)
 
-    def forward(self, x: torch.Tensor, counts: torch.Tensor, cu: torch.Tensor | None, max_rows: int) -> torch.Tensor:
+    def forward(self, x: torch.Tensor, counts: torch.Tensor, cu: torch.Tensor | None, max_rows: int,
+                drafted: bool = False) -> torch.Tensor:
         """x [rows, hidden]: the next counts[b] tokens of every sequence, row offsets cu
-        (None: the same number each)."""
+        (None: the same number each).  drafted: keep_only may take some of them back."""
         batch = self.lens.shape[0]
         before = self.lens.clone()
         self.lens += counts
@@ -107,6 +108,10 @@ class DecoderLayer:
         qkv = self._adapt("qkv", qkv, normed, ids).unflatten(1, (-1, self.d))
         q, k, v = qkv.split((self.hq, self.hkv, self.hkv), 1)
         q, k = qg.qk_norm_rope(q, k, self.q_norm, self.k_norm, self.cos_sin, positions)
+        if drafted:   # the pages that hold tokens already and get new ones: theirs are requantized with the new ones' scale
+            page = (before // qg.KV8_PAGE).clamp(max=self.table.shape[1] - 1).long()
+            page = self.table.gather(1, page[:, None])[:, 0].long()
+            self.before = page, self.codes[page], self.scales[page], k, v
         qg.kv8_append(k, v, self.codes, self.scales, self.table, self.lens, cu=cu, max_new=max_rows)
         a = qg.attn_kv8(q, self.codes, self.scales, self.table, self.lens, cu=cu, max_q=max_rows, max_len=self.max_len).flatten(1)
         o = self._adapt("o", qg.qgemm_w4a16(a, self.o, self.hidden), a, ids)
@@ -116,6 +121,18 @@ class DecoderLayer:
                                            groups=self.groups, top_groups=self.groups // 2, group_best=2)
             return x + qg.moe_w4a16_picked(normed, chosen, weights, self.gate_up, self.down, self.inter)
         return x + qg.moe_w4a16(normed, self.router, self.gate_up, self.down, self.inter, self.top_k)
+
+    def keep_only(self, kept: torch.Tensor) -> None:
+        """Leaves the cache as if of the last step's rows (`drafted`, the same number each) sequence b had fed the first
+        kept[b] >= 1 alone; lens counts these already.  A shorter length by itself would leave them, and the tokens
+        before them, with the scales that the others raised, or made NaN."""
+        page, codes, scales, k, v = self.before
+        self.codes[page], self.scales[page] = codes, scales
+        rows = k.shape[0] // kept.shape[0]
+        gone = torch.arange(rows, device=k.device) >= kept[:, None]
+        order = gone.flatten().to(torch.uint8).argsort(stable=True)      # the kept rows, then those that no sequence has
+        cu = torch.cat([torch.zeros_like(kept[:1]), kept.cumsum(0, dtype=torch.int32)])
+        qg.kv8_append(k[order], v[order], self.codes, self.scales, self.table, self.lens, cu=cu, max_new=rows)
 
     def prompts(self, x: list) -> torch.Tensor:
         """Feeds prompts [n_b, hidden] in chunks of at most 64 rows in all; the last output row of each."""
@@ -153,17 +170,19 @@ class Speculator:
     def step(self, last: torch.Tensor, drafts: int) -> tuple:
         """One step for every sequence: its last token and `drafts` drafted ones (drawn evenly
         from the vocabulary here; a draft model's otherwise).  (accepted [b], next token [b]);
-        the cache is left with the accepted tokens."""
+        the cache is left with the last and the accepted tokens alone."""
         layer, device = self.layer, last.device
         b, rows = last.shape[0], last.shape[0] * (drafts + 1)
         tokens = torch.randint(0, self.vocabulary, (b, drafts), generator=self.g, device=device)
         q = torch.full((b * drafts, self.vocabulary), 1 / self.vocabulary, device=device)
         x = self.embedding[torch.cat([last[:, None].long(), tokens], 1).flatten()]
-        y = layer.forward(x, torch.full_like(layer.lens, drafts + 1), None, drafts + 1)
+        y = layer.forward(x, torch.full_like(layer.lens, drafts + 1), None, drafts + 1, drafted=True)
         cu = torch.arange(0, rows + 1, drafts + 1, dtype=torch.int32, device=device)
         u = torch.rand(b * drafts, generator=self.g, device=device)
-        return qg.verify_drafts(self.probabilities(y), q, tokens.flatten().to(torch.int32), u,
-                                torch.rand(b, generator=self.g, device=device), cu, lens=layer.lens)
+        accepted, following = qg.verify_drafts(self.probabilities(y), q, tokens.flatten().to(torch.int32), u,
+                                               torch.rand(b, generator=self.g, device=device), cu, lens=layer.lens)
+        layer.keep_only(accepted + 1)
+        return accepted, following
 
 
 def prompt_lengths(longest: int, batch: int) -> list:

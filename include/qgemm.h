@@ -438,6 +438,11 @@ int32_t qg_qk_norm_rope(const void *q, int64_t q_token_stride, int64_t q_head_st
  * A new value that is an infinity or a NaN makes its block's scale NaN.
  * Codes after the last token of a written block are unspecified.  Writing the
  * same rows again changes nothing.  A page belongs to one sequence of a call.
+ * A shorter length drops tokens, not what they did to a block that keeps others:
+ * its scale and the held codes' rounding stay (NaN, too, where a dropped value was
+ * none).  A caller that feeds drafted tokens and wants the cache as without the
+ * rejected ones puts back, from a copy of before the append, the codes and scales of
+ * the page that its last token then was in, and appends the accepted rows to that.
  *   k, v       in : bf16 [rows, hkv, d], strides as qg_qk_norm_rope
  *   lens       in : lengths with the new tokens counted
  *   max_new    in : no sequence has more new rows (a sequence's rows from
@@ -632,7 +637,8 @@ int32_t qg_moe_route(const void *logits, int32_t logits_dtype, int64_t t, int64_
  *   tokens, u  in : int32 and fp32 [rows - b]; u in [0, 1)
  *   u_next     in : fp32 [b], in [0, 1);   cu in : int32 [b + 1]
  *   lens       in/out: int32 [b], less the drafts that were not accepted (the
- *                   lengths that a cache is left with); may be NULL
+ *                   lengths that a cache is left with; for the scales of its blocks
+ *                   see qg_kv8_append); may be NULL
  *   accepted, next out: int32 [b]
  *   ws            : qg_verify_drafts_workspace_bytes(...) bytes; contents unspecified;
  *                   NULL where that is 0

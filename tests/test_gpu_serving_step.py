@@ -164,3 +164,63 @@ def test_a_captured_step_with_all_of_them(example):
         torch.cuda.synchronize()
         assert torch.equal(x, outs[i]), i
     assert torch.equal(layer.codes, eager.codes) and torch.equal(layer.lens, eager.lens)
+
+
+def small_layer(example):
+    """Blocks that are empty, partly held and full, and one whose next tokens lie in two pages."""
+    layer = example.DecoderLayer(6, 200, hidden=256, hq=4, hkv=2, d=64, experts=8, top_k=2, inter=256)
+    g = torch.Generator().manual_seed(11)
+    layer.prompts([torch.randn(n, 256, generator=g).bfloat16().cuda() for n in (9, 3, 30, 16, 17, 61)])
+    return layer
+
+
+def state_and_next(example, layer):
+    """Lengths, the cache's tokens as they are read back, and the same after a further token, with its output."""
+    def held():
+        return example.qg.kv8_read(layer.codes, layer.scales, layer.table, layer.lens, layer.max_len, out_dtype=torch.float32)
+
+    x = torch.randn(6, 256, generator=torch.Generator().manual_seed(3)).bfloat16().cuda()
+    return [layer.lens.clone(), *held(), layer.forward(x, torch.ones_like(layer.lens), None, 1), *held()]
+
+
+@pytest.mark.parametrize("infinite", [False, True])
+def test_rejected_drafts_leave_nothing_in_the_cache(example, monkeypatch, infinite):
+    """Steps with the same last tokens whose drafts, other ones each, are all rejected: the same cache, and the same output of
+    the next token."""
+    def rejected(p, q, tokens, u, u_next, cu, lens=None):
+        drafts.append(tokens.clone())
+        lens -= cu[1:] - cu[:-1] - 1
+        return torch.zeros_like(lens), torch.zeros_like(lens)
+
+    drafts, seen = [], []
+    monkeypatch.setattr(example.qg, "verify_drafts", rejected)
+    for seed in (1, 2):
+        layer = small_layer(example)
+        s = example.Speculator(layer, vocabulary=512)
+        s.g.manual_seed(seed)
+        if infinite and seed == 2:
+            s.embedding[1:, 5] = float("inf")      # all tokens but the last ones
+        s.step(torch.zeros(6, dtype=torch.int32, device="cuda"), 4)
+        seen.append(state_and_next(example, layer))
+    assert not torch.equal(*drafts) and seen[0][0].tolist() == [10, 4, 31, 17, 18, 62]
+    assert all(torch.equal(a, b) for a, b in zip(*seen)) and bool(seen[1][3].isfinite().all())
+
+
+@pytest.mark.parametrize("rest", [1.0, 100.0, float("inf")])
+def test_the_cache_keeps_the_accepted_rows_alone(example, rest):
+    """Two layers whose steps agree in the accepted rows, from the last token alone to all, and not in the others."""
+    kept = torch.tensor([1, 2, 3, 4, 5, 4], dtype=torch.int32, device="cuda")
+    g = torch.Generator().manual_seed(4)
+    x = torch.randn(6, 5, 256, generator=g).bfloat16().cuda()
+    gone = torch.arange(5, device="cuda") >= kept[:, None]
+    seen = []
+    for size in (1.0, rest):
+        layer = small_layer(example)
+        x[gone] = torch.randn(int(gone.sum()), 256, generator=g).bfloat16().cuda()
+        x[..., 7] = torch.where(gone, size, x[..., 7])
+        layer.forward(x.view(30, 256), torch.full_like(layer.lens, 5), None, 5, drafted=True)
+        layer.lens -= 5 - kept
+        layer.keep_only(kept)
+        seen.append(state_and_next(example, layer))
+    assert seen[0][0].tolist() == [10, 5, 33, 20, 22, 65]
+    assert all(torch.equal(a, b) for a, b in zip(*seen)) and bool(seen[1][3].isfinite().all())
