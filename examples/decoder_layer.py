@@ -192,6 +192,11 @@ def prompt_lengths(longest: int, batch: int) -> list:
     return [max(1, longest - 3 * (b % 5)) for b in range(batch)]
 
 
+def most_tokens(prompt: int, steps: int, drafts: int) -> int:
+    """Tokens of the longest sequence: its prompt and all that the steps feed, up to two before the timed ones too."""
+    return prompt + (steps + 2) * (drafts + 1)
+
+
 def main() -> None:
     p = argparse.ArgumentParser(description=__doc__, formatter_class=argparse.RawDescriptionHelpFormatter)
     p.add_argument("--batch", type=int, default=8)
@@ -206,7 +211,7 @@ def main() -> None:
     if a.drafts and (a.graph or a.batch * (a.drafts + 1) > qg.binding.MAX_M):
         p.error(f"--drafts takes no --graph, and at most {qg.binding.MAX_M} rows a step")
     dev = torch.device("cuda")
-    layer = DecoderLayer(a.batch, a.prompt + a.steps * (a.drafts + 1) + 8, adapters=a.adapters, groups=a.groups, act8=a.act8)
+    layer = DecoderLayer(a.batch, most_tokens(a.prompt, a.steps, a.drafts), adapters=a.adapters, groups=a.groups, act8=a.act8)
     torch.manual_seed(1)
     x = layer.prompts([torch.randn(n, layer.hidden, device=dev).bfloat16() for n in prompt_lengths(a.prompt, a.batch)])
     one = torch.ones(a.batch, dtype=torch.int32, device=dev)

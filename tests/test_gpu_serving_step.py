@@ -224,3 +224,30 @@ def test_the_cache_keeps_the_accepted_rows_alone(example, rest):
         seen.append(state_and_next(example, layer))
     assert seen[0][0].tolist() == [10, 5, 33, 20, 22, 65]
     assert all(torch.equal(a, b) for a, b in zip(*seen)) and bool(seen[1][3].isfinite().all())
+
+
+@pytest.mark.parametrize("args", [["--drafts", "15", "--batch", "4"], ["--batch", "3"], ["--batch", "3", "--graph"]], ids=lambda a: a[0][2:] + a[-1][2:])
+def test_the_longest_sequences_have_room(example, monkeypatch, capsys, args):
+    """The program with every draft accepted: no token past the table of positions or the pages, so outputs are finite."""
+    layers, outs = [], []
+
+    class Layer(example.DecoderLayer):
+        def __init__(self, *a, **kw):
+            super().__init__(*a, **kw)
+            layers.append(self)
+
+        def forward(self, *a, **kw):
+            outs.append(super().forward(*a, **kw))
+            return outs[-1]
+
+    def accepted(p, q, tokens, u, u_next, cu, lens=None):
+        return cu[1:] - cu[:-1] - 1, torch.zeros_like(lens)
+
+    monkeypatch.setattr(example, "DecoderLayer", Layer)
+    monkeypatch.setattr(example.qg, "verify_drafts", accepted)
+    monkeypatch.setattr(sys, "argv", ["decoder_layer.py", "--prompt", "5", "--steps", "2", *args])
+    example.main()
+    assert "us a step" in capsys.readouterr().out
+    layer, = layers
+    assert int(layer.lens.max()) <= layer.max_len == layer.cos_sin.shape[0] <= layer.table.shape[1] * example.qg.KV8_PAGE
+    assert all(bool(y.isfinite().all()) for y in outs)
