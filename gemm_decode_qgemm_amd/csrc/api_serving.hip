@@ -20,8 +20,10 @@ hipError_t launch_verify_drafts(VerifyArgs a, hipStream_t stream);
 namespace {
 
 constexpr int64_t kMaxStride = (int64_t)1 << 40;
-constexpr int64_t kMaxBlocks = ((int64_t)1 << 24) - 1;   // the x extent of a grid: below 2^32 threads at 256
-constexpr int64_t kMaxNormRows = ((int64_t)1 << 22) - 1; // and at 1024
+// The x extent of a grid, below 2^32 threads: a row for each workgroup of 1024, eight
+// tokens for each of 512.
+constexpr int64_t kMaxNormRows = ((int64_t)1 << 22) - 1;
+constexpr int64_t kMaxRouteTokens = 8 * (((int64_t)1 << 23) - 1);
 constexpr int64_t kMaxWidth = 32768;                     // channels of a normed row
 
 bool aligned(const void* p, uintptr_t n) { return ((uintptr_t)p & (n - 1)) == 0; }
@@ -144,7 +146,7 @@ int32_t qg_lora_add(const void* x_bf16, int64_t m, int64_t k, const void* a_bf16
 int32_t qg_moe_route(const void* logits, int32_t logits_dtype, int64_t t, int64_t e, int64_t top_k, int32_t sigmoid,
                      const float* bias, int64_t groups, int64_t top_groups, int32_t group_best, int32_t renormalize,
                      float scale, int32_t* ids, float* weights, void* stream) {
-  if (t < 0 || t > 4 * kMaxBlocks || e < 1 || e > 512 || top_k < 1 || top_k > 32) return QG_E_SHAPE;
+  if (t < 0 || t > kMaxRouteTokens || e < 1 || e > 512 || top_k < 1 || top_k > 32) return QG_E_SHAPE;
   if (groups < 1 || groups > 64 || e % groups != 0 || top_groups < 1 || top_groups > groups) return QG_E_SHAPE;
   if (group_best < 1 || group_best > 2 || group_best > e / groups || top_k > top_groups * (e / groups))
     return QG_E_SHAPE;

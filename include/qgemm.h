@@ -557,8 +557,8 @@ int32_t qg_moe_w4a16_picked(const void *x_bf16, int64_t t, int64_t h, const int3
  *   y            out: [rows, h], bf16 or fp32 (y_dtype).  It may be x itself (contiguous,
  *                     same type).
  *   codes        out: int8 [rows, h];   scales out: fp32 [rows] or [rows, h / 32]
- * h: a multiple of 8 (group_scales: of 32) up to 32768; strides: multiples of 8.
- * rows = 0 is fine.
+ * h: a multiple of 8 (group_scales: of 32) up to 32768; strides: multiples of 8;
+ * rows < 2^22.  rows = 0 is fine.
  * Errors: QG_E_NULL, QG_E_SHAPE, QG_E_STRIDE, QG_E_ALIGN, QG_E_DTYPE. */
 int32_t qg_rms_norm(const void *x, int32_t x_dtype, int64_t x_row_stride, const void *residual,
                     int32_t residual_dtype, int64_t residual_row_stride, int64_t rows, int64_t h,
@@ -613,7 +613,8 @@ int32_t qg_lora_add(const void *x_bf16, int64_t m, int64_t k, const void *a_bf16
  *   logits  in : [t, e], bf16 or fp32;   bias in : fp32 [e], or NULL
  *   ids     out: int32 [t, top_k];       weights out: fp32 [t, top_k]
  * e <= 512; top_k <= 32 and <= top_groups * e / groups; groups <= 64 divides e.
- * t = 0 is fine.  Errors: QG_E_NULL, QG_E_SHAPE, QG_E_DTYPE, QG_E_ALIGN. */
+ * t <= 2^26 - 8; t = 0 is fine.  Errors: QG_E_NULL, QG_E_SHAPE, QG_E_DTYPE,
+ * QG_E_ALIGN. */
 int32_t qg_moe_route(const void *logits, int32_t logits_dtype, int64_t t, int64_t e, int64_t top_k,
                      int32_t sigmoid, const float *bias, int64_t groups, int64_t top_groups,
                      int32_t group_best, int32_t renormalize, float scale, int32_t *ids, float *weights,

@@ -168,3 +168,10 @@ def test_wrappers_refuse_host_tensors_and_wrong_types():
     f = torch.zeros(2)
     with pytest.raises(ValueError, match="device"):
         qg.verify_drafts(x, None, ids, f, f, ids)
+
+
+@pytest.mark.parametrize("kw", [dict(), dict(e=6, groups=1, top=1, best=1, k=2), dict(k=32), dict(e=512)])
+def test_route_refuses_more_tokens_than_its_grids_hold(kw):
+    """2^23 workgroups of 512 threads and eight tokens each would be 2^32 threads."""
+    for t in ((1 << 26) - 7, (1 << 26) - 4, 1 << 40):
+        assert route(t=t, **kw) == E_SHAPE
