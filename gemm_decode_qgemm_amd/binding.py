@@ -241,6 +241,8 @@ def _out(m: int, n: int, out_dtype: torch.dtype, device, out: torch.Tensor | Non
         out = torch.empty((m, n), dtype=out_dtype, device=device)
     else:
         _dev(out, "out", out_dtype, 2)
+        if out.numel() < m * n:
+            raise ValueError("out must hold [m, n]")
     return out, (QG_F32 if out_dtype == torch.float32 else QG_BF16)
 
 
@@ -250,6 +252,8 @@ def _workspace(m, n, k, split_k, device, workspace):
         return None, 0
     if workspace is None:
         workspace = torch.empty(need, dtype=torch.uint8, device=device)
+    elif not workspace.is_contiguous():
+        raise ValueError("workspace must be contiguous")
     return workspace, workspace.numel() * workspace.element_size()
 
 

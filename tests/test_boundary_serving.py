@@ -175,3 +175,37 @@ def test_route_refuses_more_tokens_than_its_grids_hold(kw):
     """2^23 workgroups of 512 threads and eight tokens each would be 2^32 threads."""
     for t in ((1 << 26) - 7, (1 << 26) - 4, 1 << 40):
         assert route(t=t, **kw) == E_SHAPE
+
+
+class OnDevice:
+    """What a wrapper's checks see of a device tensor."""
+
+    def __init__(self, shape, dtype, contiguous=True):
+        self.shape, self.dtype, self._contiguous, self.is_cuda = torch.Size(shape), dtype, contiguous, True
+
+    def dim(self):
+        return len(self.shape)
+
+    def numel(self):
+        return self.shape.numel()
+
+    def element_size(self):
+        return self.dtype.itemsize
+
+    def is_contiguous(self):
+        return self._contiguous
+
+
+def test_linears_refuse_an_out_or_workspace_that_they_would_write_past():
+    from gemm_decode_qgemm_amd import binding
+    bf16, u8 = torch.bfloat16, torch.uint8
+    for shape in ((4, 99), (3, 100), (0, 100), (1, 1)):
+        with pytest.raises(ValueError, match="out"):
+            binding._out(4, 100, bf16, None, OnDevice(shape, bf16))
+    for shape in ((4, 100), (64, 100)):
+        assert binding._out(4, 100, bf16, None, OnDevice(shape, bf16))[0].shape == shape
+    need = binding.workspace_bytes(1, 128, 512, 2)
+    assert need > 0
+    with pytest.raises(ValueError, match="workspace"):
+        binding._workspace(1, 128, 512, 2, None, OnDevice((need,), u8, contiguous=False))
+    assert binding._workspace(1, 128, 512, 2, None, OnDevice((need,), u8))[1] == need
