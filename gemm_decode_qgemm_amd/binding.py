@@ -411,6 +411,10 @@ def qgemm_w4a8_rows(codes: torch.Tensor, scales: torch.Tensor, packed: torch.Ten
     _dev(scales, "scales", torch.float32, 2 if groups else 1)
     if tuple(scales.shape) != ((m, k // GROUP) if groups else (m,)):
         raise ValueError("scales must be [m] or [m, k / 32]")
+    if packed.element_size() != 1 or not packed.is_contiguous():
+        raise ValueError("packed must be contiguous bytes (uint8)")
+    if out is not None and (out.dim() != 2 or out.shape[1] != n):
+        raise ValueError("out must be [m, n]")
     _same_device(codes.device, scales=scales, packed=packed, out=out, workspace=workspace)
     y, yd = _out(m, n, out_dtype, codes.device, out)
     ws, ws_bytes = _workspace(m, n, k, split_k, codes.device, workspace)

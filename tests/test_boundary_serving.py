@@ -182,6 +182,7 @@ class OnDevice:
 
     def __init__(self, shape, dtype, contiguous=True):
         self.shape, self.dtype, self._contiguous, self.is_cuda = torch.Size(shape), dtype, contiguous, True
+        self.device = torch.device("cuda:0")
 
     def dim(self):
         return len(self.shape)
@@ -209,3 +210,14 @@ def test_linears_refuse_an_out_or_workspace_that_they_would_write_past():
     with pytest.raises(ValueError, match="workspace"):
         binding._workspace(1, 128, 512, 2, None, OnDevice((need,), u8, contiguous=False))
     assert binding._workspace(1, 128, 512, 2, None, OnDevice((need,), u8))[1] == need
+
+
+def test_quantized_rows_refuse_a_weight_or_out_of_another_kind():
+    bf16, u8, f32 = torch.bfloat16, torch.uint8, torch.float32
+    codes, scales, packed = OnDevice((4, 256), torch.int8), OnDevice((4,), f32), OnDevice((9472 * 2,), u8)
+    for kw, name in ((dict(packed=OnDevice((9472 * 2,), torch.int32)), "packed"), (dict(packed=OnDevice((9472 * 2,), u8, False)), "packed"),
+                     (dict(out=OnDevice((4, 127), bf16)), "out"), (dict(out=OnDevice((3, 128), bf16)), "out"),
+                     (dict(out=OnDevice((4, 256), bf16)), "out"), (dict(out=OnDevice((128, 4), bf16)), "out"), (dict(out=OnDevice((4, 128), f32)), "out")):
+        a = dict(codes=codes, scales=scales, packed=packed, n=128, out=None) | kw
+        with pytest.raises(ValueError, match=name):
+            qg.qgemm_w4a8_rows(**a)
