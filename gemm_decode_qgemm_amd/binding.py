@@ -418,8 +418,10 @@ def qgemm_w4a8_rows(codes: torch.Tensor, scales: torch.Tensor, packed: torch.Ten
     _same_device(codes.device, scales=scales, packed=packed, out=out, workspace=workspace)
     y, yd = _out(m, n, out_dtype, codes.device, out)
     ws, ws_bytes = _workspace(m, n, k, split_k, codes.device, workspace)
-    st = lib.qgemm_w4a8_rows(codes.data_ptr(), scales.data_ptr(), groups, m, k, packed.data_ptr(), packed.numel(),
-                             scale_codes, n, y.data_ptr(), yd, split_k, _ptr(ws), ws_bytes, _stream(codes.device))
+    dev = codes.get_device()
+    call = lib.qgemm_w4a8_rows if _current() == dev else _elsewhere(dev, lib.qgemm_w4a8_rows)
+    st = call(codes.data_ptr(), scales.data_ptr(), groups, m, k, packed.data_ptr(), packed.numel(), scale_codes, n,
+              y.data_ptr(), yd, split_k, _ptr(ws), ws_bytes, _stream_of(dev))
     _check(st, "qgemm_w4a8_rows")
     return y
 

@@ -114,3 +114,15 @@ def test_after_the_norm_in_a_graph(dev):
         assert torch.equal(out[0], want[0]) and torch.equal(out[1], want[1]), k
         near = qg.qgemm_w4a16(qg.rms_norm(x, w, residual=res)[0], packed, n)
         assert float((out[0].float() - near.float()).norm()) <= 0.02 * float(near.float().norm())
+
+
+@pytest.mark.parametrize("m", [1, 12])
+def test_a_device_that_is_not_the_current_one(dev, monkeypatch, m):
+    """The tensors' device is made current for the launch, which otherwise goes to the current device's own stream."""
+    packed = weight(128, 512, False, dev, 8)
+    codes, scales = torch.ones(m, 512, dtype=torch.int8, device=dev), torch.ones(m, device=dev)
+    want = qg.qgemm_w4a8_rows(codes, scales, packed, 128)
+    made, elsewhere = [], qg.binding._elsewhere
+    monkeypatch.setattr(qg.binding, "_current", lambda: 1)
+    monkeypatch.setattr(qg.binding, "_elsewhere", lambda index, fn: made.append(index) or elsewhere(index, fn))
+    assert torch.equal(qg.qgemm_w4a8_rows(codes, scales, packed, 128), want) and made == [dev.index]
