@@ -18,10 +18,11 @@
 // The matrix instruction (16x16x32) has the rows of an adapter on one side and up to
 // 16 rows of x on the other.  A single row wastes 15/16 of it, which is
 // nothing: the kernels are bound by reading A and B, and where these are small by
-// latency.  Kernels alone, in bf16: one row, rank 16, 6656 to 256 columns 4.3 + 2.0 us; 41
-// rows of 24 adapters to 8448 columns 5.3 + 4.4; 64 adapters of rank 64, 6656 to 39936
-// columns 13.4 (54 MB, 4.1 TB/s) + 61.5 (337 MB, 5.5 TB/s; reads alone in this pattern
-// take 53).
+// latency.  Kernels alone, in bf16: one row, rank 16, 6656 to 256 columns 4.4 + 2.1 us; 41
+// rows of 24 adapters to 8448 columns 5.4 + 4.4; 64 adapters of rank 64, 6656 to 39936
+// columns 13.5 (54 MB, 4.0 TB/s) + 61.5 to 63.5 (337 MB, 5.3 to 5.5 TB/s; reads alone in
+// this pattern take 53).  Many rows of one adapter go four at a time through the same
+// workgroups: 64 rows, rank 16, 6656 to 8448 columns 27.6 us for both, to 39936 28.4.
 #include <algorithm>
 
 #include "layer_common.h"

@@ -13,7 +13,11 @@
 //  * else c is formed in 32 bits with a bound on its error, and where all
 //    numbers that were compared are further apart than that, the choice is the
 //    exact one; a token where they are not (about one in a thousand) is done again
-//    in 64 bits.
+//    in 64 bits;
+//  * groups that are not a power of two of whole lanes (160 and 384 experts in 2, 4 or 8,
+//    for example) are chosen in 64 bits for every token, the logits alone among them
+//    (us, 160 and 384 experts in 8 groups, against 128 and 512: one token 7.2, 10.1 / 3.3,
+//    4.1; 61 8.8, 13.1 / 4.3, 5.8; 16385 37.7, 64.4 / 9.6, 23.9).
 // Weights are formed in 64 bits from the picked logits, a lane each, by one wave for
 // several tokens.
 //
@@ -765,12 +769,17 @@ __global__ __launch_bounds__(256) void moe_route_rows_kernel(RouteArgs a) {
   }
 }
 
-// From here on four tokens a wave pay, from twice as many for more than 64 experts and four
-// times for more than 128 (64 experts: 4096 tokens 3.8 us against 4.9, 16385 5.1 against
-// 10.0, 2048 4.0 both; 500000 of 8 64 against 194; 128 experts: 4096 6.5 against 6.0, 16385
-// 9.1 against 13.5, 65536 25 against 43; 256, grouped: 16385 15.1 against 17.2, 65536 39
-// against 48.  Of the 15.1 a wave lives for 8, 880 vector instructions one behind the
-// other with four waves a SIMD, and the few that end in 64 bits longer).
+// From here on four tokens a wave are taken, from twice as many for more than 64 experts
+// and four times for more than 128 (four tokens a wave against one, us in a graph.  64
+// experts, softmax: 4096 tokens 3.4 against 4.8, 16385 4.6 against 10.3; 500000 of 8 64
+// against 194.  128, biased: 4096 6.3 against 6.1, 8192 6.9 against 8.8, 16385 9.9 against
+// 11.5, 65536 22.5 against 34.9.  256, biased: 8192 11.3 against 10.0, 16384 14.6 against
+// 13.9, 24576 21.6 against 18.8, 32768 19.5 against 23.2; grouped: 8192 10.4 against 11.6,
+// 16384 19.0 against 16.5, 16385 15.2 against 16.6, 24576 25.7 against 21.9, 32768 23.1
+// against 27.1).  There it is about even up to 32768 tokens and goes by how many of them
+// end in 64 bits, for which the other three of their wave wait.  Where the logits decide
+// none does, and four tokens a wave would pay from 1024 on (256 experts: 4.2 against 4.5,
+// 8192 5.3 against 8.0): the rule does not tell these apart.
 constexpr int64_t kRouteRowsFrom = 4096;
 
 hipError_t launch_moe_route(RouteArgs a, hipStream_t stream) {

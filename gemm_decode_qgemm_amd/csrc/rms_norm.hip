@@ -11,8 +11,9 @@
 // thing that waits: a wave per row up to 2048 channels, else a workgroup.  The
 // 32 channels of a scale group are the chunks of four neighbouring lanes.  Long prompts
 // are bound by memory (16383 rows of 4096 on a 32-bit stream, 8-bit rows: 402 MB read
-// and 344 written in 127 us, 5.8 TB/s), few rows by latency (one row of 6656 3.0 us, 61
-// in 8 bits 5.0).
+// and 344 written in 130 to 134 us, 5.6 to 5.7 TB/s), few rows by latency (one row of
+// 6656 3.2 us, 61 in 8 bits 5.2), rows much narrower than a wave's 512 channels by the
+// lanes that have none (65536 rows of 64 16 us where a copy takes 3.5, of 256 18 for 14).
 #include "act_q8.h"
 #include "layer_common.h"
 
